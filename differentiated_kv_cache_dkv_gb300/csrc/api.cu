@@ -193,6 +193,67 @@ bool valid_decode_tables(const dkv_decode_batch *b, const dkv_pool *pool, const 
   return true;
 }
 
+// The shape, tables and pointers both multi-token calls share.
+bool valid_extend(const dkv_extend_batch *b, const dkv_pool *pool, const dkv_tables *t) {
+  if (!b || !valid_pool(pool) || !t || !t->fwd || !t->unit_hdr || !aligned(t->unit_hdr, 16) || !aligned(t->fwd, 4) ||
+      t->pmax < 2)
+    return false;
+  if (b->L < 1 || b->R < 0 || b->R > 65535 || b->Hkv < 1 || b->Hq < b->Hkv || b->Hq % b->Hkv != 0 ||
+      b->Hq > dkv::kMaxHq || b->cap < 1 || b->layer0 < 0 || b->n_layers < 0 ||
+      b->layer0 + static_cast<int64_t>(b->n_layers) > b->L || b->max_new < 0 || b->T < 0 || b->T > INT32_MAX ||
+      !std::isfinite(b->scale))
+    return false;
+  if (static_cast<int64_t>(b->L) * b->R * b->Hkv > INT32_MAX) return false;
+  if ((b->k_new == nullptr) != (b->v_new == nullptr)) return false;
+  if (b->T == 0) return true;
+  return b->q && b->new_lens && b->ctx_lens && aligned(b->q, 16) && aligned(b->k_new, 16) && aligned(b->v_new, 16) &&
+         aligned(b->new_lens, 4) && aligned(b->ctx_lens, 4) && aligned(b->lse, 4);
+}
+
+dkv::ExtendArgs extend_args(const dkv_extend_batch *b, const dkv_pool *pool, const dkv_tables *t) {
+  dkv::ExtendArgs a{};
+  a.L = b->L; a.R = b->R; a.Hq = b->Hq; a.Hkv = b->Hkv; a.G = b->Hq / b->Hkv; a.P = pool->P; a.pmax = t->pmax;
+  a.cap = b->cap; a.layer0 = b->layer0; a.n_layers = b->n_layers; a.max_new = b->max_new; a.scheme = pool->scheme;
+  a.T = b->T; a.F = pool->F; a.scale = b->scale;
+  a.q = static_cast<const uint16_t *>(b->q);
+  a.k_new = static_cast<const uint16_t *>(b->k_new);
+  a.v_new = static_cast<const uint16_t *>(b->v_new);
+  a.new_lens = b->new_lens; a.ctx_lens = b->ctx_lens;
+  a.out = static_cast<uint16_t *>(b->out); a.lse = b->lse;
+  a.fwd = t->fwd; a.unit_hdr = t->unit_hdr; a.pages = pool->pages; a.status = pool->status;
+  return a;
+}
+
+// Tables of U units with global ids [unit_base, unit_base + U), and a
+// workspace for the page operations on them.
+bool valid_page_op(const dkv_pool *pool, const dkv_tables *t, int64_t U, int64_t unit_base, const void *ws,
+                   size_t ws_bytes) {
+  return valid_pool(pool) && t && t->fwd && t->unit_hdr && aligned(t->unit_hdr, 16) && aligned(t->fwd, 4) &&
+         t->pmax >= 1 && U >= 1 && unit_base >= 0 && unit_base + U <= INT32_MAX && ws && aligned(ws, 256) &&
+         ws_bytes >= dkv::page_op_ws_layout(U, pool->F).bytes;
+}
+
+dkv::PageOpArgs page_op_args(const dkv_pool *pool, const dkv_tables *t, int64_t U, int64_t unit_base, void *ws) {
+  dkv::PageOpArgs a{};
+  a.P = pool->P; a.pmax = t->pmax; a.F = pool->F; a.U = U; a.unit_base = unit_base;
+  a.page_bytes = dkv::page_geom(pool->scheme, pool->P).bytes;
+  a.free_list = pool->free_list; a.cursors = pool->cursors; a.rev_unit = pool->rev_unit; a.rev_idx = pool->rev_idx;
+  a.page_cls = pool->page_cls; a.pages = pool->pages; a.status = pool->status;
+  a.fwd = t->fwd; a.unit_hdr = t->unit_hdr;
+  const dkv::PageOpWsLayout lay = dkv::page_op_ws_layout(U, pool->F);
+  uint8_t *w = static_cast<uint8_t *>(ws);
+  a.ws = reinterpret_cast<dkv::PageOpWsHeader *>(w);
+  a.part = reinterpret_cast<longlong2 *>(w + lay.part);
+  a.list = reinterpret_cast<int2 *>(w + lay.list);
+  return a;
+}
+
+// The shape of a request list's tables.
+bool valid_list(int32_t L, int32_t R, int32_t Hkv, int32_t n) {
+  return L >= 1 && R >= 1 && R <= 65535 && Hkv >= 1 && n >= 0 && n <= R &&
+         static_cast<int64_t>(L) * R <= INT32_MAX / Hkv;
+}
+
 // Largest head group per apply block whose shared memory fits; 0 if none.
 int32_t apply_heads(int32_t Hkv, int32_t words, int32_t pmax) {
   int32_t hpc = Hkv < dkv::kMaxApplyWarps ? Hkv : dkv::kMaxApplyWarps;
@@ -469,6 +530,86 @@ int32_t dkv_prefill_attention(const dkv_prefill_batch *b, const dkv_pool *pool, 
   if (sig_bytes > 0)
     if (const int32_t rc = cuda_status(cudaMemsetAsync(b->sig_sum, 0, sig_bytes, s))) return rc;
   return cuda_status(dkv::launch_prefill(a, s));
+}
+
+int32_t dkv_extend_workspace_size(const dkv_extend_batch *b, const dkv_pool *pool, const dkv_tables *t,
+                                  size_t *bytes) {
+  if (!bytes || !valid_extend(b, pool, t)) return DKV_E_INVAL;
+  *bytes = 0;
+  return DKV_OK;
+}
+
+int32_t dkv_extend_attention(const dkv_extend_batch *b, const dkv_pool *pool, const dkv_tables *t, void *workspace,
+                             size_t workspace_bytes, void *stream) {
+  if (!valid_extend(b, pool, t)) return DKV_E_INVAL;
+  if (b->T == 0 || b->R == 0 || b->n_layers == 0) return DKV_OK;
+  if (!b->out || !aligned(b->out, 16)) return DKV_E_INVAL;
+  (void)workspace;
+  (void)workspace_bytes;
+  return cuda_status(dkv::launch_extend(extend_args(b, pool, t), static_cast<cudaStream_t>(stream)));
+}
+
+int32_t dkv_extend_significance(const dkv_extend_batch *b, const int32_t *acc_lens, float *sig_sum,
+                                const dkv_pool *pool, const dkv_tables *t, void *stream) {
+  if (!valid_extend(b, pool, t)) return DKV_E_INVAL;
+  if (b->T == 0 || b->R == 0 || b->n_layers == 0) return DKV_OK;
+  if (!b->lse || !acc_lens || !sig_sum || !aligned(acc_lens, 4) || !aligned(sig_sum, 16)) return DKV_E_INVAL;
+  dkv::ExtendArgs a = extend_args(b, pool, t);
+  a.acc_lens = acc_lens;
+  a.sig_sum = sig_sum;
+  return cuda_status(dkv::launch_extend_sig(a, static_cast<cudaStream_t>(stream)));
+}
+
+int32_t dkv_page_ops_workspace_size(const dkv_pool *pool, int64_t U, size_t *bytes) {
+  if (!bytes || !valid_pool(pool) || U < 1 || U > INT32_MAX) return DKV_E_INVAL;
+  *bytes = dkv::page_op_ws_layout(U, pool->F).bytes;
+  return DKV_OK;
+}
+
+int32_t dkv_fork(const dkv_fork_batch *b, const dkv_pool *pool, const dkv_tables *t, void *workspace,
+                 size_t workspace_bytes, void *stream) {
+  if (!b || !valid_list(b->L, b->R, b->Hkv, b->n)) return DKV_E_INVAL;
+  const int64_t U = static_cast<int64_t>(b->L) * b->R * b->Hkv;
+  if (!valid_page_op(pool, t, U, b->unit_base, workspace, workspace_bytes)) return DKV_E_INVAL;
+  const bool rows = b->classes || b->slot_of || b->sig_sum || b->sig_cnt;
+  if (rows && (b->cap < 16 || b->cap % 16 != 0 || (b->sig_sum && b->Hq < 1))) return DKV_E_INVAL;
+  if (!aligned(b->classes, 16) || !aligned(b->slot_of, 16) || !aligned(b->sig_sum, 16) || !aligned(b->sig_cnt, 16))
+    return DKV_E_INVAL;
+  if (b->n == 0) return DKV_OK;
+  if (!b->src || !b->dst || !aligned(b->src, 4) || !aligned(b->dst, 4) || rows != (b->ctx_lens != nullptr) ||
+      !aligned(b->ctx_lens, 4))
+    return DKV_E_INVAL;
+  int sms = 0, pack_bps = 0;
+  if (!device_info(&sms, &pack_bps)) return cuda_status(cudaErrorInvalidDevice);
+  dkv::PageOpArgs a = page_op_args(pool, t, U, b->unit_base, workspace);
+  a.L = b->L; a.R = b->R; a.Hq = b->Hq; a.Hkv = b->Hkv; a.n = b->n; a.cap = b->cap;
+  a.V = static_cast<int64_t>(b->L) * b->n * b->Hkv;
+  a.src = b->src; a.dst = b->dst; a.ctx_lens = b->ctx_lens;
+  a.classes = b->classes; a.slot_of = b->slot_of; a.sig_sum = b->sig_sum; a.sig_cnt = b->sig_cnt;
+  return cuda_status(dkv::launch_fork(a, sms, static_cast<cudaStream_t>(stream)));
+}
+
+int32_t dkv_release(const dkv_release_batch *b, const dkv_pool *pool, const dkv_tables *t, void *workspace,
+                    size_t workspace_bytes, void *stream) {
+  if (!b || !valid_list(b->L, b->R, b->Hkv, b->n)) return DKV_E_INVAL;
+  const int64_t U = static_cast<int64_t>(b->L) * b->R * b->Hkv;
+  if (!valid_page_op(pool, t, U, b->unit_base, workspace, workspace_bytes)) return DKV_E_INVAL;
+  if (b->n == 0) return DKV_OK;
+  if (!b->reqs || !aligned(b->reqs, 4)) return DKV_E_INVAL;
+  dkv::PageOpArgs a = page_op_args(pool, t, U, b->unit_base, workspace);
+  a.L = b->L; a.R = b->R; a.Hkv = b->Hkv; a.n = b->n;
+  a.V = static_cast<int64_t>(b->L) * b->n * b->Hkv;
+  a.src = b->reqs;
+  return cuda_status(dkv::launch_release(a, static_cast<cudaStream_t>(stream)));
+}
+
+int32_t dkv_defrag(const dkv_pool *pool, const dkv_tables *t, int64_t U, int64_t unit_base, void *workspace,
+                   size_t workspace_bytes, void *stream) {
+  if (U > INT32_MAX || !valid_page_op(pool, t, U, unit_base, workspace, workspace_bytes)) return DKV_E_INVAL;
+  int sms = 0, pack_bps = 0;
+  if (!device_info(&sms, &pack_bps)) return cuda_status(cudaErrorInvalidDevice);
+  return cuda_status(dkv::launch_defrag(page_op_args(pool, t, U, unit_base, workspace), sms,
+                                        static_cast<cudaStream_t>(stream)));
 }
 
 int32_t dkv_dequant_page(const dkv_pool *pool, int32_t page_id, float *k_out, float *v_out, int32_t *pos_out,

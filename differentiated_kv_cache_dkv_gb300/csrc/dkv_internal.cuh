@@ -371,6 +371,64 @@ struct PrefillArgs {
   int32_t *status;
 };
 
+// Page operations (maintain.cu): fork, release, defrag.
+constexpr int kPlanUnits = 32;       // list units per block
+constexpr int kDefragPages = 2048;   // page ids per block
+
+struct PageOpWsHeader {
+  uint64_t head, tail;  // free-list cursors before the call
+  int64_t total;        // pages to copy or move; -1 after an error
+  int64_t pad[5];
+};
+
+struct PageOpWsLayout {
+  size_t part;   // longlong2 [blocks]: partial sums and errors of the plan kernel
+  size_t list;   // int2 [F]: (source, destination) pages
+  size_t bytes;
+};
+
+inline PageOpWsLayout page_op_ws_layout(int64_t U, int64_t F) {
+  PageOpWsLayout w{};
+  const int64_t a = (U + kPlanUnits - 1) / kPlanUnits, b = (F + kDefragPages - 1) / kDefragPages;
+  size_t o = align256(sizeof(PageOpWsHeader));
+  w.part = o; o = align256(o + 16 * static_cast<size_t>(a > b ? a : b));
+  w.list = o; o = align256(o + 8 * static_cast<size_t>(F));
+  w.bytes = o;
+  return w;
+}
+
+struct PageOpArgs {
+  int32_t L, R, Hq, Hkv, n, P, pmax, cap;
+  int64_t F, U, V, unit_base, page_bytes;  // V = L n Hkv list units
+  const int32_t *src, *dst, *ctx_lens;     // release: src names the requests, dst is null
+  uint8_t *classes;
+  int32_t *slot_of;
+  float *sig_sum;
+  int32_t *sig_cnt;
+  int32_t *free_list;
+  uint64_t *cursors;
+  int32_t *rev_unit, *rev_idx;
+  uint8_t *page_cls, *pages;
+  int32_t *status, *fwd, *unit_hdr;
+  PageOpWsHeader *ws;
+  longlong2 *part;
+  int2 *list;
+};
+
+// Attention of several new tokens a request (extend.cu).
+struct ExtendArgs {
+  int32_t L, R, Hq, Hkv, G, P, pmax, cap, layer0, n_layers, max_new, scheme;
+  int64_t T, F;
+  float scale;
+  const uint16_t *q, *k_new, *v_new;
+  const int32_t *new_lens, *ctx_lens, *acc_lens;
+  uint16_t *out;
+  float *lse, *sig_sum;
+  const int32_t *fwd, *unit_hdr;
+  const uint8_t *pages;
+  int32_t *status;
+};
+
 }  // namespace dkv
 
 // Launchers (defined in the kernel translation units).
@@ -394,4 +452,9 @@ cudaError_t launch_index(const DecodeArgs &a, int grid, cudaStream_t s);
 size_t apply_smem(int32_t hpc, int32_t words, int32_t pmax);
 cudaError_t launch_attend(const AttnArgs &a, int32_t S, cudaStream_t s);
 cudaError_t launch_prefill(const PrefillArgs &a, cudaStream_t s);
+cudaError_t launch_fork(const PageOpArgs &a, int sms, cudaStream_t s);
+cudaError_t launch_release(const PageOpArgs &a, cudaStream_t s);
+cudaError_t launch_defrag(const PageOpArgs &a, int sms, cudaStream_t s);
+cudaError_t launch_extend(const ExtendArgs &a, cudaStream_t s);
+cudaError_t launch_extend_sig(const ExtendArgs &a, cudaStream_t s);
 }  // namespace dkv

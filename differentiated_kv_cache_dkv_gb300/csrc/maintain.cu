@@ -1,0 +1,480 @@
+// maintain.cu -- page operations of a pool that serves many requests:
+// dkv_fork (copy requests), dkv_release (free requests), dkv_defrag (move the
+// live pages to the lowest ids).
+//
+// DiffKV (arXiv 2412.03131), "What carries the argument" and abstract: the
+// on-GPU memory manager allocates and recycles pages through a circular free
+// list in one coordinated step.  The pages describe the allocation; these are
+// the other steps of a pool's life, with the same prefix-sum placement.
+//
+// Every operation is two or three launches in stream order: a plan kernel
+// checks everything and leaves one partial sum per block, the next kernel
+// adds up the partial sums itself (each block reads all of them: at most a
+// few thousand 16-byte entries from L2, less than a look-back's waits or a
+// launch would take), stops if any check failed or the pages do not suffice,
+// and places its block's share.  Nothing is written to the pool before every
+// check of the call has passed, which makes the calls all-or-nothing.
+//   fork     k_fork_plan, k_fork_place (tables, copy list), k_fork_copy
+//   release  k_release_plan, k_release_place
+//   defrag   k_defrag_plan, k_defrag_list, k_defrag_move
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "dkv_internal.cuh"
+
+namespace dkv {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr unsigned kFull = 0xffffffffu;
+
+// Sum of x over the block (all threads get it).  `sm` holds kWarps values.
+__device__ __forceinline__ int64_t block_sum(int64_t x, int64_t *sm) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(kFull, x, o);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = x;
+  __syncthreads();
+  int64_t t = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) t += sm[w];
+  return t;
+}
+
+// A list unit (l, k, h) of request list q: its index in the tables.
+__device__ __forceinline__ int64_t list_unit(const PageOpArgs &a, int64_t v, const int32_t *q, int32_t &k) {
+  const int32_t h = static_cast<int32_t>(v % a.Hkv);
+  const int64_t lk = v / a.Hkv;
+  k = static_cast<int32_t>(lk % a.n);
+  const int32_t r = __ldg(q + k);
+  if (r < 0 || r >= a.R) return -1;
+  return ((lk / a.n) * a.R + r) * a.Hkv + h;
+}
+
+// Pages of a unit from its header; -1 when the header contradicts itself.
+__device__ __forceinline__ int32_t unit_pages(const PageOpArgs &a, const int4 &h) {
+  if (h.x < 0 || h.y < 0 || h.z != (static_cast<int64_t>(h.x) + a.P - 1) / a.P ||
+      h.w != (static_cast<int64_t>(h.y) + 2 * a.P - 1) / (2 * a.P) || h.z + h.w > a.pmax)
+    return -1;
+  return h.z + h.w;
+}
+
+// The request lists themselves (one block): no request may be named twice as
+// a destination (fork) or at all (release), nor be both source and
+// destination.  `bits` has room for R bits twice.
+__device__ int32_t check_lists(const PageOpArgs &a, uint32_t *bits) {
+  const int32_t words = (a.R + 31) / 32;
+  for (int32_t i = threadIdx.x; i < 2 * words; i += kThreads) bits[i] = 0;
+  __syncthreads();
+  int32_t bad = 0;
+  const int32_t *once = a.dst ? a.dst : a.src;
+  for (int32_t k = threadIdx.x; k < a.n; k += kThreads) {
+    const int32_t r = __ldg(once + k);
+    if (r < 0 || r >= a.R) bad = 1;
+    else if (atomicOr(bits + (r >> 5), 1u << (r & 31)) >> (r & 31) & 1u) bad = 1;
+  }
+  __syncthreads();
+  if (a.dst) {
+    for (int32_t k = threadIdx.x; k < a.n; k += kThreads) {
+      const int32_t r = __ldg(a.src + k);
+      if (r < 0 || r >= a.R || (bits[r >> 5] >> (r & 31) & 1u)) bad = 1;
+      // the context whose rows are copied must lie in the request's rows
+      else if (a.ctx_lens && (__ldg(a.ctx_lens + r) < 0 || __ldg(a.ctx_lens + r) > a.cap)) bad |= 2;
+    }
+  }
+  bad = __syncthreads_or(bad & 1) ? 1 : (__syncthreads_or(bad & 2) ? 2 : 0);
+  return bad == 1 ? DKV_E_INTERNAL : (bad == 2 ? DKV_E_LENS : 0);
+}
+
+// ---------------------------------------------------------- fork, release --
+
+// One warp per list unit, kPlanUnits units a block: header, page ids and (for
+// a release) reverse entries agree, destinations (for a fork) are empty;
+// part[block] = {pages of the block's units, error}.
+template <bool kFork>
+__global__ void __launch_bounds__(kThreads) k_list_plan(PageOpArgs a) {
+  extern __shared__ uint32_t bits[];
+  __shared__ int64_t sm[kWarps];
+  __shared__ int32_t err_s;
+  if (threadIdx.x == 0) err_s = 0;
+  __syncthreads();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t sum = 0;
+  int32_t err = 0;
+  for (int i = warp; i < kPlanUnits; i += kWarps) {
+    const int64_t v = static_cast<int64_t>(blockIdx.x) * kPlanUnits + i;
+    if (v >= a.V) break;
+    int32_t k, d = 0;
+    const int64_t u = list_unit(a, v, a.src, k);
+    if (u >= 0) {
+      d = unit_pages(a, *reinterpret_cast<const int4 *>(a.unit_hdr + 4 * u));
+      if (d < 0) err = DKV_E_INTERNAL;
+      for (int32_t j = lane; j < d; j += 32) {
+        const int32_t id = a.fwd[u * a.pmax + j];
+        if (id < 0 || id >= a.F) err = DKV_E_INTERNAL;
+        else if (a.rev_unit[id] != a.unit_base + u || a.rev_idx[id] != j) err = DKV_E_INTERNAL;
+      }
+    } else {
+      err = DKV_E_INTERNAL;
+    }
+    if (kFork) {
+      const int64_t w = list_unit(a, v, a.dst, k);
+      if (w < 0) {
+        err = DKV_E_INTERNAL;
+      } else {
+        const int4 h = *reinterpret_cast<const int4 *>(a.unit_hdr + 4 * w);
+        if (h.x | h.y | h.z | h.w) err = DKV_E_INTERNAL;
+      }
+    }
+    if (lane == 0) sum += max(d, 0);
+  }
+  if (blockIdx.x == 0) {
+    const int32_t e = check_lists(a, bits);
+    if (e) err = e;
+    if (threadIdx.x == 0) {  // the cursors before the call: the next kernel moves them
+      a.ws->head = a.cursors[0];
+      a.ws->tail = a.cursors[1];
+    }
+  }
+  if (err) atomicCAS(&err_s, 0, err);
+  sum = block_sum(sum, sm);
+  if (threadIdx.x == 0) a.part[blockIdx.x] = make_longlong2(sum, err_s);
+}
+
+// Sum of the plan's partial sums before this block and of all, and the first
+// error in block order.  Every thread of the block calls it.
+__device__ __forceinline__ int32_t plan_totals(const longlong2 *part, int32_t nparts, int64_t *sm, int64_t &before,
+                                               int64_t &total) {
+  int64_t b = 0, t = 0, e = INT64_MAX;
+  for (int32_t i = threadIdx.x; i < nparts; i += kThreads) {
+    const longlong2 p = part[i];
+    t += p.x;
+    if (i < static_cast<int32_t>(blockIdx.x)) b += p.x;
+    if (p.y && e == INT64_MAX) e = (static_cast<int64_t>(i) << 8) - p.y;  // -p.y is 1 .. 7
+  }
+  before = block_sum(b, sm);
+  total = block_sum(t, sm);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) e = min(e, __shfl_xor_sync(kFull, e, o));
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = e;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) e = min(e, sm[w]);
+  return e == INT64_MAX ? 0 : -static_cast<int32_t>(e & 0xff);
+}
+
+// Same blocks as the plan: places the block's units after the sum of the
+// blocks before.  Fork: new page ids into the destination's tables, (old,
+// new) into the copy list.  Release: ids into the ring, tables cleared.
+template <bool kFork>
+__global__ void __launch_bounds__(kThreads) k_list_place(PageOpArgs a, int32_t nparts) {
+  __shared__ int64_t sm[kWarps];
+  __shared__ int32_t d_s[kPlanUnits];
+  int64_t before, total;
+  int32_t err = plan_totals(a.part, nparts, sm, before, total);
+  const uint64_t head = a.ws->head, tail = a.ws->tail;
+  const int64_t free = static_cast<int64_t>(tail - head);
+  if (!err && (free < 0 || free > a.F || (!kFork && free + total > a.F))) err = DKV_E_INTERNAL;
+  if (!err && kFork && total > free) err = DKV_E_NOMEM;
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    a.ws->total = err ? -1 : total;
+    if (err) set_error(a.status, err);
+    else a.cursors[kFork ? 0 : 1] = (kFork ? head : tail) + total;
+  }
+  if (err) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t v0 = static_cast<int64_t>(blockIdx.x) * kPlanUnits;
+  for (int i = threadIdx.x; i < kPlanUnits; i += kThreads) {
+    int32_t k, d = 0;
+    if (v0 + i < a.V) {
+      const int64_t u = list_unit(a, v0 + i, a.src, k);
+      const int4 h = *reinterpret_cast<const int4 *>(a.unit_hdr + 4 * u);
+      d = h.z + h.w;
+    }
+    d_s[i] = d;
+  }
+  __syncthreads();
+  const uint64_t at0 = ((kFork ? head : tail) + before) % static_cast<uint64_t>(a.F);
+  for (int i = warp; i < kPlanUnits; i += kWarps) {
+    if (v0 + i >= a.V) break;
+    int64_t off = 0;
+    for (int j = lane; j < i; j += 32) off += d_s[j];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) off += __shfl_xor_sync(kFull, off, o);
+    const int32_t d = d_s[i];
+    int32_t k;
+    const int64_t u = list_unit(a, v0 + i, a.src, k);
+    int4 *hdr = reinterpret_cast<int4 *>(a.unit_hdr);
+    if (kFork) {
+      const int64_t w = list_unit(a, v0 + i, a.dst, k);
+      const int4 h = hdr[u];
+      for (int32_t j = lane; j < d; j += 32) {
+        const int32_t id = a.free_list[(at0 + off + j) % static_cast<uint64_t>(a.F)];
+        if (id < 0 || id >= a.F) {  // the ring is not what the contract says: skip the page
+          set_error(a.status, DKV_E_INTERNAL);
+          a.list[before + off + j] = make_int2(-1, -1);
+          continue;
+        }
+        a.list[before + off + j] = make_int2(a.fwd[u * a.pmax + j], id);
+        a.fwd[w * a.pmax + j] = id;
+        a.rev_unit[id] = static_cast<int32_t>(a.unit_base + w);
+        a.rev_idx[id] = j;
+        a.page_cls[id] = j < h.z ? DKV_CLASS_K8V4 : DKV_CLASS_K4V2;
+      }
+      for (int32_t j = d + lane; j < a.pmax; j += 32) a.fwd[w * a.pmax + j] = -1;
+      if (lane == 0) hdr[w] = h;
+    } else {
+      for (int32_t j = lane; j < d; j += 32) {
+        const int32_t id = a.fwd[u * a.pmax + j];
+        a.free_list[(at0 + off + j) % static_cast<uint64_t>(a.F)] = id;
+        a.rev_unit[id] = -1;
+        a.rev_idx[id] = -1;
+        a.page_cls[id] = 0;
+        a.fwd[u * a.pmax + j] = -1;
+      }
+      if (lane == 0) hdr[u] = make_int4(0, 0, 0, 0);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ copies --
+
+constexpr int kUnroll = 8;  // 16-byte loads in flight per lane
+
+// One warp copies n 16-byte words.
+__device__ __forceinline__ void warp_copy(uint4 *dst, const uint4 *src, int32_t n, int lane) {
+  for (int32_t c = lane; c < n; c += 32 * kUnroll) {
+    uint4 x[kUnroll];
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i)
+      if (c + 32 * i < n) x[i] = __ldcs(src + c + 32 * i);
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i)
+      if (c + 32 * i < n) __stcs(dst + c + 32 * i, x[i]);
+  }
+}
+
+constexpr int64_t kRowPiece = 4096;  // bytes of a row array one warp copies
+
+// Piece p of the rows [0, ctx) of one (layer, fork) in an array with `row`
+// bytes a position; `base` is the array at that layer.
+__device__ __forceinline__ void copy_rows(uint8_t *base, const PageOpArgs &a, int32_t src, int32_t dst, int64_t row,
+                                          int64_t p, int lane) {
+  const int64_t bytes = __ldg(a.ctx_lens + src) * row, o = p * kRowPiece;
+  if (o >= bytes) return;
+  const uint8_t *s = base + src * (a.cap * row) + o;
+  uint8_t *d = base + dst * (a.cap * row) + o;
+  const int64_t n = min(bytes - o, kRowPiece);
+  warp_copy(reinterpret_cast<uint4 *>(d), reinterpret_cast<const uint4 *>(s), static_cast<int32_t>(n / 16), lane);
+  for (int64_t c = (n & ~int64_t(15)) + lane; c < n; c += 32) d[c] = s[c];
+}
+
+// A warp per page of the copy list, then a warp per piece of the row arrays.
+__global__ void __launch_bounds__(kThreads) k_fork_copy(PageOpArgs a) {
+  const int64_t total = a.ws->total;
+  if (total < 0) return;
+  const int lane = threadIdx.x & 31;
+  const int64_t warp = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
+  const int64_t b = a.page_bytes;
+  for (int64_t j = warp; j < total; j += step) {
+    const int2 p = a.list[j];
+    if (p.x < 0) continue;
+    warp_copy(reinterpret_cast<uint4 *>(a.pages + p.y * b), reinterpret_cast<const uint4 *>(a.pages + p.x * b),
+              static_cast<int32_t>(b / 16), lane);
+  }
+  if (!a.ctx_lens) return;
+  // row pieces of one (layer, fork): classes, slots, significance, counts
+  const int64_t row[4] = {a.classes ? a.Hkv : 0, a.slot_of ? 4 * a.Hkv : 0, a.sig_sum ? 4 * a.Hq : 0,
+                          a.sig_cnt ? 4 : 0};
+  int64_t per = 0, np[4];
+  for (int i = 0; i < 4; ++i) per += np[i] = (a.cap * row[i] + kRowPiece - 1) / kRowPiece;
+  uint8_t *base[4] = {a.classes, reinterpret_cast<uint8_t *>(a.slot_of), reinterpret_cast<uint8_t *>(a.sig_sum),
+                      reinterpret_cast<uint8_t *>(a.sig_cnt)};
+  for (int64_t j = warp; j < per * a.L * a.n; j += step) {
+    int64_t p = j % per;
+    const int64_t lk = j / per;
+    const int32_t k = static_cast<int32_t>(lk % a.n), l = static_cast<int32_t>(lk / a.n);
+    int i = 0;
+    while (p >= np[i]) p -= np[i++];
+    if (i == 3 && l != 0) continue;  // the counts are shared by the layers
+    copy_rows(base[i] + l * (static_cast<int64_t>(a.R) * a.cap * row[i]), a, __ldg(a.src + k), __ldg(a.dst + k),
+              row[i], p, lane);
+  }
+}
+
+// ------------------------------------------------------------------ defrag --
+
+// kDefragPages page ids a block: free pages below n (the live count) and live
+// pages at or above it are counted; what the tables say of each live page is
+// checked.  part = {holes, movers << 32 | error}.
+__global__ void __launch_bounds__(kThreads) k_defrag_plan(PageOpArgs a) {
+  __shared__ int64_t sm[kWarps];
+  __shared__ int32_t err_s;
+  if (threadIdx.x == 0) err_s = 0;
+  __syncthreads();
+  const uint64_t head = a.cursors[0], tail = a.cursors[1];
+  const int64_t n = a.F - static_cast<int64_t>(tail - head);
+  const bool ok = tail >= head && n >= 0;
+  int64_t holes = 0, movers = 0;
+  const int64_t p0 = static_cast<int64_t>(blockIdx.x) * kDefragPages;
+  for (int i = threadIdx.x; i < kDefragPages && p0 + i < a.F; i += kThreads) {
+    const int64_t p = p0 + i;
+    const int32_t u = a.rev_unit[p];
+    const uint8_t c = a.page_cls[p];
+    bool good = ok && (c == 0) == (u < 0);
+    if (c != 0 && good) {
+      const int64_t t = u - a.unit_base;
+      const int32_t j = a.rev_idx[p];
+      good = t >= 0 && t < a.U && j >= 0 && j < a.pmax && a.fwd[t * a.pmax + j] == p;
+    }
+    if (!good) err_s = 1;
+    if (c == 0 && p < n) ++holes;
+    if (c != 0 && p >= n) ++movers;
+  }
+  holes = block_sum(holes, sm);
+  movers = block_sum(movers, sm);
+  if (threadIdx.x == 0) {
+    a.part[blockIdx.x] = make_longlong2(holes, (movers << 1) | err_s);
+    if (blockIdx.x == 0) {
+      a.ws->head = head;
+      a.ws->tail = tail;
+    }
+  }
+}
+
+// Same blocks: the block's holes and movers go to the lists at the ranks the
+// sums before give, in ascending order of id.
+__global__ void __launch_bounds__(kThreads) k_defrag_list(PageOpArgs a, int32_t nparts) {
+  __shared__ int64_t sm[kWarps];
+  __shared__ int32_t wsum[2][kWarps];
+  int64_t hb = 0, ht = 0, mb = 0, mt = 0, bad = 0;
+  for (int32_t i = threadIdx.x; i < nparts; i += kThreads) {
+    const longlong2 p = a.part[i];
+    ht += p.x;
+    mt += p.y >> 1;
+    bad += p.y & 1;
+    if (i < static_cast<int32_t>(blockIdx.x)) {
+      hb += p.x;
+      mb += p.y >> 1;
+    }
+  }
+  ht = block_sum(ht, sm);
+  mt = block_sum(mt, sm);
+  bad = block_sum(bad, sm);
+  hb = block_sum(hb, sm);
+  mb = block_sum(mb, sm);
+  const bool fail = bad != 0 || ht != mt;
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    a.ws->total = fail ? -1 : mt;
+    if (fail) set_error(a.status, DKV_E_INTERNAL);
+  }
+  if (fail) return;
+  const int64_t n = a.F - static_cast<int64_t>(a.ws->tail - a.ws->head);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t p0 = static_cast<int64_t>(blockIdx.x) * kDefragPages;
+  for (int i0 = 0; i0 < kDefragPages && p0 + i0 < a.F; i0 += kThreads) {
+    const int64_t p = p0 + i0 + threadIdx.x;
+    const bool live = p < a.F && a.page_cls[p] != 0;
+    const bool hole = p < a.F && p < n && !live, mover = p >= n && live;
+    const uint32_t hm = __ballot_sync(kFull, hole), mm = __ballot_sync(kFull, mover);
+    if (lane == 0) {
+      wsum[0][warp] = __popc(hm);
+      wsum[1][warp] = __popc(mm);
+    }
+    __syncthreads();
+    int64_t h = hb, m = mb;
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) {
+        h += wsum[0][w];
+        m += wsum[1][w];
+      }
+      hb += wsum[0][w];
+      mb += wsum[1][w];
+    }
+    const uint32_t below = (1u << lane) - 1u;
+    if (hole) a.list[h + __popc(hm & below)].y = static_cast<int32_t>(p);
+    if (mover) a.list[m + __popc(mm & below)].x = static_cast<int32_t>(p);
+    __syncthreads();
+  }
+}
+
+// A warp per move: the page's bytes, its reverse entry and class, the owner's
+// forward entry; then the free list and the cursors.  Sources (ids >= n) and
+// destinations (ids < n) are disjoint, so the order of the moves is free.
+__global__ void __launch_bounds__(kThreads) k_defrag_move(PageOpArgs a) {
+  const int64_t total = a.ws->total;
+  if (total < 0) return;
+  const int lane = threadIdx.x & 31;
+  const int64_t warp = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
+  const int64_t b = a.page_bytes;
+  for (int64_t j = warp; j < total; j += step) {
+    const int2 p = a.list[j];  // x: the page that moves, y: where to
+    if (lane == 0) {
+      const int32_t u = a.rev_unit[p.x], k = a.rev_idx[p.x];
+      a.rev_unit[p.y] = u;
+      a.rev_idx[p.y] = k;
+      a.page_cls[p.y] = a.page_cls[p.x];
+      a.fwd[(u - a.unit_base) * a.pmax + k] = p.y;
+      a.rev_unit[p.x] = -1;
+      a.rev_idx[p.x] = -1;
+      a.page_cls[p.x] = 0;
+    }
+    warp_copy(reinterpret_cast<uint4 *>(a.pages + p.y * b), reinterpret_cast<const uint4 *>(a.pages + p.x * b),
+              static_cast<int32_t>(b / 16), lane);
+  }
+  const uint64_t head = a.ws->head, tail = a.ws->tail, F = static_cast<uint64_t>(a.F);
+  const uint64_t n = F - (tail - head);
+  for (int64_t i = n + blockIdx.x * kThreads + threadIdx.x; i < a.F; i += static_cast<int64_t>(gridDim.x) * kThreads)
+    a.free_list[i] = static_cast<int32_t>(i);
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    const uint64_t h = head + (n + F - head % F) % F;  // the next value that is n mod F
+    a.cursors[0] = h;
+    a.cursors[1] = h + (F - n);
+  }
+}
+
+int copy_grid(int64_t warps, int sms) {
+  // 8 blocks of 256 threads fill an SM
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((warps + kWarps - 1) / kWarps, int64_t{sms} * 8)));
+}
+
+}  // namespace
+
+cudaError_t launch_fork(const PageOpArgs &a, int sms, cudaStream_t s) {
+  const int32_t parts = static_cast<int32_t>((a.V + kPlanUnits - 1) / kPlanUnits);
+  const size_t bits = 8 * static_cast<size_t>((a.R + 31) / 32);
+  k_list_plan<true><<<parts, kThreads, bits, s>>>(a);
+  if (cudaError_t e = cudaGetLastError()) return e;
+  k_list_place<true><<<parts, kThreads, 0, s>>>(a, parts);
+  if (cudaError_t e = cudaGetLastError()) return e;
+  const int64_t most = a.V * a.pmax + (a.ctx_lens ? static_cast<int64_t>(a.L) * a.n * (a.cap / 16 + 4) : 0);
+  k_fork_copy<<<copy_grid(most, sms), kThreads, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_release(const PageOpArgs &a, cudaStream_t s) {
+  const int32_t parts = static_cast<int32_t>((a.V + kPlanUnits - 1) / kPlanUnits);
+  const size_t bits = 8 * static_cast<size_t>((a.R + 31) / 32);
+  k_list_plan<false><<<parts, kThreads, bits, s>>>(a);
+  if (cudaError_t e = cudaGetLastError()) return e;
+  k_list_place<false><<<parts, kThreads, 0, s>>>(a, parts);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_defrag(const PageOpArgs &a, int sms, cudaStream_t s) {
+  const int32_t parts = static_cast<int32_t>((a.F + kDefragPages - 1) / kDefragPages);
+  k_defrag_plan<<<parts, kThreads, 0, s>>>(a);
+  if (cudaError_t e = cudaGetLastError()) return e;
+  k_defrag_list<<<parts, kThreads, 0, s>>>(a, parts);
+  if (cudaError_t e = cudaGetLastError()) return e;
+  k_defrag_move<<<copy_grid(a.F, sms), kThreads, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace dkv

@@ -99,6 +99,30 @@ class dkv_prefill_batch(ctypes.Structure):
     ]
 
 
+class dkv_extend_batch(ctypes.Structure):
+    _fields_ = [
+        ("L", ctypes.c_int32), ("R", ctypes.c_int32), ("Hq", ctypes.c_int32), ("Hkv", ctypes.c_int32),
+        ("cap", ctypes.c_int32), ("layer0", ctypes.c_int32), ("n_layers", ctypes.c_int32),
+        ("max_new", ctypes.c_int32), ("T", ctypes.c_int64), ("q", ctypes.c_void_p), ("k_new", ctypes.c_void_p),
+        ("v_new", ctypes.c_void_p), ("new_lens", ctypes.c_void_p), ("ctx_lens", ctypes.c_void_p),
+        ("scale", ctypes.c_float), ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+    ]
+
+
+class dkv_fork_batch(ctypes.Structure):
+    _fields_ = [
+        ("L", ctypes.c_int32), ("R", ctypes.c_int32), ("Hq", ctypes.c_int32), ("Hkv", ctypes.c_int32),
+        ("cap", ctypes.c_int32), ("n", ctypes.c_int32), ("unit_base", ctypes.c_int64), ("src", ctypes.c_void_p),
+        ("dst", ctypes.c_void_p), ("ctx_lens", ctypes.c_void_p), ("classes", ctypes.c_void_p),
+        ("slot_of", ctypes.c_void_p), ("sig_sum", ctypes.c_void_p), ("sig_cnt", ctypes.c_void_p),
+    ]
+
+
+class dkv_release_batch(ctypes.Structure):
+    _fields_ = [("L", ctypes.c_int32), ("R", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("n", ctypes.c_int32),
+                ("unit_base", ctypes.c_int64), ("reqs", ctypes.c_void_p)]
+
+
 def load():
     """Load libdkv.so (raises if it was not built)."""
     global _lib
@@ -128,6 +152,13 @@ def load():
                              vp], i32),
         "dkv_decode_attention": ([P(dkv_attn_batch), P(dkv_pool), P(dkv_tables), vp], i32),
         "dkv_prefill_attention": ([P(dkv_prefill_batch), P(dkv_pool), vp], i32),
+        "dkv_extend_workspace_size": ([P(dkv_extend_batch), P(dkv_pool), P(dkv_tables), P(ctypes.c_size_t)], i32),
+        "dkv_extend_attention": ([P(dkv_extend_batch), P(dkv_pool), P(dkv_tables), vp, ctypes.c_size_t, vp], i32),
+        "dkv_extend_significance": ([P(dkv_extend_batch), vp, vp, P(dkv_pool), P(dkv_tables), vp], i32),
+        "dkv_page_ops_workspace_size": ([P(dkv_pool), i64, P(ctypes.c_size_t)], i32),
+        "dkv_fork": ([P(dkv_fork_batch), P(dkv_pool), P(dkv_tables), vp, ctypes.c_size_t, vp], i32),
+        "dkv_release": ([P(dkv_release_batch), P(dkv_pool), P(dkv_tables), vp, ctypes.c_size_t, vp], i32),
+        "dkv_defrag": ([P(dkv_pool), P(dkv_tables), i64, i64, vp, ctypes.c_size_t, vp], i32),
         "dkv_profiler_create": ([i32, P(vp)], i32),
         "dkv_profiler_read": ([vp, vp, i32], i32),
         "dkv_profiler_destroy": ([vp], i32),
@@ -181,6 +212,25 @@ class DevicePool:
         self.pages = torch.empty((self.F, dkv_page_bytes(self.scheme, self.P)), dtype=torch.uint8, device=d)
         self.status = torch.zeros(1, dtype=torch.int32, device=d)
 
+    @classmethod
+    def from_tensors(cls, P: int, scheme: int, free_list, cursors, rev_unit, rev_idx, page_cls, pages,
+                     status) -> "DevicePool":
+        """A pool over device tensors that the caller allocated and keeps in a
+        valid state (F is the length of free_list)."""
+        self = cls.__new__(cls)
+        self.F, self.P, self.scheme = int(free_list.numel()), int(P), int(scheme)
+        self.free_list, self.cursors, self.rev_unit, self.rev_idx = free_list, cursors, rev_unit, rev_idx
+        self.page_cls, self.pages, self.status = page_cls, pages, status
+        for name, dtype, n in (("free_list", torch.int32, self.F), ("cursors", torch.int64, 2),
+                               ("rev_unit", torch.int32, self.F), ("rev_idx", torch.int32, self.F),
+                               ("page_cls", torch.uint8, self.F),
+                               ("pages", torch.uint8, self.F * dkv_page_bytes(self.scheme, self.P)),
+                               ("status", torch.int32, 1)):
+            t = getattr(self, name)
+            if t.dtype != dtype or t.numel() != n or not t.is_contiguous():
+                raise ValueError(f"{name}: a contiguous {dtype} tensor of {n} elements is wanted")
+        return self
+
     def c(self) -> dkv_pool:
         return dkv_pool(self.F, self.P, self.scheme, _p(self.free_list), _p(self.cursors), _p(self.rev_unit),
                         _p(self.rev_idx), _p(self.page_cls), _p(self.pages), _p(self.status))
@@ -191,6 +241,16 @@ class DeviceTables:
         self.pmax = int(pmax)
         self.fwd = torch.empty((U, self.pmax), dtype=torch.int32, device=device)
         self.unit_hdr = torch.empty((U, 4), dtype=torch.int32, device=device)
+
+    @classmethod
+    def from_tensors(cls, fwd: torch.Tensor, unit_hdr: torch.Tensor) -> "DeviceTables":
+        """Tables over the caller's int32 tensors fwd [U][pmax] and unit_hdr [U][4]."""
+        if fwd.dtype != torch.int32 or unit_hdr.dtype != torch.int32 or fwd.dim() != 2 or \
+                tuple(unit_hdr.shape) != (fwd.shape[0], 4) or not (fwd.is_contiguous() and unit_hdr.is_contiguous()):
+            raise ValueError("fwd [U][pmax] and unit_hdr [U][4]: contiguous int32 tensors are wanted")
+        self = cls.__new__(cls)
+        self.pmax, self.fwd, self.unit_hdr = int(fwd.shape[1]), fwd, unit_hdr
+        return self
 
     def c(self) -> dkv_tables:
         return dkv_tables(_p(self.fwd), self.pmax, 0, _p(self.unit_hdr))
@@ -371,6 +431,98 @@ def dkv_prefill_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, len
         raise DkvError(rc, "dkv_prefill_attention")
 
 
+# ------------------------------------- several tokens a request, page operations --
+
+def make_extend_batch(L: int, Hkv: int, cap: int, q: torch.Tensor, new_lens: torch.Tensor, ctx_lens: torch.Tensor,
+                      max_new: int, scale: float, k_new: torch.Tensor | None = None,
+                      v_new: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                      lse: torch.Tensor | None = None, layer0: int = 0) -> dkv_extend_batch:
+    """q, out bf16 [n_layers][T][Hq][128]; k_new, v_new bf16 [n_layers][T][Hkv][128]; lse fp32 [n_layers][T][Hq]."""
+    n_layers, T, Hq = int(q.shape[0]), int(q.shape[1]), int(q.shape[2])
+    return dkv_extend_batch(int(L), int(new_lens.numel()), Hq, int(Hkv), int(cap), int(layer0), n_layers,
+                            int(max_new), T, _p(q), _p(k_new), _p(v_new), _p(new_lens), _p(ctx_lens), float(scale),
+                            _p(out), _p(lse))
+
+
+def dkv_extend_workspace_size(batch: dkv_extend_batch, pool: DevicePool, tables) -> int:
+    n = ctypes.c_size_t(0)
+    pc, tc = pool.c(), tables.c()
+    rc = load().dkv_extend_workspace_size(ctypes.byref(batch), ctypes.byref(pc), ctypes.byref(tc), ctypes.byref(n))
+    if rc != DKV_OK:
+        raise DkvError(rc, "dkv_extend_workspace_size")
+    return int(n.value)
+
+
+def _workspace(w: torch.Tensor | None):
+    return (None, 0) if w is None or w.numel() == 0 else (_p(w), w.numel() * w.element_size())
+
+
+def dkv_extend_attention(batch: dkv_extend_batch, pool: DevicePool, tables, workspace: torch.Tensor | None,
+                         stream=None) -> None:
+    pc, tc = pool.c(), tables.c()
+    rc = load().dkv_extend_attention(ctypes.byref(batch), ctypes.byref(pc), ctypes.byref(tc), *_workspace(workspace),
+                                     _stream(stream))
+    if rc != DKV_OK:
+        raise DkvError(rc, "dkv_extend_attention")
+
+
+def dkv_extend_significance(batch: dkv_extend_batch, acc_lens: torch.Tensor, sig_sum: torch.Tensor,
+                            pool: DevicePool, tables, stream=None) -> None:
+    pc, tc = pool.c(), tables.c()
+    rc = load().dkv_extend_significance(ctypes.byref(batch), _p(acc_lens), _p(sig_sum), ctypes.byref(pc),
+                                        ctypes.byref(tc), _stream(stream))
+    if rc != DKV_OK:
+        raise DkvError(rc, "dkv_extend_significance")
+
+
+def dkv_page_ops_workspace_size(pool: DevicePool, tables) -> int:
+    n = ctypes.c_size_t(0)
+    pc = pool.c()
+    rc = load().dkv_page_ops_workspace_size(ctypes.byref(pc), int(tables.fwd.shape[0]), ctypes.byref(n))
+    if rc != DKV_OK:
+        raise DkvError(rc, "dkv_page_ops_workspace_size")
+    return int(n.value)
+
+
+def make_fork_batch(L: int, R: int, Hq: int, Hkv: int, cap: int, src: torch.Tensor, dst: torch.Tensor,
+                    ctx_lens: torch.Tensor | None = None, classes: torch.Tensor | None = None,
+                    slot_of: torch.Tensor | None = None, sig_sum: torch.Tensor | None = None,
+                    sig_cnt: torch.Tensor | None = None, unit_base: int = 0) -> dkv_fork_batch:
+    if src.numel() != dst.numel():
+        raise ValueError("src and dst name the same number of requests")
+    return dkv_fork_batch(int(L), int(R), int(Hq), int(Hkv), int(cap), int(src.numel()), int(unit_base), _p(src),
+                          _p(dst), _p(ctx_lens), _p(classes), _p(slot_of), _p(sig_sum), _p(sig_cnt))
+
+
+def make_release_batch(L: int, R: int, Hkv: int, reqs: torch.Tensor, unit_base: int = 0) -> dkv_release_batch:
+    return dkv_release_batch(int(L), int(R), int(Hkv), int(reqs.numel()), int(unit_base), _p(reqs))
+
+
+def dkv_fork(batch: dkv_fork_batch, pool: DevicePool, tables, workspace: torch.Tensor, stream=None) -> None:
+    pc, tc = pool.c(), tables.c()
+    rc = load().dkv_fork(ctypes.byref(batch), ctypes.byref(pc), ctypes.byref(tc), *_workspace(workspace),
+                         _stream(stream))
+    if rc != DKV_OK:
+        raise DkvError(rc, "dkv_fork")
+
+
+def dkv_release(batch: dkv_release_batch, pool: DevicePool, tables, workspace: torch.Tensor, stream=None) -> None:
+    pc, tc = pool.c(), tables.c()
+    rc = load().dkv_release(ctypes.byref(batch), ctypes.byref(pc), ctypes.byref(tc), *_workspace(workspace),
+                            _stream(stream))
+    if rc != DKV_OK:
+        raise DkvError(rc, "dkv_release")
+
+
+def dkv_defrag(pool: DevicePool, tables, workspace: torch.Tensor, unit_base: int = 0, stream=None) -> None:
+    """Pack the pool; `tables` hold every unit that owns pages of it."""
+    pc, tc = pool.c(), tables.c()
+    rc = load().dkv_defrag(ctypes.byref(pc), ctypes.byref(tc), int(tables.fwd.shape[0]), int(unit_base),
+                           *_workspace(workspace), _stream(stream))
+    if rc != DKV_OK:
+        raise DkvError(rc, "dkv_defrag")
+
+
 class _TableView:
     """Tables of a contiguous run of units (pointer offsets into DeviceTables)."""
 
@@ -402,7 +554,7 @@ class Decoder:
         self.slot_of = torch.full((rows,), -1, dtype=torch.int32, device=device)
         self.workspace = torch.empty(dkv_decode_workspace_size(self.batch({})), dtype=torch.uint8, device=device)
         dkv_init_pool(self.pool)
-        self._pre_ws = None
+        self._pre_ws = self._ext_ws = self._ops_ws = None
 
     def batch(self, d: dict) -> dkv_decode_batch:
         g = d.get
@@ -438,3 +590,46 @@ class Decoder:
         b = dkv_attn_batch(self.L, self.R, self.Hq, self.Hkv, self.cap, int(layer0), int(q.shape[0]), _p(q),
                            _p(k_new), _p(v_new), _p(new_lens), _p(ctx_lens), float(scale), _p(out), _p(sig_sum))
         dkv_decode_attention(b, self.pool, self.tables, stream=stream)
+
+    def extend(self, q: torch.Tensor, new_lens: torch.Tensor, ctx_lens: torch.Tensor, max_new: int, out: torch.Tensor,
+               scale: float, k_new: torch.Tensor | None = None, v_new: torch.Tensor | None = None,
+               lse: torch.Tensor | None = None, layer0: int = 0, stream=None) -> None:
+        """dkv_extend_attention of several new tokens a request over layers [layer0, layer0 + q.shape[0])."""
+        b = make_extend_batch(self.L, self.Hkv, self.cap, q, new_lens, ctx_lens, max_new, scale, k_new=k_new,
+                              v_new=v_new, out=out, lse=lse, layer0=layer0)
+        need = dkv_extend_workspace_size(b, self.pool, self.tables)
+        if need and (self._ext_ws is None or self._ext_ws.numel() < need):
+            self._ext_ws = torch.empty(need, dtype=torch.uint8, device=self.device)
+        dkv_extend_attention(b, self.pool, self.tables, self._ext_ws, stream=stream)
+
+    def extend_significance(self, q: torch.Tensor, new_lens: torch.Tensor, acc_lens: torch.Tensor,
+                            ctx_lens: torch.Tensor, max_new: int, scale: float, lse: torch.Tensor,
+                            sig_sum: torch.Tensor, k_new: torch.Tensor | None = None,
+                            v_new: torch.Tensor | None = None, layer0: int = 0, stream=None) -> None:
+        """dkv_extend_significance of the first acc_lens[r] of those tokens."""
+        b = make_extend_batch(self.L, self.Hkv, self.cap, q, new_lens, ctx_lens, max_new, scale, k_new=k_new,
+                              v_new=v_new, lse=lse, layer0=layer0)
+        dkv_extend_significance(b, acc_lens, sig_sum, self.pool, self.tables, stream=stream)
+
+    def _page_ops_ws(self) -> torch.Tensor:
+        if self._ops_ws is None:
+            self._ops_ws = torch.empty(dkv_page_ops_workspace_size(self.pool, self.tables), dtype=torch.uint8,
+                                       device=self.device)
+        return self._ops_ws
+
+    def fork(self, src: torch.Tensor, dst: torch.Tensor, ctx_lens: torch.Tensor, sig_sum: torch.Tensor | None = None,
+             sig_cnt: torch.Tensor | None = None, stream=None) -> None:
+        """dkv_fork: request dst[k] becomes a copy of src[k] (pages, classes, slots and, where given, its
+        significance rows and counts); the caller sets ctx_lens[dst] = ctx_lens[src]."""
+        b = make_fork_batch(self.L, self.R, self.Hq, self.Hkv, self.cap, src, dst, ctx_lens, self.classes,
+                            self.slot_of, sig_sum, sig_cnt)
+        dkv_fork(b, self.pool, self.tables, self._page_ops_ws(), stream=stream)
+
+    def release(self, reqs: torch.Tensor, stream=None) -> None:
+        """dkv_release: the requests' pages go back to the free list; the caller sets their ctx_lens to 0."""
+        dkv_release(make_release_batch(self.L, self.R, self.Hkv, reqs), self.pool, self.tables, self._page_ops_ws(),
+                    stream=stream)
+
+    def defrag(self, stream=None) -> None:
+        """dkv_defrag: the live pages move to the lowest ids."""
+        dkv_defrag(self.pool, self.tables, self._page_ops_ws(), stream=stream)

@@ -392,6 +392,151 @@ typedef struct dkv_prefill_batch {
  * order. */
 int32_t dkv_prefill_attention(const dkv_prefill_batch *b, const dkv_pool *pool, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Attention of several new tokens a request over the unified pages: drafted
+ * tokens to verify, the next turn of a conversation, a chunk of a prompt.
+ *
+ * dkv_decode_attention's definition for new_lens[r] >= 0 query tokens instead
+ * of one.  The batch's T = sum(new_lens) tokens are packed request after
+ * request; token i of request r stands at position ctx_lens[r] + i.  For
+ * query head q of that token (unit (l, r, q / G)) the attended tokens are
+ * every used slot of the unit's high- and low-class lists, with K and V the
+ * dequantised values fma(code, scale, zero), and, when k_new is given, the
+ * request's new tokens 0 .. i (bf16 K and V):
+ *   x_t = scale * (q . k_t),  out = sum_t exp(x_t - lse) v_t,
+ *   lse = log sum_t exp(x_t).
+ * A row that attends nothing gives a zero output and lse = -inf.  The pages
+ * are not changed: tokens that are kept enter the cache through
+ * dkv_decode_step.
+ *
+ * dkv_extend_significance adds to sig_sum what dkv_decode_attention's
+ * significance update adds, for the first acc_lens[r] new tokens of each
+ * request (drafts that were rejected leave no trace): with p(i, t) =
+ * exp(x_t - lse) recomputed from the lse of dkv_extend_attention,
+ *   sig_sum[l][r * cap + pos(t)][q] += sum_{i < acc} p(i, t)   held token t,
+ *   sig_sum[l][r * cap + ctx + j][q] = sum_{j <= i < acc} p(i, j)  new j < acc
+ * (the new tokens' rows when k_new is given).  Each sum is formed by one
+ * thread in a fixed order, so equal inputs give equal bits.  Counts (sig_cnt)
+ * are the caller's: + acc_lens[r] for every held position, acc_lens[r] - j
+ * for new token j.
+ * ------------------------------------------------------------------------ */
+typedef struct dkv_extend_batch {
+  int32_t L, R, Hq, Hkv;     /* the tables' shape, as in dkv_decode_batch; 1 <= Hq / Hkv <= 128 */
+  int32_t cap;               /* positions per request (sig_sum rows); ctx + new <= cap */
+  int32_t layer0, n_layers;  /* attend layers [layer0, layer0 + n_layers) of the tables */
+  int32_t max_new;           /* >= every new_lens[r] */
+  int64_t T;                 /* sum of new_lens */
+  const void *q;             /* bf16 [n_layers][T][Hq][128], 16-byte aligned */
+  const void *k_new;         /* bf16 [n_layers][T][Hkv][128], finite, or NULL; 16-byte aligned */
+  const void *v_new;         /* bf16, as k_new (NULL exactly when k_new is; not read by
+                                dkv_extend_significance) */
+  const int32_t *new_lens;   /* int32 [R], device */
+  const int32_t *ctx_lens;   /* int32 [R], device */
+  float scale;               /* softmax scale, finite */
+  void *out;                 /* out bf16 [n_layers][T][Hq][128], 16-byte aligned (attention only) */
+  float *lse;                /* fp32 [n_layers][T][Hq], natural log: out of the attention (may be
+                                NULL there), in of the significance */
+} dkv_extend_batch;
+
+/* Workspace bytes of dkv_extend_attention (host only; may be 0). */
+int32_t dkv_extend_workspace_size(const dkv_extend_batch *b, const dkv_pool *pool, const dkv_tables *t,
+                                  size_t *bytes);
+
+/* Attention of several new tokens (above), asynchronous; allocates nothing.
+ * workspace: device, 256-byte aligned, >= dkv_extend_workspace_size bytes
+ * (NULL when that is 0), scratch: calls that may overlap on the GPU (two
+ * streams, two captured graphs) need one each.  Pool and tables are read
+ * only.  Synchronous DKV_E_INVAL: a bad shape, pointer or workspace.
+ * Device-side (pool status word): DKV_E_LENS when a new_lens[r] is outside
+ * [0, max_new], ctx_lens[r] + new_lens[r] is outside [0, cap] or the lengths do not add up to T:
+ * nothing is written then; DKV_E_RANGE for a new K or V value that is not
+ * finite (taken as 0); DKV_E_INTERNAL for a unit header or page id that
+ * contradicts the tables (that unit's lists or that page's tokens are left out);
+ * DKV_E_TIMEOUT when a bounded wait gave up (outputs undefined). */
+int32_t dkv_extend_attention(const dkv_extend_batch *b, const dkv_pool *pool, const dkv_tables *t,
+                             void *workspace, size_t workspace_bytes, void *stream);
+
+/* Significance of the accepted new tokens (above), asynchronous; needs no
+ * workspace and allocates nothing.  acc_lens: int32 [R], device, 0 <= acc <=
+ * new; sig_sum: in/out fp32 [L][R * cap][Hq], 16-byte aligned.  A row whose
+ * lse is -inf adds nothing.  Errors as dkv_extend_attention; DKV_E_LENS also
+ * for an acc_lens[r] outside [0, new_lens[r]], DKV_E_INTERNAL also for a
+ * stored position outside [0, ctx_lens[r]) (that token is left out). */
+int32_t dkv_extend_significance(const dkv_extend_batch *b, const int32_t *acc_lens, float *sig_sum,
+                                const dkv_pool *pool, const dkv_tables *t, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Page operations of a pool that serves many requests: a request is forked,
+ * requests leave, a fragmented pool is packed.  All three are all-or-nothing:
+ * on a device-side error (status word) nothing has changed.
+ *
+ * They share one workspace (device, 256-byte aligned, at least
+ * dkv_page_ops_workspace_size bytes for the tables' U units, scratch).
+ * Requests are named by device lists; "list units" of requests q[0..n) are
+ * the units (l, q[k], h) in the order (l, k, h), so a call over L layers
+ * equals L one-layer calls (unit_base and table offsets as in dkv_compact).
+ * ------------------------------------------------------------------------ */
+int32_t dkv_page_ops_workspace_size(const dkv_pool *pool, int64_t U, size_t *bytes);
+
+typedef struct dkv_fork_batch {
+  int32_t L, R, Hq, Hkv;     /* the tables' shape; R <= 65535; Hq is read with sig_sum only */
+  int32_t cap;               /* positions per request; a multiple of 16 */
+  int32_t n;                 /* forks */
+  int64_t unit_base;         /* global id of unit 0 of the tables */
+  const int32_t *src, *dst;  /* int32 [n], device: request dst[k] becomes a copy of src[k] */
+  const int32_t *ctx_lens;   /* int32 [R], device: positions held (read for the rows below; NULL
+                                exactly when all four are) */
+  uint8_t *classes;          /* NULL or in/out [L][R * cap][Hkv], as in dkv_decode_batch */
+  int32_t *slot_of;          /* NULL or in/out [L][R * cap][Hkv] */
+  float *sig_sum;            /* NULL or in/out [L][R * cap][Hq] */
+  int32_t *sig_cnt;          /* NULL or in/out [R * cap] */
+} dkv_fork_batch;
+
+/* Fork requests, asynchronous.  A page has one owner and a generation step
+ * moves and requantises tokens in place, so a fork copies: the d_v pages of
+ * source list unit v are copied to the pages of free-list slots
+ * [head + off_v, head + off_v + d_v) mod F (off_v the exclusive prefix sum of
+ * d_v over the list units), in their order; the destination's forward row,
+ * header, rev_unit, rev_idx and page_cls follow, and head advances by the
+ * sum.  Of each given row array the rows of positions [0, ctx_lens[src]) are
+ * copied to the destination request (16-byte aligned arrays); later rows stay
+ * as they were, and the caller sets ctx_lens[dst].  One source may be forked several times.  Device-side
+ * errors: DKV_E_NOMEM (pages), DKV_E_INTERNAL (a request index out of range, a destination named
+ * twice, that is also a source, or whose units still hold pages; headers or page ids that contradict the
+ * tables), DKV_E_LENS (ctx_lens[src] outside [0, cap]). */
+int32_t dkv_fork(const dkv_fork_batch *b, const dkv_pool *pool, const dkv_tables *t, void *workspace,
+                 size_t workspace_bytes, void *stream);
+
+typedef struct dkv_release_batch {
+  int32_t L, R, Hkv;         /* the tables' shape; R <= 65535 */
+  int32_t n;                 /* requests that leave */
+  int64_t unit_base;         /* global id of unit 0 of the tables */
+  const int32_t *reqs;       /* int32 [n], device */
+} dkv_release_batch;
+
+/* Release requests, asynchronous: the pages of the list units are appended
+ * at the free list's tail in (list unit, page index) order with rev_unit =
+ * rev_idx = -1 and page_cls 0, their forward rows become -1 and their headers
+ * 0, and tail advances by the count.  Page contents, classes, slots and
+ * significance rows stay as they were.  A request without pages releases
+ * none.  Device-side: DKV_E_INTERNAL (a request out of range or named twice;
+ * a header, page id or reverse entry that contradicts the tables). */
+int32_t dkv_release(const dkv_release_batch *b, const dkv_pool *pool, const dkv_tables *t, void *workspace,
+                    size_t workspace_bytes, void *stream);
+
+/* Pack the pool, asynchronous: with n = F - (tail - head) pages live, the
+ * live pages with ids >= n move into the free ids below n, ascending into
+ * ascending, so that the live pages are exactly [0, n).  Contents, rev_unit,
+ * rev_idx, page_cls and the owners' forward entries follow.  The free list becomes
+ * the ids [n, F) in order, at slots of the same numbers: head advances to the
+ * next value that is n mod F and tail = head + F - n (both stay monotone),
+ * so the memory of [n, F) can be handed back.  `t` holds all U units that
+ * own pages of the pool (global ids [unit_base, unit_base + U)).
+ * Device-side: DKV_E_INTERNAL (page classes, reverse entries, forward rows
+ * and cursors contradict one another). */
+int32_t dkv_defrag(const dkv_pool *pool, const dkv_tables *t, int64_t U, int64_t unit_base, void *workspace,
+                   size_t workspace_bytes, void *stream);
+
 /* Synchronise `stream`, return the pool's device status word (DKV_OK or the
  * first device-side error since the last read) and clear it. */
 int32_t dkv_get_status(const dkv_pool *pool, void *stream);

@@ -25,7 +25,7 @@ LIB_PATH_SAN = os.path.join(HERE, "lib", "libdkv_san.so")
 HOST_SAN = ["-Xcompiler", "-fsanitize=address", "-Xcompiler", "-fsanitize=undefined",
             "-Xcompiler", "-fno-sanitize-recover=all", "-Xcompiler", "-fno-omit-frame-pointer"]
 SOURCES = ["api.cu", "classify.cu", "alloc.cu", "pack.cu", "pool.cu", "noalloc.cu", "decode.cu", "attend.cu", "prefill.cu",
-           "maintain.cu", "extend.cu"]
+           "maintain.cu", "extend.cu", "extend_sig.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall"]
 
@@ -39,7 +39,7 @@ def _nvcc() -> str:
 def _stale(obj: str, src: str) -> bool:
     if not os.path.exists(obj):
         return True
-    deps = [src, os.path.join(CSRC, "dkv_internal.cuh"),
+    deps = [src, os.path.join(CSRC, "dkv_internal.cuh"), os.path.join(CSRC, "tensor_ops.cuh"),
             os.path.join(os.path.dirname(HERE), "include", "dkv.h")]
     return os.path.getmtime(obj) < max(os.path.getmtime(d) for d in deps)
 

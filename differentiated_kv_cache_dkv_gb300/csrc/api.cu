@@ -224,6 +224,11 @@ dkv::ExtendArgs extend_args(const dkv_extend_batch *b, const dkv_pool *pool, con
   return a;
 }
 
+dkv::ExtendPlan extend_plan_of(const dkv_extend_batch *b) {
+  return dkv::extend_plan(static_cast<int64_t>(b->n_layers) * b->R * b->Hkv, b->max_new, b->Hq / b->Hkv, b->cap,
+                          b->n_layers * b->T * b->Hq);
+}
+
 // Tables of U units with global ids [unit_base, unit_base + U), and a
 // workspace for the page operations on them.
 bool valid_page_op(const dkv_pool *pool, const dkv_tables *t, int64_t U, int64_t unit_base, const void *ws,
@@ -535,7 +540,9 @@ int32_t dkv_prefill_attention(const dkv_prefill_batch *b, const dkv_pool *pool, 
 int32_t dkv_extend_workspace_size(const dkv_extend_batch *b, const dkv_pool *pool, const dkv_tables *t,
                                   size_t *bytes) {
   if (!bytes || !valid_extend(b, pool, t)) return DKV_E_INVAL;
-  *bytes = 0;
+  const dkv::ExtendPlan p = extend_plan_of(b);
+  if (p.blocks > INT32_MAX) return DKV_E_INVAL;
+  *bytes = p.parts ? p.bytes : 0;
   return DKV_OK;
 }
 
@@ -544,9 +551,10 @@ int32_t dkv_extend_attention(const dkv_extend_batch *b, const dkv_pool *pool, co
   if (!valid_extend(b, pool, t)) return DKV_E_INVAL;
   if (b->T == 0 || b->R == 0 || b->n_layers == 0) return DKV_OK;
   if (!b->out || !aligned(b->out, 16)) return DKV_E_INVAL;
-  (void)workspace;
-  (void)workspace_bytes;
-  return cuda_status(dkv::launch_extend(extend_args(b, pool, t), static_cast<cudaStream_t>(stream)));
+  const dkv::ExtendPlan p = extend_plan_of(b);
+  if (p.blocks > INT32_MAX) return DKV_E_INVAL;
+  if (p.parts && (!workspace || !aligned(workspace, 256) || workspace_bytes < p.bytes)) return DKV_E_INVAL;
+  return cuda_status(dkv::launch_extend(extend_args(b, pool, t), p, workspace, static_cast<cudaStream_t>(stream)));
 }
 
 int32_t dkv_extend_significance(const dkv_extend_batch *b, const int32_t *acc_lens, float *sig_sum,

@@ -429,6 +429,15 @@ struct ExtendArgs {
   int32_t *status;
 };
 
+// How dkv_extend_attention cuts its work: blocks of 128 mt rows, each row's
+// tiles in `splits` runs, and the partial results that are joined afterwards
+// (parts = 0: the blocks write the outputs themselves).
+struct ExtendPlan {
+  int32_t mt, row_tiles, splits, parts;
+  int64_t blocks;
+  size_t o, bytes;  // workspace: float2 [parts][rows] at 0, float [parts][rows][128] at o
+};
+
 }  // namespace dkv
 
 // Launchers (defined in the kernel translation units).
@@ -455,6 +464,7 @@ cudaError_t launch_prefill(const PrefillArgs &a, cudaStream_t s);
 cudaError_t launch_fork(const PageOpArgs &a, int sms, cudaStream_t s);
 cudaError_t launch_release(const PageOpArgs &a, cudaStream_t s);
 cudaError_t launch_defrag(const PageOpArgs &a, int sms, cudaStream_t s);
-cudaError_t launch_extend(const ExtendArgs &a, cudaStream_t s);
+ExtendPlan extend_plan(int64_t units, int32_t max_new, int32_t G, int32_t cap, int64_t rows);
+cudaError_t launch_extend(const ExtendArgs &a, const ExtendPlan &p, void *ws, cudaStream_t s);
 cudaError_t launch_extend_sig(const ExtendArgs &a, cudaStream_t s);
 }  // namespace dkv

@@ -1,302 +1,766 @@
 // extend.cu -- attention of several new tokens a request over the unified
-// pages (dkv_extend_attention), and the significance their accepted ones give
-// (dkv_extend_significance).
+// pages (dkv_extend_attention), on the fifth-generation tensor cores.
 //
 // A row is one (new token i, query head g of the KV head's group), numbered
 // i G + g within its unit.  With codes c, scale s and zero z of a token,
 //   x = scale (s (q . c) + z (sum of q)),  out = sum_t exp(x_t - lse) v_t.
-#include <cuda_fp16.h>
-#include <cuda_runtime.h>
-
+// A block takes 128 MT rows of one unit (MT = 1 or 2) and a contiguous range of the
+// unit's token tiles: 128 tokens of the high list, of the low list, or of the
+// request's new tokens.  Its roles, pipelined through mbarriers:
+//   dequant warps (8)  read the codes of a tile straight from the pages into
+//     registers, one tile ahead, and write two operands to shared memory: K as
+//     the codes themselves in fp16, less the middle code (exact; scale and
+//     zero stay in fp32 and are applied to the logits), and V as
+//     fp16(fma(c, s, z)) -- every cached value is a multiple of 2^-24, so
+//     fp16 holds it to half a step of its 11 bits, subnormals exactly;
+//   softmax warps (2 x 4)  a thread per row: logits, running maximum and sum
+//     in fp32, P = 2^(y - m) in fp16 back into the columns of S.  One thread of
+//     each warpgroup issues its products: O += P V of a tile (P read from
+//     tensor memory) as soon as its P is complete, then S = Q K^T of its next
+//     tile into the same columns (the tensor cores run one thread's products
+//     in order), while the other warpgroup is in its softmax.  A separate
+//     issuing warp would be the seventeenth and cost every thread a quarter of
+//     its registers.
+// Q is scaled per row by a power of two into fp16's range (undone in the
+// exponent's multiply-add), so q . c is exact up to the fp32 accumulation.
+// New tokens: K is scaled per token the same way; V stays the bf16 it is, and
+// that product takes P in bf16 (both operands of one MMA have one type).
+//
+// The maximum is lazy: a row's reference m (a whole number, log2 units) moves
+// only when a logit exceeds it by more than 8, and then the softmax warp
+// itself multiplies its row of O by the exact power of two.  P is stored
+// scaled by 2^7, at most 2^15 (fp16's largest is 2^16), so weights down to
+// 2^-21 of the row's largest keep all 11 bits and 2^-32 is where they vanish.
+//
+// MT = 2 (more than 128 rows): the two softmax warpgroups take 128 rows each
+// and every tile serves both, which halves the conversions per logit.  MT = 1:
+// both take the same rows and every other tile; their two partial results
+// meet, as those of the blocks that share a row's tiles do, in k_extend_merge.
 #include <algorithm>
 #include <cmath>
 
-#include "dkv_internal.cuh"
+#include "tensor_ops.cuh"
 
 namespace dkv {
 
 namespace {
 
-constexpr unsigned kFull = 0xffffffffu;
+using namespace tc;
 
-__device__ __forceinline__ float bf16f(uint16_t x) { return __uint_as_float(static_cast<uint32_t>(x) << 16); }
-__device__ __forceinline__ uint16_t f2bf16(float x) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(0.0f), "f"(x));
-  return static_cast<uint16_t>(r);
+constexpr int kSoftWarps = 8, kDeqWarps = 8;
+constexpr int kThreads = 32 * (kSoftWarps + kDeqWarps);
+constexpr uint32_t kTmemCols = 512;  // S (and P) of warpgroup w at 128 w, O at 256 + 128 w
+constexpr int kMeta = 4;             // ring of the tiles' scales and zeros
+constexpr float kGrow = 8.0f;        // growth of a logit over m that moves m
+constexpr float kLift = 7.0f;        // P = 2^(y - m + kLift)
+
+template <int MT>
+struct __align__(1024) Smem {
+  uint8_t q[MT][kTileBytes];
+  uint8_t k[2][kTileBytes];
+  uint8_t v[2][kTileBytes];
+  float s[kMeta][128], z[kMeta][128];  // per token: scale s and z + mid s, times scale log2 e
+  uint8_t valid[kMeta][128];           // looked at only when a page id of the unit is bad
+  uint64_t qready, kfull[2], kempty[2], vfull[2], vempty[2], mfull[kMeta];
+  uint64_t sfull[2], pready[2], odone[2], done[2];
+  uint32_t tmem;
+  int32_t abort, bad;
+};
+template <int MT>
+constexpr size_t smem_bytes() { return sizeof(Smem<MT>) + 1024; }
+static_assert(smem_bytes<2>() <= 227 * 1024, "shared memory");
+
+struct Partial {
+  float *o;    // [parts][rows][128]
+  float2 *ml;  // [parts][rows]: reference (log2 units, lift included) and sum
+  int64_t rows;
+};
+
+// Quotient and remainder by P with M = 2^32 / P + 1 (the quotient is at most
+// one too large below 2^31).
+__device__ __forceinline__ void split(int32_t t, int32_t P, uint32_t M, int32_t &k, int32_t &r) {
+  k = static_cast<int32_t>(__umulhi(static_cast<uint32_t>(t), M));
+  r = t - k * P;
+  if (r < 0) {
+    --k;
+    r += P;
+  }
 }
 
-// Every length in range and their sum T; `before` gets the tokens of the
-// requests before r.  Warp 0 works, every thread of the block calls it.
-__device__ __forceinline__ bool lens_valid(const ExtendArgs &a, int32_t r, int64_t &before) {
-  __shared__ int64_t before_s;
+// The dequant warps' view of one tile.
+struct Tile {
+  int32_t kind, t0, n;  // 0 high, 1 low, 2 new; first token in its list; tokens
+};
+
+__device__ __forceinline__ Tile tile_at(const Tiles &ts, const Unit &x, int32_t fresh, int32_t j) {
+  Tile t;
+  if (j < ts.hi) t = {0, 128 * j, x.n_hi};
+  else if (j < ts.hi + ts.lo) t = {1, 128 * (j - ts.hi), x.n_lo};
+  else t = {2, 128 * (j - ts.hi - ts.lo), fresh};
+  t.n = min(128, t.n - t.t0);
+  return t;
+}
+
+// ------------------------------------------------------- dequantising warps --
+
+// Four tokens of a tile (tk + 32 p) of one thread: page ids, then codes.
+struct Held {
+  int32_t id[4];
+  uint32_t k[4][4], v[4][4];
+  uint2 md[4];
+};
+
+struct DeqCtx {
+  const ExtendArgs *a;
+  Unit x;
+  uint32_t m1, m2;  // split() by P and 2 P
+  int64_t bytes;
+  int32_t vbase, meta;
+  int tk, c;
+};
+
+__device__ __forceinline__ void fetch_ids(const DeqCtx &d, const Tile &t, Held &h) {
+  if (t.kind == 2) return;
+  const int32_t P = d.a->P;
+#pragma unroll
+  for (int p = 0; p < 4; ++p) {
+    const int32_t i = d.tk + 32 * p;
+    h.id[p] = -1;
+    if (i < t.n) {
+      int32_t k, s;
+      if (t.kind == 0) split(t.t0 + i, P, d.m1, k, s);
+      else split(t.t0 + i, 2 * P, d.m2, k, s), k += d.x.p_hi;
+      h.id[p] = __ldg(d.a->fwd + d.x.u * d.a->pmax + k);
+    }
+  }
+}
+
+// Page and slot of token tk + 32 p, null when there is none.
+__device__ __forceinline__ const uint8_t *page_of(const DeqCtx &d, const Tile &t, const Held &h, int p,
+                                                  int32_t &slot) {
+  const int32_t id = h.id[p];
+  if (id < 0 || id >= d.a->F) return nullptr;
+  int32_t k;
+  if (t.kind == 0) split(t.t0 + d.tk + 32 * p, d.a->P, d.m1, k, slot);
+  else split(t.t0 + d.tk + 32 * p, 2 * d.a->P, d.m2, k, slot);
+  return d.a->pages + id * d.bytes;
+}
+
+template <int W>
+__device__ __forceinline__ void fetch_k(const DeqCtx &d, const Tile &t, Held &h) {
+#pragma unroll
+  for (int p = 0; p < 4; ++p) {
+    int32_t slot;
+    const uint8_t *pg = page_of(d, t, h, p, slot);
+    h.k[p][0] = h.k[p][1] = h.k[p][2] = h.k[p][3] = 0;
+    if (pg) load16<W>(h.k[p], pg + slot * (16 * W) + d.c * (2 * W));
+  }
+}
+
+template <int W>
+__device__ __forceinline__ void fetch_v(const DeqCtx &d, const Tile &t, Held &h) {
+#pragma unroll
+  for (int p = 0; p < 4; ++p) {
+    int32_t slot;
+    const uint8_t *pg = page_of(d, t, h, p, slot);
+    h.v[p][0] = h.v[p][1] = h.v[p][2] = h.v[p][3] = 0;
+    h.md[p] = make_uint2(0, 0);
+    if (pg) {
+      load16<W>(h.v[p], pg + d.vbase + slot * (16 * W) + d.c * (2 * W));
+      h.md[p] = __ldg(reinterpret_cast<const uint2 *>(pg + d.meta + 8 * slot));
+    }
+  }
+}
+
+// The two 16-byte groups of a thread's 16 channels; threads of the upper box
+// write their second group first, so that the eight threads of a row touch
+// eight different chunks.
+__device__ __forceinline__ void store_groups(uint8_t *tile, int row, int c, const uint4 &g0, const uint4 &g1) {
+  const bool up = c >= 4;
+  *reinterpret_cast<uint4 *>(tile + group_at(row, 2 * c + (up ? 1 : 0))) = up ? g1 : g0;
+  *reinterpret_cast<uint4 *>(tile + group_at(row, 2 * c + (up ? 0 : 1))) = up ? g0 : g1;
+}
+
+template <int W, class S>
+__device__ __forceinline__ void convert_k(const DeqCtx &d, const Held &h, S &sm, uint8_t *dst, int slot, float f) {
+  constexpr float kMid = 1 << (W - 1);
+#pragma unroll
+  for (int p = 0; p < 4; ++p) {
+    const int row = d.tk + 32 * p;
+    uint4 g[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      uint32_t w0, w1;
+      __half2 o[4];
+      group_of<W>(h.k[p], i, w0, w1);
+      group_codes<W>(w0, w1, kMid, o);
+      g[i] = make_uint4(h2u(o[0]), h2u(o[1]), h2u(o[2]), h2u(o[3]));
+    }
+    store_groups(dst, row, d.c, g[0], g[1]);
+    if (d.c == 0) {
+      const __half2 m = u2h(h.md[p].x);
+      const float s = __low2float(m), z = __high2float(m);
+      sm.s[slot][row] = s * f;
+      sm.z[slot][row] = fmaf(kMid, s, z) * f;
+      sm.valid[slot][row] = h.id[p] >= 0 && h.id[p] < d.a->F;
+    }
+  }
+}
+
+template <int W>
+__device__ __forceinline__ void convert_v(const DeqCtx &d, const Held &h, uint8_t *dst) {
+#pragma unroll
+  for (int p = 0; p < 4; ++p) {
+    const __half2 m = u2h(h.md[p].y);
+    const __half2 s = __low2half2(m), z = __high2half2(m);
+    uint4 g[2];
+    // a dequantised value can pass fp16's largest by half a scale step
+    const bool big = fmaf(static_cast<float>((1 << W) - 1), __low2float(m), fabsf(__high2float(m))) > 65000.0f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      uint32_t w0, w1;
+      __half2 o[4];
+      group_of<W>(h.v[p], i, w0, w1);
+      group_codes<W>(w0, w1, 0.0f, o);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] = __hfma2(o[e], s, z);
+      if (big) {
+        const __half2 top = __float2half2_rn(65504.0f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = __hmax2(__hmin2(o[e], top), __hneg2(top));
+      }
+      g[i] = make_uint4(h2u(o[0]), h2u(o[1]), h2u(o[2]), h2u(o[3]));
+    }
+    store_groups(dst, d.tk + 32 * p, d.c, g[0], g[1]);
+  }
+}
+
+// 16 bf16 of a new token's row (0 when it has none), not finite -> 0.
+__device__ __forceinline__ void load_new(const DeqCtx &d, const uint16_t *base, int64_t row, bool have, uint4 (&x)[2]) {
+  x[0] = x[1] = make_uint4(0, 0, 0, 0);
+  if (!have) return;
+  const uint4 *src = reinterpret_cast<const uint4 *>(base + row * 128) + 2 * d.c;
+  x[0] = __ldg(src);
+  x[1] = __ldg(src + 1);
+  uint32_t *w = reinterpret_cast<uint32_t *>(x);
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if ((w[i] & 0x7f80u) == 0x7f80u) w[i] &= 0xffff0000u, bad = true;
+    if ((w[i] & 0x7f800000u) == 0x7f800000u) w[i] &= 0x0000ffffu, bad = true;
+  }
+  if (bad) set_error(d.a->status, DKV_E_RANGE);
+}
+
+// K of the new tokens: each row times the power of two that puts its largest
+// value into [2^14, 2^15), in fp16; the scale carries it back.
+template <class S>
+__device__ __forceinline__ void new_k(const DeqCtx &d, const Tile &t, int64_t tok0, int32_t h, S &sm, uint8_t *dst,
+                                      int slot, float f) {
+#pragma unroll 1
+  for (int p = 0; p < 4; ++p) {
+    const int row = d.tk + 32 * p;
+    uint4 x[2];
+    load_new(d, d.a->k_new, (tok0 + t.t0 + row) * d.a->Hkv + h, row < t.n, x);
+    const uint32_t *w = reinterpret_cast<const uint32_t *>(x);
+    float mx = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) mx = fmaxf(mx, fmaxf(fabsf(bf16_lo(w[i])), fabsf(bf16_hi(w[i]))));
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
+    const int e = mx > 0.0f ? min(max(14 + 127 - static_cast<int>(__float_as_uint(mx) >> 23), -120), 120) : 0;
+    const float sc = pow2f(e);
+    uint4 g[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint4 v = x[i];
+      g[i] = make_uint4(f16x2_rn(bf16_lo(v.x) * sc, bf16_lo(v.z) * sc), f16x2_rn(bf16_hi(v.x) * sc, bf16_hi(v.z) * sc),
+                        f16x2_rn(bf16_lo(v.y) * sc, bf16_lo(v.w) * sc), f16x2_rn(bf16_hi(v.y) * sc, bf16_hi(v.w) * sc));
+    }
+    store_groups(dst, row, d.c, g[0], g[1]);
+    if (d.c == 0) {
+      sm.s[slot][row] = pow2f(-e) * f;
+      sm.z[slot][row] = 0.0f;
+      sm.valid[slot][row] = 1;
+    }
+  }
+}
+
+__device__ __forceinline__ void new_v(const DeqCtx &d, const Tile &t, int64_t tok0, int32_t h, uint8_t *dst) {
+#pragma unroll 1
+  for (int p = 0; p < 4; ++p) {
+    const int row = d.tk + 32 * p;
+    uint4 x[2];
+    load_new(d, d.a->v_new, (tok0 + t.t0 + row) * d.a->Hkv + h, row < t.n, x);
+    uint32_t g0[4], g1[4];
+    group_bf16(x[0], g0);
+    group_bf16(x[1], g1);
+    store_groups(dst, row, d.c, make_uint4(g0[0], g0[1], g0[2], g0[3]), make_uint4(g1[0], g1[1], g1[2], g1[3]));
+  }
+}
+
+// ------------------------------------------------------------ softmax warps --
+
+// A row of Q (row < rows) into fp16 operand form: the power of two it is
+// scaled by is 2^e; returns the sum of the scaled row.  `dst` may be null.
+__device__ __forceinline__ float stage_q(const uint16_t *src, bool have, uint8_t *dst, int row, int &e) {
+  uint4 x[16];
+  float mx = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    x[i] = have ? __ldg(reinterpret_cast<const uint4 *>(src) + i) : make_uint4(0, 0, 0, 0);
+    mx = max3(mx, max3(fabsf(bf16_lo(x[i].x)), fabsf(bf16_hi(x[i].x)), fabsf(bf16_lo(x[i].y))),
+              max3(fabsf(bf16_hi(x[i].y)), fabsf(bf16_lo(x[i].z)), fabsf(bf16_hi(x[i].z))));
+    mx = max3(mx, fabsf(bf16_lo(x[i].w)), fabsf(bf16_hi(x[i].w)));
+  }
+  e = mx > 0.0f ? min(max(14 + 127 - static_cast<int>(__float_as_uint(mx) >> 23), -120), 120) : 0;
+  const float sc = pow2f(e);
+  float sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const uint4 v = x[i];
+    const float c0 = bf16_lo(v.x) * sc, c1 = bf16_hi(v.x) * sc, c2 = bf16_lo(v.y) * sc, c3 = bf16_hi(v.y) * sc;
+    const float c4 = bf16_lo(v.z) * sc, c5 = bf16_hi(v.z) * sc, c6 = bf16_lo(v.w) * sc, c7 = bf16_hi(v.w) * sc;
+    sum += ((c0 + c1) + (c2 + c3)) + ((c4 + c5) + (c6 + c7));
+    if (dst)
+      *reinterpret_cast<uint4 *>(dst + group_at(row, i)) =
+          make_uint4(f16x2_rn(c0, c4), f16x2_rn(c1, c5), f16x2_rn(c2, c6), f16x2_rn(c3, c7));
+  }
+  return sum;
+}
+
+// Columns of one row of O: 32 values in operand order, to channel order.
+__device__ __forceinline__ void channel_order(const uint32_t *r, float *x) {
+#pragma unroll
+  for (int g = 0; g < 4; ++g)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[8 * g + i] = __uint_as_float(r[8 * g + 2 * i]);
+      x[8 * g + 4 + i] = __uint_as_float(r[8 * g + 2 * i + 1]);
+    }
+}
+
+template <int SC, int MT>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_extend(ExtendArgs a, int32_t row_tiles, int32_t splits, Partial part) {
+  constexpr int KH = scheme_kh(SC), VH = scheme_vh(SC);
+  extern __shared__ unsigned char smem_raw[];
+  Smem<MT> &sm = *reinterpret_cast<Smem<MT> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int32_t sp = static_cast<int32_t>(blockIdx.x % splits);
+  const int64_t ur = blockIdx.x / splits;
+  const int32_t rt = static_cast<int32_t>(ur % row_tiles);
+  const int64_t ui = ur / row_tiles;
+  const int32_t h = static_cast<int32_t>(ui % a.Hkv), r = static_cast<int32_t>((ui / a.Hkv) % a.R);
+  const int32_t li = static_cast<int32_t>(ui / (static_cast<int64_t>(a.Hkv) * a.R));
+  int64_t before;
+  if (!lens_valid(a, r, before)) return;
+  const int32_t rows = __ldg(a.new_lens + r) * a.G, row0 = rt * (128 * MT);
+  if (row0 >= rows) return;
+  const Unit x = load_unit(a, (static_cast<int64_t>(a.layer0 + li) * a.R + r) * a.Hkv + h);
+  const int32_t fresh = a.k_new ? (min(row0 + 128 * MT, rows) - 1) / a.G + 1 : 0;
+  const Tiles ts{(x.n_hi + 127) / 128, (x.n_lo + 127) / 128, (fresh + 127) / 128};
+  // this block's share of the tiles
+  const int32_t nt = ts.count(), per = (nt + splits - 1) / splits;
+  const int32_t j0 = min(nt, sp * per), n = min(nt, j0 + per) - j0;
+  const int64_t tok0 = static_cast<int64_t>(li) * a.T + before;
+  volatile int32_t *abort = &sm.abort;
+
+  if (tid == 0) {
+    mbar_init(&sm.qready, kSoftWarps);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.kfull[i], kDeqWarps);
+      mbar_init(&sm.kempty[i], MT);
+      mbar_init(&sm.vfull[i], kDeqWarps);
+      mbar_init(&sm.vempty[i], MT);
+      mbar_init(&sm.sfull[i], 1);
+      mbar_init(&sm.pready[i], 4);
+      mbar_init(&sm.odone[i], 1);
+      mbar_init(&sm.done[i], 1);
+    }
+    for (int i = 0; i < kMeta; ++i) mbar_init(&sm.mfull[i], kDeqWarps);
+    sm.abort = 0;
+    sm.bad = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 0) tmem_alloc(&sm.tmem, kTmemCols);
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = sm.tmem;
+  // a page id out of range anywhere in the unit: logits are masked token by token
+  for (int32_t k = tid; k < (x.n_hi + a.P - 1) / a.P + (x.n_lo + 2 * a.P - 1) / (2 * a.P); k += kThreads) {
+    const int32_t id = __ldg(a.fwd + x.u * a.pmax + k);
+    if (id < 0 || id >= a.F) {
+      sm.bad = 1;
+      set_error(a.status, DKV_E_INTERNAL);
+    }
+  }
+  __syncthreads();
+  auto wait = [&](uint64_t *bar, uint32_t parity) { return wait_or_abort(bar, parity, abort, a.status); };
+  // the same answer in every lane: the loops below hold warp-wide instructions
+  auto warp_wait = [&](uint64_t *bar, uint32_t parity) { return __all_sync(kFull, wait(bar, parity)) != 0; };
+
+  if (warp < kSoftWarps) {
+    // ================= softmax warps: a thread per row
+    const int wg = warp >> 2, row = tid & 127;
+    const int32_t grow = row0 + (MT == 2 ? 128 * wg : 0) + row;  // row of the unit
+    const bool have = grow < rows;
+    const int32_t qi = grow / a.G, qg = grow - qi * a.G;
+    const int64_t at = (tok0 + qi) * a.Hq + h * a.G + qg;
+    int e;
+    const float qsum = stage_q(a.q + at * 128, have, MT == 2 || wg == 0 ? sm.q[MT == 2 ? wg : 0] : nullptr, row, e);
+    fence_async();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.qready);
+    const float rq = pow2f(-e);
+    const uint64_t qs2 = f2_pack(qsum, qsum), rq2 = f2_pack(rq, rq);
+    const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    const uint32_t ts_s = tmem + lanes + 128 * wg, ts_o = tmem + lanes + 256 + 128 * wg;
+    float m = -INFINITY;
+    uint64_t l2 = f2_pack(0.0f, 0.0f);
+    // one thread issues the warpgroup's products
+    const bool issuer = (warp & 3) == 0 && lane == 0;
+    constexpr uint32_t kStep = kTileBytes >> 4;
+    const uint64_t dq = sw128_desc(saddr(sm.q[MT == 2 ? wg : 0]), 16, 1024);
+    const uint64_t dk = sw128_desc(saddr(sm.k[0]), 16, 1024), dv = sw128_desc(saddr(sm.v[0]), kBox, 1024);
+    // S of tile j: 16 channels a step
+    auto issue_s = [&](int32_t j) {
+      const uint64_t db = dk + (j & 1) * kStep;
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk) {
+        const uint32_t o = ((kk >> 2) * kBox + (kk & 3) * 32) >> 4;
+        mma_ss(tmem + 128 * wg, dq + o, db + o, idesc(false, 128, 128, false), kk > 0 ? 1u : 0u);
+      }
+      mma_commit(&sm.sfull[wg]);
+      mma_commit(&sm.kempty[j & 1]);
+    };
+    // O += P V of tile j: 16 tokens a step (8 columns of P, 16 rows of V)
+    auto issue_o = [&](int32_t j, bool bf16, bool first) {
+      const uint32_t id = bf16 ? idesc(true, 128, 128, true) : idesc(false, 128, 128, true);
+      const uint64_t db = dv + (j & 1) * kStep;
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk)
+        mma_ts(tmem + 256 + 128 * wg, tmem + 128 * wg + 8 * kk, db + ((kk * 2048) >> 4), id, first && kk == 0 ? 0u : 1u);
+      mma_commit(&sm.odone[wg]);
+      mma_commit(&sm.vempty[j & 1]);
+    };
+    const int32_t first = MT == 2 ? 0 : wg, step = MT == 2 ? 1 : 2;
+    if (issuer && first < n && wait(&sm.qready, 0) && wait(&sm.kfull[first & 1], 0)) {
+      fence_after();
+      issue_s(first);
+    }
+    __syncwarp();
+    bool ok = true;
+    int32_t t = 0;  // tiles of this warpgroup
+    for (int32_t j = first; j < n && ok; j += step, ++t) {
+      const Tile tl = tile_at(ts, x, fresh, j0 + j);
+      const int ms = j % kMeta;
+      if (!(ok = warp_wait(&sm.mfull[ms], (j / kMeta) & 1u) && warp_wait(&sm.sfull[wg], t & 1u))) break;
+      fence_after();
+      const int32_t lim = tl.kind == 2 ? min(tl.n, qi - tl.t0 + 1) : tl.n;
+      const bool masked = __any_sync(kFull, lim < 128) || sm.bad;
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        uint32_t u[64];
+        tmem_ld32(ts_s + 64 * hf, u);
+        tmem_ld32(ts_s + 64 * hf + 32, u + 32);
+        tmem_wait_ld();
+        const float4 *s4 = reinterpret_cast<const float4 *>(sm.s[ms] + 64 * hf);
+        const float4 *z4 = reinterpret_cast<const float4 *>(sm.z[ms] + 64 * hf);
+        float mx = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float4 s = s4[i], z = z4[i];
+          float y0, y1, y2, y3;
+          f2_unpack(f2_fma(f2_pack(s.x, s.y), f2_pack(__uint_as_float(u[4 * i]), __uint_as_float(u[4 * i + 1])),
+                           f2_mul(f2_pack(z.x, z.y), qs2)), y0, y1);
+          f2_unpack(f2_fma(f2_pack(s.z, s.w), f2_pack(__uint_as_float(u[4 * i + 2]), __uint_as_float(u[4 * i + 3])),
+                           f2_mul(f2_pack(z.z, z.w), qs2)), y2, y3);
+          u[4 * i] = __float_as_uint(y0);
+          u[4 * i + 1] = __float_as_uint(y1);
+          u[4 * i + 2] = __float_as_uint(y2);
+          u[4 * i + 3] = __float_as_uint(y3);
+        }
+        if (masked) {
+#pragma unroll
+          for (int i = 0; i < 64; ++i)
+            if (64 * hf + i >= lim || (sm.bad && !sm.valid[ms][64 * hf + i])) u[i] = 0xff800000u;  // -inf
+        }
+#pragma unroll
+        for (int i = 0; i < 64; i += 2) mx = max3(mx, __uint_as_float(u[i]), __uint_as_float(u[i + 1]));
+        const float ymax = mx * rq;
+        if (__any_sync(kFull, ymax > m + kGrow)) {  // some row's reference moves
+          const bool grow_ = ymax > m + kGrow;
+          const float mn = grow_ ? ceilf(ymax) : m;
+          const float f = grow_ ? ex2(m - mn) : 1.0f;  // a power of two, 0 at first
+          l2 = f2_mul(l2, f2_pack(f, f));
+          if (hf == 1) {  // P of the tile's first half has the old reference
+            uint32_t pw[32];
+            tmem_ld32(ts_s, pw);
+            tmem_wait_ld();
+            if (tl.kind == 2) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) pw[i] = bf16x2_rn(bf16_lo(pw[i]) * f, bf16_hi(pw[i]) * f);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                const float2 p2 = __half22float2(u2h(pw[i]));
+                pw[i] = f16x2_rn(p2.x * f, p2.y * f);
+              }
+            }
+            tmem_st32(ts_s, pw);
+          }
+          if (t > 0) {  // O of the tiles before
+            if (!(ok = warp_wait(&sm.odone[wg], (t - 1) & 1u))) break;
+            fence_after();
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              uint32_t o[32];
+              tmem_ld32(ts_o + 32 * c, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              tmem_st32(ts_o + 32 * c, o);
+            }
+          }
+          m = mn;
+        }
+        const float mo = m == -INFINITY ? 0.0f : m - kLift;
+        const uint64_t nm2 = f2_pack(-mo, -mo);
+        uint32_t w[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          float y0, y1;
+          f2_unpack(f2_fma(f2_pack(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1])), rq2, nm2), y0, y1);
+          y0 = ex2(y0);
+          y1 = ex2(y1);
+          l2 = f2_add(l2, f2_pack(y0, y1));
+          w[i] = tl.kind == 2 ? bf16x2_rn(y0, y1) : f16x2_rn(y0, y1);
+        }
+        tmem_st32(ts_s + 32 * hf, w);
+      }
+      if (!ok) break;
+      tmem_wait_st();
+      fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.pready[wg]);
+      if (issuer && (ok = wait(&sm.vfull[j & 1], (j >> 1) & 1u) && wait(&sm.pready[wg], t & 1u))) {
+        fence_after();
+        issue_o(j, tl.kind == 2, t == 0);
+        const int32_t jn = j + step;
+        if (jn < n && (ok = wait(&sm.kfull[jn & 1], (jn >> 1) & 1u))) {
+          fence_after();
+          issue_s(jn);
+        }
+      }
+      ok = __all_sync(kFull, ok);
+    }
+    if (issuer) {  // every product of the warpgroup done (also after an abort)
+      mma_commit(&sm.done[wg]);
+      mbar_wait(&sm.done[wg], 0, nullptr);
+    }
+    ok = __all_sync(kFull, ok);
+    // ---- this warpgroup's rows: sums and O
+    float l0, l1;
+    f2_unpack(l2, l0, l1);
+    const float l = l0 + l1, mo = m == -INFINITY ? 0.0f : m - kLift;
+    if (ok && t > 0) ok = warp_wait(&sm.odone[wg], (t - 1) & 1u);
+    fence_after();
+    const bool direct = MT == 2 && splits == 1;
+    const int64_t slot = (MT == 2 ? sp : 2 * sp + wg) * part.rows + at;
+    if (ok) {
+      const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);  // NaN stays NaN
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        uint32_t o[32];
+        float f[32];
+        if (t > 0) {
+          tmem_ld32(ts_o + 32 * c, o);
+          tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = 0;
+        }
+        channel_order(o, f);
+        if (!have) continue;
+        if (direct) {
+          uint4 *dst = reinterpret_cast<uint4 *>(a.out + at * 128 + 32 * c);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            dst[i] = make_uint4(bf16x2_rn(f[8 * i] * inv, f[8 * i + 1] * inv), bf16x2_rn(f[8 * i + 2] * inv, f[8 * i + 3] * inv),
+                                bf16x2_rn(f[8 * i + 4] * inv, f[8 * i + 5] * inv), bf16x2_rn(f[8 * i + 6] * inv, f[8 * i + 7] * inv));
+        } else if (t > 0) {
+          float4 *dst = reinterpret_cast<float4 *>(part.o + slot * 128 + 32 * c);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) dst[i] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+        }
+      }
+      if (have) {
+        if (!direct) part.ml[slot] = make_float2(t > 0 ? mo : -INFINITY, l);
+        else if (a.lse) a.lse[at] = l == 0.0f ? -INFINITY : (mo + log2f(l)) * 0.693147180559945309f;
+      }
+    }
+    fence_before();
+  } else {
+    // ================= dequantising warps
+    const int dt = tid - 32 * kSoftWarps;
+    const PageGeom g = page_geom(SC, a.P);
+    DeqCtx d{&a, x, 0xffffffffu / a.P + 1, 0xffffffffu / (2 * a.P) + 1, g.bytes, static_cast<int32_t>(g.vbase),
+             static_cast<int32_t>(g.meta), dt >> 3, dt & 7};
+    const float f = a.scale * kLog2e;
+    Held hd;
+    bool ok = true;
+    auto load_k = [&](const Tile &t) {
+      if (t.kind == 0) fetch_k<KH>(d, t, hd);
+      else if (t.kind == 1) fetch_k<KH / 2>(d, t, hd);
+    };
+    auto load_v = [&](const Tile &t) {
+      if (t.kind == 0) fetch_v<VH>(d, t, hd);
+      else if (t.kind == 1) fetch_v<VH / 2>(d, t, hd);
+    };
+    Tile t{}, tn{};
+    Held nx;  // ids of the next tile
+    if (n > 0) {
+      t = tile_at(ts, x, fresh, j0);
+      fetch_ids(d, t, hd);
+      load_k(t);
+      load_v(t);
+    }
+    if (n > 1) {
+      tn = tile_at(ts, x, fresh, j0 + 1);
+      fetch_ids(d, tn, nx);
+    }
+    for (int32_t j = 0; j < n; ++j) {
+      const int b = j & 1, ms = j % kMeta;
+      if (j >= 2 && !(ok = warp_wait(&sm.kempty[b], ((j >> 1) - 1) & 1u))) break;
+      if (t.kind == 0) convert_k<KH>(d, hd, sm, sm.k[b], ms, f);
+      else if (t.kind == 1) convert_k<KH / 2>(d, hd, sm, sm.k[b], ms, f);
+      else new_k(d, t, tok0, h, sm, sm.k[b], ms, f);
+      fence_async();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&sm.kfull[b]);
+        mbar_arrive(&sm.mfull[ms]);
+      }
+      const Tile cur = t;
+      if (j + 1 < n) {
+        t = tn;
+#pragma unroll
+        for (int p = 0; p < 4; ++p) hd.id[p] = nx.id[p];
+        load_k(t);
+      }
+      if (j >= 2 && !(ok = warp_wait(&sm.vempty[b], ((j >> 1) - 1) & 1u))) break;
+      if (cur.kind == 0) convert_v<VH>(d, hd, sm.v[b]);
+      else if (cur.kind == 1) convert_v<VH / 2>(d, hd, sm.v[b]);
+      else new_v(d, cur, tok0, h, sm.v[b]);
+      fence_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.vfull[b]);
+      if (j + 1 < n) load_v(t);
+      if (j + 2 < n) {
+        tn = tile_at(ts, x, fresh, j0 + j + 2);
+        fetch_ids(d, tn, nx);
+      }
+    }
+    (void)ok;
+  }
+  __syncwarp();
+  fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    fence_after();
+    tmem_free(tmem, kTmemCols);
+  }
+}
+
+// Joins the partial results of a row: a warp per row, four channels a lane.
+__global__ void __launch_bounds__(256) k_extend_merge(ExtendArgs a, int32_t parts, Partial part) {
   __shared__ int32_t ok_s;
-  if (threadIdx.x < 32) {
-    int64_t b = 0, t = 0;
+  if (threadIdx.x < 32) {  // the lengths were wrong: the attention wrote nothing
+    int64_t t = 0;
     int bad = 0;
     for (int32_t i = threadIdx.x; i < a.R; i += 32) {
       const int32_t n = __ldg(a.new_lens + i), c = __ldg(a.ctx_lens + i);
       if (n < 0 || n > a.max_new || c < 0 || static_cast<int64_t>(c) + n > a.cap) bad = 1;
-      if (a.acc_lens && (__ldg(a.acc_lens + i) < 0 || __ldg(a.acc_lens + i) > n)) bad = 1;
       t += n;
-      if (i < r) b += n;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-      b += __shfl_xor_sync(kFull, b, o);
       t += __shfl_xor_sync(kFull, t, o);
       bad |= __shfl_xor_sync(kFull, bad, o);
     }
-    if (threadIdx.x == 0) {
-      before_s = b;
-      ok_s = !bad && t == a.T;
-      if (!ok_s) set_error(a.status, DKV_E_LENS);
-    }
+    if (threadIdx.x == 0) ok_s = !bad && t == a.T;
   }
   __syncthreads();
-  before = before_s;
-  return ok_s != 0;
+  if (!ok_s) return;
+  const int lane = threadIdx.x & 31;
+  const int64_t at = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  if (at >= part.rows) return;
+  float M = -INFINITY;
+  for (int32_t p = 0; p < parts; ++p) {
+    const float2 ml = part.ml[p * part.rows + at];
+    if (ml.y != 0.0f) M = fmaxf(M, ml.x);
+  }
+  float l = 0.0f;
+  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int32_t p = 0; p < parts; ++p) {
+    const float2 ml = part.ml[p * part.rows + at];
+    if (ml.y == 0.0f) continue;  // attends nothing there (or no tile): O may not be written
+    const float f = ex2(ml.x - M);
+    const float4 v = *reinterpret_cast<const float4 *>(part.o + (p * part.rows + at) * 128 + 4 * lane);
+    l = fmaf(f, ml.y, l);
+    o.x = fmaf(f, v.x, o.x);
+    o.y = fmaf(f, v.y, o.y);
+    o.z = fmaf(f, v.z, o.z);
+    o.w = fmaf(f, v.w, o.w);
+  }
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  *reinterpret_cast<uint2 *>(a.out + at * 128 + 4 * lane) =
+      make_uint2(bf16x2_rn(o.x * inv, o.y * inv), bf16x2_rn(o.z * inv, o.w * inv));
+  if (a.lse && lane == 0) a.lse[at] = l == 0.0f ? -INFINITY : (M + log2f(l)) * 0.693147180559945309f;
 }
 
-// The lists of a unit (empty when its header contradicts itself).
-struct Unit {
-  int64_t u;             // index in the tables
-  int32_t n_hi, n_lo, p_hi;
-};
-
-__device__ __forceinline__ Unit load_unit(const ExtendArgs &a, int64_t u) {
-  const int4 h = *reinterpret_cast<const int4 *>(a.unit_hdr + 4 * u);
-  Unit x{u, h.x, h.y, h.z};
-  if (h.x < 0 || h.y < 0 || h.z != (static_cast<int64_t>(h.x) + a.P - 1) / a.P ||
-      h.w != (static_cast<int64_t>(h.y) + 2 * a.P - 1) / (2 * a.P) || h.z + h.w > a.pmax) {
-    set_error(a.status, DKV_E_INTERNAL);
-    x.n_hi = x.n_lo = x.p_hi = 0;
-  }
-  return x;
-}
-
-// Page and slot of token t of a unit's lists (the high list, then the low
-// list); null when the table's page id is out of range.
-__device__ __forceinline__ const uint8_t *token_page(const ExtendArgs &a, const PageGeom &g, const Unit &x, int32_t t,
-                                                     bool &high, int32_t &slot) {
-  high = t < x.n_hi;
-  int32_t k;
-  if (high) {
-    k = t / a.P;
-    slot = t - k * a.P;
-  } else {
-    const int32_t j = t - x.n_hi;
-    k = j / (2 * a.P);
-    slot = j - k * 2 * a.P;
-    k += x.p_hi;
-  }
-  const int32_t id = __ldg(a.fwd + x.u * a.pmax + k);
-  if (id < 0 || id >= a.F) {
-    set_error(a.status, DKV_E_INTERNAL);
-    return nullptr;
-  }
-  return a.pages + id * g.bytes;
-}
-
-__device__ __forceinline__ float code_of(const uint8_t *row, int ch, int bits) {
-  return static_cast<float>((row[(ch * bits) >> 3] >> ((ch * bits) & 7)) & ((1 << bits) - 1));
-}
-
-constexpr int kRows = 16, kTok = 32;
-
-// Simple form: 16 rows a block, 32 tokens at a time dequantised into shared
-// memory, one warp for four rows, a lane per token (logits) and per four
-// channels (values).
-__global__ void __launch_bounds__(128) k_extend(ExtendArgs a, int32_t tiles) {
-  __shared__ float ks[kTok][129], qs[kRows][128];
-  __shared__ __align__(16) float vs[kTok][132];  // read as float4
-  __shared__ int32_t ok_s[kTok];
-  const int64_t ui = blockIdx.x / tiles;
-  const int32_t tile = blockIdx.x % tiles;
-  const int32_t h = ui % a.Hkv, r = (ui / a.Hkv) % a.R, li = ui / (static_cast<int64_t>(a.Hkv) * a.R);
-  int64_t before;
-  if (!lens_valid(a, r, before)) return;
-  const int32_t n = __ldg(a.new_lens + r), rows = n * a.G, row0 = tile * kRows;
-  if (row0 >= rows) return;
-  const PageGeom g = page_geom(a.scheme, a.P);
-  const Unit x = load_unit(a, (static_cast<int64_t>(a.layer0 + li) * a.R + r) * a.Hkv + h);
-  const int32_t held = x.n_hi + x.n_lo, last_i = min(row0 + kRows - 1, rows - 1) / a.G;
-  const int32_t total = held + (a.k_new ? last_i + 1 : 0);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t tok0 = static_cast<int64_t>(li) * a.T + before;
-  for (int e = threadIdx.x; e < kRows * 128; e += 128) {
-    const int32_t row = row0 + e / 128;
-    qs[e / 128][e % 128] =
-        row < rows ? bf16f(a.q[((tok0 + row / a.G) * a.Hq + h * a.G + row % a.G) * 128 + e % 128]) : 0.0f;
-  }
-  float m[4], l[4], o[4][4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    m[k] = -INFINITY;
-    l[k] = o[k][0] = o[k][1] = o[k][2] = o[k][3] = 0.0f;
-  }
-  for (int32_t t0 = 0; t0 < total; t0 += kTok) {
-    __syncthreads();
-    {
-      const int t = threadIdx.x / 4, c0 = 32 * (threadIdx.x % 4);
-      const int32_t tt = t0 + t;
-      int32_t ok = 0;
-      if (tt < held) {
-        bool high;
-        int32_t slot;
-        const uint8_t *pg = token_page(a, g, x, tt, high, slot);
-        if (pg) {
-          ok = 1;
-          const int kb = high ? g.kh : g.kh / 2, vb = high ? g.vh : g.vh / 2;
-          const __half *md = reinterpret_cast<const __half *>(pg + g.meta + 8 * slot);
-          const float sk = __half2float(md[0]), zk = __half2float(md[1]), sv = __half2float(md[2]),
-                      zv = __half2float(md[3]);
-          const uint8_t *kr = pg + slot * 16 * kb, *vr = pg + g.vbase + slot * 16 * vb;
-          for (int c = c0; c < c0 + 32; ++c) {
-            ks[t][c] = fmaf(code_of(kr, c, kb), sk, zk);
-            vs[t][c] = fmaf(code_of(vr, c, vb), sv, zv);
-          }
-        }
-      } else if (tt < total) {
-        ok = 1;
-        const int64_t row = ((tok0 + tt - held) * a.Hkv + h) * 128;
-        for (int c = c0; c < c0 + 32; ++c) {
-          float k = bf16f(a.k_new[row + c]), v = bf16f(a.v_new[row + c]);
-          if (!isfinite(k) || !isfinite(v)) set_error(a.status, DKV_E_RANGE);
-          ks[t][c] = isfinite(k) ? k : 0.0f;
-          vs[t][c] = isfinite(v) ? v : 0.0f;
-        }
-      }
-      if (!ok)
-        for (int c = c0; c < c0 + 32; ++c) ks[t][c] = vs[t][c] = 0.0f;
-      if (c0 == 0) ok_s[t] = ok;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int row = row0 + 4 * warp + k;
-      const int32_t i = row / a.G, tt = t0 + lane;
-      float s = 0.0f;
-      for (int c = 0; c < 128; ++c) s = fmaf(qs[4 * warp + k][c], ks[lane][c], s);
-      s = ok_s[lane] && (tt < held || tt - held <= i) ? s * a.scale : -INFINITY;
-      float mx = s;
-      for (int w = 16; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, w));
-      const float mn = fmaxf(m[k], mx);
-      if (mn == -INFINITY) continue;
-      const float f = expf(m[k] - mn), p = expf(s - mn);
-      float sum = p;
-      for (int w = 16; w > 0; w >>= 1) sum += __shfl_xor_sync(kFull, sum, w);
-      l[k] = l[k] * f + sum;
-      m[k] = mn;
-      for (int c = 0; c < 4; ++c) o[k][c] *= f;
-      for (int t = 0; t < kTok; ++t) {
-        const float pt = __shfl_sync(kFull, p, t);
-        const float4 v = *reinterpret_cast<const float4 *>(&vs[t][4 * lane]);
-        o[k][0] = fmaf(pt, v.x, o[k][0]);
-        o[k][1] = fmaf(pt, v.y, o[k][1]);
-        o[k][2] = fmaf(pt, v.z, o[k][2]);
-        o[k][3] = fmaf(pt, v.w, o[k][3]);
-      }
-    }
-  }
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int32_t row = row0 + 4 * warp + k;
-    if (row >= rows) continue;
-    const int64_t at = (tok0 + row / a.G) * a.Hq + h * a.G + row % a.G;
-    const float inv = l[k] > 0.0f ? 1.0f / l[k] : 0.0f;
-    for (int c = 0; c < 4; ++c) a.out[at * 128 + 4 * lane + c] = f2bf16(o[k][c] * inv);
-    if (a.lse && lane == 0) a.lse[at] = l[k] > 0.0f ? m[k] + logf(l[k]) : -INFINITY;
-  }
-}
-
-// Simple form: a block per 32 tokens of a unit (held or new), one warp per
-// query head of the group in turn, a lane per token; the rows pass through
-// shared memory 16 at a time.
-__global__ void __launch_bounds__(128) k_extend_sig(ExtendArgs a, int32_t tiles) {
-  __shared__ float ks[kTok][129], qs[4][128];
-  __shared__ int32_t ok_s[kTok], pos_s[kTok];
-  const int64_t ui = blockIdx.x / tiles;
-  const int32_t tile = blockIdx.x % tiles;
-  const int32_t h = ui % a.Hkv, r = (ui / a.Hkv) % a.R, li = ui / (static_cast<int64_t>(a.Hkv) * a.R);
-  int64_t before;
-  if (!lens_valid(a, r, before)) return;
-  const int32_t acc = __ldg(a.acc_lens + r), ctx = __ldg(a.ctx_lens + r);
-  const PageGeom g = page_geom(a.scheme, a.P);
-  const Unit x = load_unit(a, (static_cast<int64_t>(a.layer0 + li) * a.R + r) * a.Hkv + h);
-  const int32_t held = x.n_hi + x.n_lo, total = held + (a.k_new ? acc : 0), t0 = tile * kTok;
-  if (acc == 0 || t0 >= total) return;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t tok0 = static_cast<int64_t>(li) * a.T + before;
-  {
-    const int t = threadIdx.x / 4, c0 = 32 * (threadIdx.x % 4);
-    const int32_t tt = t0 + t;
-    int32_t ok = 0, pos = 0;
-    if (tt < held) {
-      bool high;
-      int32_t slot;
-      const uint8_t *pg = token_page(a, g, x, tt, high, slot);
-      if (pg) {
-        pos = *reinterpret_cast<const int32_t *>(pg + g.pos + 4 * slot);
-        ok = pos >= 0 && pos < ctx;
-        if (!ok) set_error(a.status, DKV_E_INTERNAL);
-        const int kb = high ? g.kh : g.kh / 2;
-        const __half *md = reinterpret_cast<const __half *>(pg + g.meta + 8 * slot);
-        const float sk = __half2float(md[0]), zk = __half2float(md[1]);
-        for (int c = c0; c < c0 + 32; ++c) ks[t][c] = fmaf(code_of(pg + slot * 16 * kb, c, kb), sk, zk);
-      }
-    } else if (tt < total) {
-      ok = 1;
-      pos = ctx + tt - held;
-      const int64_t row = ((tok0 + tt - held) * a.Hkv + h) * 128;
-      for (int c = c0; c < c0 + 32; ++c) {
-        const float k = bf16f(a.k_new[row + c]);
-        if (!isfinite(k)) set_error(a.status, DKV_E_RANGE);
-        ks[t][c] = isfinite(k) ? k : 0.0f;
-      }
-    }
-    if (c0 == 0) {
-      ok_s[t] = ok;
-      pos_s[t] = pos;
-    }
-  }
-  __syncthreads();
-  const int32_t tt = t0 + lane;
-  for (int32_t gq = warp; gq < a.G; gq += 4) {
-    float sum = 0.0f;
-    for (int32_t i = 0; i < acc; ++i) {
-      const int64_t at = (tok0 + i) * a.Hq + h * a.G + gq;
-      __syncwarp();
-      for (int c = lane; c < 128; c += 32) qs[warp][c] = bf16f(a.q[at * 128 + c]);
-      __syncwarp();
-      const float lse = a.lse[at];
-      float s = 0.0f;
-      for (int c = 0; c < 128; ++c) s = fmaf(qs[warp][c], ks[lane][c], s);
-      if (ok_s[lane] && lse != -INFINITY && (tt < held || tt - held <= i)) sum += expf(s * a.scale - lse);
-    }
-    if (ok_s[lane]) {
-      float *dst = a.sig_sum + ((static_cast<int64_t>(a.layer0 + li) * a.R + r) * a.cap + pos_s[lane]) * a.Hq +
-                   h * a.G + gq;
-      *dst = tt < held ? *dst + sum : sum;
-    }
-  }
+template <int SC, int MT>
+cudaError_t launch(const ExtendArgs &a, const ExtendPlan &p, const Partial &part, cudaStream_t s) {
+  const int smem = static_cast<int>(smem_bytes<MT>());
+  if (cudaError_t e = cudaFuncSetAttribute(k_extend<SC, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem))
+    return e;
+  k_extend<SC, MT><<<static_cast<unsigned>(p.blocks), kThreads, smem, s>>>(a, p.row_tiles, p.splits, part);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_extend(const ExtendArgs &a, cudaStream_t s) {
-  const int64_t tiles = (static_cast<int64_t>(a.max_new) * a.G + kRows - 1) / kRows;
-  const int64_t grid = static_cast<int64_t>(a.n_layers) * a.R * a.Hkv * tiles;
-  if (grid == 0) return cudaSuccess;
-  k_extend<<<static_cast<unsigned>(grid), 128, 0, s>>>(a, static_cast<int32_t>(tiles));
-  return cudaGetLastError();
+ExtendPlan extend_plan(int64_t units, int32_t max_new, int32_t G, int32_t cap, int64_t rows) {
+  ExtendPlan p{};
+  const int64_t most = static_cast<int64_t>(max_new) * G;
+  p.mt = most > 128 ? 2 : 1;
+  p.row_tiles = static_cast<int32_t>((most + 128 * p.mt - 1) / (128 * p.mt));
+  const int64_t tiles = (static_cast<int64_t>(cap) + 127) / 128 + 2;
+  p.splits = 1;
+  while (units * p.row_tiles * p.splits < 152 && p.splits * 4 <= tiles) p.splits *= 2;
+  p.blocks = units * p.row_tiles * p.splits;
+  p.parts = p.mt == 2 ? (p.splits == 1 ? 0 : p.splits) : 2 * p.splits;
+  size_t o = align256(sizeof(float2) * static_cast<size_t>(p.parts) * rows);
+  p.o = o;
+  p.bytes = o + align256(512 * static_cast<size_t>(p.parts) * rows);
+  return p;
 }
 
-cudaError_t launch_extend_sig(const ExtendArgs &a, cudaStream_t s) {
-  const int64_t tiles = (static_cast<int64_t>(a.cap) + a.max_new + kTok - 1) / kTok;
-  const int64_t grid = static_cast<int64_t>(a.n_layers) * a.R * a.Hkv * tiles;
-  if (grid == 0) return cudaSuccess;
-  k_extend_sig<<<static_cast<unsigned>(grid), 128, 0, s>>>(a, static_cast<int32_t>(tiles));
+cudaError_t launch_extend(const ExtendArgs &a, const ExtendPlan &p, void *ws, cudaStream_t s) {
+  if (p.blocks == 0) return cudaSuccess;
+  Partial part{};
+  part.rows = a.n_layers * a.T * a.Hq;
+  part.ml = static_cast<float2 *>(ws);
+  part.o = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + p.o);
+  cudaError_t e;
+  if (p.mt == 2)
+    e = a.scheme == 0 ? launch<0, 2>(a, p, part, s) : a.scheme == 1 ? launch<1, 2>(a, p, part, s) : launch<2, 2>(a, p, part, s);
+  else
+    e = a.scheme == 0 ? launch<0, 1>(a, p, part, s) : a.scheme == 1 ? launch<1, 1>(a, p, part, s) : launch<2, 1>(a, p, part, s);
+  if (e != cudaSuccess || p.parts == 0) return e;
+  k_extend_merge<<<static_cast<unsigned>((part.rows + 7) / 8), 256, 0, s>>>(a, p.parts, part);
   return cudaGetLastError();
 }
 

@@ -21,16 +21,19 @@
 //     in order), while the other warpgroup is in its softmax.  A separate
 //     issuing warp would be the seventeenth and cost every thread a quarter of
 //     its registers.
-// Q is scaled per row by a power of two into fp16's range (undone in the
-// exponent's multiply-add), so q . c is exact up to the fp32 accumulation.
+// The block's rows of Q are scaled by one power of two that puts their largest
+// finite value into [2^14, 2^15) (the tokens' scales undo it): a value 28
+// binades below it still has all its bits in fp16, so q . c is exact up to the
+// fp32 accumulation.
 // New tokens: K is scaled per token the same way; V stays the bf16 it is, and
 // that product takes P in bf16 (both operands of one MMA have one type).
 //
-// The maximum is lazy: a row's reference m (a whole number, log2 units) moves
-// only when a logit exceeds it by more than 8, and then the softmax warp
-// itself multiplies its row of O by the exact power of two.  P is stored
-// scaled by 2^7, at most 2^15 (fp16's largest is 2^16), so weights down to
-// 2^-21 of the row's largest keep all 11 bits and 2^-32 is where they vanish.
+// The maximum is lazy: P = 2^(y - m + 7) with a row's reference m (a whole
+// number, log2 units) that moves only when the sum of 32 weights passes 2^15,
+// so the usual chunk needs no maximum at all; then the softmax warp raises m to
+// the chunk's maximum and multiplies its row of O by the exact power of two.
+// Weights stay at or below 2^15 (fp16's largest is 2^16); those down to 2^-21
+// of the row's largest keep all 11 bits and 2^-32 is where they vanish.
 //
 // MT = 2 (more than 128 rows): the two softmax warpgroups take 128 rows each
 // and every tile serves both, which halves the conversions per logit.  MT = 1:
@@ -51,8 +54,8 @@ constexpr int kSoftWarps = 8, kDeqWarps = 8;
 constexpr int kThreads = 32 * (kSoftWarps + kDeqWarps);
 constexpr uint32_t kTmemCols = 512;  // S (and P) of warpgroup w at 128 w, O at 256 + 128 w
 constexpr int kMeta = 4;             // ring of the tiles' scales and zeros
-constexpr float kGrow = 8.0f;        // growth of a logit over m that moves m
 constexpr float kLift = 7.0f;        // P = 2^(y - m + kLift)
+constexpr float kMost = 32768.0f;    // sum of 32 weights that moves m
 
 template <int MT>
 struct __align__(1024) Smem {
@@ -62,8 +65,9 @@ struct __align__(1024) Smem {
   float s[kMeta][128], z[kMeta][128];  // per token: scale s and z + mid s, times scale log2 e
   uint8_t valid[kMeta][128];           // looked at only when a page id of the unit is bad
   uint64_t qready, kfull[2], kempty[2], vfull[2], vempty[2], mfull[kMeta];
-  uint64_t sfull[2], pready[2], odone[2], done[2];
+  uint64_t sfull[2], pready[2], odone[2], turn[2], done[2];
   uint32_t tmem;
+  uint32_t qmax;  // largest finite |q| of the block's rows (bits)
   int32_t abort, bad;
 };
 template <int MT>
@@ -87,6 +91,25 @@ __device__ __forceinline__ void split(int32_t t, int32_t P, uint32_t M, int32_t 
   }
 }
 
+// Largest |value| of a bf16 row as bits; 0 when it is not finite.
+__device__ __forceinline__ uint32_t row_max(const uint16_t *src) {
+  float mx = 0.0f;
+#pragma unroll 4
+  for (int i = 0; i < 16; ++i) {
+    const uint4 v = __ldg(reinterpret_cast<const uint4 *>(src) + i);
+    mx = max3(mx, max3(fabsf(bf16_lo(v.x)), fabsf(bf16_hi(v.x)), fabsf(bf16_lo(v.y))),
+              max3(fabsf(bf16_hi(v.y)), fabsf(bf16_lo(v.z)), fabsf(bf16_hi(v.z))));
+    mx = max3(mx, fabsf(bf16_lo(v.w)), fabsf(bf16_hi(v.w)));
+  }
+  const uint32_t b = __float_as_uint(mx);
+  return b < 0x7f800000u ? b : 0;
+}
+
+// The exponent e that puts a largest value (its bits) into [2^14, 2^15).
+__device__ __forceinline__ int lift_exponent(uint32_t bits) {
+  return bits ? min(max(14 + 127 - static_cast<int>(bits >> 23), -120), 120) : 0;
+}
+
 // The dequant warps' view of one tile.
 struct Tile {
   int32_t kind, t0, n;  // 0 high, 1 low, 2 new; first token in its list; tokens
@@ -102,107 +125,92 @@ __device__ __forceinline__ Tile tile_at(const Tiles &ts, const Unit &x, int32_t 
 }
 
 // ------------------------------------------------------- dequantising warps --
-
-// Four tokens of a tile (tk + 32 p) of one thread: page ids, then codes.
-struct Held {
-  int32_t id[4];
-  uint32_t k[4][4], v[4][4];
-  uint2 md[4];
-};
-
+//
+// Four threads a token, 32 channels each, two tokens (tk and tk + 64) a
+// thread.  The thread of channels 64 .. takes its two 16-channel halves in the
+// other order, so that the eight threads of two neighbouring rows always
+// write eight different 16-byte chunks of the swizzled rows.
 struct DeqCtx {
   const ExtendArgs *a;
   Unit x;
   uint32_t m1, m2;  // split() by P and 2 P
   int64_t bytes;
   int32_t vbase, meta;
-  int tk, c;
+  int tk, c, hs;    // token, quarter of the channels, which half comes first
+  uint32_t off[4];  // operand-tile offsets of the thread's four groups (token tk)
 };
 
-__device__ __forceinline__ void fetch_ids(const DeqCtx &d, const Tile &t, Held &h) {
+struct Held {
+  uint32_t k[2][2][4], v[2][2][4];  // [token][half][words]
+  uint2 md[2];
+  bool ok[2];
+};
+
+// Where the two tokens of a tile lie: page ids (-1: no token) and slots.
+struct Where {
+  int32_t id[2], slot[2];
+};
+
+__device__ __forceinline__ void locate(const DeqCtx &d, const Tile &t, Where &w) {
   if (t.kind == 2) return;
-  const int32_t P = d.a->P;
+  const bool high = t.kind == 0;
+  const int32_t per = high ? d.a->P : 2 * d.a->P, first = high ? 0 : d.x.p_hi;
+  const uint32_t M = high ? d.m1 : d.m2;
 #pragma unroll
-  for (int p = 0; p < 4; ++p) {
-    const int32_t i = d.tk + 32 * p;
-    h.id[p] = -1;
-    if (i < t.n) {
-      int32_t k, s;
-      if (t.kind == 0) split(t.t0 + i, P, d.m1, k, s);
-      else split(t.t0 + i, 2 * P, d.m2, k, s), k += d.x.p_hi;
-      h.id[p] = __ldg(d.a->fwd + d.x.u * d.a->pmax + k);
+  for (int p = 0; p < 2; ++p) {
+    const int32_t i = d.tk + 64 * p;
+    int32_t k;
+    split(t.t0 + i, per, M, k, w.slot[p]);
+    w.id[p] = i < t.n ? __ldg(d.a->fwd + d.x.u * d.a->pmax + first + k) : -1;
+  }
+}
+
+template <int KW, int VW>
+__device__ __forceinline__ void fetch(const DeqCtx &d, const Where &w, Held &h, bool k, bool v) {
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    const bool ok = w.id[p] >= 0 && w.id[p] < d.a->F;
+    const uint8_t *pg = d.a->pages + (ok ? w.id[p] : 0) * d.bytes;  // page 0 stands in: masked, or its scale is 0
+    if (k) {
+      const uint8_t *src = pg + w.slot[p] * (16 * KW) + d.c * (4 * KW);
+      load16<KW>(h.k[p][0], src + d.hs * (2 * KW));
+      load16<KW>(h.k[p][1], src + (d.hs ^ 1) * (2 * KW));
+    }
+    if (v) {
+      const uint8_t *src = pg + d.vbase + w.slot[p] * (16 * VW) + d.c * (4 * VW);
+      load16<VW>(h.v[p][0], src + d.hs * (2 * VW));
+      load16<VW>(h.v[p][1], src + (d.hs ^ 1) * (2 * VW));
+      h.md[p] = __ldg(reinterpret_cast<const uint2 *>(pg + d.meta + 8 * w.slot[p]));
+      h.ok[p] = ok;
+      if (!ok) h.md[p] = make_uint2(0, 0);
     }
   }
 }
 
-// Page and slot of token tk + 32 p, null when there is none.
-__device__ __forceinline__ const uint8_t *page_of(const DeqCtx &d, const Tile &t, const Held &h, int p,
-                                                  int32_t &slot) {
-  const int32_t id = h.id[p];
-  if (id < 0 || id >= d.a->F) return nullptr;
-  int32_t k;
-  if (t.kind == 0) split(t.t0 + d.tk + 32 * p, d.a->P, d.m1, k, slot);
-  else split(t.t0 + d.tk + 32 * p, 2 * d.a->P, d.m2, k, slot);
-  return d.a->pages + id * d.bytes;
-}
-
-template <int W>
-__device__ __forceinline__ void fetch_k(const DeqCtx &d, const Tile &t, Held &h) {
-#pragma unroll
-  for (int p = 0; p < 4; ++p) {
-    int32_t slot;
-    const uint8_t *pg = page_of(d, t, h, p, slot);
-    h.k[p][0] = h.k[p][1] = h.k[p][2] = h.k[p][3] = 0;
-    if (pg) load16<W>(h.k[p], pg + slot * (16 * W) + d.c * (2 * W));
-  }
-}
-
-template <int W>
-__device__ __forceinline__ void fetch_v(const DeqCtx &d, const Tile &t, Held &h) {
-#pragma unroll
-  for (int p = 0; p < 4; ++p) {
-    int32_t slot;
-    const uint8_t *pg = page_of(d, t, h, p, slot);
-    h.v[p][0] = h.v[p][1] = h.v[p][2] = h.v[p][3] = 0;
-    h.md[p] = make_uint2(0, 0);
-    if (pg) {
-      load16<W>(h.v[p], pg + d.vbase + slot * (16 * W) + d.c * (2 * W));
-      h.md[p] = __ldg(reinterpret_cast<const uint2 *>(pg + d.meta + 8 * slot));
-    }
-  }
-}
-
-// The two 16-byte groups of a thread's 16 channels; threads of the upper box
-// write their second group first, so that the eight threads of a row touch
-// eight different chunks.
-__device__ __forceinline__ void store_groups(uint8_t *tile, int row, int c, const uint4 &g0, const uint4 &g1) {
-  const bool up = c >= 4;
-  *reinterpret_cast<uint4 *>(tile + group_at(row, 2 * c + (up ? 1 : 0))) = up ? g1 : g0;
-  *reinterpret_cast<uint4 *>(tile + group_at(row, 2 * c + (up ? 0 : 1))) = up ? g0 : g1;
+__device__ __forceinline__ void put(uint8_t *tile, uint32_t at, const __half2 (&o)[4]) {
+  *reinterpret_cast<uint4 *>(tile + at) = make_uint4(h2u(o[0]), h2u(o[1]), h2u(o[2]), h2u(o[3]));
 }
 
 template <int W, class S>
 __device__ __forceinline__ void convert_k(const DeqCtx &d, const Held &h, S &sm, uint8_t *dst, int slot, float f) {
   constexpr float kMid = 1 << (W - 1);
 #pragma unroll
-  for (int p = 0; p < 4; ++p) {
-    const int row = d.tk + 32 * p;
-    uint4 g[2];
+  for (int p = 0; p < 2; ++p) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
       uint32_t w0, w1;
       __half2 o[4];
-      group_of<W>(h.k[p], i, w0, w1);
+      group_of<W>(h.k[p][i >> 1], i & 1, w0, w1);
       group_codes<W>(w0, w1, kMid, o);
-      g[i] = make_uint4(h2u(o[0]), h2u(o[1]), h2u(o[2]), h2u(o[3]));
+      put(dst, d.off[i] + p * (64 * 128), o);
     }
-    store_groups(dst, row, d.c, g[0], g[1]);
     if (d.c == 0) {
+      const int row = d.tk + 64 * p;
       const __half2 m = u2h(h.md[p].x);
       const float s = __low2float(m), z = __high2float(m);
       sm.s[slot][row] = s * f;
       sm.z[slot][row] = fmaf(kMid, s, z) * f;
-      sm.valid[slot][row] = h.id[p] >= 0 && h.id[p] < d.a->F;
+      sm.valid[slot][row] = h.ok[p];
     }
   }
 }
@@ -210,17 +218,16 @@ __device__ __forceinline__ void convert_k(const DeqCtx &d, const Held &h, S &sm,
 template <int W>
 __device__ __forceinline__ void convert_v(const DeqCtx &d, const Held &h, uint8_t *dst) {
 #pragma unroll
-  for (int p = 0; p < 4; ++p) {
+  for (int p = 0; p < 2; ++p) {
     const __half2 m = u2h(h.md[p].y);
     const __half2 s = __low2half2(m), z = __high2half2(m);
-    uint4 g[2];
     // a dequantised value can pass fp16's largest by half a scale step
     const bool big = fmaf(static_cast<float>((1 << W) - 1), __low2float(m), fabsf(__high2float(m))) > 65000.0f;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
       uint32_t w0, w1;
       __half2 o[4];
-      group_of<W>(h.v[p], i, w0, w1);
+      group_of<W>(h.v[p][i >> 1], i & 1, w0, w1);
       group_codes<W>(w0, w1, 0.0f, o);
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[e] = __hfma2(o[e], s, z);
@@ -229,17 +236,18 @@ __device__ __forceinline__ void convert_v(const DeqCtx &d, const Held &h, uint8_
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[e] = __hmax2(__hmin2(o[e], top), __hneg2(top));
       }
-      g[i] = make_uint4(h2u(o[0]), h2u(o[1]), h2u(o[2]), h2u(o[3]));
+      put(dst, d.off[i] + p * (64 * 128), o);
     }
-    store_groups(dst, d.tk + 32 * p, d.c, g[0], g[1]);
   }
 }
 
-// 16 bf16 of a new token's row (0 when it has none), not finite -> 0.
-__device__ __forceinline__ void load_new(const DeqCtx &d, const uint16_t *base, int64_t row, bool have, uint4 (&x)[2]) {
+// 16 bf16 of a new token's row (0 when it has none), not finite -> 0: half
+// `half` (in the thread's order) of its 32 channels.
+__device__ __forceinline__ void load_new(const DeqCtx &d, const uint16_t *base, int64_t row, bool have, int half,
+                                         uint4 (&x)[2]) {
   x[0] = x[1] = make_uint4(0, 0, 0, 0);
   if (!have) return;
-  const uint4 *src = reinterpret_cast<const uint4 *>(base + row * 128) + 2 * d.c;
+  const uint4 *src = reinterpret_cast<const uint4 *>(base + row * 128) + 4 * d.c + 2 * (half ^ d.hs);
   x[0] = __ldg(src);
   x[1] = __ldg(src + 1);
   uint32_t *w = reinterpret_cast<uint32_t *>(x);
@@ -258,26 +266,28 @@ template <class S>
 __device__ __forceinline__ void new_k(const DeqCtx &d, const Tile &t, int64_t tok0, int32_t h, S &sm, uint8_t *dst,
                                       int slot, float f) {
 #pragma unroll 1
-  for (int p = 0; p < 4; ++p) {
-    const int row = d.tk + 32 * p;
-    uint4 x[2];
-    load_new(d, d.a->k_new, (tok0 + t.t0 + row) * d.a->Hkv + h, row < t.n, x);
-    const uint32_t *w = reinterpret_cast<const uint32_t *>(x);
+  for (int p = 0; p < 2; ++p) {
+    const int row = d.tk + 64 * p;
+    uint4 x[2][2];
     float mx = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) mx = fmaxf(mx, fmaxf(fabsf(bf16_lo(w[i])), fabsf(bf16_hi(w[i]))));
+    for (int e = 0; e < 2; ++e) {
+      load_new(d, d.a->k_new, (tok0 + t.t0 + row) * d.a->Hkv + h, row < t.n, e, x[e]);
+      const uint32_t *w = reinterpret_cast<const uint32_t *>(x[e]);
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
-    const int e = mx > 0.0f ? min(max(14 + 127 - static_cast<int>(__float_as_uint(mx) >> 23), -120), 120) : 0;
-    const float sc = pow2f(e);
-    uint4 g[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint4 v = x[i];
-      g[i] = make_uint4(f16x2_rn(bf16_lo(v.x) * sc, bf16_lo(v.z) * sc), f16x2_rn(bf16_hi(v.x) * sc, bf16_hi(v.z) * sc),
-                        f16x2_rn(bf16_lo(v.y) * sc, bf16_lo(v.w) * sc), f16x2_rn(bf16_hi(v.y) * sc, bf16_hi(v.w) * sc));
+      for (int i = 0; i < 8; ++i) mx = max3(mx, fabsf(bf16_lo(w[i])), fabsf(bf16_hi(w[i])));
     }
-    store_groups(dst, row, d.c, g[0], g[1]);
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
+    const int e = lift_exponent(__float_as_uint(mx));
+    const float sc = pow2f(e);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint4 v = x[i >> 1][i & 1];
+      *reinterpret_cast<uint4 *>(dst + d.off[i] + p * (64 * 128)) = make_uint4(
+          f16x2_rn(bf16_lo(v.x) * sc, bf16_lo(v.z) * sc), f16x2_rn(bf16_hi(v.x) * sc, bf16_hi(v.z) * sc),
+          f16x2_rn(bf16_lo(v.y) * sc, bf16_lo(v.w) * sc), f16x2_rn(bf16_hi(v.y) * sc, bf16_hi(v.w) * sc));
+    }
     if (d.c == 0) {
       sm.s[slot][row] = pow2f(-e) * f;
       sm.z[slot][row] = 0.0f;
@@ -288,37 +298,30 @@ __device__ __forceinline__ void new_k(const DeqCtx &d, const Tile &t, int64_t to
 
 __device__ __forceinline__ void new_v(const DeqCtx &d, const Tile &t, int64_t tok0, int32_t h, uint8_t *dst) {
 #pragma unroll 1
-  for (int p = 0; p < 4; ++p) {
-    const int row = d.tk + 32 * p;
-    uint4 x[2];
-    load_new(d, d.a->v_new, (tok0 + t.t0 + row) * d.a->Hkv + h, row < t.n, x);
-    uint32_t g0[4], g1[4];
-    group_bf16(x[0], g0);
-    group_bf16(x[1], g1);
-    store_groups(dst, row, d.c, make_uint4(g0[0], g0[1], g0[2], g0[3]), make_uint4(g1[0], g1[1], g1[2], g1[3]));
+  for (int p = 0; p < 2; ++p) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int row = d.tk + 64 * p;
+      uint4 x[2];
+      load_new(d, d.a->v_new, (tok0 + t.t0 + row) * d.a->Hkv + h, row < t.n, e, x);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        uint32_t g[4];
+        group_bf16(x[i], g);
+        *reinterpret_cast<uint4 *>(dst + d.off[2 * e + i] + p * (64 * 128)) = make_uint4(g[0], g[1], g[2], g[3]);
+      }
+    }
   }
 }
 
 // ------------------------------------------------------------ softmax warps --
 
-// A row of Q (row < rows) into fp16 operand form: the power of two it is
-// scaled by is 2^e; returns the sum of the scaled row.  `dst` may be null.
-__device__ __forceinline__ float stage_q(const uint16_t *src, bool have, uint8_t *dst, int row, int &e) {
-  uint4 x[16];
-  float mx = 0.0f;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    x[i] = have ? __ldg(reinterpret_cast<const uint4 *>(src) + i) : make_uint4(0, 0, 0, 0);
-    mx = max3(mx, max3(fabsf(bf16_lo(x[i].x)), fabsf(bf16_hi(x[i].x)), fabsf(bf16_lo(x[i].y))),
-              max3(fabsf(bf16_hi(x[i].y)), fabsf(bf16_lo(x[i].z)), fabsf(bf16_hi(x[i].z))));
-    mx = max3(mx, fabsf(bf16_lo(x[i].w)), fabsf(bf16_hi(x[i].w)));
-  }
-  e = mx > 0.0f ? min(max(14 + 127 - static_cast<int>(__float_as_uint(mx) >> 23), -120), 120) : 0;
-  const float sc = pow2f(e);
+// A row of Q times sc into operand form (`dst` may be null); returns its sum.
+__device__ __forceinline__ float stage_q(const uint16_t *src, bool have, uint8_t *dst, int row, float sc) {
   float sum = 0.0f;
-#pragma unroll
+#pragma unroll 4
   for (int i = 0; i < 16; ++i) {
-    const uint4 v = x[i];
+    const uint4 v = have ? __ldg(reinterpret_cast<const uint4 *>(src) + i) : make_uint4(0, 0, 0, 0);
     const float c0 = bf16_lo(v.x) * sc, c1 = bf16_hi(v.x) * sc, c2 = bf16_lo(v.y) * sc, c3 = bf16_hi(v.y) * sc;
     const float c4 = bf16_lo(v.z) * sc, c5 = bf16_hi(v.z) * sc, c6 = bf16_lo(v.w) * sc, c7 = bf16_hi(v.w) * sc;
     sum += ((c0 + c1) + (c2 + c3)) + ((c4 + c5) + (c6 + c7));
@@ -327,6 +330,15 @@ __device__ __forceinline__ float stage_q(const uint16_t *src, bool have, uint8_t
           make_uint4(f16x2_rn(c0, c4), f16x2_rn(c1, c5), f16x2_rn(c2, c6), f16x2_rn(c3, c7));
   }
   return sum;
+}
+
+// Columns a row keeps of 32: the first `lim`, and of those the valid ones.
+__device__ __forceinline__ uint32_t column_mask(int32_t lim, const uint8_t *valid) {
+  uint32_t k = lim >= 32 ? 0xffffffffu : (lim <= 0 ? 0u : (1u << lim) - 1u);
+  if (valid)
+    for (int i = 0; i < 32; ++i)
+      if (!valid[i]) k &= ~(1u << i);
+  return k;
 }
 
 // Columns of one row of O: 32 values in operand order, to channel order.
@@ -342,10 +354,11 @@ __device__ __forceinline__ void channel_order(const uint32_t *r, float *x) {
 
 template <int SC, int MT>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_extend(ExtendArgs a, int32_t row_tiles, int32_t splits, Partial part) {
+    k_extend(const __grid_constant__ ExtendArgs a, int32_t row_tiles, int32_t splits, Partial part) {
   constexpr int KH = scheme_kh(SC), VH = scheme_vh(SC);
   extern __shared__ unsigned char smem_raw[];
-  Smem<MT> &sm = *reinterpret_cast<Smem<MT> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // aligned by an offset, not by an integer address: the compiler then knows that these are shared accesses
+  Smem<MT> &sm = *reinterpret_cast<Smem<MT> *>(smem_raw + (-saddr(smem_raw) & 1023u));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int32_t sp = static_cast<int32_t>(blockIdx.x % splits);
   const int64_t ur = blockIdx.x / splits;
@@ -376,11 +389,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sm.sfull[i], 1);
       mbar_init(&sm.pready[i], 4);
       mbar_init(&sm.odone[i], 1);
+      mbar_init(&sm.turn[i], 1);
       mbar_init(&sm.done[i], 1);
     }
     for (int i = 0; i < kMeta; ++i) mbar_init(&sm.mfull[i], kDeqWarps);
     sm.abort = 0;
     sm.bad = 0;
+    sm.qmax = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 0) tmem_alloc(&sm.tmem, kTmemCols);
@@ -388,6 +403,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   fence_after();
   const uint32_t tmem = sm.tmem;
+  if (warp < kSoftWarps) {
+    const int32_t grow = row0 + (MT == 2 ? tid : tid & 127);
+    const uint32_t b = grow < rows ? row_max(a.q + ((tok0 + grow / a.G) * a.Hq + h * a.G + grow % a.G) * 128) : 0;
+    const uint32_t w = __reduce_max_sync(kFull, b);
+    if (lane == 0 && w) atomicMax(&sm.qmax, w);
+  }
   // a page id out of range anywhere in the unit: logits are masked token by token
   for (int32_t k = tid; k < (x.n_hi + a.P - 1) / a.P + (x.n_lo + 2 * a.P - 1) / (2 * a.P); k += kThreads) {
     const int32_t id = __ldg(a.fwd + x.u * a.pmax + k);
@@ -397,6 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   __syncthreads();
+  const int e = lift_exponent(sm.qmax);
   auto wait = [&](uint64_t *bar, uint32_t parity) { return wait_or_abort(bar, parity, abort, a.status); };
   // the same answer in every lane: the loops below hold warp-wide instructions
   auto warp_wait = [&](uint64_t *bar, uint32_t parity) { return __all_sync(kFull, wait(bar, parity)) != 0; };
@@ -408,17 +430,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool have = grow < rows;
     const int32_t qi = grow / a.G, qg = grow - qi * a.G;
     const int64_t at = (tok0 + qi) * a.Hq + h * a.G + qg;
-    int e;
-    const float qsum = stage_q(a.q + at * 128, have, MT == 2 || wg == 0 ? sm.q[MT == 2 ? wg : 0] : nullptr, row, e);
+    const float qsum =
+        stage_q(a.q + at * 128, have, MT == 2 || wg == 0 ? sm.q[MT == 2 ? wg : 0] : nullptr, row, pow2f(e));
     fence_async();
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.qready);
-    const float rq = pow2f(-e);
-    const uint64_t qs2 = f2_pack(qsum, qsum), rq2 = f2_pack(rq, rq);
+    const uint64_t qs2 = f2_pack(qsum, qsum);
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const uint32_t ts_s = tmem + lanes + 128 * wg, ts_o = tmem + lanes + 256 + 128 * wg;
     float m = -INFINITY;
-    uint64_t l2 = f2_pack(0.0f, 0.0f);
+    uint64_t l2 = 0;  // running sum, even and odd columns
+    const bool some = __any_sync(kFull, have);
     // one thread issues the warpgroup's products
     const bool issuer = (warp & 3) == 0 && lane == 0;
     constexpr uint32_t kStep = kTileBytes >> 4;
@@ -460,92 +482,113 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_after();
       const int32_t lim = tl.kind == 2 ? min(tl.n, qi - tl.t0 + 1) : tl.n;
       const bool masked = __any_sync(kFull, lim < 128) || sm.bad;
+      const float *sv = sm.s[ms], *zv = sm.z[ms];
+      const uint8_t *valid = sm.bad ? sm.valid[ms] : nullptr;
+      // y - mo of columns 32 c .. + 31, -inf where masked
+      auto logits = [&](uint32_t (&u)[32], int c, float mo) {
+        const uint64_t nm2 = f2_pack(-mo, -mo);
+        tmem_ld32(ts_s + 32 * c, u);
+        tmem_wait32(u);
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        uint32_t u[64];
-        tmem_ld32(ts_s + 64 * hf, u);
-        tmem_ld32(ts_s + 64 * hf + 32, u + 32);
-        tmem_wait_ld();
-        const float4 *s4 = reinterpret_cast<const float4 *>(sm.s[ms] + 64 * hf);
-        const float4 *z4 = reinterpret_cast<const float4 *>(sm.z[ms] + 64 * hf);
-        float mx = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float4 s = s4[i], z = z4[i];
-          float y0, y1, y2, y3;
+        for (int i = 0; i < 8; ++i) {
+          const float4 s = *reinterpret_cast<const float4 *>(sv + 32 * c + 4 * i);
+          const float4 z = *reinterpret_cast<const float4 *>(zv + 32 * c + 4 * i);
+          float y0, y1;
           f2_unpack(f2_fma(f2_pack(s.x, s.y), f2_pack(__uint_as_float(u[4 * i]), __uint_as_float(u[4 * i + 1])),
-                           f2_mul(f2_pack(z.x, z.y), qs2)), y0, y1);
-          f2_unpack(f2_fma(f2_pack(s.z, s.w), f2_pack(__uint_as_float(u[4 * i + 2]), __uint_as_float(u[4 * i + 3])),
-                           f2_mul(f2_pack(z.z, z.w), qs2)), y2, y3);
+                           f2_fma(f2_pack(z.x, z.y), qs2, nm2)), y0, y1);
           u[4 * i] = __float_as_uint(y0);
           u[4 * i + 1] = __float_as_uint(y1);
-          u[4 * i + 2] = __float_as_uint(y2);
-          u[4 * i + 3] = __float_as_uint(y3);
+          f2_unpack(f2_fma(f2_pack(s.z, s.w), f2_pack(__uint_as_float(u[4 * i + 2]), __uint_as_float(u[4 * i + 3])),
+                           f2_fma(f2_pack(z.z, z.w), qs2, nm2)), y0, y1);
+          u[4 * i + 2] = __float_as_uint(y0);
+          u[4 * i + 3] = __float_as_uint(y1);
         }
-        if (masked) {
+        if (__builtin_expect(masked, 0)) {
+          const uint32_t keep = column_mask(lim - 32 * c, valid ? valid + 32 * c : nullptr);
 #pragma unroll
-          for (int i = 0; i < 64; ++i)
-            if (64 * hf + i >= lim || (sm.bad && !sm.valid[ms][64 * hf + i])) u[i] = 0xff800000u;  // -inf
+          for (int i = 0; i < 32; ++i)
+            if (!(keep >> i & 1u)) u[i] = 0xff800000u;
         }
+      };
+      // m moves to the maximum of columns 32 c .. + 31: the sum, P of the tile's
+      // columns before and O of the tiles before follow
+      auto raise = [&](uint32_t (&u)[32], int c) -> bool {
+        logits(u, c, 0.0f);
+        float mx = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < 64; i += 2) mx = max3(mx, __uint_as_float(u[i]), __uint_as_float(u[i + 1]));
-        const float ymax = mx * rq;
-        if (__any_sync(kFull, ymax > m + kGrow)) {  // some row's reference moves
-          const bool grow_ = ymax > m + kGrow;
-          const float mn = grow_ ? ceilf(ymax) : m;
-          const float f = grow_ ? ex2(m - mn) : 1.0f;  // a power of two, 0 at first
-          l2 = f2_mul(l2, f2_pack(f, f));
-          if (hf == 1) {  // P of the tile's first half has the old reference
-            uint32_t pw[32];
-            tmem_ld32(ts_s, pw);
-            tmem_wait_ld();
-            if (tl.kind == 2) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) pw[i] = bf16x2_rn(bf16_lo(pw[i]) * f, bf16_hi(pw[i]) * f);
-            } else {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                const float2 p2 = __half22float2(u2h(pw[i]));
-                pw[i] = f16x2_rn(p2.x * f, p2.y * f);
-              }
-            }
-            tmem_st32(ts_s, pw);
-          }
-          if (t > 0) {  // O of the tiles before
-            if (!(ok = warp_wait(&sm.odone[wg], (t - 1) & 1u))) break;
-            fence_after();
+        for (int i = 0; i < 32; i += 2) mx = max3(mx, __uint_as_float(u[i]), __uint_as_float(u[i + 1]));
+        const float mn = fmaxf(m, ceilf(mx));
+        const float f = mn == m ? 1.0f : ex2(m - mn);  // a power of two, 0 at first
+        l2 = f2_mul(l2, f2_pack(f, f));
+        m = mn;
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              uint32_t o[32];
-              tmem_ld32(ts_o + 32 * c, o);
-              tmem_wait_ld();
+        for (int i = 0; i < c; ++i) {
+          tmem_ld16(ts_s + 16 * i, u);
+          tmem_wait16(u);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-              tmem_st32(ts_o + 32 * c, o);
-            }
+          for (int e = 0; e < 16; ++e) {
+            const float2 p2 = tl.kind == 2 ? make_float2(bf16_lo(u[e]), bf16_hi(u[e])) : __half22float2(u2h(u[e]));
+            u[e] = tl.kind == 2 ? bf16x2_rn(p2.x * f, p2.y * f) : f16x2_rn(p2.x * f, p2.y * f);
           }
-          m = mn;
+          tmem_st16(ts_s + 16 * i, u);
         }
-        const float mo = m == -INFINITY ? 0.0f : m - kLift;
-        const uint64_t nm2 = f2_pack(-mo, -mo);
-        uint32_t w[32];
+        if (t == 0) return true;
+        if (!warp_wait(&sm.odone[wg], (t - 1) & 1u)) return false;
+        fence_after();
+#pragma unroll 1
+        for (int i = 0; i < 8; ++i) {
+          tmem_ld16(ts_o + 16 * i, u);
+          tmem_wait16(u);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          float y0, y1;
-          f2_unpack(f2_fma(f2_pack(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1])), rq2, nm2), y0, y1);
-          y0 = ex2(y0);
-          y1 = ex2(y1);
-          l2 = f2_add(l2, f2_pack(y0, y1));
-          w[i] = tl.kind == 2 ? bf16x2_rn(y0, y1) : f16x2_rn(y0, y1);
+          for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * f);
+          tmem_st16(ts_o + 16 * i, u);
         }
-        tmem_st32(ts_s + 32 * hf, w);
+        return true;
+      };
+      // 32 columns at a time: the short loop stays in the instruction cache.  A
+      // warp of padding rows leaves its rows of P as they are.
+#pragma unroll 1
+      for (int c = some ? 0 : 4; c < 4 && ok; ++c) {
+        uint32_t u[32];
+        uint64_t sum[4];
+#pragma unroll 1
+        for (int pass = 0;; ++pass) {
+          logits(u, c, m == -INFINITY ? 0.0f : m - kLift);
+          sum[0] = sum[1] = sum[2] = sum[3] = 0;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float p0 = ex2(__uint_as_float(u[2 * i])), p1 = ex2(__uint_as_float(u[2 * i + 1]));
+            sum[i & 3] = f2_add(sum[i & 3], f2_pack(p0, p1));
+            u[2 * i] = __float_as_uint(p0);
+            u[2 * i + 1] = __float_as_uint(p1);
+          }
+          sum[0] = f2_add(f2_add(sum[0], sum[1]), f2_add(sum[2], sum[3]));
+          float a0, a1;
+          f2_unpack(sum[0], a0, a1);
+          a0 += a1;
+          if (__builtin_expect(!__any_sync(kFull, a0 > kMost || (m == -INFINITY && a0 > 0.0f)), 1) || pass) break;
+          uint32_t r[32];
+          if (!(ok = raise(r, c))) break;
+        }
+        l2 = f2_add(l2, sum[0]);
+        if (tl.kind == 2) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) u[i] = bf16x2_rn(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) u[i] = f16x2_rn(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
+        }
+        tmem_st16(ts_s + 16 * c, u);
       }
       if (!ok) break;
       tmem_wait_st();
       fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.pready[wg]);
-      if (issuer && (ok = wait(&sm.vfull[j & 1], (j >> 1) & 1u) && wait(&sm.pready[wg], t & 1u))) {
+      // the warpgroups issue in turn: products that interleave would all finish
+      // late and keep both warpgroups in their softmax at the same time
+      if (issuer && (ok = wait(&sm.vfull[j & 1], (j >> 1) & 1u) && wait(&sm.pready[wg], t & 1u) &&
+                          (wg == 0 && t == 0 || wait(&sm.turn[wg], (wg == 0 ? t - 1 : t) & 1u)))) {
         fence_after();
         issue_o(j, tl.kind == 2, t == 0);
         const int32_t jn = j + step;
@@ -553,6 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_after();
           issue_s(jn);
         }
+        mbar_arrive(&sm.turn[wg ^ 1]);
       }
       ok = __all_sync(kFull, ok);
     }
@@ -577,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float f[32];
         if (t > 0) {
           tmem_ld32(ts_o + 32 * c, o);
-          tmem_wait_ld();
+          tmem_wait32(o);
         } else {
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = 0;
@@ -607,30 +651,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int dt = tid - 32 * kSoftWarps;
     const PageGeom g = page_geom(SC, a.P);
     DeqCtx d{&a, x, 0xffffffffu / a.P + 1, 0xffffffffu / (2 * a.P) + 1, g.bytes, static_cast<int32_t>(g.vbase),
-             static_cast<int32_t>(g.meta), dt >> 3, dt & 7};
-    const float f = a.scale * kLog2e;
+             static_cast<int32_t>(g.meta), dt >> 2, dt & 3, (dt & 3) >> 1, {}};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) d.off[i] = group_at(d.tk, 4 * d.c + (i ^ (2 * d.hs)));
+    const float f = a.scale * kLog2e * pow2f(-e);
     Held hd;
+    Where w0, w1;  // the tile whose codes are loaded, the next one
     bool ok = true;
-    auto load_k = [&](const Tile &t) {
-      if (t.kind == 0) fetch_k<KH>(d, t, hd);
-      else if (t.kind == 1) fetch_k<KH / 2>(d, t, hd);
-    };
-    auto load_v = [&](const Tile &t) {
-      if (t.kind == 0) fetch_v<VH>(d, t, hd);
-      else if (t.kind == 1) fetch_v<VH / 2>(d, t, hd);
+    auto load = [&](const Tile &t, const Where &w, bool k, bool v) {
+      if (t.kind == 0) fetch<KH, VH>(d, w, hd, k, v);
+      else if (t.kind == 1) fetch<KH / 2, VH / 2>(d, w, hd, k, v);
     };
     Tile t{}, tn{};
-    Held nx;  // ids of the next tile
     if (n > 0) {
       t = tile_at(ts, x, fresh, j0);
-      fetch_ids(d, t, hd);
-      load_k(t);
-      load_v(t);
+      locate(d, t, w0);
+      load(t, w0, true, true);
     }
     if (n > 1) {
       tn = tile_at(ts, x, fresh, j0 + 1);
-      fetch_ids(d, tn, nx);
+      locate(d, tn, w1);
     }
+#pragma unroll 1
     for (int32_t j = 0; j < n; ++j) {
       const int b = j & 1, ms = j % kMeta;
       if (j >= 2 && !(ok = warp_wait(&sm.kempty[b], ((j >> 1) - 1) & 1u))) break;
@@ -646,9 +688,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Tile cur = t;
       if (j + 1 < n) {
         t = tn;
-#pragma unroll
-        for (int p = 0; p < 4; ++p) hd.id[p] = nx.id[p];
-        load_k(t);
+        w0 = w1;
+        load(t, w0, true, false);
       }
       if (j >= 2 && !(ok = warp_wait(&sm.vempty[b], ((j >> 1) - 1) & 1u))) break;
       if (cur.kind == 0) convert_v<VH>(d, hd, sm.v[b]);
@@ -657,10 +698,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.vfull[b]);
-      if (j + 1 < n) load_v(t);
+      if (j + 1 < n) load(t, w0, false, true);
       if (j + 2 < n) {
         tn = tile_at(ts, x, fresh, j0 + j + 2);
-        fetch_ids(d, tn, nx);
+        locate(d, tn, w1);
       }
     }
     (void)ok;

@@ -40,6 +40,7 @@ def _stale(obj: str, src: str) -> bool:
     if not os.path.exists(obj):
         return True
     deps = [src, os.path.join(CSRC, "dkv_internal.cuh"), os.path.join(CSRC, "tensor_ops.cuh"),
+            os.path.join(CSRC, "token_tiles.cuh"),
             os.path.join(os.path.dirname(HERE), "include", "dkv.h")]
     return os.path.getmtime(obj) < max(os.path.getmtime(d) for d in deps)
 

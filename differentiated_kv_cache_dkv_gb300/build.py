@@ -25,7 +25,7 @@ LIB_PATH_SAN = os.path.join(HERE, "lib", "libdkv_san.so")
 HOST_SAN = ["-Xcompiler", "-fsanitize=address", "-Xcompiler", "-fsanitize=undefined",
             "-Xcompiler", "-fno-sanitize-recover=all", "-Xcompiler", "-fno-omit-frame-pointer"]
 SOURCES = ["api.cu", "classify.cu", "alloc.cu", "pack.cu", "pool.cu", "noalloc.cu", "decode.cu", "attend.cu", "prefill.cu",
-           "maintain.cu", "extend.cu", "extend_sig.cu"]
+           "maintain.cu", "extend.cu", "extend_few.cu", "extend_sig.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall"]
 

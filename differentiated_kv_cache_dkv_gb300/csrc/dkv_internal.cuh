@@ -429,8 +429,16 @@ struct ExtendArgs {
   int32_t *status;
 };
 
-// How dkv_extend_attention cuts its work: blocks of 128 mt rows, each row's
-// tiles in `splits` runs, and the partial results that are joined afterwards
+// Partial results of dkv_extend_attention's rows.
+struct ExtendPartial {
+  float *o;     // [parts][rows][128]
+  float2 *ml;   // [parts][rows]: reference (log2 units, lift included) and sum; null: no parts
+  int64_t rows;
+};
+
+// How dkv_extend_attention cuts its work: blocks of 128 mt rows (mt = 0: at
+// most 32 rows a unit, extend_few.cu), each row's tiles in `splits` runs, and
+// the partial results that are joined afterwards
 // (parts = 0: the blocks write the outputs themselves).
 struct ExtendPlan {
   int32_t mt, row_tiles, splits, parts;
@@ -466,5 +474,6 @@ cudaError_t launch_release(const PageOpArgs &a, cudaStream_t s);
 cudaError_t launch_defrag(const PageOpArgs &a, int sms, cudaStream_t s);
 ExtendPlan extend_plan(int64_t units, int32_t max_new, int32_t G, int32_t cap, int64_t rows);
 cudaError_t launch_extend(const ExtendArgs &a, const ExtendPlan &p, void *ws, cudaStream_t s);
+cudaError_t launch_extend_few(const ExtendArgs &a, const ExtendPlan &p, const ExtendPartial &part, cudaStream_t s);
 cudaError_t launch_extend_sig(const ExtendArgs &a, cudaStream_t s);
 }  // namespace dkv

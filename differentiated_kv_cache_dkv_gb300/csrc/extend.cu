@@ -74,12 +74,6 @@ template <int MT>
 constexpr size_t smem_bytes() { return sizeof(Smem<MT>) + 1024; }
 static_assert(smem_bytes<2>() <= 227 * 1024, "shared memory");
 
-struct Partial {
-  float *o;    // [parts][rows][128]
-  float2 *ml;  // [parts][rows]: reference (log2 units, lift included) and sum
-  int64_t rows;
-};
-
 // ------------------------------------------------------------ softmax warps --
 
 // A row of Q times sc into operand form (`dst` may be null); returns its sum.
@@ -120,18 +114,16 @@ __device__ __forceinline__ void channel_order(const uint32_t *r, float *x) {
 
 template <int SC, int MT>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_extend(const __grid_constant__ ExtendArgs a, int32_t row_tiles, int32_t splits, Partial part) {
+    k_extend(const __grid_constant__ ExtendArgs a, int32_t row_tiles, int32_t splits, ExtendPartial part) {
   constexpr int KH = scheme_kh(SC), VH = scheme_vh(SC);
   extern __shared__ unsigned char smem_raw[];
   // aligned by an offset, not by an integer address: the compiler then knows that these are shared accesses
   Smem<MT> &sm = *reinterpret_cast<Smem<MT> *>(smem_raw + (-saddr(smem_raw) & 1023u));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int32_t sp = static_cast<int32_t>(blockIdx.x % splits);
-  const int64_t ur = blockIdx.x / splits;
-  const int32_t rt = static_cast<int32_t>(ur % row_tiles);
-  const int64_t ui = ur / row_tiles;
-  const int32_t h = static_cast<int32_t>(ui % a.Hkv), r = static_cast<int32_t>((ui / a.Hkv) % a.R);
-  const int32_t li = static_cast<int32_t>(ui / (static_cast<int64_t>(a.Hkv) * a.R));
+  const uint32_t ur = blockIdx.x / splits, ui = ur / row_tiles, rh = ui / a.Hkv;  // ..., unit, (layer, request)
+  const int32_t sp = static_cast<int32_t>(blockIdx.x - ur * splits), rt = static_cast<int32_t>(ur - ui * row_tiles);
+  const int32_t h = static_cast<int32_t>(ui - rh * a.Hkv);
+  const int32_t li = static_cast<int32_t>(rh / a.R), r = static_cast<int32_t>(rh - li * a.R);
   int64_t before;
   if (!lens_valid(a, r, before)) return;
   const int32_t rows = __ldg(a.new_lens + r) * a.G, row0 = rt * (128 * MT);
@@ -416,15 +408,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ================= dequantising warps
     const int dt = tid - 32 * kSoftWarps;
     const PageGeom g = page_geom(SC, a.P);
-    DeqCtx d{&a, x, 0xffffffffu / a.P + 1, 0xffffffffu / (2 * a.P) + 1, g.bytes, static_cast<int32_t>(g.vbase),
-             static_cast<int32_t>(g.meta), dt >> 2, dt & 3, (dt & 3) >> 1, {}};
+    DeqCtx d{&a, x, 0xffffffffu / a.P + 1, 0xffffffffu / (2 * a.P) + 1, static_cast<int32_t>(g.bytes),
+             static_cast<uint32_t>(g.vbase), static_cast<uint32_t>(g.meta), dt >> 2, dt & 3, (dt & 3) >> 1, {}};
 #pragma unroll
     for (int i = 0; i < 4; ++i) d.off[i] = group_at(d.tk, 4 * d.c + (i ^ (2 * d.hs)));
     const float f = a.scale * kLog2e * pow2f(-e);
-    Held hd;
-    Where w0, w1;  // the tile whose codes are loaded, the next one
+    Held<2> hd;
+    Where<2> w0, w1;  // the tile whose codes are loaded, the next one
     bool ok = true;
-    auto load = [&](const Tile &t, const Where &w, bool k, bool v) {
+    auto load = [&](const Tile &t, const Where<2> &w, bool k, bool v) {
       if (t.kind == 0) fetch<KH, VH>(d, w, hd, k, v);
       else if (t.kind == 1) fetch<KH / 2, VH / 2>(d, w, hd, k, v);
     };
@@ -444,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (j >= 2 && !(ok = warp_wait(&sm.kempty[b], ((j >> 1) - 1) & 1u))) break;
       if (t.kind == 0) convert_k<KH>(d, hd, sm, sm.k[b], ms, f);
       else if (t.kind == 1) convert_k<KH / 2>(d, hd, sm, sm.k[b], ms, f);
-      else new_k<true>(d, t, tok0, h, sm, sm.k[b], ms, f);
+      else new_k<2, true>(d, t, tok0, h, sm, sm.k[b], ms, f);
       fence_async();
       __syncwarp();
       if (lane == 0) {
@@ -460,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (j >= 2 && !(ok = warp_wait(&sm.vempty[b], ((j >> 1) - 1) & 1u))) break;
       if (cur.kind == 0) convert_v<VH>(d, hd, sm.v[b]);
       else if (cur.kind == 1) convert_v<VH / 2>(d, hd, sm.v[b]);
-      else new_v(d, cur, tok0, h, sm.v[b]);
+      else new_v<2>(d, cur, tok0, h, sm.v[b]);
       fence_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.vfull[b]);
@@ -482,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the partial results of a row: a warp per row, four channels a lane.
-__global__ void __launch_bounds__(256) k_extend_merge(ExtendArgs a, int32_t parts, Partial part) {
+__global__ void __launch_bounds__(256) k_extend_merge(ExtendArgs a, int32_t parts, ExtendPartial part) {
   __shared__ int32_t ok_s;
   if (threadIdx.x < 32) {  // the lengths were wrong: the attention wrote nothing
     int64_t t = 0;
@@ -505,12 +497,14 @@ __global__ void __launch_bounds__(256) k_extend_merge(ExtendArgs a, int32_t part
   const int64_t at = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   if (at >= part.rows) return;
   float M = -INFINITY;
+#pragma unroll 2
   for (int32_t p = 0; p < parts; ++p) {
     const float2 ml = part.ml[p * part.rows + at];
     if (ml.y != 0.0f) M = fmaxf(M, ml.x);
   }
   float l = 0.0f;
   float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 2
   for (int32_t p = 0; p < parts; ++p) {
     const float2 ml = part.ml[p * part.rows + at];
     if (ml.y == 0.0f) continue;  // attends nothing there (or no tile): O may not be written
@@ -529,7 +523,7 @@ __global__ void __launch_bounds__(256) k_extend_merge(ExtendArgs a, int32_t part
 }
 
 template <int SC, int MT>
-cudaError_t launch(const ExtendArgs &a, const ExtendPlan &p, const Partial &part, cudaStream_t s) {
+cudaError_t launch(const ExtendArgs &a, const ExtendPlan &p, const ExtendPartial &part, cudaStream_t s) {
   const int smem = static_cast<int>(smem_bytes<MT>());
   if (cudaError_t e = cudaFuncSetAttribute(k_extend<SC, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem))
     return e;
@@ -539,16 +533,26 @@ cudaError_t launch(const ExtendArgs &a, const ExtendPlan &p, const Partial &part
 
 }  // namespace
 
+// A few waves of blocks of the few-row kernel even out units of different
+// lengths.
+constexpr int64_t kFewBlocks = 152 * 3;
+
 ExtendPlan extend_plan(int64_t units, int32_t max_new, int32_t G, int32_t cap, int64_t rows) {
   ExtendPlan p{};
   const int64_t most = static_cast<int64_t>(max_new) * G;
-  p.mt = most > 128 ? 2 : 1;
-  p.row_tiles = static_cast<int32_t>((most + 128 * p.mt - 1) / (128 * p.mt));
   const int64_t tiles = (static_cast<int64_t>(cap) + 127) / 128 + 2;
   p.splits = 1;
-  while (units * p.row_tiles * p.splits < 152 && p.splits * 4 <= tiles) p.splits *= 2;
+  if (most <= 32) {
+    p.mt = 0;
+    p.row_tiles = 1;
+    while (units * p.splits < kFewBlocks && p.splits * 4 <= tiles) p.splits *= 2;
+  } else {
+    p.mt = most > 128 ? 2 : 1;
+    p.row_tiles = static_cast<int32_t>((most + 128 * p.mt - 1) / (128 * p.mt));
+    while (units * p.row_tiles * p.splits < 152 && p.splits * 4 <= tiles) p.splits *= 2;
+  }
   p.blocks = units * p.row_tiles * p.splits;
-  p.parts = p.mt == 2 ? (p.splits == 1 ? 0 : p.splits) : 2 * p.splits;
+  p.parts = p.mt == 1 ? 2 * p.splits : (p.splits == 1 ? 0 : p.splits);
   size_t o = align256(sizeof(float2) * static_cast<size_t>(p.parts) * rows);
   p.o = o;
   p.bytes = o + align256(512 * static_cast<size_t>(p.parts) * rows);
@@ -556,13 +560,15 @@ ExtendPlan extend_plan(int64_t units, int32_t max_new, int32_t G, int32_t cap, i
 }
 
 cudaError_t launch_extend(const ExtendArgs &a, const ExtendPlan &p, void *ws, cudaStream_t s) {
-  if (p.blocks == 0) return cudaSuccess;
-  Partial part{};
+  if (p.blocks == 0 || p.row_tiles == 0) return cudaSuccess;
+  ExtendPartial part{};
   part.rows = a.n_layers * a.T * a.Hq;
-  part.ml = static_cast<float2 *>(ws);
+  part.ml = p.parts ? static_cast<float2 *>(ws) : nullptr;
   part.o = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + p.o);
   cudaError_t e;
-  if (p.mt == 2)
+  if (p.mt == 0)
+    e = launch_extend_few(a, p, part, s);
+  else if (p.mt == 2)
     e = a.scheme == 0 ? launch<0, 2>(a, p, part, s) : a.scheme == 1 ? launch<1, 2>(a, p, part, s) : launch<2, 2>(a, p, part, s);
   else
     e = a.scheme == 0 ? launch<0, 1>(a, p, part, s) : a.scheme == 1 ? launch<1, 1>(a, p, part, s) : launch<2, 1>(a, p, part, s);

@@ -63,7 +63,7 @@ struct Key {
 };
 
 template <int KW>
-__device__ __forceinline__ void fetch_key(const DeqCtx &d, const Where &w, Key &h, int32_t posoff) {
+__device__ __forceinline__ void fetch_key(const DeqCtx &d, const Where<2> &w, Key &h, int32_t posoff) {
 #pragma unroll
   for (int p = 0; p < 2; ++p) {
     const bool ok = w.id[p] >= 0 && w.id[p] < d.a->F;
@@ -78,9 +78,9 @@ __device__ __forceinline__ void fetch_key(const DeqCtx &d, const Where &w, Key &
 }
 
 template <int W>
-__device__ __forceinline__ void convert_key(const DeqCtx &d, const Where &w, const Key &h, Smem &sm, uint8_t *dst,
+__device__ __forceinline__ void convert_key(const DeqCtx &d, const Where<2> &w, const Key &h, Smem &sm, uint8_t *dst,
                                             int slot, float f, int32_t ctx) {
-  constexpr float kMid = 1 << (W - 1);
+  constexpr int kMid = 1 << (W - 1);
 #pragma unroll
   for (int p = 0; p < 2; ++p) {
 #pragma unroll
@@ -88,7 +88,7 @@ __device__ __forceinline__ void convert_key(const DeqCtx &d, const Where &w, con
       uint32_t w0, w1;
       __half2 o[4];
       group_of<W>(h.k[p][i >> 1], i & 1, w0, w1);
-      group_codes<W>(w0, w1, kMid, o);
+      group_codes<W, kMid>(w0, w1, o);
       put(dst, d.off[i] + p * (64 * 128), o);
     }
     if (d.c == 0) {
@@ -116,10 +116,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(16) unsigned char smem_raw[];
   Smem &sm = *reinterpret_cast<Smem *>(smem_raw + (-saddr(smem_raw) & 1023u));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int32_t sp = static_cast<int32_t>(blockIdx.x % splits);
-  const int64_t ui = blockIdx.x / splits;
-  const int32_t h = static_cast<int32_t>(ui % a.Hkv), r = static_cast<int32_t>((ui / a.Hkv) % a.R);
-  const int32_t li = static_cast<int32_t>(ui / (static_cast<int64_t>(a.Hkv) * a.R));
+  const uint32_t ui = blockIdx.x / splits, rh = ui / a.Hkv;  // unit, (layer, request)
+  const int32_t sp = static_cast<int32_t>(blockIdx.x - ui * splits), h = static_cast<int32_t>(ui - rh * a.Hkv);
+  const int32_t li = static_cast<int32_t>(rh / a.R), r = static_cast<int32_t>(rh - li * a.R);
   int64_t before;
   if (!lens_valid(a, r, before)) return;
   const int32_t acc_n = __ldg(a.acc_lens + r), ctx = __ldg(a.ctx_lens + r);
@@ -266,14 +265,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ================= convert warps
     const int dt = tid - 32 * kSumWarps;
     const PageGeom pg = page_geom(SC, a.P);
-    DeqCtx d{&a, x, 0xffffffffu / a.P + 1, 0xffffffffu / (2 * a.P) + 1, pg.bytes, static_cast<int32_t>(pg.vbase),
-             static_cast<int32_t>(pg.meta), dt >> 2, dt & 3, (dt & 3) >> 1, {}};
+    DeqCtx d{&a, x, 0xffffffffu / a.P + 1, 0xffffffffu / (2 * a.P) + 1, static_cast<int32_t>(pg.bytes),
+             static_cast<uint32_t>(pg.vbase), static_cast<uint32_t>(pg.meta), dt >> 2, dt & 3, (dt & 3) >> 1, {}};
 #pragma unroll
     for (int i = 0; i < 4; ++i) d.off[i] = group_at(d.tk, 4 * d.c + (i ^ (2 * d.hs)));
     const float f = a.scale * kLog2e;
     const int32_t posoff = static_cast<int32_t>(pg.pos);
     Key key;
-    Where w0, w1;
+    Where<2> w0, w1;
     bool ok = true;
     Tile t{}, tn{};
     auto load = [&] {
@@ -368,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if (t.kind == 1) {
           convert_key<KH / 2>(d, w0, key, sm, sm.k[q], ms, f, ctx);
         } else {
-          new_k<false>(d, t, tok0, h, sm, sm.k[q], ms, f);
+          new_k<2, false>(d, t, tok0, h, sm, sm.k[q], ms, f);
           if (d.c == 0) {
 #pragma unroll
             for (int p = 0; p < 2; ++p) {

@@ -41,19 +41,24 @@ __device__ __forceinline__ void mbar_expect_tx(uint64_t *bar, uint32_t bytes) {
                : "memory");
 }
 
+__device__ __forceinline__ bool mbar_try(uint32_t addr, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+      : "=r"(done)
+      : "r"(addr), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+
 // Bounded wait for the phase of the given parity: false after about kWaitNs,
-// or as soon as *abort (when given) is set by another thread.
-__device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, const volatile int32_t *abort) {
-  const uint32_t addr = saddr(bar);
+// or as soon as *abort (when given) is set by another thread.  The loop is out
+// of line: the kernels have a dozen waits, and their code has to fit the
+// instruction cache.
+static __device__ __noinline__ bool mbar_wait_loop(uint32_t addr, uint32_t parity, const volatile int32_t *abort) {
   uint64_t t0 = 0;
   for (uint32_t i = 0; i < kWaitPolls; ++i) {
-    uint32_t done;
-    asm volatile(
-        "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
-        : "=r"(done)
-        : "r"(addr), "r"(parity)
-        : "memory");
-    if (done) return true;
+    if (mbar_try(addr, parity)) return true;
     if ((i & 63) == 63) {
       if (abort && *abort) return false;
       const uint64_t t = global_ns();
@@ -62,6 +67,10 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, const 
     }
   }
   return false;
+}
+__device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, const volatile int32_t *abort) {
+  const uint32_t addr = saddr(bar);
+  return mbar_try(addr, parity) || mbar_wait_loop(addr, parity, abort);
 }
 
 // A wait that gives up records the timeout once and makes everyone stop.
@@ -98,6 +107,8 @@ __host__ __device__ constexpr uint32_t idesc(bool bf16, int M, int N, bool b_mn)
   return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | ((b_mn ? 1u : 0u) << 16) |
          (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
+
+constexpr uint32_t kAMn = 1u << 15;  // ... with A MN-major
 
 // D[tmem] (+)= A[smem] B[smem].
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
@@ -149,6 +160,14 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t *r) {
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld4(uint32_t taddr, uint32_t *r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait4(uint32_t *r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]) : : "memory");
 }
 // Loads done: the registers they filled pass through, so that nothing reads
 // them earlier.
@@ -256,39 +275,56 @@ __device__ __forceinline__ __half2 u2h(uint32_t x) { return *reinterpret_cast<__
 // 1024 + 2^k c, and one half-precision multiply-add (exact: |result| <= 255)
 // makes it c - mid.
 
+// fp16 bits of a value that fp16 holds exactly in its normal range (compile
+// time: a conversion in the loop would cost as much as the codes').
+__host__ __device__ constexpr uint32_t half_bits(double x) {
+  if (x == 0.0) return 0;
+  const uint32_t sign = x < 0 ? 0x8000u : 0u;
+  double a = x < 0 ? -x : x;
+  int e = 15;
+  while (a >= 2.0) a /= 2.0, ++e;
+  while (a < 1.0) a *= 2.0, --e;
+  return sign | static_cast<uint32_t>(e) << 10 | static_cast<uint32_t>((a - 1.0) * 1024.0);
+}
+__host__ __device__ constexpr uint32_t half_pair(double lo, double hi) { return half_bits(lo) | half_bits(hi) << 16; }
+
 // Codes of one group (8 channels, W bits each, in `w0`, for W = 8 also `w1`)
-// as four fp16 pairs, minus `mid`.
-template <int W>
-__device__ __forceinline__ void group_codes(uint32_t w0, uint32_t w1, float mid, __half2 (&o)[4]) {
+// as four fp16 pairs, minus MID.
+template <int W, int MID>
+__device__ __forceinline__ void group_codes(uint32_t w0, uint32_t w1, __half2 (&o)[4]) {
   constexpr uint32_t kExp = 0x64006400u;
   if constexpr (W == 8) {
+    constexpr uint32_t b = half_pair(-1024.0 - MID, -1024.0 - MID);
     const uint32_t p01 = __byte_perm(w0, w1, 0x5140), p23 = __byte_perm(w0, w1, 0x7362);
-    const __half2 b = __float2half2_rn(-1024.0f - mid);
-    o[0] = __hadd2(u2h(__byte_perm(p01, kExp, 0x7170)), b);
-    o[1] = __hadd2(u2h(__byte_perm(p01, kExp, 0x7372)), b);
-    o[2] = __hadd2(u2h(__byte_perm(p23, kExp, 0x7170)), b);
-    o[3] = __hadd2(u2h(__byte_perm(p23, kExp, 0x7372)), b);
+    o[0] = __hadd2(u2h(__byte_perm(p01, kExp, 0x7170)), u2h(b));
+    o[1] = __hadd2(u2h(__byte_perm(p01, kExp, 0x7372)), u2h(b));
+    o[2] = __hadd2(u2h(__byte_perm(p23, kExp, 0x7170)), u2h(b));
+    o[3] = __hadd2(u2h(__byte_perm(p23, kExp, 0x7372)), u2h(b));
   } else if constexpr (W == 4) {
+    constexpr uint32_t b0 = half_pair(-1024.0 - MID, -1024.0 - MID), b1 = half_pair(-64.0 - MID, -64.0 - MID);
+    constexpr uint32_t q = half_pair(0.0625, 0.0625);
     const uint32_t y = w0 >> 8;
-    const __half2 b0 = __float2half2_rn(-1024.0f - mid), b1 = __float2half2_rn(-64.0f - mid),
-                  q = __float2half2_rn(0.0625f);
-    o[0] = __hadd2(u2h((w0 & 0x000f000fu) | kExp), b0);
-    o[1] = __hfma2(u2h((w0 & 0x00f000f0u) | kExp), q, b1);
-    o[2] = __hadd2(u2h((y & 0x000f000fu) | kExp), b0);
-    o[3] = __hfma2(u2h((y & 0x00f000f0u) | kExp), q, b1);
+    o[0] = __hadd2(u2h((w0 & 0x000f000fu) | kExp), u2h(b0));
+    o[1] = __hfma2(u2h((w0 & 0x00f000f0u) | kExp), u2h(q), u2h(b1));
+    o[2] = __hadd2(u2h((y & 0x000f000fu) | kExp), u2h(b0));
+    o[3] = __hfma2(u2h((y & 0x00f000f0u) | kExp), u2h(q), u2h(b1));
   } else if constexpr (W == 2) {  // the low 16 bits
+    constexpr uint32_t q[4] = {half_pair(1.0, 1.0), half_pair(0.25, 0.25), half_pair(0.0625, 0.0625),
+                               half_pair(0.015625, 0.015625)};
+    constexpr uint32_t b[4] = {half_pair(-1024.0 - MID, -1024.0 - MID), half_pair(-256.0 - MID, -256.0 - MID),
+                               half_pair(-64.0 - MID, -64.0 - MID), half_pair(-16.0 - MID, -16.0 - MID)};
     const uint32_t y = __byte_perm(w0, 0, 0x4140);
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      o[k] = __hfma2(u2h((y & (0x00030003u << (2 * k))) | kExp), __float2half2_rn(1.0f / (1 << (2 * k))),
-                     __float2half2_rn(-1024.0f / (1 << (2 * k)) - mid));
+    for (int k = 0; k < 4; ++k) o[k] = __hfma2(u2h((y & (0x00030003u << (2 * k))) | kExp), u2h(q[k]), u2h(b[k]));
   } else {  // W == 1: the low 8 bits
+    constexpr uint32_t q[4] = {half_pair(1.0, 0.0625), half_pair(0.5, 0.03125), half_pair(0.25, 0.015625),
+                               half_pair(0.125, 0.0078125)};
+    constexpr uint32_t b[4] = {half_pair(-1024.0 - MID, -64.0 - MID), half_pair(-512.0 - MID, -32.0 - MID),
+                               half_pair(-256.0 - MID, -16.0 - MID), half_pair(-128.0 - MID, -8.0 - MID)};
     const uint32_t y = __byte_perm(w0, 0, 0x4040);
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      o[k] = __hfma2(u2h((y & ((1u << k) | (0x100000u << k))) | kExp),
-                     __floats2half2_rn(1.0f / (1 << k), 1.0f / (16 << k)),
-                     __floats2half2_rn(-1024.0f / (1 << k) - mid, -64.0f / (1 << k) - mid));
+      o[k] = __hfma2(u2h((y & ((1u << k) | (0x100000u << k))) | kExp), u2h(q[k]), u2h(b[k]));
   }
 }
 

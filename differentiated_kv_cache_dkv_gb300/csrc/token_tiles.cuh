@@ -54,61 +54,65 @@ __device__ __forceinline__ Tile tile_at(const Tiles &ts, const Unit &x, int32_t 
 
 // ------------------------------------------------------- dequantising warps --
 //
-// Four threads a token, 32 channels each, two tokens (tk and tk + 64) a
-// thread.  The thread of channels 64 .. takes its two 16-channel halves in the
+// Four threads a token, 32 channels each, NP tokens a thread: tk + p 128 / NP.  The thread of channels 64 .. takes its two 16-channel halves in the
 // other order, so that the eight threads of two neighbouring rows always
 // write eight different 16-byte chunks of the swizzled rows.
 struct DeqCtx {
   const ExtendArgs *a;
   Unit x;
   uint32_t m1, m2;  // split() by P and 2 P
-  int64_t bytes;
-  int32_t vbase, meta;
+  int32_t bytes;
+  uint32_t vbase, meta;
   int tk, c, hs;    // token, quarter of the channels, which half comes first
   uint32_t off[4];  // operand-tile offsets of the thread's four groups (token tk)
 };
 
+template <int NP>
 struct Held {
-  uint32_t k[2][2][4], v[2][2][4];  // [token][half][words]
-  uint2 md[2];
-  bool ok[2];
+  uint32_t k[NP][2][4], v[NP][2][4];  // [token][half][words]
+  uint2 md[NP];
+  bool ok[NP];
 };
 
-// Where the two tokens of a tile lie: page ids (-1: no token) and slots.
+// Where the thread's tokens of a tile lie: page ids (-1: no token) and slots.
+template <int NP>
 struct Where {
-  int32_t id[2], slot[2];
+  int32_t id[NP], slot[NP];
 };
 
-__device__ __forceinline__ void locate(const DeqCtx &d, const Tile &t, Where &w) {
+template <int NP>
+__device__ __forceinline__ void locate(const DeqCtx &d, const Tile &t, Where<NP> &w) {
   if (t.kind == 2) return;
   const bool high = t.kind == 0;
   const int32_t per = high ? d.a->P : 2 * d.a->P, first = high ? 0 : d.x.p_hi;
   const uint32_t M = high ? d.m1 : d.m2;
 #pragma unroll
-  for (int p = 0; p < 2; ++p) {
-    const int32_t i = d.tk + 64 * p;
+  for (int p = 0; p < NP; ++p) {
+    const int32_t i = d.tk + 128 / NP * p;
     int32_t k;
     split(t.t0 + i, per, M, k, w.slot[p]);
     w.id[p] = i < t.n ? __ldg(d.a->fwd + d.x.u * d.a->pmax + first + k) : -1;
   }
 }
 
-template <int KW, int VW>
-__device__ __forceinline__ void fetch(const DeqCtx &d, const Where &w, Held &h, bool k, bool v) {
+// Codes of the thread's tokens: its two 16-channel halves of a W-bit row lie
+// 2 W (8 slot + 2 c + half) bytes into the rows.
+template <int KW, int VW, int NP>
+__device__ __forceinline__ void fetch(const DeqCtx &d, const Where<NP> &w, Held<NP> &h, bool k, bool v) {
 #pragma unroll
-  for (int p = 0; p < 2; ++p) {
+  for (int p = 0; p < NP; ++p) {
     const bool ok = w.id[p] >= 0 && w.id[p] < d.a->F;
-    const uint8_t *pg = d.a->pages + (ok ? w.id[p] : 0) * d.bytes;  // page 0 stands in: masked, or its scale is 0
+    // page 0 stands in for none: masked, or its scale is 0
+    const uint8_t *pg = d.a->pages + static_cast<int64_t>(ok ? w.id[p] : 0) * d.bytes;
+    const uint32_t u0 = 8 * w.slot[p] + 2 * d.c + d.hs, u1 = u0 ^ 1u;
     if (k) {
-      const uint8_t *src = pg + w.slot[p] * (16 * KW) + d.c * (4 * KW);
-      load16<KW>(h.k[p][0], src + d.hs * (2 * KW));
-      load16<KW>(h.k[p][1], src + (d.hs ^ 1) * (2 * KW));
+      load16<KW>(h.k[p][0], pg + 2 * KW * u0);
+      load16<KW>(h.k[p][1], pg + 2 * KW * u1);
     }
     if (v) {
-      const uint8_t *src = pg + d.vbase + w.slot[p] * (16 * VW) + d.c * (4 * VW);
-      load16<VW>(h.v[p][0], src + d.hs * (2 * VW));
-      load16<VW>(h.v[p][1], src + (d.hs ^ 1) * (2 * VW));
-      h.md[p] = __ldg(reinterpret_cast<const uint2 *>(pg + d.meta + 8 * w.slot[p]));
+      load16<VW>(h.v[p][0], pg + (d.vbase + 2 * VW * u0));
+      load16<VW>(h.v[p][1], pg + (d.vbase + 2 * VW * u1));
+      h.md[p] = __ldg(reinterpret_cast<const uint2 *>(pg + (d.meta + 8u * w.slot[p])));
       h.ok[p] = ok;
       if (!ok) h.md[p] = make_uint2(0, 0);
     }
@@ -119,21 +123,21 @@ __device__ __forceinline__ void put(uint8_t *tile, uint32_t at, const __half2 (&
   *reinterpret_cast<uint4 *>(tile + at) = make_uint4(h2u(o[0]), h2u(o[1]), h2u(o[2]), h2u(o[3]));
 }
 
-template <int W, class S>
-__device__ __forceinline__ void convert_k(const DeqCtx &d, const Held &h, S &sm, uint8_t *dst, int slot, float f) {
-  constexpr float kMid = 1 << (W - 1);
+template <int W, class S, int NP>
+__device__ __forceinline__ void convert_k(const DeqCtx &d, const Held<NP> &h, S &sm, uint8_t *dst, int slot, float f) {
+  constexpr int kMid = 1 << (W - 1);
 #pragma unroll
-  for (int p = 0; p < 2; ++p) {
+  for (int p = 0; p < NP; ++p) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       uint32_t w0, w1;
       __half2 o[4];
       group_of<W>(h.k[p][i >> 1], i & 1, w0, w1);
-      group_codes<W>(w0, w1, kMid, o);
-      put(dst, d.off[i] + p * (64 * 128), o);
+      group_codes<W, kMid>(w0, w1, o);
+      put(dst, d.off[i] + p * (128 / NP * 128), o);
     }
     if (d.c == 0) {
-      const int row = d.tk + 64 * p;
+      const int row = d.tk + 128 / NP * p;
       const __half2 m = u2h(h.md[p].x);
       const float s = __low2float(m), z = __high2float(m);
       sm.s[slot][row] = s * f;
@@ -143,28 +147,31 @@ __device__ __forceinline__ void convert_k(const DeqCtx &d, const Held &h, S &sm,
   }
 }
 
-template <int W>
-__device__ __forceinline__ void convert_v(const DeqCtx &d, const Held &h, uint8_t *dst) {
+template <int W, int NP>
+__device__ __forceinline__ void convert_v(const DeqCtx &d, const Held<NP> &h, uint8_t *dst) {
 #pragma unroll
-  for (int p = 0; p < 2; ++p) {
+  for (int p = 0; p < NP; ++p) {
     const __half2 m = u2h(h.md[p].y);
     const __half2 s = __low2half2(m), z = __high2half2(m);
-    // a dequantised value can pass fp16's largest by half a scale step
-    const bool big = fmaf(static_cast<float>((1 << W) - 1), __low2float(m), fabsf(__high2float(m))) > 65000.0f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       uint32_t w0, w1;
       __half2 o[4];
       group_of<W>(h.v[p][i >> 1], i & 1, w0, w1);
-      group_codes<W>(w0, w1, 0.0f, o);
+      group_codes<W, 0>(w0, w1, o);
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[e] = __hfma2(o[e], s, z);
-      if (big) {
-        const __half2 top = __float2half2_rn(65504.0f);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] = __hmax2(__hmin2(o[e], top), __hneg2(top));
+      put(dst, d.off[i] + p * (128 / NP * 128), o);
+    }
+    // a dequantised value can pass fp16's largest by half a scale step: the
+    // infinities go back to it (out of the way of the usual tokens' code)
+    if (__builtin_expect(fmaf(static_cast<float>((1 << W) - 1), __low2float(m), fabsf(__high2float(m))) > 65000.0f, 0)) {
+#pragma unroll 1
+      for (int i = 0; i < 16; ++i) {
+        const uint32_t off = group_at(d.tk + 128 / NP * p, 4 * d.c + (i >> 2)) + 4 * (i & 3);
+        __half2 *x = reinterpret_cast<__half2 *>(dst + off);
+        *x = __hmax2(__hmin2(*x, u2h(0x7bff7bffu)), u2h(0xfbfffbffu));
       }
-      put(dst, d.off[i] + p * (64 * 128), o);
     }
   }
 }
@@ -190,12 +197,12 @@ __device__ __forceinline__ void load_new(const DeqCtx &d, const uint16_t *base, 
 
 // K of the new tokens: each row times the power of two that puts its largest
 // value into [2^14, 2^15), in fp16; the scale carries it back.
-template <bool kValid, class S>
+template <int NP, bool kValid, class S>
 __device__ __forceinline__ void new_k(const DeqCtx &d, const Tile &t, int64_t tok0, int32_t h, S &sm, uint8_t *dst,
                                       int slot, float f) {
 #pragma unroll 1
-  for (int p = 0; p < 2; ++p) {
-    const int row = d.tk + 64 * p;
+  for (int p = 0; p < NP; ++p) {
+    const int row = d.tk + 128 / NP * p;
     uint4 x[2][2];
     float mx = 0.0f;
 #pragma unroll
@@ -212,7 +219,7 @@ __device__ __forceinline__ void new_k(const DeqCtx &d, const Tile &t, int64_t to
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint4 v = x[i >> 1][i & 1];
-      *reinterpret_cast<uint4 *>(dst + d.off[i] + p * (64 * 128)) = make_uint4(
+      *reinterpret_cast<uint4 *>(dst + d.off[i] + p * (128 / NP * 128)) = make_uint4(
           f16x2_rn(bf16_lo(v.x) * sc, bf16_lo(v.z) * sc), f16x2_rn(bf16_hi(v.x) * sc, bf16_hi(v.z) * sc),
           f16x2_rn(bf16_lo(v.y) * sc, bf16_lo(v.w) * sc), f16x2_rn(bf16_hi(v.y) * sc, bf16_hi(v.w) * sc));
     }
@@ -224,19 +231,20 @@ __device__ __forceinline__ void new_k(const DeqCtx &d, const Tile &t, int64_t to
   }
 }
 
+template <int NP>
 __device__ __forceinline__ void new_v(const DeqCtx &d, const Tile &t, int64_t tok0, int32_t h, uint8_t *dst) {
 #pragma unroll 1
-  for (int p = 0; p < 2; ++p) {
+  for (int p = 0; p < NP; ++p) {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const int row = d.tk + 64 * p;
+      const int row = d.tk + 128 / NP * p;
       uint4 x[2];
       load_new(d, d.a->v_new, (tok0 + t.t0 + row) * d.a->Hkv + h, row < t.n, e, x);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         uint32_t g[4];
         group_bf16(x[i], g);
-        *reinterpret_cast<uint4 *>(dst + d.off[2 * e + i] + p * (64 * 128)) = make_uint4(g[0], g[1], g[2], g[3]);
+        *reinterpret_cast<uint4 *>(dst + d.off[2 * e + i] + p * (128 / NP * 128)) = make_uint4(g[0], g[1], g[2], g[3]);
       }
     }
   }

@@ -48,8 +48,7 @@ struct __align__(1024) Smem {
   uint8_t v[2][kTileBytes];
   uint8_t p[128 * 128];       // tokens x 64 rows
   uint8_t q[2][64 * 128];     // 64 rows x 64 channels, twice
-  uint8_t raw[kRaw][192 * 128];  // codes of a tile: K rows, then V rows (192 bytes a token at most)
-  uint2 md[kRaw][128];           // its tokens' scales and zeros
+  uint8_t raw[kRaw][200 * 128];  // a tile's pages: codes, scales and zeros (200 bytes a token at most)
   uint32_t there[kRaw][4];       // which of its tokens exist
   float s[kMeta][128], z[kMeta][128];
   uint8_t valid[kMeta][128];
@@ -66,7 +65,7 @@ struct __align__(1024) Smem {
 constexpr size_t kSmemBytes = sizeof(Smem) + 1024;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 static_assert(offsetof(Smem, q) % 1024 == 0 && offsetof(Smem, p) % 1024 == 0, "swizzled operands");
-static_assert(offsetof(Smem, raw) % 16 == 0 && offsetof(Smem, md) % 16 == 0, "bulk copies");
+static_assert(offsetof(Smem, raw) % 16 == 0, "bulk copies");
 
 __device__ __forceinline__ uint32_t ordered(float x) {
   const int32_t i = __float_as_int(x);
@@ -94,15 +93,35 @@ __device__ __forceinline__ void copy_bulk(void *dst, const void *src, uint32_t n
                : "memory");
 }
 
-// The two 16-channel halves of each of the thread's tokens, in its order, from
-// the token's raw row of 16 W bytes.
+// How a raw tile lies in shared memory: token i is slot i mod 2^lg of "page"
+// i >> lg, pages `stride` bytes apart, with V codes and scales at vb and mo.
+// Where pages divide a tile those are the pages themselves, as they lie in
+// memory up to their last used scale: one copy a page.  Otherwise it is one
+// page of 128 slots, which three copies per page and tile put together.
+struct RawForm {
+  int32_t lg, stride, vb, mo;
+  bool whole;
+};
+
+template <int KW, int VW>
+__device__ __forceinline__ RawForm raw_form(int32_t P, bool high) {
+  const int32_t per = high ? P : 2 * P;
+  const bool whole = per <= 128 && (per & (per - 1)) == 0;
+  const int32_t n = whole ? per : 128;
+  // per W-bit slots take 16 W per bytes, scales 8 per
+  return RawForm{31 - __clz(n), n * (16 * (KW + VW) + 8), n * 16 * KW, n * 16 * (KW + VW), whole};
+}
+
+// The two 16-channel halves of each of the thread's tokens, in its order.
 template <int W>
-__device__ __forceinline__ void read_raw(const DeqCtx &d, const uint8_t *raw, uint32_t (&x)[kNP][2][4]) {
+__device__ __forceinline__ void read_raw(const DeqCtx &d, const RawForm &f, const uint8_t *raw, uint32_t (&x)[kNP][2][4]) {
 #pragma unroll
-  for (int p = 0; p < kNP; ++p)
+  for (int p = 0; p < kNP; ++p) {
+    const int i = d.tk + 128 / kNP * p, slot = i & ((1 << f.lg) - 1);
+    const uint8_t *row = raw + (i >> f.lg) * f.stride + slot * (16 * W);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const uint8_t *src = raw + (d.tk + 128 / kNP * p) * (16 * W) + 2 * W * (2 * d.c + (d.hs ^ e));
+      const uint8_t *src = row + 2 * W * (2 * d.c + (d.hs ^ e));
       if constexpr (W == 8) {
         const uint4 v = *reinterpret_cast<const uint4 *>(src);
         x[p][e][0] = v.x, x[p][e][1] = v.y, x[p][e][2] = v.z, x[p][e][3] = v.w;
@@ -115,47 +134,77 @@ __device__ __forceinline__ void read_raw(const DeqCtx &d, const uint8_t *raw, ui
         x[p][e][0] = *reinterpret_cast<const uint16_t *>(src);
       }
     }
+  }
 }
 
-// One warp: the rows of tile t into a raw tile.  A page's tokens of the tile
-// are contiguous in each of its parts; P is even, so a page's first slot here
-// and an even count keep the 8-byte scales on 16-byte boundaries (an odd last
-// token takes its neighbour's along, still inside the page).
+__device__ __forceinline__ uint2 read_md(const RawForm &f, const uint8_t *raw, int i) {
+  return *reinterpret_cast<const uint2 *>(raw + (i >> f.lg) * f.stride + f.mo + 8 * (i & ((1 << f.lg) - 1)));
+}
+
+// A tile's pages [k0, k0 + n) of the forward row; a lane holds the ids of three
+// at most (pages of two tokens: 65 in a tile).
+struct Pages {
+  int32_t k0, n, id[3];
+};
+
+__device__ __forceinline__ Pages pages_of(const ExtendArgs &a, const Unit &x, const Tile &t) {
+  Pages g{};
+  if (t.kind == 2) return g;
+  const int32_t per = t.kind == 0 ? a.P : 2 * a.P, lane = threadIdx.x & 31;
+  g.k0 = t.t0 / per;
+  g.n = (t.t0 + t.n - 1) / per - g.k0 + 1;
+  const int32_t *fwd = a.fwd + x.u * a.pmax + (t.kind == 0 ? 0 : x.p_hi) + g.k0;
+#pragma unroll
+  for (int i = 0; i < 3; ++i) g.id[i] = lane + 32 * i < g.n ? __ldg(fwd + lane + 32 * i) : -1;
+  return g;
+}
+
+// One warp: the pages of tile t into a raw tile.  P is even, so that a page's
+// first slot here and an even count keep the 8-byte scales on 16-byte
+// boundaries (an odd last token takes its neighbour's along, still inside the
+// page).
 template <int KW, int VW>
-__device__ __forceinline__ void copy_tile(const ExtendArgs &a, const Unit &x, const Tile &t, uint8_t *raw, uint2 *md,
+__device__ __forceinline__ void copy_tile(const ExtendArgs &a, const Tile &t, const Pages &g, uint8_t *raw,
                                           uint32_t *there, uint64_t *bar, uint32_t vbase, uint32_t meta, int64_t bytes) {
   const int lane = threadIdx.x & 31;
-  const int32_t per = t.kind == 0 ? a.P : 2 * a.P;
-  const int32_t k0 = t.t0 / per, pages = (t.t0 + t.n - 1) / per - k0 + 1;
-  const int32_t *fwd = a.fwd + x.u * a.pmax + (t.kind == 0 ? 0 : x.p_hi) + k0;
+  const bool high = t.kind == 0;
+  const int32_t per = high ? a.P : 2 * a.P;
+  const RawForm f = raw_form<KW, VW>(a.P, high);
   uint32_t sum = 0;
   if (lane < 4) there[lane] = 0;
   __syncwarp();
-  for (int32_t k = lane; k < pages; k += 32) {  // bytes first: the barrier must expect them before they land
-    const int32_t id = __ldg(fwd + k);
-    const int32_t first = max(t.t0 - (k0 + k) * per, 0), n = min((k0 + k + 1) * per, t.t0 + t.n) - (k0 + k) * per - first;
-    if (id < 0 || id >= a.F) {
+  int32_t first[3], n[3], to[3];  // first slot, slots, first token of the tile
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    const int32_t k = lane + 32 * i, p0 = (g.k0 + k) * per;
+    n[i] = 0;
+    if (k >= g.n) continue;
+    if (g.id[i] < 0 || g.id[i] >= a.F) {
       set_error(a.status, DKV_E_INTERNAL);
-    } else {
-      sum += n * (16 * KW + 16 * VW) + 8 * ((n + 1) & ~1);
-      const int32_t to = (k0 + k) * per + first - t.t0;
-      for (int32_t i = to; i < to + n; i += 32 - (i & 31))  // bits [to, to + n)
-        atomicOr(there + (i >> 5), (0xffffffffu >> (32 - min(32 - (i & 31), to + n - i))) << (i & 31));
+      continue;
     }
+    first[i] = max(t.t0 - p0, 0);
+    n[i] = min(p0 + per, t.t0 + t.n) - p0 - first[i];
+    to[i] = p0 + first[i] - t.t0;
+    sum += f.whole ? f.stride : n[i] * (16 * KW + 16 * VW) + 8 * ((n[i] + 1) & ~1);
+    for (int32_t b = to[i]; b < to[i] + n[i]; b += 32 - (b & 31))  // bits [to, to + n)
+      atomicOr(there + (b >> 5), (0xffffffffu >> (32 - min(32 - (b & 31), to[i] + n[i] - b))) << (b & 31));
   }
   sum = __reduce_add_sync(kFull, sum);
   __syncwarp();  // the bits above are part of what the arrival publishes
-  if (lane == 0) mbar_expect_tx(bar, sum);
+  if (lane == 0) mbar_expect_tx(bar, sum);  // before any copy can land
   __syncwarp();
-  for (int32_t k = lane; k < pages; k += 32) {
-    const int32_t id = __ldg(fwd + k);
-    if (id < 0 || id >= a.F) continue;
-    const int32_t first = max(t.t0 - (k0 + k) * per, 0), n = min((k0 + k + 1) * per, t.t0 + t.n) - (k0 + k) * per - first;
-    const int32_t to = (k0 + k) * per + first - t.t0;
-    const uint8_t *pg = a.pages + id * bytes;
-    copy_bulk(raw + to * (16 * KW), pg + first * (16 * KW), n * (16 * KW), bar);
-    copy_bulk(raw + 128 * 16 * KW + to * (16 * VW), pg + vbase + first * (16 * VW), n * (16 * VW), bar);
-    copy_bulk(md + to, pg + meta + 8 * first, 8 * ((n + 1) & ~1), bar);
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    if (n[i] == 0) continue;
+    const uint8_t *pg = a.pages + g.id[i] * bytes;
+    if (f.whole) {
+      copy_bulk(raw + (to[i] >> f.lg) * f.stride, pg, f.stride, bar);
+    } else {
+      copy_bulk(raw + to[i] * (16 * KW), pg + first[i] * (16 * KW), n[i] * (16 * KW), bar);
+      copy_bulk(raw + f.vb + to[i] * (16 * VW), pg + vbase + first[i] * (16 * VW), n[i] * (16 * VW), bar);
+      copy_bulk(raw + f.mo + to[i] * 8, pg + meta + 8 * first[i], 8 * ((n[i] + 1) & ~1), bar);
+    }
   }
 }
 
@@ -449,21 +498,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int ms = j % kMeta, st = j % kRaw;
       Held<kNP> hd;
       if (!(ok = warp_wait(&sm.rfull[st], (j / kRaw) & 1u))) break;
+      const RawForm rf = t.kind == 0 ? raw_form<KH, VH>(a.P, true) : raw_form<KH / 2, VH / 2>(a.P, false);
 #pragma unroll
       for (int p = 0; p < kNP; ++p) {
         const int row = d.tk + 128 / kNP * p;
         hd.ok[p] = sm.there[st][row >> 5] >> (row & 31) & 1u;
-        hd.md[p] = hd.ok[p] ? sm.md[st][row] : make_uint2(0, 0);
+        hd.md[p] = hd.ok[p] ? read_md(rf, sm.raw[st], row) : make_uint2(0, 0);
       }
       if (j >= 1 && !(ok = warp_wait(&sm.kempty, (j - 1) & 1u))) break;
       if (t.kind == 0) {
-        read_raw<KH>(d, sm.raw[st], hd.k);
+        read_raw<KH>(d, rf, sm.raw[st], hd.k);
         convert_k<KH>(d, hd, sm, sm.k, ms, f);
-        read_raw<VH>(d, sm.raw[st] + 128 * 16 * KH, hd.v);
+        read_raw<VH>(d, rf, sm.raw[st] + rf.vb, hd.v);
       } else if (t.kind == 1) {
-        read_raw<KH / 2>(d, sm.raw[st], hd.k);
+        read_raw<KH / 2>(d, rf, sm.raw[st], hd.k);
         convert_k<KH / 2>(d, hd, sm, sm.k, ms, f);
-        read_raw<VH / 2>(d, sm.raw[st] + 128 * 8 * KH, hd.v);
+        read_raw<VH / 2>(d, rf, sm.raw[st] + rf.vb, hd.v);
       } else {
         new_k<kNP, true>(d, t, tok0, h, sm, sm.k, ms, f);
       }
@@ -488,17 +538,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     const PageGeom pg = page_geom(SC, a.P);
     bool ok = true;
     int32_t j = 0;
+    Pages next = pages_of(a, x, tile_at(ts, x, fresh, j0));
 #pragma unroll 1
     for (; j < n; ++j) {
       const Tile t = tile_at(ts, x, fresh, j0 + j);
+      const Pages g = next;
+      if (j + 1 < n) next = pages_of(a, x, tile_at(ts, x, fresh, j0 + j + 1));
       const int st = j % kRaw;
       if (j >= kRaw && !(ok = warp_wait(&sm.rempty[st], (j / kRaw - 1) & 1u))) break;
       if (t.kind == 0) {
-        copy_tile<KH, VH>(a, x, t, sm.raw[st], sm.md[st], sm.there[st], &sm.rfull[st], static_cast<uint32_t>(pg.vbase),
+        copy_tile<KH, VH>(a, t, g, sm.raw[st], sm.there[st], &sm.rfull[st], static_cast<uint32_t>(pg.vbase),
                           static_cast<uint32_t>(pg.meta), pg.bytes);
       } else if (t.kind == 1) {
-        copy_tile<KH / 2, VH / 2>(a, x, t, sm.raw[st], sm.md[st], sm.there[st], &sm.rfull[st],
-                                  static_cast<uint32_t>(pg.vbase), static_cast<uint32_t>(pg.meta), pg.bytes);
+        copy_tile<KH / 2, VH / 2>(a, t, g, sm.raw[st], sm.there[st], &sm.rfull[st], static_cast<uint32_t>(pg.vbase),
+                                  static_cast<uint32_t>(pg.meta), pg.bytes);
       } else if (lane == 0) {
         mbar_arrive(&sm.rfull[st]);  // new tokens are read where they are converted
       }

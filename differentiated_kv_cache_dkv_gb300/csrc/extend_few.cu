@@ -86,13 +86,6 @@ __device__ __forceinline__ bool meet(bool p) {
   return r != 0;
 }
 
-// Bulk copy of n bytes (a multiple of 16, as both addresses) to shared memory.
-__device__ __forceinline__ void copy_bulk(void *dst, const void *src, uint32_t n, uint64_t *bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(saddr(dst)),
-               "l"(src), "r"(n), "r"(saddr(bar))
-               : "memory");
-}
-
 // How a raw tile lies in shared memory: token i is slot i mod 2^lg of "page"
 // i >> lg, pages `stride` bytes apart, with V codes and scales at vb and mo.
 // Where pages divide a tile those are the pages themselves, as they lie in
@@ -122,17 +115,7 @@ __device__ __forceinline__ void read_raw(const DeqCtx &d, const RawForm &f, cons
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const uint8_t *src = row + 2 * W * (2 * d.c + (d.hs ^ e));
-      if constexpr (W == 8) {
-        const uint4 v = *reinterpret_cast<const uint4 *>(src);
-        x[p][e][0] = v.x, x[p][e][1] = v.y, x[p][e][2] = v.z, x[p][e][3] = v.w;
-      } else if constexpr (W == 4) {
-        const uint2 v = *reinterpret_cast<const uint2 *>(src);
-        x[p][e][0] = v.x, x[p][e][1] = v.y;
-      } else if constexpr (W == 2) {
-        x[p][e][0] = *reinterpret_cast<const uint32_t *>(src);
-      } else {
-        x[p][e][0] = *reinterpret_cast<const uint16_t *>(src);
-      }
+      read16<W>(x[p][e], src);
     }
   }
 }

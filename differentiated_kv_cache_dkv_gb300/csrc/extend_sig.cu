@@ -22,6 +22,7 @@
 //   sum warps (2 x 4)  a thread per token, tiles w and w + 2 of the group.
 #include <algorithm>
 #include <cmath>
+#include <cstddef>
 
 #include "token_tiles.cuh"
 
@@ -32,21 +33,31 @@ namespace {
 using namespace tc;
 
 constexpr int kSumWarps = 8, kConvWarps = 8;
-constexpr int kMmaWarp = kSumWarps + kConvWarps;
-constexpr int kThreads = 32 * (kMmaWarp + 1);
+constexpr int kMmaWarp = kSumWarps + kConvWarps, kCopyWarp = kMmaWarp + 1, kCopyWarps = 3;
+constexpr int kThreads = 32 * (kCopyWarp + kCopyWarps);
 constexpr uint32_t kTmemCols = 512;
 constexpr int kGroup = 4;    // token tiles resident at once
-constexpr int kMaxAcc = 8;   // heads whose sums wait in shared memory for one joint update
+constexpr int kHeads = 8;    // most heads of a block of Q
+
+// Raw tiles: K codes of 128 tokens, K's scales and zeros, positions.  The ring lies behind the first
+// block of Q and takes the second one's place too where there is none.
+template <int KH>
+struct Raw {
+  static constexpr int kMd = 128 * 16 * KH, kPos = kMd + 128 * 4, kSlot = kPos + 128 * 4;
+};
+constexpr int kExtra = 3 * Raw<8>::kSlot - kTileBytes;
+constexpr int kRaw = kCopyWarps;  // a slot each
 
 struct __align__(1024) Smem {
   uint8_t k[kGroup][kTileBytes];
   uint8_t q[2][kTileBytes];
-  float s[2 * kGroup][128], z[2 * kGroup][128];  // by parity of the group
-  int32_t pos[2 * kGroup][128];                  // -1: not a token
-  float4 col[4][64];                             // per column pair: row sums of Q, -lse (log2)
-  float acc[kGroup][kMaxAcc][128];
-  uint64_t kfull[kGroup], kempty[kGroup], mfull[2 * kGroup], sfull[kGroup], sfree[kGroup];
-  uint64_t qfull[2], qempty[2], cfull[4], qm[4], done;
+  uint8_t extra[kExtra];
+  float s[kGroup][128], z[kGroup][128];
+  int32_t pos[kGroup][128];     // -1: not a token
+  float4 col[4][64];            // per column pair: row sums of Q, -lse (log2)
+  uint32_t there[kRaw][4];   // which of a raw tile's tokens exist
+  uint64_t kfull[kGroup], kempty[kGroup], sfull[kGroup], sfree[kGroup];
+  uint64_t qfull[2], qempty[2], cfull[4], cempty[4], qm[4], done, rfull[kRaw], rempty[kRaw];
   uint32_t qmax[4];
   float qf[4];  // 2^-e of the block's Q
   uint32_t tmem;
@@ -54,52 +65,86 @@ struct __align__(1024) Smem {
 };
 constexpr size_t kSmemBytes = sizeof(Smem) + 1024;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+static_assert(offsetof(Smem, extra) == offsetof(Smem, q) + 2 * kTileBytes, "one region");
 
-// Tokens tk and tk + 64 of a tile: K codes, scale and zero, position.
-struct Key {
-  uint32_t k[2][2][4];
-  uint32_t md[2];
-  int32_t pos[2];
+// Pages [k0, k0 + n) of a unit's list that a tile lies in: fwd, their ids; id,
+// the lane's of the first 32.
+struct PageRange {
+  int32_t per, k0, n, id;
+  uint32_t M;
+  const int32_t *fwd;
 };
 
-template <int KW>
-__device__ __forceinline__ void fetch_key(const DeqCtx &d, const Where<2> &w, Key &h, int32_t posoff) {
+// One warp: the tile's K codes, scales and positions into a raw tile.  The
+// codes go by one bulk copy a page (issuing one takes a warp about 54 cycles,
+// whatever its size), the rest by asynchronous copies of four bytes.
+template <int KH>
+__device__ __forceinline__ void copy_keys(const ExtendArgs &a, const Tile &t, const PageRange &g, const PageGeom &pg,
+                                          uint8_t *raw, uint32_t *there, uint64_t *bar) {
+  const int lane = threadIdx.x & 31;
+  const int32_t rowb = t.kind == 0 ? 16 * KH : 8 * KH;
+  int32_t k, slot;
+  split(t.t0 + lane, g.per, g.M, k, slot);
+  uint32_t have = 0;
 #pragma unroll
-  for (int p = 0; p < 2; ++p) {
-    const bool ok = w.id[p] >= 0 && w.id[p] < d.a->F;
-    const uint8_t *pg = d.a->pages + (ok ? w.id[p] : 0) * d.bytes;
-    const uint8_t *src = pg + w.slot[p] * (16 * KW) + d.c * (4 * KW);
-    load16<KW>(h.k[p][0], src + d.hs * (2 * KW));
-    load16<KW>(h.k[p][1], src + (d.hs ^ 1) * (2 * KW));
-    h.md[p] = __ldg(reinterpret_cast<const uint32_t *>(pg + d.meta + 8 * w.slot[p]));
-    h.pos[p] = ok ? __ldg(reinterpret_cast<const int32_t *>(pg + posoff + 4 * w.slot[p])) : -1;
-    if (!ok && w.id[p] != -1) set_error(d.a->status, DKV_E_INTERNAL);
+  for (int i = 0; i < 4; ++i) {
+    const int32_t in = k - g.k0, other = __shfl_sync(kFull, g.id, in & 31);
+    const int32_t id = lane + 32 * i >= t.n ? -1 : in < 32 ? other : __ldg(g.fwd + in);
+    const bool ok = id >= 0 && id < a.F;
+    if (ok) {
+      const uint8_t *src = a.pages + id * pg.bytes;
+      copy_async4(raw + Raw<KH>::kMd + 4 * (lane + 32 * i), src + pg.meta + 8 * slot);
+      copy_async4(raw + Raw<KH>::kPos + 4 * (lane + 32 * i), src + pg.pos + 4 * slot);
+    } else if (lane + 32 * i < t.n) {
+      set_error(a.status, DKV_E_INTERNAL);
+    }
+    const uint32_t b = __ballot_sync(kFull, ok);
+    have += __popc(b);
+    if (lane == 0) there[i] = b;
+    for (slot += 32; slot >= g.per; slot -= g.per) ++k;
   }
+  if (lane == 0) mbar_expect_tx(bar, have * rowb);  // before any copy can land
+  __syncwarp();
+#pragma unroll 1
+  for (int32_t k = lane; k < g.n; k += 32) {
+    const int32_t id = k < 32 ? g.id : __ldg(g.fwd + k);
+    if (id < 0 || id >= a.F) continue;
+    const int32_t p0 = (g.k0 + k) * g.per, first = max(t.t0 - p0, 0);
+    const int32_t n = min(p0 + g.per, t.t0 + t.n) - p0 - first;
+    copy_bulk(raw + (p0 + first - t.t0) * rowb, a.pages + id * pg.bytes + first * rowb, n * rowb, bar);
+  }
+  arrive_async(bar);
 }
 
-template <int W>
-__device__ __forceinline__ void convert_key(const DeqCtx &d, const Where<2> &w, const Key &h, Smem &sm, uint8_t *dst,
-                                            int slot, float f, int32_t ctx) {
+// Tokens tk and tk + 64 of a raw tile: codes, scale and zero, position.
+template <int W, int KH>
+__device__ __forceinline__ void convert_key(const DeqCtx &d, const uint8_t *raw, const uint32_t *there, Smem &sm, int q,
+                                            float f, int32_t ctx) {
   constexpr int kMid = 1 << (W - 1);
-#pragma unroll
+#pragma unroll 1
   for (int p = 0; p < 2; ++p) {
+    const int row = d.tk + 64 * p;
+    uint32_t x[2][4];
+    read16<W>(x[0], raw + row * (16 * W) + 2 * W * (2 * d.c + d.hs));
+    read16<W>(x[1], raw + row * (16 * W) + 2 * W * (2 * d.c + (d.hs ^ 1)));
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       uint32_t w0, w1;
       __half2 o[4];
-      group_of<W>(h.k[p][i >> 1], i & 1, w0, w1);
+      group_of<W>(x[i >> 1], i & 1, w0, w1);
       group_codes<W, kMid>(w0, w1, o);
-      put(dst, d.off[i] + p * (64 * 128), o);
+      put(sm.k[q], d.off[i] + p * (64 * 128), o);
     }
     if (d.c == 0) {
-      const int row = d.tk + 64 * p;
-      const __half2 m = u2h(h.md[p]);
+      const bool ok = there[row >> 5] >> (row & 31) & 1u;
+      const __half2 m = u2h(ok ? *reinterpret_cast<const uint32_t *>(raw + Raw<KH>::kMd + 4 * row) : 0u);
+      const int32_t at = ok ? *reinterpret_cast<const int32_t *>(raw + Raw<KH>::kPos + 4 * row) : 0;
       const float s = __low2float(m), z = __high2float(m);
-      sm.s[slot][row] = s * f;
-      sm.z[slot][row] = fmaf(kMid, s, z) * f;
-      const bool bad = h.pos[p] >= ctx || h.pos[p] < 0;
-      if (bad && w.id[p] >= 0 && w.id[p] < d.a->F) set_error(d.a->status, DKV_E_INTERNAL);
-      sm.pos[slot][row] = bad ? -1 : h.pos[p];
+      sm.s[q][row] = s * f;
+      sm.z[q][row] = fmaf(kMid, s, z) * f;
+      const bool in = ok && at >= 0 && at < ctx;
+      if (ok && !in) set_error(d.a->status, DKV_E_INTERNAL);
+      sm.pos[q][row] = in ? at : -1;
     }
   }
 }
@@ -111,7 +156,7 @@ struct Block {
 
 template <int SC>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_extend_sig(const __grid_constant__ ExtendArgs a, int32_t splits, int32_t nb) {
+    k_extend_sig(const __grid_constant__ ExtendArgs a, int32_t splits, int32_t lg) {
   constexpr int KH = scheme_kh(SC);
   extern __shared__ __align__(16) unsigned char smem_raw[];
   Smem &sm = *reinterpret_cast<Smem *>(smem_raw + (-saddr(smem_raw) & 1023u));
@@ -126,27 +171,37 @@ __global__ void __launch_bounds__(kThreads, 1)
   const Unit x = load_unit(a, (static_cast<int64_t>(a.layer0 + li) * a.R + r) * a.Hkv + h);
   const int32_t fresh = a.k_new ? acc_n : 0;
   const Tiles ts{(x.n_hi + 127) / 128, (x.n_lo + 127) / 128, (fresh + 127) / 128};
-  const int32_t nt = ts.count(), per = (nt + splits - 1) / splits;
+  // whole groups, as even as they go: a group's Q is staged whether it has one tile or four
+  const int32_t nt = ts.count(), per = ((nt + kGroup - 1) / kGroup + splits - 1) / splits * kGroup;
   const int32_t j0 = min(nt, sp * per), n = min(nt, j0 + per) - j0;
   if (n == 0) return;
   const int64_t tok0 = static_cast<int64_t>(li) * a.T + before;
   volatile int32_t *abort = &sm.abort;
-  // blocks of Q: hpb heads each, or (nb = 128) 128 tokens of one head
-  const int32_t hpb = min(a.G, 128 / nb), ib = nb == 128 ? (acc_n + 127) / 128 : 1;
-  const int32_t nblk = (a.G + hpb - 1) / hpb * ib, cols = hpb * nb, groups = (n + kGroup - 1) / kGroup;
+  // blocks of Q, 2^lg columns per head: hpb heads each, or (lg = 7) 128 tokens of one head
+  const int32_t nb = 1 << lg;
+  const int32_t hpb = min(a.G, min(128 >> lg, kHeads)), ib = lg == 7 ? (acc_n + 127) / 128 : 1;
+  const int32_t nblk = (a.G + hpb - 1) / hpb * ib, cols = (hpb * nb + 31) & ~31, groups = (n + kGroup - 1) / kGroup;
   auto block_at = [&](int32_t b) { return Block{b / ib * hpb, b % ib * 128}; };
+  // raw tiles: behind the blocks of Q, of which one is enough where it stays
+  static_assert(kRaw * Raw<KH>::kSlot <= kTileBytes + kExtra && Raw<KH>::kSlot <= kExtra);
+  const int32_t nraw = nblk == 1 ? kRaw : 1;
+  uint8_t *const raw = nblk == 1 ? sm.q[1] : sm.extra;
 
   if (tid == 0) {
     for (int i = 0; i < kGroup; ++i) {
       mbar_init(&sm.kfull[i], kConvWarps);
-      mbar_init(&sm.kempty[i], 1);
+      mbar_init(&sm.kempty[i], kSumWarps / 2);
       mbar_init(&sm.sfull[i], 1);
       mbar_init(&sm.sfree[i], kSumWarps / 2);
       mbar_init(&sm.cfull[i], kConvWarps);
+      mbar_init(&sm.cempty[i], kSumWarps);
       mbar_init(&sm.qm[i], kConvWarps);
       sm.qmax[i] = 0;
     }
-    for (int i = 0; i < 2 * kGroup; ++i) mbar_init(&sm.mfull[i], kConvWarps);
+    for (int i = 0; i < kRaw; ++i) {
+      mbar_init(&sm.rfull[i], 33);  // the copy warp's lanes and its first one's byte count
+      mbar_init(&sm.rempty[i], kConvWarps);
+    }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.qfull[i], kConvWarps);
       mbar_init(&sm.qempty[i], 1);
@@ -168,140 +223,133 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ================= sum warps: a thread per token
     const int wg = warp >> 2, row = tid & 127;
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-    const bool joint = a.G <= kMaxAcc;  // the heads' sums wait for one update of the token's row
-    float s[2], z[2], run[2] = {0.0f, 0.0f};
-    int32_t pos[2], tj[2];  // position; index among the new tokens (held: -1)
+    const bool wide = (a.G & 3) == 0 && (reinterpret_cast<uintptr_t>(a.sig_sum) & 15) == 0;
+    uint64_t carry[2] = {0, 0};  // sums of a head that goes on in the next block, over even and odd columns
     bool ok = true;
+#pragma unroll 1
     for (int32_t g = 0; g < groups && ok; ++g) {
       const int32_t ng = min(kGroup, n - g * kGroup);
+#pragma unroll 1
       for (int32_t b = 0; b < nblk && ok; ++b) {
         const int32_t qi = nblk == 1 ? 0 : g * nblk + b;
         const Block bk = block_at(b);
         if ((nblk > 1 || g == 0) && !(ok = warp_wait(&sm.cfull[qi & 3], (qi >> 2) & 1u))) break;
         const float qf = sm.qf[qi & 3];
         const float4 *col = sm.col[qi & 3];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int t = wg + 2 * e;
-          if (t >= ng || !ok) continue;
-          if (b == 0) {
-            const int ms = (g & 1) * kGroup + t;
-            if (!(ok = warp_wait(&sm.mfull[ms], (g >> 1) & 1u))) continue;
-            s[e] = sm.s[ms][row];
-            z[e] = sm.z[ms][row];
-            pos[e] = sm.pos[ms][row];
-            const Tile tl = tile_at(ts, x, fresh, j0 + g * kGroup + t);
-            tj[e] = tl.kind == 2 ? tl.t0 + row : -1;
-          }
-          // the row that the sums are added to, early
-          const bool last = b == nblk - 1;
-          float *dst = a.sig_sum + ((static_cast<int64_t>(a.layer0 + li) * a.R + r) * a.cap + max(pos[e], 0)) * a.Hq +
-                       h * a.G;
-          float old[kMaxAcc];
-          if (last && joint) {
-#pragma unroll
-            for (int q = 0; q < kMaxAcc; ++q) old[q] = q < a.G && pos[e] >= 0 && tj[e] < 0 ? dst[q] : 0.0f;
-          }
-          if (!(ok = warp_wait(&sm.sfull[t], (g * nblk + b) & 1u))) continue;
-          fence_after();
-          const float se = s[e] * qf, ze = z[e] * qf;
-          const uint64_t s2 = f2_pack(se, se), z2 = f2_pack(ze, ze);
-          const bool diag = __any_sync(kFull, tj[e] >= 0 && bk.i0 < tj[e]);
 #pragma unroll 1
-          for (int32_t c = 0; c < cols; c += 16) {
-            uint32_t u[16];
-            tmem_ld16(tmem + lanes + 128 * t + c, u);
-            tmem_wait16(u);
-            uint64_t sum[2] = {0, 0};
-            // new token tj: rows before it do not attend to it
-            const int32_t skip = diag ? tj[e] - (bk.i0 + c % nb) : 0;
+        for (int t = wg; t < ng; t += 2) {
+          if (!(ok = warp_wait(&sm.kfull[t], g & 1u) && warp_wait(&sm.sfull[t], (g * nblk + b) & 1u))) break;
+          fence_after();
+          const float se = sm.s[t][row] * qf, ze = sm.z[t][row] * qf;
+          const int32_t pos = sm.pos[t][row];  // -1: no token
+          const Tile tl = tile_at(ts, x, fresh, j0 + g * kGroup + t);
+          const int32_t tj = tl.kind == 2 ? tl.t0 + row : -1;  // index among the new tokens (held: -1)
+          // this thread alone adds to the token's sums
+          float *dst = a.sig_sum + ((static_cast<int64_t>(a.layer0 + li) * a.R + r) * a.cap + pos) * a.Hq + h * a.G;
+          const uint64_t s2 = f2_pack(se, se), z2 = f2_pack(ze, ze);
+          const bool diag = __any_sync(kFull, bk.i0 < tj);
+          uint64_t run = t == wg ? carry[0] : carry[1];
+#pragma unroll 1
+          for (int32_t c = 0; c < cols; c += 32) {
+            uint32_t u[32];
+            tmem_ld32(tmem + lanes + 128 * t + c, u);
+            tmem_wait32(u);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < 16; ++i) {
               const float4 cv = col[(c >> 1) + i];
               float y0, y1;
               f2_unpack(f2_fma(s2, f2_pack(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1])),
                                f2_fma(z2, f2_pack(cv.x, cv.y), f2_pack(cv.z, cv.w))), y0, y1);
-              y0 = ex2(y0);
-              y1 = ex2(y1);
-              if (diag) {
-                y0 = 2 * i < skip ? 0.0f : y0;
-                y1 = 2 * i + 1 < skip ? 0.0f : y1;
-              }
-              sum[i & 1] = f2_add(sum[i & 1], f2_pack(y0, y1));
+              u[2 * i] = __float_as_uint(y0);
+              u[2 * i + 1] = __float_as_uint(y1);
             }
-            float a0, a1;
-            f2_unpack(f2_add(sum[0], sum[1]), a0, a1);
-            run[e] += a0 + a1;
-            if ((c + 16) % nb == 0 && (nb < 128 || b % ib == ib - 1)) {  // the head is done
-              const int32_t hd = bk.head0 + c / nb;
-              if (joint) {
-                if (hd < a.G) sm.acc[t][hd][row] = run[e];
-              } else if (hd < a.G && pos[e] >= 0) {
-                dst[hd] = tj[e] < 0 ? dst[hd] + run[e] : run[e];
-              }
-              run[e] = 0.0f;
-            }
-          }
-          fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sm.sfree[t]);
-          if (last && joint && pos[e] >= 0) {
-            float v[kMaxAcc];
+            if (diag) {  // rows before new token tj do not attend to it
+              const int32_t skip = tj - bk.i0 - (c & (nb - 1));
 #pragma unroll
-            for (int q = 0; q < kMaxAcc; ++q) v[q] = q < a.G ? old[q] + sm.acc[t][q][row] : 0.0f;
-            if ((a.G & 3) == 0) {  // 16-byte aligned: Hq is a multiple of 4 as well
-              *reinterpret_cast<float4 *>(dst) = make_float4(v[0], v[1], v[2], v[3]);
-              if (a.G == 8) *reinterpret_cast<float4 *>(dst + 4) = make_float4(v[4], v[5], v[6], v[7]);
+              for (int i = 0; i < 32; ++i) u[i] = (i & (nb - 1)) < skip ? 0xff800000u : u[i];
+            }
+            uint64_t q8[4];  // eight columns each
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const uint64_t w = f2_pack(ex2(__uint_as_float(u[2 * i])), ex2(__uint_as_float(u[2 * i + 1])));
+              q8[i >> 2] = i & 3 ? f2_add(q8[i >> 2], w) : w;
+            }
+            // heads that end here: four, two, or the one of the last columns
+            int32_t heads = 4;
+            float v[4];
+            if (lg >= 4) {
+              q8[0] = f2_add(q8[0], q8[1]);
+              q8[1] = f2_add(q8[2], q8[3]);
+              heads = 2;
+              if (lg > 4) {
+                run = f2_add(run, f2_add(q8[0], q8[1]));
+                q8[0] = run;
+                heads = ((c + 32) & (nb - 1)) == 0 && (ib == 1 || b % ib == ib - 1);
+                if (heads) run = 0;
+              }
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[q] = f2_sum(q8[q]);
+            const int32_t head = bk.head0 + (c >> lg);
+            heads = pos < 0 ? 0 : min(heads, a.G - head);
+            if (wide && heads == 4 && tj < 0) {
+              red_add4(dst + head, v[0], v[1], v[2], v[3]);
             } else {
 #pragma unroll
-              for (int q = 0; q < kMaxAcc; ++q)
-                if (q < a.G) dst[q] = v[q];
+              for (int q = 0; q < 4; ++q) {
+                if (q < heads && tj < 0) red_add(dst + head + q, v[q]);
+                if (q < heads && tj >= 0) dst[head + q] = v[q];
+              }
             }
           }
+          if (t == wg) carry[0] = run;
+          else carry[1] = run;
+          fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&sm.sfree[t]);
+            if (b == nblk - 1) mbar_arrive(&sm.kempty[t]);
+          }
         }
+        __syncwarp();
+        if (lane == 0 && nblk > 1) mbar_arrive(&sm.cempty[qi & 3]);
       }
     }
   } else if (warp < kMmaWarp) {
     // ================= convert warps
     const int dt = tid - 32 * kSumWarps;
-    const PageGeom pg = page_geom(SC, a.P);
-    DeqCtx d{&a, x, 0xffffffffu / a.P + 1, 0xffffffffu / (2 * a.P) + 1, static_cast<int32_t>(pg.bytes),
-             static_cast<uint32_t>(pg.vbase), static_cast<uint32_t>(pg.meta), dt >> 2, dt & 3, (dt & 3) >> 1, {}};
+    DeqCtx d{&a, x, 0, 0, 0, 0, 0, dt >> 2, dt & 3, ((dt & 3) >> 1) ^ (__popc(dt >> 2 & 7) & 1), {}};
 #pragma unroll
     for (int i = 0; i < 4; ++i) d.off[i] = group_at(d.tk, 4 * d.c + (i ^ (2 * d.hs)));
     const float f = a.scale * kLog2e;
-    const int32_t posoff = static_cast<int32_t>(pg.pos);
-    Key key;
-    Where<2> w0, w1;
     bool ok = true;
-    Tile t{}, tn{};
-    auto load = [&] {
-      if (t.kind == 0) fetch_key<KH>(d, w0, key, posoff);
-      else if (t.kind == 1) fetch_key<KH / 2>(d, w0, key, posoff);
-    };
     // block b of Q into buffer qi
     auto stage = [&](int32_t b, int32_t qi) -> bool {
       const Block bk = block_at(b);
-      if (qi >= 2 && !warp_wait(&sm.qempty[qi & 1], ((qi >> 1) - 1) & 1u)) return false;
       uint4 v[2][4];
       uint32_t mx = 0;
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
-        const int32_t cl = d.tk + 64 * p, hd = bk.head0 + cl / nb, i = bk.i0 + cl % nb;
-        const bool have = cl < cols && hd < a.G && i < acc_n;
+        const int32_t cl = d.tk + 64 * p, hd = bk.head0 + (cl >> lg), i = bk.i0 + (cl & (nb - 1));
+        const bool have = cl < hpb * nb && hd < a.G && i < acc_n;
         const uint4 *src = reinterpret_cast<const uint4 *>(a.q + ((tok0 + i) * a.Hq + h * a.G + hd) * 128) + 4 * d.c;
-        uint32_t rm = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[p][k] = have ? __ldg(src + (k ^ (2 * d.hs))) : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        uint32_t m2 = 0;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          v[p][k] = have ? __ldg(src + (k ^ (2 * d.hs))) : make_uint4(0, 0, 0, 0);
-          const uint32_t *w = reinterpret_cast<const uint32_t *>(&v[p][k]);
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            rm = max(rm, max((w[q] << 16) & 0x7fffffffu, w[q] & 0x7fff0000u));  // bits of |value|: they order like it
+          m2 = max_bf16x2(m2, v[p][k].x & 0x7fff7fffu);
+          m2 = max_bf16x2(m2, v[p][k].y & 0x7fff7fffu);
+          m2 = max_bf16x2(m2, v[p][k].z & 0x7fff7fffu);
+          m2 = max_bf16x2(m2, v[p][k].w & 0x7fff7fffu);
         }
+        uint32_t rm = max(m2 << 16, m2 & 0xffff0000u);  // bits of |value|: they order like it
         rm = max(rm, __shfl_xor_sync(kFull, rm, 1));
         rm = max(rm, __shfl_xor_sync(kFull, rm, 2));
-        if (rm < 0x7f800000u) mx = max(mx, rm);  // a row that is not finite spoils itself alone
+        if (rm < 0x7f800000u) mx = max(mx, rm);  // an infinity spoils its own row alone
       }
       mx = __reduce_max_sync(kFull, mx);
       if (lane == 0) {
@@ -311,24 +359,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!warp_wait(&sm.qm[qi & 3], (qi >> 2) & 1u)) return false;
       const int e = lift_exponent(*const_cast<volatile uint32_t *>(&sm.qmax[qi & 3]));
       const float sc = pow2f(e);
+      const uint64_t sc2 = f2_pack(sc, sc);
+      if (qi >= 2 && !warp_wait(&sm.qempty[qi & 1], ((qi >> 1) - 1) & 1u)) return false;
+      if (qi >= 4 && !warp_wait(&sm.cempty[qi & 3], ((qi >> 2) - 1) & 1u)) return false;
       if (dt == 0) {
         sm.qf[qi & 3] = pow2f(-e);
         sm.qmax[(qi + 2) & 3] = 0;  // last used two blocks ago
       }
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
-        const int32_t cl = d.tk + 64 * p, hd = bk.head0 + cl / nb, i = bk.i0 + cl % nb;
-        const bool have = cl < cols && hd < a.G && i < acc_n;
-        float sum = 0.0f;
+        const int32_t cl = d.tk + 64 * p, hd = bk.head0 + (cl >> lg), i = bk.i0 + (cl & (nb - 1));
+        const bool have = cl < hpb * nb && hd < a.G && i < acc_n;
+        uint64_t acc = 0;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const uint4 y = v[p][k];
-          const float c0 = bf16_lo(y.x) * sc, c1 = bf16_hi(y.x) * sc, c2 = bf16_lo(y.y) * sc, c3 = bf16_hi(y.y) * sc;
-          const float c4 = bf16_lo(y.z) * sc, c5 = bf16_hi(y.z) * sc, c6 = bf16_lo(y.w) * sc, c7 = bf16_hi(y.w) * sc;
-          sum += ((c0 + c1) + (c2 + c3)) + ((c4 + c5) + (c6 + c7));
+          const uint64_t c04 = f2_mul(sc2, f2_pack(bf16_lo(y.x), bf16_lo(y.z))), c15 = f2_mul(sc2, f2_pack(bf16_hi(y.x), bf16_hi(y.z)));
+          const uint64_t c26 = f2_mul(sc2, f2_pack(bf16_lo(y.y), bf16_lo(y.w))), c37 = f2_mul(sc2, f2_pack(bf16_hi(y.y), bf16_hi(y.w)));
+          acc = f2_add(acc, f2_add(f2_add(c04, c15), f2_add(c26, c37)));
           *reinterpret_cast<uint4 *>(sm.q[qi & 1] + d.off[k] + p * (64 * 128)) =
-              make_uint4(f16x2_rn(c0, c4), f16x2_rn(c1, c5), f16x2_rn(c2, c6), f16x2_rn(c3, c7));
+              make_uint4(f16x2_of(c04), f16x2_of(c15), f16x2_of(c26), f16x2_of(c37));
         }
+        float sum = f2_sum(acc);
         sum += __shfl_xor_sync(kFull, sum, 1);
         sum += __shfl_xor_sync(kFull, sum, 2);
         if (d.c == 0) {
@@ -346,33 +398,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       return true;
     };
-    t = tile_at(ts, x, fresh, j0);
-    locate(d, t, w0);
-    load();
-    if (n > 1) {
-      tn = tile_at(ts, x, fresh, j0 + 1);
-      locate(d, tn, w1);
-    }
+    int32_t st = 0;
+    uint32_t ph = 0;
 #pragma unroll 1
     for (int32_t g = 0; g < groups && ok; ++g) {
-      if (nblk > 1 || g == 0) ok = stage(0, g * nblk);
       const int32_t ng = min(kGroup, n - g * kGroup);
 #pragma unroll 1
-      for (int32_t q = 0; q < ng && ok; ++q) {
-        const int32_t j = g * kGroup + q;
-        const int ms = (g & 1) * kGroup + q;
+      for (int32_t b = 0; b < nblk && ok; ++b) {
+        if (nblk > 1 || g == 0) ok = stage(b, g * nblk + b);
+        if (b > 0) continue;
+#pragma unroll 1
+        for (int32_t q = 0; q < ng && ok; ++q) {
+        const Tile t = tile_at(ts, x, fresh, j0 + g * kGroup + q);
+        const uint8_t *src = raw + st * Raw<KH>::kSlot;
+        if (!(ok = warp_wait(&sm.rfull[st], ph))) break;
         if (g > 0 && !(ok = warp_wait(&sm.kempty[q], (g - 1) & 1u))) break;
         if (t.kind == 0) {
-          convert_key<KH>(d, w0, key, sm, sm.k[q], ms, f, ctx);
+          convert_key<KH, KH>(d, src, sm.there[st], sm, q, f, ctx);
         } else if (t.kind == 1) {
-          convert_key<KH / 2>(d, w0, key, sm, sm.k[q], ms, f, ctx);
+          convert_key<KH / 2, KH>(d, src, sm.there[st], sm, q, f, ctx);
         } else {
-          new_k<2, false>(d, t, tok0, h, sm, sm.k[q], ms, f);
+          new_k<2, false>(d, t, tok0, h, sm, sm.k[q], q, f);
           if (d.c == 0) {
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
               const int row = d.tk + 64 * p;
-              sm.pos[ms][row] = row < t.n ? ctx + t.t0 + row : -1;
+              sm.pos[q][row] = row < t.n ? ctx + t.t0 + row : -1;
             }
           }
         }
@@ -380,21 +431,49 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(&sm.kfull[q]);
-          mbar_arrive(&sm.mfull[ms]);
+          mbar_arrive(&sm.rempty[st]);
         }
-        if (j + 1 < n) {
-          t = tn;
-          w0 = w1;
-          load();
-        }
-        if (j + 2 < n) {
-          tn = tile_at(ts, x, fresh, j0 + j + 2);
-          locate(d, tn, w1);
-        }
+        if (++st == nraw) st = 0, ph ^= 1u;
       }
-#pragma unroll 1
-      for (int32_t b = 1; b < nblk && ok; ++b) ok = stage(b, g * nblk + b);
+      }
     }
+  } else if (warp >= kCopyWarp) {
+    // ================= copy warps: a raw tile each (the first one alone where there is one raw tile)
+    const PageGeom pg = page_geom(SC, a.P);
+    const int st = warp - kCopyWarp;
+    uint8_t *const slot = raw + st * Raw<KH>::kSlot;
+    bool ok = st < nraw;
+    Tile t{};
+    PageRange g{};
+    auto ahead = [&](int32_t j) {  // tile j, and the lane's page of it
+      t = tile_at(ts, x, fresh, j0 + j);
+      if (t.kind == 2) return;
+      const bool high = t.kind == 0;
+      int32_t last, rem;
+      g.per = high ? a.P : 2 * a.P;
+      g.M = 0xffffffffu / g.per + 1;
+      split(t.t0, g.per, g.M, g.k0, rem);
+      split(t.t0 + t.n - 1, g.per, g.M, last, rem);
+      g.n = last - g.k0 + 1;
+      g.fwd = a.fwd + x.u * a.pmax + (high ? 0 : x.p_hi) + g.k0;
+      g.id = lane < g.n ? __ldg(g.fwd + lane) : -1;
+    };
+    if (ok && st < n) ahead(st);
+    int32_t uses = 0;
+#pragma unroll 1
+    for (int32_t j = st; j < n && ok; j += nraw) {
+      if (uses > 0 && !(ok = warp_wait(&sm.rempty[st], (uses - 1) & 1u))) break;
+      if (t.kind != 2) {
+        copy_keys<KH>(a, t, g, pg, slot, sm.there[st], &sm.rfull[st]);
+      } else {  // new tokens are read where they are converted
+        mbar_arrive(&sm.rfull[st]);
+        if (lane == 0) mbar_arrive(&sm.rfull[st]);
+      }
+      ++uses;
+      if (j + nraw < n) ahead(j + nraw);
+    }
+    // every copy has landed before the block leaves (bounded)
+    if (uses > 0) mbar_wait(&sm.rfull[st], (uses - 1) & 1u, nullptr);
   } else if (lane == 0) {
     // ================= MMA warp, one lane
     const uint32_t id = idesc(false, 128, cols, false);
@@ -417,7 +496,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             mma_ss(tmem + 128 * t, dk + t * kStep + o, dq + (qi & 1) * kStep + o, id, kk > 0 ? 1u : 0u);
           }
           mma_commit(&sm.sfull[t]);
-          if (b == nblk - 1) mma_commit(&sm.kempty[t]);
         }
         if (ok && nblk > 1) mma_commit(&sm.qempty[qi & 1]);
       }
@@ -436,10 +514,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int SC>
-cudaError_t launch(const ExtendArgs &a, int64_t blocks, int32_t splits, int32_t nb, cudaStream_t s) {
+cudaError_t launch(const ExtendArgs &a, int64_t blocks, int32_t splits, int32_t lg, cudaStream_t s) {
   const int smem = static_cast<int>(kSmemBytes);
   if (cudaError_t e = cudaFuncSetAttribute(k_extend_sig<SC>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) return e;
-  k_extend_sig<SC><<<static_cast<unsigned>(blocks), kThreads, smem, s>>>(a, splits, nb);
+  k_extend_sig<SC><<<static_cast<unsigned>(blocks), kThreads, smem, s>>>(a, splits, lg);
   return cudaGetLastError();
 }
 
@@ -447,17 +525,16 @@ cudaError_t launch(const ExtendArgs &a, int64_t blocks, int32_t splits, int32_t 
 
 cudaError_t launch_extend_sig(const ExtendArgs &a, cudaStream_t s) {
   const int64_t units = static_cast<int64_t>(a.n_layers) * a.R * a.Hkv;
-  const int32_t nb = a.max_new <= 16 ? 16 : a.max_new <= 32 ? 32 : a.max_new <= 64 ? 64 : 128;
+  const int32_t lg = a.max_new <= 8 ? 3 : a.max_new <= 16 ? 4 : a.max_new <= 32 ? 5 : a.max_new <= 64 ? 6 : 7;
   // runs of a unit's tiles, until every SM has a few blocks of at least one group
   const int64_t tiles = (static_cast<int64_t>(a.cap) + 127) / 128 + 2;
-  int64_t splits = 1;
-  while (units * splits < 4 * 152 && splits * 2 * kGroup <= tiles) splits *= 2;
+  const int64_t splits = std::clamp<int64_t>((4 * 152 + units - 1) / std::max<int64_t>(units, 1), 1, (tiles + kGroup - 1) / kGroup);
   const int64_t blocks = units * splits;
   if (blocks == 0 || a.max_new == 0) return cudaSuccess;
   if (blocks > INT32_MAX) return cudaErrorInvalidValue;
   const int32_t sp = static_cast<int32_t>(splits);
-  return a.scheme == 0 ? launch<0>(a, blocks, sp, nb, s) : a.scheme == 1 ? launch<1>(a, blocks, sp, nb, s)
-                                                                       : launch<2>(a, blocks, sp, nb, s);
+  return a.scheme == 0 ? launch<0>(a, blocks, sp, lg, s) : a.scheme == 1 ? launch<1>(a, blocks, sp, lg, s)
+                                                                       : launch<2>(a, blocks, sp, lg, s);
 }
 
 }  // namespace dkv

@@ -119,6 +119,22 @@ __device__ __forceinline__ void fetch(const DeqCtx &d, const Where<NP> &w, Held<
   }
 }
 
+// Sixteen W-bit codes of a row in shared memory.
+template <int W>
+__device__ __forceinline__ void read16(uint32_t (&x)[4], const uint8_t *src) {
+  if constexpr (W == 8) {
+    const uint4 v = *reinterpret_cast<const uint4 *>(src);
+    x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+  } else if constexpr (W == 4) {
+    const uint2 v = *reinterpret_cast<const uint2 *>(src);
+    x[0] = v.x, x[1] = v.y;
+  } else if constexpr (W == 2) {
+    x[0] = *reinterpret_cast<const uint32_t *>(src);
+  } else {
+    x[0] = *reinterpret_cast<const uint16_t *>(src);
+  }
+}
+
 __device__ __forceinline__ void put(uint8_t *tile, uint32_t at, const __half2 (&o)[4]) {
   *reinterpret_cast<uint4 *>(tile + at) = make_uint4(h2u(o[0]), h2u(o[1]), h2u(o[2]), h2u(o[3]));
 }

@@ -32,9 +32,17 @@ namespace {
 
 using namespace tc;
 
-constexpr int kSumWarps = 8, kConvWarps = 8;
-constexpr int kMmaWarp = kSumWarps + kConvWarps, kCopyWarp = kMmaWarp + 1, kCopyWarps = 3;
-constexpr int kThreads = 32 * (kCopyWarp + kCopyWarps);
+// Two warpgroups sum where one block of Q holds every head (then the conversion
+// of K bounds the kernel, and its threads want 96 registers), four where
+// several blocks stream past a group (then the sums do, and they want more
+// warps): 199 and 703 us with two, 235 and 549 us with four, for 64 requests
+// with drafts and for a chunk of 4 x 1024 tokens.
+template <bool kMany>
+struct Roles {
+  static constexpr int kWg = kMany ? 4 : 2, kConv = 4 * kWg, kMma = kConv + 8, kCopy = kMma + 1;
+  static constexpr int kThreads = 32 * (kCopy + 3);
+};
+constexpr int kConvWarps = 8, kCopyWarps = 3;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kGroup = 4;    // token tiles resident at once
 constexpr int kHeads = 8;    // most heads of a block of Q
@@ -154,10 +162,11 @@ struct Block {
   int32_t head0, i0;
 };
 
-template <int SC>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int SC, bool kMany>
+__global__ void __launch_bounds__(Roles<kMany>::kThreads, 1)
     k_extend_sig(const __grid_constant__ ExtendArgs a, int32_t splits, int32_t lg) {
-  constexpr int KH = scheme_kh(SC);
+  constexpr int KH = scheme_kh(SC), kWg = Roles<kMany>::kWg;
+  constexpr int kConvWarp = Roles<kMany>::kConv, kMmaWarp = Roles<kMany>::kMma, kCopyWarp = Roles<kMany>::kCopy;
   extern __shared__ __align__(16) unsigned char smem_raw[];
   Smem &sm = *reinterpret_cast<Smem *>(smem_raw + (-saddr(smem_raw) & 1023u));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -184,17 +193,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto block_at = [&](int32_t b) { return Block{b / ib * hpb, b % ib * 128}; };
   // raw tiles: behind the blocks of Q, of which one is enough where it stays
   static_assert(kRaw * Raw<KH>::kSlot <= kTileBytes + kExtra && Raw<KH>::kSlot <= kExtra);
-  const int32_t nraw = nblk == 1 ? kRaw : 1;
-  uint8_t *const raw = nblk == 1 ? sm.q[1] : sm.extra;
+  const int32_t nraw = kMany ? 1 : kRaw;
+  uint8_t *const raw = kMany ? sm.extra : sm.q[1];
 
   if (tid == 0) {
     for (int i = 0; i < kGroup; ++i) {
       mbar_init(&sm.kfull[i], kConvWarps);
-      mbar_init(&sm.kempty[i], kSumWarps / 2);
+      mbar_init(&sm.kempty[i], 4);
       mbar_init(&sm.sfull[i], 1);
-      mbar_init(&sm.sfree[i], kSumWarps / 2);
+      mbar_init(&sm.sfree[i], 4);
       mbar_init(&sm.cfull[i], kConvWarps);
-      mbar_init(&sm.cempty[i], kSumWarps);
+      mbar_init(&sm.cempty[i], 4 * kWg);
       mbar_init(&sm.qm[i], kConvWarps);
       sm.qmax[i] = 0;
     }
@@ -219,43 +228,42 @@ __global__ void __launch_bounds__(kThreads, 1)
   // the same answer in every lane: the loops below hold warp-wide instructions
   auto warp_wait = [&](uint64_t *bar, uint32_t parity) { return __all_sync(kFull, wait(bar, parity)) != 0; };
 
-  if (warp < kSumWarps) {
+  if (warp < kConvWarp) {
     // ================= sum warps: a thread per token
     const int wg = warp >> 2, row = tid & 127;
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const bool wide = (a.G & 3) == 0 && (reinterpret_cast<uintptr_t>(a.sig_sum) & 15) == 0;
-    uint64_t carry[2] = {0, 0};  // sums of a head that goes on in the next block, over even and odd columns
+    uint64_t run = 0;  // a head's sums so far, over even and odd columns (one tile a warp where it passes a block's end)
     bool ok = true;
 #pragma unroll 1
     for (int32_t g = 0; g < groups && ok; ++g) {
       const int32_t ng = min(kGroup, n - g * kGroup);
 #pragma unroll 1
       for (int32_t b = 0; b < nblk && ok; ++b) {
-        const int32_t qi = nblk == 1 ? 0 : g * nblk + b;
+        const int32_t qi = kMany ? g * nblk + b : 0;
         const Block bk = block_at(b);
-        if ((nblk > 1 || g == 0) && !(ok = warp_wait(&sm.cfull[qi & 3], (qi >> 2) & 1u))) break;
+        if ((kMany || g == 0) && !(ok = warp_wait(&sm.cfull[qi & 3], (qi >> 2) & 1u))) break;
         const float qf = sm.qf[qi & 3];
         const float4 *col = sm.col[qi & 3];
 #pragma unroll 1
-        for (int t = wg; t < ng; t += 2) {
+        for (int32_t t = wg; t < ng; t += kWg) {
           if (!(ok = warp_wait(&sm.kfull[t], g & 1u) && warp_wait(&sm.sfull[t], (g * nblk + b) & 1u))) break;
           fence_after();
           const float se = sm.s[t][row] * qf, ze = sm.z[t][row] * qf;
           const int32_t pos = sm.pos[t][row];  // -1: no token
+          const uint64_t s2 = f2_pack(se, se), z2 = f2_pack(ze, ze);
           const Tile tl = tile_at(ts, x, fresh, j0 + g * kGroup + t);
           const int32_t tj = tl.kind == 2 ? tl.t0 + row : -1;  // index among the new tokens (held: -1)
-          // this thread alone adds to the token's sums
-          float *dst = a.sig_sum + ((static_cast<int64_t>(a.layer0 + li) * a.R + r) * a.cap + pos) * a.Hq + h * a.G;
-          const uint64_t s2 = f2_pack(se, se), z2 = f2_pack(ze, ze);
-          const bool diag = __any_sync(kFull, bk.i0 < tj);
-          uint64_t run = t == wg ? carry[0] : carry[1];
+          const bool diag = __any_sync(kFull, bk.i0 < tj), ends = ib == 1 || b % ib == ib - 1;
+          int32_t cnt = 0;  // heads that are done, v: the last four
+          float v[4];
 #pragma unroll 1
-          for (int32_t c = 0; c < cols; c += 32) {
-            uint32_t u[32];
-            tmem_ld32(tmem + lanes + 128 * t + c, u);
-            tmem_wait32(u);
+          for (int32_t c = 0; c < cols; c += 16) {
+            uint32_t u[16];
+            tmem_ld16(tmem + lanes + 128 * t + c, u);
+            tmem_wait16(u);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
+            for (int i = 0; i < 8; ++i) {
               const float4 cv = col[(c >> 1) + i];
               float y0, y1;
               f2_unpack(f2_fma(s2, f2_pack(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1])),
@@ -266,44 +274,46 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (diag) {  // rows before new token tj do not attend to it
               const int32_t skip = tj - bk.i0 - (c & (nb - 1));
 #pragma unroll
-              for (int i = 0; i < 32; ++i) u[i] = (i & (nb - 1)) < skip ? 0xff800000u : u[i];
+              for (int i = 0; i < 16; ++i) u[i] = (i & (nb - 1)) < skip ? 0xff800000u : u[i];
             }
-            uint64_t q8[4];  // eight columns each
+            uint64_t q8[2];  // eight columns each
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
+            for (int i = 0; i < 8; ++i) {
               const uint64_t w = f2_pack(ex2(__uint_as_float(u[2 * i])), ex2(__uint_as_float(u[2 * i + 1])));
               q8[i >> 2] = i & 3 ? f2_add(q8[i >> 2], w) : w;
             }
-            // heads that end here: four, two, or the one of the last columns
-            int32_t heads = 4;
-            float v[4];
-            if (lg >= 4) {
-              q8[0] = f2_add(q8[0], q8[1]);
-              q8[1] = f2_add(q8[2], q8[3]);
-              heads = 2;
-              if (lg > 4) {
-                run = f2_add(run, f2_add(q8[0], q8[1]));
-                q8[0] = run;
-                heads = ((c + 32) & (nb - 1)) == 0 && (ib == 1 || b % ib == ib - 1);
-                if (heads) run = 0;
-              }
+            if (lg == 3) {
+              v[0] = v[2];
+              v[1] = v[3];
+              v[2] = f2_sum(q8[0]);
+              v[3] = f2_sum(q8[1]);
+              cnt += 2;
+            } else {
+              run = f2_add(run, f2_add(q8[0], q8[1]));
+              if (((c + 16) & (nb - 1)) != 0 || !ends) continue;
+              v[0] = v[1];
+              v[1] = v[2];
+              v[2] = v[3];
+              v[3] = f2_sum(run);
+              run = 0;
+              ++cnt;
             }
-#pragma unroll
-            for (int q = 0; q < 4; ++q) v[q] = f2_sum(q8[q]);
-            const int32_t head = bk.head0 + (c >> lg);
-            heads = pos < 0 ? 0 : min(heads, a.G - head);
-            if (wide && heads == 4 && tj < 0) {
-              red_add4(dst + head, v[0], v[1], v[2], v[3]);
+            if (((cnt & 3) != 0 && c + 16 < cols) || pos < 0) continue;
+            // heads [base, cnt) of the block to their places; this thread alone adds to the token's sums
+            const int32_t base = (cnt - 1) & ~3, most = min(cnt, min(hpb, a.G - bk.head0));
+            float *dst = a.sig_sum + ((static_cast<int64_t>(a.layer0 + li) * a.R + r) * a.cap + pos) * a.Hq + h * a.G +
+                         bk.head0 + cnt - 4;
+            if (wide && most - base == 4 && tj < 0) {
+              red_add4(dst, v[0], v[1], v[2], v[3]);
             } else {
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
-                if (q < heads && tj < 0) red_add(dst + head + q, v[q]);
-                if (q < heads && tj >= 0) dst[head + q] = v[q];
+                if (cnt - 4 + q < base || cnt - 4 + q >= most) continue;
+                if (tj < 0) red_add(dst + q, v[q]);
+                else dst[q] = v[q];
               }
             }
           }
-          if (t == wg) carry[0] = run;
-          else carry[1] = run;
           fence_before();
           __syncwarp();
           if (lane == 0) {
@@ -312,12 +322,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         __syncwarp();
-        if (lane == 0 && nblk > 1) mbar_arrive(&sm.cempty[qi & 3]);
+        if (lane == 0 && kMany) mbar_arrive(&sm.cempty[qi & 3]);
       }
     }
   } else if (warp < kMmaWarp) {
     // ================= convert warps
-    const int dt = tid - 32 * kSumWarps;
+    const int dt = tid - 32 * kConvWarp;
     DeqCtx d{&a, x, 0, 0, 0, 0, 0, dt >> 2, dt & 3, ((dt & 3) >> 1) ^ (__popc(dt >> 2 & 7) & 1), {}};
 #pragma unroll
     for (int i = 0; i < 4; ++i) d.off[i] = group_at(d.tk, 4 * d.c + (i ^ (2 * d.hs)));
@@ -405,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int32_t ng = min(kGroup, n - g * kGroup);
 #pragma unroll 1
       for (int32_t b = 0; b < nblk && ok; ++b) {
-        if (nblk > 1 || g == 0) ok = stage(b, g * nblk + b);
+        if (kMany || g == 0) ok = stage(b, g * nblk + b);
         if (b > 0) continue;
 #pragma unroll 1
         for (int32_t q = 0; q < ng && ok; ++q) {
@@ -483,8 +493,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int32_t g = 0; g < groups && ok; ++g) {
       const int32_t ng = min(kGroup, n - g * kGroup);
       for (int32_t b = 0; b < nblk && ok; ++b) {
-        const int32_t qi = nblk == 1 ? 0 : g * nblk + b;
-        if ((nblk > 1 || g == 0) && !(ok = wait(&sm.qfull[qi & 1], (qi >> 1) & 1u))) break;
+        const int32_t qi = kMany ? g * nblk + b : 0;
+        if ((kMany || g == 0) && !(ok = wait(&sm.qfull[qi & 1], (qi >> 1) & 1u))) break;
         const int32_t use = g * nblk + b;  // of every tensor-memory buffer
         for (int32_t t = 0; t < ng; ++t) {
           if (b == 0 && !(ok = wait(&sm.kfull[t], g & 1u))) break;
@@ -497,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           mma_commit(&sm.sfull[t]);
         }
-        if (ok && nblk > 1) mma_commit(&sm.qempty[qi & 1]);
+        if (ok && kMany) mma_commit(&sm.qempty[qi & 1]);
       }
     }
     // every MMA of the block done (also after an abort)
@@ -513,11 +523,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int SC>
+template <int SC, bool kMany>
 cudaError_t launch(const ExtendArgs &a, int64_t blocks, int32_t splits, int32_t lg, cudaStream_t s) {
   const int smem = static_cast<int>(kSmemBytes);
-  if (cudaError_t e = cudaFuncSetAttribute(k_extend_sig<SC>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) return e;
-  k_extend_sig<SC><<<static_cast<unsigned>(blocks), kThreads, smem, s>>>(a, splits, lg);
+  if (cudaError_t e = cudaFuncSetAttribute(k_extend_sig<SC, kMany>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) return e;
+  k_extend_sig<SC, kMany><<<static_cast<unsigned>(blocks), Roles<kMany>::kThreads, smem, s>>>(a, splits, lg);
   return cudaGetLastError();
 }
 
@@ -533,8 +543,12 @@ cudaError_t launch_extend_sig(const ExtendArgs &a, cudaStream_t s) {
   if (blocks == 0 || a.max_new == 0) return cudaSuccess;
   if (blocks > INT32_MAX) return cudaErrorInvalidValue;
   const int32_t sp = static_cast<int32_t>(splits);
-  return a.scheme == 0 ? launch<0>(a, blocks, sp, lg, s) : a.scheme == 1 ? launch<1>(a, blocks, sp, lg, s)
-                                                                       : launch<2>(a, blocks, sp, lg, s);
+  const bool many = lg == 7 || a.G > std::min(128 >> lg, kHeads);  // more than one block of Q (max_new bounds every request)
+  if (many)
+    return a.scheme == 0 ? launch<0, true>(a, blocks, sp, lg, s) : a.scheme == 1 ? launch<1, true>(a, blocks, sp, lg, s)
+                                                                                : launch<2, true>(a, blocks, sp, lg, s);
+  return a.scheme == 0 ? launch<0, false>(a, blocks, sp, lg, s) : a.scheme == 1 ? launch<1, false>(a, blocks, sp, lg, s)
+                                                                               : launch<2, false>(a, blocks, sp, lg, s);
 }
 
 }  // namespace dkv

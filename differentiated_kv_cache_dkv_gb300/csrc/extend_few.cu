@@ -32,10 +32,10 @@ namespace {
 using namespace tc;
 
 constexpr int kSoftWarps = 8, kConvWarps = 8;
-constexpr int kMmaWarp = kSoftWarps + kConvWarps, kCopyWarp = kMmaWarp + 1;
-constexpr int kThreads = 32 * (kCopyWarp + 1);
+constexpr int kMmaWarp = kSoftWarps + kConvWarps, kCopyWarp = kMmaWarp + 1, kCopyWarps = 3;
+constexpr int kThreads = 32 * (kCopyWarp + kCopyWarps);
 constexpr int kNP = 2;               // tokens a convert thread holds
-constexpr int kRaw = 3;              // raw tiles in flight
+constexpr int kRaw = kCopyWarps;     // raw tiles in flight, one a copy warp
 constexpr uint32_t kTmemCols = 256;  // S^T at 0 and 64, O^T at 128
 constexpr uint32_t kColO = 128;
 constexpr int kMeta = 4;             // ring of the tiles' scales and zeros
@@ -124,70 +124,58 @@ __device__ __forceinline__ uint2 read_md(const RawForm &f, const uint8_t *raw, i
   return *reinterpret_cast<const uint2 *>(raw + (i >> f.lg) * f.stride + f.mo + 8 * (i & ((1 << f.lg) - 1)));
 }
 
-// A tile's pages [k0, k0 + n) of the forward row; a lane holds the ids of three
-// at most (pages of two tokens: 65 in a tile).
-struct Pages {
-  int32_t k0, n, id[3];
+// Pages [k0, k0 + n) of a unit's list that a tile lies in: fwd, their ids; id,
+// the lane's of the first 32.
+struct PageRange {
+  int32_t per, k0, n, id;
+  const int32_t *fwd;
 };
 
-__device__ __forceinline__ Pages pages_of(const ExtendArgs &a, const Unit &x, const Tile &t) {
-  Pages g{};
-  if (t.kind == 2) return g;
-  const int32_t per = t.kind == 0 ? a.P : 2 * a.P, lane = threadIdx.x & 31;
-  g.k0 = t.t0 / per;
-  g.n = (t.t0 + t.n - 1) / per - g.k0 + 1;
-  const int32_t *fwd = a.fwd + x.u * a.pmax + (t.kind == 0 ? 0 : x.p_hi) + g.k0;
-#pragma unroll
-  for (int i = 0; i < 3; ++i) g.id[i] = lane + 32 * i < g.n ? __ldg(fwd + lane + 32 * i) : -1;
-  return g;
-}
-
-// One warp: the pages of tile t into a raw tile.  P is even, so that a page's
-// first slot here and an even count keep the 8-byte scales on 16-byte
-// boundaries (an odd last token takes its neighbour's along, still inside the
-// page).
-template <int KW, int VW>
-__device__ __forceinline__ void copy_tile(const ExtendArgs &a, const Tile &t, const Pages &g, uint8_t *raw,
-                                          uint32_t *there, uint64_t *bar, uint32_t vbase, uint32_t meta, int64_t bytes) {
+// One warp: the pages of tile t into a raw tile (issuing a bulk copy takes a
+// warp about 54 cycles, whatever its size).  P is even, so that a page's first
+// slot here and an even count keep the 8-byte scales on 16-byte boundaries (an
+// odd last token takes its neighbour's along, still inside the page).
+template <int KH, int VH>
+__device__ __forceinline__ void copy_tile(const ExtendArgs &a, const Tile &t, const PageRange &g, const PageGeom &pg,
+                                          uint8_t *raw, uint32_t *there, uint64_t *bar) {
   const int lane = threadIdx.x & 31;
-  const bool high = t.kind == 0;
-  const int32_t per = high ? a.P : 2 * a.P;
-  const RawForm f = raw_form<KW, VW>(a.P, high);
-  uint32_t sum = 0;
+  const RawForm f = t.kind == 0 ? raw_form<KH, VH>(a.P, true) : raw_form<KH / 2, VH / 2>(a.P, false);
+  const int32_t kb = t.kind == 0 ? 16 * KH : 8 * KH, vb = t.kind == 0 ? 16 * VH : 8 * VH;
   if (lane < 4) there[lane] = 0;
   __syncwarp();
-  int32_t first[3], n[3], to[3];  // first slot, slots, first token of the tile
-#pragma unroll
-  for (int i = 0; i < 3; ++i) {
-    const int32_t k = lane + 32 * i, p0 = (g.k0 + k) * per;
-    n[i] = 0;
-    if (k >= g.n) continue;
-    if (g.id[i] < 0 || g.id[i] >= a.F) {
-      set_error(a.status, DKV_E_INTERNAL);
-      continue;
+  // bytes to come, then the copies
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+    uint32_t sum = 0;
+#pragma unroll 1
+    for (int32_t k = lane; k < g.n; k += 32) {
+      const int32_t id = k < 32 ? g.id : __ldg(g.fwd + k);
+      if (id < 0 || id >= a.F) {
+        set_error(a.status, DKV_E_INTERNAL);
+        continue;
+      }
+      const int32_t p0 = (g.k0 + k) * g.per, first = max(t.t0 - p0, 0);
+      const int32_t n = min(p0 + g.per, t.t0 + t.n) - p0 - first, to = p0 + first - t.t0, md = 8 * ((n + 1) & ~1);
+      if (pass == 0) {
+        sum += f.whole ? f.stride : n * (kb + vb) + md;
+        for (int32_t b = to; b < to + n; b += 32 - (b & 31))  // bits [to, to + n)
+          atomicOr(there + (b >> 5), (0xffffffffu >> (32 - min(32 - (b & 31), to + n - b))) << (b & 31));
+        continue;
+      }
+      const uint8_t *src = a.pages + id * pg.bytes;
+      if (f.whole) {
+        copy_bulk(raw + (to >> f.lg) * f.stride, src, f.stride, bar);
+      } else {
+        copy_bulk(raw + to * kb, src + first * kb, n * kb, bar);
+        copy_bulk(raw + f.vb + to * vb, src + pg.vbase + first * vb, n * vb, bar);
+        copy_bulk(raw + f.mo + to * 8, src + pg.meta + 8 * first, md, bar);
+      }
     }
-    first[i] = max(t.t0 - p0, 0);
-    n[i] = min(p0 + per, t.t0 + t.n) - p0 - first[i];
-    to[i] = p0 + first[i] - t.t0;
-    sum += f.whole ? f.stride : n[i] * (16 * KW + 16 * VW) + 8 * ((n[i] + 1) & ~1);
-    for (int32_t b = to[i]; b < to[i] + n[i]; b += 32 - (b & 31))  // bits [to, to + n)
-      atomicOr(there + (b >> 5), (0xffffffffu >> (32 - min(32 - (b & 31), to[i] + n[i] - b))) << (b & 31));
-  }
-  sum = __reduce_add_sync(kFull, sum);
-  __syncwarp();  // the bits above are part of what the arrival publishes
-  if (lane == 0) mbar_expect_tx(bar, sum);  // before any copy can land
-  __syncwarp();
-#pragma unroll
-  for (int i = 0; i < 3; ++i) {
-    if (n[i] == 0) continue;
-    const uint8_t *pg = a.pages + g.id[i] * bytes;
-    if (f.whole) {
-      copy_bulk(raw + (to[i] >> f.lg) * f.stride, pg, f.stride, bar);
-    } else {
-      copy_bulk(raw + to[i] * (16 * KW), pg + first[i] * (16 * KW), n[i] * (16 * KW), bar);
-      copy_bulk(raw + f.vb + to[i] * (16 * VW), pg + vbase + first[i] * (16 * VW), n[i] * (16 * VW), bar);
-      copy_bulk(raw + f.mo + to[i] * 8, pg + meta + 8 * first[i], 8 * ((n[i] + 1) & ~1), bar);
-    }
+    if (pass) break;
+    sum = __reduce_add_sync(kFull, sum);
+    __syncwarp();  // the bits above are part of what the arrival publishes
+    if (lane == 0) mbar_expect_tx(bar, sum);  // before any copy can land
+    __syncwarp();
   }
 }
 
@@ -470,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int dt = tid - 32 * kSoftWarps;
     const PageGeom pg = page_geom(SC, a.P);
     DeqCtx d{&a, x, 0xffffffffu / a.P + 1, 0xffffffffu / (2 * a.P) + 1, static_cast<int32_t>(pg.bytes),
-             static_cast<uint32_t>(pg.vbase), static_cast<uint32_t>(pg.meta), dt >> 2, dt & 3, (dt & 3) >> 1, {}};
+             static_cast<uint32_t>(pg.vbase), static_cast<uint32_t>(pg.meta), dt >> 2, dt & 3, ((dt & 3) >> 1) ^ (__popc(dt >> 2 & 7) & 1), {}};
 #pragma unroll
     for (int i = 0; i < 4; ++i) d.off[i] = group_at(d.tk, 4 * d.c + (i ^ (2 * d.hs)));
     const float f = a.scale * kLog2e * pow2f(-e);
@@ -516,31 +504,35 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(&sm.vfull[j & 1]);
     }
     (void)ok;
-  } else if (warp == kCopyWarp) {
-    // ================= copy warp
+  } else if (warp >= kCopyWarp) {
+    // ================= copy warps: a raw tile each
     const PageGeom pg = page_geom(SC, a.P);
+    const int st = warp - kCopyWarp;
     bool ok = true;
-    int32_t j = 0;
-    Pages next = pages_of(a, x, tile_at(ts, x, fresh, j0));
+    int32_t uses = 0;
+    Tile t{};
+    PageRange g{};
+    auto ahead = [&](int32_t j) {  // tile j, and the lane's page of it
+      t = tile_at(ts, x, fresh, j0 + j);
+      if (t.kind == 2) return;
+      const bool high = t.kind == 0;
+      g.per = high ? a.P : 2 * a.P;
+      g.k0 = t.t0 / g.per;
+      g.n = (t.t0 + t.n - 1) / g.per - g.k0 + 1;
+      g.fwd = a.fwd + x.u * a.pmax + (high ? 0 : x.p_hi) + g.k0;
+      g.id = lane < g.n ? __ldg(g.fwd + lane) : -1;
+    };
+    if (st < n) ahead(st);
 #pragma unroll 1
-    for (; j < n; ++j) {
-      const Tile t = tile_at(ts, x, fresh, j0 + j);
-      const Pages g = next;
-      if (j + 1 < n) next = pages_of(a, x, tile_at(ts, x, fresh, j0 + j + 1));
-      const int st = j % kRaw;
-      if (j >= kRaw && !(ok = warp_wait(&sm.rempty[st], (j / kRaw - 1) & 1u))) break;
-      if (t.kind == 0) {
-        copy_tile<KH, VH>(a, t, g, sm.raw[st], sm.there[st], &sm.rfull[st], static_cast<uint32_t>(pg.vbase),
-                          static_cast<uint32_t>(pg.meta), pg.bytes);
-      } else if (t.kind == 1) {
-        copy_tile<KH / 2, VH / 2>(a, t, g, sm.raw[st], sm.there[st], &sm.rfull[st], static_cast<uint32_t>(pg.vbase),
-                                  static_cast<uint32_t>(pg.meta), pg.bytes);
-      } else if (lane == 0) {
-        mbar_arrive(&sm.rfull[st]);  // new tokens are read where they are converted
-      }
+    for (int32_t j = st; j < n; j += kRaw) {
+      if (uses > 0 && !(ok = warp_wait(&sm.rempty[st], (uses - 1) & 1u))) break;
+      if (t.kind != 2) copy_tile<KH, VH>(a, t, g, pg, sm.raw[st], sm.there[st], &sm.rfull[st]);
+      else if (lane == 0) mbar_arrive(&sm.rfull[st]);  // new tokens are read where they are converted
+      ++uses;
+      if (j + kRaw < n) ahead(j + kRaw);
     }
     // every copy has landed before the block leaves (bounded)
-    for (int32_t c = max(0, j - kRaw); c < j; ++c) mbar_wait(&sm.rfull[c % kRaw], (c / kRaw) & 1u, nullptr);
+    if (uses > 0) mbar_wait(&sm.rfull[st], (uses - 1) & 1u, nullptr);
     (void)ok;
   } else if (lane == 0) {
     // ================= MMA warp, one lane

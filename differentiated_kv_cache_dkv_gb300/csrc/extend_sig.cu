@@ -170,9 +170,11 @@ __global__ void __launch_bounds__(Roles<kMany>::kThreads, 1)
   extern __shared__ __align__(16) unsigned char smem_raw[];
   Smem &sm = *reinterpret_cast<Smem *>(smem_raw + (-saddr(smem_raw) & 1023u));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint32_t ui = blockIdx.x / splits, rh = ui / a.Hkv;  // unit, (layer, request)
-  const int32_t sp = static_cast<int32_t>(blockIdx.x - ui * splits), h = static_cast<int32_t>(ui - rh * a.Hkv);
-  const int32_t li = static_cast<int32_t>(rh / a.R), r = static_cast<int32_t>(rh - li * a.R);
+  // blocks in the order (request, the longest first; layer, head; part)
+  const uint32_t ui = blockIdx.x / splits, lh = static_cast<uint32_t>(a.n_layers) * a.Hkv, k = ui / lh, rest = ui - k * lh;
+  const int32_t sp = static_cast<int32_t>(blockIdx.x - ui * splits);
+  const int32_t li = static_cast<int32_t>(rest / a.Hkv), h = static_cast<int32_t>(rest - li * a.Hkv);
+  const int32_t r = longest_first(a, static_cast<int32_t>(k));
   int64_t before;
   if (!lens_valid(a, r, before)) return;
   const int32_t acc_n = __ldg(a.acc_lens + r), ctx = __ldg(a.ctx_lens + r);

@@ -442,6 +442,31 @@ __device__ __forceinline__ bool lens_valid(const ExtendArgs &a, int32_t r, int64
   return ok_s != 0;
 }
 
+// The request with the k-th most tokens (ties: the first one), or k itself when
+// there are more requests than that is worth.  Every block asks, all its threads.
+constexpr int32_t kOrder = 512;
+__device__ __forceinline__ int32_t longest_first(const ExtendArgs &a, int32_t k) {
+  __shared__ __align__(16) int32_t len[kOrder];
+  __shared__ int32_t pick;
+  if (a.R > kOrder) return k;
+  const int32_t tid = threadIdx.x, n4 = (a.R + 3) / 4;
+  if (tid == 0) pick = k;
+  for (int32_t i = tid; i < 4 * n4; i += blockDim.x) len[i] = i < a.R ? __ldg(a.ctx_lens + i) : INT32_MIN;
+  __syncthreads();
+  for (int32_t i = tid; i < a.R; i += blockDim.x) {
+    const int32_t mine = len[i];
+    int32_t rank = 0;
+    for (int32_t j = 0; j < n4; ++j) {
+      const int4 x = *reinterpret_cast<const int4 *>(len + 4 * j);
+      rank += (x.x > mine || (x.x == mine && 4 * j < i)) + (x.y > mine || (x.y == mine && 4 * j + 1 < i)) +
+              (x.z > mine || (x.z == mine && 4 * j + 2 < i)) + (x.w > mine || (x.w == mine && 4 * j + 3 < i));
+    }
+    if (rank == k) pick = i;
+  }
+  __syncthreads();
+  return pick;
+}
+
 // The lists of a unit (empty when its header contradicts itself).
 struct Unit {
   int64_t u;  // index in the tables

@@ -592,6 +592,7 @@ int32_t dkv_fork(const dkv_fork_batch *b, const dkv_pool *pool, const dkv_tables
   dkv::PageOpArgs a = page_op_args(pool, t, U, b->unit_base, workspace);
   a.L = b->L; a.R = b->R; a.Hq = b->Hq; a.Hkv = b->Hkv; a.n = b->n; a.cap = b->cap;
   a.V = static_cast<int64_t>(b->L) * b->n * b->Hkv;
+  a.upb = dkv::plan_units(a.V);
   a.src = b->src; a.dst = b->dst; a.ctx_lens = b->ctx_lens;
   a.classes = b->classes; a.slot_of = b->slot_of; a.sig_sum = b->sig_sum; a.sig_cnt = b->sig_cnt;
   return cuda_status(dkv::launch_fork(a, sms, static_cast<cudaStream_t>(stream)));
@@ -607,6 +608,7 @@ int32_t dkv_release(const dkv_release_batch *b, const dkv_pool *pool, const dkv_
   dkv::PageOpArgs a = page_op_args(pool, t, U, b->unit_base, workspace);
   a.L = b->L; a.R = b->R; a.Hkv = b->Hkv; a.n = b->n;
   a.V = static_cast<int64_t>(b->L) * b->n * b->Hkv;
+  a.upb = dkv::plan_units(a.V);
   a.src = b->reqs;
   return cuda_status(dkv::launch_release(a, static_cast<cudaStream_t>(stream)));
 }

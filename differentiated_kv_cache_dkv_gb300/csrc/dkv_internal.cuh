@@ -20,6 +20,7 @@
 //   k_commit    forward / reverse tables, page classes, head cursor, status
 #pragma once
 
+#include <algorithm>
 #include <cstdint>
 
 #include "../../include/dkv.h"
@@ -372,8 +373,15 @@ struct PrefillArgs {
 };
 
 // Page operations (maintain.cu): fork, release, defrag.
-constexpr int kPlanUnits = 32;       // list units per block
-constexpr int kDefragPages = 2048;   // page ids per block
+// List units per block: a warp each, and more from 8192 units on, because every
+// block of the second kernel adds up all the blocks' sums.
+constexpr int kPlanUnits = 8, kMaxPlanUnits = 256;
+inline int32_t plan_units(int64_t V) {
+  int32_t n = kPlanUnits;
+  while (n < kMaxPlanUnits && V > int64_t{1024} * n) n *= 2;
+  return n;
+}
+constexpr int kDefragPages = 1024;   // page ids per block
 
 struct PageOpWsHeader {
   uint64_t head, tail;  // free-list cursors before the call
@@ -389,7 +397,10 @@ struct PageOpWsLayout {
 
 inline PageOpWsLayout page_op_ws_layout(int64_t U, int64_t F) {
   PageOpWsLayout w{};
-  const int64_t a = (U + kPlanUnits - 1) / kPlanUnits, b = (F + kDefragPages - 1) / kDefragPages;
+  // plan_units(V), V <= U, is never more blocks than this; a small call has 8
+  int64_t a = std::max<int64_t>(U / kMaxPlanUnits + 1, std::min<int64_t>(U / kPlanUnits + 1, 1024));
+  a = std::max<int64_t>(a, 8);
+  const int64_t b = (F + kDefragPages - 1) / kDefragPages;
   size_t o = align256(sizeof(PageOpWsHeader));
   w.part = o; o = align256(o + 16 * static_cast<size_t>(a > b ? a : b));
   w.list = o; o = align256(o + 8 * static_cast<size_t>(F));
@@ -398,7 +409,7 @@ inline PageOpWsLayout page_op_ws_layout(int64_t U, int64_t F) {
 }
 
 struct PageOpArgs {
-  int32_t L, R, Hq, Hkv, n, P, pmax, cap;
+  int32_t L, R, Hq, Hkv, n, P, pmax, cap, upb;
   int64_t F, U, V, unit_base, page_bytes;  // V = L n Hkv list units
   const int32_t *src, *dst, *ctx_lens;     // release: src names the requests, dst is null
   uint8_t *classes;

@@ -91,11 +91,13 @@ __device__ int32_t check_lists(const PageOpArgs &a, uint32_t *bits) {
 
 // ---------------------------------------------------------- fork, release --
 
-// One warp per list unit, kPlanUnits units a block: header, page ids and (for
-// a release) reverse entries agree, destinations (for a fork) are empty;
-// part[block] = {pages of the block's units, error}.
+// One warp per list unit, a.upb units a block: header, page ids and reverse
+// entries agree, destinations (for a fork) are empty; part[block] = {pages of
+// the block's units, error}.  The loads of a unit depend on each other (request,
+// header, ids, reverse entries), so a warp takes one unit where the blocks
+// allow it, and 128 pages of it at a time.
 template <bool kFork>
-__global__ void __launch_bounds__(kThreads) k_list_plan(PageOpArgs a) {
+__device__ __forceinline__ void list_plan(const PageOpArgs &a) {
   extern __shared__ uint32_t bits[];
   __shared__ int64_t sm[kWarps];
   __shared__ int32_t err_s;
@@ -104,18 +106,31 @@ __global__ void __launch_bounds__(kThreads) k_list_plan(PageOpArgs a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int64_t sum = 0;
   int32_t err = 0;
-  for (int i = warp; i < kPlanUnits; i += kWarps) {
-    const int64_t v = static_cast<int64_t>(blockIdx.x) * kPlanUnits + i;
+  for (int i = warp; i < a.upb; i += kWarps) {
+    const int64_t v = static_cast<int64_t>(blockIdx.x) * a.upb + i;
     if (v >= a.V) break;
     int32_t k, d = 0;
     const int64_t u = list_unit(a, v, a.src, k);
     if (u >= 0) {
       d = unit_pages(a, *reinterpret_cast<const int4 *>(a.unit_hdr + 4 * u));
       if (d < 0) err = DKV_E_INTERNAL;
-      for (int32_t j = lane; j < d; j += 32) {
-        const int32_t id = a.fwd[u * a.pmax + j];
-        if (id < 0 || id >= a.F) err = DKV_E_INTERNAL;
-        else if (a.rev_unit[id] != a.unit_base + u || a.rev_idx[id] != j) err = DKV_E_INTERNAL;
+      for (int32_t j0 = lane; j0 < d; j0 += 128) {
+        int32_t id[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int32_t j = j0 + 32 * e;
+          id[e] = j < d ? a.fwd[u * a.pmax + j] : 0;
+          if (id[e] < 0 || id[e] >= a.F) {
+            err = DKV_E_INTERNAL;
+            id[e] = 0;
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int32_t j = j0 + 32 * e;
+          const bool same = a.rev_unit[id[e]] == a.unit_base + u && a.rev_idx[id[e]] == j;
+          if (j < d && !same) err = DKV_E_INTERNAL;
+        }
       }
     } else {
       err = DKV_E_INTERNAL;
@@ -144,6 +159,9 @@ __global__ void __launch_bounds__(kThreads) k_list_plan(PageOpArgs a) {
   if (threadIdx.x == 0) a.part[blockIdx.x] = make_longlong2(sum, err_s);
 }
 
+// A place of the ring: x < 2 F.
+__device__ __forceinline__ int64_t ring(int64_t x, int64_t F) { return x < F ? x : x - F; }
+
 // Sum of the plan's partial sums before this block and of all, and the first
 // error in block order.  Every thread of the block calls it.
 __device__ __forceinline__ int32_t plan_totals(const longlong2 *part, int32_t nparts, int64_t *sm, int64_t &before,
@@ -171,9 +189,9 @@ __device__ __forceinline__ int32_t plan_totals(const longlong2 *part, int32_t np
 // blocks before.  Fork: new page ids into the destination's tables, (old,
 // new) into the copy list.  Release: ids into the ring, tables cleared.
 template <bool kFork>
-__global__ void __launch_bounds__(kThreads) k_list_place(PageOpArgs a, int32_t nparts) {
+__device__ __forceinline__ void list_place(const PageOpArgs &a, int32_t nparts) {
   __shared__ int64_t sm[kWarps];
-  __shared__ int32_t d_s[kPlanUnits];
+  __shared__ int32_t d_s[kMaxPlanUnits];
   int64_t before, total;
   int32_t err = plan_totals(a.part, nparts, sm, before, total);
   const uint64_t head = a.ws->head, tail = a.ws->tail;
@@ -187,8 +205,8 @@ __global__ void __launch_bounds__(kThreads) k_list_place(PageOpArgs a, int32_t n
   }
   if (err) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t v0 = static_cast<int64_t>(blockIdx.x) * kPlanUnits;
-  for (int i = threadIdx.x; i < kPlanUnits; i += kThreads) {
+  const int64_t v0 = static_cast<int64_t>(blockIdx.x) * a.upb;
+  for (int i = threadIdx.x; i < a.upb; i += kThreads) {
     int32_t k, d = 0;
     if (v0 + i < a.V) {
       const int64_t u = list_unit(a, v0 + i, a.src, k);
@@ -198,8 +216,8 @@ __global__ void __launch_bounds__(kThreads) k_list_place(PageOpArgs a, int32_t n
     d_s[i] = d;
   }
   __syncthreads();
-  const uint64_t at0 = ((kFork ? head : tail) + before) % static_cast<uint64_t>(a.F);
-  for (int i = warp; i < kPlanUnits; i += kWarps) {
+  const int64_t at0 = static_cast<int64_t>(((kFork ? head : tail) + before) % static_cast<uint64_t>(a.F));
+  for (int i = warp; i < a.upb; i += kWarps) {
     if (v0 + i >= a.V) break;
     int64_t off = 0;
     for (int j = lane; j < i; j += 32) off += d_s[j];
@@ -212,8 +230,9 @@ __global__ void __launch_bounds__(kThreads) k_list_place(PageOpArgs a, int32_t n
     if (kFork) {
       const int64_t w = list_unit(a, v0 + i, a.dst, k);
       const int4 h = hdr[u];
+#pragma unroll 4
       for (int32_t j = lane; j < d; j += 32) {
-        const int32_t id = a.free_list[(at0 + off + j) % static_cast<uint64_t>(a.F)];
+        const int32_t id = a.free_list[ring(at0 + off + j, a.F)];
         if (id < 0 || id >= a.F) {  // the ring is not what the contract says: skip the page
           set_error(a.status, DKV_E_INTERNAL);
           a.list[before + off + j] = make_int2(-1, -1);
@@ -228,9 +247,10 @@ __global__ void __launch_bounds__(kThreads) k_list_place(PageOpArgs a, int32_t n
       for (int32_t j = d + lane; j < a.pmax; j += 32) a.fwd[w * a.pmax + j] = -1;
       if (lane == 0) hdr[w] = h;
     } else {
+#pragma unroll 4
       for (int32_t j = lane; j < d; j += 32) {
         const int32_t id = a.fwd[u * a.pmax + j];
-        a.free_list[(at0 + off + j) % static_cast<uint64_t>(a.F)] = id;
+        a.free_list[ring(at0 + off + j, a.F)] = id;
         a.rev_unit[id] = -1;
         a.rev_idx[id] = -1;
         a.page_cls[id] = 0;
@@ -274,7 +294,7 @@ __device__ __forceinline__ void copy_rows(uint8_t *base, const PageOpArgs &a, in
 }
 
 // A warp per page of the copy list, then a warp per piece of the row arrays.
-__global__ void __launch_bounds__(kThreads) k_fork_copy(PageOpArgs a) {
+__device__ __forceinline__ void fork_copy(const PageOpArgs &a) {
   const int64_t total = a.ws->total;
   if (total < 0) return;
   const int lane = threadIdx.x & 31;
@@ -312,7 +332,7 @@ __global__ void __launch_bounds__(kThreads) k_fork_copy(PageOpArgs a) {
 // kDefragPages page ids a block: free pages below n (the live count) and live
 // pages at or above it are counted; what the tables say of each live page is
 // checked.  part = {holes, movers << 32 | error}.
-__global__ void __launch_bounds__(kThreads) k_defrag_plan(PageOpArgs a) {
+__device__ __forceinline__ void defrag_plan(const PageOpArgs &a) {
   __shared__ int64_t sm[kWarps];
   __shared__ int32_t err_s;
   if (threadIdx.x == 0) err_s = 0;
@@ -322,20 +342,28 @@ __global__ void __launch_bounds__(kThreads) k_defrag_plan(PageOpArgs a) {
   const bool ok = tail >= head && n >= 0;
   int64_t holes = 0, movers = 0;
   const int64_t p0 = static_cast<int64_t>(blockIdx.x) * kDefragPages;
-  for (int i = threadIdx.x; i < kDefragPages && p0 + i < a.F; i += kThreads) {
-    const int64_t p = p0 + i;
-    const int32_t u = a.rev_unit[p];
-    const uint8_t c = a.page_cls[p];
-    bool good = ok && (c == 0) == (u < 0);
-    if (c != 0 && good) {
-      const int64_t t = u - a.unit_base;
-      const int32_t j = a.rev_idx[p];
-      good = t >= 0 && t < a.U && j >= 0 && j < a.pmax && a.fwd[t * a.pmax + j] == p;
-    }
-    if (!good) err_s = 1;
-    if (c == 0 && p < n) ++holes;
-    if (c != 0 && p >= n) ++movers;
+  constexpr int kEach = kDefragPages / kThreads;
+  int32_t u[kEach], j[kEach], c[kEach];
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int64_t p = p0 + threadIdx.x + i * kThreads;
+    const bool in = p < a.F;
+    u[i] = in ? a.rev_unit[p] : -1;
+    j[i] = in ? a.rev_idx[p] : 0;
+    c[i] = in ? a.page_cls[p] : 0;
   }
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int64_t p = p0 + threadIdx.x + i * kThreads, t = u[i] - a.unit_base;
+    bool good = ok && (c[i] == 0) == (u[i] < 0);
+    if (c[i] != 0) good = good && t >= 0 && t < a.U && j[i] >= 0 && j[i] < a.pmax && a.fwd[t * a.pmax + j[i]] == p;
+    if (p >= a.F) continue;
+    bad |= !good;
+    if (c[i] == 0 && p < n) ++holes;
+    if (c[i] != 0 && p >= n) ++movers;
+  }
+  if (bad) err_s = 1;
   holes = block_sum(holes, sm);
   movers = block_sum(movers, sm);
   if (threadIdx.x == 0) {
@@ -349,7 +377,7 @@ __global__ void __launch_bounds__(kThreads) k_defrag_plan(PageOpArgs a) {
 
 // Same blocks: the block's holes and movers go to the lists at the ranks the
 // sums before give, in ascending order of id.
-__global__ void __launch_bounds__(kThreads) k_defrag_list(PageOpArgs a, int32_t nparts) {
+__device__ __forceinline__ void defrag_list(const PageOpArgs &a, int32_t nparts) {
   __shared__ int64_t sm[kWarps];
   __shared__ int32_t wsum[2][kWarps];
   int64_t hb = 0, ht = 0, mb = 0, mt = 0, bad = 0;
@@ -406,7 +434,7 @@ __global__ void __launch_bounds__(kThreads) k_defrag_list(PageOpArgs a, int32_t 
 // A warp per move: the page's bytes, its reverse entry and class, the owner's
 // forward entry; then the free list and the cursors.  Sources (ids >= n) and
 // destinations (ids < n) are disjoint, so the order of the moves is free.
-__global__ void __launch_bounds__(kThreads) k_defrag_move(PageOpArgs a) {
+__device__ __forceinline__ void defrag_move(const PageOpArgs &a) {
   const int64_t total = a.ws->total;
   if (total < 0) return;
   const int lane = threadIdx.x & 31;
@@ -439,6 +467,45 @@ __global__ void __launch_bounds__(kThreads) k_defrag_move(PageOpArgs a) {
   }
 }
 
+// ----------------------------------------------------------------- launches --
+
+template <bool kFork>
+__global__ void __launch_bounds__(kThreads) k_list_plan(const __grid_constant__ PageOpArgs a) { list_plan<kFork>(a); }
+template <bool kFork>
+__global__ void __launch_bounds__(kThreads) k_list_place(const __grid_constant__ PageOpArgs a, int32_t nparts) {
+  list_place<kFork>(a, nparts);
+}
+__global__ void __launch_bounds__(kThreads) k_fork_copy(const __grid_constant__ PageOpArgs a) { fork_copy(a); }
+__global__ void __launch_bounds__(kThreads) k_defrag_plan(const __grid_constant__ PageOpArgs a) { defrag_plan(a); }
+__global__ void __launch_bounds__(kThreads) k_defrag_list(const __grid_constant__ PageOpArgs a, int32_t nparts) {
+  defrag_list(a, nparts);
+}
+__global__ void __launch_bounds__(kThreads) k_defrag_move(const __grid_constant__ PageOpArgs a) { defrag_move(a); }
+
+// The steps of a small call in one launch: a cluster of kCluster blocks, whose
+// barrier (hardware's, so every block is there) stands for the launches' order.
+constexpr int kCluster = 8;
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+enum Op { kForkOp, kReleaseOp, kDefragOp };
+template <int kOp>
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) k_small(const __grid_constant__ PageOpArgs a) {
+  if (kOp == kDefragOp) defrag_plan(a);
+  else list_plan<kOp == kForkOp>(a);
+  __threadfence();
+  cluster_sync();
+  if (kOp == kDefragOp) defrag_list(a, kCluster);
+  else list_place<kOp == kForkOp>(a, kCluster);
+  if (kOp == kReleaseOp) return;
+  __threadfence();
+  cluster_sync();
+  if (kOp == kForkOp) fork_copy(a);
+  else defrag_move(a);
+}
+
 int copy_grid(int64_t warps, int sms) {
   // 8 blocks of 256 threads fill an SM
   return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((warps + kWarps - 1) / kWarps, int64_t{sms} * 8)));
@@ -446,21 +513,34 @@ int copy_grid(int64_t warps, int sms) {
 
 }  // namespace
 
+// Up to 64 list units (or 8192 pages to look through) and 4 MB of copies eight
+// blocks do as fast as the launches that more of them would take.
+constexpr int64_t kSmallBytes = 4 << 20;
+
 cudaError_t launch_fork(const PageOpArgs &a, int sms, cudaStream_t s) {
-  const int32_t parts = static_cast<int32_t>((a.V + kPlanUnits - 1) / kPlanUnits);
+  const int32_t parts = static_cast<int32_t>((a.V + a.upb - 1) / a.upb);
   const size_t bits = 8 * static_cast<size_t>((a.R + 31) / 32);
+  const int64_t rows = a.ctx_lens ? static_cast<int64_t>(a.L) * a.n * a.cap : 0;
+  const int64_t most = a.V * a.pmax * a.page_bytes + rows * (5 * a.Hkv + 4 * a.Hq + 4);
+  if (parts <= kCluster && most <= kSmallBytes) {
+    k_small<kForkOp><<<kCluster, kThreads, bits, s>>>(a);
+    return cudaGetLastError();
+  }
   k_list_plan<true><<<parts, kThreads, bits, s>>>(a);
   if (cudaError_t e = cudaGetLastError()) return e;
   k_list_place<true><<<parts, kThreads, 0, s>>>(a, parts);
   if (cudaError_t e = cudaGetLastError()) return e;
-  const int64_t most = a.V * a.pmax + (a.ctx_lens ? static_cast<int64_t>(a.L) * a.n * (a.cap / 16 + 4) : 0);
-  k_fork_copy<<<copy_grid(most, sms), kThreads, 0, s>>>(a);
+  k_fork_copy<<<copy_grid(a.V * a.pmax + rows / 16 + 1, sms), kThreads, 0, s>>>(a);
   return cudaGetLastError();
 }
 
 cudaError_t launch_release(const PageOpArgs &a, cudaStream_t s) {
-  const int32_t parts = static_cast<int32_t>((a.V + kPlanUnits - 1) / kPlanUnits);
+  const int32_t parts = static_cast<int32_t>((a.V + a.upb - 1) / a.upb);
   const size_t bits = 8 * static_cast<size_t>((a.R + 31) / 32);
+  if (parts <= kCluster) {
+    k_small<kReleaseOp><<<kCluster, kThreads, bits, s>>>(a);
+    return cudaGetLastError();
+  }
   k_list_plan<false><<<parts, kThreads, bits, s>>>(a);
   if (cudaError_t e = cudaGetLastError()) return e;
   k_list_place<false><<<parts, kThreads, 0, s>>>(a, parts);
@@ -469,6 +549,10 @@ cudaError_t launch_release(const PageOpArgs &a, cudaStream_t s) {
 
 cudaError_t launch_defrag(const PageOpArgs &a, int sms, cudaStream_t s) {
   const int32_t parts = static_cast<int32_t>((a.F + kDefragPages - 1) / kDefragPages);
+  if (parts <= kCluster && a.F * a.page_bytes <= kSmallBytes) {
+    k_small<kDefragOp><<<kCluster, kThreads, 0, s>>>(a);
+    return cudaGetLastError();
+  }
   k_defrag_plan<<<parts, kThreads, 0, s>>>(a);
   if (cudaError_t e = cudaGetLastError()) return e;
   k_defrag_list<<<parts, kThreads, 0, s>>>(a, parts);

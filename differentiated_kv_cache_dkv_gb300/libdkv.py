@@ -554,7 +554,8 @@ class Decoder:
         self.slot_of = torch.full((rows,), -1, dtype=torch.int32, device=device)
         self.workspace = torch.empty(dkv_decode_workspace_size(self.batch({})), dtype=torch.uint8, device=device)
         dkv_init_pool(self.pool)
-        self._pre_ws = self._ext_ws = self._ops_ws = None
+        self._pre_ws = self._ops_ws = None
+        self._ext_ws: list[torch.Tensor] = []  # outgrown ones stay: a captured graph may use them
 
     def batch(self, d: dict) -> dkv_decode_batch:
         g = d.get
@@ -593,14 +594,20 @@ class Decoder:
 
     def extend(self, q: torch.Tensor, new_lens: torch.Tensor, ctx_lens: torch.Tensor, max_new: int, out: torch.Tensor,
                scale: float, k_new: torch.Tensor | None = None, v_new: torch.Tensor | None = None,
-               lse: torch.Tensor | None = None, layer0: int = 0, stream=None) -> None:
-        """dkv_extend_attention of several new tokens a request over layers [layer0, layer0 + q.shape[0])."""
+               lse: torch.Tensor | None = None, layer0: int = 0, workspace: torch.Tensor | None = None,
+               stream=None) -> None:
+        """dkv_extend_attention of several new tokens a request over layers [layer0, layer0 + q.shape[0]).
+
+        Calls (and replays of captured ones) that may run at the same time need a workspace each, of
+        dkv_extend_workspace_size bytes; without one they share the decoder's and run in stream order."""
         b = make_extend_batch(self.L, self.Hkv, self.cap, q, new_lens, ctx_lens, max_new, scale, k_new=k_new,
                               v_new=v_new, out=out, lse=lse, layer0=layer0)
-        need = dkv_extend_workspace_size(b, self.pool, self.tables)
-        if need and (self._ext_ws is None or self._ext_ws.numel() < need):
-            self._ext_ws = torch.empty(need, dtype=torch.uint8, device=self.device)
-        dkv_extend_attention(b, self.pool, self.tables, self._ext_ws, stream=stream)
+        if workspace is None:
+            need = dkv_extend_workspace_size(b, self.pool, self.tables)
+            if need and (not self._ext_ws or self._ext_ws[-1].numel() < need):
+                self._ext_ws.append(torch.empty(need, dtype=torch.uint8, device=self.device))
+            workspace = self._ext_ws[-1] if need else None
+        dkv_extend_attention(b, self.pool, self.tables, workspace, stream=stream)
 
     def extend_significance(self, q: torch.Tensor, new_lens: torch.Tensor, acc_lens: torch.Tensor,
                             ctx_lens: torch.Tensor, max_new: int, scale: float, lse: torch.Tensor,

@@ -77,7 +77,8 @@ def reference(st: dict, w: W.Workload, q, k_new, v_new, new_lens, acc_lens=None,
     fp16's normal range) against held values rounded to fp16 (2^-11), and to
     bf16 (2^-8) against the exact bf16 new values; fp32 sums of n terms add
     n u.  The result is rounded to bf16: 2^-8."""
-    q, kn, vn = (x.float().numpy().astype(np.float64) for x in (q, k_new, v_new))
+    has = k_new is not None  # else the held tokens alone are attended
+    q, kn, vn = (x.float().numpy().astype(np.float64) for x in (q, k_new if has else q[:, :0], v_new if has else q[:, :0]))
     nl, T = q.shape[:2]
     G = w.Hq // w.Hkv
     out = np.zeros((nl, T, w.Hq, 128))
@@ -94,14 +95,20 @@ def reference(st: dict, w: W.Workload, q, k_new, v_new, new_lens, acc_lens=None,
                 u = ((layer0 + li) * w.R + r) * w.Hkv + h
                 k, v, ka, pos = unit_arrays(st, u, w.P, w.scheme)
                 m = len(pos)
-                k = np.concatenate([k, kn[li, t0:t0 + n, h]])
-                v = np.concatenate([v, vn[li, t0:t0 + n, h]])
-                ka = np.concatenate([ka, np.abs(kn[li, t0:t0 + n, h])])
-                seen = np.concatenate([np.ones((n, m), bool), np.tril(np.ones((n, n), bool))], 1)
-                half = np.concatenate([np.full(m, 2.0 ** -10), np.full(n, 2.0 ** -8)])
+                f = n if has else 0
+                if has:
+                    k = np.concatenate([k, kn[li, t0:t0 + n, h]])
+                    v = np.concatenate([v, vn[li, t0:t0 + n, h]])
+                    ka = np.concatenate([ka, np.abs(kn[li, t0:t0 + n, h])])
+                seen = np.concatenate([np.ones((n, m), bool), np.tril(np.ones((n, n), bool))[:, :f]], 1)
+                half = np.concatenate([np.full(m, 2.0 ** -10), np.full(f, 2.0 ** -8)])
                 for g in range(G):
                     qh = q[li, t0:t0 + n, h * G + g]
                     if n == 0:
+                        continue
+                    if m + f == 0:  # nothing attended: 0 and -inf
+                        if acc_lens is not None:
+                            sig[li, r, h * G + g] = (pos, np.zeros(0), np.zeros(0))
                         continue
                     x = np.where(seen, scale * (qh @ k.T), -np.inf)
                     mx = x.max(1, keepdims=True)

@@ -453,7 +453,7 @@ struct ExtendPartial {
 // (parts = 0: the blocks write the outputs themselves).
 struct ExtendPlan {
   int32_t mt, row_tiles, splits, parts;
-  int64_t blocks;
+  int64_t full, blocks;  // row tiles that one block does, all blocks
   size_t o, bytes;  // workspace: float2 [parts][rows] at 0, float [parts][rows][128] at o
 };
 
@@ -483,7 +483,7 @@ cudaError_t launch_prefill(const PrefillArgs &a, cudaStream_t s);
 cudaError_t launch_fork(const PageOpArgs &a, int sms, cudaStream_t s);
 cudaError_t launch_release(const PageOpArgs &a, cudaStream_t s);
 cudaError_t launch_defrag(const PageOpArgs &a, int sms, cudaStream_t s);
-ExtendPlan extend_plan(int64_t units, int32_t max_new, int32_t G, int32_t cap, int64_t rows);
+ExtendPlan extend_plan(int64_t units, int32_t R, int32_t max_new, int32_t G, int32_t cap, int64_t rows);
 cudaError_t launch_extend(const ExtendArgs &a, const ExtendPlan &p, void *ws, cudaStream_t s);
 cudaError_t launch_extend_few(const ExtendArgs &a, const ExtendPlan &p, const ExtendPartial &part, cudaStream_t s);
 cudaError_t launch_extend_sig(const ExtendArgs &a, cudaStream_t s);

@@ -69,6 +69,7 @@ struct __align__(1024) Smem {
   uint32_t tmem;
   uint32_t qmax;  // largest finite |q| of the block's rows (bits)
   int32_t abort, bad;
+  int64_t u, tok0;  // unit and first new token, for the conversion (which has no registers for them)
 };
 template <int MT>
 constexpr size_t smem_bytes() { return sizeof(Smem<MT>) + 1024; }
@@ -112,18 +113,24 @@ __device__ __forceinline__ void channel_order(const uint32_t *r, float *x) {
     }
 }
 
-template <int SC, int MT>
+// The first `full` blocks do a row tile each, the others one of `splits` parts
+// of a row tile's token tiles.
+template <int SC, int MT, bool kSorted>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_extend(const __grid_constant__ ExtendArgs a, int32_t row_tiles, int32_t splits, ExtendPartial part) {
+    k_extend(const __grid_constant__ ExtendArgs a, int32_t row_tiles, uint32_t full, int32_t splits, ExtendPartial part) {
   constexpr int KH = scheme_kh(SC), VH = scheme_vh(SC);
   extern __shared__ unsigned char smem_raw[];
   // aligned by an offset, not by an integer address: the compiler then knows that these are shared accesses
   Smem<MT> &sm = *reinterpret_cast<Smem<MT> *>(smem_raw + (-saddr(smem_raw) & 1023u));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint32_t ur = blockIdx.x / splits, ui = ur / row_tiles, rh = ui / a.Hkv;  // ..., unit, (layer, request)
-  const int32_t sp = static_cast<int32_t>(blockIdx.x - ur * splits), rt = static_cast<int32_t>(ur - ui * row_tiles);
-  const int32_t h = static_cast<int32_t>(ui - rh * a.Hkv);
-  const int32_t li = static_cast<int32_t>(rh / a.R), r = static_cast<int32_t>(rh - li * a.R);
+  // in the order (request, the longest first when sorted; layer, head; row tile; part)
+  const bool whole = blockIdx.x < full;
+  const uint32_t pb = blockIdx.x - full, ur = whole ? blockIdx.x : full + pb / splits, ui = ur / row_tiles;
+  const uint32_t lh = static_cast<uint32_t>(a.n_layers) * a.Hkv, k = ui / lh, rest = ui - k * lh;
+  const int32_t sp = whole ? 0 : static_cast<int32_t>(pb % splits), ns = whole ? 1 : splits;
+  const int32_t rt = static_cast<int32_t>(ur - ui * row_tiles);
+  const int32_t li = static_cast<int32_t>(rest / a.Hkv), h = static_cast<int32_t>(rest - li * a.Hkv);
+  const int32_t r = kSorted ? longest_first(a, static_cast<int32_t>(k)) : static_cast<int32_t>(k);
   int64_t before;
   if (!lens_valid(a, r, before)) return;
   const int32_t rows = __ldg(a.new_lens + r) * a.G, row0 = rt * (128 * MT);
@@ -132,7 +139,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int32_t fresh = a.k_new ? (min(row0 + 128 * MT, rows) - 1) / a.G + 1 : 0;
   const Tiles ts{(x.n_hi + 127) / 128, (x.n_lo + 127) / 128, (fresh + 127) / 128};
   // this block's share of the tiles
-  const int32_t nt = ts.count(), per = (nt + splits - 1) / splits;
+  const int32_t nt = ts.count(), per = (nt + ns - 1) / ns;
   const int32_t j0 = min(nt, sp * per), n = min(nt, j0 + per) - j0;
   const int64_t tok0 = static_cast<int64_t>(li) * a.T + before;
   volatile int32_t *abort = &sm.abort;
@@ -153,6 +160,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kMeta; ++i) mbar_init(&sm.mfull[i], kDeqWarps);
     sm.abort = 0;
     sm.bad = 0;
+    sm.u = x.u;
+    sm.tok0 = tok0;
     sm.qmax = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -369,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float l = l0 + l1, mo = m == -INFINITY ? 0.0f : m - kLift;
     if (ok && t > 0) ok = warp_wait(&sm.odone[wg], (t - 1) & 1u);
     fence_after();
-    const bool direct = MT == 2 && splits == 1;
+    const bool direct = MT == 2 && (whole || splits == 1);
     const int64_t slot = (MT == 2 ? sp : 2 * sp + wg) * part.rows + at;
     if (ok) {
       const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);  // NaN stays NaN
@@ -400,7 +409,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (have) {
         if (!direct) part.ml[slot] = make_float2(t > 0 ? mo : -INFINITY, l);
-        else if (a.lse) a.lse[at] = l == 0.0f ? -INFINITY : (mo + log2f(l)) * 0.693147180559945309f;
+        else if (part.ml) part.ml[at] = make_float2(0.0f, -1.0f);  // nothing to merge
+        if (direct && a.lse) a.lse[at] = l == 0.0f ? -INFINITY : (mo + log2f(l)) * 0.693147180559945309f;
       }
     }
     fence_before();
@@ -408,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ================= dequantising warps
     const int dt = tid - 32 * kSoftWarps;
     const PageGeom g = page_geom(SC, a.P);
-    DeqCtx d{&a, x, 0xffffffffu / a.P + 1, 0xffffffffu / (2 * a.P) + 1, static_cast<int32_t>(g.bytes),
+    DeqCtx d{&a, x, &sm.u, 0xffffffffu / a.P + 1, 0xffffffffu / (2 * a.P) + 1, static_cast<int32_t>(g.bytes),
              static_cast<uint32_t>(g.vbase), static_cast<uint32_t>(g.meta), dt >> 2, dt & 3, (dt & 3) >> 1, {}};
 #pragma unroll
     for (int i = 0; i < 4; ++i) d.off[i] = group_at(d.tk, 4 * d.c + (i ^ (2 * d.hs)));
@@ -436,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (j >= 2 && !(ok = warp_wait(&sm.kempty[b], ((j >> 1) - 1) & 1u))) break;
       if (t.kind == 0) convert_k<KH>(d, hd, sm, sm.k[b], ms, f);
       else if (t.kind == 1) convert_k<KH / 2>(d, hd, sm, sm.k[b], ms, f);
-      else new_k<2, true>(d, t, tok0, h, sm, sm.k[b], ms, f);
+      else new_k<2, true>(d, t, *const_cast<volatile int64_t *>(&sm.tok0), h, sm, sm.k[b], ms, f);
       fence_async();
       __syncwarp();
       if (lane == 0) {
@@ -452,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (j >= 2 && !(ok = warp_wait(&sm.vempty[b], ((j >> 1) - 1) & 1u))) break;
       if (cur.kind == 0) convert_v<VH>(d, hd, sm.v[b]);
       else if (cur.kind == 1) convert_v<VH / 2>(d, hd, sm.v[b]);
-      else new_v<2>(d, cur, tok0, h, sm.v[b]);
+      else new_v<2>(d, cur, *const_cast<volatile int64_t *>(&sm.tok0), h, sm.v[b]);
       fence_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.vfull[b]);
@@ -496,6 +506,7 @@ __global__ void __launch_bounds__(256) k_extend_merge(ExtendArgs a, int32_t part
   const int lane = threadIdx.x & 31;
   const int64_t at = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   if (at >= part.rows) return;
+  if (part.ml[at].y < 0.0f) return;  // written by its one block
   float M = -INFINITY;
 #pragma unroll 2
   for (int32_t p = 0; p < parts; ++p) {
@@ -522,13 +533,24 @@ __global__ void __launch_bounds__(256) k_extend_merge(ExtendArgs a, int32_t part
   if (a.lse && lane == 0) a.lse[at] = l == 0.0f ? -INFINITY : (M + log2f(l)) * 0.693147180559945309f;
 }
 
-template <int SC, int MT>
-cudaError_t launch(const ExtendArgs &a, const ExtendPlan &p, const ExtendPartial &part, cudaStream_t s) {
+template <int SC, int MT, bool kSorted>
+cudaError_t launch_kernel(const ExtendArgs &a, const ExtendPlan &p, const ExtendPartial &part, cudaStream_t s) {
   const int smem = static_cast<int>(smem_bytes<MT>());
-  if (cudaError_t e = cudaFuncSetAttribute(k_extend<SC, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem))
+  if (cudaError_t e = cudaFuncSetAttribute(k_extend<SC, MT, kSorted>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem))
     return e;
-  k_extend<SC, MT><<<static_cast<unsigned>(p.blocks), kThreads, smem, s>>>(a, p.row_tiles, p.splits, part);
+  k_extend<SC, MT, kSorted><<<static_cast<unsigned>(p.blocks), kThreads, smem, s>>>(a, p.row_tiles,
+                                                                                   static_cast<uint32_t>(p.full), p.splits, part);
   return cudaGetLastError();
+}
+
+// Sorting lets the blocks of short requests fill the gaps that those of long
+// ones leave (16 ragged requests: 188 -> 164 us); it costs registers in the
+// loop (four equal requests: 1626 -> 1668 us), so a few requests go unsorted.
+constexpr int32_t kUnsorted = 4;
+template <int SC>
+cudaError_t launch(const ExtendArgs &a, const ExtendPlan &p, const ExtendPartial &part, cudaStream_t s) {
+  if (p.mt == 1) return launch_kernel<SC, 1, true>(a, p, part, s);
+  return a.R > kUnsorted ? launch_kernel<SC, 2, true>(a, p, part, s) : launch_kernel<SC, 2, false>(a, p, part, s);
 }
 
 }  // namespace
@@ -537,7 +559,7 @@ cudaError_t launch(const ExtendArgs &a, const ExtendPlan &p, const ExtendPartial
 // lengths.
 constexpr int64_t kFewBlocks = 152 * 3;
 
-ExtendPlan extend_plan(int64_t units, int32_t max_new, int32_t G, int32_t cap, int64_t rows) {
+ExtendPlan extend_plan(int64_t units, int32_t R, int32_t max_new, int32_t G, int32_t cap, int64_t rows) {
   ExtendPlan p{};
   const int64_t most = static_cast<int64_t>(max_new) * G;
   const int64_t tiles = (static_cast<int64_t>(cap) + 127) / 128 + 2;
@@ -549,9 +571,18 @@ ExtendPlan extend_plan(int64_t units, int32_t max_new, int32_t G, int32_t cap, i
   } else {
     p.mt = most > 128 ? 2 : 1;
     p.row_tiles = static_cast<int32_t>((most + 128 * p.mt - 1) / (128 * p.mt));
-    while (units * p.row_tiles * p.splits < 152 && p.splits * 4 <= tiles) p.splits *= 2;
+    const int64_t items = units * p.row_tiles, rest = items % 152;
+    if (items < 152 || p.mt == 1) {
+      while (items * p.splits < 152 && p.splits * 4 <= tiles) p.splits *= 2;
+    } else if (R <= kUnsorted && rest > 0 && items < 16 * 152) {
+      // the last, incomplete wave in parts, as many as fill it (a chunk of
+      // 512 row tiles: 4 waves of 1, or 3 and one of 1/2; 1626 -> 1513 us)
+      p.splits = static_cast<int32_t>(std::clamp<int64_t>(152 / rest, 1, std::min<int64_t>(8, std::max<int64_t>(tiles / 4, 1))));
+      if (p.splits > 1) p.full = items - rest;
+    }
   }
-  p.blocks = units * p.row_tiles * p.splits;
+  const int64_t items = units * p.row_tiles;
+  p.blocks = p.full + (items - p.full) * p.splits;
   p.parts = p.mt == 1 ? 2 * p.splits : (p.splits == 1 ? 0 : p.splits);
   size_t o = align256(sizeof(float2) * static_cast<size_t>(p.parts) * rows);
   p.o = o;
@@ -568,10 +599,8 @@ cudaError_t launch_extend(const ExtendArgs &a, const ExtendPlan &p, void *ws, cu
   cudaError_t e;
   if (p.mt == 0)
     e = launch_extend_few(a, p, part, s);
-  else if (p.mt == 2)
-    e = a.scheme == 0 ? launch<0, 2>(a, p, part, s) : a.scheme == 1 ? launch<1, 2>(a, p, part, s) : launch<2, 2>(a, p, part, s);
   else
-    e = a.scheme == 0 ? launch<0, 1>(a, p, part, s) : a.scheme == 1 ? launch<1, 1>(a, p, part, s) : launch<2, 1>(a, p, part, s);
+    e = a.scheme == 0 ? launch<0>(a, p, part, s) : a.scheme == 1 ? launch<1>(a, p, part, s) : launch<2>(a, p, part, s);
   if (e != cudaSuccess || p.parts == 0) return e;
   k_extend_merge<<<static_cast<unsigned>((part.rows + 7) / 8), 256, 0, s>>>(a, p.parts, part);
   return cudaGetLastError();

@@ -442,7 +442,7 @@ __device__ __forceinline__ bool lens_valid(const ExtendArgs &a, int32_t r, int64
   return ok_s != 0;
 }
 
-// The request with the k-th most tokens (ties: the first one), or k itself when
+// The request with the k-th most tokens, held and new (ties: the first one), or k itself when
 // there are more requests than that is worth.  Every block asks, all its threads.
 constexpr int32_t kOrder = 512;
 __device__ __forceinline__ int32_t longest_first(const ExtendArgs &a, int32_t k) {
@@ -451,7 +451,10 @@ __device__ __forceinline__ int32_t longest_first(const ExtendArgs &a, int32_t k)
   if (a.R > kOrder) return k;
   const int32_t tid = threadIdx.x, n4 = (a.R + 3) / 4;
   if (tid == 0) pick = k;
-  for (int32_t i = tid; i < 4 * n4; i += blockDim.x) len[i] = i < a.R ? __ldg(a.ctx_lens + i) : INT32_MIN;
+  for (int32_t i = tid; i < 4 * n4; i += blockDim.x) {
+    // lengths that are not valid yet may wrap: any order will do for them
+    len[i] = i < a.R ? static_cast<int32_t>(static_cast<uint32_t>(__ldg(a.ctx_lens + i)) + __ldg(a.new_lens + i)) : INT32_MIN;
+  }
   __syncthreads();
   for (int32_t i = tid; i < a.R; i += blockDim.x) {
     const int32_t mine = len[i];
@@ -464,7 +467,7 @@ __device__ __forceinline__ int32_t longest_first(const ExtendArgs &a, int32_t k)
     if (rank == k) pick = i;
   }
   __syncthreads();
-  return pick;
+  return static_cast<int32_t>(__reduce_max_sync(kFull, static_cast<uint32_t>(pick)));  // into a uniform register
 }
 
 // The lists of a unit (empty when its header contradicts itself).

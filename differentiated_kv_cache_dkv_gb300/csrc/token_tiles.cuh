@@ -60,6 +60,7 @@ __device__ __forceinline__ Tile tile_at(const Tiles &ts, const Unit &x, int32_t 
 struct DeqCtx {
   const ExtendArgs *a;
   Unit x;
+  const volatile int64_t *u;  // x.u in shared memory
   uint32_t m1, m2;  // split() by P and 2 P
   int32_t bytes;
   uint32_t vbase, meta;
@@ -91,7 +92,7 @@ __device__ __forceinline__ void locate(const DeqCtx &d, const Tile &t, Where<NP>
     const int32_t i = d.tk + 128 / NP * p;
     int32_t k;
     split(t.t0 + i, per, M, k, w.slot[p]);
-    w.id[p] = i < t.n ? __ldg(d.a->fwd + d.x.u * d.a->pmax + first + k) : -1;
+    w.id[p] = i < t.n ? __ldg(d.a->fwd + *d.u * d.a->pmax + first + k) : -1;
   }
 }
 

@@ -164,3 +164,9 @@ def test_page_operations_on_more_units_than_a_warp_each():
     dec.release(_i32(src))
     assert libdkv.dkv_get_status(dec.pool) == libdkv.DKV_OK
     assert_equal(pool_state(dec.pool, dec.tables), want, "release")
+
+
+def test_a_last_wave_in_parts():
+    """More row tiles than multiprocessors: the last, incomplete wave is split and merged."""
+    w = W.small("waves", L=2, lens=[700, 150, 260], Hq=32, Hkv=8)
+    _check(w, [250, 249, 0], 250, acc=[0, 249, 0])  # 48 units x 4 row tiles: a wave of 152 and 40 in halves

@@ -507,26 +507,36 @@ __global__ void __launch_bounds__(256) k_extend_merge(ExtendArgs a, int32_t part
   const int64_t at = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   if (at >= part.rows) return;
   if (part.ml[at].y < 0.0f) return;  // written by its one block
+  // a lane per part for the references and sums, then the parts' O one by one
   float M = -INFINITY;
-#pragma unroll 2
-  for (int32_t p = 0; p < parts; ++p) {
+  for (int32_t p = lane; p < parts; p += 32) {
     const float2 ml = part.ml[p * part.rows + at];
     if (ml.y != 0.0f) M = fmaxf(M, ml.x);
   }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
   float l = 0.0f;
   float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 2
-  for (int32_t p = 0; p < parts; ++p) {
-    const float2 ml = part.ml[p * part.rows + at];
-    if (ml.y == 0.0f) continue;  // attends nothing there (or no tile): O may not be written
-    const float f = ex2(ml.x - M);
-    const float4 v = *reinterpret_cast<const float4 *>(part.o + (p * part.rows + at) * 128 + 4 * lane);
-    l = fmaf(f, ml.y, l);
-    o.x = fmaf(f, v.x, o.x);
-    o.y = fmaf(f, v.y, o.y);
-    o.z = fmaf(f, v.z, o.z);
-    o.w = fmaf(f, v.w, o.w);
+  for (int32_t p0 = 0; p0 < parts; p0 += 32) {
+    const float2 ml = p0 + lane < parts ? part.ml[(p0 + lane) * part.rows + at] : make_float2(0.0f, 0.0f);
+    const bool some = ml.y != 0.0f;  // else it attends nothing there (or has no tile): O may not be written
+    const float f = some ? ex2(ml.x - M) : 0.0f;
+    if (some) l = fmaf(f, ml.y, l);
+    const uint32_t live = __ballot_sync(kFull, some);
+#pragma unroll 4
+    for (int i = 0; i < min(32, parts - p0); ++i) {
+      const float fi = __shfl_sync(kFull, f, i);
+      const float4 v = live >> i & 1u
+                           ? *reinterpret_cast<const float4 *>(part.o + ((p0 + i) * part.rows + at) * 128 + 4 * lane)
+                           : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      o.x = fmaf(fi, v.x, o.x);
+      o.y = fmaf(fi, v.y, o.y);
+      o.z = fmaf(fi, v.z, o.z);
+      o.w = fmaf(fi, v.w, o.w);
+    }
   }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(kFull, l, d);
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   *reinterpret_cast<uint2 *>(a.out + at * 128 + 4 * lane) =
       make_uint2(bf16x2_rn(o.x * inv, o.y * inv), bf16x2_rn(o.z * inv, o.w * inv));
@@ -555,9 +565,13 @@ cudaError_t launch(const ExtendArgs &a, const ExtendPlan &p, const ExtendPartial
 
 }  // namespace
 
-// A few waves of blocks of the few-row kernel even out units of different
-// lengths.
-constexpr int64_t kFewBlocks = 152 * 3;
+// Parts of a context, while the blocks with at most 32 rows do not pass two
+// waves of the 152 multiprocessors, with six tiles each at least (requests of
+// 2048 .. 8192 tokens with 8 heads, one wave / two / three: 1 request 30 / 30 /
+// 30 us, 8: 58 / 52 / 62, 16: 90 / 80 / 87, 24: 92 / 92 / 113; powers of two up
+// to three waves: 42, 72, 94 and 116).  Blocks of 128 or 256 rows: one wave (a
+// request with 512 new tokens over 8192: 138 / 155 / 162 us).
+constexpr int64_t kFewBlocks = 152 * 2;
 
 ExtendPlan extend_plan(int64_t units, int32_t R, int32_t max_new, int32_t G, int32_t cap, int64_t rows) {
   ExtendPlan p{};
@@ -567,13 +581,13 @@ ExtendPlan extend_plan(int64_t units, int32_t R, int32_t max_new, int32_t G, int
   if (most <= 32) {
     p.mt = 0;
     p.row_tiles = 1;
-    while (units * p.splits < kFewBlocks && p.splits * 4 <= tiles) p.splits *= 2;
+    p.splits = static_cast<int32_t>(std::clamp<int64_t>(kFewBlocks / std::max<int64_t>(units, 1), 1, std::max<int64_t>(tiles / 6, 1)));
   } else {
     p.mt = most > 128 ? 2 : 1;
     p.row_tiles = static_cast<int32_t>((most + 128 * p.mt - 1) / (128 * p.mt));
     const int64_t items = units * p.row_tiles, rest = items % 152;
     if (items < 152 || p.mt == 1) {
-      while (items * p.splits < 152 && p.splits * 4 <= tiles) p.splits *= 2;
+      p.splits = static_cast<int32_t>(std::clamp<int64_t>(152 / std::max<int64_t>(items, 1), 1, std::max<int64_t>(tiles / 4, 1)));
     } else if (R <= kUnsorted && rest > 0 && items < 16 * 152) {
       // the last, incomplete wave in parts, as many as fill it (a chunk of
       // 512 row tiles: 4 waves of 1, or 3 and one of 1/2; 1626 -> 1513 us)

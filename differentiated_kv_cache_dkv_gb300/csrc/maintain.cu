@@ -146,7 +146,7 @@ __device__ __forceinline__ void list_plan(const PageOpArgs &a) {
     }
     if (lane == 0) sum += max(d, 0);
   }
-  if (blockIdx.x == 0) {
+  if (blockIdx.x == gridDim.x - 1) {  // in a small call a block without units
     const int32_t e = check_lists(a, bits);
     if (e) err = e;
     if (threadIdx.x == 0) {  // the cursors before the call: the next kernel moves them
@@ -167,6 +167,24 @@ __device__ __forceinline__ int64_t ring(int64_t x, int64_t F) { return x < F ? x
 __device__ __forceinline__ int32_t plan_totals(const longlong2 *part, int32_t nparts, int64_t *sm, int64_t &before,
                                                int64_t &total) {
   int64_t b = 0, t = 0, e = INT64_MAX;
+  if (nparts <= 32) {  // every warp for itself
+    const int32_t i = threadIdx.x & 31;
+    if (i < nparts) {
+      const longlong2 p = part[i];
+      t = p.x;
+      if (i < static_cast<int32_t>(blockIdx.x)) b = p.x;
+      if (p.y) e = (static_cast<int64_t>(i) << 8) - p.y;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      b += __shfl_xor_sync(kFull, b, o);
+      t += __shfl_xor_sync(kFull, t, o);
+      e = min(e, __shfl_xor_sync(kFull, e, o));
+    }
+    before = b;
+    total = t;
+    return e == INT64_MAX ? 0 : -static_cast<int32_t>(e & 0xff);
+  }
   for (int32_t i = threadIdx.x; i < nparts; i += kThreads) {
     const longlong2 p = part[i];
     t += p.x;

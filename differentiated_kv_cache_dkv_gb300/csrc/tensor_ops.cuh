@@ -448,7 +448,7 @@ constexpr int32_t kOrder = 512;
 __device__ __forceinline__ int32_t longest_first(const ExtendArgs &a, int32_t k) {
   __shared__ __align__(16) int32_t len[kOrder];
   __shared__ int32_t pick;
-  if (a.R > kOrder) return k;
+  if (a.R == 1 || a.R > kOrder) return k;
   const int32_t tid = threadIdx.x, n4 = (a.R + 3) / 4;
   if (tid == 0) pick = k;
   for (int32_t i = tid; i < 4 * n4; i += blockDim.x) {

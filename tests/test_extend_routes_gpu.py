@@ -170,3 +170,11 @@ def test_a_last_wave_in_parts():
     """More row tiles than multiprocessors: the last, incomplete wave is split and merged."""
     w = W.small("waves", L=2, lens=[700, 150, 260], Hq=32, Hkv=8)
     _check(w, [250, 249, 0], 250, acc=[0, 249, 0])  # 48 units x 4 row tiles: a wave of 152 and 40 in halves
+
+
+def test_many_parts():
+    """One unit over a long context: more parts than a warp has lanes."""
+    w = W.small("parts", L=1, lens=[30000], Hq=2, Hkv=1)
+    _check(w, [7], 8, acc=[4])
+    w = W.small("parts64", L=1, lens=[20000], Hq=8, Hkv=1)
+    _check(w, [9], 9, acc=[9])

@@ -248,31 +248,48 @@ __device__ __forceinline__ void list_place(const PageOpArgs &a, int32_t nparts) 
     if (kFork) {
       const int64_t w = list_unit(a, v0 + i, a.dst, k);
       const int4 h = hdr[u];
-#pragma unroll 4
-      for (int32_t j = lane; j < d; j += 32) {
-        const int32_t id = a.free_list[ring(at0 + off + j, a.F)];
-        if (id < 0 || id >= a.F) {  // the ring is not what the contract says: skip the page
-          set_error(a.status, DKV_E_INTERNAL);
-          a.list[before + off + j] = make_int2(-1, -1);
-          continue;
+      for (int32_t j0 = lane; j0 < d; j0 += 128) {
+        int32_t id[4], old[4];  // the loads before the stores, which might alias for all the compiler knows
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int32_t j = j0 + 32 * e;
+          if (j >= d) break;
+          id[e] = a.free_list[ring(at0 + off + j, a.F)];
+          old[e] = a.fwd[u * a.pmax + j];
         }
-        a.list[before + off + j] = make_int2(a.fwd[u * a.pmax + j], id);
-        a.fwd[w * a.pmax + j] = id;
-        a.rev_unit[id] = static_cast<int32_t>(a.unit_base + w);
-        a.rev_idx[id] = j;
-        a.page_cls[id] = j < h.z ? DKV_CLASS_K8V4 : DKV_CLASS_K4V2;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int32_t j = j0 + 32 * e;
+          if (j >= d) break;
+          const bool ok = id[e] >= 0 && id[e] < a.F;
+          a.list[before + off + j] = ok ? make_int2(old[e], id[e]) : make_int2(-1, -1);
+          if (!ok) {  // the ring is not what the contract says: skip the page
+            set_error(a.status, DKV_E_INTERNAL);
+            continue;
+          }
+          a.fwd[w * a.pmax + j] = id[e];
+          a.rev_unit[id[e]] = static_cast<int32_t>(a.unit_base + w);
+          a.rev_idx[id[e]] = j;
+          a.page_cls[id[e]] = j < h.z ? DKV_CLASS_K8V4 : DKV_CLASS_K4V2;
+        }
       }
       for (int32_t j = d + lane; j < a.pmax; j += 32) a.fwd[w * a.pmax + j] = -1;
       if (lane == 0) hdr[w] = h;
     } else {
-#pragma unroll 4
-      for (int32_t j = lane; j < d; j += 32) {
-        const int32_t id = a.fwd[u * a.pmax + j];
-        a.free_list[ring(at0 + off + j, a.F)] = id;
-        a.rev_unit[id] = -1;
-        a.rev_idx[id] = -1;
-        a.page_cls[id] = 0;
-        a.fwd[u * a.pmax + j] = -1;
+      for (int32_t j0 = lane; j0 < d; j0 += 128) {
+        int32_t id[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) id[e] = j0 + 32 * e < d ? a.fwd[u * a.pmax + j0 + 32 * e] : 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int32_t j = j0 + 32 * e;
+          if (j >= d) break;
+          a.free_list[ring(at0 + off + j, a.F)] = id[e];
+          a.rev_unit[id[e]] = -1;
+          a.rev_idx[id[e]] = -1;
+          a.page_cls[id[e]] = 0;
+          a.fwd[u * a.pmax + j] = -1;
+        }
       }
       if (lane == 0) hdr[u] = make_int4(0, 0, 0, 0);
     }
@@ -525,8 +542,10 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) k_s
 }
 
 int copy_grid(int64_t warps, int sms) {
-  // 8 blocks of 256 threads fill an SM
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((warps + kWarps - 1) / kWarps, int64_t{sms} * 8)));
+  // Many short-lived blocks, a few pages a warp: 8 / 64 / 128 / 512 blocks a
+  // multiprocessor take 547 / 530 / 524 / 580 us (8 prompts of 32 layers forked)
+  // and 172 / 162 / 164 / 174 us (a 60% live pool packed).
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((warps + kWarps - 1) / kWarps, int64_t{sms} * 96)));
 }
 
 }  // namespace

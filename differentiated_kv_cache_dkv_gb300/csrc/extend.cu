@@ -386,6 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = 0; c < 4; ++c) {
         uint32_t o[32];
         float f[32];
+        __syncwarp();  // rows that are padding have skipped ahead
         if (t > 0) {
           tmem_ld32(ts_o + 32 * c, o);
           tmem_wait32(o);

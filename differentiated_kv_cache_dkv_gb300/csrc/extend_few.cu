@@ -447,6 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int c0 = kMine * half; c0 < min(rows, kMine * half + kMine); c0 += 4) {
         uint32_t o[4];
+        __syncwarp();
         tmem_ld4(tmem + lanes + kColO + c0, o);
         tmem_wait4(o);
 #pragma unroll

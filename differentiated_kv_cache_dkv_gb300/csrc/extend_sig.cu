@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(Roles<kMany>::kThreads, 1)
     // ================= sum warps: a thread per token
     const int wg = warp >> 2, row = tid & 127;
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-    const bool wide = (a.G & 3) == 0 && (reinterpret_cast<uintptr_t>(a.sig_sum) & 15) == 0;
+    const bool wide = (a.G & 3) == 0;  // sig_sum is 16-byte aligned, and so are four heads of it then
     uint64_t run = 0;  // a head's sums so far, over even and odd columns (one tile a warp where it passes a block's end)
     bool ok = true;
 #pragma unroll 1
@@ -262,6 +262,7 @@ __global__ void __launch_bounds__(Roles<kMany>::kThreads, 1)
 #pragma unroll 1
           for (int32_t c = 0; c < cols; c += 16) {
             uint32_t u[16];
+            __syncwarp();  // lanes without a token have skipped ahead
             tmem_ld16(tmem + lanes + 128 * t + c, u);
             tmem_wait16(u);
 #pragma unroll
@@ -544,7 +545,7 @@ cudaError_t launch_extend_sig(const ExtendArgs &a, cudaStream_t s) {
   const int64_t tiles = (static_cast<int64_t>(a.cap) + 127) / 128 + 2;
   const int64_t splits = std::clamp<int64_t>(2 * 152 / std::max<int64_t>(units, 1), 1, (tiles + kGroup - 1) / kGroup);
   const int64_t blocks = units * splits;
-  if (blocks == 0 || a.max_new == 0) return cudaSuccess;
+  if (blocks == 0) return cudaSuccess;
   if (blocks > INT32_MAX) return cudaErrorInvalidValue;
   const int32_t sp = static_cast<int32_t>(splits);
   const bool many = lg == 7 || a.G > std::min(128 >> lg, kHeads);  // more than one block of Q (max_new bounds every request)

@@ -522,7 +522,7 @@ __global__ void __launch_bounds__(kThreads) k_defrag_move(const __grid_constant_
 constexpr int kCluster = 8;
 
 __device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
 enum Op { kForkOp, kReleaseOp, kDefragOp };
@@ -558,8 +558,7 @@ cudaError_t launch_fork(const PageOpArgs &a, int sms, cudaStream_t s) {
   const int32_t parts = static_cast<int32_t>((a.V + a.upb - 1) / a.upb);
   const size_t bits = 8 * static_cast<size_t>((a.R + 31) / 32);
   const int64_t rows = a.ctx_lens ? static_cast<int64_t>(a.L) * a.n * a.cap : 0;
-  const int64_t most = a.V * a.pmax * a.page_bytes + rows * (5 * a.Hkv + 4 * a.Hq + 4);
-  if (parts <= kCluster && most <= kSmallBytes) {
+  if (parts <= kCluster && a.V * a.pmax * a.page_bytes + rows * (5 * a.Hkv + 4 * a.Hq + 4) <= kSmallBytes) {
     k_small<kForkOp><<<kCluster, kThreads, bits, s>>>(a);
     return cudaGetLastError();
   }

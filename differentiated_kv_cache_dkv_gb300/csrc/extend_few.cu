@@ -6,10 +6,10 @@
 //   S^T = K Q^T     a token per tensor-memory lane, 64 columns of which `rows`
 //                   are real;
 //   O^T += V^T P^T  channels x rows.
-//   copy warp          bulk copies of the pages' rows (K codes, V codes, scales
-//     and zeros) into a ring of raw tiles, three tiles ahead: loads of single
-//     threads, or their asynchronous copies, cost the load unit about 1500
-//     cycles a tile, the bulk copies none;
+//   copy warps (3)     bulk copies of the pages (K codes, V codes, scales and
+//     zeros) into a ring of raw tiles, one tile each: loads of single threads,
+//     or their asynchronous copies, cost the load unit about 1500 cycles a
+//     tile, the bulk copies none, but issuing one costs its warp 54 cycles;
 //   convert warps (8)  four threads a token: K codes less their middle and V =
 //     fma(c, s, z), both fp16;
 //   softmax warps (8)  two threads per token: the token's logits against half of
@@ -19,6 +19,13 @@
 // A row's reference m is as in extend.cu, but a row is a column here: the
 // softmax warps meet at a named barrier once per tile, which also tells whether any
 // weight passed 2^15 and the references have to move (rarely).
+//
+// Measured (64 requests with 1 .. 8 drafts over 2048 .. 8192 tokens, 32 heads
+// over 8): 219 us for 374 MB, 1.71 TB/s, 26% of the measured copy rate.  A tile
+// takes about 2400 cycles: the conversion of K (880) and V (830) by eight warps,
+// K behind the product that read the tile before.  The kernel for 128 rows takes
+// 399 us there.  A call of four tokens over 512 takes 18 us, almost all of it
+// the latency of one block's start, its few tiles and its end.
 #include <algorithm>
 #include <cmath>
 #include <cstddef>

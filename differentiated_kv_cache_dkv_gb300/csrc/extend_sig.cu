@@ -17,9 +17,22 @@
 //   convert warps (8)  K tiles as in the attention (codes less their middle,
 //     fp16); Q blocks as fp16 times one power of two per block, with the sums
 //     of their rows and -lse (log2) per column;
+//   copy warps (3)     K codes by bulk copies, their scales and positions by
+//     asynchronous ones, into a ring of raw tiles;
 //   MMA warp           S^T of every (block, tile) into four tensor-memory
 //     buffers, one per tile of the group;
-//   sum warps (2 x 4)  a thread per token, tiles w and w + 2 of the group.
+//   sum warps          a thread per token, two or four warpgroups in turn.  A
+//     token's sums go to memory as additions without a result (each address
+//     has one adder a call, so their order cannot show).
+//
+// Measured (32 heads over 8): the drafts of 64 requests over 2048 .. 8192
+// tokens 172 us for 330 MB, 1.92 TB/s, 29% of the measured copy rate (a tile
+// takes its conversion, about 1250 cycles, and hand-overs: 2300); 4 requests of
+// 1024 tokens over 8192 541 us for 0.262 TFLOP, 484 TFLOP/s, 25% of the measured
+// bf16 rate: a block of 128 columns against four tiles takes 7200 cycles, where
+// the products would take 2048, the exponentials 2048 and the broadcast reads of
+// the columns' sums and lse 2150 of shared memory's time, which the products'
+// operands want as well.
 #include <algorithm>
 #include <cmath>
 #include <cstddef>

@@ -7,16 +7,24 @@
 // list in one coordinated step.  The pages describe the allocation; these are
 // the other steps of a pool's life, with the same prefix-sum placement.
 //
-// Every operation is two or three launches in stream order: a plan kernel
+// An operation is two or three launches in stream order: a plan kernel
 // checks everything and leaves one partial sum per block, the next kernel
 // adds up the partial sums itself (each block reads all of them: at most a
 // few thousand 16-byte entries from L2, less than a look-back's waits or a
 // launch would take), stops if any check failed or the pages do not suffice,
 // and places its block's share.  Nothing is written to the pool before every
 // check of the call has passed, which makes the calls all-or-nothing.
-//   fork     k_fork_plan, k_fork_place (tables, copy list), k_fork_copy
-//   release  k_release_plan, k_release_place
+//   fork     k_list_plan, k_list_place (tables, copy list), k_fork_copy
+//   release  k_list_plan, k_list_place
 //   defrag   k_defrag_plan, k_defrag_list, k_defrag_move
+// Small calls run their steps in one launch (k_small).
+//
+// Measured: 8 prompts of 2048 .. 6144 tokens in 32 layers forked 525 us for
+// 2.88 GB, 5.5 TB/s, 82% of the measured copy rate (the copies alone 87%); a
+// 28-layer pool of 0.83 GB moved 162 us, 5.1 TB/s, 77%; 8 requests of 32 layers
+// released 29 us, for 400,000 pages whose entries lie scattered: the latency of
+// two kernels' dependent loads and 1.2 million 32-byte sectors; the calls on
+// one small request 10 to 14 us of dependent loads.
 #include <cuda_runtime.h>
 
 #include <algorithm>

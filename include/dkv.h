@@ -446,7 +446,9 @@ int32_t dkv_extend_workspace_size(const dkv_extend_batch *b, const dkv_pool *poo
  * workspace: device, 256-byte aligned, >= dkv_extend_workspace_size bytes
  * (NULL when that is 0), scratch: calls that may overlap on the GPU (two
  * streams, two captured graphs) need one each.  Pool and tables are read
- * only.  Synchronous DKV_E_INVAL: a bad shape, pointer or workspace.
+ * only.  T = 0, R = 0 or n_layers = 0 is DKV_OK with nothing launched (the
+ * lengths are not looked at).  Synchronous DKV_E_INVAL: a bad shape, pointer
+ * or workspace.
  * Device-side (pool status word): DKV_E_LENS when a new_lens[r] is outside
  * [0, max_new], ctx_lens[r] + new_lens[r] is outside [0, cap] or the lengths do not add up to T:
  * nothing is written then; DKV_E_RANGE for a new K or V value that is not
@@ -468,7 +470,10 @@ int32_t dkv_extend_significance(const dkv_extend_batch *b, const int32_t *acc_le
 /* ------------------------------------------------------------------------
  * Page operations of a pool that serves many requests: a request is forked,
  * requests leave, a fragmented pool is packed.  All three are all-or-nothing:
- * on a device-side error (status word) nothing has changed.
+ * on a device-side error (status word) nothing has changed.  (One exception:
+ * the entries of the free list are trusted; an id outside [0, F) in it is
+ * reported as DKV_E_INTERNAL by the fork that draws it, which leaves that page
+ * out.)  n = 0 is DKV_OK with nothing launched.
  *
  * They share one workspace (device, 256-byte aligned, at least
  * dkv_page_ops_workspace_size bytes for the tables' U units, scratch).

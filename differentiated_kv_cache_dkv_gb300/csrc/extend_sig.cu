@@ -26,8 +26,8 @@
 //     has one adder a call, so their order cannot show).
 //
 // Measured (32 heads over 8): the drafts of 64 requests over 2048 .. 8192
-// tokens 172 us for 330 MB, 1.92 TB/s, 29% of the measured copy rate (a tile
-// takes its conversion, about 1250 cycles, and hand-overs: 2300); 4 requests of
+// tokens 156 us for 330 MB, 2.12 TB/s, 32% of the measured copy rate (a tile
+// takes its conversion, about 1000 cycles, and hand-overs: 2050); 4 requests of
 // 1024 tokens over 8192 541 us for 0.262 TFLOP, 484 TFLOP/s, 25% of the measured
 // bf16 rate: a block of 128 columns against four tiles takes 7200 cycles, where
 // the products would take 2048, the exponentials 2048 and the broadcast reads of
@@ -142,7 +142,7 @@ template <int W, int KH>
 __device__ __forceinline__ void convert_key(const DeqCtx &d, const uint8_t *raw, const uint32_t *there, Smem &sm, int q,
                                             float f, int32_t ctx) {
   constexpr int kMid = 1 << (W - 1);
-#pragma unroll 1
+#pragma unroll
   for (int p = 0; p < 2; ++p) {
     const int row = d.tk + 64 * p;
     uint32_t x[2][4];

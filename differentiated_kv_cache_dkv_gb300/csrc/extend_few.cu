@@ -471,9 +471,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp < kMmaWarp) {
     // ================= convert warps
     const int dt = tid - 32 * kSoftWarps;
-    const PageGeom pg = page_geom(SC, a.P);
-    DeqCtx d{&a, x, nullptr, 0xffffffffu / a.P + 1, 0xffffffffu / (2 * a.P) + 1, static_cast<int32_t>(pg.bytes),
-             static_cast<uint32_t>(pg.vbase), static_cast<uint32_t>(pg.meta), dt >> 2, dt & 3, ((dt & 3) >> 1) ^ (__popc(dt >> 2 & 7) & 1), {}};
+    // which half a token's threads take first alternates, so that the reads of
+    // neighbouring raw rows meet different banks as well as the writes
+    DeqCtx d{&a, x, nullptr, 0, 0, 0, 0, 0, dt >> 2, dt & 3, ((dt & 3) >> 1) ^ (__popc(dt >> 2 & 7) & 1), {}};
 #pragma unroll
     for (int i = 0; i < 4; ++i) d.off[i] = group_at(d.tk, 4 * d.c + (i ^ (2 * d.hs)));
     const float f = a.scale * kLog2e * pow2f(-e);

@@ -1,6 +1,6 @@
 // token_tiles.cuh -- token tiles of a unit as tensor-core operands: where 128
 // tokens of a list lie in the pages, their codes into registers and from there
-// into the swizzled rows of an operand (extend.cu, extend_sig.cu).
+// into the swizzled rows of an operand (extend.cu, extend_few.cu, extend_sig.cu).
 #pragma once
 
 #include "tensor_ops.cuh"
@@ -54,9 +54,11 @@ __device__ __forceinline__ Tile tile_at(const Tiles &ts, const Unit &x, int32_t 
 
 // ------------------------------------------------------- dequantising warps --
 //
-// Four threads a token, 32 channels each, NP tokens a thread: tk + p 128 / NP.  The thread of channels 64 .. takes its two 16-channel halves in the
-// other order, so that the eight threads of two neighbouring rows always
-// write eight different 16-byte chunks of the swizzled rows.
+// Four threads a token, 32 channels each, NP tokens a thread: tk + p 128 / NP.
+// The thread of channels 64 .. takes its two 16-channel halves in the other
+// order, so that the eight threads of two neighbouring rows always write eight
+// different 16-byte chunks of the swizzled rows.  (u, m1 .. meta: for locate and
+// fetch, where the codes come straight from the pages.)
 struct DeqCtx {
   const ExtendArgs *a;
   Unit x;

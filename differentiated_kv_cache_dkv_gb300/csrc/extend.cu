@@ -26,7 +26,9 @@
 // binades below it still has all its bits in fp16, so q . c is exact up to the
 // fp32 accumulation.
 // New tokens: K is scaled per token the same way; V stays the bf16 it is, and
-// that product takes P in bf16 (both operands of one MMA have one type).
+// that product takes P as the sum of two bf16 values in two products (both
+// operands of one MMA have one type; one bf16 value alone showed as a third of
+// the output's error where few tokens are attended).
 //
 // The maximum is lazy: P = 2^(y - m + 7) with a row's reference m (a whole
 // number, log2 units) that moves only when the sum of 32 weights passes 2^15,
@@ -42,8 +44,8 @@
 // Units with at most 32 rows have a kernel of their own (extend_few.cu).
 //
 // Measured (32 heads over 8, 4 requests of 1024 new tokens over 16384 held, half
-// of those in the high list, 39% in the low one): 1513 us, 1.01 TFLOP, 670 TFLOP/s,
-// 35% of the measured bf16 rate.  The tensor pipe is busy for 30% of the
+// of those in the high list, 39% in the low one): 1571 us, 1.01 TFLOP, 644 TFLOP/s,
+// 33% of the measured bf16 rate.  The tensor pipe is busy for 30% of the
 // cycles: a warpgroup's tile takes 6640, of which its softmax 3730 (932 for 32
 // columns, one warp a scheduler: the latencies of the tensor-memory load, of
 // the scales' broadcast reads and of the exponentials follow one another) and
@@ -234,13 +236,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       mma_commit(&sm.sfull[wg]);
       mma_commit(&sm.kempty[j & 1]);
     };
-    // O += P V of tile j: 16 tokens a step (8 columns of P, 16 rows of V)
+    // O += P V of tile j: 16 tokens a step (8 columns of P, 16 rows of V).  P of
+    // 32 tokens takes the first 16 of their 32 columns of S; against new tokens
+    // P is the sum of two bf16 values, the second ones in the other 16.
     auto issue_o = [&](int32_t j, bool bf16, bool first) {
       const uint32_t id = bf16 ? idesc(true, 128, 128, true) : idesc(false, 128, 128, true);
       const uint64_t db = dv + (j & 1) * kStep;
 #pragma unroll
       for (int kk = 0; kk < 8; ++kk)
-        mma_ts(tmem + 256 + 128 * wg, tmem + 128 * wg + 8 * kk, db + ((kk * 2048) >> 4), id, first && kk == 0 ? 0u : 1u);
+        mma_ts(tmem + 256 + 128 * wg, tmem + 128 * wg + 32 * (kk >> 1) + 8 * (kk & 1), db + ((kk * 2048) >> 4), id,
+               first && kk == 0 ? 0u : 1u);
+      if (bf16) {  // the weights' second halves
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          mma_ts(tmem + 256 + 128 * wg, tmem + 128 * wg + 32 * (kk >> 1) + 16 + 8 * (kk & 1), db + ((kk * 2048) >> 4), id, 1u);
+      }
       mma_commit(&sm.odone[wg]);
       mma_commit(&sm.vempty[j & 1]);
     };
@@ -299,15 +309,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         l2 = f2_mul(l2, f2_pack(f, f));
         m = mn;
 #pragma unroll 1
-        for (int i = 0; i < c; ++i) {
-          tmem_ld16(ts_s + 16 * i, u);
+        for (int i = 0; i < (tl.kind == 2 ? 2 * c : c); ++i) {
+          const uint32_t at_p = ts_s + (tl.kind == 2 ? 16 * i : 32 * i);
+          tmem_ld16(at_p, u);
           tmem_wait16(u);
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const float2 p2 = tl.kind == 2 ? make_float2(bf16_lo(u[e]), bf16_hi(u[e])) : __half22float2(u2h(u[e]));
             u[e] = tl.kind == 2 ? bf16x2_rn(p2.x * f, p2.y * f) : f16x2_rn(p2.x * f, p2.y * f);
           }
-          tmem_st16(ts_s + 16 * i, u);
+          tmem_st16(at_p, u);
         }
         if (t == 0) return true;
         if (!warp_wait(&sm.odone[wg], (t - 1) & 1u)) return false;
@@ -349,13 +360,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         l2 = f2_add(l2, sum[0]);
         if (tl.kind == 2) {
+          uint32_t w[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) u[i] = bf16x2_rn(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
+          for (int i = 0; i < 16; ++i) {
+            const float p0 = __uint_as_float(u[2 * i]), p1 = __uint_as_float(u[2 * i + 1]);
+            w[i] = bf16x2_rn(p0, p1);
+            u[i] = bf16x2_rest(p0, p1, w[i]);
+          }
+          tmem_st16(ts_s + 32 * c, w);
+          tmem_st16(ts_s + 32 * c + 16, u);
         } else {
 #pragma unroll
           for (int i = 0; i < 16; ++i) u[i] = f16x2_rn(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
+          tmem_st16(ts_s + 32 * c, u);
         }
-        tmem_st16(ts_s + 16 * c, u);
       }
       if (!ok) break;
       tmem_wait_st();

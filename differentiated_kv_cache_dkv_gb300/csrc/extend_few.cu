@@ -5,7 +5,7 @@
 // 128 rows would be mostly padding.  Here the tokens are the long side:
 //   S^T = K Q^T     a token per tensor-memory lane, 64 columns of which `rows`
 //                   are real;
-//   O^T += V^T P^T  channels x rows.
+//   O^T += V^T P^T  channels x rows; against new tokens P in two bf16 parts.
 //   copy warps (3)     bulk copies of the pages (K codes, V codes, scales and
 //     zeros) into a ring of raw tiles, one tile each: loads of single threads,
 //     or their asynchronous copies, cost the load unit about 1500 cycles a
@@ -21,7 +21,7 @@
 // weight passed 2^15 and the references have to move (rarely).
 //
 // Measured (64 requests with 1 .. 8 drafts over 2048 .. 8192 tokens, 32 heads
-// over 8): 219 us for 374 MB, 1.71 TB/s, 26% of the measured copy rate.  A tile
+// over 8): 224 us for 374 MB, 1.67 TB/s, 25% of the measured copy rate.  A tile
 // takes about 2400 cycles: the conversion of K (880) and V (830) by eight warps,
 // K behind the product that read the tile before.  The kernel for 128 rows takes
 // 399 us there.  A call of four tokens over 512 takes 18 us, almost all of it
@@ -72,7 +72,7 @@ struct __align__(1024) Smem {
 constexpr size_t kSmemBytes = sizeof(Smem) + 1024;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 static_assert(offsetof(Smem, q) % 1024 == 0 && offsetof(Smem, p) % 1024 == 0, "swizzled operands");
-static_assert(offsetof(Smem, raw) % 16 == 0, "bulk copies");
+static_assert(offsetof(Smem, raw) % 1024 == 0 && sizeof(Smem::raw[0]) % 1024 == 0, "bulk copies, weights of new tokens");
 
 __device__ __forceinline__ uint32_t ordered(float x) {
   const int32_t i = __float_as_int(x);
@@ -410,9 +410,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t w[kMine / 2];
 #pragma unroll
         for (int c = 0; c < kMine; ++c) l[c] += __uint_as_float(u[c]);
-        if (cur.kind == 2) {
+        if (cur.kind == 2) {  // the sum of two bf16 values; the second ones go where the tile has no codes
+          uint32_t rest[kMine / 2];
 #pragma unroll
-          for (int c = 0; c < kMine / 2; ++c) w[c] = bf16x2_rn(__uint_as_float(u[2 * c]), __uint_as_float(u[2 * c + 1]));
+          for (int c = 0; c < kMine / 2; ++c) {
+            const float p0 = __uint_as_float(u[2 * c]), p1 = __uint_as_float(u[2 * c + 1]);
+            w[c] = bf16x2_rn(p0, p1);
+            rest[c] = bf16x2_rest(p0, p1, w[c]);
+          }
+#pragma unroll
+          for (int c = 0; c < kMine / 8; ++c)
+            *reinterpret_cast<uint4 *>(sm.raw[j % kRaw] + row * 128 + (((2 * half + c) ^ (row & 7)) << 4)) =
+                make_uint4(rest[4 * c], rest[4 * c + 1], rest[4 * c + 2], rest[4 * c + 3]);
         } else {
 #pragma unroll
           for (int c = 0; c < kMine / 2; ++c) w[c] = f16x2_rn(__uint_as_float(u[2 * c]), __uint_as_float(u[2 * c + 1]));
@@ -569,11 +578,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (j >= 0) {  // O^T += V^T P^T of tile j: 16 tokens a step
         if (!(ok = wait(&sm.vfull[j & 1], (j >> 1) & 1u) && wait(&sm.pready, j & 1u))) break;
         fence_after();
-        const uint32_t id = idesc(j0 + j >= ts.hi + ts.lo, 128, 64, true) | kAMn;
+        const bool bf16 = j0 + j >= ts.hi + ts.lo;
+        const uint32_t id = idesc(bf16, 128, 64, true) | kAMn;
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
           mma_ss(tmem + kColO, dv + (((j & 1) * kTileBytes + kk * 2048) >> 4), dp + ((kk * 2048) >> 4), id,
                  j > 0 || kk > 0 ? 1u : 0u);
+        if (bf16) {  // the weights' second halves
+          const uint64_t dr = sw128_desc(saddr(sm.raw[j % kRaw]), kBox, 1024);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            mma_ss(tmem + kColO, dv + (((j & 1) * kTileBytes + kk * 2048) >> 4), dr + ((kk * 2048) >> 4), id, 1u);
+        }
         mma_commit(&sm.odone);
         mma_commit(&sm.vempty[j & 1]);
       }

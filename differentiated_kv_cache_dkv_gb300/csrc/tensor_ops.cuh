@@ -300,6 +300,10 @@ __device__ __forceinline__ uint32_t bf16x2_rn(float lo, float hi) {
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+// What bf16x2_rn(lo, hi) = w left of the two values, as bf16.
+__device__ __forceinline__ uint32_t bf16x2_rest(float lo, float hi, uint32_t w) {
+  return bf16x2_rn(lo - bf16_lo(w), hi - bf16_hi(w));
+}
 __device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
 
 __device__ __forceinline__ uint32_t h2u(__half2 x) { return *reinterpret_cast<uint32_t *>(&x); }

@@ -74,9 +74,9 @@ def reference(st: dict, w: W.Workload, q, k_new, v_new, new_lens, acc_lens=None,
     running rescales.  lse errs by sum_t p eta plus 2^-22 + u |lse|.
     Probabilities enter the value product rounded to fp16 (half a step is
     2^-11 of the value, 2^-32 of the row's largest weight where it is below
-    fp16's normal range) against held values rounded to fp16 (2^-11), and to
-    bf16 (2^-8) against the exact bf16 new values; fp32 sums of n terms add
-    n u.  The result is rounded to bf16: 2^-8."""
+    fp16's normal range) against held values rounded to fp16 (2^-11), and as
+    the sum of two bf16 values (2^-8 of 2^-8 at most) against the exact bf16
+    new values; fp32 sums of n terms add n u.  The result is rounded to bf16: 2^-8."""
     has = k_new is not None  # else the held tokens alone are attended
     q, kn, vn = (x.float().numpy().astype(np.float64) for x in (q, k_new if has else q[:, :0], v_new if has else q[:, :0]))
     nl, T = q.shape[:2]
@@ -101,7 +101,7 @@ def reference(st: dict, w: W.Workload, q, k_new, v_new, new_lens, acc_lens=None,
                     v = np.concatenate([v, vn[li, t0:t0 + n, h]])
                     ka = np.concatenate([ka, np.abs(kn[li, t0:t0 + n, h])])
                 seen = np.concatenate([np.ones((n, m), bool), np.tril(np.ones((n, n), bool))[:, :f]], 1)
-                half = np.concatenate([np.full(m, 2.0 ** -10), np.full(f, 2.0 ** -8)])
+                half = np.concatenate([np.full(m, 2.0 ** -10), np.full(f, 2.0 ** -16)])
                 for g in range(G):
                     qh = q[li, t0:t0 + n, h * G + g]
                     if n == 0:

@@ -54,12 +54,12 @@ __device__ __forceinline__ int64_t block_sum(int64_t x, int64_t *sm) {
 
 // A list unit (l, k, h) of request list q: its index in the tables.
 __device__ __forceinline__ int64_t list_unit(const PageOpArgs &a, int64_t v, const int32_t *q, int32_t &k) {
-  const int32_t h = static_cast<int32_t>(v % a.Hkv);
-  const int64_t lk = v / a.Hkv;
-  k = static_cast<int32_t>(lk % a.n);
+  // v < 2^31: 32-bit divisions
+  const uint32_t lk = static_cast<uint32_t>(v) / a.Hkv, l = lk / a.n;
+  k = static_cast<int32_t>(lk - l * a.n);
   const int32_t r = __ldg(q + k);
   if (r < 0 || r >= a.R) return -1;
-  return ((lk / a.n) * a.R + r) * a.Hkv + h;
+  return (static_cast<int64_t>(l) * a.R + r) * a.Hkv + static_cast<int32_t>(static_cast<uint32_t>(v) - lk * a.Hkv);
 }
 
 // Pages of a unit from its header; -1 when the header contradicts itself.

@@ -7,8 +7,9 @@
 // A block takes 128 MT rows of one unit (MT = 1 or 2) and a contiguous range of the
 // unit's token tiles: 128 tokens of the high list, of the low list, or of the
 // request's new tokens.  Its roles, pipelined through mbarriers:
-//   dequant warps (8)  read the codes of a tile straight from the pages into
-//     registers, one tile ahead, and write two operands to shared memory: K as
+//   dequant warps (8)  copy the pages of a tile into shared memory by bulk
+//     copies, one tile ahead, read their codes into registers and write two
+//     operands to shared memory: K as
 //     the codes themselves in fp16, less the middle code (exact; scale and
 //     zero stay in fp32 and are applied to the logits), and V as
 //     fp16(fma(c, s, z)) -- every cached value is a multiple of 2^-24, so
@@ -53,6 +54,7 @@
 // rate a tile's products for both warpgroups take 2048.
 #include <algorithm>
 #include <cmath>
+#include <cstddef>
 
 #include "token_tiles.cuh"
 
@@ -76,7 +78,8 @@ struct __align__(1024) Smem {
   uint8_t v[2][kTileBytes];
   float s[kMeta][128], z[kMeta][128];  // per token: scale s and z + mid s, times scale log2 e
   uint8_t valid[kMeta][128];           // looked at only when a page id of the unit is bad
-  uint64_t qready, kfull[2], kempty[2], vfull[2], vempty[2], mfull[kMeta];
+  uint8_t raw[200 * 128];              // a tile's pages: codes, scales and zeros (200 bytes a token at most)
+  uint64_t rfull, rempty, qready, kfull[2], kempty[2], vfull[2], vempty[2], mfull[kMeta];
   uint64_t sfull[2], pready[2], odone[2], turn[2], done[2];
   uint32_t tmem;
   uint32_t qmax;  // largest finite |q| of the block's rows (bits)
@@ -86,6 +89,7 @@ struct __align__(1024) Smem {
 template <int MT>
 constexpr size_t smem_bytes() { return sizeof(Smem<MT>) + 1024; }
 static_assert(smem_bytes<2>() <= 227 * 1024, "shared memory");
+static_assert(offsetof(Smem<1>, raw) % 16 == 0 && offsetof(Smem<2>, raw) % 16 == 0, "bulk copies");
 
 // ------------------------------------------------------------ softmax warps --
 
@@ -158,6 +162,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     mbar_init(&sm.qready, kSoftWarps);
+    mbar_init(&sm.rfull, kDeqWarps);
+    mbar_init(&sm.rempty, kDeqWarps);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.kfull[i], kDeqWarps);
       mbar_init(&sm.kempty[i], MT);
@@ -447,31 +453,90 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ================= dequantising warps
     const int dt = tid - 32 * kSoftWarps;
     const PageGeom g = page_geom(SC, a.P);
-    DeqCtx d{&a, x, &sm.u, 0xffffffffu / a.P + 1, 0xffffffffu / (2 * a.P) + 1, static_cast<int32_t>(g.bytes),
-             static_cast<uint32_t>(g.vbase), static_cast<uint32_t>(g.meta), dt >> 2, dt & 3, (dt & 3) >> 1, {}};
+    DeqCtx d{&a, x, dt >> 2, dt & 3, ((dt & 3) >> 1) ^ (__popc(dt >> 2 & 7) & 1), {}};
 #pragma unroll
     for (int i = 0; i < 4; ++i) d.off[i] = group_at(d.tk, 4 * d.c + (i ^ (2 * d.hs)));
     const float f = a.scale * kLog2e * pow2f(-e);
     Held<2> hd;
-    Where<2> w0, w1;  // the tile whose codes are loaded, the next one
     bool ok = true;
-    auto load = [&](const Tile &t, const Where<2> &w, bool k, bool v) {
-      if (t.kind == 0) fetch<KH, VH>(d, w, hd, k, v);
-      else if (t.kind == 1) fetch<KH / 2, VH / 2>(d, w, hd, k, v);
+    const int32_t *const fwd = a.fwd + *const_cast<volatile int64_t *>(&sm.u) * a.pmax;
+    // The pages of a tile: this warp copies those numbered warp, warp + 8, ...,
+    // a lane each (pages of two tokens: 65 in a tile); `page` is the lane's id.
+    int32_t page = -1, k0 = 0, pages = 0;
+    Tile tn{};
+    auto ahead = [&](int32_t j) {
+      tn = tile_at(ts, x, fresh, j0 + j);
+      if (tn.kind == 2) return;
+      const int32_t per = tn.kind == 0 ? a.P : 2 * a.P, k = (warp - kSoftWarps) + kDeqWarps * lane;
+      k0 = tn.t0 / per;
+      pages = (tn.t0 + tn.n - 1) / per - k0 + 1;
+      page = k < pages ? __ldg(fwd + (tn.kind == 0 ? 0 : x.p_hi) + k0 + k) : -1;
     };
-    Tile t{}, tn{};
+    auto copy = [&] {  // tile tn into the raw tile
+      uint32_t sum = 0;
+      const bool high = tn.kind == 0;
+      const int32_t per = high ? a.P : 2 * a.P, k = (warp - kSoftWarps) + kDeqWarps * lane;
+      const RawForm rf = high ? raw_form<KH, VH>(a.P, true) : raw_form<KH / 2, VH / 2>(a.P, false);
+      const int32_t kb = high ? 16 * KH : 8 * KH, vb = high ? 16 * VH : 8 * VH;
+      const int32_t p0 = (k0 + k) * per, first = max(tn.t0 - p0, 0), to = p0 + first - tn.t0;
+      const int32_t n_in = min(p0 + per, tn.t0 + tn.n) - p0 - first, md = 8 * ((n_in + 1) & ~1);
+      const bool mine = tn.kind != 2 && k < pages && page >= 0 && page < a.F;  // else the tokens are masked (sm.bad)
+      if (mine) sum = rf.whole ? rf.stride : n_in * (kb + vb) + md;
+      sum = __reduce_add_sync(kFull, sum);
+      if (lane == 0) mbar_expect_tx(&sm.rfull, sum);  // before any copy can land
+      __syncwarp();
+      if (mine) {
+        const uint8_t *src = a.pages + page * g.bytes;
+        if (rf.whole) {
+          copy_bulk(sm.raw + (to >> rf.lg) * rf.stride, src, rf.stride, &sm.rfull);
+        } else {
+          copy_bulk(sm.raw + to * kb, src + first * kb, n_in * kb, &sm.rfull);
+          copy_bulk(sm.raw + rf.vb + to * vb, src + g.vbase + first * vb, n_in * vb, &sm.rfull);
+          copy_bulk(sm.raw + rf.mo + to * 8, src + g.meta + 8 * first, md, &sm.rfull);
+        }
+      }
+      __syncwarp();
+    };
     if (n > 0) {
-      t = tile_at(ts, x, fresh, j0);
-      locate(d, t, w0);
-      load(t, w0, true, true);
+      ahead(0);
+      copy();
     }
-    if (n > 1) {
-      tn = tile_at(ts, x, fresh, j0 + 1);
-      locate(d, tn, w1);
-    }
+    int32_t last = 0;  // the tile copied last
 #pragma unroll 1
     for (int32_t j = 0; j < n; ++j) {
       const int b = j & 1, ms = j % kMeta;
+      const Tile t = tn;
+      if (j + 1 < n) ahead(j + 1);
+      if (!(ok = warp_wait(&sm.rfull, j & 1u))) break;
+      if (t.kind != 2) {  // into registers, so that the next tile's copies can go ahead
+        const bool high = t.kind == 0;
+        const RawForm rf = high ? raw_form<KH, VH>(a.P, true) : raw_form<KH / 2, VH / 2>(a.P, false);
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          const int row = d.tk + 64 * p;
+          bool have = row < t.n;
+          if (__builtin_expect(sm.bad, 0) && have) {
+            const int32_t id = __ldg(fwd + (high ? 0 : x.p_hi) + (t.t0 + row) / (high ? a.P : 2 * a.P));
+            have = id >= 0 && id < a.F;
+          }
+          hd.ok[p] = have;
+          hd.md[p] = have ? read_md(rf, sm.raw, row) : make_uint2(0, 0);
+        }
+        if (high) {
+          read_raw<KH>(d, rf, sm.raw, hd.k);
+          read_raw<VH>(d, rf, sm.raw + rf.vb, hd.v);
+        } else {
+          read_raw<KH / 2>(d, rf, sm.raw, hd.k);
+          read_raw<VH / 2>(d, rf, sm.raw + rf.vb, hd.v);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.rempty);
+      if (j + 1 < n) {
+        if (!(ok = warp_wait(&sm.rempty, j & 1u))) break;
+        copy();
+        last = j + 1;
+      }
       if (j >= 2 && !(ok = warp_wait(&sm.kempty[b], ((j >> 1) - 1) & 1u))) break;
       if (t.kind == 0) convert_k<KH>(d, hd, sm, sm.k[b], ms, f);
       else if (t.kind == 1) convert_k<KH / 2>(d, hd, sm, sm.k[b], ms, f);
@@ -482,26 +547,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(&sm.kfull[b]);
         mbar_arrive(&sm.mfull[ms]);
       }
-      const Tile cur = t;
-      if (j + 1 < n) {
-        t = tn;
-        w0 = w1;
-        load(t, w0, true, false);
-      }
       if (j >= 2 && !(ok = warp_wait(&sm.vempty[b], ((j >> 1) - 1) & 1u))) break;
-      if (cur.kind == 0) convert_v<VH>(d, hd, sm.v[b]);
-      else if (cur.kind == 1) convert_v<VH / 2>(d, hd, sm.v[b]);
-      else new_v<2>(d, cur, *const_cast<volatile int64_t *>(&sm.tok0), h, sm.v[b]);
+      if (t.kind == 0) convert_v<VH>(d, hd, sm.v[b]);
+      else if (t.kind == 1) convert_v<VH / 2>(d, hd, sm.v[b]);
+      else new_v<2>(d, t, *const_cast<volatile int64_t *>(&sm.tok0), h, sm.v[b]);
       fence_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.vfull[b]);
-      if (j + 1 < n) load(t, w0, false, true);
-      if (j + 2 < n) {
-        tn = tile_at(ts, x, fresh, j0 + j + 2);
-        locate(d, tn, w1);
-      }
     }
-    (void)ok;
+    // after an abort: this warp's last copies land before the block leaves (bounded)
+    if (!ok) mbar_wait(&sm.rfull, last & 1u, nullptr);
   }
   __syncwarp();
   fence_before();

@@ -96,44 +96,6 @@ __device__ __forceinline__ bool meet(bool p) {
   return r != 0;
 }
 
-// How a raw tile lies in shared memory: token i is slot i mod 2^lg of "page"
-// i >> lg, pages `stride` bytes apart, with V codes and scales at vb and mo.
-// Where pages divide a tile those are the pages themselves, as they lie in
-// memory up to their last used scale: one copy a page.  Otherwise it is one
-// page of 128 slots, which three copies per page and tile put together.
-struct RawForm {
-  int32_t lg, stride, vb, mo;
-  bool whole;
-};
-
-template <int KW, int VW>
-__device__ __forceinline__ RawForm raw_form(int32_t P, bool high) {
-  const int32_t per = high ? P : 2 * P;
-  const bool whole = per <= 128 && (per & (per - 1)) == 0;
-  const int32_t n = whole ? per : 128;
-  // per W-bit slots take 16 W per bytes, scales 8 per
-  return RawForm{31 - __clz(n), n * (16 * (KW + VW) + 8), n * 16 * KW, n * 16 * (KW + VW), whole};
-}
-
-// The two 16-channel halves of each of the thread's tokens, in its order.
-template <int W>
-__device__ __forceinline__ void read_raw(const DeqCtx &d, const RawForm &f, const uint8_t *raw, uint32_t (&x)[kNP][2][4]) {
-#pragma unroll
-  for (int p = 0; p < kNP; ++p) {
-    const int i = d.tk + 128 / kNP * p, slot = i & ((1 << f.lg) - 1);
-    const uint8_t *row = raw + (i >> f.lg) * f.stride + slot * (16 * W);
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const uint8_t *src = row + 2 * W * (2 * d.c + (d.hs ^ e));
-      read16<W>(x[p][e], src);
-    }
-  }
-}
-
-__device__ __forceinline__ uint2 read_md(const RawForm &f, const uint8_t *raw, int i) {
-  return *reinterpret_cast<const uint2 *>(raw + (i >> f.lg) * f.stride + f.mo + 8 * (i & ((1 << f.lg) - 1)));
-}
-
 // Pages [k0, k0 + n) of a unit's list that a tile lies in: fwd, their ids; id,
 // the lane's of the first 32.
 struct PageRange {
@@ -480,9 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp < kMmaWarp) {
     // ================= convert warps
     const int dt = tid - 32 * kSoftWarps;
-    // which half a token's threads take first alternates, so that the reads of
-    // neighbouring raw rows meet different banks as well as the writes
-    DeqCtx d{&a, x, nullptr, 0, 0, 0, 0, 0, dt >> 2, dt & 3, ((dt & 3) >> 1) ^ (__popc(dt >> 2 & 7) & 1), {}};
+    DeqCtx d{&a, x, dt >> 2, dt & 3, ((dt & 3) >> 1) ^ (__popc(dt >> 2 & 7) & 1), {}};
 #pragma unroll
     for (int i = 0; i < 4; ++i) d.off[i] = group_at(d.tk, 4 * d.c + (i ^ (2 * d.hs)));
     const float f = a.scale * kLog2e * pow2f(-e);

@@ -371,22 +371,6 @@ __device__ __forceinline__ void group_codes(uint32_t w0, uint32_t w1, __half2 (&
   }
 }
 
-// A thread's 16 channels of one token (two groups): 2 W bytes of codes.
-template <int W>
-__device__ __forceinline__ void load16(uint32_t (&x)[4], const uint8_t *p) {
-  if constexpr (W == 8) {
-    const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p));
-    x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
-  } else if constexpr (W == 4) {
-    const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p));
-    x[0] = v.x, x[1] = v.y;
-  } else if constexpr (W == 2) {
-    x[0] = __ldg(reinterpret_cast<const uint32_t *>(p));
-  } else {
-    x[0] = __ldg(reinterpret_cast<const uint16_t *>(p));
-  }
-}
-
 // Words of group g (0 or 1) of those 16 channels.
 template <int W>
 __device__ __forceinline__ void group_of(const uint32_t (&x)[4], int g, uint32_t &w0, uint32_t &w1) {

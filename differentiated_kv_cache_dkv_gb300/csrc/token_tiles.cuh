@@ -55,17 +55,13 @@ __device__ __forceinline__ Tile tile_at(const Tiles &ts, const Unit &x, int32_t 
 // ------------------------------------------------------- dequantising warps --
 //
 // Four threads a token, 32 channels each, NP tokens a thread: tk + p 128 / NP.
-// The thread of channels 64 .. takes its two 16-channel halves in the other
-// order, so that the eight threads of two neighbouring rows always write eight
-// different 16-byte chunks of the swizzled rows.  (u, m1 .. meta: for locate and
-// fetch, where the codes come straight from the pages.)
+// Which of its two 16-channel halves a thread takes first alternates with the
+// channels and the rows (hs), so that neighbouring threads read different banks
+// of the raw rows and the eight threads of two neighbouring rows always write
+// eight different 16-byte chunks of the swizzled rows.
 struct DeqCtx {
   const ExtendArgs *a;
   Unit x;
-  const volatile int64_t *u;  // x.u in shared memory
-  uint32_t m1, m2;  // split() by P and 2 P
-  int32_t bytes;
-  uint32_t vbase, meta;
   int tk, c, hs;    // token, quarter of the channels, which half comes first
   uint32_t off[4];  // operand-tile offsets of the thread's four groups (token tk)
 };
@@ -76,51 +72,6 @@ struct Held {
   uint2 md[NP];
   bool ok[NP];
 };
-
-// Where the thread's tokens of a tile lie: page ids (-1: no token) and slots.
-template <int NP>
-struct Where {
-  int32_t id[NP], slot[NP];
-};
-
-template <int NP>
-__device__ __forceinline__ void locate(const DeqCtx &d, const Tile &t, Where<NP> &w) {
-  if (t.kind == 2) return;
-  const bool high = t.kind == 0;
-  const int32_t per = high ? d.a->P : 2 * d.a->P, first = high ? 0 : d.x.p_hi;
-  const uint32_t M = high ? d.m1 : d.m2;
-#pragma unroll
-  for (int p = 0; p < NP; ++p) {
-    const int32_t i = d.tk + 128 / NP * p;
-    int32_t k;
-    split(t.t0 + i, per, M, k, w.slot[p]);
-    w.id[p] = i < t.n ? __ldg(d.a->fwd + *d.u * d.a->pmax + first + k) : -1;
-  }
-}
-
-// Codes of the thread's tokens: its two 16-channel halves of a W-bit row lie
-// 2 W (8 slot + 2 c + half) bytes into the rows.
-template <int KW, int VW, int NP>
-__device__ __forceinline__ void fetch(const DeqCtx &d, const Where<NP> &w, Held<NP> &h, bool k, bool v) {
-#pragma unroll
-  for (int p = 0; p < NP; ++p) {
-    const bool ok = w.id[p] >= 0 && w.id[p] < d.a->F;
-    // page 0 stands in for none: masked, or its scale is 0
-    const uint8_t *pg = d.a->pages + static_cast<int64_t>(ok ? w.id[p] : 0) * d.bytes;
-    const uint32_t u0 = 8 * w.slot[p] + 2 * d.c + d.hs, u1 = u0 ^ 1u;
-    if (k) {
-      load16<KW>(h.k[p][0], pg + 2 * KW * u0);
-      load16<KW>(h.k[p][1], pg + 2 * KW * u1);
-    }
-    if (v) {
-      load16<VW>(h.v[p][0], pg + (d.vbase + 2 * VW * u0));
-      load16<VW>(h.v[p][1], pg + (d.vbase + 2 * VW * u1));
-      h.md[p] = __ldg(reinterpret_cast<const uint2 *>(pg + (d.meta + 8u * w.slot[p])));
-      h.ok[p] = ok;
-      if (!ok) h.md[p] = make_uint2(0, 0);
-    }
-  }
-}
 
 // Sixteen W-bit codes of a row in shared memory.
 template <int W>
@@ -136,6 +87,44 @@ __device__ __forceinline__ void read16(uint32_t (&x)[4], const uint8_t *src) {
   } else {
     x[0] = *reinterpret_cast<const uint16_t *>(src);
   }
+}
+
+// How a raw tile lies in shared memory: token i is slot i mod 2^lg of "page"
+// i >> lg, pages `stride` bytes apart, with V codes and scales at vb and mo.
+// Where pages divide a tile those are the pages themselves, as they lie in
+// memory up to their last used scale: one copy a page.  Otherwise it is one
+// page of 128 slots, which three copies per page and tile put together.
+struct RawForm {
+  int32_t lg, stride, vb, mo;
+  bool whole;
+};
+
+template <int KW, int VW>
+__device__ __forceinline__ RawForm raw_form(int32_t P, bool high) {
+  const int32_t per = high ? P : 2 * P;
+  const bool whole = per <= 128 && (per & (per - 1)) == 0;
+  const int32_t n = whole ? per : 128;
+  // per W-bit slots take 16 W per bytes, scales 8 per
+  return RawForm{31 - __clz(n), n * (16 * (KW + VW) + 8), n * 16 * KW, n * 16 * (KW + VW), whole};
+}
+
+// The two 16-channel halves of each of the thread's tokens, in its order.
+template <int W, int NP>
+__device__ __forceinline__ void read_raw(const DeqCtx &d, const RawForm &f, const uint8_t *raw, uint32_t (&x)[NP][2][4]) {
+#pragma unroll
+  for (int p = 0; p < NP; ++p) {
+    const int i = d.tk + 128 / NP * p, slot = i & ((1 << f.lg) - 1);
+    const uint8_t *row = raw + (i >> f.lg) * f.stride + slot * (16 * W);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const uint8_t *src = row + 2 * W * (2 * d.c + (d.hs ^ e));
+      read16<W>(x[p][e], src);
+    }
+  }
+}
+
+__device__ __forceinline__ uint2 read_md(const RawForm &f, const uint8_t *raw, int i) {
+  return *reinterpret_cast<const uint2 *>(raw + (i >> f.lg) * f.stride + f.mo + 8 * (i & ((1 << f.lg) - 1)));
 }
 
 __device__ __forceinline__ void put(uint8_t *tile, uint32_t at, const __half2 (&o)[4]) {

@@ -45,8 +45,8 @@
 // Units with at most 32 rows have a kernel of their own (extend_few.cu).
 //
 // Measured (32 heads over 8, 4 requests of 1024 new tokens over 16384 held, half
-// of those in the high list, 39% in the low one): 1571 us, 1.01 TFLOP, 644 TFLOP/s,
-// 33% of the measured bf16 rate.  The tensor pipe is busy for 30% of the
+// of those in the high list, 39% in the low one): 1518 us, 1.01 TFLOP, 667 TFLOP/s,
+// 35% of the measured bf16 rate.  The tensor pipe is busy for 30% of the
 // cycles: a warpgroup's tile takes 6640, of which its softmax 3730 (932 for 32
 // columns, one warp a scheduler: the latencies of the tensor-memory load, of
 // the scales' broadcast reads and of the exponentials follow one another) and
@@ -131,7 +131,7 @@ __device__ __forceinline__ void channel_order(const uint32_t *r, float *x) {
 
 // The first `full` blocks do a row tile each, the others one of `splits` parts
 // of a row tile's token tiles.
-template <int SC, int MT, bool kSorted>
+template <int SC, int MT>
 __global__ void __launch_bounds__(kThreads, 1)
     k_extend(const __grid_constant__ ExtendArgs a, int32_t row_tiles, uint32_t full, int32_t splits, ExtendPartial part) {
   constexpr int KH = scheme_kh(SC), VH = scheme_vh(SC);
@@ -139,14 +139,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   // aligned by an offset, not by an integer address: the compiler then knows that these are shared accesses
   Smem<MT> &sm = *reinterpret_cast<Smem<MT> *>(smem_raw + (-saddr(smem_raw) & 1023u));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  // in the order (request, the longest first when sorted; layer, head; row tile; part)
+  // in the order (request, the longest first; layer, head; row tile; part): the
+  // blocks of short requests fill the gaps that those of long ones leave (16
+  // ragged requests: 188 -> 164 us)
   const bool whole = blockIdx.x < full;
   const uint32_t pb = blockIdx.x - full, ur = whole ? blockIdx.x : full + pb / splits, ui = ur / row_tiles;
   const uint32_t lh = static_cast<uint32_t>(a.n_layers) * a.Hkv, k = ui / lh, rest = ui - k * lh;
   const int32_t sp = whole ? 0 : static_cast<int32_t>(pb % splits), ns = whole ? 1 : splits;
   const int32_t rt = static_cast<int32_t>(ur - ui * row_tiles);
   const int32_t li = static_cast<int32_t>(rest / a.Hkv), h = static_cast<int32_t>(rest - li * a.Hkv);
-  const int32_t r = kSorted ? longest_first(a, static_cast<int32_t>(k)) : static_cast<int32_t>(k);
+  const int32_t r = longest_first(a, static_cast<int32_t>(k));
   int64_t before;
   if (!lens_valid(a, r, before)) return;
   const int32_t rows = __ldg(a.new_lens + r) * a.G, row0 = rt * (128 * MT);
@@ -435,7 +437,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             dst[i] = make_uint4(bf16x2_rn(f[8 * i] * inv, f[8 * i + 1] * inv), bf16x2_rn(f[8 * i + 2] * inv, f[8 * i + 3] * inv),
-                                bf16x2_rn(f[8 * i + 4] * inv, f[8 * i + 5] * inv), bf16x2_rn(f[8 * i + 6] * inv, f[8 * i + 7] * inv));
+                                bf16x2_rn(f[8 * i + 4] * inv, f[8 * i + 5] * inv),
+                                bf16x2_rn(f[8 * i + 6] * inv, f[8 * i + 7] * inv));
         } else if (t > 0) {
           float4 *dst = reinterpret_cast<float4 *>(part.o + slot * 128 + 32 * c);
 #pragma unroll
@@ -627,24 +630,18 @@ __global__ void __launch_bounds__(256) k_extend_merge(ExtendArgs a, int32_t part
   if (a.lse && lane == 0) a.lse[at] = l == 0.0f ? -INFINITY : (M + log2f(l)) * 0.693147180559945309f;
 }
 
-template <int SC, int MT, bool kSorted>
+template <int SC, int MT>
 cudaError_t launch_kernel(const ExtendArgs &a, const ExtendPlan &p, const ExtendPartial &part, cudaStream_t s) {
   const int smem = static_cast<int>(smem_bytes<MT>());
-  if (cudaError_t e = cudaFuncSetAttribute(k_extend<SC, MT, kSorted>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem))
-    return e;
-  k_extend<SC, MT, kSorted><<<static_cast<unsigned>(p.blocks), kThreads, smem, s>>>(a, p.row_tiles,
-                                                                                   static_cast<uint32_t>(p.full), p.splits, part);
+  if (cudaError_t e = cudaFuncSetAttribute(k_extend<SC, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) return e;
+  k_extend<SC, MT><<<static_cast<unsigned>(p.blocks), kThreads, smem, s>>>(a, p.row_tiles, static_cast<uint32_t>(p.full),
+                                                                          p.splits, part);
   return cudaGetLastError();
 }
 
-// Sorting lets the blocks of short requests fill the gaps that those of long
-// ones leave (16 ragged requests: 188 -> 164 us); it costs registers in the
-// loop (four equal requests: 1626 -> 1668 us), so a few requests go unsorted.
-constexpr int32_t kUnsorted = 4;
 template <int SC>
 cudaError_t launch(const ExtendArgs &a, const ExtendPlan &p, const ExtendPartial &part, cudaStream_t s) {
-  if (p.mt == 1) return launch_kernel<SC, 1, true>(a, p, part, s);
-  return a.R > kUnsorted ? launch_kernel<SC, 2, true>(a, p, part, s) : launch_kernel<SC, 2, false>(a, p, part, s);
+  return p.mt == 1 ? launch_kernel<SC, 1>(a, p, part, s) : launch_kernel<SC, 2>(a, p, part, s);
 }
 
 }  // namespace
@@ -656,6 +653,7 @@ cudaError_t launch(const ExtendArgs &a, const ExtendPlan &p, const ExtendPartial
 // to three waves: 42, 72, 94 and 116).  Blocks of 128 or 256 rows: one wave (a
 // request with 512 new tokens over 8192: 138 / 155 / 162 us).
 constexpr int64_t kFewBlocks = 152 * 2;
+constexpr int32_t kFewRequests = 4;
 
 ExtendPlan extend_plan(int64_t units, int32_t R, int32_t max_new, int32_t G, int32_t cap, int64_t rows) {
   ExtendPlan p{};
@@ -665,16 +663,19 @@ ExtendPlan extend_plan(int64_t units, int32_t R, int32_t max_new, int32_t G, int
   if (most <= 32) {
     p.mt = 0;
     p.row_tiles = 1;
-    p.splits = static_cast<int32_t>(std::clamp<int64_t>(kFewBlocks / std::max<int64_t>(units, 1), 1, std::max<int64_t>(tiles / 6, 1)));
+    p.splits = static_cast<int32_t>(
+        std::clamp<int64_t>(kFewBlocks / std::max<int64_t>(units, 1), 1, std::max<int64_t>(tiles / 6, 1)));
   } else {
     p.mt = most > 128 ? 2 : 1;
     p.row_tiles = static_cast<int32_t>((most + 128 * p.mt - 1) / (128 * p.mt));
     const int64_t items = units * p.row_tiles, rest = items % 152;
     if (items < 152 || p.mt == 1) {
       p.splits = static_cast<int32_t>(std::clamp<int64_t>(152 / std::max<int64_t>(items, 1), 1, std::max<int64_t>(tiles / 4, 1)));
-    } else if (R <= kUnsorted && rest > 0 && items < 16 * 152) {
+    } else if (R <= kFewRequests && rest > 0 && items < 16 * 152) {
       // the last, incomplete wave in parts, as many as fill it (a chunk of
-      // 512 row tiles: 4 waves of 1, or 3 and one of 1/2; 1626 -> 1513 us)
+      // 512 row tiles: 4 waves of 1, or 3 and one of 1/2; 1626 -> 1513 us).
+      // Many requests are ragged, and the order fills the last wave instead (16
+      // requests: 165 us without parts, 180 with them)
       p.splits = static_cast<int32_t>(std::clamp<int64_t>(152 / rest, 1, std::min<int64_t>(8, std::max<int64_t>(tiles / 4, 1))));
       if (p.splits > 1) p.full = items - rest;
     }

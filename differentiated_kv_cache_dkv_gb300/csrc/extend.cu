@@ -456,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ================= dequantising warps
     const int dt = tid - 32 * kSoftWarps;
     const PageGeom g = page_geom(SC, a.P);
-    DeqCtx d{&a, x, dt >> 2, dt & 3, ((dt & 3) >> 1) ^ (__popc(dt >> 2 & 7) & 1), {}};
+    DeqCtx d{&a, dt >> 2, dt & 3, ((dt & 3) >> 1) ^ (__popc(dt >> 2 & 7) & 1), {}};
 #pragma unroll
     for (int i = 0; i < 4; ++i) d.off[i] = group_at(d.tk, 4 * d.c + (i ^ (2 * d.hs)));
     const float f = a.scale * kLog2e * pow2f(-e);

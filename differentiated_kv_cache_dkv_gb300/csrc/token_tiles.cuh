@@ -61,7 +61,6 @@ __device__ __forceinline__ Tile tile_at(const Tiles &ts, const Unit &x, int32_t 
 // eight different 16-byte chunks of the swizzled rows.
 struct DeqCtx {
   const ExtendArgs *a;
-  Unit x;
   int tk, c, hs;    // token, quarter of the channels, which half comes first
   uint32_t off[4];  // operand-tile offsets of the thread's four groups (token tk)
 };

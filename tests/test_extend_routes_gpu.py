@@ -64,7 +64,7 @@ def test_few_rows_of_a_range_of_layers():
 
 
 @pytest.mark.parametrize("max_new,G", [(8, 1), (8, 12), (9, 16), (16, 8), (17, 4), (32, 5), (33, 2), (64, 3), (65, 1),
-                                       (70, 4), (129, 2), (300, 1)])
+                                       (70, 4), (129, 2), (300, 1), (1, 33), (2, 40), (1, 64)])
 def test_columns_of_a_head(max_new, G):
     w = W.small("columns", L=1, lens=[300, 130], Hq=2 * G, Hkv=2)
     _check(w, [max_new, (max_new + 1) // 2], max_new, acc=[max_new - max_new // 3, (max_new + 1) // 2])

@@ -512,18 +512,55 @@ __device__ __forceinline__ void defrag_move(const PageOpArgs &a) {
 
 // ----------------------------------------------------------------- launches --
 
+// A later step's blocks may start while the step before still runs (all of its
+// blocks have begun then) and wait here for its end: launch latency is hidden,
+// the order kept.
+__device__ __forceinline__ void after_step_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_step_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 template <bool kFork>
-__global__ void __launch_bounds__(kThreads) k_list_plan(const __grid_constant__ PageOpArgs a) { list_plan<kFork>(a); }
+__global__ void __launch_bounds__(kThreads) k_list_plan(const __grid_constant__ PageOpArgs a) {
+  let_next_step_start();
+  list_plan<kFork>(a);
+}
 template <bool kFork>
 __global__ void __launch_bounds__(kThreads) k_list_place(const __grid_constant__ PageOpArgs a, int32_t nparts) {
+  let_next_step_start();
+  after_step_before();
   list_place<kFork>(a, nparts);
 }
-__global__ void __launch_bounds__(kThreads) k_fork_copy(const __grid_constant__ PageOpArgs a) { fork_copy(a); }
-__global__ void __launch_bounds__(kThreads) k_defrag_plan(const __grid_constant__ PageOpArgs a) { defrag_plan(a); }
+__global__ void __launch_bounds__(kThreads) k_fork_copy(const __grid_constant__ PageOpArgs a) {
+  after_step_before();
+  fork_copy(a);
+}
+__global__ void __launch_bounds__(kThreads) k_defrag_plan(const __grid_constant__ PageOpArgs a) {
+  let_next_step_start();
+  defrag_plan(a);
+}
 __global__ void __launch_bounds__(kThreads) k_defrag_list(const __grid_constant__ PageOpArgs a, int32_t nparts) {
+  let_next_step_start();
+  after_step_before();
   defrag_list(a, nparts);
 }
-__global__ void __launch_bounds__(kThreads) k_defrag_move(const __grid_constant__ PageOpArgs a) { defrag_move(a); }
+__global__ void __launch_bounds__(kThreads) k_defrag_move(const __grid_constant__ PageOpArgs a) {
+  after_step_before();
+  defrag_move(a);
+}
+
+// A launch that may overlap the end of the one before it (above).
+template <class... P, class... A>
+cudaError_t next_step(void (*k)(P...), int grid, cudaStream_t s, A... args) {
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3(grid);
+  c.blockDim = dim3(kThreads);
+  c.stream = s;
+  c.attrs = &attr;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, k, static_cast<P>(args)...);
+}
 
 // The steps of a small call in one launch: a cluster of kCluster blocks, whose
 // barrier (hardware's, so every block is there) stands for the launches' order.
@@ -572,10 +609,8 @@ cudaError_t launch_fork(const PageOpArgs &a, int sms, cudaStream_t s) {
   }
   k_list_plan<true><<<parts, kThreads, bits, s>>>(a);
   if (cudaError_t e = cudaGetLastError()) return e;
-  k_list_place<true><<<parts, kThreads, 0, s>>>(a, parts);
-  if (cudaError_t e = cudaGetLastError()) return e;
-  k_fork_copy<<<copy_grid(a.V * a.pmax + rows / 16 + 1, sms), kThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  if (cudaError_t e = next_step(k_list_place<true>, parts, s, a, parts)) return e;
+  return next_step(k_fork_copy, copy_grid(a.V * a.pmax + rows / 16 + 1, sms), s, a);
 }
 
 cudaError_t launch_release(const PageOpArgs &a, cudaStream_t s) {
@@ -587,8 +622,7 @@ cudaError_t launch_release(const PageOpArgs &a, cudaStream_t s) {
   }
   k_list_plan<false><<<parts, kThreads, bits, s>>>(a);
   if (cudaError_t e = cudaGetLastError()) return e;
-  k_list_place<false><<<parts, kThreads, 0, s>>>(a, parts);
-  return cudaGetLastError();
+  return next_step(k_list_place<false>, parts, s, a, parts);
 }
 
 cudaError_t launch_defrag(const PageOpArgs &a, int sms, cudaStream_t s) {
@@ -599,10 +633,8 @@ cudaError_t launch_defrag(const PageOpArgs &a, int sms, cudaStream_t s) {
   }
   k_defrag_plan<<<parts, kThreads, 0, s>>>(a);
   if (cudaError_t e = cudaGetLastError()) return e;
-  k_defrag_list<<<parts, kThreads, 0, s>>>(a, parts);
-  if (cudaError_t e = cudaGetLastError()) return e;
-  k_defrag_move<<<copy_grid(a.F, sms), kThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  if (cudaError_t e = next_step(k_defrag_list, parts, s, a, parts)) return e;
+  return next_step(k_defrag_move, copy_grid(a.F, sms), s, a);
 }
 
 }  // namespace dkv

@@ -45,7 +45,7 @@
 // Units with at most 32 rows have a kernel of their own (extend_few.cu).
 //
 // Measured (32 heads over 8, 4 requests of 1024 new tokens over 16384 held, half
-// of those in the high list, 39% in the low one): 1518 us, 1.01 TFLOP, 667 TFLOP/s,
+// of those in the high list, 39% in the low one): 1513 us, 1.01 TFLOP, 669 TFLOP/s,
 // 35% of the measured bf16 rate.  The tensor pipe is busy for 30% of the
 // cycles: a warpgroup's tile takes 6640, of which its softmax 3730 (932 for 32
 // columns, one warp a scheduler: the latencies of the tensor-memory load, of
@@ -135,6 +135,9 @@ template <int SC, int MT>
 __global__ void __launch_bounds__(kThreads, 1)
     k_extend(const __grid_constant__ ExtendArgs a, int32_t row_tiles, uint32_t full, int32_t splits, ExtendPartial part) {
   constexpr int KH = scheme_kh(SC), VH = scheme_vh(SC);
+  // with MT = 1 it costs more than it hides (16 new tokens over 16384: 41 us
+  // without, 47 with; drafts of two requests 23.6 with, 25.7 without)
+  if constexpr (MT == 2) let_merge_start();
   extern __shared__ unsigned char smem_raw[];
   // aligned by an offset, not by an integer address: the compiler then knows that these are shared accesses
   Smem<MT> &sm = *reinterpret_cast<Smem<MT> *>(smem_raw + (-saddr(smem_raw) & 1023u));
@@ -572,6 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Joins the partial results of a row: a warp per row, four channels a lane.
 __global__ void __launch_bounds__(256) k_extend_merge(ExtendArgs a, int32_t parts, ExtendPartial part) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are there
   __shared__ int32_t ok_s;
   if (threadIdx.x < 32) {  // the lengths were wrong: the attention wrote nothing
     int64_t t = 0;
@@ -701,8 +705,16 @@ cudaError_t launch_extend(const ExtendArgs &a, const ExtendPlan &p, void *ws, cu
   else
     e = a.scheme == 0 ? launch<0>(a, p, part, s) : a.scheme == 1 ? launch<1>(a, p, part, s) : launch<2>(a, p, part, s);
   if (e != cudaSuccess || p.parts == 0) return e;
-  k_extend_merge<<<static_cast<unsigned>((part.rows + 7) / 8), 256, 0, s>>>(a, p.parts, part);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3(static_cast<unsigned>((part.rows + 7) / 8));
+  c.blockDim = dim3(256);
+  c.stream = s;
+  c.attrs = &attr;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, k_extend_merge, a, p.parts, part);
 }
 
 }  // namespace dkv

@@ -155,6 +155,7 @@ template <int SC>
 __global__ void __launch_bounds__(kThreads, 1)
     k_extend_few(const __grid_constant__ ExtendArgs a, int32_t splits, ExtendPartial part) {
   constexpr int KH = scheme_kh(SC), VH = scheme_vh(SC);
+  let_merge_start();
   extern __shared__ __align__(16) unsigned char smem_raw[];
   Smem &sm = *reinterpret_cast<Smem *>(smem_raw + (-saddr(smem_raw) & 1023u));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;

@@ -19,10 +19,10 @@
 //   defrag   k_defrag_plan, k_defrag_list, k_defrag_move
 // Small calls run their steps in one launch (k_small).
 //
-// Measured: 8 prompts of 2048 .. 6144 tokens in 32 layers forked 525 us for
+// Measured: 8 prompts of 2048 .. 6144 tokens in 32 layers forked 521 us for
 // 2.88 GB, 5.5 TB/s, 82% of the measured copy rate (the copies alone 87%); a
-// 28-layer pool of 0.83 GB moved 162 us, 5.1 TB/s, 77%; 8 requests of 32 layers
-// released 29 us, for 400,000 pages whose entries lie scattered: the latency of
+// 28-layer pool of 0.83 GB moved 157 us, 5.3 TB/s, 79%; 8 requests of 32 layers
+// released 27 us, for 400,000 pages whose entries lie scattered: the latency of
 // two kernels' dependent loads and 1.2 million 32-byte sectors; the calls on
 // one small request 10 to 14 us of dependent loads.
 #include <cuda_runtime.h>

@@ -430,6 +430,10 @@ __device__ __forceinline__ bool lens_valid(const ExtendArgs &a, int32_t r, int64
   return ok_s != 0;
 }
 
+// Lets k_extend_merge's blocks start while the attention's last ones run (they
+// wait for its end: only the launch overlaps).
+__device__ __forceinline__ void let_merge_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // The request with the k-th most tokens, held and new (ties: the first one), or k itself when
 // there are more requests than that is worth.  Every block asks, all its threads.
 constexpr int32_t kOrder = 512;

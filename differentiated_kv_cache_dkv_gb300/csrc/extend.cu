@@ -319,6 +319,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float f = mn == m ? 1.0f : ex2(m - mn);  // a power of two, 0 at first
         l2 = f2_mul(l2, f2_pack(f, f));
         m = mn;
+        // P of earlier columns, and O where m has moved in this tile before, were
+        // stored by this thread: a load sees a store only after this wait
+        tmem_wait_st();
 #pragma unroll 1
         for (int i = 0; i < (tl.kind == 2 ? 2 * c : c); ++i) {
           const uint32_t at_p = ts_s + (tl.kind == 2 ? 16 * i : 32 * i);

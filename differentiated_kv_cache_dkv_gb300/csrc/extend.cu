@@ -32,9 +32,10 @@
 // the output's error where few tokens are attended).
 //
 // The maximum is lazy: P = 2^(y - m + 7) with a row's reference m (a whole
-// number, log2 units) that moves only when the sum of 32 weights passes 2^15,
-// so the usual chunk needs no maximum at all; then the softmax warp raises m to
-// the chunk's maximum and multiplies its row of O by the exact power of two.
+// number, log2 units) that is set by the first chunk of columns the row attends
+// and moves only when the sum of 32 weights passes 2^15, so the usual chunk needs
+// no maximum at all; then the softmax warp raises m to the chunk's maximum and
+// multiplies its row of O by the exact power of two.
 // Weights stay at or below 2^15 (fp16's largest is 2^16); those down to 2^-21
 // of the row's largest keep all 11 bits and 2^-32 is where they vanish.
 //
@@ -368,7 +369,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           float a0, a1;
           f2_unpack(sum[0], a0, a1);
           a0 += a1;
-          if (__builtin_expect(!__any_sync(kFull, a0 > kMost || (m == -INFINITY && a0 > 0.0f)), 1) || pass) break;
+          // A row's first columns set its reference whatever their sum: against 0
+          // the weights of logits below -87 are all zero.
+          if (__builtin_expect(!__any_sync(kFull, a0 > kMost || (m == -INFINITY && lim > 32 * c)), 1) || pass) break;
           uint32_t r[32];
           if (!(ok = raise(r, c))) break;
         }

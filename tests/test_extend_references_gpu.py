@@ -57,3 +57,29 @@ def test_logits_that_grow_from_one_piece_of_a_tile_to_the_next(rows, scheme, lis
     """6.5 more every 32 tokens: the references move several times in a tile,
     over weights and outputs that are already there."""
     _check(NEW[rows], lambda t: 6.5 * (t // 32), lambda t: 6.5 * (t // 32 + 4), scheme, lists, f"{rows} {lists}")
+
+
+@pytest.mark.parametrize("with_new", [False, True])
+@pytest.mark.parametrize("lists", list(LISTS))
+@pytest.mark.parametrize("level", [-100.0, -1000.0])
+@pytest.mark.parametrize("rows", list(NEW))
+def test_logits_that_are_all_far_below_zero(rows, level, lists, with_new):
+    """Keys with a common part against queries: every logit of every row lies
+    below the smallest weight against 0, and the softmax is an ordinary one."""
+    _check(NEW[rows], lambda t: level, (lambda t: level) if with_new else None, 0, lists, f"{rows} {level}")
+
+
+@pytest.mark.parametrize("rows", list(NEW))
+def test_first_tokens_below_the_smallest_weight_and_the_rest_above(rows):
+    """Three quarters of the context at -92, the rest at -84: log2 units -132.7
+    and -121.2 around the -126 below which a weight against 0 is none."""
+    _check(NEW[rows], lambda t: -92.0 if t < 225 else -84.0, None, what=rows)
+    _check(NEW[rows], lambda t: -87.6 if t < 225 else -87.0, None, what=rows)
+
+
+@pytest.mark.parametrize("with_new", [False, True])
+@pytest.mark.parametrize("rows", list(NEW))
+def test_first_piece_below_and_the_first_tile_below(rows, with_new):
+    for edge in (32, 128):
+        _check(NEW[rows], lambda t: -120.0 if t < edge else -88.0, (lambda t: -110.0 + t % 7) if with_new else None,
+               what=f"{rows} {edge}")

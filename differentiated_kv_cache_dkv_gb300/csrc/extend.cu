@@ -23,9 +23,10 @@
 //     issuing warp would be the seventeenth and cost every thread a quarter of
 //     its registers.
 // The block's rows of Q are scaled by one power of two that puts their largest
-// finite value into [2^14, 2^15) (the tokens' scales undo it): a value 28
-// binades below it still has all its bits in fp16, so q . c is exact up to the
-// fp32 accumulation.
+// finite value into [2^14, 2^15) (the tokens' scales undo it), and a row whose
+// own largest lies 2^12 and more below by a further one of its own (row_shift):
+// values 19 binades below a row's largest still have all their bits in fp16, so
+// q . c is exact up to the fp32 accumulation, whatever the rows beside it are.
 // New tokens: K is scaled per token the same way; V stays the bf16 it is, and
 // that product takes P as the sum of two bf16 values in two products (both
 // operands of one MMA have one type; one bf16 value alone showed as a third of
@@ -84,6 +85,7 @@ struct __align__(1024) Smem {
   uint64_t sfull[2], pready[2], odone[2], turn[2], done[2];
   uint32_t tmem;
   uint32_t qmax;  // largest finite |q| of the block's rows (bits)
+  float w[256];   // 2^-d of the softmax threads' rows (row_shift)
   int32_t abort, bad;
   int64_t u, tok0;  // unit and first new token, for the conversion (which has no registers for them)
 };
@@ -194,10 +196,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   fence_after();
   const uint32_t tmem = sm.tmem;
+  uint32_t qbits = 0;
   if (warp < kSoftWarps) {
     const int32_t grow = row0 + (MT == 2 ? tid : tid & 127);
-    const uint32_t b = grow < rows ? row_max(a.q + ((tok0 + grow / a.G) * a.Hq + h * a.G + grow % a.G) * 128) : 0;
-    const uint32_t w = __reduce_max_sync(kFull, b);
+    qbits = grow < rows ? row_max(a.q + ((tok0 + grow / a.G) * a.Hq + h * a.G + grow % a.G) * 128) : 0;
+    const uint32_t w = __reduce_max_sync(kFull, qbits);
     if (lane == 0 && w) atomicMax(&sm.qmax, w);
   }
   // a page id out of range anywhere in the unit: logits are masked token by token
@@ -209,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   __syncthreads();
-  const int e = lift_exponent(sm.qmax);
+  const int e = block_exponent(sm.qmax);
   auto wait = [&](uint64_t *bar, uint32_t parity) { return wait_or_abort(bar, parity, abort, a.status); };
   // the same answer in every lane: the loops below hold warp-wide instructions
   auto warp_wait = [&](uint64_t *bar, uint32_t parity) { return __all_sync(kFull, wait(bar, parity)) != 0; };
@@ -221,8 +224,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool have = grow < rows;
     const int32_t qi = grow / a.G, qg = grow - qi * a.G;
     const int64_t at = (tok0 + qi) * a.Hq + h * a.G + qg;
-    const float qsum =
-        stage_q(a.q + at * 128, have, MT == 2 || wg == 0 ? sm.q[MT == 2 ? wg : 0] : nullptr, row, pow2f(e));
+    const int shift = row_shift(qbits >> 23, e);
+    const float qsum = pow2f(-shift) * stage_q(a.q + at * 128, have, MT == 2 || wg == 0 ? sm.q[MT == 2 ? wg : 0] : nullptr,
+                                               row, pow2f(e + shift));
+    sm.w[tid] = pow2f(-shift);
+    bool odd = __any_sync(kFull, shift != 0);  // rows with a shift of their own, or references beyond kFar
     fence_async();
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.qready);
@@ -283,8 +289,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool masked = __any_sync(kFull, lim < 128) || sm.bad;
       const float *sv = sm.s[ms], *zv = sm.z[ms];
       const uint8_t *valid = sm.bad ? sm.valid[ms] : nullptr;
-      // y - mo of columns 32 c .. + 31, -inf where masked
-      auto logits = [&](uint32_t (&u)[32], int c, float mo) {
+      auto mask = [&](uint32_t (&u)[32], int c) {
+        if (__builtin_expect(masked, 0)) {
+          const uint32_t keep = column_mask(lim - 32 * c, valid ? valid + 32 * c : nullptr);
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (!(keep >> i & 1u)) u[i] = 0xff800000u;
+        }
+      };
+      // 2^(x - mo) in the place of x; returns the sum, even and odd columns
+      auto weigh = [&](uint32_t (&u)[32], float mo) -> uint64_t {
+        uint64_t sum[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float p0 = ex2(__uint_as_float(u[2 * i]) - mo), p1 = ex2(__uint_as_float(u[2 * i + 1]) - mo);
+          sum[i & 3] = f2_add(sum[i & 3], f2_pack(p0, p1));
+          u[2 * i] = __float_as_uint(p0);
+          u[2 * i + 1] = __float_as_uint(p1);
+        }
+        return f2_add(f2_add(sum[0], sum[1]), f2_add(sum[2], sum[3]));
+      };
+      // P of columns 32 c .. + 31, the usual way: y - mo in one multiply-add a
+      // value, -inf where masked, and the sum
+      auto usual = [&](uint32_t (&u)[32], int c) -> uint64_t {
+        const float mo = m == -INFINITY ? 0.0f : m - kLift;
         const uint64_t nm2 = f2_pack(-mo, -mo);
         tmem_ld32(ts_s + 32 * c, u);
         tmem_wait32(u);
@@ -302,80 +330,79 @@ __global__ void __launch_bounds__(kThreads, 1)
           u[4 * i + 2] = __float_as_uint(y0);
           u[4 * i + 3] = __float_as_uint(y1);
         }
-        if (__builtin_expect(masked, 0)) {
-          const uint32_t keep = column_mask(lim - 32 * c, valid ? valid + 32 * c : nullptr);
+        mask(u, c);
+        return weigh(u, 0.0f);
+      };
+      // The same with y rounded before m is taken off, rows' own shifts, and m
+      // moved to the columns' maximum where that is larger: the sum, P of the
+      // tile's columns before and O of the tiles before follow.
+      auto careful = [&](uint32_t (&u)[32], int c, uint64_t &sum) -> bool {
+        auto y_of = [&] {
+          const float w = sm.w[tid];
+          tmem_ld32(ts_s + 32 * c, u);
+          tmem_wait32(u);
 #pragma unroll
           for (int i = 0; i < 32; ++i)
-            if (!(keep >> i & 1u)) u[i] = 0xff800000u;
-        }
-      };
-      // m moves to the maximum of columns 32 c .. + 31: the sum, P of the tile's
-      // columns before and O of the tiles before follow
-      auto raise = [&](uint32_t (&u)[32], int c) -> bool {
-        logits(u, c, 0.0f);
+            u[i] = __float_as_uint(fmaf(sv[32 * c + i], __uint_as_float(u[i]) * w, zv[32 * c + i] * qsum));
+          mask(u, c);
+        };
+        y_of();
         float mx = -INFINITY;
 #pragma unroll
         for (int i = 0; i < 32; i += 2) mx = max3(mx, __uint_as_float(u[i]), __uint_as_float(u[i + 1]));
         const float mn = fmaxf(m, ceilf(mx));
         const float f = mn == m ? 1.0f : ex2(m - mn);  // a power of two, 0 at first
-        l2 = f2_mul(l2, f2_pack(f, f));
-        m = mn;
-        // P of earlier columns, and O where m has moved in this tile before, were
-        // stored by this thread: a load sees a store only after this wait
-        tmem_wait_st();
+        if (__any_sync(kFull, f != 1.0f)) {
+          l2 = f2_mul(l2, f2_pack(f, f));
+          m = mn;
+          odd |= __any_sync(kFull, fabsf(m) > kFar && m != -INFINITY);
+          // P of earlier columns, and O where m has moved in this tile before, were
+          // stored by this thread: a load sees a store only after this wait
+          tmem_wait_st();
 #pragma unroll 1
-        for (int i = 0; i < (tl.kind == 2 ? 2 * c : c); ++i) {
-          const uint32_t at_p = ts_s + (tl.kind == 2 ? 16 * i : 32 * i);
-          tmem_ld16(at_p, u);
-          tmem_wait16(u);
+          for (int i = 0; i < (tl.kind == 2 ? 2 * c : c); ++i) {
+            const uint32_t at_p = ts_s + (tl.kind == 2 ? 16 * i : 32 * i);
+            tmem_ld16(at_p, u);
+            tmem_wait16(u);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float2 p2 = tl.kind == 2 ? make_float2(bf16_lo(u[e]), bf16_hi(u[e])) : __half22float2(u2h(u[e]));
-            u[e] = tl.kind == 2 ? bf16x2_rn(p2.x * f, p2.y * f) : f16x2_rn(p2.x * f, p2.y * f);
+            for (int e = 0; e < 16; ++e) {
+              const float2 p2 = tl.kind == 2 ? make_float2(bf16_lo(u[e]), bf16_hi(u[e])) : __half22float2(u2h(u[e]));
+              u[e] = tl.kind == 2 ? bf16x2_rn(p2.x * f, p2.y * f) : f16x2_rn(p2.x * f, p2.y * f);
+            }
+            tmem_st16(at_p, u);
           }
-          tmem_st16(at_p, u);
-        }
-        if (t == 0) return true;
-        if (!warp_wait(&sm.odone[wg], (t - 1) & 1u)) return false;
-        fence_after();
+          if (t > 0) {
+            if (!warp_wait(&sm.odone[wg], (t - 1) & 1u)) return false;
+            fence_after();
 #pragma unroll 1
-        for (int i = 0; i < 8; ++i) {
-          tmem_ld16(ts_o + 16 * i, u);
-          tmem_wait16(u);
+            for (int i = 0; i < 8; ++i) {
+              tmem_ld16(ts_o + 16 * i, u);
+              tmem_wait16(u);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * f);
-          tmem_st16(ts_o + 16 * i, u);
+              for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * f);
+              tmem_st16(ts_o + 16 * i, u);
+            }
+          }
+          y_of();
         }
+        sum = weigh(u, m == -INFINITY ? 0.0f : m - kLift);
         return true;
       };
       // 32 columns at a time: the short loop stays in the instruction cache.  A
       // warp of padding rows leaves its rows of P as they are.
 #pragma unroll 1
-      for (int c = some ? 0 : 4; c < 4 && ok; ++c) {
+      for (int c = some ? 0 : 4; c < 4; ++c) {
         uint32_t u[32];
-        uint64_t sum[4];
-#pragma unroll 1
-        for (int pass = 0;; ++pass) {
-          logits(u, c, m == -INFINITY ? 0.0f : m - kLift);
-          sum[0] = sum[1] = sum[2] = sum[3] = 0;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float p0 = ex2(__uint_as_float(u[2 * i])), p1 = ex2(__uint_as_float(u[2 * i + 1]));
-            sum[i & 3] = f2_add(sum[i & 3], f2_pack(p0, p1));
-            u[2 * i] = __float_as_uint(p0);
-            u[2 * i + 1] = __float_as_uint(p1);
-          }
-          sum[0] = f2_add(f2_add(sum[0], sum[1]), f2_add(sum[2], sum[3]));
-          float a0, a1;
-          f2_unpack(sum[0], a0, a1);
-          a0 += a1;
-          // A row's first columns set its reference whatever their sum: against 0
-          // the weights of logits below -87 are all zero.
-          if (__builtin_expect(!__any_sync(kFull, a0 > kMost || (m == -INFINITY && lim > 32 * c)), 1) || pass) break;
-          uint32_t r[32];
-          if (!(ok = raise(r, c))) break;
+        uint64_t sum = 0;
+        bool rare = odd;
+        if (!rare) {
+          sum = usual(u, c);
+          // a row's first columns set its reference whatever their sum: against 0
+          // the weights of logits below -87 are all zero
+          rare = __any_sync(kFull, f2_sum(sum) > kMost || (m == -INFINITY && lim > 32 * c));
         }
-        l2 = f2_add(l2, sum[0]);
+        if (__builtin_expect(rare, 0) && !(ok = careful(u, c, sum))) break;
+        l2 = f2_add(l2, sum);
         if (tl.kind == 2) {
           uint32_t w[16];
 #pragma unroll

@@ -29,6 +29,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstddef>
+#include <type_traits>
 
 #include "token_tiles.cuh"
 
@@ -66,8 +67,9 @@ struct __align__(1024) Smem {
   int64_t at[kCols];          // output rows
   uint32_t top[kCols];        // maxima of a tile, as ordered integers
   uint64_t rfull[kRaw], rempty[kRaw], kfull, kempty, mfull[kMeta], vfull[2], vempty[2], sfull[2], pready, odone, done;
+  float w[kCols];             // 2^-d of the rows (row_shift)
   uint32_t qmax, tmem;
-  int32_t abort, unset;
+  int32_t abort, unset, odd;  // odd: a row has a shift of its own, or a reference beyond kFar
 };
 constexpr size_t kSmemBytes = sizeof(Smem) + 1024;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
@@ -208,19 +210,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sm.done, 1);
     sm.abort = 0;
     sm.qmax = 0;
+    sm.odd = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 0) tmem_alloc(&sm.tmem, kTmemCols);
   // four warps stage Q: two threads per row, 64 rows
   const int qrow = (tid & 127) >> 1, qhalf = tid & 1;
   uint4 qv[8];
+  uint32_t rm = 0;  // bits of the row's largest |value|
   fence_before();
   __syncthreads();
   fence_after();
   if (warp < 4) {
     const bool have = qrow < rows;
     const uint4 *src = reinterpret_cast<const uint4 *>(a.q + (have ? row_at(qrow) : 0) * 128) + 8 * qhalf;
-    uint32_t rm = 0;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       qv[k] = have ? __ldg(src + k) : make_uint4(0, 0, 0, 0);
@@ -231,13 +234,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     rm = max(rm, __shfl_xor_sync(kFull, rm, 1));
     if (rm >= 0x7f800000u) rm = 0;  // a row that is not finite spoils itself alone
-    rm = __reduce_max_sync(kFull, rm);
-    if (lane == 0 && rm) atomicMax(&sm.qmax, rm);
+    const uint32_t wm = __reduce_max_sync(kFull, rm);
+    if (lane == 0 && wm) atomicMax(&sm.qmax, wm);
   }
   if (warp < kCopyWarp) meet_all();  // the copy warps have gone ahead
-  const int e = lift_exponent(sm.qmax);
+  const int e = block_exponent(sm.qmax);
   if (warp < 4) {
-    const float sc = pow2f(e);
+    const int shift = row_shift(rm >> 23, e);
+    const float sc = pow2f(e + shift);
     float sum = 0.0f;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
@@ -251,8 +255,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     sum += __shfl_xor_sync(kFull, sum, 1);
     if (qhalf == 0 && qrow < kCols) {
       float *dst = reinterpret_cast<float *>(&sm.col[qrow >> 1]) + (qrow & 1);
-      dst[0] = sum;
+      dst[0] = sum * pow2f(-shift);
       dst[2] = 0.0f;
+      sm.w[qrow] = pow2f(-shift);
+      if (shift != 0) sm.odd = 1;
       sm.m[qrow] = -INFINITY;
       sm.top[qrow] = 0;
     }
@@ -288,19 +294,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool masked = __any_sync(kFull, from > 0);
       const uint64_t s2 = f2_pack(s_cur, s_cur), z2 = f2_pack(z_cur, z_cur);
       const float4 *col = sm.col + (kMine / 2) * half;
+      bool odd = sm.odd != 0;
       uint32_t u[kMine];
       // y - m (+ lift), -inf where masked; `plain`: y itself
-      auto logits = [&](bool plain) {
+      auto logits = [&](auto which, bool plain) {
+        constexpr bool odd = decltype(which)::value;
         tmem_ld16(ts_s, u);
         tmem_wait16(u);
+        if constexpr (odd) {
+#pragma unroll
+          for (int c = 0; c < kMine; ++c) u[c] = __float_as_uint(__uint_as_float(u[c]) * sm.w[kMine * half + c]);
+        }
 #pragma unroll
         for (int i = 0; i < kMine / 2; ++i) {
           const float4 cv = col[i];
           float y0, y1;
           f2_unpack(f2_fma(s2, f2_pack(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1])),
-                           f2_fma(z2, f2_pack(cv.x, cv.y), plain ? 0 : f2_pack(cv.z, cv.w))), y0, y1);
+                           f2_fma(z2, f2_pack(cv.x, cv.y), plain || odd ? 0 : f2_pack(cv.z, cv.w))), y0, y1);
           u[2 * i] = __float_as_uint(y0);
           u[2 * i + 1] = __float_as_uint(y1);
+        }
+        if (odd && !plain) {
+#pragma unroll
+          for (int i = 0; i < kMine / 2; ++i) {
+            u[2 * i] = __float_as_uint(__uint_as_float(u[2 * i]) + col[i].z);
+            u[2 * i + 1] = __float_as_uint(__uint_as_float(u[2 * i + 1]) + col[i].w);
+          }
         }
         if (masked) {
 #pragma unroll
@@ -312,7 +331,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int pass = 0;; ++pass) {
         float mx = 0.0f;
         if (ok && some) {
-          logits(false);
+          if (__builtin_expect(odd, 0)) logits(std::true_type{}, false);
+          else logits(std::false_type{}, false);
 #pragma unroll
           for (int c = 0; c < kMine; c += 2) {
             const float p0 = ex2(__uint_as_float(u[c])), p1 = ex2(__uint_as_float(u[c + 1]));
@@ -326,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---- the references move to the tile's maxima where those are larger
         if ((stop = meet(!ok))) break;
         if (some) {
-          logits(true);
+          logits(std::true_type{}, true);  // shifts are 0 where no row is odd
 #pragma unroll 1
           for (int c = 0; c < kMine; ++c) {
             uint32_t v = 0;  // u[c], with the loop kept short
@@ -346,9 +366,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           (reinterpret_cast<float *>(&sm.col[tid >> 1]) + (tid & 1))[2] = m1 == -INFINITY ? 0.0f : kLift - m1;
           const uint32_t un = __ballot_sync(kFull, tid < rows && m1 == -INFINITY);
           if (tid == 0) sm.unset = un != 0;
+          if (fabsf(m1) > kFar && m1 != -INFINITY) sm.odd = 1;
         }
         meet(false);
         force = sm.unset != 0;
+        odd = sm.odd != 0;
 #pragma unroll
         for (int c = 0; c < kMine; ++c) l[c] *= sm.f[kMine * half + c];
         if (j > 0) {

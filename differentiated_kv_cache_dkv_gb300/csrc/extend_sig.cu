@@ -36,6 +36,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstddef>
+#include <type_traits>
 
 #include "token_tiles.cuh"
 
@@ -79,6 +80,8 @@ struct __align__(1024) Smem {
   uint32_t there[kRaw][4];   // which of a raw tile's tokens exist
   uint64_t kfull[kGroup], kempty[kGroup], sfull[kGroup], sfree[kGroup];
   uint64_t qfull[2], qempty[2], cfull[4], cempty[4], qm[4], done, rfull[kRaw], rempty[kRaw];
+  int8_t d[4][128];         // per column: row_shift
+  alignas(8) uint8_t odd[4][kConvWarps];  // a convert warp's columns have such shifts, or normalisers beyond kFar
   uint32_t qmax[4];
   float qf[4];  // 2^-e of the block's Q
   uint32_t tmem;
@@ -260,6 +263,7 @@ __global__ void __launch_bounds__(Roles<kMany>::kThreads, 1)
         if ((kMany || g == 0) && !(ok = warp_wait(&sm.cfull[qi & 3], (qi >> 2) & 1u))) break;
         const float qf = sm.qf[qi & 3];
         const float4 *col = sm.col[qi & 3];
+        const bool odd = *reinterpret_cast<const uint64_t *>(sm.odd[qi & 3]) != 0;
 #pragma unroll 1
         for (int32_t t = wg; t < ng; t += kWg) {
           if (!(ok = warp_wait(&sm.kfull[t], g & 1u) && warp_wait(&sm.sfull[t], (g * nblk + b) & 1u))) break;
@@ -272,64 +276,79 @@ __global__ void __launch_bounds__(Roles<kMany>::kThreads, 1)
           const bool diag = __any_sync(kFull, bk.i0 < tj), ends = ib == 1 || b % ib == ib - 1;
           int32_t cnt = 0;  // heads that are done, v: the last four
           float v[4];
+          // blocks with odd columns have a copy of the loop of their own, out of
+          // the usual one's way in the instruction cache
+          auto columns = [&](auto which) {
+            constexpr bool odd = decltype(which)::value;
 #pragma unroll 1
-          for (int32_t c = 0; c < cols; c += 16) {
-            uint32_t u[16];
-            __syncwarp();  // lanes without a token have skipped ahead
-            tmem_ld16(tmem + lanes + 128 * t + c, u);
-            tmem_wait16(u);
+            for (int32_t c = 0; c < cols; c += 16) {
+              uint32_t u[16];
+              __syncwarp();  // lanes without a token have skipped ahead
+              tmem_ld16(tmem + lanes + 128 * t + c, u);
+              tmem_wait16(u);
+              if constexpr (odd) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float4 cv = col[(c >> 1) + i];
-              float y0, y1;
-              f2_unpack(f2_fma(s2, f2_pack(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1])),
-                               f2_fma(z2, f2_pack(cv.x, cv.y), f2_pack(cv.z, cv.w))), y0, y1);
-              u[2 * i] = __float_as_uint(y0);
-              u[2 * i + 1] = __float_as_uint(y1);
-            }
-            if (diag) {  // rows before new token tj do not attend to it
-              const int32_t skip = tj - bk.i0 - (c & (nb - 1));
+                for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(__uint_as_float(u[i]) * pow2f(-sm.d[qi & 3][c + i]));
+              }
 #pragma unroll
-              for (int i = 0; i < 16; ++i) u[i] = (i & (nb - 1)) < skip ? 0xff800000u : u[i];
-            }
-            uint64_t q8[2];  // eight columns each
+              for (int i = 0; i < 8; ++i) {
+                const float4 cv = col[(c >> 1) + i];
+                float y0, y1;
+                f2_unpack(f2_fma(s2, f2_pack(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1])),
+                                 f2_fma(z2, f2_pack(cv.x, cv.y), f2_pack(cv.z, cv.w))), y0, y1);
+                u[2 * i] = __float_as_uint(y0);
+                u[2 * i + 1] = __float_as_uint(y1);
+              }
+              if constexpr (odd) {  // a normaliser's own rounding can put x above it: weights end at 1
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const uint64_t w = f2_pack(ex2(__uint_as_float(u[2 * i])), ex2(__uint_as_float(u[2 * i + 1])));
-              q8[i >> 2] = i & 3 ? f2_add(q8[i >> 2], w) : w;
-            }
-            if (lg == 3) {
-              v[0] = v[2];
-              v[1] = v[3];
-              v[2] = f2_sum(q8[0]);
-              v[3] = f2_sum(q8[1]);
-              cnt += 2;
-            } else {
-              run = f2_add(run, f2_add(q8[0], q8[1]));
-              if (((c + 16) & (nb - 1)) != 0 || !ends) continue;
-              v[0] = v[1];
-              v[1] = v[2];
-              v[2] = v[3];
-              v[3] = f2_sum(run);
-              run = 0;
-              ++cnt;
-            }
-            if (((cnt & 3) != 0 && c + 16 < cols) || pos < 0) continue;
-            // heads [base, cnt) of the block to their places; this thread alone adds to the token's sums
-            const int32_t base = (cnt - 1) & ~3, most = min(cnt, min(hpb, a.G - bk.head0));
-            float *dst = a.sig_sum + ((static_cast<int64_t>(a.layer0 + li) * a.R + r) * a.cap + pos) * a.Hq + h * a.G +
-                         bk.head0 + cnt - 4;
-            if (wide && most - base == 4 && tj < 0) {
-              red_add4(dst, v[0], v[1], v[2], v[3]);
-            } else {
+                for (int i = 0; i < 16; ++i) u[i] = __uint_as_float(u[i]) > 0.0f ? 0u : u[i];
+              }
+              if (diag) {  // rows before new token tj do not attend to it
+                const int32_t skip = tj - bk.i0 - (c & (nb - 1));
 #pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                if (cnt - 4 + q < base || cnt - 4 + q >= most) continue;
-                if (tj < 0) red_add(dst + q, v[q]);
-                else dst[q] = v[q];
+                for (int i = 0; i < 16; ++i) u[i] = (i & (nb - 1)) < skip ? 0xff800000u : u[i];
+              }
+              uint64_t q8[2];  // eight columns each
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const uint64_t w = f2_pack(ex2(__uint_as_float(u[2 * i])), ex2(__uint_as_float(u[2 * i + 1])));
+                q8[i >> 2] = i & 3 ? f2_add(q8[i >> 2], w) : w;
+              }
+              if (lg == 3) {
+                v[0] = v[2];
+                v[1] = v[3];
+                v[2] = f2_sum(q8[0]);
+                v[3] = f2_sum(q8[1]);
+                cnt += 2;
+              } else {
+                run = f2_add(run, f2_add(q8[0], q8[1]));
+                if (((c + 16) & (nb - 1)) != 0 || !ends) continue;
+                v[0] = v[1];
+                v[1] = v[2];
+                v[2] = v[3];
+                v[3] = f2_sum(run);
+                run = 0;
+                ++cnt;
+              }
+              if (((cnt & 3) != 0 && c + 16 < cols) || pos < 0) continue;
+              // heads [base, cnt) of the block to their places; this thread alone adds to the token's sums
+              const int32_t base = (cnt - 1) & ~3, most = min(cnt, min(hpb, a.G - bk.head0));
+              float *dst = a.sig_sum + ((static_cast<int64_t>(a.layer0 + li) * a.R + r) * a.cap + pos) * a.Hq + h * a.G +
+                           bk.head0 + cnt - 4;
+              if (wide && most - base == 4 && tj < 0) {
+                red_add4(dst, v[0], v[1], v[2], v[3]);
+              } else {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  if (cnt - 4 + q < base || cnt - 4 + q >= most) continue;
+                  if (tj < 0) red_add(dst + q, v[q]);
+                  else dst[q] = v[q];
+                }
               }
             }
-          }
+          };
+          if (__builtin_expect(odd, 0)) columns(std::true_type{});
+          else columns(std::false_type{});
           fence_before();
           __syncwarp();
           if (lane == 0) {
@@ -353,7 +372,7 @@ __global__ void __launch_bounds__(Roles<kMany>::kThreads, 1)
     auto stage = [&](int32_t b, int32_t qi) -> bool {
       const Block bk = block_at(b);
       uint4 v[2][4];
-      uint32_t mx = 0;
+      uint32_t mx = 0, ex = 0;  // largest finite |value| of the block (bits), of the thread's columns (exponents)
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
         const int32_t cl = d.tk + 64 * p, hd = bk.head0 + (cl >> lg), i = bk.i0 + (cl & (nb - 1));
@@ -375,7 +394,9 @@ __global__ void __launch_bounds__(Roles<kMany>::kThreads, 1)
         uint32_t rm = max(m2 << 16, m2 & 0xffff0000u);  // bits of |value|: they order like it
         rm = max(rm, __shfl_xor_sync(kFull, rm, 1));
         rm = max(rm, __shfl_xor_sync(kFull, rm, 2));
-        if (rm < 0x7f800000u) mx = max(mx, rm);  // an infinity spoils its own row alone
+        if (rm >= 0x7f800000u) rm = 0;  // an infinity spoils its own row alone
+        mx = max(mx, rm);
+        ex |= rm >> 23 << (8 * p);
       }
       mx = __reduce_max_sync(kFull, mx);
       if (lane == 0) {
@@ -383,19 +404,30 @@ __global__ void __launch_bounds__(Roles<kMany>::kThreads, 1)
         mbar_arrive(&sm.qm[qi & 3]);
       }
       if (!warp_wait(&sm.qm[qi & 3], (qi >> 2) & 1u)) return false;
-      const int e = lift_exponent(*const_cast<volatile uint32_t *>(&sm.qmax[qi & 3]));
-      const float sc = pow2f(e);
-      const uint64_t sc2 = f2_pack(sc, sc);
+      const int e = block_exponent(*const_cast<volatile uint32_t *>(&sm.qmax[qi & 3]));
       if (qi >= 2 && !warp_wait(&sm.qempty[qi & 1], ((qi >> 1) - 1) & 1u)) return false;
       if (qi >= 4 && !warp_wait(&sm.cempty[qi & 3], ((qi >> 2) - 1) & 1u)) return false;
       if (dt == 0) {
         sm.qf[qi & 3] = pow2f(-e);
         sm.qmax[(qi + 2) & 3] = 0;  // last used two blocks ago
       }
+      {  // the columns' own shifts: by way of shared memory, the registers are full of Q
+        const int s0 = row_shift(ex & 255u, e), s1 = row_shift(ex >> 8, e);
+        if (d.c == 0) {
+          sm.d[qi & 3][d.tk] = static_cast<int8_t>(s0);
+          sm.d[qi & 3][d.tk + 64] = static_cast<int8_t>(s1);
+        }
+        const bool odd = __any_sync(kFull, (s0 | s1) != 0);
+        if (lane == 0) sm.odd[qi & 3][warp - kConvWarp] = odd;
+        __syncwarp();
+      }
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
         const int32_t cl = d.tk + 64 * p, hd = bk.head0 + (cl >> lg), i = bk.i0 + (cl & (nb - 1));
         const bool have = cl < hpb * nb && hd < a.G && i < acc_n;
+        const int shift = sm.d[qi & 3][cl];
+        const float sc = pow2f(e + shift);
+        const uint64_t sc2 = f2_pack(sc, sc);
         uint64_t acc = 0;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -412,8 +444,9 @@ __global__ void __launch_bounds__(Roles<kMany>::kThreads, 1)
         if (d.c == 0) {
           const float ls = have ? a.lse[(tok0 + i) * a.Hq + h * a.G + hd] : -INFINITY;
           float *dst = reinterpret_cast<float *>(&sm.col[qi & 3][cl >> 1]) + (cl & 1);
-          dst[0] = have ? sum : 0.0f;
+          dst[0] = have ? sum * pow2f(-shift) : 0.0f;
           dst[2] = ls == -INFINITY ? -INFINITY : -ls * kLog2e;  // -inf: the column adds nothing
+          if (fabsf(dst[2]) > kFar && ls != -INFINITY) sm.odd[qi & 3][warp - kConvWarp] = 1;
         }
       }
       fence_async();
@@ -424,6 +457,7 @@ __global__ void __launch_bounds__(Roles<kMany>::kThreads, 1)
       }
       return true;
     };
+    if (!kMany) ok = stage(0, 0);
     int32_t st = 0;
     uint32_t ph = 0;
 #pragma unroll 1
@@ -431,36 +465,36 @@ __global__ void __launch_bounds__(Roles<kMany>::kThreads, 1)
       const int32_t ng = min(kGroup, n - g * kGroup);
 #pragma unroll 1
       for (int32_t b = 0; b < nblk && ok; ++b) {
-        if (kMany || g == 0) ok = stage(b, g * nblk + b);
+        if (kMany) ok = stage(b, g * nblk + b);
         if (b > 0) continue;
 #pragma unroll 1
         for (int32_t q = 0; q < ng && ok; ++q) {
-        const Tile t = tile_at(ts, x, fresh, j0 + g * kGroup + q);
-        const uint8_t *src = raw + st * Raw<KH>::kSlot;
-        if (!(ok = warp_wait(&sm.rfull[st], ph))) break;
-        if (g > 0 && !(ok = warp_wait(&sm.kempty[q], (g - 1) & 1u))) break;
-        if (t.kind == 0) {
-          convert_key<KH, KH>(d, src, sm.there[st], sm, q, f, ctx);
-        } else if (t.kind == 1) {
-          convert_key<KH / 2, KH>(d, src, sm.there[st], sm, q, f, ctx);
-        } else {
-          new_k<2, false>(d, t, tok0, h, sm, sm.k[q], q, f);
-          if (d.c == 0) {
+          const Tile t = tile_at(ts, x, fresh, j0 + g * kGroup + q);
+          const uint8_t *src = raw + st * Raw<KH>::kSlot;
+          if (!(ok = warp_wait(&sm.rfull[st], ph))) break;
+          if (g > 0 && !(ok = warp_wait(&sm.kempty[q], (g - 1) & 1u))) break;
+          if (t.kind == 0) {
+            convert_key<KH, KH>(d, src, sm.there[st], sm, q, f, ctx);
+          } else if (t.kind == 1) {
+            convert_key<KH / 2, KH>(d, src, sm.there[st], sm, q, f, ctx);
+          } else {
+            new_k<2, false>(d, t, tok0, h, sm, sm.k[q], q, f);
+            if (d.c == 0) {
 #pragma unroll
-            for (int p = 0; p < 2; ++p) {
-              const int row = d.tk + 64 * p;
-              sm.pos[q][row] = row < t.n ? ctx + t.t0 + row : -1;
+              for (int p = 0; p < 2; ++p) {
+                const int row = d.tk + 64 * p;
+                sm.pos[q][row] = row < t.n ? ctx + t.t0 + row : -1;
+              }
             }
           }
+          fence_async();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&sm.kfull[q]);
+            mbar_arrive(&sm.rempty[st]);
+          }
+          if (++st == nraw) st = 0, ph ^= 1u;
         }
-        fence_async();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&sm.kfull[q]);
-          mbar_arrive(&sm.rempty[st]);
-        }
-        if (++st == nraw) st = 0, ph ^= 1u;
-      }
       }
     }
   } else if (warp >= kCopyWarp) {

@@ -38,6 +38,22 @@ __device__ __forceinline__ int lift_exponent(uint32_t bits) {
   return bits ? min(max(14 + 127 - static_cast<int>(bits >> 23), -120), 120) : 0;
 }
 
+// The exponent of a block of Q, and how much further a row of it is shifted.  A
+// block's rows share one power of two, which the tokens' scales undo; a row
+// whose largest value lies 2^12 and more below the block's would lose bits of
+// fp16, and is shifted by its own d (its products are multiplied by 2^-d, as is
+// the sum of its values).  The block's largest counts as 2^35 at most, so that
+// scales times 2^20 stay finite in fp32; rows above that have d < 0.
+__device__ __forceinline__ int block_exponent(uint32_t bits) { return max(lift_exponent(bits), -20); }
+__device__ __forceinline__ int row_shift(uint32_t ex, int e) {  // ex: the biased exponent of the row's largest
+  if (!ex) return 0;  // zeros (or as good as), or not finite
+  const int d = lift_exponent(ex << 23) - e;
+  return d < 0 || d > 12 ? min(d, 126) : 0;
+}
+// References and normalisers above this (log2 units) leave y - m, summed in one
+// multiply-add, off by more than the weights' range allows: y is rounded first.
+constexpr float kFar = 1048576.0f;
+
 // The dequant warps' view of one tile.
 struct Tile {
   int32_t kind, t0, n;  // 0 high, 1 low, 2 new; first token in its list; tokens

@@ -605,7 +605,7 @@ class Decoder:
         if workspace is None:
             need = dkv_extend_workspace_size(b, self.pool, self.tables)
             if need and (not self._ext_ws or self._ext_ws[-1].numel() < need):
-                self._ext_ws.append(torch.empty(need, dtype=torch.uint8, device=self.device))
+                self._ext_ws.append(self._scratch(need, stream))
             workspace = self._ext_ws[-1] if need else None
         dkv_extend_attention(b, self.pool, self.tables, workspace, stream=stream)
 
@@ -618,10 +618,15 @@ class Decoder:
                               v_new=v_new, lse=lse, layer0=layer0)
         dkv_extend_significance(b, acc_lens, sig_sum, self.pool, self.tables, stream=stream)
 
-    def _page_ops_ws(self) -> torch.Tensor:
+    def _scratch(self, n: int, stream) -> torch.Tensor:
+        # memory of the stream it is first used on: another stream's could still
+        # be read or written by work that had it before
+        with torch.cuda.stream(stream):
+            return torch.empty(n, dtype=torch.uint8, device=self.device)
+
+    def _page_ops_ws(self, stream) -> torch.Tensor:
         if self._ops_ws is None:
-            self._ops_ws = torch.empty(dkv_page_ops_workspace_size(self.pool, self.tables), dtype=torch.uint8,
-                                       device=self.device)
+            self._ops_ws = self._scratch(dkv_page_ops_workspace_size(self.pool, self.tables), stream)
         return self._ops_ws
 
     def fork(self, src: torch.Tensor, dst: torch.Tensor, ctx_lens: torch.Tensor, sig_sum: torch.Tensor | None = None,
@@ -630,13 +635,13 @@ class Decoder:
         significance rows and counts); the caller sets ctx_lens[dst] = ctx_lens[src]."""
         b = make_fork_batch(self.L, self.R, self.Hq, self.Hkv, self.cap, src, dst, ctx_lens, self.classes,
                             self.slot_of, sig_sum, sig_cnt)
-        dkv_fork(b, self.pool, self.tables, self._page_ops_ws(), stream=stream)
+        dkv_fork(b, self.pool, self.tables, self._page_ops_ws(stream), stream=stream)
 
     def release(self, reqs: torch.Tensor, stream=None) -> None:
         """dkv_release: the requests' pages go back to the free list; the caller sets their ctx_lens to 0."""
-        dkv_release(make_release_batch(self.L, self.R, self.Hkv, reqs), self.pool, self.tables, self._page_ops_ws(),
-                    stream=stream)
+        dkv_release(make_release_batch(self.L, self.R, self.Hkv, reqs), self.pool, self.tables,
+                    self._page_ops_ws(stream), stream=stream)
 
     def defrag(self, stream=None) -> None:
         """dkv_defrag: the live pages move to the lowest ids."""
-        dkv_defrag(self.pool, self.tables, self._page_ops_ws(), stream=stream)
+        dkv_defrag(self.pool, self.tables, self._page_ops_ws(stream), stream=stream)

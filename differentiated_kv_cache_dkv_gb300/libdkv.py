@@ -437,7 +437,10 @@ def make_extend_batch(L: int, Hkv: int, cap: int, q: torch.Tensor, new_lens: tor
                       max_new: int, scale: float, k_new: torch.Tensor | None = None,
                       v_new: torch.Tensor | None = None, out: torch.Tensor | None = None,
                       lse: torch.Tensor | None = None, layer0: int = 0) -> dkv_extend_batch:
-    """q, out bf16 [n_layers][T][Hq][128]; k_new, v_new bf16 [n_layers][T][Hkv][128]; lse fp32 [n_layers][T][Hq]."""
+    """q, out bf16 [n_layers][T][Hq][128]; k_new, v_new bf16 [n_layers][T][Hkv][128]; lse fp32 [n_layers][T][Hq];
+    new_lens, ctx_lens int32 [R]: of every request of the tables."""
+    if ctx_lens.numel() != new_lens.numel():
+        raise ValueError("new_lens and ctx_lens name the same requests")
     n_layers, T, Hq = int(q.shape[0]), int(q.shape[1]), int(q.shape[2])
     return dkv_extend_batch(int(L), int(new_lens.numel()), Hq, int(Hkv), int(cap), int(layer0), n_layers,
                             int(max_new), T, _p(q), _p(k_new), _p(v_new), _p(new_lens), _p(ctx_lens), float(scale),
@@ -468,6 +471,8 @@ def dkv_extend_attention(batch: dkv_extend_batch, pool: DevicePool, tables, work
 
 def dkv_extend_significance(batch: dkv_extend_batch, acc_lens: torch.Tensor, sig_sum: torch.Tensor,
                             pool: DevicePool, tables, stream=None) -> None:
+    if acc_lens.numel() != batch.R:
+        raise ValueError("acc_lens and new_lens name the same requests")
     pc, tc = pool.c(), tables.c()
     rc = load().dkv_extend_significance(ctypes.byref(batch), _p(acc_lens), _p(sig_sum), ctypes.byref(pc),
                                         ctypes.byref(tc), _stream(stream))
@@ -592,6 +597,11 @@ class Decoder:
                            _p(k_new), _p(v_new), _p(new_lens), _p(ctx_lens), float(scale), _p(out), _p(sig_sum))
         dkv_decode_attention(b, self.pool, self.tables, stream=stream)
 
+    def _extend_batch(self, q: torch.Tensor, new_lens: torch.Tensor, *args, **kw) -> dkv_extend_batch:
+        if new_lens.numel() != self.R:  # the tables' units are numbered by all of them
+            raise ValueError(f"new_lens: the {self.R} requests' lengths are wanted, 0 for those without new tokens")
+        return make_extend_batch(self.L, self.Hkv, self.cap, q, new_lens, *args, **kw)
+
     def extend(self, q: torch.Tensor, new_lens: torch.Tensor, ctx_lens: torch.Tensor, max_new: int, out: torch.Tensor,
                scale: float, k_new: torch.Tensor | None = None, v_new: torch.Tensor | None = None,
                lse: torch.Tensor | None = None, layer0: int = 0, workspace: torch.Tensor | None = None,
@@ -600,8 +610,8 @@ class Decoder:
 
         Calls (and replays of captured ones) that may run at the same time need a workspace each, of
         dkv_extend_workspace_size bytes; without one they share the decoder's and run in stream order."""
-        b = make_extend_batch(self.L, self.Hkv, self.cap, q, new_lens, ctx_lens, max_new, scale, k_new=k_new,
-                              v_new=v_new, out=out, lse=lse, layer0=layer0)
+        b = self._extend_batch(q, new_lens, ctx_lens, max_new, scale, k_new=k_new, v_new=v_new, out=out, lse=lse,
+                               layer0=layer0)
         if workspace is None:
             need = dkv_extend_workspace_size(b, self.pool, self.tables)
             if need and (not self._ext_ws or self._ext_ws[-1].numel() < need):
@@ -614,8 +624,7 @@ class Decoder:
                             sig_sum: torch.Tensor, k_new: torch.Tensor | None = None,
                             v_new: torch.Tensor | None = None, layer0: int = 0, stream=None) -> None:
         """dkv_extend_significance of the first acc_lens[r] of those tokens."""
-        b = make_extend_batch(self.L, self.Hkv, self.cap, q, new_lens, ctx_lens, max_new, scale, k_new=k_new,
-                              v_new=v_new, lse=lse, layer0=layer0)
+        b = self._extend_batch(q, new_lens, ctx_lens, max_new, scale, k_new=k_new, v_new=v_new, lse=lse, layer0=layer0)
         dkv_extend_significance(b, acc_lens, sig_sum, self.pool, self.tables, stream=stream)
 
     def _scratch(self, n: int, stream) -> torch.Tensor:

@@ -225,7 +225,8 @@ dkv::ExtendArgs extend_args(const dkv_extend_batch *b, const dkv_pool *pool, con
 }
 
 dkv::ExtendPlan extend_plan_of(const dkv_extend_batch *b) {
-  return dkv::extend_plan(static_cast<int64_t>(b->n_layers) * b->R * b->Hkv, b->R, b->max_new, b->Hq / b->Hkv, b->cap,
+  return dkv::extend_plan(static_cast<int64_t>(b->n_layers) * b->R * b->Hkv,
+                          b->T == static_cast<int64_t>(b->R) * b->max_new, b->max_new, b->Hq / b->Hkv, b->cap,
                           b->n_layers * b->T * b->Hq);
 }
 

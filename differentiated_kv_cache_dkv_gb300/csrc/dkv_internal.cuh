@@ -483,7 +483,8 @@ cudaError_t launch_prefill(const PrefillArgs &a, cudaStream_t s);
 cudaError_t launch_fork(const PageOpArgs &a, int sms, cudaStream_t s);
 cudaError_t launch_release(const PageOpArgs &a, cudaStream_t s);
 cudaError_t launch_defrag(const PageOpArgs &a, int sms, cudaStream_t s);
-ExtendPlan extend_plan(int64_t units, int32_t R, int32_t max_new, int32_t G, int32_t cap, int64_t rows);
+// equal: every request has max_new new tokens
+ExtendPlan extend_plan(int64_t units, bool equal, int32_t max_new, int32_t G, int32_t cap, int64_t rows);
 cudaError_t launch_extend(const ExtendArgs &a, const ExtendPlan &p, void *ws, cudaStream_t s);
 cudaError_t launch_extend_few(const ExtendArgs &a, const ExtendPlan &p, const ExtendPartial &part, cudaStream_t s);
 cudaError_t launch_extend_sig(const ExtendArgs &a, cudaStream_t s);

@@ -690,9 +690,8 @@ cudaError_t launch(const ExtendArgs &a, const ExtendPlan &p, const ExtendPartial
 // to three waves: 42, 72, 94 and 116).  Blocks of 128 or 256 rows: one wave (a
 // request with 512 new tokens over 8192: 138 / 155 / 162 us).
 constexpr int64_t kFewBlocks = 152 * 2;
-constexpr int32_t kFewRequests = 4;
 
-ExtendPlan extend_plan(int64_t units, int32_t R, int32_t max_new, int32_t G, int32_t cap, int64_t rows) {
+ExtendPlan extend_plan(int64_t units, bool equal, int32_t max_new, int32_t G, int32_t cap, int64_t rows) {
   ExtendPlan p{};
   const int64_t most = static_cast<int64_t>(max_new) * G;
   const int64_t tiles = (static_cast<int64_t>(cap) + 127) / 128 + 2;
@@ -708,11 +707,15 @@ ExtendPlan extend_plan(int64_t units, int32_t R, int32_t max_new, int32_t G, int
     const int64_t items = units * p.row_tiles, rest = items % 152;
     if (items < 152 || p.mt == 1) {
       p.splits = static_cast<int32_t>(std::clamp<int64_t>(152 / std::max<int64_t>(items, 1), 1, std::max<int64_t>(tiles / 4, 1)));
-    } else if (R <= kFewRequests && rest > 0 && items < 16 * 152) {
-      // the last, incomplete wave in parts, as many as fill it (a chunk of
-      // 512 row tiles: 4 waves of 1, or 3 and one of 1/2; 1626 -> 1513 us).
-      // Many requests are ragged, and the order fills the last wave instead (16
-      // requests: 165 us without parts, 180 with them)
+    } else if (equal && rest > 0 && items < 16 * 152) {
+      // the last, incomplete wave in parts, as many as fill it, where every
+      // request has max_new new tokens (512 row tiles: 4 waves of 1, or 3 and one
+      // of 1/2).  Requests with 32 heads over 8, without parts and with them:
+      //   512 new over 8192, 3 requests 436 / 324, 8: 870 / 805 us
+      //   333 new over 5000, 4: 285 / 215, 11: 571 / 538, 16: 834 / 753 us
+      // Of ragged ones the order fills the last wave, and parts cost more than
+      // they bring (100 .. 333 new over 5000, 4: 154 / 160, 16: 558 / 569; over
+      // 1000 .. 5000, 11: 250 / 250, 16: 346 / 358 us).
       p.splits = static_cast<int32_t>(std::clamp<int64_t>(152 / rest, 1, std::min<int64_t>(8, std::max<int64_t>(tiles / 4, 1))));
       if (p.splits > 1) p.full = items - rest;
     }

@@ -450,6 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float l = l0 + l1, mo = m == -INFINITY ? 0.0f : m - kLift;
     if (ok && t > 0) ok = warp_wait(&sm.odone[wg], (t - 1) & 1u);
     fence_after();
+    const int64_t n_rows = a.n_layers * a.T * a.Hq;
     const bool direct = MT == 2 && (whole || splits == 1);
     const int64_t slot = (MT == 2 ? sp : 2 * sp + wg) * part.rows + at;
     if (ok) {
@@ -467,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 32; ++i) o[i] = 0;
         }
         channel_order(o, f);
-        if (!have) continue;
+        if (!have || !in_range(at, n_rows, a.status)) continue;
         if (direct) {
           uint4 *dst = reinterpret_cast<uint4 *>(a.out + at * 128 + 32 * c);
 #pragma unroll
@@ -481,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 8; ++i) dst[i] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
         }
       }
-      if (have) {
+      if (have && in_range(at, n_rows, a.status)) {
         if (!direct) part.ml[slot] = make_float2(t > 0 ? mo : -INFINITY, l);
         else if (part.ml) part.ml[at] = make_float2(0.0f, -1.0f);  // nothing to merge
         if (direct && a.lse) a.lse[at] = l == 0.0f ? -INFINITY : (mo + log2f(l)) * 0.693147180559945309f;
@@ -519,7 +520,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int32_t kb = high ? 16 * KH : 8 * KH, vb = high ? 16 * VH : 8 * VH;
       const int32_t p0 = (k0 + k) * per, first = max(tn.t0 - p0, 0), to = p0 + first - tn.t0;
       const int32_t n_in = min(p0 + per, tn.t0 + tn.n) - p0 - first, md = 8 * ((n_in + 1) & ~1);
-      const bool mine = tn.kind != 2 && k < pages && page >= 0 && page < a.F;  // else the tokens are masked (sm.bad)
+      const bool mine = tn.kind != 2 && k < pages && page >= 0 && page < a.F &&  // else the tokens are masked (sm.bad)
+                        in_range(to, 129 - n_in, a.status) && in_range(first, per + 1 - n_in, a.status);
       if (mine) sum = rf.whole ? rf.stride : n_in * (kb + vb) + md;
       sum = __reduce_add_sync(kFull, sum);
       if (lane == 0) mbar_expect_tx(&sm.rfull, sum);  // before any copy can land

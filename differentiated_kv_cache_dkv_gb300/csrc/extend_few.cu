@@ -130,6 +130,7 @@ __device__ __forceinline__ void copy_tile(const ExtendArgs &a, const Tile &t, co
       }
       const int32_t p0 = (g.k0 + k) * g.per, first = max(t.t0 - p0, 0);
       const int32_t n = min(p0 + g.per, t.t0 + t.n) - p0 - first, to = p0 + first - t.t0, md = 8 * ((n + 1) & ~1);
+      if (!in_range(to, 129 - n, a.status) || !in_range(first, g.per + 1 - n, a.status)) continue;
       if (pass == 0) {
         sum += f.whole ? f.stride : n * (kb + vb) + md;
         for (int32_t b = to; b < to + n; b += 32 - (b & 31))  // bits [to, to + n)
@@ -430,13 +431,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) sm.l[warp & 3][kMine * half + c] = v;
     }
     meet(false);
+    const int64_t n_rows = a.n_layers * a.T * a.Hq;
     if (tid < rows) {  // a thread per row: sum, reference, where it goes
       const float ls = (sm.l[0][tid] + sm.l[1][tid]) + (sm.l[2][tid] + sm.l[3][tid]);
       const float mo = sm.m[tid] == -INFINITY ? 0.0f : sm.m[tid] - kLift;
       const int64_t at = row_at(tid);
       sm.at[tid] = at;
       sm.inv[tid] = part.ml ? 1.0f : (ls == 0.0f ? 0.0f : 1.0f / ls);
-      if (part.ml) part.ml[sp * part.rows + at] = make_float2(mo, ls);
+      if (!in_range(at, n_rows, a.status)) sm.inv[tid] = 0.0f;
+      else if (part.ml) part.ml[sp * part.rows + at] = make_float2(mo, ls);
       else if (a.lse) a.lse[at] = ls == 0.0f ? -INFINITY : (mo + log2f(ls)) * 0.693147180559945309f;
     }
     meet(false);
@@ -453,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_wait4(o);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          if (c0 + i >= rows) break;
+          if (c0 + i >= rows || !in_range(sm.at[c0 + i], n_rows, a.status)) break;
           const float v = __uint_as_float(o[i]) * sm.inv[c0 + i];
           const int64_t to = sm.at[c0 + i] * 128 + ch;
           if (part.ml) part.o[sp * part.rows * 128 + to] = v;

@@ -114,7 +114,7 @@ __device__ __forceinline__ void copy_keys(const ExtendArgs &a, const Tile &t, co
   for (int i = 0; i < 4; ++i) {
     const int32_t in = k - g.k0, other = __shfl_sync(kFull, g.id, in & 31);
     const int32_t id = lane + 32 * i >= t.n ? -1 : in < 32 ? other : __ldg(g.fwd + in);
-    const bool ok = id >= 0 && id < a.F;
+    const bool ok = id >= 0 && id < a.F && in_range(slot, g.per, a.status);
     if (ok) {
       const uint8_t *src = a.pages + id * pg.bytes;
       copy_async4(raw + Raw<KH>::kMd + 4 * (lane + 32 * i), src + pg.meta + 8 * slot);
@@ -135,6 +135,7 @@ __device__ __forceinline__ void copy_keys(const ExtendArgs &a, const Tile &t, co
     if (id < 0 || id >= a.F) continue;
     const int32_t p0 = (g.k0 + k) * g.per, first = max(t.t0 - p0, 0);
     const int32_t n = min(p0 + g.per, t.t0 + t.n) - p0 - first;
+    if (!in_range(p0 + first - t.t0, 129 - n, a.status) || !in_range(first, g.per + 1 - n, a.status)) continue;
     copy_bulk(raw + (p0 + first - t.t0) * rowb, a.pages + id * pg.bytes + first * rowb, n * rowb, bar);
   }
   arrive_async(bar);
@@ -333,8 +334,9 @@ __global__ void __launch_bounds__(Roles<kMany>::kThreads, 1)
               if (((cnt & 3) != 0 && c + 16 < cols) || pos < 0) continue;
               // heads [base, cnt) of the block to their places; this thread alone adds to the token's sums
               const int32_t base = (cnt - 1) & ~3, most = min(cnt, min(hpb, a.G - bk.head0));
-              float *dst = a.sig_sum + ((static_cast<int64_t>(a.layer0 + li) * a.R + r) * a.cap + pos) * a.Hq + h * a.G +
-                           bk.head0 + cnt - 4;
+              const int64_t at = (static_cast<int64_t>(a.layer0 + li) * a.R + r) * a.cap + pos;
+              if (!in_range(at, static_cast<int64_t>(a.L) * a.R * a.cap, a.status)) continue;
+              float *dst = a.sig_sum + at * a.Hq + h * a.G + bk.head0 + cnt - 4;
               if (wide && most - base == 4 && tj < 0) {
                 red_add4(dst, v[0], v[1], v[2], v[3]);
               } else {

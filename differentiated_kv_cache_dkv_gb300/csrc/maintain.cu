@@ -136,6 +136,7 @@ __device__ __forceinline__ void list_plan(const PageOpArgs &a) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int32_t j = j0 + 32 * e;
+          if (!in_range(id[e], a.F, a.status)) continue;
           const bool same = a.rev_unit[id[e]] == a.unit_base + u && a.rev_idx[id[e]] == j;
           if (j < d && !same) err = DKV_E_INTERNAL;
         }
@@ -261,14 +262,14 @@ __device__ __forceinline__ void list_place(const PageOpArgs &a, int32_t nparts) 
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int32_t j = j0 + 32 * e;
-          if (j >= d) break;
+          if (j >= d || !in_range(at0 + off + j, 2 * a.F, a.status)) break;
           id[e] = a.free_list[ring(at0 + off + j, a.F)];
           old[e] = a.fwd[u * a.pmax + j];
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int32_t j = j0 + 32 * e;
-          if (j >= d) break;
+          if (j >= d || !in_range(before + off + j, a.F, a.status)) break;
           const bool ok = id[e] >= 0 && id[e] < a.F;
           a.list[before + off + j] = ok ? make_int2(old[e], id[e]) : make_int2(-1, -1);
           if (!ok) {  // the ring is not what the contract says: skip the page
@@ -291,7 +292,7 @@ __device__ __forceinline__ void list_place(const PageOpArgs &a, int32_t nparts) 
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int32_t j = j0 + 32 * e;
-          if (j >= d) break;
+          if (j >= d || !in_range(at0 + off + j, 2 * a.F, a.status) || !in_range(id[e], a.F, a.status)) break;
           a.free_list[ring(at0 + off + j, a.F)] = id[e];
           a.rev_unit[id[e]] = -1;
           a.rev_idx[id[e]] = -1;
@@ -328,7 +329,7 @@ constexpr int64_t kRowPiece = 4096;  // bytes of a row array one warp copies
 __device__ __forceinline__ void copy_rows(uint8_t *base, const PageOpArgs &a, int32_t src, int32_t dst, int64_t row,
                                           int64_t p, int lane) {
   const int64_t bytes = __ldg(a.ctx_lens + src) * row, o = p * kRowPiece;
-  if (o >= bytes) return;
+  if (o >= bytes || !in_range(bytes, a.cap * row + 1, a.status) || !in_range(dst, a.R, a.status)) return;
   const uint8_t *s = base + src * (a.cap * row) + o;
   uint8_t *d = base + dst * (a.cap * row) + o;
   const int64_t n = min(bytes - o, kRowPiece);
@@ -346,7 +347,7 @@ __device__ __forceinline__ void fork_copy(const PageOpArgs &a) {
   const int64_t b = a.page_bytes;
   for (int64_t j = warp; j < total; j += step) {
     const int2 p = a.list[j];
-    if (p.x < 0) continue;
+    if (p.x < 0 || !in_range(p.x, a.F, a.status) || !in_range(p.y, a.F, a.status)) continue;
     warp_copy(reinterpret_cast<uint4 *>(a.pages + p.y * b), reinterpret_cast<const uint4 *>(a.pages + p.x * b),
               static_cast<int32_t>(b / 16), lane);
   }
@@ -468,8 +469,9 @@ __device__ __forceinline__ void defrag_list(const PageOpArgs &a, int32_t nparts)
       mb += wsum[1][w];
     }
     const uint32_t below = (1u << lane) - 1u;
-    if (hole) a.list[h + __popc(hm & below)].y = static_cast<int32_t>(p);
-    if (mover) a.list[m + __popc(mm & below)].x = static_cast<int32_t>(p);
+    if (hole && in_range(h + __popc(hm & below), a.F, a.status)) a.list[h + __popc(hm & below)].y = static_cast<int32_t>(p);
+    if (mover && in_range(m + __popc(mm & below), a.F, a.status))
+      a.list[m + __popc(mm & below)].x = static_cast<int32_t>(p);
     __syncthreads();
   }
 }
@@ -486,6 +488,7 @@ __device__ __forceinline__ void defrag_move(const PageOpArgs &a) {
   const int64_t b = a.page_bytes;
   for (int64_t j = warp; j < total; j += step) {
     const int2 p = a.list[j];  // x: the page that moves, y: where to
+    if (!in_range(p.x, a.F, a.status) || !in_range(p.y, a.F, a.status)) continue;
     if (lane == 0) {
       const int32_t u = a.rev_unit[p.x], k = a.rev_idx[p.x];
       a.rev_unit[p.y] = u;

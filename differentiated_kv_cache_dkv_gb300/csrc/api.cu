@@ -203,7 +203,9 @@ bool valid_extend(const dkv_extend_batch *b, const dkv_pool *pool, const dkv_tab
       b->layer0 + static_cast<int64_t>(b->n_layers) > b->L || b->max_new < 0 || b->T < 0 || b->T > INT32_MAX ||
       !std::isfinite(b->scale))
     return false;
-  if (static_cast<int64_t>(b->L) * b->R * b->Hkv > INT32_MAX) return false;
+  if (static_cast<int64_t>(b->L) * b->R > INT32_MAX / b->Hkv) return false;
+  // 2^34 rows of q alone take 4 TB; below that every size fits its type
+  if (b->n_layers > 0 && b->T > (int64_t{1} << 34) / b->Hq / b->n_layers) return false;
   if ((b->k_new == nullptr) != (b->v_new == nullptr)) return false;
   if (b->T == 0) return true;
   return b->q && b->new_lens && b->ctx_lens && aligned(b->q, 16) && aligned(b->k_new, 16) && aligned(b->v_new, 16) &&
@@ -591,7 +593,7 @@ int32_t dkv_fork(const dkv_fork_batch *b, const dkv_pool *pool, const dkv_tables
   int sms = 0, pack_bps = 0;
   if (!device_info(&sms, &pack_bps)) return cuda_status(cudaErrorInvalidDevice);
   dkv::PageOpArgs a = page_op_args(pool, t, U, b->unit_base, workspace);
-  a.L = b->L; a.R = b->R; a.Hq = b->Hq; a.Hkv = b->Hkv; a.n = b->n; a.cap = b->cap;
+  a.L = b->L; a.R = b->R; a.Hq = b->sig_sum ? b->Hq : 0; a.Hkv = b->Hkv; a.n = b->n; a.cap = b->cap;
   a.V = static_cast<int64_t>(b->L) * b->n * b->Hkv;
   a.upb = dkv::plan_units(a.V);
   a.src = b->src; a.dst = b->dst; a.ctx_lens = b->ctx_lens;

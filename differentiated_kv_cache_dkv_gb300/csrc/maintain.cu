@@ -353,8 +353,8 @@ __device__ __forceinline__ void fork_copy(const PageOpArgs &a) {
   }
   if (!a.ctx_lens) return;
   // row pieces of one (layer, fork): classes, slots, significance, counts
-  const int64_t row[4] = {a.classes ? a.Hkv : 0, a.slot_of ? 4 * a.Hkv : 0, a.sig_sum ? 4 * a.Hq : 0,
-                          a.sig_cnt ? 4 : 0};
+  const int64_t row[4] = {a.classes ? a.Hkv : 0, a.slot_of ? int64_t{4} * a.Hkv : 0,
+                          a.sig_sum ? int64_t{4} * a.Hq : 0, a.sig_cnt ? 4 : 0};
   int64_t per = 0, np[4];
   for (int i = 0; i < 4; ++i) per += np[i] = (a.cap * row[i] + kRowPiece - 1) / kRowPiece;
   uint8_t *base[4] = {a.classes, reinterpret_cast<uint8_t *>(a.slot_of), reinterpret_cast<uint8_t *>(a.sig_sum),
@@ -606,7 +606,7 @@ cudaError_t launch_fork(const PageOpArgs &a, int sms, cudaStream_t s) {
   const int32_t parts = static_cast<int32_t>((a.V + a.upb - 1) / a.upb);
   const size_t bits = 8 * static_cast<size_t>((a.R + 31) / 32);
   const int64_t rows = a.ctx_lens ? static_cast<int64_t>(a.L) * a.n * a.cap : 0;
-  if (parts <= kCluster && a.V * a.pmax * a.page_bytes + rows * (5 * a.Hkv + 4 * a.Hq + 4) <= kSmallBytes) {
+  if (parts <= kCluster && a.V * a.pmax * a.page_bytes + rows * (int64_t{5} * a.Hkv + int64_t{4} * a.Hq + 4) <= kSmallBytes) {
     k_small<kForkOp><<<kCluster, kThreads, bits, s>>>(a);
     return cudaGetLastError();
   }

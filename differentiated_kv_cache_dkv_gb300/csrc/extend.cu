@@ -47,10 +47,10 @@
 // Units with at most 32 rows have a kernel of their own (extend_few.cu).
 //
 // Measured (32 heads over 8, 4 requests of 1024 new tokens over 16384 held, half
-// of those in the high list, 39% in the low one): 1513 us, 1.01 TFLOP, 669 TFLOP/s,
+// of those in the high list, 39% in the low one): 1490 us, 1.01 TFLOP, 680 TFLOP/s,
 // 35% of the measured bf16 rate.  The tensor pipe is busy for 30% of the
-// cycles: a warpgroup's tile takes 6640, of which its softmax 3730 (932 for 32
-// columns, one warp a scheduler: the latencies of the tensor-memory load, of
+// cycles: a warpgroup's tile takes 6640 (traced with a call at 1513 us), of which
+// its softmax 3730 (932 for 32 columns, one warp a scheduler: the latencies of the tensor-memory load, of
 // the scales' broadcast reads and of the exponentials follow one another) and
 // the issue of its products, their completion and the hand-overs 2900; at full
 // rate a tile's products for both warpgroups take 2048.

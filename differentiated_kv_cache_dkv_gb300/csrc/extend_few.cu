@@ -16,20 +16,20 @@
 //     the rows lie in its own lane, its scale and zero are two registers;
 //   MMA warp           issues every product.
 //
-// A row's reference m is as in extend.cu, but a row is a column here: the
+// A row's reference m is as in extend.cu (set by the first tile), and so are its
+// power of two and the care where logits are large, but a row is a column here: the
 // softmax warps meet at a named barrier once per tile, which also tells whether any
 // weight passed 2^15 and the references have to move (rarely).
 //
 // Measured (64 requests with 1 .. 8 drafts over 2048 .. 8192 tokens, 32 heads
-// over 8): 224 us for 374 MB, 1.67 TB/s, 25% of the measured copy rate.  A tile
+// over 8): 228 us for 374 MB, 1.64 TB/s, 25% of the measured copy rate.  A tile
 // takes about 2400 cycles: the conversion of K (880) and V (830) by eight warps,
 // K behind the product that read the tile before.  The kernel for 128 rows takes
-// 399 us there.  A call of four tokens over 512 takes 18 us, almost all of it
+// 315 us there.  A call of four tokens over 512 takes 18 us, almost all of it
 // the latency of one block's start, its few tiles and its end.
 #include <algorithm>
 #include <cmath>
 #include <cstddef>
-#include <type_traits>
 
 #include "token_tiles.cuh"
 
@@ -84,10 +84,10 @@ __device__ __forceinline__ float unordered(uint32_t u) {
   return __int_as_float(u & 0x80000000u ? static_cast<int32_t>(u ^ 0x80000000u) : static_cast<int32_t>(~u));
 }
 
-// Barrier of the softmax warps that also reduces a predicate.
-// All warps but the copy warps.
+// Barrier of all warps but the copy warps.
 __device__ __forceinline__ void meet_all() { asm volatile("bar.sync 2, %0;" ::"n"(32 * kCopyWarp) : "memory"); }
 
+// Barrier of the softmax warps that also reduces a predicate.
 __device__ __forceinline__ bool meet(bool p) {
   uint32_t r;
   asm volatile(
@@ -295,59 +295,58 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool masked = __any_sync(kFull, from > 0);
       const uint64_t s2 = f2_pack(s_cur, s_cur), z2 = f2_pack(z_cur, z_cur);
       const float4 *col = sm.col + (kMine / 2) * half;
-      bool odd = sm.odd != 0;
+      const bool odd = sm.odd != 0;
       uint32_t u[kMine];
-      // y - m (+ lift), -inf where masked; `plain`: y itself
-      auto logits = [&](auto which, bool plain) {
-        constexpr bool odd = decltype(which)::value;
-        tmem_ld16(ts_s, u);
-        tmem_wait16(u);
-        if constexpr (odd) {
-#pragma unroll
-          for (int c = 0; c < kMine; ++c) u[c] = __float_as_uint(__uint_as_float(u[c]) * sm.w[kMine * half + c]);
-        }
-#pragma unroll
-        for (int i = 0; i < kMine / 2; ++i) {
-          const float4 cv = col[i];
-          float y0, y1;
-          f2_unpack(f2_fma(s2, f2_pack(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1])),
-                           f2_fma(z2, f2_pack(cv.x, cv.y), plain || odd ? 0 : f2_pack(cv.z, cv.w))), y0, y1);
-          u[2 * i] = __float_as_uint(y0);
-          u[2 * i + 1] = __float_as_uint(y1);
-        }
-        if (odd && !plain) {
-#pragma unroll
-          for (int i = 0; i < kMine / 2; ++i) {
-            u[2 * i] = __float_as_uint(__uint_as_float(u[2 * i]) + col[i].z);
-            u[2 * i + 1] = __float_as_uint(__uint_as_float(u[2 * i + 1]) + col[i].w);
-          }
-        }
+      auto mask = [&] {
         if (masked) {
 #pragma unroll
           for (int c = 0; c < kMine; ++c) u[c] = c >= from ? u[c] : 0xff800000u;
         }
       };
-      bool stop = false;
-#pragma unroll 1
-      for (int pass = 0;; ++pass) {
+      // 2^x in the place of x; returns the largest
+      auto weigh = [&] {
         float mx = 0.0f;
-        if (ok && some) {
-          if (__builtin_expect(odd, 0)) logits(std::true_type{}, false);
-          else logits(std::false_type{}, false);
 #pragma unroll
-          for (int c = 0; c < kMine; c += 2) {
-            const float p0 = ex2(__uint_as_float(u[c])), p1 = ex2(__uint_as_float(u[c + 1]));
-            u[c] = __float_as_uint(p0);
-            u[c + 1] = __float_as_uint(p1);
-            mx = max3(mx, p0, p1);
-          }
+        for (int c = 0; c < kMine; c += 2) {
+          const float p0 = ex2(__uint_as_float(u[c])), p1 = ex2(__uint_as_float(u[c + 1]));
+          u[c] = __float_as_uint(p0);
+          u[c + 1] = __float_as_uint(p1);
+          mx = max3(mx, p0, p1);
         }
-        fence_before();
-        if (__builtin_expect(!meet(!ok || mx > kMost || (force && pass == 0)), 1) || pass) break;
-        // ---- the references move to the tile's maxima where those are larger
-        if ((stop = meet(!ok))) break;
-        if (some) {
-          logits(std::true_type{}, true);  // shifts are 0 where no row is odd
+        return mx;
+      };
+      float mx = 0.0f;
+      if (ok && some && !odd) {  // y - m + lift in one multiply-add a value, -inf where masked
+        tmem_ld16(ts_s, u);
+        tmem_wait16(u);
+#pragma unroll
+        for (int i = 0; i < kMine / 2; ++i) {
+          const float4 cv = col[i];
+          float y0, y1;
+          f2_unpack(f2_fma(s2, f2_pack(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1])),
+                           f2_fma(z2, f2_pack(cv.x, cv.y), f2_pack(cv.z, cv.w))), y0, y1);
+          u[2 * i] = __float_as_uint(y0);
+          u[2 * i + 1] = __float_as_uint(y1);
+        }
+        mask();
+        mx = weigh();
+      }
+      fence_before();
+      if (__builtin_expect(meet(!ok || mx > kMost || force || odd), 0)) {
+        // ---- the references move to the tile's maxima where those are larger; y is
+        // rounded before they are taken off, and rows' own shifts are taken back
+        bool stop = meet(!ok);
+        if (!stop && some) {
+          tmem_ld16(ts_s, u);
+          tmem_wait16(u);
+#pragma unroll
+          for (int i = 0; i < kMine / 2; ++i) {
+            const float4 cv = col[i];
+            const float2 w = *reinterpret_cast<const float2 *>(sm.w + kMine * half + 2 * i);
+            u[2 * i] = __float_as_uint(fmaf(s_cur, __uint_as_float(u[2 * i]) * w.x, z_cur * cv.x));
+            u[2 * i + 1] = __float_as_uint(fmaf(s_cur, __uint_as_float(u[2 * i + 1]) * w.y, z_cur * cv.y));
+          }
+          mask();
 #pragma unroll 1
           for (int c = 0; c < kMine; ++c) {
             uint32_t v = 0;  // u[c], with the loop kept short
@@ -357,8 +356,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) atomicMax(&sm.top[kMine * half + c], k);
           }
         }
-        if (j > 0) ok = warp_wait(&sm.odone, (j - 1) & 1u);
-        if ((stop = meet(!ok))) break;
+        if (!stop && j > 0) ok = warp_wait(&sm.odone, (j - 1) & 1u);
+        stop = stop || meet(!ok);
+        if (stop) {
+          ok = false;
+          break;
+        }
         if (tid < kCols) {
           const float m0 = sm.m[tid], m1 = fmaxf(m0, ceilf(unordered(sm.top[tid])));
           sm.f[tid] = m1 == m0 ? 1.0f : ex2(m0 - m1);  // a power of two, 0 at first
@@ -369,9 +372,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (tid == 0) sm.unset = un != 0;
           if (fabsf(m1) > kFar && m1 != -INFINITY) sm.odd = 1;
         }
-        meet(false);
+        meet(false);  // the next tile's first meeting keeps f until everyone has used it
         force = sm.unset != 0;
-        odd = sm.odd != 0;
 #pragma unroll
         for (int c = 0; c < kMine; ++c) l[c] *= sm.f[kMine * half + c];
         if (j > 0) {
@@ -384,11 +386,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_st16(tmem + lanes + kColO + kMine * half, o);
           tmem_wait_st();
         }
-        meet(false);  // everyone has used f
-      }
-      if (stop) {
-        ok = false;
-        break;
+        if (some) {
+#pragma unroll
+          for (int i = 0; i < kMine / 2; ++i) {
+            u[2 * i] = __float_as_uint(__uint_as_float(u[2 * i]) + col[i].z);
+            u[2 * i + 1] = __float_as_uint(__uint_as_float(u[2 * i + 1]) + col[i].w);
+          }
+          weigh();
+        }
       }
       // P of the tile before must have been read
       if (ok && j > 0) ok = warp_wait(&sm.odone, (j - 1) & 1u);

@@ -8,15 +8,16 @@
 // attention only has when it is done, and only the accepted rows count.
 //
 // S^T = K Q^T puts a token on a tensor-memory lane, so its scale and zero are
-// two registers and its sums plain additions of one thread in a fixed order
-// (no atomics).  A block takes a contiguous range of one unit's token tiles,
+// two registers and its sums plain additions of one thread in a fixed order.
+// A block takes a contiguous range of one unit's token tiles,
 // four tiles (a group) at a time, K converted once and resident, and streams
 // the rows of Q past them in blocks of 128 columns: `nb` columns per head, as
 // many heads as fit (a draft of eight tokens: 16 columns for each of four
 // heads), so every 16 columns belong to one head.
 //   convert warps (8)  K tiles as in the attention (codes less their middle,
-//     fp16); Q blocks as fp16 times one power of two per block, with the sums
-//     of their rows and -lse (log2) per column;
+//     fp16); Q blocks as fp16 times one power of two per block (and one of a
+//     column's own where it is far smaller), with the sums of their rows and
+//     -lse (log2) per column;
 //   copy warps (3)     K codes by bulk copies, their scales and positions by
 //     asynchronous ones, into a ring of raw tiles;
 //   MMA warp           S^T of every (block, tile) into four tensor-memory
@@ -26,9 +27,9 @@
 //     has one adder a call, so their order cannot show).
 //
 // Measured (32 heads over 8): the drafts of 64 requests over 2048 .. 8192
-// tokens 156 us for 330 MB, 2.12 TB/s, 32% of the measured copy rate (a tile
+// tokens 160 us for 330 MB, 2.06 TB/s, 31% of the measured copy rate (a tile
 // takes its conversion, about 1000 cycles, and hand-overs: 2050); 4 requests of
-// 1024 tokens over 8192 541 us for 0.262 TFLOP, 484 TFLOP/s, 25% of the measured
+// 1024 tokens over 8192 560 us for 0.262 TFLOP, 468 TFLOP/s, 24% of the measured
 // bf16 rate: a block of 128 columns against four tiles takes 7200 cycles, where
 // the products would take 2048, the exponentials 2048 and the broadcast reads of
 // the columns' sums and lse 2150 of shared memory's time, which the products'

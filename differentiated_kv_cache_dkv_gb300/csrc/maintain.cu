@@ -375,7 +375,7 @@ __device__ __forceinline__ void fork_copy(const PageOpArgs &a) {
 
 // kDefragPages page ids a block: free pages below n (the live count) and live
 // pages at or above it are counted; what the tables say of each live page is
-// checked.  part = {holes, movers << 32 | error}.
+// checked.  part = {holes, movers << 1 | error}.
 __device__ __forceinline__ void defrag_plan(const PageOpArgs &a) {
   __shared__ int64_t sm[kWarps];
   __shared__ int32_t err_s;

@@ -22,7 +22,7 @@
 // weight passed 2^15 and the references have to move (rarely).
 //
 // Measured (64 requests with 1 .. 8 drafts over 2048 .. 8192 tokens, 32 heads
-// over 8): 228 us for 374 MB, 1.64 TB/s, 25% of the measured copy rate.  A tile
+// over 8): 224 us for 374 MB, 1.67 TB/s, 25% of the measured copy rate.  A tile
 // takes about 2400 cycles: the conversion of K (880) and V (830) by eight warps,
 // K behind the product that read the tile before.  The kernel for 128 rows takes
 // 315 us there.  A call of four tokens over 512 takes 18 us, almost all of it

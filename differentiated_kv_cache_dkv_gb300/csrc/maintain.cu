@@ -24,7 +24,8 @@
 // 28-layer pool of 0.83 GB moved 157 us, 5.3 TB/s, 79%; 8 requests of 32 layers
 // released 27 us, for 400,000 pages whose entries lie scattered: the latency of
 // two kernels' dependent loads and 1.2 million 32-byte sectors; the calls on
-// one small request 10 to 14 us of dependent loads.
+// one small request 10 to 14 us of dependent loads.  (The calls alone: a timing
+// that puts the tables back before every pass adds 5 to 12 us.)
 #include <cuda_runtime.h>
 
 #include <algorithm>

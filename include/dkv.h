@@ -409,6 +409,18 @@ int32_t dkv_prefill_attention(const dkv_prefill_batch *b, const dkv_pool *pool, 
  * are not changed: tokens that are kept enter the cache through
  * dkv_decode_step.
  *
+ * Precision: logits, references, sums, outputs in progress and the
+ * significance are fp32, the products' operands 16 bits.  Of K the codes enter
+ * exactly; a query value keeps its 8 bits down to 2^-19 of its row's largest;
+ * held V is rounded to fp16 (and held at +-65504), the weights against it to
+ * fp16 (none below 2^-32 of the row's largest); weights against the new tokens
+ * are the sum of two bf16 values; out is bf16.  dkv_decode_attention keeps
+ * weights and V to more bits and writes fp32.
+ * Range: queries and new keys of any finite size; a row depends on no other
+ * row's query.  Logits count as fp32 does: beyond 2^24 the largest alone is
+ * left.  New values up to 2^100.  A query that is not finite spoils its own
+ * row alone.
+ *
  * dkv_extend_significance adds to sig_sum what dkv_decode_attention's
  * significance update adds, for the first acc_lens[r] new tokens of each
  * request (drafts that were rejected leave no trace): with p(i, t) =
@@ -418,7 +430,8 @@ int32_t dkv_prefill_attention(const dkv_prefill_batch *b, const dkv_pool *pool, 
  * (the new tokens' rows when k_new is given).  Each sum is formed by one
  * thread in a fixed order, so equal inputs give equal bits.  Counts (sig_cnt)
  * are the caller's: + acc_lens[r] for every held position, acc_lens[r] - j
- * for new token j.
+ * for new token j.  lse rounded to fp32 is all that is left of a row: where
+ * |lse| passes 2^20 its p are 0 or 1 by that rounding.
  * ------------------------------------------------------------------------ */
 typedef struct dkv_extend_batch {
   int32_t L, R, Hq, Hkv;     /* the tables' shape, as in dkv_decode_batch; 1 <= Hq / Hkv <= 128 */
@@ -445,7 +458,8 @@ int32_t dkv_extend_workspace_size(const dkv_extend_batch *b, const dkv_pool *poo
 /* Attention of several new tokens (above), asynchronous; allocates nothing.
  * workspace: device, 256-byte aligned, >= dkv_extend_workspace_size bytes
  * (NULL when that is 0), scratch: calls that may overlap on the GPU (two
- * streams, two captured graphs) need one each.  Pool and tables are read
+ * streams, two captured graphs) need one each.  The size grows with T, and
+ * not otherwise in one order: ask for each shape.  Pool and tables are read
  * only.  T = 0, R = 0 or n_layers = 0 is DKV_OK with nothing launched (the
  * lengths are not looked at).  Synchronous DKV_E_INVAL: a bad shape, pointer
  * or workspace.

@@ -68,3 +68,39 @@ def test_one_large_query(rows, size, scheme):
     after = reference(st, w, q, k, v, new, new)[4][0, 0, head][1][:len(pos)]
     slack = 1e-3 * (1 + after)
     assert np.all(d >= own - slack) and np.all(d <= before[0, pos, head] + after + 1 + slack)
+
+
+@pytest.mark.parametrize("size", [1e6, 1e12, 1e20, 1e30])
+@pytest.mark.parametrize("rows", list(NEW))
+def test_one_large_new_key_and_one_large_new_value(rows, size):
+    """Rows before the key do not see it; a row after it takes its value alone or
+    not at all, by the sign of the logit.  Values are linear."""
+    new = NEW[rows]
+    w = W.small("range", L=1, lens=[300, 170], Hq=8, Hkv=2, P=16, alpha_h=0.3, alpha_l=0.0)
+    dec, _, _, ctx = make_decoder(w, 400)
+    q, k, v = draw_new(w, new, 1, 9)
+    tok = 2
+    k[0, tok, 1] = (k[0, tok, 1].float() * size).bfloat16()
+    v[0, tok, 1, 3] = size
+    st = pool_state(dec.pool, dec.tables)
+    out = torch.full(q.shape, float("nan"), dtype=torch.bfloat16, device="cuda")
+    lse = torch.full(q.shape[:3], float("nan"), device="cuda")
+    dec.extend(q.cuda(), _i32(new), ctx, max(new), out, SCALE, k_new=k.cuda(), v_new=v.cuda(), lse=lse)
+    assert libdkv.dkv_get_status(dec.pool) == libdkv.DKV_OK
+    got, gl = out[0, :new[0]].float().cpu().numpy(), lse[0, :new[0]].cpu().numpy()
+    assert np.isfinite(got).all() and np.isfinite(gl).all()
+    qd, kd, vd = (x[0, :new[0]].float().numpy().astype(np.float64) for x in (q, k, v))
+    for h in range(8):
+        kk, vv, _, _ = unit_arrays(st, h // 4, w.P, 0)
+        kk, vv = np.concatenate([kk, kd[:, h // 4]]), np.concatenate([vv, vd[:, h // 4]])
+        x = SCALE * (qd[:, h] @ kk.T)
+        x[:, -new[0]:] = np.where(np.tril(np.ones((new[0], new[0]), bool)), x[:, -new[0]:], -np.inf)
+        mx = x.max(1, keepdims=True)
+        p = np.exp(x - mx)
+        s = p.sum(1, keepdims=True)
+        p /= s
+        # half a step of bf16 of the result; fp16 weights and values, and logits of
+        # up to 60 that 300 additions leave 2^-10 uncertain: 2^-8 of the terms
+        assert np.all(np.abs(got[:, h] - p @ vv) <= 2.0 ** -8 * np.abs(p @ vv) + 2.0 ** -8 * (p @ np.abs(vv))), h
+        ls = (mx + np.log(s))[:, 0]
+        assert np.all(np.abs(gl[:, h] - ls) <= 2.0 ** -10 + 1e-4 * np.abs(ls)), h

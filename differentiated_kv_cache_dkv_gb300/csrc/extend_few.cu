@@ -336,6 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---- the references move to the tile's maxima where those are larger; y is
         // rounded before they are taken off, and rows' own shifts are taken back
         bool stop = meet(!ok);
+        __syncwarp();
         if (!stop && some) {
           tmem_ld16(ts_s, u);
           tmem_wait16(u);
@@ -377,6 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < kMine; ++c) l[c] *= sm.f[kMine * half + c];
         if (j > 0) {
+          __syncwarp();
           fence_after();
           uint32_t o[kMine];
           tmem_ld16(tmem + lanes + kColO + kMine * half, o);

@@ -630,6 +630,8 @@ class Decoder:
     def _scratch(self, n: int, stream) -> torch.Tensor:
         # memory of the stream it is first used on: another stream's could still
         # be read or written by work that had it before
+        if stream is not None and not isinstance(stream, torch.cuda.Stream):  # another library's
+            stream = torch.cuda.ExternalStream(stream.cuda_stream, device=self.device)
         with torch.cuda.stream(stream):
             return torch.empty(n, dtype=torch.uint8, device=self.device)
 

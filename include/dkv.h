@@ -431,7 +431,7 @@ int32_t dkv_prefill_attention(const dkv_prefill_batch *b, const dkv_pool *pool, 
  * thread in a fixed order, so equal inputs give equal bits.  Counts (sig_cnt)
  * are the caller's: + acc_lens[r] for every held position, acc_lens[r] - j
  * for new token j.  lse rounded to fp32 is all that is left of a row: where
- * |lse| passes 2^20 its p are 0 or 1 by that rounding.
+ * |lse| passes 2^20 its p are 0 or 1 by that rounding; p below 2^-126 are 0.
  * ------------------------------------------------------------------------ */
 typedef struct dkv_extend_batch {
   int32_t L, R, Hq, Hkv;     /* the tables' shape, as in dkv_decode_batch; 1 <= Hq / Hkv <= 128 */

@@ -2,6 +2,8 @@
 stream: another stream's could still be in use by work that had it before."""
 from __future__ import annotations
 
+from types import SimpleNamespace
+
 import pytest
 import torch
 
@@ -23,7 +25,7 @@ def _i32(x):
     return torch.tensor(list(x), dtype=torch.int32, device="cuda")
 
 
-@pytest.mark.parametrize("side", [False, True])
+@pytest.mark.parametrize("side", ["current", "side", "another library's"])
 def test_scratch_is_memory_of_the_call_s_stream(side):
     w = W.small("scratch", L=1, lens=[2000, 0], Hq=8, Hkv=2)
     dec, _, _, ctx = make_decoder(w, 2080)
@@ -32,7 +34,8 @@ def test_scratch_is_memory_of_the_call_s_stream(side):
     outs = [torch.empty_like(x) for x in (q, q2)]
     lens, lists = [_i32([4, 0]), _i32([40, 0])], [_i32([0]), _i32([1])]  # alive until the side stream is done
     torch.cuda.synchronize()
-    s = torch.cuda.Stream() if side else None
+    keep = torch.cuda.Stream()
+    s = {"current": None, "side": keep, "another library's": SimpleNamespace(cuda_stream=keep.cuda_stream)}[side]
     want = torch.cuda.current_stream().cuda_stream if s is None else s.cuda_stream
     # the second call outgrows the first one's
     dec.extend(q, lens[0], ctx, 4, outs[0], SCALE, k_new=k, v_new=v, stream=s)

@@ -418,8 +418,8 @@ int32_t dkv_prefill_attention(const dkv_prefill_batch *b, const dkv_pool *pool, 
  * weights and V to more bits and writes fp32.
  * Range: queries and new keys of any finite size; a row depends on no other
  * row's query.  Logits count as fp32 does: beyond 2^24 the largest alone is
- * left.  New values up to 2^100.  A query that is not finite spoils its own
- * row alone.
+ * left, and one that passes fp32's range spoils its row.  New values up to
+ * 2^100.  A query that is not finite spoils its own row alone.
  *
  * dkv_extend_significance adds to sig_sum what dkv_decode_attention's
  * significance update adds, for the first acc_lens[r] new tokens of each
@@ -437,7 +437,7 @@ typedef struct dkv_extend_batch {
   int32_t L, R, Hq, Hkv;     /* the tables' shape, as in dkv_decode_batch; 1 <= Hq / Hkv <= 128 */
   int32_t cap;               /* positions per request (sig_sum rows); ctx + new <= cap */
   int32_t layer0, n_layers;  /* attend layers [layer0, layer0 + n_layers) of the tables */
-  int32_t max_new;           /* >= every new_lens[r] */
+  int32_t max_new;           /* >= every new_lens[r]; the work is divided by it, so that exact is fastest */
   int64_t T;                 /* sum of new_lens */
   const void *q;             /* bf16 [n_layers][T][Hq][128], 16-byte aligned */
   const void *k_new;         /* bf16 [n_layers][T][Hkv][128], finite, or NULL; 16-byte aligned */

@@ -262,6 +262,61 @@ bool valid_list(int32_t L, int32_t R, int32_t Hkv, int32_t n) {
          static_cast<int64_t>(L) * R <= INT32_MAX / Hkv;
 }
 
+// The shape, pages and pointers both calls of a chunk share.
+bool valid_chunk(const dkv_chunk_batch *b, const dkv_chunk_pages *p) {
+  if (!b || !p || b->L < 1 || b->L > 65535 || b->R < 0 || b->R > 65535 || b->Hkv < 1 || b->Hq < b->Hkv || b->Hq % b->Hkv != 0 ||
+      b->Hq > dkv::kMaxHq || b->cap < 1 || b->layer0 < 0 || b->n_layers < 0 ||
+      b->layer0 + static_cast<int64_t>(b->n_layers) > b->L || b->max_new < 0 || b->T < 0 || b->T > INT32_MAX ||
+      !std::isfinite(b->scale) || !(b->scale > 0.0f))
+    return false;
+  if (p->F < 1 || p->F > INT32_MAX || p->B < 8 || p->B > 128 || (p->B & (p->B - 1)) || p->tmax < 1 ||
+      static_cast<int64_t>(p->tmax) * p->B < b->cap)
+    return false;
+  // rows of the pages and of q are 32-bit TMA coordinates; units and the sums of their tiles stay below 2^62
+  if (p->F > INT32_MAX / p->B / b->L || static_cast<int64_t>(b->R) * p->tmax > INT32_MAX ||
+      static_cast<int64_t>(b->n_layers) * b->R > INT32_MAX / b->Hkv ||
+      (b->n_layers > 0 && b->T > INT32_MAX / b->n_layers))
+    return false;
+  if (b->q_stride < 0 || b->q_stride % 8 != 0 || (b->q_stride && b->q_stride < b->Hq * int64_t{128}) ||
+      b->q_stride > (int64_t{1} << 32) || b->kv_stride < 0 || b->kv_stride % 8 != 0 ||
+      (b->kv_stride && b->kv_stride < b->Hkv * int64_t{128}) || b->kv_stride > (int64_t{1} << 32))
+    return false;
+  if ((b->k_new == nullptr) != (b->v_new == nullptr)) return false;
+  if (b->T == 0 || b->R == 0 || b->n_layers == 0) return true;
+  return b->q && b->new_lens && b->ctx_lens && p->k && p->v && p->table && aligned(b->q, 16) && aligned(b->k_new, 16) &&
+         aligned(b->v_new, 16) && aligned(b->new_lens, 4) && aligned(b->ctx_lens, 4) && aligned(b->lse, 4) &&
+         aligned(p->k, 16) && aligned(p->v, 16) && aligned(p->table, 4);
+}
+
+dkv::ChunkArgs chunk_args(const dkv_chunk_batch *b, const dkv_chunk_pages *p, const dkv_pool *pool) {
+  dkv::ChunkArgs a{};
+  a.L = b->L; a.R = b->R; a.Hq = b->Hq; a.Hkv = b->Hkv; a.G = b->Hq / b->Hkv; a.cap = b->cap; a.layer0 = b->layer0;
+  a.n_layers = b->n_layers; a.max_new = b->max_new; a.B = p->B; a.tmax = p->tmax; a.T = b->T; a.F = p->F;
+  a.q_stride = b->q_stride ? b->q_stride : b->Hq * int64_t{128};
+  a.kv_stride = b->kv_stride ? b->kv_stride : b->Hkv * int64_t{128};
+  a.scale = b->scale;
+  a.q = static_cast<const uint16_t *>(b->q);
+  a.k_new = static_cast<const uint16_t *>(b->k_new);
+  a.v_new = static_cast<const uint16_t *>(b->v_new);
+  a.new_lens = b->new_lens; a.ctx_lens = b->ctx_lens; a.table = p->table;
+  a.k = static_cast<uint16_t *>(p->k);
+  a.v = static_cast<uint16_t *>(p->v);
+  a.out = static_cast<uint16_t *>(b->out); a.lse = b->lse;
+  a.status = pool ? pool->status : nullptr;
+  return a;
+}
+
+bool valid_evict(const dkv_evict_batch *b, const dkv_pool *pool, const dkv_tables *t) {
+  if (!b || !valid_pool(pool) || !t || !t->fwd || !t->unit_hdr || !aligned(t->unit_hdr, 16) || !aligned(t->fwd, 4) ||
+      t->pmax < 1)
+    return false;
+  if (!valid_list(b->L, b->R, b->Hkv, 0) || b->Hq < b->Hkv || b->Hq % b->Hkv != 0 || b->cap < 16 || b->cap % 16 != 0 ||
+      b->cap > dkv::kEvictCap || b->sinks < 0 || b->window < 0 || b->reserved != 0)
+    return false;
+  const int64_t U = static_cast<int64_t>(b->L) * b->R * b->Hkv;
+  return b->unit_base >= 0 && b->unit_base + U <= INT32_MAX;
+}
+
 // Largest head group per apply block whose shared memory fits; 0 if none.
 int32_t apply_heads(int32_t Hkv, int32_t words, int32_t pmax) {
   int32_t hpc = Hkv < dkv::kMaxApplyWarps ? Hkv : dkv::kMaxApplyWarps;
@@ -569,6 +624,67 @@ int32_t dkv_extend_significance(const dkv_extend_batch *b, const int32_t *acc_le
   a.acc_lens = acc_lens;
   a.sig_sum = sig_sum;
   return cuda_status(dkv::launch_extend_sig(a, static_cast<cudaStream_t>(stream)));
+}
+
+int32_t dkv_chunk_workspace_size(const dkv_chunk_batch *b, const dkv_chunk_pages *pages, size_t *bytes) {
+  if (!bytes || !valid_chunk(b, pages)) return DKV_E_INVAL;
+  *bytes = 0;
+  if (b->T == 0 || b->R == 0 || b->n_layers == 0) return DKV_OK;
+  *bytes = dkv::chunk_workspace(chunk_args(b, pages, nullptr));
+  return DKV_OK;
+}
+
+int32_t dkv_chunk_attention(const dkv_chunk_batch *b, const dkv_chunk_pages *pages, const dkv_pool *pool,
+                            void *workspace, size_t workspace_bytes, void *stream) {
+  if (!valid_chunk(b, pages) || !pool || !pool->status || !aligned(pool->status, 4)) return DKV_E_INVAL;
+  if (b->T == 0 || b->R == 0 || b->n_layers == 0) return DKV_OK;
+  if (!b->out || !aligned(b->out, 16)) return DKV_E_INVAL;
+  const dkv::ChunkArgs a = chunk_args(b, pages, pool);
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < dkv::chunk_workspace(a)) return DKV_E_INVAL;
+  return cuda_status(dkv::launch_chunk(a, workspace, static_cast<cudaStream_t>(stream)));
+}
+
+int32_t dkv_chunk_significance(const dkv_chunk_batch *b, const dkv_chunk_pages *pages, float *sig_sum,
+                               const dkv_pool *pool, void *stream) {
+  if (!valid_chunk(b, pages) || !pool || !pool->status || !aligned(pool->status, 4)) return DKV_E_INVAL;
+  if (b->T == 0 || b->R == 0 || b->n_layers == 0) return DKV_OK;
+  if (!b->lse || !sig_sum || !aligned(sig_sum, 16)) return DKV_E_INVAL;
+  dkv::ChunkArgs a = chunk_args(b, pages, pool);
+  a.sig_sum = sig_sum;
+  return cuda_status(dkv::launch_chunk_sig(a, static_cast<cudaStream_t>(stream)));
+}
+
+int32_t dkv_evict_workspace_size(const dkv_evict_batch *b, const dkv_pool *pool, const dkv_tables *t, size_t *bytes) {
+  if (!bytes || !valid_evict(b, pool, t)) return DKV_E_INVAL;
+  *bytes = dkv::evict_ws_layout(static_cast<int64_t>(b->L) * b->R * b->Hkv, b->cap).bytes;
+  return DKV_OK;
+}
+
+int32_t dkv_evict(const dkv_evict_batch *b, const dkv_pool *pool, const dkv_tables *t, void *workspace,
+                  size_t workspace_bytes, void *stream) {
+  if (!valid_evict(b, pool, t)) return DKV_E_INVAL;
+  if (!b->budgets || !b->ctx_lens || !b->sig_sum || !b->classes || !b->slot_of || !aligned(b->budgets, 4) ||
+      !aligned(b->ctx_lens, 4) || !aligned(b->sig_sum, 16) || !aligned(b->sig_cnt, 4) || !aligned(b->slot_of, 4))
+    return DKV_E_INVAL;
+  dkv::EvictArgs a{};
+  a.U = static_cast<int64_t>(b->L) * b->R * b->Hkv;
+  const dkv::EvictWsLayout lay = dkv::evict_ws_layout(a.U, b->cap);
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < lay.bytes) return DKV_E_INVAL;
+  a.pg = dkv::page_geom(pool->scheme, pool->P);
+  a.L = b->L; a.R = b->R; a.Hq = b->Hq; a.Hkv = b->Hkv; a.G = b->Hq / b->Hkv; a.P = pool->P; a.pmax = t->pmax;
+  a.cap = b->cap; a.sinks = b->sinks; a.window = b->window; a.F = pool->F; a.unit_base = b->unit_base;
+  a.budgets = b->budgets; a.ctx_lens = b->ctx_lens; a.sig_sum = b->sig_sum; a.sig_cnt = b->sig_cnt;
+  a.classes = b->classes; a.slot_of = b->slot_of;
+  a.free_list = pool->free_list; a.cursors = pool->cursors; a.rev_unit = pool->rev_unit; a.rev_idx = pool->rev_idx;
+  a.page_cls = pool->page_cls; a.pages = pool->pages; a.status = pool->status;
+  a.fwd = t->fwd; a.unit_hdr = t->unit_hdr;
+  uint8_t *w = static_cast<uint8_t *>(workspace);
+  a.ws = reinterpret_cast<dkv::EvictWsHeader *>(w);
+  a.unit = reinterpret_cast<dkv::EvictUnit *>(w + lay.unit);
+  a.off = reinterpret_cast<int64_t *>(w + lay.off);
+  a.gone = reinterpret_cast<uint32_t *>(w + lay.gone);
+  a.keys = reinterpret_cast<uint32_t *>(w + lay.keys);
+  return cuda_status(dkv::launch_evict(a, static_cast<cudaStream_t>(stream)));
 }
 
 int32_t dkv_page_ops_workspace_size(const dkv_pool *pool, int64_t U, size_t *bytes) {

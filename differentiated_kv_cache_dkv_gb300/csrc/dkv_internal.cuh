@@ -457,6 +457,72 @@ struct ExtendPlan {
   size_t o, bytes;  // workspace: float2 [parts][rows] at 0, float [parts][rows][128] at o
 };
 
+// Attention of a chunk over bf16 pages, and its significance (chunk.cu, chunk_sig.cu).
+struct ChunkArgs {
+  int32_t L, R, Hq, Hkv, G, cap, layer0, n_layers, max_new, B, tmax;
+  int64_t T, F, q_stride, kv_stride;  // strides in elements
+  float scale;
+  const uint16_t *q, *k_new, *v_new;
+  const int32_t *new_lens, *ctx_lens, *table;
+  uint16_t *k, *v;  // pages
+  uint16_t *out;
+  float *lse, *sig_sum;
+  int32_t *status;
+};
+
+// Eviction (evict.cu).
+constexpr int32_t kEvictCap = 1 << 18;   // positions per request: bitmaps of them lie in shared memory
+constexpr int32_t kEvictKeys = 40960;    // of them, those whose keys do too
+
+struct EvictWsHeader {
+  uint64_t tail;   // the free list's tail before the call
+  int32_t err;     // first error of the plans, in no order; nothing is changed then
+  int32_t pad[13];
+};
+
+// What the plan leaves of a unit (keep < 0: the unit stays as it is).
+struct EvictUnit {
+  int32_t keep_hi, keep_lo, freed, pad;
+};
+
+struct EvictWsLayout {
+  size_t unit;   // EvictUnit [U]
+  size_t off;    // int64 [U]: freed pages of the units before
+  size_t gone;   // uint32 [U][cap / 32, rounded up]: evicted positions
+  size_t keys;   // uint32 [U][cap], where a unit's keys do not fit shared memory
+  size_t bytes;
+};
+
+inline EvictWsLayout evict_ws_layout(int64_t U, int32_t cap) {
+  EvictWsLayout w{};
+  size_t o = align256(sizeof(EvictWsHeader));
+  w.unit = o; o = align256(o + sizeof(EvictUnit) * static_cast<size_t>(U));
+  w.off = o;  o = align256(o + sizeof(int64_t) * static_cast<size_t>(U));
+  w.gone = o; o = align256(o + 4 * static_cast<size_t>(U) * ((cap + 31) / 32));
+  w.keys = o; o = align256(o + (cap > kEvictKeys ? 4 * static_cast<size_t>(U) * cap : 0));
+  w.bytes = o;
+  return w;
+}
+
+struct EvictArgs {
+  PageGeom pg;
+  int32_t L, R, Hq, Hkv, G, P, pmax, cap, sinks, window;
+  int64_t F, U, unit_base;
+  const int32_t *budgets, *ctx_lens, *sig_cnt;
+  const float *sig_sum;
+  uint8_t *classes;
+  int32_t *slot_of;
+  int32_t *free_list;
+  uint64_t *cursors;
+  int32_t *rev_unit, *rev_idx;
+  uint8_t *page_cls, *pages;
+  int32_t *status, *fwd, *unit_hdr;
+  EvictWsHeader *ws;
+  EvictUnit *unit;
+  int64_t *off;
+  uint32_t *gone, *keys;
+};
+
 }  // namespace dkv
 
 // Launchers (defined in the kernel translation units).
@@ -488,4 +554,8 @@ ExtendPlan extend_plan(int64_t units, bool equal, int32_t max_new, int32_t G, in
 cudaError_t launch_extend(const ExtendArgs &a, const ExtendPlan &p, void *ws, cudaStream_t s);
 cudaError_t launch_extend_few(const ExtendArgs &a, const ExtendPlan &p, const ExtendPartial &part, cudaStream_t s);
 cudaError_t launch_extend_sig(const ExtendArgs &a, cudaStream_t s);
+cudaError_t launch_chunk(const ChunkArgs &a, void *ws, cudaStream_t s);
+cudaError_t launch_chunk_sig(const ChunkArgs &a, cudaStream_t s);
+size_t chunk_workspace(const ChunkArgs &a);
+cudaError_t launch_evict(const EvictArgs &a, cudaStream_t s);
 }  // namespace dkv

@@ -1,0 +1,540 @@
+// evict.cu -- eviction of a unit's least attended tokens (dkv_evict).
+//
+// DiffKV (arXiv 2412.03131) prunes by a threshold on the average attention a
+// token has received; a pool that runs out needs a bound on the tokens
+// instead.  Of a unit's held tokens those with the K largest weights w(p)
+// stay, K the budget: a selection, no sort.
+//
+//   k_evict_plan   a block per unit: the weights become 32-bit keys in the
+//     order of the floats (in shared memory), four counting passes of 8 bits
+//     find the K-th largest key T and how many equal to it stay; the position
+//     of the last of those decides between equals.  Survivors and evicted are
+//     counted against headers and slots, pages against the reverse table: all
+//     that could be wrong is found here.  Leaves the survivors' counts and the
+//     evicted positions as bits.
+//   k_evict_scan   one block: freed pages of the units before each (prefix
+//     sum), the first error, the tail.  After an error nothing is changed.
+//   k_evict_apply  a block per unit: a bitmap of the slots that stay, whose
+//     prefix counts give every mover its hole; the moves, a group of lanes
+//     each; the cleared slots, the tables and the ring.
+//
+// What bounds it: the significance (4 Hq bytes a position) and the moved
+// tokens' bytes.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "dkv_internal.cuh"
+
+namespace dkv {
+
+namespace {
+
+constexpr unsigned kFull = 0xffffffffu;
+constexpr int kPlanThreads = 512, kScanThreads = 1024, kApplyThreads = 256;
+constexpr int kMoves = 2048;  // moves a block lists at a time
+
+// Order of the floats as unsigned numbers; 0 is left for "not held" and the
+// largest for the protected; a NaN is below every number.
+__device__ __forceinline__ uint32_t order_key(float x) {
+  const uint32_t b = __float_as_uint(x + 0.0f);  // -0 counts as 0
+  if (x != x) return 1u;
+  return (b & 0x80000000u) ? ~b : b | 0x80000000u;
+}
+
+// Sum over the block, to every thread; `sm` holds one int a warp.
+__device__ __forceinline__ int32_t block_sum(int32_t x, int32_t *sm) {
+  x = __reduce_add_sync(kFull, x);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = x;
+  __syncthreads();
+  int32_t t = 0;
+  for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) t += sm[w];
+  return t;
+}
+
+// A unit of the tables: its request, head, and where its rows start.
+struct Place {
+  int32_t r, h;
+  int64_t row;  // index of position 0 in [L][R * cap]
+};
+__device__ __forceinline__ Place place_of(const EvictArgs &a, int32_t u) {
+  const uint32_t lr = static_cast<uint32_t>(u) / a.Hkv;
+  Place p;
+  p.h = static_cast<int32_t>(static_cast<uint32_t>(u) - lr * a.Hkv);
+  p.r = static_cast<int32_t>(lr % a.R);
+  p.row = static_cast<int64_t>(lr) * a.cap;
+  return p;
+}
+
+// Words of the slot bitmaps: the high list's, then the low list's.
+__device__ __forceinline__ int32_t words_of(int32_t n) { return (n + 31) >> 5; }
+
+__global__ void __launch_bounds__(kPlanThreads) k_evict_plan(const __grid_constant__ EvictArgs a) {
+  extern __shared__ uint32_t dyn[];
+  __shared__ int32_t sm[kPlanThreads / 32];
+  __shared__ uint32_t hist[256];
+  __shared__ int32_t pick_s[3], bad_s;
+  const int32_t u = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
+  const Place pl = place_of(a, u);
+  const int32_t ctx = __ldg(a.ctx_lens + pl.r), budget = __ldg(a.budgets + pl.r);
+  const int4 hd = *reinterpret_cast<const int4 *>(a.unit_hdr + 4 * static_cast<int64_t>(u));
+  const int32_t n_hi = hd.x, n_lo = hd.y;
+  int32_t err = 0;
+  if (ctx < 0 || ctx > a.cap) err = DKV_E_LENS;
+  else if (n_hi < 0 || n_lo < 0 || static_cast<int64_t>(n_hi) + n_lo > ctx || hd.z != (n_hi + a.P - 1) / a.P ||
+           hd.w != (n_lo + 2 * a.P - 1) / (2 * a.P) || hd.z + hd.w > a.pmax)
+    err = DKV_E_INTERNAL;
+  if (err || budget < 0 || n_hi + n_lo <= budget) {
+    if (tid == 0) a.unit[u] = EvictUnit{-1, -1, 0, err};
+    return;
+  }
+  const int32_t held = n_hi + n_lo, wh = words_of(n_hi), words = wh + words_of(n_lo);
+  uint32_t *stay = dyn, *gone = dyn + words;
+  uint32_t *key = a.cap > kEvictKeys ? a.keys + static_cast<int64_t>(u) * a.cap : dyn + 2 * (a.cap / 32 + 2);
+  for (int32_t i = tid; i < 2 * words; i += kPlanThreads) dyn[i] = 0;
+  if (tid == 0) bad_s = 0;
+  if (tid < 256) hist[tid] = 0;
+  __syncthreads();
+
+  // keys, the first counting pass, and what the classes say is held
+  int32_t hi = 0, lo = 0, safe = 0;
+  const uint8_t *cls = a.classes + pl.row * a.Hkv + pl.h;
+  const int32_t G = a.G;
+  const bool quad = (G & 3) == 0 && (a.Hq & 3) == 0;  // then a token's scores are whole 16-byte words
+  const float *sig = a.sig_sum + pl.row * a.Hq + pl.h * G;
+  const int32_t *cnt = a.sig_cnt ? a.sig_cnt + static_cast<int64_t>(pl.r) * a.cap : nullptr;
+  constexpr int kEach = 4;  // positions a thread has in flight
+  for (int32_t p0 = tid; p0 < ctx; p0 += kEach * kPlanThreads) {
+    int32_t c[kEach];
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      const int32_t p = p0 + e * kPlanThreads;
+      c[e] = p < ctx ? cls[static_cast<int64_t>(p) * a.Hkv] : 0;
+    }
+    float w[kEach];
+    if (quad) {
+#pragma unroll
+      for (int e = 0; e < kEach; ++e) {
+        const int32_t p = p0 + e * kPlanThreads;
+        w[e] = -INFINITY;
+        if (c[e]) {
+          const float4 *x = reinterpret_cast<const float4 *>(sig + static_cast<int64_t>(p) * a.Hq);
+          float4 y = __ldg(x);
+          bool nan = !(y.x == y.x && y.y == y.y && y.z == y.z && y.w == y.w);
+          w[e] = fmaxf(fmaxf(y.x, y.y), fmaxf(y.z, y.w));
+          for (int g = 1; g < (G >> 2); ++g) {
+            y = __ldg(x + g);
+            nan |= !(y.x == y.x && y.y == y.y && y.z == y.z && y.w == y.w);
+            w[e] = fmaxf(w[e], fmaxf(fmaxf(y.x, y.y), fmaxf(y.z, y.w)));
+          }
+          if (nan) w[e] = NAN;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < kEach; ++e) {
+        const int32_t p = p0 + e * kPlanThreads;
+        w[e] = -INFINITY;
+        if (c[e]) {
+          bool nan = false;
+          for (int g = 0; g < G; ++g) {
+            const float y = __ldg(sig + static_cast<int64_t>(p) * a.Hq + g);
+            nan |= y != y;
+            w[e] = fmaxf(w[e], y);
+          }
+          if (nan) w[e] = NAN;
+        }
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      const int32_t p = p0 + e * kPlanThreads;
+      if (p >= ctx) continue;
+      uint32_t k = 0;
+      if (c[e]) {
+        const bool s = p < a.sinks || p >= static_cast<int64_t>(ctx) - a.window;
+        if (c[e] > DKV_CLASS_K8V4) bad_s = 1;
+        hi += c[e] == DKV_CLASS_K8V4;
+        lo += c[e] == DKV_CLASS_K4V2;
+        safe += s;
+        if (cnt) w[e] = __fdiv_rn(w[e], static_cast<float>(__ldg(cnt + p)));
+        k = s ? 0xffffffffu : order_key(w[e]);
+        atomicAdd(hist + (k >> 24), 1u);
+      }
+      key[p] = k;
+    }
+  }
+  hi = block_sum(hi, sm);
+  lo = block_sum(lo, sm);
+  safe = block_sum(safe, sm);
+  if (hi != n_hi || lo != n_lo || bad_s) err = DKV_E_INTERNAL;
+  const int32_t K = max(budget, safe);
+  if (err || K >= held) {  // block-wide alike
+    if (tid == 0) a.unit[u] = EvictUnit{-1, -1, 0, err};
+    return;
+  }
+
+  // T: the K-th largest key; `left`: how many of the keys equal to it stay
+  uint32_t T = 0xffffffffu;
+  int32_t left = 0, ties = 0;
+  if (K > 0) {
+    T = 0;
+    left = K;
+    for (int shift = 24; shift >= 0; shift -= 8) {
+      if (shift < 24) {
+        if (tid < 256) hist[tid] = 0;
+        __syncthreads();
+        for (int32_t p = tid; p < ctx; p += kPlanThreads) {
+          const uint32_t k = key[p];
+          if (k && (k >> (shift + 8)) == (T >> (shift + 8))) atomicAdd(hist + (k >> shift & 255u), 1u);
+        }
+        __syncthreads();
+      }
+      if (tid < 32) {  // lane i: buckets 255 - 8 i and down
+        int32_t n[8], sum = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum += n[j] = static_cast<int32_t>(hist[255 - 8 * lane - j]);
+        int32_t above = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int32_t x = __shfl_up_sync(kFull, above, o);
+          if (lane >= o) above += x;
+        }
+        above -= sum;
+        if (above < left && above + sum >= left) {
+          int j = 0;
+          while (above + n[j] < left) above += n[j++];
+          pick_s[0] = 255 - 8 * lane - j;
+          pick_s[1] = left - above;
+          pick_s[2] = n[j];
+        }
+      }
+      __syncthreads();
+      T |= static_cast<uint32_t>(pick_s[0]) << shift;
+      left = pick_s[1];
+      ties = pick_s[2];
+      __syncthreads();
+    }
+  }
+  // of more equals than may stay the lowest positions do: up to the left-th
+  if (ties > left) {
+    if (tid < 32) {
+      int32_t seen = 0, cut = -1;
+      for (int32_t p = lane; p - lane < ctx; p += 32) {
+        uint32_t m = __ballot_sync(kFull, p < ctx && key[p] == T);
+        if (seen + __popc(m) >= left) {
+          while (seen + 1 < left) {
+            m &= m - 1u;
+            ++seen;
+          }
+          cut = p - lane + __ffs(m) - 1;
+          break;
+        }
+        seen += __popc(m);
+      }
+      if (lane == 0) pick_s[0] = cut;
+    }
+    __syncthreads();
+  } else {
+    if (tid == 0) pick_s[0] = left > 0 ? ctx : -1;
+    __syncthreads();
+  }
+  const int32_t cut = pick_s[0];
+
+  // survivors and evicted, by slot and by position
+  uint32_t *gone_pos = a.gone + static_cast<int64_t>(u) * ((a.cap + 31) / 32);
+  const int32_t *slots = a.slot_of + pl.row * a.Hkv + pl.h;
+  bool bad = false;
+  for (int32_t p0 = 0; p0 < ctx; p0 += kPlanThreads) {
+    const int32_t p = p0 + tid;
+    bool out = false;
+    const uint32_t k = p < ctx ? key[p] : 0;
+    if (k) {
+      const int32_t c = cls[static_cast<int64_t>(p) * a.Hkv], s = slots[static_cast<int64_t>(p) * a.Hkv];
+      const bool high = c == DKV_CLASS_K8V4;
+      out = !(k > T || (k == T && p <= cut));
+      if (s < 0 || s >= (high ? n_hi : n_lo)) {
+        bad = true;
+      } else {
+        const uint32_t bit = 1u << (s & 31);
+        bad |= (atomicOr((out ? gone : stay) + (high ? 0 : wh) + (s >> 5), bit) & bit) != 0;
+      }
+    }
+    const uint32_t m = __ballot_sync(kFull, out);
+    if (lane == 0 && p < ctx) gone_pos[p >> 5] = m;
+  }
+  if (bad) bad_s = 1;
+  __syncthreads();
+  int32_t all = 0, kh = 0, kl = 0;
+  for (int32_t i = tid; i < words; i += kPlanThreads) {
+    all += __popc(stay[i] | gone[i]);
+    if (i < wh) kh += __popc(stay[i]);
+    else kl += __popc(stay[i]);
+  }
+  all = block_sum(all, sm);
+  kh = block_sum(kh, sm);
+  kl = block_sum(kl, sm);
+  // pages and their reverse entries
+  bool wrong = all != held;
+  for (int32_t j = tid; j < hd.z + hd.w; j += kPlanThreads) {
+    const int32_t id = a.fwd[static_cast<int64_t>(u) * a.pmax + j];
+    if (id < 0 || id >= a.F || a.rev_unit[id] != a.unit_base + u || a.rev_idx[id] != j) wrong = true;
+  }
+  if (wrong) bad_s = 1;
+  __syncthreads();
+  if (tid == 0) {
+    const int32_t freed = hd.z + hd.w - (kh + a.P - 1) / a.P - (kl + 2 * a.P - 1) / (2 * a.P);
+    a.unit[u] = bad_s ? EvictUnit{-1, -1, 0, DKV_E_INTERNAL} : EvictUnit{kh, kl, freed, 0};
+  }
+}
+
+__global__ void __launch_bounds__(kScanThreads) k_evict_scan(const __grid_constant__ EvictArgs a) {
+  __shared__ int64_t wsum[kScanThreads / 32];
+  __shared__ unsigned long long err_s;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t per = (a.U + kScanThreads - 1) / kScanThreads, u0 = tid * per, u1 = min(a.U, u0 + per);
+  if (tid == 0) err_s = ~0ull;
+  __syncthreads();
+  int64_t sum = 0;
+  unsigned long long e = ~0ull;
+  for (int64_t u = u0; u < u1; ++u) {
+    const int4 x = *reinterpret_cast<const int4 *>(a.unit + u);
+    sum += x.z;
+    if (x.w && e == ~0ull) e = static_cast<unsigned long long>(u) << 8 | static_cast<unsigned>(-x.w);
+  }
+  if (e != ~0ull) atomicMin(&err_s, e);
+  int64_t incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t x = __shfl_up_sync(kFull, incl, o);
+    if (lane >= o) incl += x;
+  }
+  if (lane == 31) wsum[warp] = incl;
+  __syncthreads();
+  int64_t before = incl - sum, total = 0;
+  for (int w = 0; w < kScanThreads / 32; ++w) {
+    if (w < warp) before += wsum[w];
+    total += wsum[w];
+  }
+  for (int64_t u = u0; u < u1; ++u) {
+    a.off[u] = before;
+    before += a.unit[u].freed;
+  }
+  if (tid == 0) {
+    const uint64_t head = a.cursors[0], tail = a.cursors[1];
+    int32_t err = err_s == ~0ull ? 0 : -static_cast<int32_t>(err_s & 0xffu);
+    if (!err && (tail < head || tail - head + static_cast<uint64_t>(total) > static_cast<uint64_t>(a.F)))
+      err = DKV_E_INTERNAL;
+    a.ws->err = err;
+    a.ws->tail = tail;
+    if (err) set_error(a.status, err);
+    else a.cursors[1] = tail + total;
+  }
+}
+
+// Where a slot of one list lies in its page.
+struct SlotAt {
+  int64_t k, v, meta, pos;  // bytes from the first page
+};
+__device__ __forceinline__ SlotAt slot_at(const EvictArgs &a, const int32_t *fw, bool high, int32_t s) {
+  const int32_t per = high ? a.P : 2 * a.P, j = s / per;
+  const int64_t ss = s - j * per, pg = static_cast<int64_t>(fw[j]) * a.pg.bytes;
+  const int32_t half = high ? 0 : 1;
+  return {pg + ss * 16 * (a.pg.kh >> half), pg + a.pg.vbase + ss * 16 * (a.pg.vh >> half), pg + a.pg.meta + 8 * ss,
+          pg + a.pg.pos + 4 * ss};
+}
+
+// Slots src[0 .. n) of a list to dst[0 .. n), kLanes lanes a move: the 16-byte
+// units of K and V, the metadata, the position.
+template <int kLanes>
+__device__ __forceinline__ void move_slots(const EvictArgs &a, const int32_t *fw, bool high, const int32_t *src,
+                                           const int32_t *dst, const int32_t *pos, int32_t n) {
+  const int32_t j = threadIdx.x % kLanes, ku = high ? a.pg.kh : a.pg.kh >> 1, vu = high ? a.pg.vh : a.pg.vh >> 1;
+  constexpr int kGroups = kApplyThreads / kLanes, kEach = 4;
+  for (int32_t m0 = threadIdx.x / kLanes; m0 < n; m0 += kGroups * kEach) {
+    uint4 x[kEach];
+    int64_t to[kEach];
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      const int32_t m = m0 + e * kGroups;
+      if (m >= n) continue;
+      const SlotAt f = slot_at(a, fw, high, src[m]), t = slot_at(a, fw, high, dst[m]);
+      to[e] = j < ku ? t.k + 16 * j : (j < ku + vu ? t.v + 16 * (j - ku) : (j == ku + vu ? t.meta : t.pos));
+      if (j < ku + vu) {
+        x[e] = *reinterpret_cast<const uint4 *>(a.pages + (j < ku ? f.k + 16 * j : f.v + 16 * (j - ku)));
+      } else if (j == ku + vu) {
+        const uint2 y = *reinterpret_cast<const uint2 *>(a.pages + f.meta);
+        x[e].x = y.x;
+        x[e].y = y.y;
+      } else {
+        x[e].x = static_cast<uint32_t>(pos[m]);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      if (m0 + e * kGroups >= n) continue;
+      uint8_t *p = a.pages + to[e];
+      if (j < ku + vu) *reinterpret_cast<uint4 *>(p) = x[e];
+      else if (j == ku + vu) *reinterpret_cast<uint2 *>(p) = make_uint2(x[e].x, x[e].y);
+      else if (j == ku + vu + 1) *reinterpret_cast<uint32_t *>(p) = x[e].x;
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kApplyThreads) k_evict_apply(const __grid_constant__ EvictArgs a) {
+  extern __shared__ uint32_t dyn[];
+  __shared__ int32_t src[kMoves], dst[kMoves], pos[kMoves];
+  __shared__ int32_t wsum[kApplyThreads / 32];
+  if (a.ws->err) return;
+  const int32_t u = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const EvictUnit un = a.unit[u];
+  if (un.keep_hi < 0) return;
+  const Place pl = place_of(a, u);
+  const int32_t ctx = __ldg(a.ctx_lens + pl.r);
+  const int4 hd = *reinterpret_cast<const int4 *>(a.unit_hdr + 4 * static_cast<int64_t>(u));
+  const int32_t wh = words_of(hd.x), words = wh + words_of(hd.y);
+  uint32_t *stay = dyn, *rank = dyn + words;  // slots that stay, and how many of them before a word
+  for (int32_t i = tid; i < words; i += kApplyThreads) stay[i] = 0;
+  __syncthreads();
+
+  // the evicted leave the rows; the others' slots make the bitmap
+  uint8_t *cls = a.classes + pl.row * a.Hkv + pl.h;
+  int32_t *slots = a.slot_of + pl.row * a.Hkv + pl.h;
+  const uint32_t *gone_pos = a.gone + static_cast<int64_t>(u) * ((a.cap + 31) / 32);
+  for (int32_t p = tid; p < ctx; p += kApplyThreads) {
+    const int64_t at = static_cast<int64_t>(p) * a.Hkv;
+    const int32_t c = cls[at];
+    if (!c) continue;
+    if (gone_pos[p >> 5] >> (p & 31) & 1u) {
+      cls[at] = DKV_CLASS_PRUNE;
+      slots[at] = -1;
+    } else {
+      const int32_t s = slots[at];
+      if (in_range(s, c == DKV_CLASS_K8V4 ? hd.x : hd.y, a.status))
+        atomicOr(stay + (c == DKV_CLASS_K8V4 ? 0 : wh) + (s >> 5), 1u << (s & 31));
+    }
+  }
+  __syncthreads();
+  {
+    const int32_t per = (words + kApplyThreads - 1) / kApplyThreads, i0 = min(words, tid * per), i1 = min(words, i0 + per);
+    int32_t sum = 0;
+    for (int32_t i = i0; i < i1; ++i) sum += __popc(stay[i]);
+    int32_t incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int32_t x = __shfl_up_sync(kFull, incl, o);
+      if (lane >= o) incl += x;
+    }
+    if (lane == 31) wsum[warp] = incl;
+    __syncthreads();
+    int32_t before = incl - sum;
+    for (int w = 0; w < warp; ++w) before += wsum[w];
+    for (int32_t i = i0; i < i1; ++i) {
+      rank[i] = before;
+      before += __popc(stay[i]);
+    }
+    __syncthreads();
+  }
+  const int32_t *fwd = a.fwd + static_cast<int64_t>(u) * a.pmax;
+  for (int list = 0; list < 2; ++list) {
+    const bool high = list == 0;
+    const int32_t n = high ? hd.x : hd.y, keep = high ? un.keep_hi : un.keep_lo, w0 = high ? 0 : wh;
+    if (keep == n) continue;
+    const int32_t base = high ? 0 : un.keep_hi;  // survivors of the lists before
+    const uint32_t *st = stay + w0, *rk = rank + w0;
+    auto below = [&](int32_t s) {  // survivors in slots below s
+      return s >= n ? keep : static_cast<int32_t>(rk[s >> 5]) - base + __popc(st[s >> 5] & ((1u << (s & 31)) - 1u));
+    };
+    const int32_t b_keep = below(keep), moves = keep - b_keep;
+    const int32_t *fw = fwd + (high ? 0 : hd.z);
+    for (int32_t m0 = 0; m0 < moves; m0 += kMoves) {
+      const int32_t nm = min(kMoves, moves - m0);
+      for (int32_t w = tid; w < words_of(keep); w += kApplyThreads) {
+        uint32_t hole = ~st[w];
+        if (keep - 32 * w < 32) hole &= (1u << (keep - 32 * w)) - 1u;
+        int32_t m = 32 * w - (static_cast<int32_t>(rk[w]) - base) - m0;
+        for (; hole; hole &= hole - 1u, ++m)
+          if (m >= 0 && m < nm) dst[m] = 32 * w + __ffs(hole) - 1;
+      }
+      for (int32_t p = tid; p < ctx; p += kApplyThreads) {
+        const int64_t at = static_cast<int64_t>(p) * a.Hkv;
+        if (cls[at] != (high ? DKV_CLASS_K8V4 : DKV_CLASS_K4V2)) continue;
+        const int32_t s = slots[at];
+        if (s < keep || !in_range(s, n, a.status)) continue;
+        const int32_t m = below(s) - b_keep - m0;
+        if (m >= 0 && m < nm) {
+          src[m] = s;
+          pos[m] = p;
+        }
+      }
+      __syncthreads();
+      for (int32_t m = tid; m < nm; m += kApplyThreads) slots[static_cast<int64_t>(pos[m]) * a.Hkv] = dst[m];
+      if (high) move_slots<16>(a, fw, true, src, dst, pos, nm);
+      else move_slots<8>(a, fw, false, src, dst, pos, nm);
+      __syncthreads();
+    }
+    // vacated slots of the last kept page
+    const int32_t per = high ? a.P : 2 * a.P, end = min(n, (keep + per - 1) / per * per);
+    const int32_t ku = high ? a.pg.kh : a.pg.kh >> 1, vu = high ? a.pg.vh : a.pg.vh >> 1, lanes = high ? 16 : 8;
+    for (int32_t i = tid; i < (end - keep) * lanes; i += kApplyThreads) {
+      const int32_t j = i % lanes;
+      const SlotAt t = slot_at(a, fw, high, keep + i / lanes);
+      if (j < ku) *reinterpret_cast<uint4 *>(a.pages + t.k + 16 * j) = make_uint4(0, 0, 0, 0);
+      else if (j < ku + vu) *reinterpret_cast<uint4 *>(a.pages + t.v + 16 * (j - ku)) = make_uint4(0, 0, 0, 0);
+      else if (j == ku + vu) *reinterpret_cast<uint2 *>(a.pages + t.meta) = make_uint2(0, 0);
+      else if (j == ku + vu + 1) *reinterpret_cast<int32_t *>(a.pages + t.pos) = -1;
+    }
+  }
+  __syncthreads();
+
+  // surplus pages to the ring, in the order of the row
+  int32_t *row = a.fwd + static_cast<int64_t>(u) * a.pmax;
+  const int32_t need_hi = (un.keep_hi + a.P - 1) / a.P, need_lo = (un.keep_lo + 2 * a.P - 1) / (2 * a.P);
+  const uint64_t F = static_cast<uint64_t>(a.F), at0 = (a.ws->tail + static_cast<uint64_t>(a.off[u])) % F;
+  const int32_t fh = hd.z - need_hi;
+  for (int32_t i = tid; i < un.freed; i += kApplyThreads) {
+    const int32_t id = i < fh ? row[need_hi + i] : row[hd.z + need_lo + i - fh];
+    uint64_t at = at0 + i;
+    if (at >= F) at -= F;
+    a.free_list[at] = id;
+    a.rev_unit[id] = -1;
+    a.rev_idx[id] = -1;
+    a.page_cls[id] = 0;
+  }
+  __syncthreads();
+  // the kept low pages follow the kept high ones
+  if (fh > 0) {
+    for (int32_t i0 = 0; i0 < need_lo; i0 += kApplyThreads) {
+      const int32_t i = i0 + tid, id = i < need_lo ? row[hd.z + i] : 0;
+      __syncthreads();
+      if (i < need_lo) {
+        row[need_hi + i] = id;
+        a.rev_idx[id] = need_hi + i;
+      }
+      __syncthreads();
+    }
+  }
+  for (int32_t i = need_hi + need_lo + tid; i < hd.z + hd.w; i += kApplyThreads) row[i] = -1;
+  if (tid == 0)
+    *reinterpret_cast<int4 *>(a.unit_hdr + 4 * static_cast<int64_t>(u)) = make_int4(un.keep_hi, un.keep_lo, need_hi, need_lo);
+}
+
+}  // namespace
+
+cudaError_t launch_evict(const EvictArgs &a, cudaStream_t s) {
+  const size_t maps = 8 * static_cast<size_t>(a.cap / 32 + 2);
+  const size_t plan = maps + (a.cap > kEvictKeys ? 0 : 4 * static_cast<size_t>(a.cap));
+  if (cudaError_t e = cudaFuncSetAttribute(k_evict_plan, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(plan)))
+    return e;
+  if (cudaError_t e = cudaFuncSetAttribute(k_evict_apply, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(maps)))
+    return e;
+  k_evict_plan<<<static_cast<unsigned>(a.U), kPlanThreads, plan, s>>>(a);
+  if (cudaError_t e = cudaGetLastError()) return e;
+  k_evict_scan<<<1, kScanThreads, 0, s>>>(a);
+  if (cudaError_t e = cudaGetLastError()) return e;
+  k_evict_apply<<<static_cast<unsigned>(a.U), kApplyThreads, maps, s>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace dkv

@@ -123,6 +123,32 @@ class dkv_release_batch(ctypes.Structure):
                 ("unit_base", ctypes.c_int64), ("reqs", ctypes.c_void_p)]
 
 
+class dkv_chunk_pages(ctypes.Structure):
+    _fields_ = [("F", ctypes.c_int64), ("B", ctypes.c_int32), ("tmax", ctypes.c_int32), ("k", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("table", ctypes.c_void_p)]
+
+
+class dkv_chunk_batch(ctypes.Structure):
+    _fields_ = [
+        ("L", ctypes.c_int32), ("R", ctypes.c_int32), ("Hq", ctypes.c_int32), ("Hkv", ctypes.c_int32),
+        ("cap", ctypes.c_int32), ("layer0", ctypes.c_int32), ("n_layers", ctypes.c_int32),
+        ("max_new", ctypes.c_int32), ("T", ctypes.c_int64), ("q_stride", ctypes.c_int64),
+        ("kv_stride", ctypes.c_int64), ("q", ctypes.c_void_p), ("k_new", ctypes.c_void_p),
+        ("v_new", ctypes.c_void_p), ("new_lens", ctypes.c_void_p), ("ctx_lens", ctypes.c_void_p),
+        ("scale", ctypes.c_float), ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+    ]
+
+
+class dkv_evict_batch(ctypes.Structure):
+    _fields_ = [
+        ("L", ctypes.c_int32), ("R", ctypes.c_int32), ("Hq", ctypes.c_int32), ("Hkv", ctypes.c_int32),
+        ("cap", ctypes.c_int32), ("sinks", ctypes.c_int32), ("window", ctypes.c_int32), ("reserved", ctypes.c_int32),
+        ("unit_base", ctypes.c_int64), ("budgets", ctypes.c_void_p), ("ctx_lens", ctypes.c_void_p),
+        ("sig_sum", ctypes.c_void_p), ("sig_cnt", ctypes.c_void_p), ("classes", ctypes.c_void_p),
+        ("slot_of", ctypes.c_void_p),
+    ]
+
+
 def load():
     """Load libdkv.so (raises if it was not built)."""
     global _lib
@@ -155,6 +181,11 @@ def load():
         "dkv_extend_workspace_size": ([P(dkv_extend_batch), P(dkv_pool), P(dkv_tables), P(ctypes.c_size_t)], i32),
         "dkv_extend_attention": ([P(dkv_extend_batch), P(dkv_pool), P(dkv_tables), vp, ctypes.c_size_t, vp], i32),
         "dkv_extend_significance": ([P(dkv_extend_batch), vp, vp, P(dkv_pool), P(dkv_tables), vp], i32),
+        "dkv_chunk_workspace_size": ([P(dkv_chunk_batch), P(dkv_chunk_pages), P(ctypes.c_size_t)], i32),
+        "dkv_chunk_attention": ([P(dkv_chunk_batch), P(dkv_chunk_pages), P(dkv_pool), vp, ctypes.c_size_t, vp], i32),
+        "dkv_chunk_significance": ([P(dkv_chunk_batch), P(dkv_chunk_pages), vp, P(dkv_pool), vp], i32),
+        "dkv_evict_workspace_size": ([P(dkv_evict_batch), P(dkv_pool), P(dkv_tables), P(ctypes.c_size_t)], i32),
+        "dkv_evict": ([P(dkv_evict_batch), P(dkv_pool), P(dkv_tables), vp, ctypes.c_size_t, vp], i32),
         "dkv_page_ops_workspace_size": ([P(dkv_pool), i64, P(ctypes.c_size_t)], i32),
         "dkv_fork": ([P(dkv_fork_batch), P(dkv_pool), P(dkv_tables), vp, ctypes.c_size_t, vp], i32),
         "dkv_release": ([P(dkv_release_batch), P(dkv_pool), P(dkv_tables), vp, ctypes.c_size_t, vp], i32),
@@ -528,6 +559,154 @@ def dkv_defrag(pool: DevicePool, tables, workspace: torch.Tensor, unit_base: int
         raise DkvError(rc, "dkv_defrag")
 
 
+# ------------------------------------------------- prompts in chunks, eviction --
+
+def _want(t: torch.Tensor | None, name: str, dtype: torch.dtype, shape: tuple, like: torch.Tensor,
+          contiguous: bool = True) -> None:
+    """A tensor of this type and shape (a single number: so many elements) on the device of `like`."""
+    if t is None:
+        return
+    fits = t.numel() == shape[0] if len(shape) == 1 else tuple(t.shape) == shape
+    if t.dtype != dtype or not fits or t.device != like.device or (contiguous and not t.is_contiguous()):
+        raise ValueError(f"{name}: a {'contiguous ' if contiguous else ''}{dtype} tensor of {list(shape)} on "
+                         f"{like.device} is wanted")
+
+
+def _token_stride(t: torch.Tensor, name: str) -> int:
+    """Elements from one token's rows [H][128] to the next of a view [n_layers][T][H][128]."""
+    n, T, H = int(t.shape[0]), int(t.shape[1]), int(t.shape[2])
+    s0, s1, s2, s3 = t.stride()
+    s = s1 if T > 1 else (s0 if n > 1 else H * 128)  # a stride over one element says nothing
+    if t.numel() and (s3 != 1 or (H > 1 and s2 != 128) or (n > 1 and s0 != T * s) or s < H * 128):
+        raise ValueError(f"{name}: tokens may stand apart, their {H} rows of 128 and the layers may not")
+    return int(s)
+
+
+class ChunkPages:
+    """bf16 pages [L][F][B][Hkv][128] of K and of V and the table [R][tmax] of the requests' pages (torch tensors
+    owned by this object): what the chunks of a prompt have left until its compaction."""
+
+    def __init__(self, L: int, R: int, Hkv: int, cap: int, B: int, F: int, device="cuda"):
+        self.k = torch.zeros((L, F, B, Hkv, 128), dtype=torch.bfloat16, device=device)
+        self.v = torch.zeros_like(self.k)
+        self.table = torch.full((R, -(-cap // B)), -1, dtype=torch.int32, device=device)
+
+    @classmethod
+    def from_tensors(cls, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor) -> "ChunkPages":
+        """Pages over the caller's bf16 tensors k, v [L][F][B][Hkv][128] and int32 table [R][tmax]."""
+        if k.dim() != 5 or k.shape[4] != 128 or table.dim() != 2:
+            raise ValueError("k and v [L][F][B][Hkv][128], table [R][tmax] are wanted")
+        _want(k, "k", torch.bfloat16, tuple(k.shape), k)
+        _want(v, "v", torch.bfloat16, tuple(k.shape), k)
+        _want(table, "table", torch.int32, tuple(table.shape), k)
+        self = cls.__new__(cls)
+        self.k, self.v, self.table = k, v, table
+        return self
+
+    def c(self) -> dkv_chunk_pages:
+        return dkv_chunk_pages(int(self.k.shape[1]), int(self.k.shape[2]), int(self.table.shape[1]), _p(self.k),
+                               _p(self.v), _p(self.table))
+
+
+def make_chunk_batch(Hkv: int, cap: int, q: torch.Tensor, new_lens: torch.Tensor, ctx_lens: torch.Tensor,
+                     max_new: int, scale: float, k_new: torch.Tensor | None = None,
+                     v_new: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                     lse: torch.Tensor | None = None, layer0: int = 0, L: int | None = None) -> dkv_chunk_batch:
+    """q bf16 [n_layers][T][Hq][128]; k_new, v_new bf16 [n_layers][T][Hkv][128] (views of one projection's output are
+    fine: rows of a token together, tokens at equal distances); out as q, contiguous; lse fp32 [n_layers][T][Hq];
+    new_lens, ctx_lens int32 [R].  L: layers of the pages (layer0 + n_layers where not given)."""
+    if q.dim() != 4 or q.shape[3] != 128:
+        raise ValueError("q [n_layers][T][Hq][128] is wanted")
+    n_layers, T, Hq = int(q.shape[0]), int(q.shape[1]), int(q.shape[2])
+    R = int(new_lens.numel())
+    if (k_new is None) != (v_new is None):
+        raise ValueError("k_new and v_new come together")
+    _want(q, "q", torch.bfloat16, tuple(q.shape), q, contiguous=False)
+    _want(k_new, "k_new", torch.bfloat16, (n_layers, T, int(Hkv), 128), q, contiguous=False)
+    _want(v_new, "v_new", torch.bfloat16, (n_layers, T, int(Hkv), 128), q, contiguous=False)
+    _want(out, "out", torch.bfloat16, tuple(q.shape), q)
+    _want(lse, "lse", torch.float32, (n_layers, T, Hq), q)
+    _want(new_lens, "new_lens", torch.int32, (R,), q)
+    _want(ctx_lens, "ctx_lens", torch.int32, (R,), q)
+    kv_stride = 0 if k_new is None else _token_stride(k_new, "k_new")
+    if v_new is not None and _token_stride(v_new, "v_new") != kv_stride:
+        raise ValueError("k_new and v_new: tokens at the same distances are wanted")
+    return dkv_chunk_batch(int(L if L is not None else layer0 + n_layers), R, Hq, int(Hkv), int(cap), int(layer0),
+                           n_layers, int(max_new), T, _token_stride(q, "q"), kv_stride, _p(q), _p(k_new), _p(v_new),
+                           _p(new_lens), _p(ctx_lens), float(scale), _p(out), _p(lse))
+
+
+def _chunk_pages(batch: dkv_chunk_batch, pages: ChunkPages) -> dkv_chunk_pages:
+    if pages.k.shape[0] != batch.L or pages.k.shape[3] != batch.Hkv or pages.table.shape[0] != batch.R:
+        raise ValueError(f"pages of {batch.L} layers and {batch.Hkv} KV heads and a table of {batch.R} requests are "
+                         f"wanted, not {pages.k.shape[0]}, {pages.k.shape[3]} and {pages.table.shape[0]}")
+    return pages.c()
+
+
+def dkv_chunk_workspace_size(batch: dkv_chunk_batch, pages: ChunkPages) -> int:
+    n = ctypes.c_size_t(0)
+    pc = _chunk_pages(batch, pages)
+    rc = load().dkv_chunk_workspace_size(ctypes.byref(batch), ctypes.byref(pc), ctypes.byref(n))
+    if rc != DKV_OK:
+        raise DkvError(rc, "dkv_chunk_workspace_size")
+    return int(n.value)
+
+
+def dkv_chunk_attention(batch: dkv_chunk_batch, pages: ChunkPages, pool: DevicePool, workspace: torch.Tensor | None,
+                        stream=None) -> None:
+    """Append the chunk to its pages and attend; of the pool the status word is used."""
+    gc, pc = _chunk_pages(batch, pages), pool.c()
+    rc = load().dkv_chunk_attention(ctypes.byref(batch), ctypes.byref(gc), ctypes.byref(pc), *_workspace(workspace),
+                                    _stream(stream))
+    if rc != DKV_OK:
+        raise DkvError(rc, "dkv_chunk_attention")
+
+
+def dkv_chunk_significance(batch: dkv_chunk_batch, pages: ChunkPages, sig_sum: torch.Tensor, pool: DevicePool,
+                           stream=None) -> None:
+    """sig_sum fp32 [L][R * cap][Hq]."""
+    _want(sig_sum, "sig_sum", torch.float32, (batch.L * batch.R * batch.cap * batch.Hq,), pages.k)
+    gc, pc = _chunk_pages(batch, pages), pool.c()
+    rc = load().dkv_chunk_significance(ctypes.byref(batch), ctypes.byref(gc), _p(sig_sum), ctypes.byref(pc),
+                                       _stream(stream))
+    if rc != DKV_OK:
+        raise DkvError(rc, "dkv_chunk_significance")
+
+
+def make_evict_batch(L: int, R: int, Hq: int, Hkv: int, cap: int, budgets: torch.Tensor, ctx_lens: torch.Tensor,
+                     sig_sum: torch.Tensor, classes: torch.Tensor, slot_of: torch.Tensor,
+                     sig_cnt: torch.Tensor | None = None, sinks: int = 0, window: int = 0,
+                     unit_base: int = 0) -> dkv_evict_batch:
+    """budgets, ctx_lens int32 [R]; sig_sum fp32 [L][R * cap][Hq]; classes uint8 and slot_of int32
+    [L][R * cap][Hkv]; sig_cnt int32 [R * cap], or None to compare the sums."""
+    rows = int(L) * int(R) * int(cap)
+    _want(budgets, "budgets", torch.int32, (int(R),), sig_sum)
+    _want(ctx_lens, "ctx_lens", torch.int32, (int(R),), sig_sum)
+    _want(sig_sum, "sig_sum", torch.float32, (rows * int(Hq),), sig_sum)
+    _want(sig_cnt, "sig_cnt", torch.int32, (int(R) * int(cap),), sig_sum)
+    _want(classes, "classes", torch.uint8, (rows * int(Hkv),), sig_sum)
+    _want(slot_of, "slot_of", torch.int32, (rows * int(Hkv),), sig_sum)
+    return dkv_evict_batch(int(L), int(R), int(Hq), int(Hkv), int(cap), int(sinks), int(window), 0, int(unit_base),
+                           _p(budgets), _p(ctx_lens), _p(sig_sum), _p(sig_cnt), _p(classes), _p(slot_of))
+
+
+def dkv_evict_workspace_size(batch: dkv_evict_batch, pool: DevicePool, tables) -> int:
+    n = ctypes.c_size_t(0)
+    pc, tc = pool.c(), tables.c()
+    rc = load().dkv_evict_workspace_size(ctypes.byref(batch), ctypes.byref(pc), ctypes.byref(tc), ctypes.byref(n))
+    if rc != DKV_OK:
+        raise DkvError(rc, "dkv_evict_workspace_size")
+    return int(n.value)
+
+
+def dkv_evict(batch: dkv_evict_batch, pool: DevicePool, tables, workspace: torch.Tensor, stream=None) -> None:
+    pc, tc = pool.c(), tables.c()
+    rc = load().dkv_evict(ctypes.byref(batch), ctypes.byref(pc), ctypes.byref(tc), *_workspace(workspace),
+                          _stream(stream))
+    if rc != DKV_OK:
+        raise DkvError(rc, "dkv_evict")
+
+
 class _TableView:
     """Tables of a contiguous run of units (pointer offsets into DeviceTables)."""
 
@@ -559,7 +738,7 @@ class Decoder:
         self.slot_of = torch.full((rows,), -1, dtype=torch.int32, device=device)
         self.workspace = torch.empty(dkv_decode_workspace_size(self.batch({})), dtype=torch.uint8, device=device)
         dkv_init_pool(self.pool)
-        self._pre_ws = self._ops_ws = None
+        self._pre_ws = self._ops_ws = self._evict_ws = None
         self._ext_ws: list[torch.Tensor] = []  # outgrown ones stay: a captured graph may use them
 
     def batch(self, d: dict) -> dkv_decode_batch:
@@ -652,6 +831,16 @@ class Decoder:
         """dkv_release: the requests' pages go back to the free list; the caller sets their ctx_lens to 0."""
         dkv_release(make_release_batch(self.L, self.R, self.Hkv, reqs), self.pool, self.tables,
                     self._page_ops_ws(stream), stream=stream)
+
+    def evict(self, budgets: torch.Tensor, ctx_lens: torch.Tensor, sig_sum: torch.Tensor,
+              sig_cnt: torch.Tensor | None = None, sinks: int = 0, window: int | None = None, stream=None) -> None:
+        """dkv_evict: each unit of a request keeps at most budgets[r] tokens (< 0: all), the most attended; the last
+        `window` positions (the decoder's own where not given) and the first `sinks` stay."""
+        b = make_evict_batch(self.L, self.R, self.Hq, self.Hkv, self.cap, budgets, ctx_lens, sig_sum, self.classes,
+                             self.slot_of, sig_cnt, sinks, self.window if window is None else window)
+        if self._evict_ws is None:
+            self._evict_ws = self._scratch(dkv_evict_workspace_size(b, self.pool, self.tables), stream)
+        dkv_evict(b, self.pool, self.tables, self._evict_ws, stream=stream)
 
     def defrag(self, stream=None) -> None:
         """dkv_defrag: the live pages move to the lowest ids."""

@@ -482,6 +482,98 @@ int32_t dkv_extend_significance(const dkv_extend_batch *b, const int32_t *acc_le
                                 const dkv_pool *pool, const dkv_tables *t, void *stream);
 
 /* ------------------------------------------------------------------------
+ * A prompt that arrives in chunks.  Its tokens can be classified when the last
+ * chunk is there: the score of a token averages over every token after it.
+ * Until then the earlier chunks' K and V are held as they are, in bf16 pages
+ * of their own, and each chunk attends to them and gives them significance;
+ * after the last one sig_sum holds what one dkv_prefill_attention over the
+ * whole prompt would have left, and dkv_compact takes the prompt over.
+ *
+ * Position p of request r lies in slot p mod B of page table[r][p / B], the
+ * same page in every layer.  A page may stand in several requests' rows (a
+ * shared prefix); a page that receives new tokens must stand in one.  Where a
+ * request's pages follow one another, their K and V rows are dkv_batch's k and
+ * v of one request and layer as they lie.
+ *
+ * dkv_chunk_attention: the batch's T = sum(new_lens) tokens are packed request
+ * after request; token i of request r stands at position ctx_lens[r] + i.
+ * With k_new given, the new tokens' K and V are first stored in their places.
+ * Then, for query head q of that token (KV head q / G, G = Hq / Hkv), over the
+ * positions t = 0 .. ctx_lens[r] + i:
+ *   x_t = scale * (q . k_t),  out = sum_t exp(x_t - lse) v_t,
+ *   lse = log sum_t exp(x_t).
+ * new_lens[r] = 1 is a generation step over the unquantised cache.
+ *
+ * Precision: products of bf16 values added in fp32; references, sums and
+ * outputs in progress are fp32; the weights enter the second product rounded
+ * to bf16; out is bf16.  Range: queries and keys of any finite size; a logit
+ * that passes fp32's range spoils its row; values up to 2^100.  Slots of a
+ * page behind a request's last token may hold anything.
+ *
+ * dkv_chunk_significance adds what those rows give: with p(i, t) =
+ * exp(x_t - lse) recomputed from the lse of dkv_chunk_attention,
+ *   sig_sum[l][r * cap + t][q] += sum_i p(i, t)         t < ctx_lens[r],
+ *   sig_sum[l][r * cap + ctx + j][q] = sum_{i >= j} p(i, ctx + j)   new j.
+ * Each sum is formed in a fixed order: equal inputs give equal bits.  Counts
+ * (sig_cnt) are the caller's: + new_lens[r] for every held position,
+ * new_lens[r] - j for new token j.  A row whose lse is -inf adds nothing; p
+ * below 2^-126 are 0.
+ * ------------------------------------------------------------------------ */
+typedef struct dkv_chunk_pages {
+  int64_t F;                 /* pages; 1 <= F */
+  int32_t B;                 /* tokens a page: 8, 16, 32, 64 or 128 */
+  int32_t tmax;              /* entries of a request's row of the table; tmax * B >= cap */
+  void *k, *v;               /* bf16 [L][F][B][Hkv][128], 16-byte aligned */
+  const int32_t *table;      /* int32 [R][tmax], device; entries behind a request's last token are not read */
+} dkv_chunk_pages;
+
+typedef struct dkv_chunk_batch {
+  int32_t L, R, Hq, Hkv;     /* the pages' layers, requests, heads; 1 <= Hq / Hkv <= 128 */
+  int32_t cap;               /* positions per request (sig_sum rows); ctx + new <= cap */
+  int32_t layer0, n_layers;  /* attend layers [layer0, layer0 + n_layers) of the pages */
+  int32_t max_new;           /* >= every new_lens[r]; exact is fastest */
+  int64_t T;                 /* sum of new_lens */
+  int64_t q_stride, kv_stride; /* elements from one token's row of q (of k_new and v_new) to the next, a
+                                multiple of 8; 0: Hq * 128 (Hkv * 128).  Layers follow T rows later */
+  const void *q;             /* bf16 [n_layers][T][Hq][128], 16-byte aligned */
+  const void *k_new;         /* bf16 [n_layers][T][Hkv][128], 16-byte aligned, or NULL: the pages hold the new
+                                tokens already (not read by dkv_chunk_significance) */
+  const void *v_new;         /* bf16, as k_new (NULL exactly when k_new is) */
+  const int32_t *new_lens;   /* int32 [R], device */
+  const int32_t *ctx_lens;   /* int32 [R], device */
+  float scale;               /* softmax scale, finite, > 0 */
+  void *out;                 /* out bf16 [n_layers][T][Hq][128], 16-byte aligned (attention only) */
+  float *lse;                /* fp32 [n_layers][T][Hq], natural log: out of the attention (may be
+                                NULL there), in of the significance */
+} dkv_chunk_batch;
+
+/* Workspace bytes of dkv_chunk_attention (host only). */
+int32_t dkv_chunk_workspace_size(const dkv_chunk_batch *b, const dkv_chunk_pages *pages, size_t *bytes);
+
+/* Chunk attention (above), asynchronous; allocates nothing.  workspace:
+ * device, 256-byte aligned, >= dkv_chunk_workspace_size bytes, scratch: calls
+ * that may overlap on the GPU (two streams, two captured graphs) need one
+ * each.  Of the pool only `status` is used.  T = 0, R = 0 or n_layers = 0 is
+ * DKV_OK with nothing launched (the lengths are not looked at).  Synchronous
+ * DKV_E_INVAL: a bad shape, pointer or workspace.  Device-side: DKV_E_LENS
+ * when a new_lens[r] is outside [0, max_new], ctx_lens[r] + new_lens[r] is
+ * outside [0, cap] or the lengths do not add up to T: nothing is written then;
+ * DKV_E_RANGE for a new K or V value that is not finite (stored and taken as
+ * 0); DKV_E_INTERNAL for a page id outside [0, F): nothing is stored for it
+ * and page 0 is read in its place, which leaves that request's outputs without
+ * meaning and the others as they are; DKV_E_TIMEOUT when a bounded wait gave
+ * up (outputs undefined). */
+int32_t dkv_chunk_attention(const dkv_chunk_batch *b, const dkv_chunk_pages *pages, const dkv_pool *pool,
+                            void *workspace, size_t workspace_bytes, void *stream);
+
+/* Significance of those rows (above), asynchronous; needs no workspace and
+ * allocates nothing.  K is read from the pages, the new tokens' too.  sig_sum:
+ * in/out fp32 [L][R * cap][Hq].  Errors as dkv_chunk_attention; a page id
+ * outside [0, F) leaves the sums of that page's tokens without meaning. */
+int32_t dkv_chunk_significance(const dkv_chunk_batch *b, const dkv_chunk_pages *pages, float *sig_sum,
+                               const dkv_pool *pool, void *stream);
+
+/* ------------------------------------------------------------------------
  * Page operations of a pool that serves many requests: a request is forked,
  * requests leave, a fragmented pool is packed.  All three are all-or-nothing:
  * on a device-side error (status word) nothing has changed.  (One exception:
@@ -555,6 +647,57 @@ int32_t dkv_release(const dkv_release_batch *b, const dkv_pool *pool, const dkv_
  * and cursors contradict one another). */
 int32_t dkv_defrag(const dkv_pool *pool, const dkv_tables *t, int64_t U, int64_t unit_base, void *workspace,
                    size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Eviction by accumulated attention.  The classes come from thresholds
+ * alpha / N, so they do not bound what a unit holds; when a pool runs out, or a
+ * request has a budget, the tokens that received the least attention go.
+ *
+ * A unit (l, r, h) of a request with budgets[r] >= 0 keeps of the tokens it
+ * holds (classes != 0, position < ctx_lens[r]) those at the first `sinks`
+ * positions and the last `window` positions [ctx - window, ctx), and of the
+ * others the budgets[r] - (those) with the largest weight
+ *   w(p) = max over the group's query heads of sig_sum[l][r * cap + p][q],
+ * divided by sig_cnt[r * cap + p] (in fp32) where sig_cnt is given; of equal
+ * weights the lowest position stays first; a weight that is NaN goes first.
+ * A negative budget leaves the request alone, as does one that its units do
+ * not pass.
+ *
+ * Lists close as in dkv_decode_step: with `keep` survivors of a list, those in
+ * slots >= keep move, in ascending slot order, into the holes below keep, in
+ * ascending order (bytes copied); each list keeps its first need = ceil(keep /
+ * P) (low: / 2P) pages and the others are appended at the free list's tail in
+ * (unit, list, page index) order with rev -1 and class 0; the vacated slots of
+ * the kept pages are cleared; classes (0) and slot_of (-1) of the evicted,
+ * slot_of of the moved, fwd, rev_idx, unit_hdr and the tail follow.  Freed pages
+ * keep their contents.
+ * ------------------------------------------------------------------------ */
+typedef struct dkv_evict_batch {
+  int32_t L, R, Hq, Hkv;     /* the tables' shape; R <= 65535 */
+  int32_t cap;               /* positions per request, as in dkv_decode_batch; a multiple of 16 */
+  int32_t sinks, window;     /* >= 0 */
+  int32_t reserved;          /* must be 0 */
+  int64_t unit_base;         /* global id of unit 0 of the tables */
+  const int32_t *budgets;    /* int32 [R], device: most tokens a unit of the request keeps; < 0: all */
+  const int32_t *ctx_lens;   /* int32 [R], device: positions held */
+  const float *sig_sum;      /* fp32 [L][R * cap][Hq], 16-byte aligned */
+  const int32_t *sig_cnt;    /* int32 [R * cap], or NULL: the sums themselves are compared */
+  uint8_t *classes;          /* in/out uint8 [L][R * cap][Hkv], as in dkv_decode_batch */
+  int32_t *slot_of;          /* in/out int32 [L][R * cap][Hkv] */
+} dkv_evict_batch;
+
+/* Workspace bytes of dkv_evict (host only). */
+int32_t dkv_evict_workspace_size(const dkv_evict_batch *b, const dkv_pool *pool, const dkv_tables *t, size_t *bytes);
+
+/* Evict (above), asynchronous; allocates nothing.  workspace: device, 256-byte
+ * aligned, >= dkv_evict_workspace_size bytes, scratch.  Synchronous
+ * DKV_E_INVAL: a bad shape, pointer or workspace.  All-or-nothing: on a
+ * device-side error (status word) nothing has changed: DKV_E_LENS (a
+ * ctx_lens[r] outside [0, cap]), DKV_E_INTERNAL (headers, classes, slots, page
+ * ids, reverse entries or cursors that contradict one another).  A unit that
+ * its budget leaves as it is is not looked into beyond its header. */
+int32_t dkv_evict(const dkv_evict_batch *b, const dkv_pool *pool, const dkv_tables *t, void *workspace,
+                  size_t workspace_bytes, void *stream);
 
 /* Synchronise `stream`, return the pool's device status word (DKV_OK or the
  * first device-side error since the last read) and clear it. */

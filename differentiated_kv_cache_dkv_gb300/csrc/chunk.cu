@@ -1,7 +1,40 @@
 // chunk.cu -- attention of a chunk of new tokens a request over bf16 pages
-// (dkv_chunk_attention).
+// (dkv_chunk_attention), on the fifth-generation tensor cores.
+//
+// A row is one (new token i, query head g of the KV head's group), numbered
+// i G + g within its unit (layer, request, KV head); with that packing the
+// heads of a group share every tile of K and V.  A row tile is tpt = 128 / G
+// whole tokens, an item two row tiles (or one, when no more rows are left) of
+// a unit against its keys, in key tiles of 128 positions.  Three launches:
+//   k_chunk_append  stores the new tokens' K and V in their pages; block 0
+//     meanwhile plans: tokens, items and key tiles of each request, and which
+//     of them each block of the attention takes.
+//   k_chunk         one block a multiprocessor.  Whole items first, block c
+//     taking items c, c + grid, ... (neighbours read the same K and V at the
+//     same time, which keeps them in L2), as many waves as leave every block at
+//     or below the mean; the rest of the key tiles, laid end to end, is cut so
+//     that all blocks end up with the same number.  Items that are cut leave
+//     partial results.
+//   k_chunk_merge   joins those.
+// The roles of a block, pipelined through mbarriers:
+//   copy warp       Q, K and V by TMA, a lane a page, through a ring of tiles;
+//   product warp    one thread: S = Q K^T, O += P V.  P is read from tensor
+//     memory.  The order S0 S1 | O0 S0 O1 S1 | ... gives the tensor cores the
+//     products of one warpgroup while the other is in its softmax;
+//   softmax warps (2 x 4)  a thread per row: P = 2^(x - m) in bf16 into the
+//     columns of S, the running sum.
+// With two row tiles the warpgroups take one each and share every key tile;
+// with one they take every other key tile of it and join their results.
+//
+// The reference m of a row is the first tile's maximum, rounded up to a whole
+// number (log2 units), and moves only when the sum of a tile's weights passes
+// 2^60: weights and outputs in progress have fp32's exponent, so nothing is
+// lost by a reference that is not the maximum, and the usual tile needs no
+// maximum at all.  P waits in registers until that test: the careful body then
+// starts again from S.
 #include <algorithm>
 #include <cmath>
+#include <cstddef>
 
 #include "chunk.cuh"
 
@@ -10,6 +43,53 @@ namespace dkv {
 namespace {
 
 using namespace tc;
+
+constexpr int kBlocks = 152;        // most blocks of the attention: one a multiprocessor
+constexpr int kMaxWaves = 64;       // of whole items; the plan looks at each
+constexpr int kSmemReqs = 1024;     // requests whose first items the plan keeps in shared memory
+
+struct PlanHeader {
+  int64_t tiles;   // key tiles of all items
+  int64_t cut0;    // tiles of the whole items that the waves take
+  int32_t waves;
+  int32_t ok;      // lengths valid
+  int32_t pad[10];
+};
+struct ReqPlan {
+  int64_t tile0;       // key tiles of the requests before
+  int32_t tok0, rt0;   // tokens, items a unit of the requests before
+  int32_t items;       // items a unit
+  int32_t tiles;       // key tiles a unit
+  int32_t ctx, n;
+};
+struct PlanPtrs {
+  PlanHeader *hdr;
+  ReqPlan *req;    // [R]
+  int32_t *pre;    // [items a unit of all requests]: key tiles of the request's items before
+  int64_t *cut;    // [grid + 1]: where each block's share of the cut tiles starts
+  float *o;        // [2 grid][rows][128] partial results
+  float2 *ml;      // [2 grid][rows]: reference and sum
+};
+
+struct ChunkLayout {
+  size_t req, pre, cut, ml, o, bytes;
+  int32_t tpt, tpi, rows;  // tokens a row tile, an item; rows of a partial result
+};
+
+__host__ ChunkLayout chunk_layout(const ChunkArgs &a) {
+  ChunkLayout w{};
+  w.tpt = 128 / a.G;
+  w.tpi = 2 * w.tpt;
+  w.rows = std::min(w.tpi, a.max_new) * a.G;
+  size_t x = align256(sizeof(PlanHeader));
+  w.req = x; x = align256(x + sizeof(ReqPlan) * static_cast<size_t>(a.R));
+  w.pre = x; x = align256(x + 4 * (static_cast<size_t>(a.T / w.tpi) + a.R + 1));
+  w.cut = x; x = align256(x + 8 * (kBlocks + 1));
+  w.ml = x;  x = align256(x + sizeof(float2) * 2 * kBlocks * static_cast<size_t>(w.rows));
+  w.o = x;   x = align256(x + 512 * 2 * kBlocks * static_cast<size_t>(w.rows));
+  w.bytes = x;
+  return w;
+}
 
 // ------------------------------------------------------------------ append --
 
@@ -26,29 +106,198 @@ __device__ __forceinline__ uint32_t finite_only(uint32_t w) {
   return w;
 }
 
-// The new tokens' K and V to their places in the pages: blocks (tokens of a
-// request, request, layer), a lane per 16 bytes.
-__global__ void __launch_bounds__(kAppendThreads) k_chunk_append(const __grid_constant__ ChunkArgs a) {
-  const int32_t r = blockIdx.y, li = blockIdx.z, t0 = blockIdx.x * kAppendTokens;
-  int64_t before;
-  if (!chunk_lens(a, r, before)) return;
-  const int32_t n = min(__ldg(a.new_lens + r) - t0, kAppendTokens), ctx = __ldg(a.ctx_lens + r);
+// Exclusive prefix sum over the block; `total` gets the sum.
+template <class T>
+__device__ __forceinline__ T block_scan(T x, T *sm, T &total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  T incl = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const T y = __shfl_up_sync(kFull, incl, o);
+    if (lane >= o) incl += y;
+  }
+  __syncthreads();
+  if (lane == 31) sm[warp] = incl;
+  __syncthreads();
+  T before = 0;
+  total = 0;
+  for (int w = 0; w < kAppendThreads / 32; ++w) {
+    if (w < warp) before += sm[w];
+    total += sm[w];
+  }
+  return before + incl - x;
+}
+
+// An item by its number: request, unit of the request and item of that unit.
+struct ItemAt {
+  int32_t r, unit, j;
+};
+// The request of item i: the last whose first item (rt0 U1) is at most i, among those that have items.
+template <class F>
+__device__ __forceinline__ int32_t find_req(int32_t R, F first, int64_t i) {
+  int32_t lo = 0, hi = R - 1;
+  while (lo < hi) {
+    const int32_t mid = (lo + hi + 1) >> 1;
+    if (first(mid) <= i) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ int32_t item_tiles(const PlanPtrs &p, const ReqPlan &q, int32_t j) {
+  return (j + 1 < q.items ? p.pre[q.rt0 + j + 1] : q.tiles) - p.pre[q.rt0 + j];
+}
+
+// Block 0: what every block of the attention takes.
+__device__ void plan(const ChunkArgs &a, const PlanPtrs &p, int32_t tpi, int32_t grid) {
+  __shared__ int64_t sm64[kAppendThreads / 32];
+  __shared__ int32_t first_s[kSmemReqs];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t U1 = static_cast<int64_t>(a.n_layers) * a.Hkv;
+  // tokens and items before each request
+  int64_t tok = 0, rts = 0;
+  for (int32_t r0 = 0; r0 < a.R; r0 += kAppendThreads) {
+    const int32_t r = r0 + tid;
+    const int64_t n = r < a.R ? __ldg(a.new_lens + r) : 0, it = (n + tpi - 1) / tpi;
+    int64_t t1, t2;
+    const int64_t tb = block_scan(n, sm64, t1), ib = block_scan(it, sm64, t2);
+    if (r < a.R) {
+      ReqPlan q;
+      q.tile0 = 0;
+      q.tok0 = static_cast<int32_t>(tok + tb);
+      q.rt0 = static_cast<int32_t>(rts + ib);
+      q.items = static_cast<int32_t>(it);
+      q.tiles = 0;
+      q.ctx = __ldg(a.ctx_lens + r);
+      q.n = static_cast<int32_t>(n);
+      p.req[r] = q;
+      if (r < kSmemReqs) first_s[r] = q.rt0;
+    }
+    tok += t1;
+    rts += t2;
+  }
+  __syncthreads();
+  // key tiles of each item: a warp a request
+  for (int32_t r = warp; r < a.R; r += kAppendThreads / 32) {
+    const ReqPlan q = p.req[r];
+    int32_t sum = 0;
+    for (int32_t j0 = 0; j0 < q.items; j0 += 32) {
+      const int32_t j = j0 + lane;
+      const int32_t t = j < q.items ? static_cast<int32_t>((q.ctx + min(static_cast<int64_t>(q.n), (j + 1) * static_cast<int64_t>(tpi)) + 127) / 128) : 0;
+      int32_t incl = t;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int32_t y = __shfl_up_sync(kFull, incl, o);
+        if (lane >= o) incl += y;
+      }
+      if (j < q.items) p.pre[q.rt0 + j] = sum + incl - t;
+      sum += __shfl_sync(kFull, incl, 31);
+    }
+    if (lane == 0) p.req[r].tiles = sum;
+  }
+  __syncthreads();
+  int64_t W = 0;
+  for (int32_t r0 = 0; r0 < a.R; r0 += kAppendThreads) {
+    const int32_t r = r0 + tid;
+    const int64_t s = r < a.R ? p.req[r].tiles * U1 : 0;
+    int64_t t1;
+    const int64_t b = block_scan(s, sm64, t1);
+    if (r < a.R) p.req[r].tile0 = W + b;
+    W += t1;
+  }
+  __syncthreads();
+  // waves of whole items, while no block gets more than the mean
+  const int64_t items = rts * U1, target = (W + grid - 1) / grid;
+  auto first = [&](int32_t r) { return (a.R <= kSmemReqs ? first_s[r] : p.req[r].rt0) * U1; };
+  int64_t mine = 0;
+  int32_t waves = 0;
+  for (; waves < kMaxWaves && (waves + 1) * static_cast<int64_t>(grid) <= items; ++waves) {
+    int64_t d = mine;
+    if (tid < grid) {
+      const int64_t i = waves * static_cast<int64_t>(grid) + tid;
+      const ReqPlan q = p.req[find_req(a.R, first, i)];
+      d += item_tiles(p, q, static_cast<int32_t>((i - q.rt0 * U1) % q.items));
+    }
+    if (__syncthreads_or(d > target)) break;
+    mine = d;
+  }
+  // the rest, so that every block ends at the mean
+  int64_t cut0 = W;
+  if (waves * static_cast<int64_t>(grid) < items) {
+    const int64_t i = waves * static_cast<int64_t>(grid);
+    const ReqPlan q = p.req[find_req(a.R, first, i)];
+    const int64_t k = i - q.rt0 * U1;
+    cut0 = q.tile0 + k / q.items * q.tiles + p.pre[q.rt0 + static_cast<int32_t>(k % q.items)];
+  }
+  int64_t all;
+  const int64_t b = block_scan(tid < grid ? target - mine : 0, sm64, all);
+  if (tid < grid) p.cut[tid] = min(W, cut0 + b);
+  if (tid == 0) {
+    p.cut[grid] = W;
+    *p.hdr = PlanHeader{W, cut0, waves, 1, {}};
+  }
+}
+
+// Block 0 plans; block 1 + b stores tokens [16 b', ...) of a layer, a lane per 16 bytes.
+__global__ void __launch_bounds__(kAppendThreads)
+    k_chunk_append(const __grid_constant__ ChunkArgs a, const PlanPtrs p, int32_t tpi, int32_t grid) {
+  let_next_launch_start();
+  __shared__ int32_t req_s[kAppendTokens], pos_s[kAppendTokens];
+  const uint32_t per = static_cast<uint32_t>((a.T + kAppendTokens - 1) / kAppendTokens);
+  const uint32_t b = blockIdx.x == 0 ? 0 : blockIdx.x - 1;
+  const int32_t li = static_cast<int32_t>(b / per);
+  const int64_t t0 = static_cast<int64_t>(b % per) * kAppendTokens;
+  int64_t unused;
+  if (!chunk_lens(a, 0, unused)) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) p.hdr->ok = 0;
+    return;
+  }
+  if (blockIdx.x == 0) {
+    plan(a, p, tpi, grid);
+    return;
+  }
+  const int32_t n = static_cast<int32_t>(min(a.T - t0, static_cast<int64_t>(kAppendTokens)));
+  if (threadIdx.x < 32) {  // requests of the block's tokens
+    const int lane = threadIdx.x;
+    int64_t before = 0;
+    int32_t done = 0;
+    for (int32_t r0 = 0; r0 < a.R && done < n; r0 += 32) {
+      const int32_t r = r0 + lane, m = r < a.R ? __ldg(a.new_lens + r) : 0;
+      int64_t incl = m;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(kFull, incl, o);
+        if (lane >= o) incl += y;
+      }
+      const int64_t lo = before + incl - m, hi = before + incl;  // this request's tokens
+      for (int64_t t = max(lo, t0); t < min(hi, t0 + n); ++t) {
+        req_s[t - t0] = r;
+        pos_s[t - t0] = static_cast<int32_t>(__ldg(a.ctx_lens + r) + t - lo);
+      }
+      before += __shfl_sync(kFull, incl, 31);
+      done = static_cast<int32_t>(min(before - t0, static_cast<int64_t>(n)));
+    }
+  }
+  __syncthreads();
   const int32_t units = a.Hkv * 16;  // 16-byte units of a token's K (or V) rows
   bool bad = false;
   for (int32_t i = threadIdx.x; i < n * units; i += kAppendThreads) {
-    const int32_t t = t0 + i / units, c = i % units, p = ctx + t;
-    const int32_t id = chunk_page(a, r, p / a.B);
+    const int32_t t = i / units, c = i - t * units, pos = pos_s[t];
+    const int32_t id = chunk_page(a, req_s[t], pos / a.B);
     if (id < 0) continue;
-    const int64_t from = (static_cast<int64_t>(li) * a.T + before + t) * a.kv_stride + c * 8;
-    const int64_t to = (((static_cast<int64_t>(a.layer0) + li) * a.F + id) * a.B + p % a.B) * (a.Hkv * int64_t{128}) + c * 8;
+    const int64_t from = (static_cast<int64_t>(li) * a.T + t0 + t) * a.kv_stride + c * 8;
+    const int64_t to = (((static_cast<int64_t>(a.layer0) + li) * a.F + id) * a.B + pos % a.B) * (a.Hkv * int64_t{128}) + c * 8;
+    uint4 x[2];
+    x[0] = *reinterpret_cast<const uint4 *>(a.k_new + from);
+    x[1] = *reinterpret_cast<const uint4 *>(a.v_new + from);
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
-      uint4 x = *reinterpret_cast<const uint4 *>((kv ? a.v_new : a.k_new) + from);
-      if (!(finite2(x.x) && finite2(x.y) && finite2(x.z) && finite2(x.w))) {
+      uint4 &y = x[kv];
+      if (!(finite2(y.x) && finite2(y.y) && finite2(y.z) && finite2(y.w))) {
         bad = true;
-        x = make_uint4(finite_only(x.x), finite_only(x.y), finite_only(x.z), finite_only(x.w));
+        y = make_uint4(finite_only(y.x), finite_only(y.y), finite_only(y.z), finite_only(y.w));
       }
-      *reinterpret_cast<uint4 *>((kv ? a.v : a.k) + to) = x;
+      *reinterpret_cast<uint4 *>((kv ? a.v : a.k) + to) = y;
     }
   }
   if (bad) set_error(a.status, DKV_E_RANGE);
@@ -56,56 +305,548 @@ __global__ void __launch_bounds__(kAppendThreads) k_chunk_append(const __grid_co
 
 // --------------------------------------------------------------- attention --
 
-constexpr int kRowWarps = 8;
+constexpr int kSoftWarps = 8, kCopyWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1;
+constexpr int kThreads = 32 * (kSoftWarps + 2);
+constexpr uint32_t kTmemCols = 512;  // S (and P) of warpgroup w at 128 w, O at 256 + 128 w
+constexpr int kRing = 5;             // K and V tiles in flight
+constexpr int kSegs = 4;
+constexpr float kMost = 0x1p60f;     // sum of a tile's weights that moves the reference
+constexpr float kFar = 0x1p20f;      // references beyond it: logits are rounded before it is taken off
 
-// A warp per (new token, query head): blocks (rows of a request, request, layer).
-__global__ void __launch_bounds__(32 * kRowWarps) k_chunk_rows(const __grid_constant__ ChunkArgs a) {
-  const int32_t r = blockIdx.y, li = blockIdx.z, lane = threadIdx.x & 31;
-  int64_t before;
-  if (!chunk_lens(a, r, before)) return;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
-  const int32_t i = static_cast<int32_t>(row / a.Hq), hq = static_cast<int32_t>(row % a.Hq), h = hq / a.G;
-  if (i >= __ldg(a.new_lens + r)) return;
-  const int32_t end = __ldg(a.ctx_lens + r) + i + 1;
-  const int64_t tok = static_cast<int64_t>(li) * a.T + before + i;
-  const uint2 qw = __ldg(reinterpret_cast<const uint2 *>(a.q + tok * a.q_stride + hq * 128) + lane);
-  const float q0 = bf16_lo(qw.x), q1 = bf16_hi(qw.x), q2 = bf16_lo(qw.y), q3 = bf16_hi(qw.y);
-  float m = -INFINITY, l = 0.0f, o0 = 0.0f, o1 = 0.0f, o2 = 0.0f, o3 = 0.0f;
-  const float sl2 = a.scale * kLog2e;
-  int32_t id = 0;
-  for (int32_t t = 0; t < end; ++t) {
-    if (t % a.B == 0) id = max(chunk_page(a, r, t / a.B), 0);
-    const int64_t at = ((((static_cast<int64_t>(a.layer0) + li) * a.F + id) * a.B + t % a.B) * a.Hkv + h) * 128;
-    const uint2 k = *(reinterpret_cast<const uint2 *>(a.k + at) + lane), v = *(reinterpret_cast<const uint2 *>(a.v + at) + lane);
-    float x = q0 * bf16_lo(k.x) + q1 * bf16_hi(k.x) + q2 * bf16_lo(k.y) + q3 * bf16_hi(k.y);
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1) x += __shfl_xor_sync(kFull, x, s);
-    x *= sl2;
-    const float mn = fmaxf(m, x), f = exp2f(m - mn), p = exp2f(x - mn);
-    m = mn;
-    l = l * f + p;
-    o0 = o0 * f + p * bf16_lo(v.x);
-    o1 = o1 * f + p * bf16_hi(v.x);
-    o2 = o2 * f + p * bf16_lo(v.y);
-    o3 = o3 * f + p * bf16_hi(v.y);
+// What a block does next: key tiles [t0, t0 + nt) of an item.
+struct Seg {
+  int32_t nt;            // 0: the end
+  int32_t t0;
+  int32_t slot;          // of the partial results, -1: the whole item
+  int32_t li, h, r;
+  int32_t tok, i0, n;    // the item's first token in the batch and in the request, its tokens
+  int32_t ctx;
+};
+
+struct __align__(1024) Smem {
+  uint8_t q[2][kTileBytes];        // row tiles; then the second warpgroup's outputs, by column
+  uint8_t ring[kRing][kTileBytes];
+  uint64_t qfull, qfree, joined, full[kRing], empty[kRing];
+  uint64_t sfull[2], pready[2], odone[2], ofree[2], ojoin, done;
+  Seg seg[kSegs];
+  float2 ml[128];                  // the second warpgroup's references and sums
+  uint32_t tmem;
+  int32_t abort;
+};
+constexpr size_t kSmemBytes = sizeof(Smem) + 1024;
+static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+
+// Block c's segment number s: whole items c, c + grid, ..., then its share of
+// the cut tiles, from w on (w: where the next of those starts).
+__device__ __forceinline__ Seg next_seg(const ChunkArgs &a, const PlanPtrs &p, int32_t waves, int64_t cut0, int32_t tpi,
+                                        int32_t grid, int32_t s, int64_t &w) {
+  const int64_t U1 = static_cast<int64_t>(a.n_layers) * a.Hkv;
+  Seg g{};
+  const int32_t c = blockIdx.x;
+  int64_t k;  // item within the request
+  ReqPlan q;
+  int32_t r;
+  if (s < waves) {
+    const int64_t i = s * static_cast<int64_t>(grid) + c;
+    r = find_req(a.R, [&](int32_t x) { return p.req[x].rt0 * U1; }, i);
+    q = p.req[r];
+    k = i - q.rt0 * U1;
+    g.t0 = 0;
+    g.nt = item_tiles(p, q, static_cast<int32_t>(k % q.items));
+    g.slot = -1;
+  } else {
+    const int64_t w0 = p.cut[c], w1 = p.cut[c + 1];
+    if (w >= w1) return g;
+    r = find_req(a.R, [&](int32_t x) { return p.req[x].tile0; }, w);
+    q = p.req[r];
+    const int64_t unit = (w - q.tile0) / q.tiles, in = (w - q.tile0) - unit * q.tiles;
+    const int32_t j = find_req(q.items, [&](int32_t x) { return static_cast<int64_t>(p.pre[q.rt0 + x]); }, in);
+    k = unit * q.items + j;
+    const int32_t all = item_tiles(p, q, j);
+    g.t0 = static_cast<int32_t>(in - p.pre[q.rt0 + j]);
+    g.nt = static_cast<int32_t>(min(static_cast<int64_t>(all - g.t0), w1 - w));
+    g.slot = g.nt == all ? -1 : 2 * c + (w == w0 ? 0 : 1);
+    w += g.nt;
   }
-  const float w = 1.0f / l;
-  *(reinterpret_cast<uint2 *>(a.out + (tok * a.Hq + hq) * 128) + lane) = make_uint2(bf16x2_rn(o0 * w, o1 * w), bf16x2_rn(o2 * w, o3 * w));
-  if (a.lse && lane == 0) a.lse[tok * a.Hq + hq] = (m + log2f(l)) * 0.693147180559945309f;
+  const int32_t unit = static_cast<int32_t>(k / q.items), j = static_cast<int32_t>(k - static_cast<int64_t>(unit) * q.items);
+  g.li = unit / a.Hkv;
+  g.h = unit - g.li * a.Hkv;
+  g.r = r;
+  g.i0 = j * tpi;
+  g.n = min(tpi, q.n - g.i0);
+  g.tok = q.tok0 + g.i0;
+  g.ctx = q.ctx;
+  return g;
+}
+
+// Columns of 32 that a row keeps: the first `lim`.
+__device__ __forceinline__ void keep_columns(uint32_t (&u)[32], int32_t lim) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i)
+    if (i >= lim) u[i] = 0xff800000u;
+}
+
+// The maximum of 32 values.
+__device__ __forceinline__ float max32(const uint32_t (&u)[32]) {
+  float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int i = 0; i < 16; ++i) m[i & 3] = max3(m[i & 3], __uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
+  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    k_chunk(const __grid_constant__ ChunkArgs a, const PlanPtrs p, const __grid_constant__ CUtensorMap qmap,
+            const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, int32_t tpt, int32_t rows) {
+  extern __shared__ unsigned char smem_raw[];
+  // aligned by an offset, not by an integer address: the compiler then knows that these are shared accesses
+  Smem &sm = *reinterpret_cast<Smem *>(smem_raw + (-saddr(smem_raw) & 1023u));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  volatile int32_t *abort = &sm.abort;
+  if (tid == 0) {
+    mbar_init(&sm.qfull, 1);
+    mbar_init(&sm.qfree, 1 + kSoftWarps);
+    mbar_init(&sm.joined, 4);
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&sm.full[i], 1);
+      mbar_init(&sm.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.sfull[i], 1);
+      mbar_init(&sm.pready[i], 4);
+      mbar_init(&sm.odone[i], 1);
+      mbar_init(&sm.ofree[i], 4);
+    }
+    mbar_init(&sm.ojoin, 4);
+    mbar_init(&sm.done, 1);
+    sm.abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 0) tmem_alloc(&sm.tmem, kTmemCols);
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = sm.tmem;
+  after_launch_before();
+  let_next_launch_start();
+  const bool valid = *reinterpret_cast<volatile int32_t *>(&p.hdr->ok) != 0;
+  const int32_t tpi = 2 * tpt, G = a.G;
+  auto wait = [&](uint64_t *bar, uint32_t parity) { return wait_or_abort(bar, parity, abort, a.status); };
+  // the same answer in every lane: the loops below hold warp-wide instructions
+  auto warp_wait = [&](uint64_t *bar, uint32_t parity) { return __all_sync(kFull, wait(bar, parity)) != 0; };
+
+  if (!valid) {
+    // nothing to do: the lengths have been reported
+  } else if (warp == kCopyWarp) {
+    // ================= copies: a segment's first K and V tiles, its Q, the others
+    const int32_t waves = p.hdr->waves, grid = gridDim.x, npg = 128 / a.B;
+    const int64_t cut0 = p.hdr->cut0;
+    int64_t w = p.cut[blockIdx.x];
+    int32_t c = 0, joins = 0;  // tiles of K or V copied, segments whose warpgroups joined
+    bool ok = true, joining = false;
+    int32_t s = 0;
+    for (; ok; ++s) {
+      const Seg g = next_seg(a, p, waves, cut0, tpi, grid, s, w);
+      const int32_t end = g.ctx + g.i0 + g.n;  // positions the item's last row attends
+      const int32_t *row = a.table + static_cast<int64_t>(g.r) * a.tmax;
+      const int64_t base = (static_cast<int64_t>(a.layer0) + g.li) * a.F;
+      // lane 2 k (+ 1): channels 0 .. 63 (64 ..) of the tile's page k
+      auto page_of = [&](int32_t t) {
+        const int32_t j = t * npg + (lane >> 1);
+        if ((lane >> 1) >= npg || j * a.B >= end) return -1;
+        const int32_t id = __ldg(row + j);
+        if (id >= 0 && id < a.F) return id;
+        set_error(a.status, DKV_E_INTERNAL);
+        return 0;
+      };
+      auto copy_tile = [&](int32_t t, int32_t id) {
+        const uint32_t boxes = __popc(__ballot_sync(kFull, id >= 0));
+        const int32_t at = static_cast<int32_t>((base + id) * a.B);
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          const int32_t slot = c % kRing;
+          if (c >= kRing && !(ok = warp_wait(&sm.empty[slot], (c / kRing - 1) & 1u))) return;
+          if (lane == 0) mbar_expect_tx(&sm.full[slot], boxes * a.B * 128);
+          __syncwarp();
+          if (id >= 0)
+            copy_box(sm.ring[slot] + (lane & 1) * kBox + (lane >> 1) * a.B * 128, kv ? &vmap : &kmap, (lane & 1) * 64, g.h, at,
+                     &sm.full[slot]);
+          ++c;
+        }
+      };
+      int32_t id = 0;
+      if (g.nt > 0) {
+        id = page_of(g.t0);
+        copy_tile(g.t0, id);
+        if (!ok) break;
+        id = g.nt > 1 ? page_of(g.t0 + 1) : -1;
+      }
+      // Q when the products of the segment before have read theirs, every warp has read what the segment is
+      // (so that none of them misses a phase of qfull) and its outputs have left the place
+      if (s > 0 && !(ok = warp_wait(&sm.qfree, (s - 1) & 1u))) break;
+      if (joining) {
+        if (!(ok = warp_wait(&sm.joined, joins & 1u))) break;
+        ++joins;
+      }
+      if (lane == 0) {
+        sm.seg[s % kSegs] = g;
+        if (g.nt > 0) {
+          const int tiles = g.n > tpt ? 2 : 1;
+          mbar_expect_tx(&sm.qfull, tiles * 2 * tpt * G * 128);
+          for (int t = 0; t < tiles; ++t)
+            for (int half = 0; half < 2; ++half)
+              copy_box(sm.q[t] + half * kBox, &qmap, half * 64, g.h * G,
+                       static_cast<int32_t>(g.li * a.T + g.tok + t * tpt), &sm.qfull);
+        } else {
+          mbar_arrive(&sm.qfull);
+        }
+      }
+      __syncwarp();
+      if (g.nt == 0) break;
+      joining = g.n <= tpt && g.nt > 1;
+      for (int32_t t = 1; t < g.nt && ok; ++t) {
+        const int32_t now = id;
+        id = t + 1 < g.nt ? page_of(g.t0 + t + 1) : -1;
+        copy_tile(g.t0 + t, now);
+      }
+    }
+    // The products have waited for every copy; where a wait gave up, the copies issued land before the block
+    // leaves (bounded).
+    if (lane == 0 && !ok) {
+      if (s > 0) mbar_wait(&sm.qfull, (s - 1) & 1u, nullptr);
+      for (int32_t i = max(0, c - kRing); i < c; ++i) mbar_wait(&sm.full[i % kRing], (i / kRing) & 1u, nullptr);
+    }
+  } else if (warp == kMmaWarp) {
+    // ================= products, by one thread
+    if (lane == 0) {
+      constexpr uint32_t kStep = kTileBytes >> 4;
+      const uint64_t dq = sw128_desc(saddr(sm.q[0]), 16, 1024), dk = sw128_desc(saddr(sm.ring[0]), 16, 1024);
+      const uint64_t dv = sw128_desc(saddr(sm.ring[0]), kBox, 1024);
+      int32_t base = 0, np[2] = {0, 0}, nseg[2] = {0, 0};  // tiles so far; P taken, segments by warpgroup
+      bool ok = true;
+      for (int32_t s = 0; ok; ++s) {
+        if (!(ok = wait(&sm.qfull, s & 1u))) break;
+        const Seg g = sm.seg[s % kSegs];
+        if (g.nt == 0) break;
+        const bool two = g.n > tpt;
+        const int32_t total = two ? 2 * g.nt : g.nt;
+        auto scores = [&](int32_t u) {
+          const int wg = u & 1;
+          const int32_t i = 2 * (base + (two ? u >> 1 : u)), slot = i % kRing;
+          if (!(ok = wait(&sm.full[slot], (i / kRing) & 1u))) return;
+          fence_after();
+          const uint64_t da = dq + (two && wg ? kStep : 0), db = dk + slot * kStep;
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            const uint32_t o = ((kk >> 2) * kBox + (kk & 3) * 32) >> 4;
+            mma_ss(tmem + 128 * wg, da + o, db + o, idesc(true, 128, 128, false), kk > 0 ? 1u : 0u);
+          }
+          mma_commit(&sm.sfull[wg]);
+          if (!two || wg) mma_commit(&sm.empty[slot]);
+          if (u == total - 1) mma_commit(&sm.qfree);
+        };
+        scores(0);
+        if (ok && total > 1) scores(1);
+        for (int32_t u = 0; u < total && ok; ++u) {
+          const int wg = u & 1;
+          const int32_t i = 2 * (base + (two ? u >> 1 : u)) + 1, slot = i % kRing;
+          if (!(ok = wait(&sm.full[slot], (i / kRing) & 1u) && wait(&sm.pready[wg], np[wg] & 1u))) break;
+          ++np[wg];
+          if (u < 2) {  // O of the segment before has been read
+            if (nseg[wg] > 0 && !(ok = wait(&sm.ofree[wg], (nseg[wg] - 1) & 1u))) break;
+            ++nseg[wg];
+          }
+          fence_after();
+          const uint64_t db = dv + slot * kStep;
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            mma_ts(tmem + 256 + 128 * wg, tmem + 128 * wg + 32 * (kk >> 1) + 8 * (kk & 1), db + ((kk * 2048) >> 4),
+                   idesc(true, 128, 128, true), u < 2 && kk == 0 ? 0u : 1u);
+          if (u >= total - 2) mma_commit(&sm.odone[wg]);
+          if (!two || wg) mma_commit(&sm.empty[slot]);
+          if (u + 2 < total) scores(u + 2);
+        }
+        base += g.nt;
+      }
+      // every product of this thread done (also after an abort)
+      mma_commit(&sm.done);
+      mbar_wait(&sm.done, 0, nullptr);
+    }
+  } else {
+    // ================= softmax warps: a thread per row
+    const int wg = warp >> 2, row = tid & 127;
+    const float sl2 = a.scale * kLog2e;  // logits in log2 units
+    const uint64_t sl2x2 = f2_pack(sl2, sl2);
+    const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    const uint32_t ts_s = tmem + lanes + 128 * wg, ts_o = tmem + lanes + 256 + 128 * wg;
+    const int32_t rt = row / G;  // token of the row tile
+    int32_t base = 0, ns = 0, nseg = 0, joins = 0;
+    bool ok = true;
+    for (int32_t s = 0; ok; ++s) {
+      if (!(ok = warp_wait(&sm.qfull, s & 1u))) break;
+      const Seg g = sm.seg[s % kSegs];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.qfree);
+      if (g.nt == 0) break;
+      const bool two = g.n > tpt;
+      const int32_t i = (two && wg ? tpt : 0) + rt;  // token of the item
+      const bool live = rt < tpt && i < g.n;
+      const bool some = __any_sync(kFull, live);
+      const int32_t end = g.ctx + g.i0 + g.n;
+      float m = live ? -INFINITY : 0.0f;
+      uint64_t l2 = 0;  // running sum, even and odd columns
+      bool started = false;
+      for (int32_t t = two ? 0 : wg; t < g.nt && ok; t += two ? 1 : 2, ++ns) {
+        if (!(ok = warp_wait(&sm.sfull[wg], ns & 1u))) break;
+        fence_after();
+        const int32_t k0 = 128 * (g.t0 + t);
+        if (some) {
+          const int32_t lim = live ? g.ctx + g.i0 + i + 1 - k0 : 128;
+          const bool masked = __any_sync(kFull, lim < 128);
+          uint32_t w[64];  // P, two columns each
+          uint64_t sum = 0;
+          auto weigh = [&](const uint32_t (&u)[32], int c, uint64_t nm2) {
+            uint64_t t2[2] = {0, 0};
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              float y0, y1;
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(u[2 * e]), __uint_as_float(u[2 * e + 1])), sl2x2, nm2), y0, y1);
+              const float p0 = ex2(y0), p1 = ex2(y1);
+              t2[e & 1] = f2_add(t2[e & 1], f2_pack(p0, p1));
+              w[16 * c + e] = bf16x2_rn(p0, p1);
+            }
+            sum = f2_add(sum, f2_add(t2[0], t2[1]));
+          };
+          bool care = __any_sync(kFull, live && !(fabsf(m) < kFar));
+          if (!care) {
+            const uint64_t nm2 = f2_pack(-m, -m);
+            uint32_t u[2][32];
+            tmem_ld32(ts_s, u[0]);
+            tmem_wait32(u[0]);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              if (c < 3) tmem_ld32(ts_s + 32 * (c + 1), u[(c + 1) & 1]);
+              if (__builtin_expect(masked, 0)) keep_columns(u[c & 1], lim - 32 * c);
+              weigh(u[c & 1], c, nm2);
+              if (c < 3) tmem_wait32(u[(c + 1) & 1]);
+            }
+            care = __any_sync(kFull, live && !(f2_sum(sum) <= kMost));
+          }
+          if (__builtin_expect(care, 0)) {
+            uint32_t u[32];
+            float mx = -INFINITY;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              tmem_ld32(ts_s + 32 * c, u);
+              tmem_wait32(u);
+              keep_columns(u, lim - 32 * c);
+              mx = fmaxf(mx, max32(u));
+            }
+            const float mn = live ? fmaxf(m, ceilf(mx * sl2)) : 0.0f;
+            const float f = mn == m ? 1.0f : ex2(m - mn);  // 2^-inf = 0 where the row starts
+            if (started && __any_sync(kFull, f != 1.0f)) {
+              // the products into O were complete when S was
+#pragma unroll 1
+              for (int c = 0; c < 8; ++c) {
+                uint32_t x[16];
+                tmem_ld16(ts_o + 16 * c, x);
+                tmem_wait16(x);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
+                tmem_st16(ts_o + 16 * c, x);
+              }
+              tmem_wait_st();
+            }
+            l2 = f2_mul(l2, f2_pack(f, f));
+            m = mn;
+            const float mo = m == -INFINITY ? 0.0f : m;
+            sum = 0;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              tmem_ld32(ts_s + 32 * c, u);
+              tmem_wait32(u);
+              keep_columns(u, lim - 32 * c);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                // rounded before the reference is taken off: what is left of the largest logit is at most 0
+                const float p0 = ex2(__fsub_rn(__fmul_rn(__uint_as_float(u[2 * e]), sl2), mo));
+                const float p1 = ex2(__fsub_rn(__fmul_rn(__uint_as_float(u[2 * e + 1]), sl2), mo));
+                sum = f2_add(sum, f2_pack(p0, p1));
+                w[16 * c + e] = bf16x2_rn(p0, p1);
+              }
+            }
+          }
+          l2 = f2_add(l2, sum);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_st16(ts_s + 32 * c, w + 16 * c);
+        }
+        started = true;
+        // rows of V behind the item's last position hold anything: zeros, as 0 times anything is not 0
+        if (end - k0 < 128) {
+          const int32_t vi = 2 * (base + t) + 1, slot = vi % kRing;
+          if (!(ok = warp_wait(&sm.full[slot], (vi / kRing) & 1u))) break;
+          if (row >= end - k0) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              *reinterpret_cast<uint4 *>(sm.ring[slot] + (e >> 3) * kBox + row * 128 + (e & 7) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_async();
+        }
+        tmem_wait_st();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.pready[wg]);
+      }
+      if (!ok) break;
+      // ---- the segment's results
+      const bool join = !two && g.nt > 1;
+      float l = f2_sum(l2);
+      const int64_t at = (static_cast<int64_t>(g.li) * a.T + g.tok + i) * a.Hq + g.h * G + (row - rt * G);
+      const int64_t part = g.slot < 0 ? 0 : static_cast<int64_t>(g.slot) * rows + (two && wg ? tpt * G : 0) + row;
+      if (started) {
+        if (!(ok = warp_wait(&sm.odone[wg], nseg & 1u))) break;
+        ++nseg;
+        fence_after();
+        float *ox = reinterpret_cast<float *>(sm.q[0]);  // [column][row]
+        float f0 = 1.0f, f1 = 0.0f;
+        if (join && wg == 0) {
+          if (!(ok = warp_wait(&sm.ojoin, joins & 1u))) break;
+          const float2 x = sm.ml[row];
+          const float mm = fmaxf(m, x.x);
+          f0 = m == mm ? 1.0f : ex2(m - mm);
+          f1 = x.x == mm ? 1.0f : ex2(x.x - mm);
+          l = l * f0 + x.y * f1;
+          m = mm;
+        }
+        const float inv = g.slot < 0 ? 1.0f / l : 1.0f;
+        f0 *= inv;
+        f1 *= inv;
+        if (some) {
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t u[32];
+            tmem_ld32(ts_o + 32 * c, u);
+            tmem_wait32(u);
+            if (join && wg == 1) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) ox[(32 * c + e) * 128 + row] = __uint_as_float(u[e]);
+              continue;
+            }
+            float x[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(u[e]) * f0;
+            if (join) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) x[e] += ox[(32 * c + e) * 128 + row] * f1;
+            }
+            if (!live) continue;
+            if (g.slot < 0) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                *reinterpret_cast<uint4 *>(a.out + at * 128 + 32 * c + 8 * e) =
+                    make_uint4(bf16x2_rn(x[8 * e], x[8 * e + 1]), bf16x2_rn(x[8 * e + 2], x[8 * e + 3]),
+                               bf16x2_rn(x[8 * e + 4], x[8 * e + 5]), bf16x2_rn(x[8 * e + 6], x[8 * e + 7]));
+            } else {
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                *reinterpret_cast<float4 *>(p.o + part * 128 + 32 * c + 4 * e) =
+                    make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+            }
+          }
+          if (join && wg == 1) sm.ml[row] = make_float2(m, l);
+          else if (live && g.slot >= 0) p.ml[part] = make_float2(m, l);
+          else if (live && a.lse) a.lse[at] = (m + log2f(l)) * 0.693147180559945309f;
+        }
+        fence_before();
+        if (join && wg == 0) fence_async();  // the next Q is copied where these reads were
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&sm.ofree[wg]);
+          if (join) mbar_arrive(wg ? &sm.ojoin : &sm.joined);
+        }
+        if (join) ++joins;
+      }
+      base += g.nt;
+    }
+  }
+
+  // ---- teardown: copies and products are complete (bounded waits above)
+  fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    fence_after();
+    tmem_free(tmem, kTmemCols);
+  }
+}
+
+// ------------------------------------------------------------------- merge --
+
+constexpr int kMergeRows = 8;  // a warp each
+
+// Block (c, rows): the item that the end of block c's share cuts, if c is the
+// first that has part of it.
+__global__ void __launch_bounds__(32 * kMergeRows)
+    k_chunk_merge(const __grid_constant__ ChunkArgs a, const PlanPtrs p, int32_t tpi, int32_t rows, int32_t grid) {
+  after_launch_before();
+  if (!p.hdr->ok) return;
+  const int32_t c = blockIdx.x, lane = threadIdx.x & 31, row = blockIdx.y * kMergeRows + (threadIdx.x >> 5);
+  const int64_t w0 = p.cut[c], w1 = p.cut[c + 1];
+  if (w1 == w0 || w1 >= p.hdr->tiles) return;
+  // the item of tile w1 - 1
+  const int32_t r = find_req(a.R, [&](int32_t x) { return p.req[x].tile0; }, w1 - 1);
+  const ReqPlan q = p.req[r];
+  const int64_t unit = (w1 - 1 - q.tile0) / q.tiles, in = w1 - 1 - q.tile0 - unit * q.tiles;
+  const int32_t j = find_req(q.items, [&](int32_t x) { return static_cast<int64_t>(p.pre[q.rt0 + x]); }, in);
+  const int64_t begin = q.tile0 + unit * q.tiles + p.pre[q.rt0 + j], end = begin + item_tiles(p, q, j);
+  if (end == w1 || begin < w0) return;  // not cut here, or an earlier block's
+  if (row >= min(tpi, q.n - j * tpi) * a.G) return;
+  // the parts: this block's, then those of the blocks after it that have tiles
+  float m = -INFINITY, l = 0.0f;
+  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int32_t b = c; b < grid && p.cut[b] < end; ++b) {
+    if (p.cut[b + 1] == p.cut[b]) continue;
+    const int64_t at = static_cast<int64_t>(2 * b + (b == c && begin != w0 ? 1 : 0)) * rows + row;
+    const float2 x = p.ml[at];
+    if (x.x == -INFINITY) continue;  // a part whose every tile lies behind the row
+    const float4 y = *reinterpret_cast<const float4 *>(p.o + at * 128 + 4 * lane);
+    const float mm = fmaxf(m, x.x), f = m == mm ? 1.0f : ex2(m - mm), e = x.x == mm ? 1.0f : ex2(x.x - mm);
+    l = l * f + x.y * e;
+    o = make_float4(o.x * f + y.x * e, o.y * f + y.y * e, o.z * f + y.z * e, o.w * f + y.w * e);
+    m = mm;
+  }
+  const float inv = 1.0f / l;
+  const int32_t li = static_cast<int32_t>(unit / a.Hkv), h = static_cast<int32_t>(unit - static_cast<int64_t>(li) * a.Hkv);
+  const int64_t at = (static_cast<int64_t>(li) * a.T + q.tok0 + j * tpi + row / a.G) * a.Hq + h * a.G + row % a.G;
+  *reinterpret_cast<uint2 *>(a.out + at * 128 + 4 * lane) = make_uint2(bf16x2_rn(o.x * inv, o.y * inv), bf16x2_rn(o.z * inv, o.w * inv));
+  if (a.lse && lane == 0) a.lse[at] = (m + log2f(l)) * 0.693147180559945309f;
 }
 
 }  // namespace
 
-size_t chunk_workspace(const ChunkArgs &) { return 256; }
+size_t chunk_workspace(const ChunkArgs &a) { return chunk_layout(a).bytes; }
 
-cudaError_t launch_chunk(const ChunkArgs &a, void *, cudaStream_t s) {
-  if (a.k_new) {
-    k_chunk_append<<<dim3((a.max_new + kAppendTokens - 1) / kAppendTokens, a.R, a.n_layers), kAppendThreads, 0, s>>>(a);
-    if (cudaError_t e = cudaGetLastError()) return e;
-  }
-  const int64_t rows = static_cast<int64_t>(a.max_new) * a.Hq;
-  k_chunk_rows<<<dim3(static_cast<unsigned>((rows + kRowWarps - 1) / kRowWarps), a.R, a.n_layers), 32 * kRowWarps, 0, s>>>(a);
-  return cudaGetLastError();
+cudaError_t launch_chunk(const ChunkArgs &a, void *ws, cudaStream_t s) {
+  const ChunkLayout w = chunk_layout(a);
+  uint8_t *b = static_cast<uint8_t *>(ws);
+  const PlanPtrs p{reinterpret_cast<PlanHeader *>(b), reinterpret_cast<ReqPlan *>(b + w.req),
+                   reinterpret_cast<int32_t *>(b + w.pre), reinterpret_cast<int64_t *>(b + w.cut),
+                   reinterpret_cast<float *>(b + w.o), reinterpret_cast<float2 *>(b + w.ml)};
+  int dev = 0, sms = 0;
+  cudaError_t e;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+  const int grid = std::max(1, std::min(sms, kBlocks));
+  alignas(64) CUtensorMap qmap, kmap, vmap;
+  if ((e = chunk_map(&qmap, a.q, a.n_layers * a.T, a.Hq, a.q_stride, a.G, w.tpt)) != cudaSuccess) return e;
+  const int64_t rows = static_cast<int64_t>(a.L) * a.F * a.B, stride = a.Hkv * int64_t{128};
+  if ((e = chunk_map(&kmap, a.k, rows, a.Hkv, stride, 1, a.B)) != cudaSuccess) return e;
+  if ((e = chunk_map(&vmap, a.v, rows, a.Hkv, stride, 1, a.B)) != cudaSuccess) return e;
+  if ((e = cudaFuncSetAttribute(k_chunk, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes))) != cudaSuccess)
+    return e;
+  const int64_t copies = a.k_new ? a.n_layers * ((a.T + kAppendTokens - 1) / kAppendTokens) : 0;
+  k_chunk_append<<<static_cast<unsigned>(1 + copies), kAppendThreads, 0, s>>>(a, p, w.tpi, grid);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if ((e = launch_after(k_chunk, dim3(grid), kThreads, kSmemBytes, s, a, p, qmap, kmap, vmap, w.tpt, w.rows)) != cudaSuccess) return e;
+  return launch_after(k_chunk_merge, dim3(grid, (w.rows + kMergeRows - 1) / kMergeRows), 32 * kMergeRows, 0, s, a, p, w.tpi, w.rows, grid);
 }
 
 }  // namespace dkv

@@ -2,6 +2,9 @@
 // lengths, and where a position lies.
 #pragma once
 
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include "tensor_ops.cuh"
 
 namespace dkv {
@@ -44,6 +47,59 @@ __device__ __forceinline__ int32_t chunk_page(const ChunkArgs &a, int32_t r, int
   if (id >= 0 && id < a.F) return id;
   set_error(a.status, DKV_E_INTERNAL);
   return -1;
+}
+
+// TMA copy of one box of a 3-D tensor map at (channel, head, row).
+__device__ __forceinline__ void copy_box(void *dst, const CUtensorMap *map, int c0, int c1, int c2, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(saddr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(saddr(bar))
+      : "memory");
+}
+
+// A later launch's blocks may start while the one before still runs and wait
+// here for its end.
+__device__ __forceinline__ void after_launch_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_launch_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// 3-D tensor map over bf16 rows [rows][H][128] that lie `stride` elements
+// apart, whose box is 64 channels of `heads` heads of `n` rows, written to
+// shared memory with the 128-byte swizzle (rows past the array read as zeros).
+inline cudaError_t chunk_map(CUtensorMap *map, const void *base, int64_t rows, int32_t H, int64_t stride, int32_t heads,
+                             int32_t n) {
+  static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
+    cudaDriverEntryPointQueryResult qr;
+    void *fn = nullptr;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &qr);
+    return e == cudaSuccess && qr == cudaDriverEntryPointSuccess ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn)
+                                                                 : nullptr;
+  }();
+  if (!encode) return cudaErrorNotSupported;
+  const cuuint64_t dims[3] = {128, static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[2] = {256, static_cast<cuuint64_t>(stride) * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(heads), static_cast<cuuint32_t>(n)};
+  const cuuint32_t one[3] = {1, 1, 1};
+  const CUresult res = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, one,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return res == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// A launch that may overlap the end of the one before it (after_launch_before).
+template <class... P, class... A>
+cudaError_t launch_after(void (*k)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, A... args) {
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c{};
+  c.gridDim = grid;
+  c.blockDim = dim3(threads);
+  c.dynamicSmemBytes = smem;
+  c.stream = s;
+  c.attrs = &attr;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, k, static_cast<P>(args)...);
 }
 
 }  // namespace tc

@@ -836,10 +836,10 @@ cudaError_t launch_chunk(const ChunkArgs &a, void *ws, cudaStream_t s) {
   if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
   const int grid = std::max(1, std::min(sms, kBlocks));
   alignas(64) CUtensorMap qmap, kmap, vmap;
-  if ((e = chunk_map(&qmap, a.q, a.n_layers * a.T, a.Hq, a.q_stride, a.G, w.tpt)) != cudaSuccess) return e;
+  if ((e = chunk_map(&qmap, a.q, a.Hq, 128, a.n_layers * a.T, a.q_stride, a.G, w.tpt)) != cudaSuccess) return e;
   const int64_t rows = static_cast<int64_t>(a.L) * a.F * a.B, stride = a.Hkv * int64_t{128};
-  if ((e = chunk_map(&kmap, a.k, rows, a.Hkv, stride, 1, a.B)) != cudaSuccess) return e;
-  if ((e = chunk_map(&vmap, a.v, rows, a.Hkv, stride, 1, a.B)) != cudaSuccess) return e;
+  if ((e = chunk_map(&kmap, a.k, a.Hkv, 128, rows, stride, 1, a.B)) != cudaSuccess) return e;
+  if ((e = chunk_map(&vmap, a.v, a.Hkv, 128, rows, stride, 1, a.B)) != cudaSuccess) return e;
   if ((e = cudaFuncSetAttribute(k_chunk, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes))) != cudaSuccess)
     return e;
   const int64_t copies = a.k_new ? a.n_layers * ((a.T + kAppendTokens - 1) / kAppendTokens) : 0;

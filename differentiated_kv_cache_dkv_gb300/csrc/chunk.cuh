@@ -63,11 +63,11 @@ __device__ __forceinline__ void copy_box(void *dst, const CUtensorMap *map, int 
 __device__ __forceinline__ void after_launch_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next_launch_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
-// 3-D tensor map over bf16 rows [rows][H][128] that lie `stride` elements
-// apart, whose box is 64 channels of `heads` heads of `n` rows, written to
-// shared memory with the 128-byte swizzle (rows past the array read as zeros).
-inline cudaError_t chunk_map(CUtensorMap *map, const void *base, int64_t rows, int32_t H, int64_t stride, int32_t heads,
-                             int32_t n) {
+// 3-D tensor map over bf16 channels of 128: extents n1 and n2 with strides s1
+// and s2 (elements), whose box is 64 channels by b1 by b2, written to shared
+// memory with the 128-byte swizzle (what lies past an extent reads as zeros).
+inline cudaError_t chunk_map(CUtensorMap *map, const void *base, int64_t n1, int64_t s1, int64_t n2, int64_t s2, int32_t b1,
+                             int32_t b2) {
   static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
     cudaDriverEntryPointQueryResult qr;
     void *fn = nullptr;
@@ -76,9 +76,9 @@ inline cudaError_t chunk_map(CUtensorMap *map, const void *base, int64_t rows, i
                                                                  : nullptr;
   }();
   if (!encode) return cudaErrorNotSupported;
-  const cuuint64_t dims[3] = {128, static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(rows)};
-  const cuuint64_t strides[2] = {256, static_cast<cuuint64_t>(stride) * 2};
-  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(heads), static_cast<cuuint32_t>(n)};
+  const cuuint64_t dims[3] = {128, static_cast<cuuint64_t>(n1), static_cast<cuuint64_t>(n2)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(s1) * 2, static_cast<cuuint64_t>(s2) * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(b1), static_cast<cuuint32_t>(b2)};
   const cuuint32_t one[3] = {1, 1, 1};
   const CUresult res = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, one,
                               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,

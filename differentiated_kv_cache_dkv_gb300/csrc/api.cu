@@ -683,6 +683,7 @@ int32_t dkv_evict(const dkv_evict_batch *b, const dkv_pool *pool, const dkv_tabl
   a.unit = reinterpret_cast<dkv::EvictUnit *>(w + lay.unit);
   a.off = reinterpret_cast<int64_t *>(w + lay.off);
   a.gone = reinterpret_cast<uint32_t *>(w + lay.gone);
+  a.stay = reinterpret_cast<uint32_t *>(w + lay.stay);
   a.keys = reinterpret_cast<uint32_t *>(w + lay.keys);
   return cuda_status(dkv::launch_evict(a, static_cast<cudaStream_t>(stream)));
 }

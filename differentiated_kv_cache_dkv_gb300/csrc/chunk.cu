@@ -617,6 +617,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             sum = f2_add(sum, f2_add(t2[0], t2[1]));
           };
           bool care = __any_sync(kFull, live && !(fabsf(m) < kFar));
+          // the usual tile; one with masked columns goes the careful way
+          care |= masked;
           if (!care) {
             const uint64_t nm2 = f2_pack(-m, -m);
             uint32_t u[2][32];
@@ -625,7 +627,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               if (c < 3) tmem_ld32(ts_s + 32 * (c + 1), u[(c + 1) & 1]);
-              if (__builtin_expect(masked, 0)) keep_columns(u[c & 1], lim - 32 * c);
               weigh(u[c & 1], c, nm2);
               if (c < 3) tmem_wait32(u[(c + 1) & 1]);
             }

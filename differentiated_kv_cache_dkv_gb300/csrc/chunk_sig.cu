@@ -23,6 +23,7 @@
 //     broadcast reads.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "chunk.cuh"
 
@@ -74,9 +75,12 @@ __device__ __forceinline__ void sort_requests(const ChunkArgs &a, Smem &sm) {
   }
 }
 
+// kWide: blocks of 128 tokens of one head; else all tokens of several heads are in one block.
+template <bool kWide>
 __global__ void __launch_bounds__(kThreads, 1)
     k_chunk_sig(const __grid_constant__ ChunkArgs a, const __grid_constant__ CUtensorMap qmap,
-                const __grid_constant__ CUtensorMap kmap, int32_t nb) {
+                const __grid_constant__ CUtensorMap kmap, int32_t tokens) {
+  const int32_t nb = kWide ? 128 : tokens;
   extern __shared__ unsigned char smem_raw[];
   // aligned by an offset, not by an integer address: the compiler then knows that these are shared accesses
   Smem &sm = *reinterpret_cast<Smem *>(smem_raw + (-saddr(smem_raw) & 1023u));
@@ -334,43 +338,59 @@ __global__ void __launch_bounds__(kThreads, 1)
             // tokens of the block that the position receives from: lo <= t < hi
             const int32_t lo = key - g.ctx - tb * nb, hi = g.n - tb * nb;
             const bool masked = hi < nb || __any_sync(kFull, lo > 0);
-            uint32_t u[2][32];
-            tmem_ld32(src, u[0]);
-            tmem_wait32(u[0]);
+            // weights of the tile's columns 16 k .. + 15 (v) to their sum; kMask: of tokens outside [lo, hi) none
+            auto sum16 = [&](const uint32_t *v, int k, auto mask) {
+              uint64_t t2[2] = {0, 0};
+              const int32_t t0 = (16 * k) & (nb - 1);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              if (i < 3) tmem_ld32(src + 32 * (i + 1), u[(i + 1) & 1]);
+              for (int e = 0; e < 4; ++e) {
+                const float4 z = nl[4 * k + e];
+                float y[4];
+                f2_unpack(f2_fma(f2_pack(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1])), s2, f2_pack(z.x, z.y)), y[0], y[1]);
+                f2_unpack(f2_fma(f2_pack(__uint_as_float(v[4 * e + 2]), __uint_as_float(v[4 * e + 3])), s2, f2_pack(z.z, z.w)), y[2], y[3]);
+                if constexpr (decltype(mask)::value) {
 #pragma unroll
-              for (int half = 0; half < 2; ++half) {
-                uint64_t t2[2] = {0, 0};
-                const int32_t t0 = (32 * i + 16 * half) & (nb - 1);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const float4 z = nl[8 * i + 4 * half + e];
-                  const uint32_t *v = &u[i & 1][16 * half + 4 * e];
-                  float y[4];
-                  f2_unpack(f2_fma(f2_pack(__uint_as_float(v[0]), __uint_as_float(v[1])), s2, f2_pack(z.x, z.y)), y[0], y[1]);
-                  f2_unpack(f2_fma(f2_pack(__uint_as_float(v[2]), __uint_as_float(v[3])), s2, f2_pack(z.z, z.w)), y[2], y[3]);
-                  if (__builtin_expect(masked, 0)) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                      if (t0 + 4 * e + j < lo || t0 + 4 * e + j >= hi) y[j] = -INFINITY;
-                  }
-                  t2[0] = f2_add(t2[0], f2_pack(ex2(y[0]), ex2(y[1])));
-                  t2[1] = f2_add(t2[1], f2_pack(ex2(y[2]), ex2(y[3])));
+                  for (int j = 0; j < 4; ++j)
+                    if (t0 + 4 * e + j < lo || t0 + 4 * e + j >= hi) y[j] = -INFINITY;
                 }
-                acc += f2_sum(f2_add(t2[0], t2[1]));
-                // the last tokens of a head
-                if (((32 * i + 16 * half + 16) & (nb - 1)) == 0 && tb == g.tb1 - 1) {
-                  const int32_t hq = b * hb + (32 * i + 16 * half) / nb;
-                  if (there && hq < G) {
-                    if (held) red_add(dst + hq, acc);
-                    else dst[hq] = acc;
-                  }
-                  acc = 0.0f;
-                }
+                t2[0] = f2_add(t2[0], f2_pack(ex2(y[0]), ex2(y[1])));
+                t2[1] = f2_add(t2[1], f2_pack(ex2(y[2]), ex2(y[3])));
               }
-              if (i < 3) tmem_wait32(u[(i + 1) & 1]);
+              return f2_add(t2[0], t2[1]);
+            };
+            auto flush = [&](int32_t hq) {  // a head's last columns are in
+              if (there && hq < G) {
+                if (held) red_add(dst + hq, acc);
+                else dst[hq] = acc;
+              }
+              acc = 0.0f;
+            };
+            auto tile = [&](auto mask) {
+              uint32_t u[2][32];
+              tmem_ld32(src, u[0]);
+              tmem_wait32(u[0]);
+              uint64_t t2 = 0;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                if (i < 3) tmem_ld32(src + 32 * (i + 1), u[(i + 1) & 1]);
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                  const uint64_t x = sum16(&u[i & 1][16 * half], 2 * i + half, mask);
+                  if constexpr (kWide) {
+                    t2 = f2_add(t2, x);
+                  } else {
+                    acc += f2_sum(x);
+                    if (((32 * i + 16 * half + 16) & (nb - 1)) == 0) flush(b * hb + (32 * i + 16 * half) / nb);
+                  }
+                }
+                if (i < 3) tmem_wait32(u[(i + 1) & 1]);
+              }
+              if constexpr (kWide) acc += f2_sum(t2);
+            };
+            if (masked) tile(std::true_type{});
+            else tile(std::false_type{});
+            if constexpr (kWide) {
+              if (tb == g.tb1 - 1) flush(b);
             }
             fence_before();
             __syncwarp();
@@ -405,9 +425,10 @@ cudaError_t launch_chunk_sig(const ChunkArgs &a, cudaStream_t s) {
   if ((e = chunk_map(&qmap, a.q, a.n_layers * a.T, a.q_stride, a.Hq, 128, nb, 128 / nb)) != cudaSuccess) return e;
   if ((e = chunk_map(&kmap, a.k, a.Hkv, 128, static_cast<int64_t>(a.L) * a.F * a.B, a.Hkv * int64_t{128}, 1, a.B)) != cudaSuccess)
     return e;
-  if ((e = cudaFuncSetAttribute(k_chunk_sig, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes))) != cudaSuccess)
+  auto *k = nb == 128 ? k_chunk_sig<true> : k_chunk_sig<false>;
+  if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes))) != cudaSuccess)
     return e;
-  k_chunk_sig<<<sms, kThreads, kSmemBytes, s>>>(a, qmap, kmap, nb);
+  k<<<sms, kThreads, kSmemBytes, s>>>(a, qmap, kmap, nb);
   return cudaGetLastError();
 }
 

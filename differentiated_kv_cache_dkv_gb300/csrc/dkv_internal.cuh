@@ -489,6 +489,7 @@ struct EvictWsLayout {
   size_t unit;   // EvictUnit [U]
   size_t off;    // int64 [U]: freed pages of the units before
   size_t gone;   // uint32 [U][cap / 32, rounded up]: evicted positions
+  size_t stay;   // uint32 [U][cap / 32 + 2]: slots of the high list that stay, then of the low list
   size_t keys;   // uint32 [U][cap], where a unit's keys do not fit shared memory
   size_t bytes;
 };
@@ -499,6 +500,7 @@ inline EvictWsLayout evict_ws_layout(int64_t U, int32_t cap) {
   w.unit = o; o = align256(o + sizeof(EvictUnit) * static_cast<size_t>(U));
   w.off = o;  o = align256(o + sizeof(int64_t) * static_cast<size_t>(U));
   w.gone = o; o = align256(o + 4 * static_cast<size_t>(U) * ((cap + 31) / 32));
+  w.stay = o; o = align256(o + 4 * static_cast<size_t>(U) * (cap / 32 + 2));
   w.keys = o; o = align256(o + (cap > kEvictKeys ? 4 * static_cast<size_t>(U) * cap : 0));
   w.bytes = o;
   return w;
@@ -520,7 +522,7 @@ struct EvictArgs {
   EvictWsHeader *ws;
   EvictUnit *unit;
   int64_t *off;
-  uint32_t *gone, *keys;
+  uint32_t *gone, *stay, *keys;
 };
 
 }  // namespace dkv

@@ -6,17 +6,17 @@
 // stay, K the budget: a selection, no sort.
 //
 //   k_evict_plan   a block per unit: the weights become 32-bit keys in the
-//     order of the floats (in shared memory), four counting passes of 8 bits
+//     order of the floats (in shared memory), counting passes of 11 bits
 //     find the K-th largest key T and how many equal to it stay; the position
 //     of the last of those decides between equals.  Survivors and evicted are
-//     counted against headers and slots, pages against the reverse table: all
-//     that could be wrong is found here.  Leaves the survivors' counts and the
-//     evicted positions as bits.
+//     counted against headers and slots, pages against the reverse table.
+//     Leaves the survivors' counts, the slots that stay and the evicted
+//     positions as bits.
 //   k_evict_scan   one block: freed pages of the units before each (prefix
 //     sum), the first error, the tail.  After an error nothing is changed.
-//   k_evict_apply  a block per unit: a bitmap of the slots that stay, whose
-//     prefix counts give every mover its hole; the moves, a group of lanes
-//     each; the cleared slots, the tables and the ring.
+//   k_evict_apply  a block per unit: prefix counts over the slots that stay
+//     give every mover its hole; the moves, a group of lanes each; the cleared
+//     slots, the rows of the evicted, the tables and the ring.
 //
 // What bounds it: the significance (4 Hq bytes a position) and the moved
 // tokens' bytes.
@@ -31,8 +31,14 @@ namespace dkv {
 namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
+constexpr int kBins = 2048;   // of a counting pass
 constexpr int kPlanThreads = 512, kScanThreads = 1024, kApplyThreads = 256;
 constexpr int kMoves = 2048;  // moves a block lists at a time
+
+// A later launch's blocks may start while the one before still runs and wait
+// here for its end.
+__device__ __forceinline__ void after_launch_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_launch_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // Order of the floats as unsigned numbers; 0 is left for "not held" and the
 // largest for the protected; a NaN is below every number.
@@ -40,6 +46,13 @@ __device__ __forceinline__ uint32_t order_key(float x) {
   const uint32_t b = __float_as_uint(x + 0.0f);  // -0 counts as 0
   if (x != x) return 1u;
   return (b & 0x80000000u) ? ~b : b | 0x80000000u;
+}
+
+// The larger one; NaN where one is NaN.
+__device__ __forceinline__ float nan_max(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
 }
 
 // Sum over the block, to every thread; `sm` holds one int a warp.
@@ -71,9 +84,10 @@ __device__ __forceinline__ Place place_of(const EvictArgs &a, int32_t u) {
 __device__ __forceinline__ int32_t words_of(int32_t n) { return (n + 31) >> 5; }
 
 __global__ void __launch_bounds__(kPlanThreads) k_evict_plan(const __grid_constant__ EvictArgs a) {
+  let_next_launch_start();
   extern __shared__ uint32_t dyn[];
   __shared__ int32_t sm[kPlanThreads / 32];
-  __shared__ uint32_t hist[256];
+  __shared__ uint32_t hist[kBins];
   __shared__ int32_t pick_s[3], bad_s;
   const int32_t u = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
   const Place pl = place_of(a, u);
@@ -94,7 +108,13 @@ __global__ void __launch_bounds__(kPlanThreads) k_evict_plan(const __grid_consta
   uint32_t *key = a.cap > kEvictKeys ? a.keys + static_cast<int64_t>(u) * a.cap : dyn + 2 * (a.cap / 32 + 2);
   for (int32_t i = tid; i < 2 * words; i += kPlanThreads) dyn[i] = 0;
   if (tid == 0) bad_s = 0;
-  if (tid < 256) hist[tid] = 0;
+  for (int i = tid; i < kBins; i += kPlanThreads) hist[i] = 0;
+  // pages and their reverse entries
+  bool wrong = false;
+  for (int32_t j = tid; j < hd.z + hd.w; j += kPlanThreads) {
+    const int32_t id = a.fwd[static_cast<int64_t>(u) * a.pmax + j];
+    if (id < 0 || id >= a.F || a.rev_unit[id] != a.unit_base + u || a.rev_idx[id] != j) wrong = true;
+  }
   __syncthreads();
 
   // keys, the first counting pass, and what the classes say is held
@@ -104,46 +124,31 @@ __global__ void __launch_bounds__(kPlanThreads) k_evict_plan(const __grid_consta
   const bool quad = (G & 3) == 0 && (a.Hq & 3) == 0;  // then a token's scores are whole 16-byte words
   const float *sig = a.sig_sum + pl.row * a.Hq + pl.h * G;
   const int32_t *cnt = a.sig_cnt ? a.sig_cnt + static_cast<int64_t>(pl.r) * a.cap : nullptr;
-  constexpr int kEach = 4;  // positions a thread has in flight
+  constexpr int kEach = 8;  // positions a thread has in flight; the scores of positions without a token are read too
   for (int32_t p0 = tid; p0 < ctx; p0 += kEach * kPlanThreads) {
     int32_t c[kEach];
+    float w[kEach];
 #pragma unroll
     for (int e = 0; e < kEach; ++e) {
-      const int32_t p = p0 + e * kPlanThreads;
-      c[e] = p < ctx ? cls[static_cast<int64_t>(p) * a.Hkv] : 0;
-    }
-    float w[kEach];
-    if (quad) {
-#pragma unroll
-      for (int e = 0; e < kEach; ++e) {
-        const int32_t p = p0 + e * kPlanThreads;
-        w[e] = -INFINITY;
-        if (c[e]) {
-          const float4 *x = reinterpret_cast<const float4 *>(sig + static_cast<int64_t>(p) * a.Hq);
-          float4 y = __ldg(x);
-          bool nan = !(y.x == y.x && y.y == y.y && y.z == y.z && y.w == y.w);
-          w[e] = fmaxf(fmaxf(y.x, y.y), fmaxf(y.z, y.w));
-          for (int g = 1; g < (G >> 2); ++g) {
-            y = __ldg(x + g);
-            nan |= !(y.x == y.x && y.y == y.y && y.z == y.z && y.w == y.w);
-            w[e] = fmaxf(w[e], fmaxf(fmaxf(y.x, y.y), fmaxf(y.z, y.w)));
-          }
-          if (nan) w[e] = NAN;
-        }
+      const int32_t p = min(p0 + e * kPlanThreads, ctx - 1);
+      c[e] = cls[static_cast<int64_t>(p) * a.Hkv];
+      const float *x = sig + static_cast<int64_t>(p) * a.Hq;
+      if (quad) {
+        const float4 y = __ldg(reinterpret_cast<const float4 *>(x));
+        w[e] = nan_max(nan_max(y.x, y.y), nan_max(y.z, y.w));
+      } else {
+        w[e] = __ldg(x);
       }
-    } else {
+    }
+    for (int g = quad ? 4 : 1; g < G; g += quad ? 4 : 1) {
 #pragma unroll
       for (int e = 0; e < kEach; ++e) {
-        const int32_t p = p0 + e * kPlanThreads;
-        w[e] = -INFINITY;
-        if (c[e]) {
-          bool nan = false;
-          for (int g = 0; g < G; ++g) {
-            const float y = __ldg(sig + static_cast<int64_t>(p) * a.Hq + g);
-            nan |= y != y;
-            w[e] = fmaxf(w[e], y);
-          }
-          if (nan) w[e] = NAN;
+        const float *x = sig + static_cast<int64_t>(min(p0 + e * kPlanThreads, ctx - 1)) * a.Hq + g;
+        if (quad) {
+          const float4 y = __ldg(reinterpret_cast<const float4 *>(x));
+          w[e] = nan_max(w[e], nan_max(nan_max(y.x, y.y), nan_max(y.z, y.w)));
+        } else {
+          w[e] = nan_max(w[e], __ldg(x));
         }
       }
     }
@@ -160,7 +165,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_evict_plan(const __grid_consta
         safe += s;
         if (cnt) w[e] = __fdiv_rn(w[e], static_cast<float>(__ldg(cnt + p)));
         k = s ? 0xffffffffu : order_key(w[e]);
-        atomicAdd(hist + (k >> 24), 1u);
+        atomicAdd(hist + (k >> 21), 1u);
       }
       key[p] = k;
     }
@@ -175,45 +180,51 @@ __global__ void __launch_bounds__(kPlanThreads) k_evict_plan(const __grid_consta
     return;
   }
 
-  // T: the K-th largest key; `left`: how many of the keys equal to it stay
-  uint32_t T = 0xffffffffu;
+  // T: the K-th largest key; `left`: how many of the keys equal to it (as far as it is known) stay
+  uint32_t T = 0xffffffffu, known = 0xffffffffu;
   int32_t left = 0, ties = 0;
+  __syncthreads();
   if (K > 0) {
-    T = 0;
+    T = known = 0;
     left = K;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      if (shift < 24) {
-        if (tid < 256) hist[tid] = 0;
+    ties = left + 1;
+    for (int shift = 21; ties > left && known != 0xffffffffu; shift -= shift > 11 ? 11 : shift) {
+      const uint32_t digit = known ? (shift ? 0x7ffu : 0x3ffu) : 0x7ffu;
+      if (known) {
+        for (int i = tid; i < kBins; i += kPlanThreads) hist[i] = 0;
         __syncthreads();
         for (int32_t p = tid; p < ctx; p += kPlanThreads) {
           const uint32_t k = key[p];
-          if (k && (k >> (shift + 8)) == (T >> (shift + 8))) atomicAdd(hist + (k >> shift & 255u), 1u);
+          if (k && (k & known) == T) atomicAdd(hist + (k >> shift & digit), 1u);
         }
         __syncthreads();
       }
-      if (tid < 32) {  // lane i: buckets 255 - 8 i and down
-        int32_t n[8], sum = 0;
+      // thread i: bins from 2047 - 4 i down
+      int32_t n[kBins / kPlanThreads], sum = 0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sum += n[j] = static_cast<int32_t>(hist[255 - 8 * lane - j]);
-        int32_t above = sum;
+      for (int j = 0; j < kBins / kPlanThreads; ++j) sum += n[j] = static_cast<int32_t>(hist[kBins - 1 - (kBins / kPlanThreads) * tid - j]);
+      int32_t above = sum;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int32_t x = __shfl_up_sync(kFull, above, o);
-          if (lane >= o) above += x;
-        }
-        above -= sum;
-        if (above < left && above + sum >= left) {
-          int j = 0;
-          while (above + n[j] < left) above += n[j++];
-          pick_s[0] = 255 - 8 * lane - j;
-          pick_s[1] = left - above;
-          pick_s[2] = n[j];
-        }
+      for (int o = 1; o < 32; o <<= 1) {
+        const int32_t x = __shfl_up_sync(kFull, above, o);
+        if (lane >= o) above += x;
+      }
+      if (lane == 31) sm[tid >> 5] = above;
+      __syncthreads();
+      above -= sum;
+      for (int w = 0; w < (tid >> 5); ++w) above += sm[w];
+      if (above < left && above + sum >= left) {
+        int j = 0;
+        while (above + n[j] < left) above += n[j++];
+        pick_s[0] = kBins - 1 - (kBins / kPlanThreads) * tid - j;
+        pick_s[1] = left - above;
+        pick_s[2] = n[j];
       }
       __syncthreads();
       T |= static_cast<uint32_t>(pick_s[0]) << shift;
       left = pick_s[1];
       ties = pick_s[2];
+      known |= digit << shift;
       __syncthreads();
     }
   }
@@ -222,7 +233,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_evict_plan(const __grid_consta
     if (tid < 32) {
       int32_t seen = 0, cut = -1;
       for (int32_t p = lane; p - lane < ctx; p += 32) {
-        uint32_t m = __ballot_sync(kFull, p < ctx && key[p] == T);
+        uint32_t m = __ballot_sync(kFull, p < ctx && key[p] && (key[p] & known) == T);
         if (seen + __popc(m) >= left) {
           while (seen + 1 < left) {
             m &= m - 1u;
@@ -253,7 +264,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_evict_plan(const __grid_consta
     if (k) {
       const int32_t c = cls[static_cast<int64_t>(p) * a.Hkv], s = slots[static_cast<int64_t>(p) * a.Hkv];
       const bool high = c == DKV_CLASS_K8V4;
-      out = !(k > T || (k == T && p <= cut));
+      out = !((k & known) > T || ((k & known) == T && p <= cut));
       if (s < 0 || s >= (high ? n_hi : n_lo)) {
         bad = true;
       } else {
@@ -275,12 +286,9 @@ __global__ void __launch_bounds__(kPlanThreads) k_evict_plan(const __grid_consta
   all = block_sum(all, sm);
   kh = block_sum(kh, sm);
   kl = block_sum(kl, sm);
-  // pages and their reverse entries
-  bool wrong = all != held;
-  for (int32_t j = tid; j < hd.z + hd.w; j += kPlanThreads) {
-    const int32_t id = a.fwd[static_cast<int64_t>(u) * a.pmax + j];
-    if (id < 0 || id >= a.F || a.rev_unit[id] != a.unit_base + u || a.rev_idx[id] != j) wrong = true;
-  }
+  wrong |= all != held;
+  uint32_t *stay_out = a.stay + static_cast<int64_t>(u) * (a.cap / 32 + 2);
+  for (int32_t i = tid; i < words; i += kPlanThreads) stay_out[i] = stay[i];
   if (wrong) bad_s = 1;
   __syncthreads();
   if (tid == 0) {
@@ -292,6 +300,8 @@ __global__ void __launch_bounds__(kPlanThreads) k_evict_plan(const __grid_consta
 __global__ void __launch_bounds__(kScanThreads) k_evict_scan(const __grid_constant__ EvictArgs a) {
   __shared__ int64_t wsum[kScanThreads / 32];
   __shared__ unsigned long long err_s;
+  let_next_launch_start();
+  after_launch_before();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t per = (a.U + kScanThreads - 1) / kScanThreads, u0 = tid * per, u1 = min(a.U, u0 + per);
   if (tid == 0) err_s = ~0ull;
@@ -346,10 +356,11 @@ __device__ __forceinline__ SlotAt slot_at(const EvictArgs &a, const int32_t *fw,
 }
 
 // Slots src[0 .. n) of a list to dst[0 .. n), kLanes lanes a move: the 16-byte
-// units of K and V, the metadata, the position.
+// units of K and V, the metadata, the position, and the index entry that goes
+// with it.
 template <int kLanes>
 __device__ __forceinline__ void move_slots(const EvictArgs &a, const int32_t *fw, bool high, const int32_t *src,
-                                           const int32_t *dst, const int32_t *pos, int32_t n) {
+                                           const int32_t *dst, int32_t n, int32_t *slots, int32_t ctx) {
   const int32_t j = threadIdx.x % kLanes, ku = high ? a.pg.kh : a.pg.kh >> 1, vu = high ? a.pg.vh : a.pg.vh >> 1;
   constexpr int kGroups = kApplyThreads / kLanes, kEach = 4;
   for (int32_t m0 = threadIdx.x / kLanes; m0 < n; m0 += kGroups * kEach) {
@@ -362,29 +373,37 @@ __device__ __forceinline__ void move_slots(const EvictArgs &a, const int32_t *fw
       const SlotAt f = slot_at(a, fw, high, src[m]), t = slot_at(a, fw, high, dst[m]);
       to[e] = j < ku ? t.k + 16 * j : (j < ku + vu ? t.v + 16 * (j - ku) : (j == ku + vu ? t.meta : t.pos));
       if (j < ku + vu) {
-        x[e] = *reinterpret_cast<const uint4 *>(a.pages + (j < ku ? f.k + 16 * j : f.v + 16 * (j - ku)));
+        x[e] = __ldcs(reinterpret_cast<const uint4 *>(a.pages + (j < ku ? f.k + 16 * j : f.v + 16 * (j - ku))));
       } else if (j == ku + vu) {
         const uint2 y = *reinterpret_cast<const uint2 *>(a.pages + f.meta);
         x[e].x = y.x;
         x[e].y = y.y;
-      } else {
-        x[e].x = static_cast<uint32_t>(pos[m]);
+      } else if (j == ku + vu + 1) {
+        x[e].x = *reinterpret_cast<const uint32_t *>(a.pages + f.pos);
       }
     }
 #pragma unroll
     for (int e = 0; e < kEach; ++e) {
-      if (m0 + e * kGroups >= n) continue;
+      const int32_t m = m0 + e * kGroups;
+      if (m >= n) continue;
       uint8_t *p = a.pages + to[e];
-      if (j < ku + vu) *reinterpret_cast<uint4 *>(p) = x[e];
-      else if (j == ku + vu) *reinterpret_cast<uint2 *>(p) = make_uint2(x[e].x, x[e].y);
-      else if (j == ku + vu + 1) *reinterpret_cast<uint32_t *>(p) = x[e].x;
+      if (j < ku + vu) {
+        *reinterpret_cast<uint4 *>(p) = x[e];
+      } else if (j == ku + vu) {
+        *reinterpret_cast<uint2 *>(p) = make_uint2(x[e].x, x[e].y);
+      } else if (j == ku + vu + 1) {
+        *reinterpret_cast<uint32_t *>(p) = x[e].x;
+        if (x[e].x < static_cast<uint32_t>(ctx)) slots[static_cast<int64_t>(x[e].x) * a.Hkv] = dst[m];
+        else set_error(a.status, DKV_E_INTERNAL);
+      }
     }
   }
 }
 
-__global__ void __launch_bounds__(kApplyThreads) k_evict_apply(const __grid_constant__ EvictArgs a) {
+__global__ void __launch_bounds__(kApplyThreads, 4) k_evict_apply(const __grid_constant__ EvictArgs a) {
+  after_launch_before();
   extern __shared__ uint32_t dyn[];
-  __shared__ int32_t src[kMoves], dst[kMoves], pos[kMoves];
+  __shared__ int32_t src[kMoves], dst[kMoves];
   __shared__ int32_t wsum[kApplyThreads / 32];
   if (a.ws->err) return;
   const int32_t u = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -395,26 +414,17 @@ __global__ void __launch_bounds__(kApplyThreads) k_evict_apply(const __grid_cons
   const int4 hd = *reinterpret_cast<const int4 *>(a.unit_hdr + 4 * static_cast<int64_t>(u));
   const int32_t wh = words_of(hd.x), words = wh + words_of(hd.y);
   uint32_t *stay = dyn, *rank = dyn + words;  // slots that stay, and how many of them before a word
-  for (int32_t i = tid; i < words; i += kApplyThreads) stay[i] = 0;
-  __syncthreads();
-
-  // the evicted leave the rows; the others' slots make the bitmap
+  const uint32_t *stay_in = a.stay + static_cast<int64_t>(u) * (a.cap / 32 + 2);
+  for (int32_t i = tid; i < words; i += kApplyThreads) stay[i] = __ldg(stay_in + i);
+  // the evicted leave the rows
   uint8_t *cls = a.classes + pl.row * a.Hkv + pl.h;
   int32_t *slots = a.slot_of + pl.row * a.Hkv + pl.h;
   const uint32_t *gone_pos = a.gone + static_cast<int64_t>(u) * ((a.cap + 31) / 32);
-  for (int32_t p = tid; p < ctx; p += kApplyThreads) {
-    const int64_t at = static_cast<int64_t>(p) * a.Hkv;
-    const int32_t c = cls[at];
-    if (!c) continue;
-    if (gone_pos[p >> 5] >> (p & 31) & 1u) {
-      cls[at] = DKV_CLASS_PRUNE;
-      slots[at] = -1;
-    } else {
-      const int32_t s = slots[at];
-      if (in_range(s, c == DKV_CLASS_K8V4 ? hd.x : hd.y, a.status))
-        atomicOr(stay + (c == DKV_CLASS_K8V4 ? 0 : wh) + (s >> 5), 1u << (s & 31));
+  for (int32_t p = tid; p < ctx; p += kApplyThreads)
+    if (__ldg(gone_pos + (p >> 5)) >> (p & 31) & 1u) {
+      cls[static_cast<int64_t>(p) * a.Hkv] = DKV_CLASS_PRUNE;
+      slots[static_cast<int64_t>(p) * a.Hkv] = -1;
     }
-  }
   __syncthreads();
   {
     const int32_t per = (words + kApplyThreads - 1) / kApplyThreads, i0 = min(words, tid * per), i1 = min(words, i0 + per);
@@ -443,35 +453,24 @@ __global__ void __launch_bounds__(kApplyThreads) k_evict_apply(const __grid_cons
     if (keep == n) continue;
     const int32_t base = high ? 0 : un.keep_hi;  // survivors of the lists before
     const uint32_t *st = stay + w0, *rk = rank + w0;
-    auto below = [&](int32_t s) {  // survivors in slots below s
-      return s >= n ? keep : static_cast<int32_t>(rk[s >> 5]) - base + __popc(st[s >> 5] & ((1u << (s & 31)) - 1u));
-    };
-    const int32_t b_keep = below(keep), moves = keep - b_keep;
+    // survivors in slots below keep; as many movers as holes
+    const int32_t b_keep = static_cast<int32_t>(rk[keep >> 5]) - base + __popc(st[keep >> 5] & ((1u << (keep & 31)) - 1u));
+    const int32_t moves = keep - b_keep;
     const int32_t *fw = fwd + (high ? 0 : hd.z);
     for (int32_t m0 = 0; m0 < moves; m0 += kMoves) {
       const int32_t nm = min(kMoves, moves - m0);
-      for (int32_t w = tid; w < words_of(keep); w += kApplyThreads) {
-        uint32_t hole = ~st[w];
-        if (keep - 32 * w < 32) hole &= (1u << (keep - 32 * w)) - 1u;
-        int32_t m = 32 * w - (static_cast<int32_t>(rk[w]) - base) - m0;
-        for (; hole; hole &= hole - 1u, ++m)
-          if (m >= 0 && m < nm) dst[m] = 32 * w + __ffs(hole) - 1;
-      }
-      for (int32_t p = tid; p < ctx; p += kApplyThreads) {
-        const int64_t at = static_cast<int64_t>(p) * a.Hkv;
-        if (cls[at] != (high ? DKV_CLASS_K8V4 : DKV_CLASS_K4V2)) continue;
-        const int32_t s = slots[at];
-        if (s < keep || !in_range(s, n, a.status)) continue;
-        const int32_t m = below(s) - b_keep - m0;
-        if (m >= 0 && m < nm) {
-          src[m] = s;
-          pos[m] = p;
-        }
+      for (int32_t w = tid; w < words_of(n); w += kApplyThreads) {
+        const int32_t s0 = 32 * w, before = static_cast<int32_t>(rk[w]) - base;
+        const uint32_t low = keep >= s0 + 32 ? ~0u : (keep <= s0 ? 0u : (1u << (keep - s0)) - 1u);  // slots below keep
+        uint32_t hole = ~st[w] & low, mover = st[w] & ~low;
+        for (int32_t m = s0 - before - m0; hole; hole &= hole - 1u, ++m)
+          if (m >= 0 && m < nm) dst[m] = s0 + __ffs(hole) - 1;
+        for (int32_t m = before + __popc(st[w] & low) - b_keep - m0; mover; mover &= mover - 1u, ++m)
+          if (m >= 0 && m < nm) src[m] = s0 + __ffs(mover) - 1;
       }
       __syncthreads();
-      for (int32_t m = tid; m < nm; m += kApplyThreads) slots[static_cast<int64_t>(pos[m]) * a.Hkv] = dst[m];
-      if (high) move_slots<16>(a, fw, true, src, dst, pos, nm);
-      else move_slots<8>(a, fw, false, src, dst, pos, nm);
+      if (high) move_slots<16>(a, fw, true, src, dst, nm, slots, ctx);
+      else move_slots<8>(a, fw, false, src, dst, nm, slots, ctx);
       __syncthreads();
     }
     // vacated slots of the last kept page
@@ -520,6 +519,20 @@ __global__ void __launch_bounds__(kApplyThreads) k_evict_apply(const __grid_cons
     *reinterpret_cast<int4 *>(a.unit_hdr + 4 * static_cast<int64_t>(u)) = make_int4(un.keep_hi, un.keep_lo, need_hi, need_lo);
 }
 
+cudaError_t launch_after(void (*k)(EvictArgs), unsigned grid, int threads, size_t smem, cudaStream_t s, const EvictArgs &a) {
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3(grid);
+  c.blockDim = dim3(threads);
+  c.dynamicSmemBytes = smem;
+  c.stream = s;
+  c.attrs = &attr;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, k, a);
+}
+
 }  // namespace
 
 cudaError_t launch_evict(const EvictArgs &a, cudaStream_t s) {
@@ -531,10 +544,8 @@ cudaError_t launch_evict(const EvictArgs &a, cudaStream_t s) {
     return e;
   k_evict_plan<<<static_cast<unsigned>(a.U), kPlanThreads, plan, s>>>(a);
   if (cudaError_t e = cudaGetLastError()) return e;
-  k_evict_scan<<<1, kScanThreads, 0, s>>>(a);
-  if (cudaError_t e = cudaGetLastError()) return e;
-  k_evict_apply<<<static_cast<unsigned>(a.U), kApplyThreads, maps, s>>>(a);
-  return cudaGetLastError();
+  if (cudaError_t e = launch_after(k_evict_scan, 1, kScanThreads, 0, s, a)) return e;
+  return launch_after(k_evict_apply, static_cast<unsigned>(a.U), kApplyThreads, maps, s, a);
 }
 
 }  // namespace dkv

@@ -482,7 +482,8 @@ struct EvictWsHeader {
 
 // What the plan leaves of a unit (keep < 0: the unit stays as it is).
 struct EvictUnit {
-  int32_t keep_hi, keep_lo, freed, pad;
+  int32_t keep_hi, keep_lo, freed;
+  int32_t pad;  // the plan's error; then the blocks that are done with the unit
 };
 
 struct EvictWsLayout {

@@ -32,8 +32,9 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kBins = 2048;   // of a counting pass
-constexpr int kPlanThreads = 512, kScanThreads = 1024, kApplyThreads = 256;
-constexpr int kMoves = 2048;  // moves a block lists at a time
+constexpr int kPlanThreads = 256, kScanThreads = 1024, kApplyThreads = 256;
+constexpr int kMoves = 256;   // moves a block lists at a time
+constexpr int kIds = 1024;    // page ids of a list that a block keeps in shared memory
 
 // A later launch's blocks may start while the one before still runs and wait
 // here for its end.
@@ -83,7 +84,7 @@ __device__ __forceinline__ Place place_of(const EvictArgs &a, int32_t u) {
 // Words of the slot bitmaps: the high list's, then the low list's.
 __device__ __forceinline__ int32_t words_of(int32_t n) { return (n + 31) >> 5; }
 
-__global__ void __launch_bounds__(kPlanThreads) k_evict_plan(const __grid_constant__ EvictArgs a) {
+__global__ void __launch_bounds__(kPlanThreads, 5) k_evict_plan(const __grid_constant__ EvictArgs a) {
   let_next_launch_start();
   extern __shared__ uint32_t dyn[];
   __shared__ int32_t sm[kPlanThreads / 32];
@@ -104,8 +105,8 @@ __global__ void __launch_bounds__(kPlanThreads) k_evict_plan(const __grid_consta
     return;
   }
   const int32_t held = n_hi + n_lo, wh = words_of(n_hi), words = wh + words_of(n_lo);
-  uint32_t *stay = dyn, *gone = dyn + words;
-  uint32_t *key = a.cap > kEvictKeys ? a.keys + static_cast<int64_t>(u) * a.cap : dyn + 2 * (a.cap / 32 + 2);
+  uint32_t *stay = dyn, *gone = dyn + words, *high = dyn + 2 * (a.cap / 32 + 2);  // high: positions of the high class
+  uint32_t *key = a.cap > kEvictKeys ? a.keys + static_cast<int64_t>(u) * a.cap : high + (a.cap / 32 + 1);
   for (int32_t i = tid; i < 2 * words; i += kPlanThreads) dyn[i] = 0;
   if (tid == 0) bad_s = 0;
   for (int i = tid; i < kBins; i += kPlanThreads) hist[i] = 0;
@@ -124,8 +125,8 @@ __global__ void __launch_bounds__(kPlanThreads) k_evict_plan(const __grid_consta
   const bool quad = (G & 3) == 0 && (a.Hq & 3) == 0;  // then a token's scores are whole 16-byte words
   const float *sig = a.sig_sum + pl.row * a.Hq + pl.h * G;
   const int32_t *cnt = a.sig_cnt ? a.sig_cnt + static_cast<int64_t>(pl.r) * a.cap : nullptr;
-  constexpr int kEach = 8;  // positions a thread has in flight; the scores of positions without a token are read too
-  for (int32_t p0 = tid; p0 < ctx; p0 += kEach * kPlanThreads) {
+  constexpr int kEach = 4;  // positions a thread has in flight; the scores of positions without a token are read too
+  for (int32_t p0 = tid; p0 - tid < ctx; p0 += kEach * kPlanThreads) {
     int32_t c[kEach];
     float w[kEach];
 #pragma unroll
@@ -155,7 +156,9 @@ __global__ void __launch_bounds__(kPlanThreads) k_evict_plan(const __grid_consta
 #pragma unroll
     for (int e = 0; e < kEach; ++e) {
       const int32_t p = p0 + e * kPlanThreads;
+      const uint32_t m = __ballot_sync(kFull, c[e] == DKV_CLASS_K8V4);  // of the positions behind the last nothing is read
       if (p >= ctx) continue;
+      if (lane == 0) high[p >> 5] = m;
       uint32_t k = 0;
       if (c[e]) {
         const bool s = p < a.sinks || p >= static_cast<int64_t>(ctx) - a.window;
@@ -257,23 +260,28 @@ __global__ void __launch_bounds__(kPlanThreads) k_evict_plan(const __grid_consta
   uint32_t *gone_pos = a.gone + static_cast<int64_t>(u) * ((a.cap + 31) / 32);
   const int32_t *slots = a.slot_of + pl.row * a.Hkv + pl.h;
   bool bad = false;
-  for (int32_t p0 = 0; p0 < ctx; p0 += kPlanThreads) {
-    const int32_t p = p0 + tid;
-    bool out = false;
-    const uint32_t k = p < ctx ? key[p] : 0;
-    if (k) {
-      const int32_t c = cls[static_cast<int64_t>(p) * a.Hkv], s = slots[static_cast<int64_t>(p) * a.Hkv];
-      const bool high = c == DKV_CLASS_K8V4;
-      out = !((k & known) > T || ((k & known) == T && p <= cut));
-      if (s < 0 || s >= (high ? n_hi : n_lo)) {
-        bad = true;
-      } else {
-        const uint32_t bit = 1u << (s & 31);
-        bad |= (atomicOr((out ? gone : stay) + (high ? 0 : wh) + (s >> 5), bit) & bit) != 0;
+  for (int32_t p0 = tid; p0 - tid < ctx; p0 += kEach * kPlanThreads) {
+    int32_t slot[kEach];
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) slot[e] = slots[static_cast<int64_t>(min(p0 + e * kPlanThreads, ctx - 1)) * a.Hkv];
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      const int32_t p = p0 + e * kPlanThreads, s = slot[e];
+      bool out = false;
+      const uint32_t k = p < ctx ? key[p] : 0;
+      if (k) {
+        const bool hi_cls = high[p >> 5] >> (p & 31) & 1u;
+        out = !((k & known) > T || ((k & known) == T && p <= cut));
+        if (s < 0 || s >= (hi_cls ? n_hi : n_lo)) {
+          bad = true;
+        } else {
+          const uint32_t bit = 1u << (s & 31);
+          bad |= (atomicOr((out ? gone : stay) + (hi_cls ? 0 : wh) + (s >> 5), bit) & bit) != 0;
+        }
       }
+      const uint32_t m = __ballot_sync(kFull, out);
+      if (lane == 0 && p < ctx) gone_pos[p >> 5] = m;
     }
-    const uint32_t m = __ballot_sync(kFull, out);
-    if (lane == 0 && p < ctx) gone_pos[p >> 5] = m;
   }
   if (bad) bad_s = 1;
   __syncthreads();
@@ -343,56 +351,65 @@ __global__ void __launch_bounds__(kScanThreads) k_evict_scan(const __grid_consta
   }
 }
 
-// Where a slot of one list lies in its page.
-struct SlotAt {
-  int64_t k, v, meta, pos;  // bytes from the first page
+// One list of a unit, as a block sees it: its pages' ids, slots a page.
+struct List {
+  const int32_t *ids;
+  int32_t per, ku, vu;  // slots a page; 16-byte units of K and of V a slot
+  float inv;
 };
-__device__ __forceinline__ SlotAt slot_at(const EvictArgs &a, const int32_t *fw, bool high, int32_t s) {
-  const int32_t per = high ? a.P : 2 * a.P, j = s / per;
-  const int64_t ss = s - j * per, pg = static_cast<int64_t>(fw[j]) * a.pg.bytes;
-  const int32_t half = high ? 0 : 1;
-  return {pg + ss * 16 * (a.pg.kh >> half), pg + a.pg.vbase + ss * 16 * (a.pg.vh >> half), pg + a.pg.meta + 8 * ss,
-          pg + a.pg.pos + 4 * ss};
+// Where a slot lies: bytes of its K, V, metadata and position.
+struct SlotAt {
+  uint8_t *k, *v, *meta, *pos;
+};
+__device__ __forceinline__ SlotAt slot_at(const EvictArgs &a, const List &l, int32_t s) {
+  // s below 2^18: the quotient is exact, the product's error is below half of 1 / per
+  const int32_t j = static_cast<int32_t>((static_cast<float>(s) + 0.5f) * l.inv), ss = s - j * l.per;
+  uint8_t *pg = a.pages + l.ids[j] * a.pg.bytes;
+  return {pg + ss * (16 * l.ku), pg + a.pg.vbase + ss * (16 * l.vu), pg + a.pg.meta + 8 * ss, pg + a.pg.pos + 4 * ss};
 }
 
 // Slots src[0 .. n) of a list to dst[0 .. n), kLanes lanes a move: the 16-byte
 // units of K and V, the metadata, the position, and the index entry that goes
 // with it.
 template <int kLanes>
-__device__ __forceinline__ void move_slots(const EvictArgs &a, const int32_t *fw, bool high, const int32_t *src,
-                                           const int32_t *dst, int32_t n, int32_t *slots, int32_t ctx) {
-  const int32_t j = threadIdx.x % kLanes, ku = high ? a.pg.kh : a.pg.kh >> 1, vu = high ? a.pg.vh : a.pg.vh >> 1;
+__device__ __forceinline__ void move_slots(const EvictArgs &a, const List &l, const int32_t *src, const int32_t *dst, int32_t n,
+                                           int32_t *slots, int32_t ctx) {
+  const int32_t j = threadIdx.x % kLanes, kind = j < l.ku ? 0 : (j < l.ku + l.vu ? 1 : j - l.ku - l.vu + 2);
+  const int32_t off = kind == 0 ? 16 * j : (kind == 1 ? 16 * (j - l.ku) : 0);
+  if (kind > 3) return;
   constexpr int kGroups = kApplyThreads / kLanes, kEach = 4;
+  auto at = [&](int32_t s) {
+    const SlotAt x = slot_at(a, l, s);
+    return (kind == 0 ? x.k : kind == 1 ? x.v : kind == 2 ? x.meta : x.pos) + off;
+  };
   for (int32_t m0 = threadIdx.x / kLanes; m0 < n; m0 += kGroups * kEach) {
     uint4 x[kEach];
-    int64_t to[kEach];
 #pragma unroll
     for (int e = 0; e < kEach; ++e) {
       const int32_t m = m0 + e * kGroups;
       if (m >= n) continue;
-      const SlotAt f = slot_at(a, fw, high, src[m]), t = slot_at(a, fw, high, dst[m]);
-      to[e] = j < ku ? t.k + 16 * j : (j < ku + vu ? t.v + 16 * (j - ku) : (j == ku + vu ? t.meta : t.pos));
-      if (j < ku + vu) {
-        x[e] = __ldcs(reinterpret_cast<const uint4 *>(a.pages + (j < ku ? f.k + 16 * j : f.v + 16 * (j - ku))));
-      } else if (j == ku + vu) {
-        const uint2 y = *reinterpret_cast<const uint2 *>(a.pages + f.meta);
+      const uint8_t *f = at(src[m]);
+      if (kind < 2) {
+        x[e] = __ldcs(reinterpret_cast<const uint4 *>(f));
+      } else if (kind == 2) {
+        const uint2 y = *reinterpret_cast<const uint2 *>(f);
         x[e].x = y.x;
         x[e].y = y.y;
-      } else if (j == ku + vu + 1) {
-        x[e].x = *reinterpret_cast<const uint32_t *>(a.pages + f.pos);
+      } else {
+        x[e].x = *reinterpret_cast<const uint32_t *>(f);
       }
     }
 #pragma unroll
     for (int e = 0; e < kEach; ++e) {
       const int32_t m = m0 + e * kGroups;
       if (m >= n) continue;
-      uint8_t *p = a.pages + to[e];
-      if (j < ku + vu) {
-        *reinterpret_cast<uint4 *>(p) = x[e];
-      } else if (j == ku + vu) {
-        *reinterpret_cast<uint2 *>(p) = make_uint2(x[e].x, x[e].y);
-      } else if (j == ku + vu + 1) {
-        *reinterpret_cast<uint32_t *>(p) = x[e].x;
+      uint8_t *t = at(dst[m]);
+      if (kind < 2) {
+        *reinterpret_cast<uint4 *>(t) = x[e];
+      } else if (kind == 2) {
+        *reinterpret_cast<uint2 *>(t) = make_uint2(x[e].x, x[e].y);
+      } else {
+        *reinterpret_cast<uint32_t *>(t) = x[e].x;
         if (x[e].x < static_cast<uint32_t>(ctx)) slots[static_cast<int64_t>(x[e].x) * a.Hkv] = dst[m];
         else set_error(a.status, DKV_E_INTERNAL);
       }
@@ -400,13 +417,17 @@ __device__ __forceinline__ void move_slots(const EvictArgs &a, const int32_t *fw
   }
 }
 
-__global__ void __launch_bounds__(kApplyThreads, 4) k_evict_apply(const __grid_constant__ EvictArgs a) {
+// `slices` blocks a unit: each a share of the evicted positions and of the
+// moves; the last one to end, which finds all moves done, clears the vacated
+// slots and writes the tables.
+__global__ void __launch_bounds__(kApplyThreads, 4) k_evict_apply(const __grid_constant__ EvictArgs a, int32_t slices) {
   after_launch_before();
   extern __shared__ uint32_t dyn[];
-  __shared__ int32_t src[kMoves], dst[kMoves];
+  __shared__ int32_t src[kMoves], dst[kMoves], ids[kIds];
   __shared__ int32_t wsum[kApplyThreads / 32];
+  __shared__ int32_t last_s;
   if (a.ws->err) return;
-  const int32_t u = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int32_t u = blockIdx.x / slices, slice = blockIdx.x - u * slices, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const EvictUnit un = a.unit[u];
   if (un.keep_hi < 0) return;
   const Place pl = place_of(a, u);
@@ -420,7 +441,7 @@ __global__ void __launch_bounds__(kApplyThreads, 4) k_evict_apply(const __grid_c
   uint8_t *cls = a.classes + pl.row * a.Hkv + pl.h;
   int32_t *slots = a.slot_of + pl.row * a.Hkv + pl.h;
   const uint32_t *gone_pos = a.gone + static_cast<int64_t>(u) * ((a.cap + 31) / 32);
-  for (int32_t p = tid; p < ctx; p += kApplyThreads)
+  for (int32_t p = slice * kApplyThreads + tid; p < ctx; p += slices * kApplyThreads)
     if (__ldg(gone_pos + (p >> 5)) >> (p & 31) & 1u) {
       cls[static_cast<int64_t>(p) * a.Hkv] = DKV_CLASS_PRUNE;
       slots[static_cast<int64_t>(p) * a.Hkv] = -1;
@@ -446,9 +467,14 @@ __global__ void __launch_bounds__(kApplyThreads, 4) k_evict_apply(const __grid_c
     }
     __syncthreads();
   }
-  const int32_t *fwd = a.fwd + static_cast<int64_t>(u) * a.pmax;
-  for (int list = 0; list < 2; ++list) {
-    const bool high = list == 0;
+  int32_t *row = a.fwd + static_cast<int64_t>(u) * a.pmax;
+  auto list_of = [&](bool high) {
+    const int32_t per = high ? a.P : 2 * a.P;
+    return List{row + (high ? 0 : hd.z), per, high ? a.pg.kh : a.pg.kh >> 1, high ? a.pg.vh : a.pg.vh >> 1,
+                1.0f / static_cast<float>(per)};
+  };
+  for (int i = 0; i < 2; ++i) {
+    const bool high = i == 0;
     const int32_t n = high ? hd.x : hd.y, keep = high ? un.keep_hi : un.keep_lo, w0 = high ? 0 : wh;
     if (keep == n) continue;
     const int32_t base = high ? 0 : un.keep_hi;  // survivors of the lists before
@@ -456,39 +482,62 @@ __global__ void __launch_bounds__(kApplyThreads, 4) k_evict_apply(const __grid_c
     // survivors in slots below keep; as many movers as holes
     const int32_t b_keep = static_cast<int32_t>(rk[keep >> 5]) - base + __popc(st[keep >> 5] & ((1u << (keep & 31)) - 1u));
     const int32_t moves = keep - b_keep;
-    const int32_t *fw = fwd + (high ? 0 : hd.z);
-    for (int32_t m0 = 0; m0 < moves; m0 += kMoves) {
+    if (slice * kMoves >= moves) continue;
+    List l = list_of(high);
+    const int32_t pages = high ? hd.z : hd.w;
+    if (pages <= kIds) {
+      for (int32_t j = tid; j < pages; j += kApplyThreads) ids[j] = l.ids[j];
+      l.ids = ids;
+    }
+    for (int32_t m0 = slice * kMoves; m0 < moves; m0 += slices * kMoves) {
       const int32_t nm = min(kMoves, moves - m0);
       for (int32_t w = tid; w < words_of(n); w += kApplyThreads) {
         const int32_t s0 = 32 * w, before = static_cast<int32_t>(rk[w]) - base;
         const uint32_t low = keep >= s0 + 32 ? ~0u : (keep <= s0 ? 0u : (1u << (keep - s0)) - 1u);  // slots below keep
         uint32_t hole = ~st[w] & low, mover = st[w] & ~low;
-        for (int32_t m = s0 - before - m0; hole; hole &= hole - 1u, ++m)
-          if (m >= 0 && m < nm) dst[m] = s0 + __ffs(hole) - 1;
-        for (int32_t m = before + __popc(st[w] & low) - b_keep - m0; mover; mover &= mover - 1u, ++m)
-          if (m >= 0 && m < nm) src[m] = s0 + __ffs(mover) - 1;
+        int32_t m = s0 - before - m0;
+        if (m < nm && m + 32 > 0)
+          for (; hole; hole &= hole - 1u, ++m)
+            if (m >= 0 && m < nm) dst[m] = s0 + __ffs(hole) - 1;
+        m = before + __popc(st[w] & low) - b_keep - m0;
+        if (m < nm && m + 32 > 0)
+          for (; mover; mover &= mover - 1u, ++m)
+            if (m >= 0 && m < nm) src[m] = s0 + __ffs(mover) - 1;
       }
       __syncthreads();
-      if (high) move_slots<16>(a, fw, true, src, dst, nm, slots, ctx);
-      else move_slots<8>(a, fw, false, src, dst, nm, slots, ctx);
+      if (high) move_slots<16>(a, l, src, dst, nm, slots, ctx);
+      else move_slots<8>(a, l, src, dst, nm, slots, ctx);
       __syncthreads();
     }
-    // vacated slots of the last kept page
-    const int32_t per = high ? a.P : 2 * a.P, end = min(n, (keep + per - 1) / per * per);
-    const int32_t ku = high ? a.pg.kh : a.pg.kh >> 1, vu = high ? a.pg.vh : a.pg.vh >> 1, lanes = high ? 16 : 8;
-    for (int32_t i = tid; i < (end - keep) * lanes; i += kApplyThreads) {
-      const int32_t j = i % lanes;
-      const SlotAt t = slot_at(a, fw, high, keep + i / lanes);
-      if (j < ku) *reinterpret_cast<uint4 *>(a.pages + t.k + 16 * j) = make_uint4(0, 0, 0, 0);
-      else if (j < ku + vu) *reinterpret_cast<uint4 *>(a.pages + t.v + 16 * (j - ku)) = make_uint4(0, 0, 0, 0);
-      else if (j == ku + vu) *reinterpret_cast<uint2 *>(a.pages + t.meta) = make_uint2(0, 0);
-      else if (j == ku + vu + 1) *reinterpret_cast<int32_t *>(a.pages + t.pos) = -1;
+    __syncthreads();
+  }
+  // the last block of the unit goes on
+  if (slices > 1) {
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) last_s = atomicAdd(&a.unit[u].pad, 1) == slices - 1;
+    __syncthreads();
+    if (!last_s) return;
+    __threadfence();
+  }
+  // vacated slots of the last kept page of each list
+  for (int i = 0; i < 2; ++i) {
+    const bool high = i == 0;
+    const int32_t n = high ? hd.x : hd.y, keep = high ? un.keep_hi : un.keep_lo;
+    const List l = list_of(high);
+    const int32_t end = min(n, (keep + l.per - 1) / l.per * l.per), lanes = high ? 16 : 8;
+    for (int32_t k = tid; k < (end - keep) * lanes; k += kApplyThreads) {
+      const int32_t j = k % lanes;
+      const SlotAt t = slot_at(a, l, keep + k / lanes);
+      if (j < l.ku) *reinterpret_cast<uint4 *>(t.k + 16 * j) = make_uint4(0, 0, 0, 0);
+      else if (j < l.ku + l.vu) *reinterpret_cast<uint4 *>(t.v + 16 * (j - l.ku)) = make_uint4(0, 0, 0, 0);
+      else if (j == l.ku + l.vu) *reinterpret_cast<uint2 *>(t.meta) = make_uint2(0, 0);
+      else if (j == l.ku + l.vu + 1) *reinterpret_cast<int32_t *>(t.pos) = -1;
     }
   }
   __syncthreads();
 
   // surplus pages to the ring, in the order of the row
-  int32_t *row = a.fwd + static_cast<int64_t>(u) * a.pmax;
   const int32_t need_hi = (un.keep_hi + a.P - 1) / a.P, need_lo = (un.keep_lo + 2 * a.P - 1) / (2 * a.P);
   const uint64_t F = static_cast<uint64_t>(a.F), at0 = (a.ws->tail + static_cast<uint64_t>(a.off[u])) % F;
   const int32_t fh = hd.z - need_hi;
@@ -519,7 +568,8 @@ __global__ void __launch_bounds__(kApplyThreads, 4) k_evict_apply(const __grid_c
     *reinterpret_cast<int4 *>(a.unit_hdr + 4 * static_cast<int64_t>(u)) = make_int4(un.keep_hi, un.keep_lo, need_hi, need_lo);
 }
 
-cudaError_t launch_after(void (*k)(EvictArgs), unsigned grid, int threads, size_t smem, cudaStream_t s, const EvictArgs &a) {
+template <class... P, class... A>
+cudaError_t launch_after(void (*k)(P...), unsigned grid, int threads, size_t smem, cudaStream_t s, A... args) {
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
@@ -530,14 +580,16 @@ cudaError_t launch_after(void (*k)(EvictArgs), unsigned grid, int threads, size_
   c.stream = s;
   c.attrs = &attr;
   c.numAttrs = 1;
-  return cudaLaunchKernelEx(&c, k, a);
+  return cudaLaunchKernelEx(&c, k, static_cast<P>(args)...);
 }
 
 }  // namespace
 
 cudaError_t launch_evict(const EvictArgs &a, cudaStream_t s) {
   const size_t maps = 8 * static_cast<size_t>(a.cap / 32 + 2);
-  const size_t plan = maps + (a.cap > kEvictKeys ? 0 : 4 * static_cast<size_t>(a.cap));
+  const size_t plan = maps + 4 * static_cast<size_t>(a.cap / 32 + 1) + (a.cap > kEvictKeys ? 0 : 4 * static_cast<size_t>(a.cap));
+  // blocks a unit: one for 2048 positions
+  const int32_t slices = static_cast<int32_t>(std::min<int64_t>((a.cap + 2047) / 2048, std::max<int64_t>(1, INT32_MAX / a.U)));
   if (cudaError_t e = cudaFuncSetAttribute(k_evict_plan, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(plan)))
     return e;
   if (cudaError_t e = cudaFuncSetAttribute(k_evict_apply, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(maps)))
@@ -545,7 +597,7 @@ cudaError_t launch_evict(const EvictArgs &a, cudaStream_t s) {
   k_evict_plan<<<static_cast<unsigned>(a.U), kPlanThreads, plan, s>>>(a);
   if (cudaError_t e = cudaGetLastError()) return e;
   if (cudaError_t e = launch_after(k_evict_scan, 1, kScanThreads, 0, s, a)) return e;
-  return launch_after(k_evict_apply, static_cast<unsigned>(a.U), kApplyThreads, maps, s, a);
+  return launch_after(k_evict_apply, static_cast<unsigned>(a.U * slices), kApplyThreads, maps, s, a, slices);
 }
 
 }  // namespace dkv

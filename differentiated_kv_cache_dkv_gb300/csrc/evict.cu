@@ -32,7 +32,7 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kBins = 2048;   // of a counting pass
-constexpr int kPlanThreads = 256, kScanThreads = 1024, kApplyThreads = 256;
+constexpr int kPlanThreads = 512, kScanThreads = 1024, kApplyThreads = 256;
 constexpr int kMoves = 256;   // moves a block lists at a time
 constexpr int kIds = 1024;    // page ids of a list that a block keeps in shared memory
 
@@ -84,7 +84,7 @@ __device__ __forceinline__ Place place_of(const EvictArgs &a, int32_t u) {
 // Words of the slot bitmaps: the high list's, then the low list's.
 __device__ __forceinline__ int32_t words_of(int32_t n) { return (n + 31) >> 5; }
 
-__global__ void __launch_bounds__(kPlanThreads, 5) k_evict_plan(const __grid_constant__ EvictArgs a) {
+__global__ void __launch_bounds__(kPlanThreads, 2) k_evict_plan(const __grid_constant__ EvictArgs a) {
   let_next_launch_start();
   extern __shared__ uint32_t dyn[];
   __shared__ int32_t sm[kPlanThreads / 32];
@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(kPlanThreads, 5) k_evict_plan(const __grid_con
   const bool quad = (G & 3) == 0 && (a.Hq & 3) == 0;  // then a token's scores are whole 16-byte words
   const float *sig = a.sig_sum + pl.row * a.Hq + pl.h * G;
   const int32_t *cnt = a.sig_cnt ? a.sig_cnt + static_cast<int64_t>(pl.r) * a.cap : nullptr;
-  constexpr int kEach = 4;  // positions a thread has in flight; the scores of positions without a token are read too
+  constexpr int kEach = 8;  // positions a thread has in flight; the scores of positions without a token are read too
   for (int32_t p0 = tid; p0 - tid < ctx; p0 += kEach * kPlanThreads) {
     int32_t c[kEach];
     float w[kEach];
@@ -134,23 +134,18 @@ __global__ void __launch_bounds__(kPlanThreads, 5) k_evict_plan(const __grid_con
       const int32_t p = min(p0 + e * kPlanThreads, ctx - 1);
       c[e] = cls[static_cast<int64_t>(p) * a.Hkv];
       const float *x = sig + static_cast<int64_t>(p) * a.Hq;
+      // a token's scores one after the other: they share sectors, which stay in the first-level cache
       if (quad) {
-        const float4 y = __ldg(reinterpret_cast<const float4 *>(x));
+        float4 y = __ldg(reinterpret_cast<const float4 *>(x));
         w[e] = nan_max(nan_max(y.x, y.y), nan_max(y.z, y.w));
+        for (int g = 4; g < G; g += 4) {
+          y = __ldg(reinterpret_cast<const float4 *>(x + g));
+          w[e] = nan_max(w[e], nan_max(nan_max(y.x, y.y), nan_max(y.z, y.w)));
+        }
       } else {
         w[e] = __ldg(x);
-      }
-    }
-    for (int g = quad ? 4 : 1; g < G; g += quad ? 4 : 1) {
-#pragma unroll
-      for (int e = 0; e < kEach; ++e) {
-        const float *x = sig + static_cast<int64_t>(min(p0 + e * kPlanThreads, ctx - 1)) * a.Hq + g;
-        if (quad) {
-          const float4 y = __ldg(reinterpret_cast<const float4 *>(x));
-          w[e] = nan_max(w[e], nan_max(nan_max(y.x, y.y), nan_max(y.z, y.w)));
-        } else {
-          w[e] = nan_max(w[e], __ldg(x));
-        }
+#pragma unroll 4
+        for (int g = 1; g < G; ++g) w[e] = nan_max(w[e], __ldg(x + g));
       }
     }
 #pragma unroll
@@ -357,60 +352,59 @@ struct List {
   int32_t per, ku, vu;  // slots a page; 16-byte units of K and of V a slot
   float inv;
 };
-// Where a slot lies: bytes of its K, V, metadata and position.
-struct SlotAt {
-  uint8_t *k, *v, *meta, *pos;
-};
-__device__ __forceinline__ SlotAt slot_at(const EvictArgs &a, const List &l, int32_t s) {
+// Where a slot lies: page id and slot of the page.
+__device__ __forceinline__ int2 slot_at(const List &l, int32_t s) {
   // s below 2^18: the quotient is exact, the product's error is below half of 1 / per
-  const int32_t j = static_cast<int32_t>((static_cast<float>(s) + 0.5f) * l.inv), ss = s - j * l.per;
-  uint8_t *pg = a.pages + l.ids[j] * a.pg.bytes;
-  return {pg + ss * (16 * l.ku), pg + a.pg.vbase + ss * (16 * l.vu), pg + a.pg.meta + 8 * ss, pg + a.pg.pos + 4 * ss};
+  const int32_t j = static_cast<int32_t>((static_cast<float>(s) + 0.5f) * l.inv);
+  return make_int2(l.ids[j], s - j * l.per);
 }
 
-// Slots src[0 .. n) of a list to dst[0 .. n), kLanes lanes a move: the 16-byte
-// units of K and V, the metadata, the position, and the index entry that goes
-// with it.
+// What lane j of a slot's lanes carries: a 16-byte unit of K or V, the
+// metadata (8 bytes), the position (4) or nothing, `off` bytes into the page
+// plus `step` a slot.
+struct LanePart {
+  int32_t bytes, off, step;
+};
+__device__ __forceinline__ LanePart lane_part(const EvictArgs &a, const List &l, int32_t j) {
+  if (j < l.ku) return {16, 16 * j, 16 * l.ku};
+  j -= l.ku;
+  if (j < l.vu) return {16, static_cast<int32_t>(a.pg.vbase) + 16 * j, 16 * l.vu};
+  j -= l.vu;
+  if (j == 0) return {8, static_cast<int32_t>(a.pg.meta), 8};
+  return {j == 1 ? 4 : 0, static_cast<int32_t>(a.pg.pos), 4};
+}
+
+// Slots src[0 .. n) of a list to dst[0 .. n), kLanes lanes a move, and the
+// index entries (to_slot) that go with the positions.
 template <int kLanes>
-__device__ __forceinline__ void move_slots(const EvictArgs &a, const List &l, const int32_t *src, const int32_t *dst, int32_t n,
-                                           int32_t *slots, int32_t ctx) {
-  const int32_t j = threadIdx.x % kLanes, kind = j < l.ku ? 0 : (j < l.ku + l.vu ? 1 : j - l.ku - l.vu + 2);
-  const int32_t off = kind == 0 ? 16 * j : (kind == 1 ? 16 * (j - l.ku) : 0);
-  if (kind > 3) return;
+__device__ __forceinline__ void move_slots(const EvictArgs &a, const List &l, const int2 *src, const int2 *dst,
+                                           const int32_t *to_slot, int32_t n, int32_t *slots, int32_t ctx) {
+  const LanePart part = lane_part(a, l, threadIdx.x % kLanes);
+  if (part.bytes == 0) return;
   constexpr int kGroups = kApplyThreads / kLanes, kEach = 4;
-  auto at = [&](int32_t s) {
-    const SlotAt x = slot_at(a, l, s);
-    return (kind == 0 ? x.k : kind == 1 ? x.v : kind == 2 ? x.meta : x.pos) + off;
-  };
+  uint8_t *base = a.pages + part.off;
+  auto at = [&](int2 s) { return base + (s.x * a.pg.bytes + s.y * part.step); };
   for (int32_t m0 = threadIdx.x / kLanes; m0 < n; m0 += kGroups * kEach) {
     uint4 x[kEach];
 #pragma unroll
     for (int e = 0; e < kEach; ++e) {
-      const int32_t m = m0 + e * kGroups;
-      if (m >= n) continue;
-      const uint8_t *f = at(src[m]);
-      if (kind < 2) {
-        x[e] = __ldcs(reinterpret_cast<const uint4 *>(f));
-      } else if (kind == 2) {
-        const uint2 y = *reinterpret_cast<const uint2 *>(f);
-        x[e].x = y.x;
-        x[e].y = y.y;
-      } else {
-        x[e].x = *reinterpret_cast<const uint32_t *>(f);
-      }
+      const uint8_t *f = at(src[min(m0 + e * kGroups, n - 1)]);
+      if (part.bytes == 16) x[e] = __ldcs(reinterpret_cast<const uint4 *>(f));
+      else if (part.bytes == 8) *reinterpret_cast<uint2 *>(&x[e]) = *reinterpret_cast<const uint2 *>(f);
+      else x[e].x = *reinterpret_cast<const uint32_t *>(f);
     }
 #pragma unroll
     for (int e = 0; e < kEach; ++e) {
       const int32_t m = m0 + e * kGroups;
-      if (m >= n) continue;
+      if (m >= n) break;
       uint8_t *t = at(dst[m]);
-      if (kind < 2) {
+      if (part.bytes == 16) {
         *reinterpret_cast<uint4 *>(t) = x[e];
-      } else if (kind == 2) {
+      } else if (part.bytes == 8) {
         *reinterpret_cast<uint2 *>(t) = make_uint2(x[e].x, x[e].y);
       } else {
         *reinterpret_cast<uint32_t *>(t) = x[e].x;
-        if (x[e].x < static_cast<uint32_t>(ctx)) slots[static_cast<int64_t>(x[e].x) * a.Hkv] = dst[m];
+        if (x[e].x < static_cast<uint32_t>(ctx)) slots[static_cast<int64_t>(x[e].x) * a.Hkv] = to_slot[m];
         else set_error(a.status, DKV_E_INTERNAL);
       }
     }
@@ -423,7 +417,8 @@ __device__ __forceinline__ void move_slots(const EvictArgs &a, const List &l, co
 __global__ void __launch_bounds__(kApplyThreads, 4) k_evict_apply(const __grid_constant__ EvictArgs a, int32_t slices) {
   after_launch_before();
   extern __shared__ uint32_t dyn[];
-  __shared__ int32_t src[kMoves], dst[kMoves], ids[kIds];
+  __shared__ int2 src[kMoves], dst[kMoves];
+  __shared__ int32_t to_slot[kMoves], ids[kIds];
   __shared__ int32_t wsum[kApplyThreads / 32];
   __shared__ int32_t last_s;
   if (a.ws->err) return;
@@ -488,6 +483,7 @@ __global__ void __launch_bounds__(kApplyThreads, 4) k_evict_apply(const __grid_c
     if (pages <= kIds) {
       for (int32_t j = tid; j < pages; j += kApplyThreads) ids[j] = l.ids[j];
       l.ids = ids;
+      __syncthreads();
     }
     for (int32_t m0 = slice * kMoves; m0 < moves; m0 += slices * kMoves) {
       const int32_t nm = min(kMoves, moves - m0);
@@ -498,15 +494,18 @@ __global__ void __launch_bounds__(kApplyThreads, 4) k_evict_apply(const __grid_c
         int32_t m = s0 - before - m0;
         if (m < nm && m + 32 > 0)
           for (; hole; hole &= hole - 1u, ++m)
-            if (m >= 0 && m < nm) dst[m] = s0 + __ffs(hole) - 1;
+            if (m >= 0 && m < nm) {
+              to_slot[m] = s0 + __ffs(hole) - 1;
+              dst[m] = slot_at(l, to_slot[m]);
+            }
         m = before + __popc(st[w] & low) - b_keep - m0;
         if (m < nm && m + 32 > 0)
           for (; mover; mover &= mover - 1u, ++m)
-            if (m >= 0 && m < nm) src[m] = s0 + __ffs(mover) - 1;
+            if (m >= 0 && m < nm) src[m] = slot_at(l, s0 + __ffs(mover) - 1);
       }
       __syncthreads();
-      if (high) move_slots<16>(a, l, src, dst, nm, slots, ctx);
-      else move_slots<8>(a, l, src, dst, nm, slots, ctx);
+      if (high) move_slots<16>(a, l, src, dst, to_slot, nm, slots, ctx);
+      else move_slots<8>(a, l, src, dst, to_slot, nm, slots, ctx);
       __syncthreads();
     }
     __syncthreads();
@@ -527,12 +526,12 @@ __global__ void __launch_bounds__(kApplyThreads, 4) k_evict_apply(const __grid_c
     const List l = list_of(high);
     const int32_t end = min(n, (keep + l.per - 1) / l.per * l.per), lanes = high ? 16 : 8;
     for (int32_t k = tid; k < (end - keep) * lanes; k += kApplyThreads) {
-      const int32_t j = k % lanes;
-      const SlotAt t = slot_at(a, l, keep + k / lanes);
-      if (j < l.ku) *reinterpret_cast<uint4 *>(t.k + 16 * j) = make_uint4(0, 0, 0, 0);
-      else if (j < l.ku + l.vu) *reinterpret_cast<uint4 *>(t.v + 16 * (j - l.ku)) = make_uint4(0, 0, 0, 0);
-      else if (j == l.ku + l.vu) *reinterpret_cast<uint2 *>(t.meta) = make_uint2(0, 0);
-      else if (j == l.ku + l.vu + 1) *reinterpret_cast<int32_t *>(t.pos) = -1;
+      const LanePart part = lane_part(a, l, k % lanes);
+      const int2 at = slot_at(l, keep + k / lanes);
+      uint8_t *t = a.pages + part.off + (at.x * a.pg.bytes + at.y * part.step);
+      if (part.bytes == 16) *reinterpret_cast<uint4 *>(t) = make_uint4(0, 0, 0, 0);
+      else if (part.bytes == 8) *reinterpret_cast<uint2 *>(t) = make_uint2(0, 0);
+      else if (part.bytes == 4) *reinterpret_cast<int32_t *>(t) = -1;
     }
   }
   __syncthreads();

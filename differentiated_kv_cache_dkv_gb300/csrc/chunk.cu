@@ -18,9 +18,9 @@
 //   k_chunk_merge   joins those.
 // The roles of a block, pipelined through mbarriers:
 //   copy warp       Q, K and V by TMA, a lane a page, through a ring of tiles;
-//   product warp    one thread: S = Q K^T, O += P V.  P is read from tensor
-//     memory.  The order S0 S1 | O0 S0 O1 S1 | ... gives the tensor cores the
-//     products of one warpgroup while the other is in its softmax;
+//   product warps (2)  S = Q K^T and O += P V of a warpgroup each, P read from
+//     tensor memory; one warpgroup's products run while the other is in its
+//     softmax;
 //   softmax warps (2 x 4)  a thread per row: P = 2^(x - m) in bf16 into the
 //     columns of S, the running sum.
 // With two row tiles the warpgroups take one each and share every key tile;
@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(kAppendThreads)
 // --------------------------------------------------------------- attention --
 
 constexpr int kSoftWarps = 8, kCopyWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1;
-constexpr int kThreads = 32 * (kSoftWarps + 2);
+constexpr int kThreads = 32 * (kSoftWarps + 3);
 constexpr uint32_t kTmemCols = 512;  // S (and P) of warpgroup w at 128 w, O at 256 + 128 w
 constexpr int kRing = 5;             // K and V tiles in flight
 constexpr int kSegs = 4;
@@ -327,7 +327,7 @@ struct __align__(1024) Smem {
   uint8_t q[2][kTileBytes];        // row tiles; then the second warpgroup's outputs, by column
   uint8_t ring[kRing][kTileBytes];
   uint64_t qfull, qfree, joined, full[kRing], empty[kRing];
-  uint64_t sfull[2], pready[2], odone[2], ofree[2], ojoin, done;
+  uint64_t sfull[2], pready[2], odone[2], ofree[2], ojoin, done[2];
   Seg seg[kSegs];
   float2 ml[128];                  // the second warpgroup's references and sums
   uint32_t tmem;
@@ -404,20 +404,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int32_t *abort = &sm.abort;
   if (tid == 0) {
     mbar_init(&sm.qfull, 1);
-    mbar_init(&sm.qfree, 1 + kSoftWarps);
+    mbar_init(&sm.qfree, 2 + kSoftWarps);
     mbar_init(&sm.joined, 4);
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&sm.full[i], 1);
-      mbar_init(&sm.empty[i], 1);
+      mbar_init(&sm.empty[i], 2);
     }
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.done[i], 1);
       mbar_init(&sm.sfull[i], 1);
       mbar_init(&sm.pready[i], 4);
       mbar_init(&sm.odone[i], 1);
       mbar_init(&sm.ofree[i], 4);
     }
     mbar_init(&sm.ojoin, 4);
-    mbar_init(&sm.done, 1);
     sm.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -515,62 +515,90 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (s > 0) mbar_wait(&sm.qfull, (s - 1) & 1u, nullptr);
       for (int32_t i = max(0, c - kRing); i < c; ++i) mbar_wait(&sm.full[i % kRing], (i / kRing) & 1u, nullptr);
     }
-  } else if (warp == kMmaWarp) {
-    // ================= products, by one thread
-    if (lane == 0) {
-      constexpr uint32_t kStep = kTileBytes >> 4;
-      const uint64_t dq = sw128_desc(saddr(sm.q[0]), 16, 1024), dk = sw128_desc(saddr(sm.ring[0]), 16, 1024);
-      const uint64_t dv = sw128_desc(saddr(sm.ring[0]), kBox, 1024);
-      int32_t base = 0, np[2] = {0, 0}, nseg[2] = {0, 0};  // tiles so far; P taken, segments by warpgroup
-      bool ok = true;
-      for (int32_t s = 0; ok; ++s) {
-        if (!(ok = wait(&sm.qfull, s & 1u))) break;
-        const Seg g = sm.seg[s % kSegs];
-        if (g.nt == 0) break;
-        const bool two = g.n > tpt;
-        const int32_t total = two ? 2 * g.nt : g.nt;
-        auto scores = [&](int32_t u) {
-          const int wg = u & 1;
-          const int32_t i = 2 * (base + (two ? u >> 1 : u)), slot = i % kRing;
-          if (!(ok = wait(&sm.full[slot], (i / kRing) & 1u))) return;
-          fence_after();
-          const uint64_t da = dq + (two && wg ? kStep : 0), db = dk + slot * kStep;
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            const uint32_t o = ((kk >> 2) * kBox + (kk & 3) * 32) >> 4;
-            mma_ss(tmem + 128 * wg, da + o, db + o, idesc(true, 128, 128, false), kk > 0 ? 1u : 0u);
-          }
-          mma_commit(&sm.sfull[wg]);
-          if (!two || wg) mma_commit(&sm.empty[slot]);
-          if (u == total - 1) mma_commit(&sm.qfree);
-        };
-        scores(0);
-        if (ok && total > 1) scores(1);
-        for (int32_t u = 0; u < total && ok; ++u) {
-          const int wg = u & 1;
-          const int32_t i = 2 * (base + (two ? u >> 1 : u)) + 1, slot = i % kRing;
-          if (!(ok = wait(&sm.full[slot], (i / kRing) & 1u) && wait(&sm.pready[wg], np[wg] & 1u))) break;
-          ++np[wg];
-          if (u < 2) {  // O of the segment before has been read
-            if (nseg[wg] > 0 && !(ok = wait(&sm.ofree[wg], (nseg[wg] - 1) & 1u))) break;
-            ++nseg[wg];
-          }
-          fence_after();
-          const uint64_t db = dv + slot * kStep;
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_ts(tmem + 256 + 128 * wg, tmem + 128 * wg + 32 * (kk >> 1) + 8 * (kk & 1), db + ((kk * 2048) >> 4),
-                   idesc(true, 128, 128, true), u < 2 && kk == 0 ? 0u : 1u);
-          if (u >= total - 2) mma_commit(&sm.odone[wg]);
-          if (!two || wg) mma_commit(&sm.empty[slot]);
-          if (u + 2 < total) scores(u + 2);
+  } else if (warp >= kMmaWarp) {
+    // ================= products: a warp waits, one lane issues.  With two row tiles each of the two warps has a
+    // warpgroup's products, and while one waits, the other's keep the tensor cores busy.  With one the first
+    // warp has both, in turn.  Both warps see every tile of the ring land, in order, and a slot is free when
+    // both are done with it: a warp that skipped some could take a phase of a barrier for a later one.
+    const int me = warp - kMmaWarp;
+    constexpr uint32_t kStep = kTileBytes >> 4;
+    const uint64_t dq = sw128_desc(saddr(sm.q[0]), 16, 1024), dk = sw128_desc(saddr(sm.ring[0]), 16, 1024);
+    const uint64_t dv = sw128_desc(saddr(sm.ring[0]), kBox, 1024);
+    int32_t base = 0, np[2] = {0, 0}, nseg[2] = {0, 0};  // tiles so far; P taken, segments by warpgroup
+    bool ok = true, by_two = false;                      // the second warpgroup's last products: the second warp's
+    for (int32_t s = 0; ok; ++s) {
+      if (!(ok = warp_wait(&sm.qfull, s & 1u))) break;
+      const int32_t nt = sm.seg[s % kSegs].nt;
+      if (nt == 0) break;
+      const bool two = sm.seg[s % kSegs].n > tpt;
+      if (!two && me == 1) {  // sees the tiles only
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.qfree);
+        for (int32_t i = 2 * base; i < 2 * (base + nt) && ok; ++i) {
+          if (!(ok = warp_wait(&sm.full[i % kRing], (i / kRing) & 1u))) break;
+          if (lane == 0) mbar_arrive(&sm.empty[i % kRing]);
         }
-        base += g.nt;
+      } else {
+        auto scores = [&](int32_t t) {
+          const int wg = two ? me : t & 1;
+          const int32_t i = 2 * (base + t), slot = i % kRing;
+          if (!(ok = warp_wait(&sm.full[slot], (i / kRing) & 1u))) return;
+          // the other warp's products into this warpgroup's columns, of the segment before, are complete
+          if (wg == 1 && t < 2 && nseg[1] > 0 && by_two != two && (two ? t == 0 : t == 1) &&
+              !(ok = warp_wait(&sm.odone[1], (nseg[1] - 1) & 1u)))
+            return;
+          fence_after();
+          if (elect_one()) {
+            const uint64_t da = dq + (two && me ? kStep : 0), db = dk + slot * kStep;
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk) {
+              const uint32_t o = ((kk >> 2) * kBox + (kk & 3) * 32) >> 4;
+              mma_ss(tmem + 128 * wg, da + o, db + o, idesc(true, 128, 128, false), kk > 0 ? 1u : 0u);
+            }
+            mma_commit(&sm.sfull[wg]);
+            mma_commit(&sm.empty[slot]);
+            if (t == nt - 1) mma_commit(&sm.qfree);
+          }
+          __syncwarp();
+        };
+        const int32_t ahead = two ? 1 : 2;  // tiles whose S is issued before the first P is waited for
+        scores(0);
+        if (!two && ok && nt > 1) scores(1);
+        for (int32_t t = 0; t < nt && ok; ++t) {
+          const int wg = two ? me : t & 1;
+          const int32_t i = 2 * (base + t) + 1, slot = i % kRing;
+          if (!(ok = warp_wait(&sm.full[slot], (i / kRing) & 1u))) break;
+          // O of the segment before has been read
+          if (t < ahead && nseg[wg] > 0 && !(ok = warp_wait(&sm.ofree[wg], (nseg[wg] - 1) & 1u))) break;
+          const int32_t taken = np[wg] + (two ? t : t >> 1);
+          if (!(ok = warp_wait(&sm.pready[wg], taken & 1u))) break;
+          fence_after();
+          if (elect_one()) {
+            const uint64_t db = dv + slot * kStep;
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              mma_ts(tmem + 256 + 128 * wg, tmem + 128 * wg + 32 * (kk >> 1) + 8 * (kk & 1), db + ((kk * 2048) >> 4),
+                     idesc(true, 128, 128, true), t < ahead && kk == 0 ? 0u : 1u);
+            if (t + ahead >= nt) mma_commit(&sm.odone[wg]);
+            mma_commit(&sm.empty[slot]);
+          }
+          __syncwarp();
+          if (t + ahead < nt) scores(t + ahead);
+        }
       }
-      // every product of this thread done (also after an abort)
-      mma_commit(&sm.done);
-      mbar_wait(&sm.done, 0, nullptr);
+      np[0] += two ? nt : (nt + 1) / 2;
+      np[1] += two ? nt : nt / 2;
+      ++nseg[0];
+      if (two || nt > 1) {
+        ++nseg[1];
+        by_two = two;
+      }
+      base += nt;
     }
+    // every product of this warp done (also after an abort)
+    if (elect_one()) mma_commit(&sm.done[me]);
+    __syncwarp();
+    mbar_wait(&sm.done[me], 0, nullptr);
   } else {
     // ================= softmax warps: a thread per row
     const int wg = warp >> 2, row = tid & 127;

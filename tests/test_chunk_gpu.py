@@ -24,6 +24,12 @@ SHAPES = {
     "prompts from the start": dict(Hq=4, Hkv=2, B=64, ctx=[0, 0, 0], new=[513, 64, 128]),
     "layers": dict(Hq=6, Hkv=3, B=32, ctx=[40, 0, 300], new=[9, 1, 70], L=4, layer0=1, n_layers=2),
     "layers of one projection": dict(Hq=4, Hkv=2, B=16, ctx=[33], new=[1], L=3, layer0=0, n_layers=3, fused=True),
+    # enough of it that a block has several items, whole and cut, of one row tile, of two and of both in turn
+    "many single tokens": dict(Hq=16, Hkv=8, B=16, ctx=[37 * i % 2000 for i in range(60)], new=[1] * 60),
+    "many short items": dict(Hq=8, Hkv=8, B=16, ctx=[i % 300 for i in range(200)], new=[1 + i % 3 for i in range(200)]),
+    "many of two row tiles": dict(Hq=16, Hkv=4, B=32, ctx=[0, 100, 2000], new=[700, 300, 500], fused=True),
+    "one and two row tiles mixed": dict(Hq=16, Hkv=4, B=64, ctx=[211 * i % 1500 for i in range(40)],
+                                        new=[(1, 33, 70, 5, 64)[i % 5] for i in range(40)]),
     "none new": dict(Hq=2, Hkv=1, B=16, ctx=[5, 300, 17], new=[0, 2, 0]),
 }
 

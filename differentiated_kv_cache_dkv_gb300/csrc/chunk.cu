@@ -327,7 +327,7 @@ struct __align__(1024) Smem {
   uint8_t q[2][kTileBytes];        // row tiles; then the second warpgroup's outputs, by column
   uint8_t ring[kRing][kTileBytes];
   uint64_t qfull, qfree, joined, full[kRing], empty[kRing];
-  uint64_t sfull[2], pready[2], odone[2], ofree[2], ojoin, done[2];
+  uint64_t sfull[2], pready[2], odone[2], ofree[2], turn[2], ojoin, done[2];
   Seg seg[kSegs];
   float2 ml[128];                  // the second warpgroup's references and sums
   uint32_t tmem;
@@ -412,6 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.done[i], 1);
+      mbar_init(&sm.turn[i], 1);
       mbar_init(&sm.sfull[i], 1);
       mbar_init(&sm.pready[i], 4);
       mbar_init(&sm.odone[i], 1);
@@ -525,6 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t dq = sw128_desc(saddr(sm.q[0]), 16, 1024), dk = sw128_desc(saddr(sm.ring[0]), 16, 1024);
     const uint64_t dv = sw128_desc(saddr(sm.ring[0]), kBox, 1024);
     int32_t base = 0, np[2] = {0, 0}, nseg[2] = {0, 0};  // tiles so far; P taken, segments by warpgroup
+    int32_t turns = 0;                                   // tiles of two row tiles so far
     bool ok = true, by_two = false;                      // the second warpgroup's last products: the second warp's
     for (int32_t s = 0; ok; ++s) {
       if (!(ok = warp_wait(&sm.qfull, s & 1u))) break;
@@ -562,7 +564,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
         };
         const int32_t ahead = two ? 1 : 2;  // tiles whose S is issued before the first P is waited for
+        // Products go in turn, PV and S of one warpgroup, then of the other.  Mixed, they would end together,
+        // and both warpgroups would be in their softmax at the same time, with the tensor cores idle (a late
+        // chunk: 1016 us mixed).
+        auto other_turn = [&] {
+          if (two && lane == 0) mbar_arrive(&sm.turn[me ^ 1]);
+        };
         scores(0);
+        if (me == 1) other_turn();
         if (!two && ok && nt > 1) scores(1);
         for (int32_t t = 0; t < nt && ok; ++t) {
           const int wg = two ? me : t & 1;
@@ -572,6 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (t < ahead && nseg[wg] > 0 && !(ok = warp_wait(&sm.ofree[wg], (nseg[wg] - 1) & 1u))) break;
           const int32_t taken = np[wg] + (two ? t : t >> 1);
           if (!(ok = warp_wait(&sm.pready[wg], taken & 1u))) break;
+          if (two && !(ok = warp_wait(&sm.turn[me], (turns + t) & 1u))) break;
           fence_after();
           if (elect_one()) {
             const uint64_t db = dv + slot * kStep;
@@ -584,7 +594,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           __syncwarp();
           if (t + ahead < nt) scores(t + ahead);
+          if (me == 0 || t + 1 < nt) other_turn();
         }
+        if (two) turns += nt;
       }
       np[0] += two ? nt : (nt + 1) / 2;
       np[1] += two ? nt : nt / 2;

@@ -589,6 +589,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int kk = 0; kk < 8; ++kk)
               mma_ts(tmem + 256 + 128 * wg, tmem + 128 * wg + 32 * (kk >> 1) + 8 * (kk & 1), db + ((kk * 2048) >> 4),
                      idesc(true, 128, 128, true), t < ahead && kk == 0 ? 0u : 1u);
+            if (!two) {  // the weights' second halves
+#pragma unroll
+              for (int kk = 0; kk < 8; ++kk)
+                mma_ts(tmem + 256 + 128 * wg, tmem + 128 * wg + 32 * (kk >> 1) + 16 + 8 * (kk & 1), db + ((kk * 2048) >> 4),
+                       idesc(true, 128, 128, true), 1u);
+            }
             if (t + ahead >= nt) mma_commit(&sm.odone[wg]);
             mma_commit(&sm.empty[slot]);
           }
@@ -657,8 +663,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             sum = f2_add(sum, f2_add(t2[0], t2[1]));
           };
           bool care = __any_sync(kFull, live && !(fabsf(m) < kFar));
-          // the usual tile; one with masked columns goes the careful way
-          care |= masked;
+          // the usual tile; one with masked columns goes the careful way, and every tile of a single row tile
+          care |= masked || !two;
           if (!care) {
             const uint64_t nm2 = f2_pack(-m, -m);
             uint32_t u[2][32];
@@ -682,7 +688,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               keep_columns(u, lim - 32 * c);
               mx = fmaxf(mx, max32(u));
             }
-            const float mn = live ? fmaxf(m, ceilf(mx * sl2)) : 0.0f;
+            // the reference moves when it is passed by more than 2^8 (and where the row starts)
+            const float top = ceilf(mx * sl2), mn = live && top > m + 8.0f ? top : m;
             const float f = mn == m ? 1.0f : ex2(m - mn);  // 2^-inf = 0 where the row starts
             if (started && __any_sync(kFull, f != 1.0f)) {
               // the products into O were complete when S was
@@ -713,7 +720,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float p1 = ex2(__fsub_rn(__fmul_rn(__uint_as_float(u[2 * e + 1]), sl2), mo));
                 sum = f2_add(sum, f2_pack(p0, p1));
                 w[16 * c + e] = bf16x2_rn(p0, p1);
+                u[e] = bf16x2_rest(p0, p1, w[16 * c + e]);
               }
+              if (!two) tmem_st16(ts_s + 32 * c + 16, u);  // what the rounding left of the weights
             }
           }
           l2 = f2_add(l2, sum);

@@ -678,16 +678,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             care = __any_sync(kFull, live && !(f2_sum(sum) <= kMost));
           }
-          if (__builtin_expect(care, 0)) {
-            uint32_t u[32];
+          if (care) {
+            // S by 32 columns, the next ones on their way while f has these
+            auto columns = [&](auto f) {
+              uint32_t u[2][32];
+              tmem_ld32(ts_s, u[0]);
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                tmem_wait32(u[c & 1]);
+                if (c < 3) tmem_ld32(ts_s + 32 * (c + 1), u[(c + 1) & 1]);
+                if (masked) keep_columns(u[c & 1], lim - 32 * c);
+                f(u[c & 1], c);
+              }
+            };
             float mx = -INFINITY;
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              tmem_ld32(ts_s + 32 * c, u);
-              tmem_wait32(u);
-              keep_columns(u, lim - 32 * c);
-              mx = fmaxf(mx, max32(u));
-            }
+            columns([&](uint32_t(&u)[32], int) { mx = fmaxf(mx, max32(u)); });
             // the reference moves when it is passed by more than 2^8 (and where the row starts)
             const float top = ceilf(mx * sl2), mn = live && top > m + 8.0f ? top : m;
             const float f = mn == m ? 1.0f : ex2(m - mn);  // 2^-inf = 0 where the row starts
@@ -707,23 +712,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             l2 = f2_mul(l2, f2_pack(f, f));
             m = mn;
             const float mo = m == -INFINITY ? 0.0f : m;
-            sum = 0;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              tmem_ld32(ts_s + 32 * c, u);
-              tmem_wait32(u);
-              keep_columns(u, lim - 32 * c);
+            uint64_t t2[2] = {0, 0};
+            columns([&](uint32_t(&u)[32], int c) {
 #pragma unroll
               for (int e = 0; e < 16; ++e) {
-                // rounded before the reference is taken off: what is left of the largest logit is at most 0
+                // rounded before the reference is taken off: what is left of the largest logit is at most 2^8
+                // (not as packed pairs: those two operations came out as one, without the rounding)
                 const float p0 = ex2(__fsub_rn(__fmul_rn(__uint_as_float(u[2 * e]), sl2), mo));
                 const float p1 = ex2(__fsub_rn(__fmul_rn(__uint_as_float(u[2 * e + 1]), sl2), mo));
-                sum = f2_add(sum, f2_pack(p0, p1));
+                t2[e & 1] = f2_add(t2[e & 1], f2_pack(p0, p1));
                 w[16 * c + e] = bf16x2_rn(p0, p1);
                 u[e] = bf16x2_rest(p0, p1, w[16 * c + e]);
               }
               if (!two) tmem_st16(ts_s + 32 * c + 16, u);  // what the rounding left of the weights
-            }
+            });
+            sum = f2_add(t2[0], t2[1]);
           }
           l2 = f2_add(l2, sum);
 #pragma unroll

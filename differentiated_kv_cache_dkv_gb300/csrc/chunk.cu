@@ -24,7 +24,11 @@
 //   softmax warps (2 x 4)  a thread per row: P = 2^(x - m) in bf16 into the
 //     columns of S, the running sum.
 // With two row tiles the warpgroups take one each and share every key tile;
-// with one they take every other key tile of it and join their results.
+// with one they take every other key tile of it and join their results.  Up to
+// 16 rows lie four times in their row tile, once in each warp's 32 lanes of
+// tensor memory, and every warp weighs a quarter of a key tile's columns: eight
+// softmaxes over keys of their own, joined at the end (one warp alone would
+// take 3000 cycles a tile: 64 single tokens 314 us).
 //
 // The reference m of a row is the first tile's maximum, rounded up to a whole
 // number (log2 units), and moves only when the sum of a tile's weights passes
@@ -326,10 +330,10 @@ struct Seg {
 struct __align__(1024) Smem {
   uint8_t q[2][kTileBytes];        // row tiles; then the second warpgroup's outputs, by column
   uint8_t ring[kRing][kTileBytes];
-  uint64_t qfull, qfree, joined, full[kRing], empty[kRing];
+  uint64_t qfull, qfree, joined, qjoin, full[kRing], empty[kRing];
   uint64_t sfull[2], pready[2], odone[2], ofree[2], turn[2], ojoin, done[2];
   Seg seg[kSegs];
-  float2 ml[128];                  // the second warpgroup's references and sums
+  float2 ml[128];                  // the second warpgroup's references and sums; [8][16] of eight warps
   uint32_t tmem;
   int32_t abort;
 };
@@ -394,9 +398,24 @@ __device__ __forceinline__ float max32(const uint32_t (&u)[32]) {
   return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
 
+// This thread's row of O times f.  (The products into O were complete when S was.)
+__device__ __forceinline__ void scale_row(uint32_t o, float f) {
+#pragma unroll 1
+  for (int c = 0; c < 8; ++c) {
+    uint32_t x[16];
+    tmem_ld16(o + 16 * c, x);
+    tmem_wait16(x);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
+    tmem_st16(o + 16 * c, x);
+  }
+  tmem_wait_st();
+}
+
 __global__ void __launch_bounds__(kThreads, 1)
     k_chunk(const __grid_constant__ ChunkArgs a, const PlanPtrs p, const __grid_constant__ CUtensorMap qmap,
-            const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, int32_t tpt, int32_t rows) {
+            const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+            const __grid_constant__ CUtensorMap qmap4, int32_t tpt, int32_t tpq, int32_t rows) {
   extern __shared__ unsigned char smem_raw[];
   // aligned by an offset, not by an integer address: the compiler then knows that these are shared accesses
   Smem &sm = *reinterpret_cast<Smem *>(smem_raw + (-saddr(smem_raw) & 1023u));
@@ -405,7 +424,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     mbar_init(&sm.qfull, 1);
     mbar_init(&sm.qfree, 2 + kSoftWarps);
-    mbar_init(&sm.joined, 4);
+    mbar_init(&sm.joined, kSoftWarps);
+    mbar_init(&sm.qjoin, kSoftWarps);
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&sm.full[i], 1);
       mbar_init(&sm.empty[i], 2);
@@ -491,19 +511,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) {
         sm.seg[s % kSegs] = g;
         if (g.nt > 0) {
-          const int tiles = g.n > tpt ? 2 : 1;
-          mbar_expect_tx(&sm.qfull, tiles * 2 * tpt * G * 128);
-          for (int t = 0; t < tiles; ++t)
-            for (int half = 0; half < 2; ++half)
-              copy_box(sm.q[t] + half * kBox, &qmap, half * 64, g.h * G,
-                       static_cast<int32_t>(g.li * a.T + g.tok + t * tpt), &sm.qfull);
+          const int32_t at = static_cast<int32_t>(g.li * a.T + g.tok);
+          if (g.n <= tpq) {
+            mbar_expect_tx(&sm.qfull, 4 * 2 * tpq * G * 128);
+            for (int t = 0; t < 4; ++t)
+              for (int half = 0; half < 2; ++half)
+                copy_box(sm.q[0] + half * kBox + 32 * t * 128, &qmap4, half * 64, g.h * G, at, &sm.qfull);
+          } else {
+            const int tiles = g.n > tpt ? 2 : 1;
+            mbar_expect_tx(&sm.qfull, tiles * 2 * tpt * G * 128);
+            for (int t = 0; t < tiles; ++t)
+              for (int half = 0; half < 2; ++half)
+                copy_box(sm.q[t] + half * kBox, &qmap, half * 64, g.h * G, at + t * tpt, &sm.qfull);
+          }
         } else {
           mbar_arrive(&sm.qfull);
         }
       }
       __syncwarp();
       if (g.nt == 0) break;
-      joining = g.n <= tpt && g.nt > 1;
+      joining = g.n <= tpq || (g.n <= tpt && g.nt > 1);
       for (int32_t t = 1; t < g.nt && ok; ++t) {
         const int32_t now = id;
         id = t + 1 < g.nt ? page_of(g.t0 + t + 1) : -1;
@@ -624,8 +651,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t sl2x2 = f2_pack(sl2, sl2);
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const uint32_t ts_s = tmem + lanes + 128 * wg, ts_o = tmem + lanes + 256 + 128 * wg;
-    const int32_t rt = row / G;  // token of the row tile
-    int32_t base = 0, ns = 0, nseg = 0, joins = 0;
+    int32_t base = 0, ns = 0, nseg = 0, joins = 0, qjoins = 0;
     bool ok = true;
     for (int32_t s = 0; ok; ++s) {
       if (!(ok = warp_wait(&sm.qfull, s & 1u))) break;
@@ -634,8 +660,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(&sm.qfree);
       if (g.nt == 0) break;
       const bool two = g.n > tpt;
-      const int32_t i = (two && wg ? tpt : 0) + rt;  // token of the item
-      const bool live = rt < tpt && i < g.n;
+      const bool four = g.n <= tpq;                   // the rows lie four times in the row tile
+      const int32_t rt = (four ? lane : row) / G;     // token of the row tile
+      const int32_t i = (two && wg ? tpt : 0) + rt;   // token of the item
+      const bool live = rt < (four ? tpq : tpt) && i < g.n;
       const bool some = __any_sync(kFull, live);
       const int32_t end = g.ctx + g.i0 + g.n;
       float m = live ? -INFINITY : 0.0f;
@@ -645,7 +673,39 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = warp_wait(&sm.sfull[wg], ns & 1u))) break;
         fence_after();
         const int32_t k0 = 128 * (g.t0 + t);
-        if (some) {
+        if (four) {
+          const int q = warp & 3;  // this warp's columns: 32 q .. + 31
+          const int32_t lim = live ? g.ctx + g.i0 + i + 1 - k0 - 32 * q : 32;
+          uint32_t u[32], w[16];
+          tmem_ld32(ts_s + 32 * q, u);
+          tmem_wait32(u);
+          if (__any_sync(kFull, lim < 32)) keep_columns(u, lim);
+          const float top = ceilf(max32(u) * sl2), mn = live && top > m + 8.0f ? top : m;
+          const float f = mn == m ? 1.0f : ex2(m - mn);
+          if (started && __any_sync(kFull, f != 1.0f)) scale_row(ts_o, f);
+          l2 = f2_mul(l2, f2_pack(f, f));
+          m = mn;
+          const float mo = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float p0 = ex2(__fsub_rn(__fmul_rn(__uint_as_float(u[2 * e]), sl2), mo));
+            const float p1 = ex2(__fsub_rn(__fmul_rn(__uint_as_float(u[2 * e + 1]), sl2), mo));
+            l2 = f2_add(l2, f2_pack(p0, p1));
+            w[e] = bf16x2_rn(p0, p1);
+            u[e] = bf16x2_rest(p0, p1, w[e]);
+          }
+          uint32_t zero[16] = {};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            if (c == q) {
+              tmem_st16(ts_s + 32 * c, w);
+              tmem_st16(ts_s + 32 * c + 16, u);
+            } else {
+              tmem_st16(ts_s + 32 * c, zero);
+              tmem_st16(ts_s + 32 * c + 16, zero);
+            }
+          }
+        } else if (some) {
           const int32_t lim = live ? g.ctx + g.i0 + i + 1 - k0 : 128;
           const bool masked = __any_sync(kFull, lim < 128);
           uint32_t w[64];  // P, two columns each
@@ -696,19 +756,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // the reference moves when it is passed by more than 2^8 (and where the row starts)
             const float top = ceilf(mx * sl2), mn = live && top > m + 8.0f ? top : m;
             const float f = mn == m ? 1.0f : ex2(m - mn);  // 2^-inf = 0 where the row starts
-            if (started && __any_sync(kFull, f != 1.0f)) {
-              // the products into O were complete when S was
-#pragma unroll 1
-              for (int c = 0; c < 8; ++c) {
-                uint32_t x[16];
-                tmem_ld16(ts_o + 16 * c, x);
-                tmem_wait16(x);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
-                tmem_st16(ts_o + 16 * c, x);
-              }
-              tmem_wait_st();
-            }
+            if (started && __any_sync(kFull, f != 1.0f)) scale_row(ts_o, f);
             l2 = f2_mul(l2, f2_pack(f, f));
             m = mn;
             const float mo = m == -INFINITY ? 0.0f : m;
@@ -751,6 +799,68 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       // ---- the segment's results
+      if (four) {
+        // a warp's rows go to shared memory, [warp][column][16 rows]; then a thread joins eight columns of a row
+        float *ox = reinterpret_cast<float *>(sm.q[0]) + warp * (128 * 16);
+        if (started) {
+          if (!(ok = warp_wait(&sm.odone[wg], nseg & 1u))) break;
+          ++nseg;
+          fence_after();
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t u[32];
+            tmem_ld32(ts_o + 32 * c, u);
+            tmem_wait32(u);
+            if (live) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) ox[(32 * c + e) * 16 + lane] = __uint_as_float(u[e]);
+            }
+          }
+        }
+        if (lane < 16) sm.ml[warp * 16 + lane] = make_float2(m, f2_sum(l2));
+        fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (started) mbar_arrive(&sm.ofree[wg]);
+          mbar_arrive(&sm.qjoin);
+        }
+        if (!(ok = warp_wait(&sm.qjoin, qjoins & 1u))) break;
+        ++qjoins;
+        const int32_t jr = tid & 15, col = 8 * (tid >> 4);
+        if (jr < g.n * G) {
+          float mm = -INFINITY, l = 0.0f, x[8] = {};
+#pragma unroll
+          for (int w = 0; w < kSoftWarps; ++w) mm = fmaxf(mm, sm.ml[w * 16 + jr].x);
+#pragma unroll
+          for (int w = 0; w < kSoftWarps; ++w) {
+            const float2 y = sm.ml[w * 16 + jr];
+            if (y.x == -INFINITY) continue;  // nothing of the row was this warp's
+            const float f = y.x == mm ? 1.0f : ex2(y.x - mm);
+            l += y.y * f;
+            const float *o = reinterpret_cast<const float *>(sm.q[0]) + (w * 128 + col) * 16 + jr;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] += o[16 * e] * f;
+          }
+          const int64_t at = (static_cast<int64_t>(g.li) * a.T + g.tok + jr / G) * a.Hq + g.h * G + jr % G;
+          if (g.slot < 0) {
+            const float inv = 1.0f / l;
+            *reinterpret_cast<uint4 *>(a.out + at * 128 + col) =
+                make_uint4(bf16x2_rn(x[0] * inv, x[1] * inv), bf16x2_rn(x[2] * inv, x[3] * inv),
+                           bf16x2_rn(x[4] * inv, x[5] * inv), bf16x2_rn(x[6] * inv, x[7] * inv));
+            if (a.lse && col == 0) a.lse[at] = (mm + log2f(l)) * 0.693147180559945309f;
+          } else {
+            const int64_t part = static_cast<int64_t>(g.slot) * rows + jr;
+            *reinterpret_cast<float4 *>(p.o + part * 128 + col) = make_float4(x[0], x[1], x[2], x[3]);
+            *reinterpret_cast<float4 *>(p.o + part * 128 + col + 4) = make_float4(x[4], x[5], x[6], x[7]);
+            if (col == 0) p.ml[part] = make_float2(mm, l);
+          }
+        }
+        fence_async();  // the next Q is copied where these reads were
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.joined);
+        base += g.nt;
+        continue;
+      }
       const bool join = !two && g.nt > 1;
       float l = f2_sum(l2);
       const int64_t at = (static_cast<int64_t>(g.li) * a.T + g.tok + i) * a.Hq + g.h * G + (row - rt * G);
@@ -810,11 +920,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           else if (live && a.lse) a.lse[at] = (m + log2f(l)) * 0.693147180559945309f;
         }
         fence_before();
-        if (join && wg == 0) fence_async();  // the next Q is copied where these reads were
+        if (join) fence_async();  // the next Q is copied where these reads (and the other's writes) were
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(&sm.ofree[wg]);
-          if (join) mbar_arrive(wg ? &sm.ojoin : &sm.joined);
+          if (join && wg == 1) mbar_arrive(&sm.ojoin);
+          if (join) mbar_arrive(&sm.joined);
         }
         if (join) ++joins;
       }
@@ -895,10 +1006,13 @@ cudaError_t launch_chunk(const ChunkArgs &a, void *ws, cudaStream_t s) {
   if ((e = chunk_map(&vmap, a.v, a.Hkv, 128, rows, stride, 1, a.B)) != cudaSuccess) return e;
   if ((e = cudaFuncSetAttribute(k_chunk, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes))) != cudaSuccess)
     return e;
+  const int32_t tpq = 16 / a.G;  // tokens whose rows lie four times in a row tile
+  alignas(64) CUtensorMap qmap4;
+  if ((e = chunk_map(&qmap4, a.q, a.Hq, 128, a.n_layers * a.T, a.q_stride, a.G, std::max(tpq, 1))) != cudaSuccess) return e;
   const int64_t copies = a.k_new ? a.n_layers * ((a.T + kAppendTokens - 1) / kAppendTokens) : 0;
   k_chunk_append<<<static_cast<unsigned>(1 + copies), kAppendThreads, 0, s>>>(a, p, w.tpi, grid);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  if ((e = launch_after(k_chunk, dim3(grid), kThreads, kSmemBytes, s, a, p, qmap, kmap, vmap, w.tpt, w.rows)) != cudaSuccess) return e;
+  if ((e = launch_after(k_chunk, dim3(grid), kThreads, kSmemBytes, s, a, p, qmap, kmap, vmap, qmap4, w.tpt, tpq, w.rows)) != cudaSuccess) return e;
   return launch_after(k_chunk_merge, dim3(grid, (w.rows + kMergeRows - 1) / kMergeRows), 32 * kMergeRows, 0, s, a, p, w.tpi, w.rows, grid);
 }
 

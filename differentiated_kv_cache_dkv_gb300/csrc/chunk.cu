@@ -5,7 +5,7 @@
 // i G + g within its unit (layer, request, KV head); with that packing the
 // heads of a group share every tile of K and V.  A row tile is tpt = 128 / G
 // whole tokens, an item two row tiles (or one, when no more rows are left) of
-// a unit against its keys, in key tiles of 128 positions.  Three launches:
+// a unit against its keys, in key tiles of 128 positions.  Two launches:
 //   k_chunk_append  stores the new tokens' K and V in their pages; block 0
 //     meanwhile plans: tokens, items and key tiles of each request, and which
 //     of them each block of the attention takes.
@@ -14,8 +14,7 @@
 //     same time, which keeps them in L2), as many waves as leave every block at
 //     or below the mean; the rest of the key tiles, laid end to end, is cut so
 //     that all blocks end up with the same number.  Items that are cut leave
-//     partial results.
-//   k_chunk_merge   joins those.
+//     partial results, which the block that ends last joins.
 // The roles of a block, pipelined through mbarriers:
 //   copy warp       Q, K and V by TMA, a lane a page, through a ring of tiles;
 //   product warps (2)  S = Q K^T and O += P V of a warpgroup each, P read from
@@ -50,7 +49,8 @@ using namespace tc;
 
 constexpr int kBlocks = 152;        // most blocks of the attention: one a multiprocessor
 constexpr int kMaxWaves = 64;       // of whole items; the plan looks at each
-constexpr int kSmemReqs = 1024;     // requests whose first items the plan keeps in shared memory
+constexpr int kSmemReqs = 256;      // requests, and items a unit of them, that the plan keeps in shared memory
+constexpr int kSmemItems = 1024;
 
 struct PlanHeader {
   int64_t tiles;   // key tiles of all items
@@ -71,12 +71,13 @@ struct PlanPtrs {
   ReqPlan *req;    // [R]
   int32_t *pre;    // [items a unit of all requests]: key tiles of the request's items before
   int64_t *cut;    // [grid + 1]: where each block's share of the cut tiles starts
-  float *o;        // [2 grid][rows][128] partial results
+  int32_t *count;  // [grid]: parts that are there, of the item whose first part is the block's last
+  float4 *o;       // [2 grid][32][rows] partial results, four channels each
   float2 *ml;      // [2 grid][rows]: reference and sum
 };
 
 struct ChunkLayout {
-  size_t req, pre, cut, ml, o, bytes;
+  size_t req, pre, cut, count, ml, o, bytes;
   int32_t tpt, tpi, rows;  // tokens a row tile, an item; rows of a partial result
 };
 
@@ -89,6 +90,7 @@ __host__ ChunkLayout chunk_layout(const ChunkArgs &a) {
   w.req = x; x = align256(x + sizeof(ReqPlan) * static_cast<size_t>(a.R));
   w.pre = x; x = align256(x + 4 * (static_cast<size_t>(a.T / w.tpi) + a.R + 1));
   w.cut = x; x = align256(x + 8 * (kBlocks + 1));
+  w.count = x; x = align256(x + 4 * kBlocks);
   w.ml = x;  x = align256(x + sizeof(float2) * 2 * kBlocks * static_cast<size_t>(w.rows));
   w.o = x;   x = align256(x + 512 * 2 * kBlocks * static_cast<size_t>(w.rows));
   w.bytes = x;
@@ -155,9 +157,13 @@ __device__ __forceinline__ int32_t item_tiles(const PlanPtrs &p, const ReqPlan &
 // Block 0: what every block of the attention takes.
 __device__ void plan(const ChunkArgs &a, const PlanPtrs &p, int32_t tpi, int32_t grid) {
   __shared__ int64_t sm64[kAppendThreads / 32];
-  __shared__ int32_t first_s[kSmemReqs];
+  __shared__ ReqPlan req_sm[kSmemReqs];
+  __shared__ int32_t pre_sm[kSmemItems];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t U1 = static_cast<int64_t>(a.n_layers) * a.Hkv;
+  // read again and again: from shared memory where there is room
+  ReqPlan *req = a.R <= kSmemReqs ? req_sm : p.req;
+  for (int32_t c = tid; c < grid; c += kAppendThreads) p.count[c] = 0;
   // tokens and items before each request
   int64_t tok = 0, rts = 0;
   for (int32_t r0 = 0; r0 < a.R; r0 += kAppendThreads) {
@@ -174,16 +180,16 @@ __device__ void plan(const ChunkArgs &a, const PlanPtrs &p, int32_t tpi, int32_t
       q.tiles = 0;
       q.ctx = __ldg(a.ctx_lens + r);
       q.n = static_cast<int32_t>(n);
-      p.req[r] = q;
-      if (r < kSmemReqs) first_s[r] = q.rt0;
+      req[r] = q;
     }
     tok += t1;
     rts += t2;
   }
+  int32_t *pre = rts <= kSmemItems ? pre_sm : p.pre;
   __syncthreads();
   // key tiles of each item: a warp a request
   for (int32_t r = warp; r < a.R; r += kAppendThreads / 32) {
-    const ReqPlan q = p.req[r];
+    const ReqPlan q = req[r];
     int32_t sum = 0;
     for (int32_t j0 = 0; j0 < q.items; j0 += 32) {
       const int32_t j = j0 + lane;
@@ -194,33 +200,40 @@ __device__ void plan(const ChunkArgs &a, const PlanPtrs &p, int32_t tpi, int32_t
         const int32_t y = __shfl_up_sync(kFull, incl, o);
         if (lane >= o) incl += y;
       }
-      if (j < q.items) p.pre[q.rt0 + j] = sum + incl - t;
+      if (j < q.items) pre[q.rt0 + j] = sum + incl - t;
       sum += __shfl_sync(kFull, incl, 31);
     }
-    if (lane == 0) p.req[r].tiles = sum;
+    if (lane == 0) req[r].tiles = sum;
   }
   __syncthreads();
   int64_t W = 0;
   for (int32_t r0 = 0; r0 < a.R; r0 += kAppendThreads) {
     const int32_t r = r0 + tid;
-    const int64_t s = r < a.R ? p.req[r].tiles * U1 : 0;
+    const int64_t s = r < a.R ? req[r].tiles * U1 : 0;
     int64_t t1;
     const int64_t b = block_scan(s, sm64, t1);
-    if (r < a.R) p.req[r].tile0 = W + b;
+    if (r < a.R) req[r].tile0 = W + b;
     W += t1;
   }
   __syncthreads();
+  if (req == req_sm)
+    for (int32_t r = tid; r < a.R; r += kAppendThreads) p.req[r] = req[r];
+  if (pre == pre_sm)
+    for (int32_t i = tid; i < static_cast<int32_t>(rts); i += kAppendThreads) p.pre[i] = pre[i];
   // waves of whole items, while no block gets more than the mean
   const int64_t items = rts * U1, target = (W + grid - 1) / grid;
-  auto first = [&](int32_t r) { return (a.R <= kSmemReqs ? first_s[r] : p.req[r].rt0) * U1; };
+  auto first = [&](int32_t r) { return req[r].rt0 * U1; };
+  auto tiles_of = [&](const ReqPlan &q, int32_t j) {
+    return (j + 1 < q.items ? pre[q.rt0 + j + 1] : q.tiles) - pre[q.rt0 + j];
+  };
   int64_t mine = 0;
   int32_t waves = 0;
   for (; waves < kMaxWaves && (waves + 1) * static_cast<int64_t>(grid) <= items; ++waves) {
     int64_t d = mine;
     if (tid < grid) {
       const int64_t i = waves * static_cast<int64_t>(grid) + tid;
-      const ReqPlan q = p.req[find_req(a.R, first, i)];
-      d += item_tiles(p, q, static_cast<int32_t>((i - q.rt0 * U1) % q.items));
+      const ReqPlan &q = req[find_req(a.R, first, i)];
+      d += tiles_of(q, static_cast<int32_t>((i - q.rt0 * U1) % q.items));
     }
     if (__syncthreads_or(d > target)) break;
     mine = d;
@@ -229,9 +242,9 @@ __device__ void plan(const ChunkArgs &a, const PlanPtrs &p, int32_t tpi, int32_t
   int64_t cut0 = W;
   if (waves * static_cast<int64_t>(grid) < items) {
     const int64_t i = waves * static_cast<int64_t>(grid);
-    const ReqPlan q = p.req[find_req(a.R, first, i)];
+    const ReqPlan &q = req[find_req(a.R, first, i)];
     const int64_t k = i - q.rt0 * U1;
-    cut0 = q.tile0 + k / q.items * q.tiles + p.pre[q.rt0 + static_cast<int32_t>(k % q.items)];
+    cut0 = q.tile0 + k / q.items * q.tiles + pre[q.rt0 + static_cast<int32_t>(k % q.items)];
   }
   int64_t all;
   const int64_t b = block_scan(tid < grid ? target - mine : 0, sm64, all);
@@ -325,17 +338,18 @@ struct Seg {
   int32_t li, h, r;
   int32_t tok, i0, n;    // the item's first token in the batch and in the request, its tokens
   int32_t ctx;
+  int32_t parts, part0, part0_slot;  // of a cut item: how many, the block that has the first, its slot
 };
 
 struct __align__(1024) Smem {
   uint8_t q[2][kTileBytes];        // row tiles; then the second warpgroup's outputs, by column
   uint8_t ring[kRing][kTileBytes];
-  uint64_t qfull, qfree, joined, qjoin, full[kRing], empty[kRing];
+  uint64_t qfull, qfree, joined, qjoin, parted, partgo, full[kRing], empty[kRing];
   uint64_t sfull[2], pready[2], odone[2], ofree[2], turn[2], ojoin, done[2];
   Seg seg[kSegs];
   float2 ml[128];                  // the second warpgroup's references and sums; [8][16] of eight warps
   uint32_t tmem;
-  int32_t abort;
+  int32_t abort, last;
 };
 constexpr size_t kSmemBytes = sizeof(Smem) + 1024;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
@@ -370,6 +384,21 @@ __device__ __forceinline__ Seg next_seg(const ChunkArgs &a, const PlanPtrs &p, i
     g.t0 = static_cast<int32_t>(in - p.pre[q.rt0 + j]);
     g.nt = static_cast<int32_t>(min(static_cast<int64_t>(all - g.t0), w1 - w));
     g.slot = g.nt == all ? -1 : 2 * c + (w == w0 ? 0 : 1);
+    if (g.slot >= 0) {  // the blocks that have a part of the item
+      const int64_t begin = w - g.t0, end = begin + all;
+      const int lane = threadIdx.x & 31;
+      g.part0 = -1;
+      for (int32_t b0 = 0; b0 < grid; b0 += 32) {
+        const int32_t b = b0 + lane;
+        const int64_t x0 = b < grid ? p.cut[b] : 0, x1 = b < grid ? p.cut[b + 1] : 0;
+        const uint32_t m = __ballot_sync(kFull, min(x1, end) > max(x0, begin));
+        if (m && g.part0 < 0) {
+          g.part0 = b0 + __ffs(m) - 1;
+          g.part0_slot = 2 * g.part0 + (__shfl_sync(kFull, x0, __ffs(m) - 1) == begin ? 0 : 1);
+        }
+        g.parts += __popc(m);
+      }
+    }
     w += g.nt;
   }
   const int32_t unit = static_cast<int32_t>(k / q.items), j = static_cast<int32_t>(k - static_cast<int64_t>(unit) * q.items);
@@ -385,9 +414,10 @@ __device__ __forceinline__ Seg next_seg(const ChunkArgs &a, const PlanPtrs &p, i
 
 // Columns of 32 that a row keeps: the first `lim`.
 __device__ __forceinline__ void keep_columns(uint32_t (&u)[32], int32_t lim) {
+  const uint32_t m = lim >= 32 ? ~0u : (lim <= 0 ? 0u : (1u << lim) - 1u);
 #pragma unroll
   for (int i = 0; i < 32; ++i)
-    if (i >= lim) u[i] = 0xff800000u;
+    if (!(m >> i & 1u)) u[i] = 0xff800000u;
 }
 
 // The maximum of 32 values.
@@ -396,6 +426,43 @@ __device__ __forceinline__ float max32(const uint32_t (&u)[32]) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) m[i & 3] = max3(m[i & 3], __uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
   return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+
+// Weights of 32 logits in bf16 (w) and what the rounding left of them (u);
+// returns their sum, even and odd columns.  The logit is rounded before the
+// reference is taken off, so that what is left of the largest is at most 2^8
+// whatever their size (not as packed pairs: those two operations came out as
+// one, without the rounding).
+__device__ __forceinline__ uint64_t weigh_rounded(uint32_t (&u)[32], uint32_t *w, float sl2, float mo) {
+  uint64_t t2[2] = {0, 0};
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    const float p0 = ex2(__fsub_rn(__fmul_rn(__uint_as_float(u[2 * e]), sl2), mo));
+    const float p1 = ex2(__fsub_rn(__fmul_rn(__uint_as_float(u[2 * e + 1]), sl2), mo));
+    t2[e & 1] = f2_add(t2[e & 1], f2_pack(p0, p1));
+    w[e] = bf16x2_rn(p0, p1);
+    u[e] = bf16x2_rest(p0, p1, w[e]);
+  }
+  return f2_add(t2[0], t2[1]);
+}
+
+// Four 16-byte words a lane (one row), transposed within four lanes: then word
+// i is of the i-th of the four rows, and the lanes' words follow one another.
+__device__ __forceinline__ void transpose4(uint4 (&e)[4]) {
+  const bool b0 = threadIdx.x & 1, b1 = threadIdx.x & 2;
+  auto swap = [](uint4 &keep0, uint4 &keep1, bool b, int o) {
+    uint4 t = b ? keep0 : keep1;
+    t.x = __shfl_xor_sync(kFull, t.x, o);
+    t.y = __shfl_xor_sync(kFull, t.y, o);
+    t.z = __shfl_xor_sync(kFull, t.z, o);
+    t.w = __shfl_xor_sync(kFull, t.w, o);
+    if (b) keep0 = t;
+    else keep1 = t;
+  };
+  swap(e[0], e[1], b0, 1);
+  swap(e[2], e[3], b0, 1);
+  swap(e[0], e[2], b1, 2);
+  swap(e[1], e[3], b1, 2);
 }
 
 // This thread's row of O times f.  (The products into O were complete when S was.)
@@ -426,6 +493,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sm.qfree, 2 + kSoftWarps);
     mbar_init(&sm.joined, kSoftWarps);
     mbar_init(&sm.qjoin, kSoftWarps);
+    mbar_init(&sm.parted, kSoftWarps);
+    mbar_init(&sm.partgo, 1);
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&sm.full[i], 1);
       mbar_init(&sm.empty[i], 2);
@@ -448,7 +517,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   fence_after();
   const uint32_t tmem = sm.tmem;
   after_launch_before();
-  let_next_launch_start();
   const bool valid = *reinterpret_cast<volatile int32_t *>(&p.hdr->ok) != 0;
   const int32_t tpi = 2 * tpt, G = a.G;
   auto wait = [&](uint64_t *bar, uint32_t parity) { return wait_or_abort(bar, parity, abort, a.status); };
@@ -651,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t sl2x2 = f2_pack(sl2, sl2);
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const uint32_t ts_s = tmem + lanes + 128 * wg, ts_o = tmem + lanes + 256 + 128 * wg;
-    int32_t base = 0, ns = 0, nseg = 0, joins = 0, qjoins = 0;
+    int32_t base = 0, ns = 0, nseg = 0, joins = 0, qjoins = 0, merges = 0;
     bool ok = true;
     for (int32_t s = 0; ok; ++s) {
       if (!(ok = warp_wait(&sm.qfull, s & 1u))) break;
@@ -685,15 +753,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (started && __any_sync(kFull, f != 1.0f)) scale_row(ts_o, f);
           l2 = f2_mul(l2, f2_pack(f, f));
           m = mn;
-          const float mo = m == -INFINITY ? 0.0f : m;
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float p0 = ex2(__fsub_rn(__fmul_rn(__uint_as_float(u[2 * e]), sl2), mo));
-            const float p1 = ex2(__fsub_rn(__fmul_rn(__uint_as_float(u[2 * e + 1]), sl2), mo));
-            l2 = f2_add(l2, f2_pack(p0, p1));
-            w[e] = bf16x2_rn(p0, p1);
-            u[e] = bf16x2_rest(p0, p1, w[e]);
-          }
+          l2 = f2_add(l2, weigh_rounded(u, w, sl2, m == -INFINITY ? 0.0f : m));
           uint32_t zero[16] = {};
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
@@ -738,21 +798,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             care = __any_sync(kFull, live && !(f2_sum(sum) <= kMost));
           }
-          if (care) {
-            // S by 32 columns, the next ones on their way while f has these
-            auto columns = [&](auto f) {
-              uint32_t u[2][32];
-              tmem_ld32(ts_s, u[0]);
+          if (!care) {
 #pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                tmem_wait32(u[c & 1]);
-                if (c < 3) tmem_ld32(ts_s + 32 * (c + 1), u[(c + 1) & 1]);
-                if (masked) keep_columns(u[c & 1], lim - 32 * c);
-                f(u[c & 1], c);
-              }
-            };
+            for (int c = 0; c < 4; ++c) tmem_st16(ts_s + 32 * c, w + 16 * c);
+          } else {
+            // in short loops: this code runs seldom, and what is not in the instruction cache costs more than it does
             float mx = -INFINITY;
-            columns([&](uint32_t(&u)[32], int) { mx = fmaxf(mx, max32(u)); });
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              uint32_t u[32];
+              tmem_ld32(ts_s + 32 * c, u);
+              tmem_wait32(u);
+              if (masked) keep_columns(u, lim - 32 * c);
+              mx = fmaxf(mx, max32(u));
+            }
             // the reference moves when it is passed by more than 2^8 (and where the row starts)
             const float top = ceilf(mx * sl2), mn = live && top > m + 8.0f ? top : m;
             const float f = mn == m ? 1.0f : ex2(m - mn);  // 2^-inf = 0 where the row starts
@@ -760,25 +819,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             l2 = f2_mul(l2, f2_pack(f, f));
             m = mn;
             const float mo = m == -INFINITY ? 0.0f : m;
-            uint64_t t2[2] = {0, 0};
-            columns([&](uint32_t(&u)[32], int c) {
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                // rounded before the reference is taken off: what is left of the largest logit is at most 2^8
-                // (not as packed pairs: those two operations came out as one, without the rounding)
-                const float p0 = ex2(__fsub_rn(__fmul_rn(__uint_as_float(u[2 * e]), sl2), mo));
-                const float p1 = ex2(__fsub_rn(__fmul_rn(__uint_as_float(u[2 * e + 1]), sl2), mo));
-                t2[e & 1] = f2_add(t2[e & 1], f2_pack(p0, p1));
-                w[16 * c + e] = bf16x2_rn(p0, p1);
-                u[e] = bf16x2_rest(p0, p1, w[16 * c + e]);
-              }
+            sum = 0;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              uint32_t u[32];
+              tmem_ld32(ts_s + 32 * c, u);
+              tmem_wait32(u);
+              if (masked) keep_columns(u, lim - 32 * c);
+              sum = f2_add(sum, weigh_rounded(u, w, sl2, mo));
+              tmem_st16(ts_s + 32 * c, w);
               if (!two) tmem_st16(ts_s + 32 * c + 16, u);  // what the rounding left of the weights
-            });
-            sum = f2_add(t2[0], t2[1]);
+            }
           }
           l2 = f2_add(l2, sum);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_st16(ts_s + 32 * c, w + 16 * c);
         }
         started = true;
         // rows of V behind the item's last position hold anything: zeros, as 0 times anything is not 0
@@ -799,6 +852,74 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       // ---- the segment's results
+      // Of a cut item: the block that finds all parts there joins them.  Every softmax warp comes here.
+      auto merge = [&] {
+        __threadfence();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.parted);
+        if (!warp_wait(&sm.parted, merges & 1u)) return false;
+        if (tid == 0) {
+          sm.last = atomicAdd(p.count + g.part0, 1) == g.parts - 1;
+          __threadfence();
+          mbar_arrive(&sm.partgo);
+        }
+        if (!warp_wait(&sm.partgo, merges & 1u)) return false;
+        ++merges;
+        if (!sm.last) return true;
+        __threadfence();
+        // a warp takes eight rows of 32 channels at a time, a thread eight channels of a row
+        const int32_t nr = g.n * G;
+        for (int32_t k = warp; k < 4 * ((nr + 7) / 8); k += kSoftWarps) {
+          const int32_t jr = 8 * (k >> 2) + (lane >> 2), unit = 8 * (k & 3) + 2 * (lane & 3);
+          if (jr >= nr) continue;
+          float mm = -INFINITY, l = 0.0f, x[8] = {};
+          int32_t left = g.parts, b = g.part0;
+          while (left > 0) {  // four parts at a time
+            float2 y[4];
+            float4 u[4], v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              y[e].x = -INFINITY;
+              if (left == 0) continue;
+              const int64_t slot = left == g.parts ? g.part0_slot : 2 * static_cast<int64_t>(b);
+              y[e] = __ldcg(p.ml + slot * rows + jr);
+              u[e] = __ldcg(p.o + (slot * 32 + unit) * rows + jr);
+              v[e] = __ldcg(p.o + (slot * 32 + unit + 1) * rows + jr);
+              --left;
+              do ++b;
+              while (left > 0 && p.cut[b + 1] == p.cut[b]);  // blocks without a share have no part
+            }
+            const float mn = fmaxf(fmaxf(fmaxf(y[0].x, y[1].x), fmaxf(y[2].x, y[3].x)), mm);
+            if (mn == -INFINITY) continue;
+            const float f = mm == mn ? 1.0f : ex2(mm - mn);
+            mm = mn;
+            l *= f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] *= f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if (y[e].x == -INFINITY) continue;  // every tile of that part lies behind the row, or there is none
+              const float f1 = y[e].x == mn ? 1.0f : ex2(y[e].x - mn);
+              l += y[e].y * f1;
+              x[0] += u[e].x * f1;
+              x[1] += u[e].y * f1;
+              x[2] += u[e].z * f1;
+              x[3] += u[e].w * f1;
+              x[4] += v[e].x * f1;
+              x[5] += v[e].y * f1;
+              x[6] += v[e].z * f1;
+              x[7] += v[e].w * f1;
+            }
+          }
+          const float inv = 1.0f / l;
+          const int64_t at = (static_cast<int64_t>(g.li) * a.T + g.tok + jr / G) * a.Hq + g.h * G + jr % G;
+          *reinterpret_cast<uint4 *>(a.out + at * 128 + 4 * unit) =
+              make_uint4(bf16x2_rn(x[0] * inv, x[1] * inv), bf16x2_rn(x[2] * inv, x[3] * inv),
+                         bf16x2_rn(x[4] * inv, x[5] * inv), bf16x2_rn(x[6] * inv, x[7] * inv));
+          if (a.lse && unit == 0) a.lse[at] = (mm + log2f(l)) * 0.693147180559945309f;
+        }
+        return true;
+      };
       if (four) {
         // a warp's rows go to shared memory, [warp][column][16 rows]; then a thread joins eight columns of a row
         float *ox = reinterpret_cast<float *>(sm.q[0]) + warp * (128 * 16);
@@ -849,22 +970,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                            bf16x2_rn(x[4] * inv, x[5] * inv), bf16x2_rn(x[6] * inv, x[7] * inv));
             if (a.lse && col == 0) a.lse[at] = (mm + log2f(l)) * 0.693147180559945309f;
           } else {
-            const int64_t part = static_cast<int64_t>(g.slot) * rows + jr;
-            *reinterpret_cast<float4 *>(p.o + part * 128 + col) = make_float4(x[0], x[1], x[2], x[3]);
-            *reinterpret_cast<float4 *>(p.o + part * 128 + col + 4) = make_float4(x[4], x[5], x[6], x[7]);
-            if (col == 0) p.ml[part] = make_float2(mm, l);
+            const int64_t part = static_cast<int64_t>(g.slot) * 32 + (col >> 2);
+            p.o[part * rows + jr] = make_float4(x[0], x[1], x[2], x[3]);
+            p.o[(part + 1) * rows + jr] = make_float4(x[4], x[5], x[6], x[7]);
+            if (col == 0) p.ml[static_cast<int64_t>(g.slot) * rows + jr] = make_float2(mm, l);
           }
         }
         fence_async();  // the next Q is copied where these reads were
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.joined);
         base += g.nt;
+        if (g.slot >= 0 && !(ok = merge())) break;
         continue;
       }
       const bool join = !two && g.nt > 1;
       float l = f2_sum(l2);
       const int64_t at = (static_cast<int64_t>(g.li) * a.T + g.tok + i) * a.Hq + g.h * G + (row - rt * G);
-      const int64_t part = g.slot < 0 ? 0 : static_cast<int64_t>(g.slot) * rows + (two && wg ? tpt * G : 0) + row;
+      const int32_t prow = (two && wg ? tpt * G : 0) + row;  // of a partial result
+      // where the four rows of this lane's group go (-1: not a row)
+      int64_t to[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) to[e] = __shfl_sync(kFull, live ? at : -1, (lane & ~3) + e);
       if (started) {
         if (!(ok = warp_wait(&sm.odone[wg], nseg & 1u))) break;
         ++nseg;
@@ -901,22 +1027,25 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int e = 0; e < 32; ++e) x[e] += ox[(32 * c + e) * 128 + row] * f1;
             }
-            if (!live) continue;
             if (g.slot < 0) {
+              uint4 y[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                *reinterpret_cast<uint4 *>(a.out + at * 128 + 32 * c + 8 * e) =
-                    make_uint4(bf16x2_rn(x[8 * e], x[8 * e + 1]), bf16x2_rn(x[8 * e + 2], x[8 * e + 3]),
-                               bf16x2_rn(x[8 * e + 4], x[8 * e + 5]), bf16x2_rn(x[8 * e + 6], x[8 * e + 7]));
-            } else {
+                y[e] = make_uint4(bf16x2_rn(x[8 * e], x[8 * e + 1]), bf16x2_rn(x[8 * e + 2], x[8 * e + 3]),
+                                  bf16x2_rn(x[8 * e + 4], x[8 * e + 5]), bf16x2_rn(x[8 * e + 6], x[8 * e + 7]));
+              transpose4(y);  // four lanes write 64 bytes of a row
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (to[e] >= 0) *reinterpret_cast<uint4 *>(a.out + to[e] * 128 + 32 * c + 8 * (lane & 3)) = y[e];
+            } else if (live) {
 #pragma unroll
               for (int e = 0; e < 8; ++e)
-                *reinterpret_cast<float4 *>(p.o + part * 128 + 32 * c + 4 * e) =
+                p.o[(static_cast<int64_t>(g.slot) * 32 + 8 * c + e) * rows + prow] =
                     make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
             }
           }
           if (join && wg == 1) sm.ml[row] = make_float2(m, l);
-          else if (live && g.slot >= 0) p.ml[part] = make_float2(m, l);
+          else if (live && g.slot >= 0) p.ml[static_cast<int64_t>(g.slot) * rows + prow] = make_float2(m, l);
           else if (live && a.lse) a.lse[at] = (m + log2f(l)) * 0.693147180559945309f;
         }
         fence_before();
@@ -930,6 +1059,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (join) ++joins;
       }
       base += g.nt;
+      if (g.slot >= 0 && !(ok = merge())) break;
     }
   }
 
@@ -942,48 +1072,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// ------------------------------------------------------------------- merge --
-
-constexpr int kMergeRows = 8;  // a warp each
-
-// Block (c, rows): the item that the end of block c's share cuts, if c is the
-// first that has part of it.
-__global__ void __launch_bounds__(32 * kMergeRows)
-    k_chunk_merge(const __grid_constant__ ChunkArgs a, const PlanPtrs p, int32_t tpi, int32_t rows, int32_t grid) {
-  after_launch_before();
-  if (!p.hdr->ok) return;
-  const int32_t c = blockIdx.x, lane = threadIdx.x & 31, row = blockIdx.y * kMergeRows + (threadIdx.x >> 5);
-  const int64_t w0 = p.cut[c], w1 = p.cut[c + 1];
-  if (w1 == w0 || w1 >= p.hdr->tiles) return;
-  // the item of tile w1 - 1
-  const int32_t r = find_req(a.R, [&](int32_t x) { return p.req[x].tile0; }, w1 - 1);
-  const ReqPlan q = p.req[r];
-  const int64_t unit = (w1 - 1 - q.tile0) / q.tiles, in = w1 - 1 - q.tile0 - unit * q.tiles;
-  const int32_t j = find_req(q.items, [&](int32_t x) { return static_cast<int64_t>(p.pre[q.rt0 + x]); }, in);
-  const int64_t begin = q.tile0 + unit * q.tiles + p.pre[q.rt0 + j], end = begin + item_tiles(p, q, j);
-  if (end == w1 || begin < w0) return;  // not cut here, or an earlier block's
-  if (row >= min(tpi, q.n - j * tpi) * a.G) return;
-  // the parts: this block's, then those of the blocks after it that have tiles
-  float m = -INFINITY, l = 0.0f;
-  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  for (int32_t b = c; b < grid && p.cut[b] < end; ++b) {
-    if (p.cut[b + 1] == p.cut[b]) continue;
-    const int64_t at = static_cast<int64_t>(2 * b + (b == c && begin != w0 ? 1 : 0)) * rows + row;
-    const float2 x = p.ml[at];
-    if (x.x == -INFINITY) continue;  // a part whose every tile lies behind the row
-    const float4 y = *reinterpret_cast<const float4 *>(p.o + at * 128 + 4 * lane);
-    const float mm = fmaxf(m, x.x), f = m == mm ? 1.0f : ex2(m - mm), e = x.x == mm ? 1.0f : ex2(x.x - mm);
-    l = l * f + x.y * e;
-    o = make_float4(o.x * f + y.x * e, o.y * f + y.y * e, o.z * f + y.z * e, o.w * f + y.w * e);
-    m = mm;
-  }
-  const float inv = 1.0f / l;
-  const int32_t li = static_cast<int32_t>(unit / a.Hkv), h = static_cast<int32_t>(unit - static_cast<int64_t>(li) * a.Hkv);
-  const int64_t at = (static_cast<int64_t>(li) * a.T + q.tok0 + j * tpi + row / a.G) * a.Hq + h * a.G + row % a.G;
-  *reinterpret_cast<uint2 *>(a.out + at * 128 + 4 * lane) = make_uint2(bf16x2_rn(o.x * inv, o.y * inv), bf16x2_rn(o.z * inv, o.w * inv));
-  if (a.lse && lane == 0) a.lse[at] = (m + log2f(l)) * 0.693147180559945309f;
-}
-
 }  // namespace
 
 size_t chunk_workspace(const ChunkArgs &a) { return chunk_layout(a).bytes; }
@@ -993,7 +1081,8 @@ cudaError_t launch_chunk(const ChunkArgs &a, void *ws, cudaStream_t s) {
   uint8_t *b = static_cast<uint8_t *>(ws);
   const PlanPtrs p{reinterpret_cast<PlanHeader *>(b), reinterpret_cast<ReqPlan *>(b + w.req),
                    reinterpret_cast<int32_t *>(b + w.pre), reinterpret_cast<int64_t *>(b + w.cut),
-                   reinterpret_cast<float *>(b + w.o), reinterpret_cast<float2 *>(b + w.ml)};
+                   reinterpret_cast<int32_t *>(b + w.count), reinterpret_cast<float4 *>(b + w.o),
+                   reinterpret_cast<float2 *>(b + w.ml)};
   int dev = 0, sms = 0;
   cudaError_t e;
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
@@ -1012,8 +1101,7 @@ cudaError_t launch_chunk(const ChunkArgs &a, void *ws, cudaStream_t s) {
   const int64_t copies = a.k_new ? a.n_layers * ((a.T + kAppendTokens - 1) / kAppendTokens) : 0;
   k_chunk_append<<<static_cast<unsigned>(1 + copies), kAppendThreads, 0, s>>>(a, p, w.tpi, grid);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  if ((e = launch_after(k_chunk, dim3(grid), kThreads, kSmemBytes, s, a, p, qmap, kmap, vmap, qmap4, w.tpt, tpq, w.rows)) != cudaSuccess) return e;
-  return launch_after(k_chunk_merge, dim3(grid, (w.rows + kMergeRows - 1) / kMergeRows), 32 * kMergeRows, 0, s, a, p, w.tpi, w.rows, grid);
+  return launch_after(k_chunk, dim3(grid), kThreads, kSmemBytes, s, a, p, qmap, kmap, vmap, qmap4, w.tpt, tpq, w.rows);
 }
 
 }  // namespace dkv

@@ -38,6 +38,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstddef>
+#include <type_traits>
 
 #include "chunk.cuh"
 
@@ -446,6 +447,31 @@ __device__ __forceinline__ uint64_t weigh_rounded(uint32_t (&u)[32], uint32_t *w
   return f2_add(t2[0], t2[1]);
 }
 
+// ... of the usual tile: one multiply-add a logit, bf16 weights alone.
+__device__ __forceinline__ uint64_t weigh(const uint32_t (&u)[32], uint32_t *w, uint64_t sl2x2, uint64_t nm2) {
+  uint64_t t2[2] = {0, 0};
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    float y0, y1;
+    f2_unpack(f2_fma(f2_pack(__uint_as_float(u[2 * e]), __uint_as_float(u[2 * e + 1])), sl2x2, nm2), y0, y1);
+    const float p0 = ex2(y0), p1 = ex2(y1);
+    t2[e & 1] = f2_add(t2[e & 1], f2_pack(p0, p1));
+    w[e] = bf16x2_rn(p0, p1);
+  }
+  return f2_add(t2[0], t2[1]);
+}
+
+// 32 bf16 weights times a power of two.
+__device__ __forceinline__ void scale_weights(uint32_t at, float f) {
+  uint32_t x[16];
+  tmem_ld16(at, x);
+  tmem_wait16(x);
+#pragma unroll
+  for (int e = 0; e < 16; ++e) x[e] = bf16x2_rn(bf16_lo(x[e]) * f, bf16_hi(x[e]) * f);
+  tmem_st16(at, x);
+  tmem_wait_st();
+}
+
 // Four 16-byte words a lane (one row), transposed within four lanes: then word
 // i is of the i-th of the four rows, and the lanes' words follow one another.
 __device__ __forceinline__ void transpose4(uint4 (&e)[4]) {
@@ -723,27 +749,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int32_t s = 0; ok; ++s) {
       if (!(ok = warp_wait(&sm.qfull, s & 1u))) break;
-      const Seg g = sm.seg[s % kSegs];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.qfree);
-      if (g.nt == 0) break;
+      // read where it is needed: every register counts in the loop over the tiles
+      const Seg &g = sm.seg[s % kSegs];
+      const int32_t nt = g.nt;
       const bool two = g.n > tpt;
       const bool four = g.n <= tpq;                   // the rows lie four times in the row tile
       const int32_t rt = (four ? lane : row) / G;     // token of the row tile
       const int32_t i = (two && wg ? tpt : 0) + rt;   // token of the item
       const bool live = rt < (four ? tpq : tpt) && i < g.n;
+      // of the segment's first key tile: columns this row keeps, positions the item has
+      const int32_t lim0 = g.ctx + g.i0 + i + 1 - 128 * g.t0, end0 = g.ctx + g.i0 + g.n - 128 * g.t0;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.qfree);
+      if (nt == 0) break;
       const bool some = __any_sync(kFull, live);
-      const int32_t end = g.ctx + g.i0 + g.n;
       float m = live ? -INFINITY : 0.0f;
       uint64_t l2 = 0;  // running sum, even and odd columns
       bool started = false;
-      for (int32_t t = two ? 0 : wg; t < g.nt && ok; t += two ? 1 : 2, ++ns) {
+      for (int32_t t = two ? 0 : wg; t < nt && ok; t += two ? 1 : 2, ++ns) {
         if (!(ok = warp_wait(&sm.sfull[wg], ns & 1u))) break;
         fence_after();
-        const int32_t k0 = 128 * (g.t0 + t);
         if (four) {
           const int q = warp & 3;  // this warp's columns: 32 q .. + 31
-          const int32_t lim = live ? g.ctx + g.i0 + i + 1 - k0 - 32 * q : 32;
+          const int32_t lim = live ? lim0 - 128 * t - 32 * q : 32;
           uint32_t u[32], w[16];
           tmem_ld32(ts_s + 32 * q, u);
           tmem_wait32(u);
@@ -766,67 +794,76 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         } else if (some) {
-          const int32_t lim = live ? g.ctx + g.i0 + i + 1 - k0 : 128;
+          const int32_t lim = live ? lim0 - 128 * t : 128;
           const bool masked = __any_sync(kFull, lim < 128);
-          uint32_t w[64];  // P, two columns each
-          uint64_t sum = 0;
-          auto weigh = [&](const uint32_t (&u)[32], int c, uint64_t nm2) {
-            uint64_t t2[2] = {0, 0};
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              float y0, y1;
-              f2_unpack(f2_fma(f2_pack(__uint_as_float(u[2 * e]), __uint_as_float(u[2 * e + 1])), sl2x2, nm2), y0, y1);
-              const float p0 = ex2(y0), p1 = ex2(y1);
-              t2[e & 1] = f2_add(t2[e & 1], f2_pack(p0, p1));
-              w[16 * c + e] = bf16x2_rn(p0, p1);
-            }
-            sum = f2_add(sum, f2_add(t2[0], t2[1]));
-          };
-          bool care = __any_sync(kFull, live && !(fabsf(m) < kFar));
-          // the usual tile; one with masked columns goes the careful way, and every tile of a single row tile
-          care |= masked || !two;
-          if (!care) {
-            const uint64_t nm2 = f2_pack(-m, -m);
-            uint32_t u[2][32];
-            tmem_ld32(ts_s, u[0]);
-            tmem_wait32(u[0]);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              if (c < 3) tmem_ld32(ts_s + 32 * (c + 1), u[(c + 1) & 1]);
-              weigh(u[c & 1], c, nm2);
-              if (c < 3) tmem_wait32(u[(c + 1) & 1]);
-            }
-            care = __any_sync(kFull, live && !(f2_sum(sum) <= kMost));
+          if (__any_sync(kFull, live && m == -INFINITY)) {  // rows start: their first columns set the reference
+            uint32_t u[32];
+            tmem_ld32(ts_s, u);
+            tmem_wait32(u);
+            if (masked) keep_columns(u, lim);
+            const float top = ceilf(max32(u) * sl2);
+            if (m == -INFINITY) m = top;
           }
-          if (!care) {
+          uint64_t sum = 0;
+          bool slow = true;
+          const bool near = two && !__any_sync(kFull, live && !(fabsf(m) < kFar));
+          // P of 32 columns takes the first 16 of their columns of S
+          if (near && !masked) {
+            const uint64_t nm2 = f2_pack(-m, -m);
+            // without a branch, and P in registers until the tile's sum is known: a test for every 32 columns made
+            // the tile 1560 cycles of 1000, masks where they are needed 1370
+            uint32_t u0[32], u1[32], w[64];
+            // columns 32 c .. + 31 in u, the next ones on their way to v
+            auto chunk = [&](auto which, uint32_t(&u)[32], uint32_t(&v)[32]) {
+              constexpr int c = decltype(which)::value;
+              if constexpr (c < 3) tmem_ld32(ts_s + 32 * (c + 1), v);
+              sum = f2_add(sum, weigh(u, w + 16 * c, sl2x2, nm2));
+              if constexpr (c < 3) tmem_wait32(v);
+            };
+            tmem_ld32(ts_s, u0);
+            tmem_wait32(u0);
+            chunk(std::integral_constant<int, 0>{}, u0, u1);
+            chunk(std::integral_constant<int, 1>{}, u1, u0);
+            chunk(std::integral_constant<int, 2>{}, u0, u1);
+            chunk(std::integral_constant<int, 3>{}, u1, u0);
+            if (__builtin_expect(!__any_sync(kFull, live && !(f2_sum(sum) <= kMost)), 1)) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_st16(ts_s + 32 * c, w + 16 * c);
-          } else {
-            // in short loops: this code runs seldom, and what is not in the instruction cache costs more than it does
-            float mx = -INFINITY;
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              uint32_t u[32];
-              tmem_ld32(ts_s + 32 * c, u);
-              tmem_wait32(u);
-              if (masked) keep_columns(u, lim - 32 * c);
-              mx = fmaxf(mx, max32(u));
+              for (int c = 0; c < 4; ++c) tmem_st16(ts_s + 32 * c, w + 16 * c);
+              slow = false;
+            } else {
+              sum = 0;
             }
-            // the reference moves when it is passed by more than 2^8 (and where the row starts)
-            const float top = ceilf(mx * sl2), mn = live && top > m + 8.0f ? top : m;
-            const float f = mn == m ? 1.0f : ex2(m - mn);  // 2^-inf = 0 where the row starts
-            if (started && __any_sync(kFull, f != 1.0f)) scale_row(ts_o, f);
-            l2 = f2_mul(l2, f2_pack(f, f));
-            m = mn;
-            const float mo = m == -INFINITY ? 0.0f : m;
-            sum = 0;
+          }
+          if (__builtin_expect(slow, 0)) {
+            // in a short loop: this code runs seldom with two row tiles, and what is not in the instruction cache
+            // costs more than it does
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
-              uint32_t u[32];
-              tmem_ld32(ts_s + 32 * c, u);
-              tmem_wait32(u);
-              if (masked) keep_columns(u, lim - 32 * c);
-              sum = f2_add(sum, weigh_rounded(u, w, sl2, mo));
+              uint32_t u[32], w[16];
+              auto load = [&] {
+                tmem_ld32(ts_s + 32 * c, u);
+                tmem_wait32(u);
+                if (masked) keep_columns(u, lim - 32 * c);
+              };
+              load();
+              const float mo = m == -INFINITY ? 0.0f : m;
+              uint64_t x = near ? weigh(u, w, sl2x2, f2_pack(-mo, -mo)) : weigh_rounded(u, w, sl2, mo);
+              if (__any_sync(kFull, live && !(f2_sum(x) <= kMost))) {
+                // the reference moves: outputs in progress, sums and the tile's earlier weights follow
+                load();
+                const float top = ceilf(max32(u) * sl2), mn = live && top > m ? top : m;
+                const float f = mn == m ? 1.0f : ex2(m - mn);
+                for (int k = 0; k < c; ++k) {
+                  scale_weights(ts_s + 32 * k, f);
+                  if (!two) scale_weights(ts_s + 32 * k + 16, f);
+                }
+                if (started) scale_row(ts_o, f);
+                l2 = f2_mul(l2, f2_pack(f, f));
+                sum = f2_mul(sum, f2_pack(f, f));
+                m = mn;
+                x = weigh_rounded(u, w, sl2, m == -INFINITY ? 0.0f : m);
+              }
+              sum = f2_add(sum, x);
               tmem_st16(ts_s + 32 * c, w);
               if (!two) tmem_st16(ts_s + 32 * c + 16, u);  // what the rounding left of the weights
             }
@@ -835,10 +872,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         started = true;
         // rows of V behind the item's last position hold anything: zeros, as 0 times anything is not 0
-        if (end - k0 < 128) {
+        const int32_t end = end0 - 128 * t;
+        if (end < 128) {
           const int32_t vi = 2 * (base + t) + 1, slot = vi % kRing;
           if (!(ok = warp_wait(&sm.full[slot], (vi / kRing) & 1u))) break;
-          if (row >= end - k0) {
+          if (row >= end) {
 #pragma unroll
             for (int e = 0; e < 16; ++e)
               *reinterpret_cast<uint4 *>(sm.ring[slot] + (e >> 3) * kBox + row * 128 + (e & 7) * 16) = make_uint4(0, 0, 0, 0);
@@ -979,11 +1017,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_async();  // the next Q is copied where these reads were
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.joined);
-        base += g.nt;
+        base += nt;
         if (g.slot >= 0 && !(ok = merge())) break;
         continue;
       }
-      const bool join = !two && g.nt > 1;
+      const bool join = !two && nt > 1;
       float l = f2_sum(l2);
       const int64_t at = (static_cast<int64_t>(g.li) * a.T + g.tok + i) * a.Hq + g.h * G + (row - rt * G);
       const int32_t prow = (two && wg ? tpt * G : 0) + row;  // of a partial result
@@ -1010,7 +1048,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         f0 *= inv;
         f1 *= inv;
         if (some) {
-#pragma unroll 1
+#pragma unroll 2
           for (int c = 0; c < 4; ++c) {
             uint32_t u[32];
             tmem_ld32(ts_o + 32 * c, u);
@@ -1058,7 +1096,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (join) ++joins;
       }
-      base += g.nt;
+      base += nt;
       if (g.slot >= 0 && !(ok = merge())) break;
     }
   }

@@ -49,28 +49,30 @@ namespace {
 using namespace tc;
 
 constexpr int kBlocks = 152;        // most blocks of the attention: one a multiprocessor
+constexpr int kStart = 3;           // what an item costs beside its key tiles, in key tiles: Q, the first S, the outputs
 constexpr int kMaxWaves = 64;       // of whole items; the plan looks at each
 constexpr int kSmemReqs = 256;      // requests, and items a unit of them, that the plan keeps in shared memory
 constexpr int kSmemItems = 1024;
 
+// Costs are in key tiles; an item's are its key tiles' and kStart before them.
 struct PlanHeader {
-  int64_t tiles;   // key tiles of all items
-  int64_t cut0;    // tiles of the whole items that the waves take
+  int64_t tiles;   // cost of all items
+  int64_t cut0;    // cost of the whole items that the waves take
   int32_t waves;
   int32_t ok;      // lengths valid
   int32_t pad[10];
 };
 struct ReqPlan {
-  int64_t tile0;       // key tiles of the requests before
+  int64_t tile0;       // cost of the requests before
   int32_t tok0, rt0;   // tokens, items a unit of the requests before
   int32_t items;       // items a unit
-  int32_t tiles;       // key tiles a unit
+  int32_t tiles;       // cost a unit
   int32_t ctx, n;
 };
 struct PlanPtrs {
   PlanHeader *hdr;
   ReqPlan *req;    // [R]
-  int32_t *pre;    // [items a unit of all requests]: key tiles of the request's items before
+  int32_t *pre;    // [items a unit of all requests]: cost of the request's items before
   int64_t *cut;    // [grid + 1]: where each block's share of the cut tiles starts
   int32_t *count;  // [grid]: parts that are there, of the item whose first part is the block's last
   float4 *o;       // [2 grid][32][rows] partial results, four channels each
@@ -151,7 +153,7 @@ __device__ __forceinline__ int32_t find_req(int32_t R, F first, int64_t i) {
   return lo;
 }
 
-__device__ __forceinline__ int32_t item_tiles(const PlanPtrs &p, const ReqPlan &q, int32_t j) {
+__device__ __forceinline__ int32_t item_cost(const PlanPtrs &p, const ReqPlan &q, int32_t j) {
   return (j + 1 < q.items ? p.pre[q.rt0 + j + 1] : q.tiles) - p.pre[q.rt0 + j];
 }
 
@@ -188,13 +190,13 @@ __device__ void plan(const ChunkArgs &a, const PlanPtrs &p, int32_t tpi, int32_t
   }
   int32_t *pre = rts <= kSmemItems ? pre_sm : p.pre;
   __syncthreads();
-  // key tiles of each item: a warp a request
+  // cost of each item: a warp a request
   for (int32_t r = warp; r < a.R; r += kAppendThreads / 32) {
     const ReqPlan q = req[r];
     int32_t sum = 0;
     for (int32_t j0 = 0; j0 < q.items; j0 += 32) {
       const int32_t j = j0 + lane;
-      const int32_t t = j < q.items ? static_cast<int32_t>((q.ctx + min(static_cast<int64_t>(q.n), (j + 1) * static_cast<int64_t>(tpi)) + 127) / 128) : 0;
+      const int32_t t = j < q.items ? static_cast<int32_t>((q.ctx + min(static_cast<int64_t>(q.n), (j + 1) * static_cast<int64_t>(tpi)) + 127) / 128) + kStart : 0;
       int32_t incl = t;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -355,8 +357,11 @@ struct __align__(1024) Smem {
 constexpr size_t kSmemBytes = sizeof(Smem) + 1024;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 
+// Key tiles that lie in the first x of an item's cost.
+__device__ __forceinline__ int32_t tiles_in(int64_t x) { return static_cast<int32_t>(max(x - kStart, int64_t{0})); }
+
 // Block c's segment number s: whole items c, c + grid, ..., then its share of
-// the cut tiles, from w on (w: where the next of those starts).
+// the cut rest, from w on (w: where the next of those starts).
 __device__ __forceinline__ Seg next_seg(const ChunkArgs &a, const PlanPtrs &p, int32_t waves, int64_t cut0, int32_t tpi,
                                         int32_t grid, int32_t s, int64_t &w) {
   const int64_t U1 = static_cast<int64_t>(a.n_layers) * a.Hkv;
@@ -371,7 +376,7 @@ __device__ __forceinline__ Seg next_seg(const ChunkArgs &a, const PlanPtrs &p, i
     q = p.req[r];
     k = i - q.rt0 * U1;
     g.t0 = 0;
-    g.nt = item_tiles(p, q, static_cast<int32_t>(k % q.items));
+    g.nt = item_cost(p, q, static_cast<int32_t>(k % q.items)) - kStart;
     g.slot = -1;
   } else {
     const int64_t w0 = p.cut[c], w1 = p.cut[c + 1];
@@ -381,26 +386,28 @@ __device__ __forceinline__ Seg next_seg(const ChunkArgs &a, const PlanPtrs &p, i
     const int64_t unit = (w - q.tile0) / q.tiles, in = (w - q.tile0) - unit * q.tiles;
     const int32_t j = find_req(q.items, [&](int32_t x) { return static_cast<int64_t>(p.pre[q.rt0 + x]); }, in);
     k = unit * q.items + j;
-    const int32_t all = item_tiles(p, q, j);
-    g.t0 = static_cast<int32_t>(in - p.pre[q.rt0 + j]);
-    g.nt = static_cast<int32_t>(min(static_cast<int64_t>(all - g.t0), w1 - w));
-    g.slot = g.nt == all ? -1 : 2 * c + (w == w0 ? 0 : 1);
+    const int32_t all = item_cost(p, q, j);
+    const int64_t begin = w - (in - p.pre[q.rt0 + j]), end = begin + all, w2 = min(w1, end);
+    g.t0 = tiles_in(w - begin);
+    g.nt = tiles_in(w2 - begin) - g.t0;
+    if (g.nt == 0) return g;  // the block's share ends before the item's first tile
+    g.slot = g.nt == all - kStart ? -1 : 2 * c + (w == w0 ? 0 : 1);
     if (g.slot >= 0) {  // the blocks that have a part of the item
-      const int64_t begin = w - g.t0, end = begin + all;
       const int lane = threadIdx.x & 31;
       g.part0 = -1;
       for (int32_t b0 = 0; b0 < grid; b0 += 32) {
         const int32_t b = b0 + lane;
         const int64_t x0 = b < grid ? p.cut[b] : 0, x1 = b < grid ? p.cut[b + 1] : 0;
-        const uint32_t m = __ballot_sync(kFull, min(x1, end) > max(x0, begin));
+        const bool has = x1 > x0 && x1 > begin && x0 < end && tiles_in(min(x1, end) - begin) > tiles_in(max(x0, begin) - begin);
+        const uint32_t m = __ballot_sync(kFull, has);
         if (m && g.part0 < 0) {
           g.part0 = b0 + __ffs(m) - 1;
-          g.part0_slot = 2 * g.part0 + (__shfl_sync(kFull, x0, __ffs(m) - 1) == begin ? 0 : 1);
+          g.part0_slot = 2 * g.part0 + (__shfl_sync(kFull, x0, __ffs(m) - 1) >= begin ? 0 : 1);
         }
         g.parts += __popc(m);
       }
     }
-    w += g.nt;
+    w = w2;
   }
   const int32_t unit = static_cast<int32_t>(k / q.items), j = static_cast<int32_t>(k - static_cast<int64_t>(unit) * q.items);
   g.li = unit / a.Hkv;

@@ -246,49 +246,45 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0 && !ok)
       for (int32_t i = max(0, c - kRing); i < c; ++i) mbar_wait(&sm.full[i % kRing], (i / kRing) & 1u, nullptr);
   } else if (warp == kMmaWarp) {
-    // ================= products: the warp waits, one lane issues
-    constexpr uint32_t kStep = kTileBytes >> 4;
-    const uint64_t dq = sw128_desc(saddr(sm.ring[0]), 16, 1024);
-    int32_t c = 0, gb = 0, nkr[2] = {0, 0};
-    bool ok = true;
-    for (int32_t s = 0; ok; ++s) {
-      if (!(ok = warp_wait(&sm.segfull, s & 1u))) break;
-      const Seg g = sm.seg[s % kSegs];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.segfree);
-      if (g.nk == 0) break;
-      for (int32_t k = 0; k < g.nk && ok; ++k, ++c) {  // K is in tensor memory: its slot is free
-        if (!(ok = warp_wait(&sm.kready[k], nkr[k] & 1u))) break;
-        ++nkr[k];
-        if (lane == 0) mbar_arrive(&sm.empty[c % kRing]);
-      }
-      const int32_t blocks = (g.b1 - g.b0) * (g.tb1 - g.tb0);
-      for (int32_t q = 0; q < blocks && ok; ++q, ++c) {
-        const int32_t slot = c % kRing;
-        if (!(ok = warp_wait(&sm.full[slot], (c / kRing) & 1u))) break;
-        for (int32_t k = 0; k < g.nk; ++k, ++gb) {
-          const int buf = gb % kBufs;
-          if (gb >= kBufs && !(ok = warp_wait(&sm.sfree[buf], (gb / kBufs - 1) & 1u))) break;
-          fence_after();
-          if (elect_one()) {
+    // ================= products: one lane waits and issues
+    if (elect_one()) {
+      constexpr uint32_t kStep = kTileBytes >> 4;
+      const uint64_t dq = sw128_desc(saddr(sm.ring[0]), 16, 1024);
+      int32_t c = 0, gb = 0, nkr[2] = {0, 0};
+      bool ok = true;
+      for (int32_t s = 0; ok; ++s) {
+        if (!(ok = wait(&sm.segfull, s & 1u))) break;
+        const int32_t nk = sm.seg[s % kSegs].nk;
+        const int32_t blocks = (sm.seg[s % kSegs].b1 - sm.seg[s % kSegs].b0) * (sm.seg[s % kSegs].tb1 - sm.seg[s % kSegs].tb0);
+        mbar_arrive(&sm.segfree);
+        if (nk == 0) break;
+        for (int32_t k = 0; k < nk && ok; ++k, ++c) {  // K is in tensor memory: its slot is free
+          if (!(ok = wait(&sm.kready[k], nkr[k] & 1u))) break;
+          ++nkr[k];
+          mbar_arrive(&sm.empty[c % kRing]);
+        }
+        for (int32_t q = 0; q < blocks && ok; ++q, ++c) {
+          const int32_t slot = c % kRing;
+          if (!(ok = wait(&sm.full[slot], (c / kRing) & 1u))) break;
+          for (int32_t k = 0; k < nk; ++k, ++gb) {
+            const int buf = gb % kBufs;
+            if (gb >= kBufs && !(ok = wait(&sm.sfree[buf], (gb / kBufs - 1) & 1u))) break;
+            fence_after();
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
               mma_ts(tmem + 128 * (1 + buf), tmem + 64 * k + 8 * kk,
                      dq + slot * kStep + (((kk >> 2) * kBox + (kk & 3) * 32) >> 4), idesc(true, 128, 128, false),
                      kk > 0 ? 1u : 0u);
             mma_commit(&sm.sfull[buf]);
-            if (k == g.nk - 1) mma_commit(&sm.empty[slot]);
+            if (k == nk - 1) mma_commit(&sm.empty[slot]);
           }
-          __syncwarp();
         }
+        if (ok) mma_commit(&sm.kdone);
       }
-      if (ok && elect_one()) mma_commit(&sm.kdone);
-      __syncwarp();
+      // every product done (also after an abort)
+      mma_commit(&sm.done);
+      mbar_wait(&sm.done, 0, nullptr);
     }
-    // every product of this warp done (also after an abort)
-    if (elect_one()) mma_commit(&sm.done);
-    __syncwarp();
-    mbar_wait(&sm.done, 0, nullptr);
   } else {
     // ================= sum warps: a thread per position
     const int wg = warp >> 2, row = tid & 127;
@@ -375,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               uint32_t u[2][32];
               tmem_ld32(src, u[0]);
               tmem_wait32(u[0]);
-              uint64_t t2 = 0;
+              [[maybe_unused]] uint64_t t2 = 0;
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 if (i < 3) tmem_ld32(src + 32 * (i + 1), u[(i + 1) & 1]);

@@ -33,7 +33,7 @@ namespace {
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kBins = 2048;   // of a counting pass
 constexpr int kPlanThreads = 512, kScanThreads = 1024, kApplyThreads = 256;
-constexpr int kMoves = 256;   // moves a block lists at a time
+constexpr int kMoves = 512;   // moves a block lists at a time
 constexpr int kIds = 1024;    // page ids of a list that a block keeps in shared memory
 
 // A later launch's blocks may start while the one before still runs and wait
@@ -110,12 +110,12 @@ __global__ void __launch_bounds__(kPlanThreads, 2) k_evict_plan(const __grid_con
   for (int32_t i = tid; i < 2 * words; i += kPlanThreads) dyn[i] = 0;
   if (tid == 0) bad_s = 0;
   for (int i = tid; i < kBins; i += kPlanThreads) hist[i] = 0;
-  // pages and their reverse entries
-  bool wrong = false;
-  for (int32_t j = tid; j < hd.z + hd.w; j += kPlanThreads) {
-    const int32_t id = a.fwd[static_cast<int64_t>(u) * a.pmax + j];
-    if (id < 0 || id >= a.F || a.rev_unit[id] != a.unit_base + u || a.rev_idx[id] != j) wrong = true;
-  }
+  // pages and their reverse entries: a thread's first one on its way through all that follows
+  const int32_t pages = hd.z + hd.w;
+  auto page_of = [&](int32_t j) { return a.fwd[static_cast<int64_t>(u) * a.pmax + j]; };
+  const int32_t id0 = tid < pages ? page_of(tid) : -1;
+  const bool in0 = id0 >= 0 && id0 < a.F;
+  const int32_t ru0 = in0 ? a.rev_unit[id0] : -1, ri0 = in0 ? a.rev_idx[id0] : -1;
   __syncthreads();
 
   // keys, the first counting pass, and what the classes say is held
@@ -168,6 +168,11 @@ __global__ void __launch_bounds__(kPlanThreads, 2) k_evict_plan(const __grid_con
       key[p] = k;
     }
   }
+  // the first slots are on their way while the threshold is found
+  const int32_t *slots = a.slot_of + pl.row * a.Hkv + pl.h;
+  int32_t slot[kEach];
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) slot[e] = slots[static_cast<int64_t>(min(tid + e * kPlanThreads, ctx - 1)) * a.Hkv];
   hi = block_sum(hi, sm);
   lo = block_sum(lo, sm);
   safe = block_sum(safe, sm);
@@ -253,12 +258,12 @@ __global__ void __launch_bounds__(kPlanThreads, 2) k_evict_plan(const __grid_con
 
   // survivors and evicted, by slot and by position
   uint32_t *gone_pos = a.gone + static_cast<int64_t>(u) * ((a.cap + 31) / 32);
-  const int32_t *slots = a.slot_of + pl.row * a.Hkv + pl.h;
   bool bad = false;
   for (int32_t p0 = tid; p0 - tid < ctx; p0 += kEach * kPlanThreads) {
-    int32_t slot[kEach];
+    if (p0 != tid) {
 #pragma unroll
-    for (int e = 0; e < kEach; ++e) slot[e] = slots[static_cast<int64_t>(min(p0 + e * kPlanThreads, ctx - 1)) * a.Hkv];
+      for (int e = 0; e < kEach; ++e) slot[e] = slots[static_cast<int64_t>(min(p0 + e * kPlanThreads, ctx - 1)) * a.Hkv];
+    }
 #pragma unroll
     for (int e = 0; e < kEach; ++e) {
       const int32_t p = p0 + e * kPlanThreads, s = slot[e];
@@ -289,7 +294,11 @@ __global__ void __launch_bounds__(kPlanThreads, 2) k_evict_plan(const __grid_con
   all = block_sum(all, sm);
   kh = block_sum(kh, sm);
   kl = block_sum(kl, sm);
-  wrong |= all != held;
+  bool wrong = all != held || (tid < pages && (ru0 != a.unit_base + u || ri0 != tid || !in0));
+  for (int32_t j = tid + kPlanThreads; j < pages; j += kPlanThreads) {
+    const int32_t id = page_of(j);
+    if (id < 0 || id >= a.F || a.rev_unit[id] != a.unit_base + u || a.rev_idx[id] != j) wrong = true;
+  }
   uint32_t *stay_out = a.stay + static_cast<int64_t>(u) * (a.cap / 32 + 2);
   for (int32_t i = tid; i < words; i += kPlanThreads) stay_out[i] = stay[i];
   if (wrong) bad_s = 1;
@@ -587,8 +596,8 @@ cudaError_t launch_after(void (*k)(P...), unsigned grid, int threads, size_t sme
 cudaError_t launch_evict(const EvictArgs &a, cudaStream_t s) {
   const size_t maps = 8 * static_cast<size_t>(a.cap / 32 + 2);
   const size_t plan = maps + 4 * static_cast<size_t>(a.cap / 32 + 1) + (a.cap > kEvictKeys ? 0 : 4 * static_cast<size_t>(a.cap));
-  // blocks a unit: one for 2048 positions
-  const int32_t slices = static_cast<int32_t>(std::min<int64_t>((a.cap + 2047) / 2048, std::max<int64_t>(1, INT32_MAX / a.U)));
+  // blocks a unit: one for 4096 positions
+  const int32_t slices = static_cast<int32_t>(std::min<int64_t>((a.cap + 4095) / 4096, std::max<int64_t>(1, INT32_MAX / a.U)));
   if (cudaError_t e = cudaFuncSetAttribute(k_evict_plan, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(plan)))
     return e;
   if (cudaError_t e = cudaFuncSetAttribute(k_evict_apply, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(maps)))

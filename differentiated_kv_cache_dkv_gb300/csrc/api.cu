@@ -277,6 +277,9 @@ bool valid_chunk(const dkv_chunk_batch *b, const dkv_chunk_pages *p) {
       static_cast<int64_t>(b->n_layers) * b->R > INT32_MAX / b->Hkv ||
       (b->n_layers > 0 && b->T > INT32_MAX / b->n_layers))
     return false;
+  // a request's key tiles, over its items (256 / G tokens) and with what each costs beside them, are counted in 32 bits
+  const int64_t tpi = 2 * (128 / (b->Hq / b->Hkv)), longest = b->max_new < b->T ? b->max_new : b->T;
+  if ((longest + tpi - 1) / tpi > INT32_MAX / ((static_cast<int64_t>(b->cap) + 127) / 128 + 4)) return false;
   if (b->q_stride < 0 || b->q_stride % 8 != 0 || (b->q_stride && b->q_stride < b->Hq * int64_t{128}) ||
       b->q_stride > (int64_t{1} << 32) || b->kv_stride < 0 || b->kv_stride % 8 != 0 ||
       (b->kv_stride && b->kv_stride < b->Hkv * int64_t{128}) || b->kv_stride > (int64_t{1} << 32))

@@ -30,10 +30,12 @@
 // take 3000 cycles a tile: 64 single tokens 314 us).
 //
 // The reference m of a row is the first tile's maximum, rounded up to a whole
-// number (log2 units), and moves only when the sum of a tile's weights passes
-// 2^60: weights and outputs in progress have fp32's exponent, so nothing is
-// lost by a reference that is not the maximum, and the usual tile needs no
-// maximum at all.  P waits in registers until that test: the careful body then
+// number (log2 units), and moves only when the sum of a tile's weights (of 32
+// columns of it in the careful body) passes 2^13: weights and outputs in
+// progress have fp32's exponent, so nothing is lost by a reference that is not
+// the maximum, and the usual tile needs no maximum at all.  A row's weights then
+// add up to at most 2^15 a tile, 2^8 cap: that times the largest value has to
+// stay below 2^128.  P waits in registers until the test: the careful body then
 // starts again from S.
 #include <algorithm>
 #include <cmath>
@@ -330,7 +332,7 @@ constexpr int kThreads = 32 * (kSoftWarps + 3);
 constexpr uint32_t kTmemCols = 512;  // S (and P) of warpgroup w at 128 w, O at 256 + 128 w
 constexpr int kRing = 5;             // K and V tiles in flight
 constexpr int kSegs = 4;
-constexpr float kMost = 0x1p60f;     // sum of a tile's weights that moves the reference
+constexpr float kMost = 0x1p13f;     // sum of a tile's weights that moves the reference
 constexpr float kFar = 0x1p20f;      // references beyond it: logits are rounded before it is taken off
 
 // What a block does next: key tiles [t0, t0 + nt) of an item.
@@ -560,6 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // nothing to do: the lengths have been reported
   } else if (warp == kCopyWarp) {
     // ================= copies: a segment's first K and V tiles, its Q, the others
+    asm volatile("fence.proxy.async;" ::: "memory");  // the copies read what the launch before stored
     const int32_t waves = p.hdr->waves, grid = gridDim.x, npg = 128 / a.B;
     const int64_t cut0 = p.hdr->cut0;
     int64_t w = p.cut[blockIdx.x];

@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto request = [&](int32_t k) { return a.R <= kSort ? sm.order[k] : k; };
     auto pairs_of = [&](int32_t r) {
       const int32_t n = __ldg(a.new_lens + r);
-      return n > 0 ? (__ldg(a.ctx_lens + r) + n + 255) / 256 : 0;
+      return n > 0 ? (__ldg(a.ctx_lens + r) + n - 1) / 256 + 1 : 0;
     };
     int64_t all = 0;
     for (int32_t k0 = 0; k0 < a.R; k0 += 32) {

@@ -505,10 +505,14 @@ int32_t dkv_extend_significance(const dkv_extend_batch *b, const int32_t *acc_le
  * new_lens[r] = 1 is a generation step over the unquantised cache.
  *
  * Precision: products of bf16 values added in fp32; references, sums and
- * outputs in progress are fp32; the weights enter the second product rounded
- * to bf16; out is bf16.  Range: queries and keys of any finite size; a logit
- * that passes fp32's range spoils its row; values up to 2^100.  Slots of a
- * page behind a request's last token may hold anything.
+ * outputs in progress are fp32; out is bf16.  A request's new tokens
+ * are worked on 2 (128 / G) at a time; their weights enter the second product
+ * rounded to bf16, and where only 128 / G or fewer are left (short chunks,
+ * single tokens), as the sum of two bf16 values.  Range: queries and keys of any finite size; a query that is not
+ * finite, or a logit that passes fp32's range, spoils its row; values up to
+ * 2^100, or 2^120 / cap where that is less.  Slots of a page behind a request's
+ * last token may hold anything; the tokens before it are finite (one that is
+ * not may spoil the rows before it too).
  *
  * dkv_chunk_significance adds what those rows give: with p(i, t) =
  * exp(x_t - lse) recomputed from the lse of dkv_chunk_attention,
@@ -517,7 +521,8 @@ int32_t dkv_extend_significance(const dkv_extend_batch *b, const int32_t *acc_le
  * Each sum is formed in a fixed order: equal inputs give equal bits.  Counts
  * (sig_cnt) are the caller's: + new_lens[r] for every held position,
  * new_lens[r] - j for new token j.  A row whose lse is -inf adds nothing; p
- * below 2^-126 are 0.
+ * below 2^-126 are 0.  Queries are finite here: one that is not spoils its
+ * head's sums.
  * ------------------------------------------------------------------------ */
 typedef struct dkv_chunk_pages {
   int64_t F;                 /* pages; 1 <= F */
@@ -531,7 +536,8 @@ typedef struct dkv_chunk_batch {
   int32_t L, R, Hq, Hkv;     /* the pages' layers, requests, heads; 1 <= Hq / Hkv <= 128 */
   int32_t cap;               /* positions per request (sig_sum rows); ctx + new <= cap */
   int32_t layer0, n_layers;  /* attend layers [layer0, layer0 + n_layers) of the pages */
-  int32_t max_new;           /* >= every new_lens[r]; exact is fastest */
+  int32_t max_new;           /* >= every new_lens[r]; exact is fastest.  A chunk's work, n G / 256 * (cap / 128 + 4)
+                                with n = min(max_new, T), has to stay below 2^31: split a larger one */
   int64_t T;                 /* sum of new_lens */
   int64_t q_stride, kv_stride; /* elements from one token's row of q (of k_new and v_new) to the next, a
                                 multiple of 8; 0: Hq * 128 (Hkv * 128).  Layers follow T rows later */
@@ -674,7 +680,7 @@ int32_t dkv_defrag(const dkv_pool *pool, const dkv_tables *t, int64_t U, int64_t
  * ------------------------------------------------------------------------ */
 typedef struct dkv_evict_batch {
   int32_t L, R, Hq, Hkv;     /* the tables' shape; R <= 65535 */
-  int32_t cap;               /* positions per request, as in dkv_decode_batch; a multiple of 16 */
+  int32_t cap;               /* positions per request, as in dkv_decode_batch; a multiple of 16, <= 2^18 */
   int32_t sinks, window;     /* >= 0 */
   int32_t reserved;          /* must be 0 */
   int64_t unit_base;         /* global id of unit 0 of the tables */
@@ -694,8 +700,11 @@ int32_t dkv_evict_workspace_size(const dkv_evict_batch *b, const dkv_pool *pool,
  * DKV_E_INVAL: a bad shape, pointer or workspace.  All-or-nothing: on a
  * device-side error (status word) nothing has changed: DKV_E_LENS (a
  * ctx_lens[r] outside [0, cap]), DKV_E_INTERNAL (headers, classes, slots, page
- * ids, reverse entries or cursors that contradict one another).  A unit that
- * its budget leaves as it is is not looked into beyond its header. */
+ * ids, reverse entries or cursors that contradict one another).  The position
+ * that a moved token's page slot holds is not compared with slot_of before: one
+ * outside [0, ctx_lens[r]) is reported (DKV_E_INTERNAL) while the token is moved
+ * and no slot_of is written for it.  A unit that its budget leaves as it is is
+ * not looked into beyond its header. */
 int32_t dkv_evict(const dkv_evict_batch *b, const dkv_pool *pool, const dkv_tables *t, void *workspace,
                   size_t workspace_bytes, void *stream);
 

@@ -81,6 +81,16 @@ def test_chunk_calls_reject_bad_arguments(lib):
     assert sig(_cbatch(T=0, q=None, lse=None)) == libdkv.DKV_OK
 
 
+def test_a_chunk_whose_work_does_not_fit_32_bits_is_refused(lib):
+    n = ctypes.c_size_t(0)
+    g = _pages(F=1 << 20, B=16, tmax=1 << 20)
+    for max_new, T, want in ((1 << 24, 1 << 24, BAD), (1 << 24, 1 << 14, libdkv.DKV_OK), (1 << 14, 1 << 24, libdkv.DKV_OK),
+                             (1 << 15, 1 << 15, BAD)):
+        # groups of 128: 2 tokens an item, each of up to 2^17 key tiles
+        b = _cbatch(R=1, Hq=128, Hkv=1, cap=1 << 24, max_new=max_new, T=T)
+        assert lib.dkv_chunk_workspace_size(ctypes.byref(b), ctypes.byref(g), ctypes.byref(n)) == want, (max_new, T)
+
+
 def test_evict_rejects_bad_arguments(lib):
     tab = libdkv.dkv_tables(256, 6, 0, 512)
     n = ctypes.c_size_t(0)

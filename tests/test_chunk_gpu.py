@@ -117,6 +117,35 @@ def test_rising_logits_move_the_reference():
     c.check(d, c.reference(scale=2.0))
 
 
+@pytest.mark.parametrize("new", [[1], [5], [20], [70]])
+def test_large_values_under_a_first_reference_far_below(new):
+    """Values of up to 2^100 whose logits lie 50 log2 units above those of a row's first positions: weights relative
+    to those would add up to 2^58."""
+    c = Chunk(2, 1, 16, [300], new, seed=14, outlier=1.0)
+    c.q[:] = 1.0
+    for p in range(300):
+        c.k[0, int(c.table[0, p // 16]), p % 16, 0] = 0.0 if p < 32 else 0.27
+    c.kn[:] = 0.27
+    c.v = (c.v.float().clamp(-4, 4) * 2.0 ** 98).bfloat16()
+    c.vn = (c.vn.float().clamp(-4, 4) * 2.0 ** 98).bfloat16()
+    d = c.device(scale=1.0)
+    assert c.attend(d) == libdkv.DKV_OK
+    c.check(d, c.reference(scale=1.0))
+
+
+def test_more_requests_than_the_plan_keeps_in_shared_memory():
+    c = Chunk(16, 16, 8, [7 * i % 50 for i in range(1100)], [1 + (i % 97 == 0) for i in range(1100)], seed=15)
+    d = c.device()
+    assert c.attend(d) == libdkv.DKV_OK
+    ref = c.reference(lse_in=d["lse"].cpu().numpy())
+    c.check(d, ref)
+    before = torch.ones((1, c.R * c.cap, c.Hq))
+    sig = before.cuda()
+    libdkv.dkv_chunk_significance(d["batch"], d["pages"], sig, d["pool"])
+    assert libdkv.dkv_get_status(d["pool"]) == libdkv.DKV_OK
+    c.check_significance(sig.cpu().numpy(), before.numpy(), ref[4])
+
+
 def test_bad_lengths_write_nothing():
     c = Chunk(4, 2, 16, [30, 50], [10, 4], seed=1)
     for over in (dict(new=[10, 5]), dict(new=[-1, 15]), dict(ctx=[30, -1]), dict(ctx=[30, c.cap - 3]), dict(max_new=9)):
@@ -268,8 +297,8 @@ def test_a_prompt_in_chunks_is_the_prompt_at_once():
         new = [min(n - c, m) for n, c, m in zip(lens, ctx, (256, 100))]
         at = torch.cat([torch.arange(s + c, s + c + n) for s, c, n in zip(start, ctx, new)]).cuda()
         o, lse = torch.empty((1, sum(new), Hq, 128), dtype=torch.bfloat16, device="cuda"), torch.empty((1, sum(new), Hq), device="cuda")
-        b = libdkv.make_chunk_batch(Hkv, cap, q[:, at], i32(new), i32(ctx), max(new), SCALE, k_new=k[:, at],
-                                    v_new=v[:, at], out=o, lse=lse)
+        qc, kc, vc, nc, cc = q[:, at], k[:, at], v[:, at], i32(new), i32(ctx)  # the batch holds their addresses alone
+        b = libdkv.make_chunk_batch(Hkv, cap, qc, nc, cc, max(new), SCALE, k_new=kc, v_new=vc, out=o, lse=lse)
         ws = torch.empty(libdkv.dkv_chunk_workspace_size(b, pages), dtype=torch.uint8, device="cuda")
         libdkv.dkv_chunk_attention(b, pages, pool, ws)
         libdkv.dkv_chunk_significance(b, pages, mysig, pool)

@@ -175,6 +175,35 @@ def test_errors_change_nothing():
         assert_untouched(_state(dec), before, what)
 
 
+@pytest.mark.parametrize("bad", [300, 304, -1, 2 ** 31 - 1])
+def test_a_position_in_a_page_that_is_none(bad):
+    """A token whose page slot names no position of its request: it is moved and reported, its own slot_of stays and
+    everything else is right."""
+    w = W.small("evict_pos", lens=[300], L=1, Hq=4, Hkv=2)
+    cap, u, G = 304, 1, 2
+    dec, sig, cnt, ctx = make_decoder(w, cap)
+    kh, vh = WIDTHS[w.scheme]
+    n_hi, n_lo, p_hi = (int(x) for x in dec.tables.unit_hdr[u, :3])
+    first, n, code, per = (0, n_hi, 2, w.P) if n_hi > 1 else (p_hi, n_lo, 1, 2 * w.P)
+    slot, cls = (x.view(cap, w.Hkv)[:, u] for x in (dec.slot_of, dec.classes))
+    p = int(((cls == code) & (slot == n - 1)).nonzero()[0, 0])  # the token in the last slot is the one that stays
+    sig.view(cap, w.Hq)[p, G * u:G * (u + 1)] = 1e6
+    id_ = int(dec.tables.fwd.view(-1)[u * dec.pmax + first + (n - 1) // per])
+    at = 16 * (kh + vh) * w.P + 16 * w.P + 4 * ((n - 1) % per)
+    page = dec.pool.pages.view(torch.uint8).view(dec.pool.F, -1)[id_]
+    assert page[at:at + 4].cpu().view(torch.int32).item() == p
+    page[at:at + 4] = torch.tensor([bad], dtype=torch.int32).view(torch.uint8).cuda()
+    before = _state(dec)
+    dec.evict(_i32([1]), ctx, sig, cnt, window=0)
+    assert libdkv.dkv_get_status(dec.pool) == libdkv.DKV_E_INTERNAL
+    want = serial_evict(before, w.L, w.R, w.Hq, w.Hkv, cap, w.P, kh, vh, [1], w.lens, sig.cpu().numpy(), cnt.cpu().numpy())
+    want["slot_of"].reshape(cap, w.Hkv)[p, u] = n - 1
+    got = _state(dec)
+    assert_equal(got, want, str(bad))
+    for k in ("classes", "slot_of"):
+        assert np.array_equal(got[k], want[k].reshape(-1)), k
+
+
 def test_a_captured_call():
     w = W.small("evict_graph", lens=[400, 150], L=1, Hq=4, Hkv=2)
     cap = 400

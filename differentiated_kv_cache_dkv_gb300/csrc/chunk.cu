@@ -27,7 +27,7 @@
 // 16 rows lie four times in their row tile, once in each warp's 32 lanes of
 // tensor memory, and every warp weighs a quarter of a key tile's columns: eight
 // softmaxes over keys of their own, joined at the end (one warp alone would
-// take 3000 cycles a tile: 64 single tokens 314 us).
+// take 3000 cycles a tile: 64 single tokens 314 us of 273).
 //
 // The reference m of a row is the first tile's maximum, rounded up to a whole
 // number (log2 units), and moves only when the sum of a tile's weights (of 32
@@ -36,7 +36,23 @@
 // the maximum, and the usual tile needs no maximum at all.  A row's weights then
 // add up to at most 2^15 a tile, 2^8 cap: that times the largest value has to
 // stay below 2^128.  P waits in registers until the test: the careful body then
-// starts again from S.
+// starts again from S.  What a row does not see is taken out of S before.
+//
+// Measured (a whole call, its append included; of 1951.6 TFLOP/s of bf16
+// products and 6773 GB/s of copies measured on the same kind of GPU):
+//   4 requests, 1024 tokens each after 16384, 32 heads over 8 (1.13 TFLOP):
+//     835 us, 69%.  A key tile takes 3200 cycles; its products alone, at the
+//     full rate, 2048.  S = Q K^T reads both operands from shared memory, 128
+//     bytes a clock, which is all there is, beside TMA's writes.
+//   4 prompts of 2048 from their start (137 GFLOP): 197 us, 36%.  An item has
+//     8.5 key tiles there, and between items 7000 cycles pass in which outputs
+//     leave and the next first softmax has no product beside it; append 14 us.
+//   16 requests, 0 to 333 tokens after 0 to 5001, 28 heads over 4 (98.7 GFLOP):
+//     143 us, 35%: the same, the joins of the cut items and the append, 8 us.
+//   64 single tokens after 2047 to 8191 (1.34 GB): 273 us, 73% of the copies'
+//     rate: five tiles of 32 KB a multiprocessor in flight, four of them 294 us,
+//     three 383; append 13 us.
+//   1 request, 16 tokens after 512: 30 us, two launches and a chain of waits.
 #include <algorithm>
 #include <cmath>
 #include <cstddef>
@@ -481,23 +497,17 @@ __device__ __forceinline__ void scale_weights(uint32_t at, float f) {
   tmem_wait_st();
 }
 
-// Four 16-byte words a lane (one row), transposed within four lanes: then word
-// i is of the i-th of the four rows, and the lanes' words follow one another.
-__device__ __forceinline__ void transpose4(uint4 (&e)[4]) {
-  const bool b0 = threadIdx.x & 1, b1 = threadIdx.x & 2;
-  auto swap = [](uint4 &keep0, uint4 &keep1, bool b, int o) {
-    uint4 t = b ? keep0 : keep1;
-    t.x = __shfl_xor_sync(kFull, t.x, o);
-    t.y = __shfl_xor_sync(kFull, t.y, o);
-    t.z = __shfl_xor_sync(kFull, t.z, o);
-    t.w = __shfl_xor_sync(kFull, t.w, o);
-    if (b) keep0 = t;
-    else keep1 = t;
-  };
-  swap(e[0], e[1], b0, 1);
-  swap(e[2], e[3], b0, 1);
-  swap(e[0], e[2], b1, 2);
-  swap(e[1], e[3], b1, 2);
+// Two 16-byte words a lane (one row), exchanged within two lanes: then e0 is of
+// the even lane's row and e1 of the odd one's, the even lane's half first.
+__device__ __forceinline__ void transpose2(uint4 &e0, uint4 &e1) {
+  const bool b = threadIdx.x & 1;
+  uint4 t = b ? e0 : e1;
+  t.x = __shfl_xor_sync(kFull, t.x, 1);
+  t.y = __shfl_xor_sync(kFull, t.y, 1);
+  t.z = __shfl_xor_sync(kFull, t.z, 1);
+  t.w = __shfl_xor_sync(kFull, t.w, 1);
+  if (b) e0 = t;
+  else e1 = t;
 }
 
 // This thread's row of O times f.  (The products into O were complete when S was.)
@@ -805,12 +815,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         } else if (some) {
           const int32_t lim = live ? lim0 - 128 * t : 128;
-          const bool masked = __any_sync(kFull, lim < 128);
+          if (__any_sync(kFull, lim < 128)) {
+            // the item's last tiles: what a row does not see leaves S before the usual code reads it
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              if (__all_sync(kFull, lim >= 32 * c + 32)) continue;
+              uint32_t u[32];
+              tmem_ld32(ts_s + 32 * c, u);
+              tmem_wait32(u);
+              keep_columns(u, lim - 32 * c);
+              tmem_st16(ts_s + 32 * c, u);
+              tmem_st16(ts_s + 32 * c + 16, u + 16);
+            }
+            tmem_wait_st();
+          }
           if (__any_sync(kFull, live && m == -INFINITY)) {  // rows start: their first columns set the reference
             uint32_t u[32];
             tmem_ld32(ts_s, u);
             tmem_wait32(u);
-            if (masked) keep_columns(u, lim);
             const float top = ceilf(max32(u) * sl2);
             if (m == -INFINITY) m = top;
           }
@@ -818,10 +840,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           bool slow = true;
           const bool near = two && !__any_sync(kFull, live && !(fabsf(m) < kFar));
           // P of 32 columns takes the first 16 of their columns of S
-          if (near && !masked) {
+          if (near) {
             const uint64_t nm2 = f2_pack(-m, -m);
             // without a branch, and P in registers until the tile's sum is known: a test for every 32 columns made
-            // the tile 1560 cycles of 1000, masks where they are needed 1370
+            // the tile 1560 cycles of 1000, masks where they are needed 1370 (and a masked tile in the loop below took
+            // 2800)
             uint32_t u0[32], u1[32], w[64];
             // columns 32 c .. + 31 in u, the next ones on their way to v
             auto chunk = [&](auto which, uint32_t(&u)[32], uint32_t(&v)[32]) {
@@ -853,7 +876,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               auto load = [&] {
                 tmem_ld32(ts_s + 32 * c, u);
                 tmem_wait32(u);
-                if (masked) keep_columns(u, lim - 32 * c);
               };
               load();
               const float mo = m == -INFINITY ? 0.0f : m;
@@ -1035,10 +1057,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       float l = f2_sum(l2);
       const int64_t at = (static_cast<int64_t>(g.li) * a.T + g.tok + i) * a.Hq + g.h * G + (row - rt * G);
       const int32_t prow = (two && wg ? tpt * G : 0) + row;  // of a partial result
-      // where the four rows of this lane's group go (-1: not a row)
-      int64_t to[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) to[e] = __shfl_sync(kFull, live ? at : -1, (lane & ~3) + e);
+      // where the two rows of this lane's pair go (-1: not a row)
+      const int64_t to0 = __shfl_sync(kFull, live ? at : -1, lane & ~1), to1 = __shfl_sync(kFull, live ? at : -1, lane | 1);
       if (started) {
         if (!(ok = warp_wait(&sm.odone[wg], nseg & 1u))) break;
         ++nseg;
@@ -1057,39 +1077,51 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float inv = g.slot < 0 ? 1.0f / l : 1.0f;
         f0 *= inv;
         f1 *= inv;
+        // loops of a few instructions: this code runs once an item, and fetching it costs as much as what it does (all
+        // columns in two bodies of two steps each: a first chunk 203 us of 197)
         if (some) {
-#pragma unroll 2
-          for (int c = 0; c < 4; ++c) {
-            uint32_t u[32];
-            tmem_ld32(ts_o + 32 * c, u);
-            tmem_wait32(u);
-            if (join && wg == 1) {
+          if (join && wg == 1) {
+#pragma unroll 1
+            for (int c = 0; c < 8; ++c) {
+              uint32_t u[16];
+              tmem_ld16(ts_o + 16 * c, u);
+              tmem_wait16(u);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) ox[(32 * c + e) * 128 + row] = __uint_as_float(u[e]);
-              continue;
+              for (int e = 0; e < 16; ++e) ox[(16 * c + e) * 128 + row] = __uint_as_float(u[e]);
             }
-            float x[32];
+          } else {
+            uint16_t *dst0 = a.out + (to0 * 128 + 8 * (lane & 1)), *dst1 = a.out + (to1 * 128 + 8 * (lane & 1));
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              uint32_t u[32];
+              tmem_ld32(ts_o + 32 * c, u);
+              tmem_wait32(u);
+              float x[32];
 #pragma unroll
-            for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(u[e]) * f0;
-            if (join) {
+              for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(u[e]) * f0;
+              if (join) {
 #pragma unroll
-              for (int e = 0; e < 32; ++e) x[e] += ox[(32 * c + e) * 128 + row] * f1;
-            }
-            if (g.slot < 0) {
-              uint4 y[4];
+                for (int e = 0; e < 32; ++e) x[e] += ox[(32 * c + e) * 128 + row] * f1;
+              }
+              if (g.slot < 0) {
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                y[e] = make_uint4(bf16x2_rn(x[8 * e], x[8 * e + 1]), bf16x2_rn(x[8 * e + 2], x[8 * e + 3]),
-                                  bf16x2_rn(x[8 * e + 4], x[8 * e + 5]), bf16x2_rn(x[8 * e + 6], x[8 * e + 7]));
-              transpose4(y);  // four lanes write 64 bytes of a row
+                for (int k = 0; k < 2; ++k) {
+                  uint4 y[2];
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if (to[e] >= 0) *reinterpret_cast<uint4 *>(a.out + to[e] * 128 + 32 * c + 8 * (lane & 3)) = y[e];
-            } else if (live) {
+                  for (int e = 0; e < 2; ++e) {
+                    const float *z = x + 16 * k + 8 * e;
+                    y[e] = make_uint4(bf16x2_rn(z[0], z[1]), bf16x2_rn(z[2], z[3]), bf16x2_rn(z[4], z[5]), bf16x2_rn(z[6], z[7]));
+                  }
+                  transpose2(y[0], y[1]);  // two lanes write 32 bytes of a row
+                  if (to0 >= 0) *reinterpret_cast<uint4 *>(dst0 + 32 * c + 16 * k) = y[0];
+                  if (to1 >= 0) *reinterpret_cast<uint4 *>(dst1 + 32 * c + 16 * k) = y[1];
+                }
+              } else if (live) {
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
-                p.o[(static_cast<int64_t>(g.slot) * 32 + 8 * c + e) * rows + prow] =
-                    make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+                for (int e = 0; e < 8; ++e)
+                  p.o[(static_cast<int64_t>(g.slot) * 32 + 8 * c + e) * rows + prow] =
+                      make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+              }
             }
           }
           if (join && wg == 1) sm.ml[row] = make_float2(m, l);

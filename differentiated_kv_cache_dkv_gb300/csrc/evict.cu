@@ -18,8 +18,17 @@
 //     give every mover its hole; the moves, a group of lanes each; the cleared
 //     slots, the rows of the evicted, the tables and the ring.
 //
-// What bounds it: the significance (4 Hq bytes a position) and the moved
-// tokens' bytes.
+// Floor: the significance (4 Hq bytes a position), slots and classes, and the
+// moved tokens' bytes.  What bounds it is latency: a unit's passes follow one
+// another (weights, counts, slots; then ranks, moves, tables), with 45% of the
+// warps' places taken.  Measured, with a copy that puts the state back: 8
+// layers of 16 requests of 2048 to 8192 positions, 8 KV heads, half evicted (0.5
+// GB) 281 us, 26% of 6773 GB/s; 28 layers of 7 requests, 4 KV heads, 85% kept (99
+// MB) 126 to 132 us, 12%; one layer of 4 requests of 512 50 us.  Four positions
+// in flight a thread in three blocks a multiprocessor: eight in two 294 us, four
+// in four 322 (spilled); 256 threads a block 305 to 342, 1024 327.  Five apply
+// blocks a multiprocessor: four 284, six 333 us; 256 or 1024 moves listed at a
+// time 291 to 293; a block for 2048 positions 302.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -84,7 +93,7 @@ __device__ __forceinline__ Place place_of(const EvictArgs &a, int32_t u) {
 // Words of the slot bitmaps: the high list's, then the low list's.
 __device__ __forceinline__ int32_t words_of(int32_t n) { return (n + 31) >> 5; }
 
-__global__ void __launch_bounds__(kPlanThreads, 2) k_evict_plan(const __grid_constant__ EvictArgs a) {
+__global__ void __launch_bounds__(kPlanThreads, 3) k_evict_plan(const __grid_constant__ EvictArgs a) {
   let_next_launch_start();
   extern __shared__ uint32_t dyn[];
   __shared__ int32_t sm[kPlanThreads / 32];
@@ -125,7 +134,7 @@ __global__ void __launch_bounds__(kPlanThreads, 2) k_evict_plan(const __grid_con
   const bool quad = (G & 3) == 0 && (a.Hq & 3) == 0;  // then a token's scores are whole 16-byte words
   const float *sig = a.sig_sum + pl.row * a.Hq + pl.h * G;
   const int32_t *cnt = a.sig_cnt ? a.sig_cnt + static_cast<int64_t>(pl.r) * a.cap : nullptr;
-  constexpr int kEach = 8;  // positions a thread has in flight; the scores of positions without a token are read too
+  constexpr int kEach = 4;  // positions a thread has in flight; the scores of positions without a token are read too
   for (int32_t p0 = tid; p0 - tid < ctx; p0 += kEach * kPlanThreads) {
     int32_t c[kEach];
     float w[kEach];
@@ -423,7 +432,7 @@ __device__ __forceinline__ void move_slots(const EvictArgs &a, const List &l, co
 // `slices` blocks a unit: each a share of the evicted positions and of the
 // moves; the last one to end, which finds all moves done, clears the vacated
 // slots and writes the tables.
-__global__ void __launch_bounds__(kApplyThreads, 4) k_evict_apply(const __grid_constant__ EvictArgs a, int32_t slices) {
+__global__ void __launch_bounds__(kApplyThreads, 5) k_evict_apply(const __grid_constant__ EvictArgs a, int32_t slices) {
   after_launch_before();
   extern __shared__ uint32_t dyn[];
   __shared__ int2 src[kMoves], dst[kMoves];

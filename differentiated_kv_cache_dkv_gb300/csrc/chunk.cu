@@ -5,7 +5,7 @@
 // i G + g within its unit (layer, request, KV head); with that packing the
 // heads of a group share every tile of K and V.  A row tile is tpt = 128 / G
 // whole tokens, an item two row tiles (or one, when no more rows are left) of
-// a unit against its keys, in key tiles of 128 positions.  Two launches:
+// a unit against its keys, in key tiles of 128 positions.  Three launches:
 //   k_chunk_append  stores the new tokens' K and V in their pages; block 0
 //     meanwhile plans: tokens, items and key tiles of each request, and which
 //     of them each block of the attention takes.
@@ -14,7 +14,8 @@
 //     same time, which keeps them in L2), as many waves as leave every block at
 //     or below the mean; the rest of the key tiles, laid end to end, is cut so
 //     that all blocks end up with the same number.  Items that are cut leave
-//     partial results, which the block that ends last joins.
+//     partial results.
+//   k_chunk_join    joins those, each item's by several blocks.
 // The roles of a block, pipelined through mbarriers:
 //   copy warp       Q, K and V by TMA, a lane a page, through a ring of tiles;
 //   product warps (2)  S = Q K^T and O += P V of a warpgroup each, P read from
@@ -27,7 +28,7 @@
 // 16 rows lie four times in their row tile, once in each warp's 32 lanes of
 // tensor memory, and every warp weighs a quarter of a key tile's columns: eight
 // softmaxes over keys of their own, joined at the end (one warp alone would
-// take 3000 cycles a tile: 64 single tokens 314 us of 273).
+// take 3000 cycles a tile: 64 single tokens 314 us, then 273).
 //
 // The reference m of a row is the first tile's maximum, rounded up to a whole
 // number (log2 units), and moves only when the sum of a tile's weights (of 32
@@ -41,18 +42,18 @@
 // Measured (a whole call, its append included; of 1951.6 TFLOP/s of bf16
 // products and 6773 GB/s of copies measured on the same kind of GPU):
 //   4 requests, 1024 tokens each after 16384, 32 heads over 8 (1.13 TFLOP):
-//     835 us, 69%.  A key tile takes 3200 cycles; its products alone, at the
+//     808 us, 72%.  A key tile takes 3200 cycles; its products alone, at the
 //     full rate, 2048.  S = Q K^T reads both operands from shared memory, 128
 //     bytes a clock, which is all there is, beside TMA's writes.
-//   4 prompts of 2048 from their start (137 GFLOP): 197 us, 36%.  An item has
+//   4 prompts of 2048 from their start (137 GFLOP): 167 us, 42%.  An item has
 //     8.5 key tiles there, and between items 7000 cycles pass in which outputs
 //     leave and the next first softmax has no product beside it; append 14 us.
 //   16 requests, 0 to 333 tokens after 0 to 5001, 28 heads over 4 (98.7 GFLOP):
-//     143 us, 35%: the same, the joins of the cut items and the append, 8 us.
-//   64 single tokens after 2047 to 8191 (1.34 GB): 273 us, 73% of the copies'
+//     122 us, 41%: the same; append 8 us.
+//   64 single tokens after 2047 to 8191 (1.34 GB): 270 us, 73% of the copies'
 //     rate: five tiles of 32 KB a multiprocessor in flight, four of them 294 us,
 //     three 383; append 13 us.
-//   1 request, 16 tokens after 512: 30 us, two launches and a chain of waits.
+//   1 request, 16 tokens after 512: 32 us, three launches and a chain of waits.
 #include <algorithm>
 #include <cmath>
 #include <cstddef>
@@ -87,18 +88,25 @@ struct ReqPlan {
   int32_t tiles;       // cost a unit
   int32_t ctx, n;
 };
+// An item that several blocks have a part of.
+struct CutItem {
+  int64_t begin, end;   // its cost lies there, key tiles behind the first kStart
+  int32_t slot;         // of the first part's results (later blocks': twice their number)
+  int32_t li, h, tok;   // as in Seg
+  int32_t n, pad;       // n = 0: there is none
+};
 struct PlanPtrs {
   PlanHeader *hdr;
   ReqPlan *req;    // [R]
   int32_t *pre;    // [items a unit of all requests]: cost of the request's items before
   int64_t *cut;    // [grid + 1]: where each block's share of the cut tiles starts
-  int32_t *count;  // [grid]: parts that are there, of the item whose first part is the block's last
+  CutItem *item;   // [grid]: the cut item whose first part is the block's
   float4 *o;       // [2 grid][32][rows] partial results, four channels each
   float2 *ml;      // [2 grid][rows]: reference and sum
 };
 
 struct ChunkLayout {
-  size_t req, pre, cut, count, ml, o, bytes;
+  size_t req, pre, cut, item, ml, o, bytes;
   int32_t tpt, tpi, rows;  // tokens a row tile, an item; rows of a partial result
 };
 
@@ -111,7 +119,7 @@ __host__ ChunkLayout chunk_layout(const ChunkArgs &a) {
   w.req = x; x = align256(x + sizeof(ReqPlan) * static_cast<size_t>(a.R));
   w.pre = x; x = align256(x + 4 * (static_cast<size_t>(a.T / w.tpi) + a.R + 1));
   w.cut = x; x = align256(x + 8 * (kBlocks + 1));
-  w.count = x; x = align256(x + 4 * kBlocks);
+  w.item = x; x = align256(x + sizeof(CutItem) * kBlocks);
   w.ml = x;  x = align256(x + sizeof(float2) * 2 * kBlocks * static_cast<size_t>(w.rows));
   w.o = x;   x = align256(x + 512 * 2 * kBlocks * static_cast<size_t>(w.rows));
   w.bytes = x;
@@ -184,7 +192,7 @@ __device__ void plan(const ChunkArgs &a, const PlanPtrs &p, int32_t tpi, int32_t
   const int64_t U1 = static_cast<int64_t>(a.n_layers) * a.Hkv;
   // read again and again: from shared memory where there is room
   ReqPlan *req = a.R <= kSmemReqs ? req_sm : p.req;
-  for (int32_t c = tid; c < grid; c += kAppendThreads) p.count[c] = 0;
+  for (int32_t c = tid; c < grid; c += kAppendThreads) p.item[c].n = 0;
   // tokens and items before each request
   int64_t tok = 0, rts = 0;
   for (int32_t r0 = 0; r0 < a.R; r0 += kAppendThreads) {
@@ -359,18 +367,17 @@ struct Seg {
   int32_t li, h, r;
   int32_t tok, i0, n;    // the item's first token in the batch and in the request, its tokens
   int32_t ctx;
-  int32_t parts, part0, part0_slot;  // of a cut item: how many, the block that has the first, its slot
 };
 
 struct __align__(1024) Smem {
   uint8_t q[2][kTileBytes];        // row tiles; then the second warpgroup's outputs, by column
   uint8_t ring[kRing][kTileBytes];
-  uint64_t qfull, qfree, joined, qjoin, parted, partgo, full[kRing], empty[kRing];
+  uint64_t qfull, qfree, joined, qjoin, full[kRing], empty[kRing];
   uint64_t sfull[2], pready[2], odone[2], ofree[2], turn[2], ojoin, done[2];
   Seg seg[kSegs];
   float2 ml[128];                  // the second warpgroup's references and sums; [8][16] of eight warps
   uint32_t tmem;
-  int32_t abort, last;
+  int32_t abort;
 };
 constexpr size_t kSmemBytes = sizeof(Smem) + 1024;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
@@ -384,6 +391,8 @@ __device__ __forceinline__ Seg next_seg(const ChunkArgs &a, const PlanPtrs &p, i
                                         int32_t grid, int32_t s, int64_t &w) {
   const int64_t U1 = static_cast<int64_t>(a.n_layers) * a.Hkv;
   Seg g{};
+  CutItem cut{};
+  bool first = false;  // a cut item whose first part this is
   const int32_t c = blockIdx.x;
   int64_t k;  // item within the request
   ReqPlan q;
@@ -410,21 +419,8 @@ __device__ __forceinline__ Seg next_seg(const ChunkArgs &a, const PlanPtrs &p, i
     g.nt = tiles_in(w2 - begin) - g.t0;
     if (g.nt == 0) return g;  // the block's share ends before the item's first tile
     g.slot = g.nt == all - kStart ? -1 : 2 * c + (w == w0 ? 0 : 1);
-    if (g.slot >= 0) {  // the blocks that have a part of the item
-      const int lane = threadIdx.x & 31;
-      g.part0 = -1;
-      for (int32_t b0 = 0; b0 < grid; b0 += 32) {
-        const int32_t b = b0 + lane;
-        const int64_t x0 = b < grid ? p.cut[b] : 0, x1 = b < grid ? p.cut[b + 1] : 0;
-        const bool has = x1 > x0 && x1 > begin && x0 < end && tiles_in(min(x1, end) - begin) > tiles_in(max(x0, begin) - begin);
-        const uint32_t m = __ballot_sync(kFull, has);
-        if (m && g.part0 < 0) {
-          g.part0 = b0 + __ffs(m) - 1;
-          g.part0_slot = 2 * g.part0 + (__shfl_sync(kFull, x0, __ffs(m) - 1) >= begin ? 0 : 1);
-        }
-        g.parts += __popc(m);
-      }
-    }
+    first = g.slot >= 0 && g.t0 == 0;
+    cut = CutItem{begin, end, g.slot, 0, 0, 0, 0, 0};
     w = w2;
   }
   const int32_t unit = static_cast<int32_t>(k / q.items), j = static_cast<int32_t>(k - static_cast<int64_t>(unit) * q.items);
@@ -435,6 +431,13 @@ __device__ __forceinline__ Seg next_seg(const ChunkArgs &a, const PlanPtrs &p, i
   g.n = min(tpi, q.n - g.i0);
   g.tok = q.tok0 + g.i0;
   g.ctx = q.ctx;
+  if (first && (threadIdx.x & 31) == 0) {
+    cut.li = g.li;
+    cut.h = g.h;
+    cut.tok = g.tok;
+    cut.n = g.n;
+    p.item[c] = cut;
+  }
   return g;
 }
 
@@ -538,8 +541,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sm.qfree, 2 + kSoftWarps);
     mbar_init(&sm.joined, kSoftWarps);
     mbar_init(&sm.qjoin, kSoftWarps);
-    mbar_init(&sm.parted, kSoftWarps);
-    mbar_init(&sm.partgo, 1);
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&sm.full[i], 1);
       mbar_init(&sm.empty[i], 2);
@@ -562,6 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   fence_after();
   const uint32_t tmem = sm.tmem;
   after_launch_before();
+  let_next_launch_start();
   const bool valid = *reinterpret_cast<volatile int32_t *>(&p.hdr->ok) != 0;
   const int32_t tpi = 2 * tpt, G = a.G;
   auto wait = [&](uint64_t *bar, uint32_t parity) { return wait_or_abort(bar, parity, abort, a.status); };
@@ -765,7 +767,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t sl2x2 = f2_pack(sl2, sl2);
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const uint32_t ts_s = tmem + lanes + 128 * wg, ts_o = tmem + lanes + 256 + 128 * wg;
-    int32_t base = 0, ns = 0, nseg = 0, joins = 0, qjoins = 0, merges = 0;
+    int32_t base = 0, ns = 0, nseg = 0, joins = 0, qjoins = 0;
     bool ok = true;
     for (int32_t s = 0; ok; ++s) {
       if (!(ok = warp_wait(&sm.qfull, s & 1u))) break;
@@ -922,74 +924,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       // ---- the segment's results
-      // Of a cut item: the block that finds all parts there joins them.  Every softmax warp comes here.
-      auto merge = [&] {
-        __threadfence();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.parted);
-        if (!warp_wait(&sm.parted, merges & 1u)) return false;
-        if (tid == 0) {
-          sm.last = atomicAdd(p.count + g.part0, 1) == g.parts - 1;
-          __threadfence();
-          mbar_arrive(&sm.partgo);
-        }
-        if (!warp_wait(&sm.partgo, merges & 1u)) return false;
-        ++merges;
-        if (!sm.last) return true;
-        __threadfence();
-        // a warp takes eight rows of 32 channels at a time, a thread eight channels of a row
-        const int32_t nr = g.n * G;
-        for (int32_t k = warp; k < 4 * ((nr + 7) / 8); k += kSoftWarps) {
-          const int32_t jr = 8 * (k >> 2) + (lane >> 2), unit = 8 * (k & 3) + 2 * (lane & 3);
-          if (jr >= nr) continue;
-          float mm = -INFINITY, l = 0.0f, x[8] = {};
-          int32_t left = g.parts, b = g.part0;
-          while (left > 0) {  // four parts at a time
-            float2 y[4];
-            float4 u[4], v[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              y[e].x = -INFINITY;
-              if (left == 0) continue;
-              const int64_t slot = left == g.parts ? g.part0_slot : 2 * static_cast<int64_t>(b);
-              y[e] = __ldcg(p.ml + slot * rows + jr);
-              u[e] = __ldcg(p.o + (slot * 32 + unit) * rows + jr);
-              v[e] = __ldcg(p.o + (slot * 32 + unit + 1) * rows + jr);
-              --left;
-              do ++b;
-              while (left > 0 && p.cut[b + 1] == p.cut[b]);  // blocks without a share have no part
-            }
-            const float mn = fmaxf(fmaxf(fmaxf(y[0].x, y[1].x), fmaxf(y[2].x, y[3].x)), mm);
-            if (mn == -INFINITY) continue;
-            const float f = mm == mn ? 1.0f : ex2(mm - mn);
-            mm = mn;
-            l *= f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] *= f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              if (y[e].x == -INFINITY) continue;  // every tile of that part lies behind the row, or there is none
-              const float f1 = y[e].x == mn ? 1.0f : ex2(y[e].x - mn);
-              l += y[e].y * f1;
-              x[0] += u[e].x * f1;
-              x[1] += u[e].y * f1;
-              x[2] += u[e].z * f1;
-              x[3] += u[e].w * f1;
-              x[4] += v[e].x * f1;
-              x[5] += v[e].y * f1;
-              x[6] += v[e].z * f1;
-              x[7] += v[e].w * f1;
-            }
-          }
-          const float inv = 1.0f / l;
-          const int64_t at = (static_cast<int64_t>(g.li) * a.T + g.tok + jr / G) * a.Hq + g.h * G + jr % G;
-          *reinterpret_cast<uint4 *>(a.out + at * 128 + 4 * unit) =
-              make_uint4(bf16x2_rn(x[0] * inv, x[1] * inv), bf16x2_rn(x[2] * inv, x[3] * inv),
-                         bf16x2_rn(x[4] * inv, x[5] * inv), bf16x2_rn(x[6] * inv, x[7] * inv));
-          if (a.lse && unit == 0) a.lse[at] = (mm + log2f(l)) * 0.693147180559945309f;
-        }
-        return true;
-      };
       if (four) {
         // a warp's rows go to shared memory, [warp][column][16 rows]; then a thread joins eight columns of a row
         float *ox = reinterpret_cast<float *>(sm.q[0]) + warp * (128 * 16);
@@ -1050,7 +984,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.joined);
         base += nt;
-        if (g.slot >= 0 && !(ok = merge())) break;
         continue;
       }
       const bool join = !two && nt > 1;
@@ -1139,7 +1072,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (join) ++joins;
       }
       base += nt;
-      if (g.slot >= 0 && !(ok = merge())) break;
     }
   }
 
@@ -1152,6 +1084,114 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// ------------------------------------------------------------------- join --
+
+constexpr int kJoinWarps = 8, kJoinShares = 4;
+
+// Block c kJoinShares + s: a share of the rows of the cut item whose first part is block c's, out of its parts' results.
+// (In the attention itself, by the block that ended last, they took 20 us behind the last tile: a first chunk 197 us of 167.)
+__global__ void __launch_bounds__(32 * kJoinWarps)
+    k_chunk_join(const __grid_constant__ ChunkArgs a, const PlanPtrs p, int32_t grid, int32_t rows) {
+  __shared__ int32_t slots[kBlocks], parts_s;
+  const int32_t c = blockIdx.x / kJoinShares, share = blockIdx.x % kJoinShares;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = a.G;
+  after_launch_before();
+  if (!p.hdr->ok) return;
+  const CutItem g = p.item[c];
+  if (4 * ((g.n * G + 7) / 8) <= kJoinWarps * share) return;
+  if (warp == 0) {
+    int32_t parts = 1;
+    if (lane == 0) slots[0] = g.slot;
+    for (int32_t b0 = c + 1; b0 < grid; b0 += 32) {
+      const int32_t b = b0 + lane;
+      const int64_t x0 = b < grid ? p.cut[b] : g.end, x1 = b < grid ? p.cut[b + 1] : g.end;
+      const bool has = x1 > x0 && x0 < g.end;
+      const uint32_t m = __ballot_sync(kFull, has);
+      if (has) slots[parts + __popc(m & ((1u << lane) - 1u))] = 2 * b;
+      parts += __popc(m);
+      if (__any_sync(kFull, x0 >= g.end)) break;
+    }
+    if (lane == 0) parts_s = parts;
+  }
+  __syncthreads();
+  const int32_t parts = parts_s;
+  // a warp takes eight rows of 32 channels, a thread eight channels of a row; nk such groups and np parts at a time
+  const int32_t nr = g.n * G, all = kJoinWarps * kJoinShares, groups = 4 * ((nr + 7) / 8);
+  auto join_parts = [&](auto nk_of, auto np_of) {
+    constexpr int nk = decltype(nk_of)::value, np = decltype(np_of)::value;
+    for (int32_t k0 = kJoinWarps * share + warp; k0 < groups; k0 += nk * all) {
+      float mm[nk], l[nk], x[nk][8];
+#pragma unroll
+      for (int k = 0; k < nk; ++k) {
+        mm[k] = -INFINITY;
+        l[k] = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[k][e] = 0.0f;
+      }
+      auto row_of = [&](int k) { return 8 * ((k0 + k * all) >> 2) + (lane >> 2); };
+      auto unit_of = [&](int k) { return 8 * ((k0 + k * all) & 3) + 2 * (lane & 3); };
+#pragma unroll 1
+      for (int32_t i0 = 0; i0 < parts; i0 += np) {
+        float2 y[nk][np];
+        float4 u[nk][np], v[nk][np];
+#pragma unroll
+        for (int i = 0; i < np; ++i) {
+          const bool is = i0 + i < parts;
+          const int64_t slot = is ? slots[i0 + i] : 0;
+#pragma unroll
+          for (int k = 0; k < nk; ++k) {
+            y[k][i].x = -INFINITY;
+            if (!is || row_of(k) >= nr) continue;
+            y[k][i] = __ldcg(p.ml + slot * rows + row_of(k));
+            u[k][i] = __ldcg(p.o + (slot * 32 + unit_of(k)) * rows + row_of(k));
+            v[k][i] = __ldcg(p.o + (slot * 32 + unit_of(k) + 1) * rows + row_of(k));
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < nk; ++k) {
+          float mn = mm[k];
+#pragma unroll
+          for (int i = 0; i < np; ++i) mn = fmaxf(mn, y[k][i].x);
+          if (mn == -INFINITY) continue;
+          const float f = mm[k] == mn ? 1.0f : ex2(mm[k] - mn);
+          mm[k] = mn;
+          l[k] *= f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[k][e] *= f;
+#pragma unroll
+          for (int i = 0; i < np; ++i) {
+            if (y[k][i].x == -INFINITY) continue;  // every tile of that part lies behind the row, or there is none
+            const float f1 = y[k][i].x == mn ? 1.0f : ex2(y[k][i].x - mn);
+            l[k] += y[k][i].y * f1;
+            x[k][0] += u[k][i].x * f1;
+            x[k][1] += u[k][i].y * f1;
+            x[k][2] += u[k][i].z * f1;
+            x[k][3] += u[k][i].w * f1;
+            x[k][4] += v[k][i].x * f1;
+            x[k][5] += v[k][i].y * f1;
+            x[k][6] += v[k][i].z * f1;
+            x[k][7] += v[k][i].w * f1;
+          }
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < nk; ++k) {
+        const int32_t jr = row_of(k), unit = unit_of(k);
+        if (jr >= nr) continue;
+        const float inv = 1.0f / l[k];
+        const int64_t at = (static_cast<int64_t>(g.li) * a.T + g.tok + jr / G) * a.Hq + g.h * G + jr % G;
+        *reinterpret_cast<uint4 *>(a.out + at * 128 + 4 * unit) =
+            make_uint4(bf16x2_rn(x[k][0] * inv, x[k][1] * inv), bf16x2_rn(x[k][2] * inv, x[k][3] * inv),
+                       bf16x2_rn(x[k][4] * inv, x[k][5] * inv), bf16x2_rn(x[k][6] * inv, x[k][7] * inv));
+        if (a.lse && unit == 0) a.lse[at] = (mm[k] + log2f(l[k])) * 0.693147180559945309f;
+      }
+    }
+  };
+  // few rows have many parts, many rows mostly two
+  if (groups <= all) join_parts(std::integral_constant<int, 1>{}, std::integral_constant<int, 4>{});
+  else join_parts(std::integral_constant<int, 2>{}, std::integral_constant<int, 2>{});
+}
+
 }  // namespace
 
 size_t chunk_workspace(const ChunkArgs &a) { return chunk_layout(a).bytes; }
@@ -1161,7 +1201,7 @@ cudaError_t launch_chunk(const ChunkArgs &a, void *ws, cudaStream_t s) {
   uint8_t *b = static_cast<uint8_t *>(ws);
   const PlanPtrs p{reinterpret_cast<PlanHeader *>(b), reinterpret_cast<ReqPlan *>(b + w.req),
                    reinterpret_cast<int32_t *>(b + w.pre), reinterpret_cast<int64_t *>(b + w.cut),
-                   reinterpret_cast<int32_t *>(b + w.count), reinterpret_cast<float4 *>(b + w.o),
+                   reinterpret_cast<CutItem *>(b + w.item), reinterpret_cast<float4 *>(b + w.o),
                    reinterpret_cast<float2 *>(b + w.ml)};
   int dev = 0, sms = 0;
   cudaError_t e;
@@ -1181,7 +1221,9 @@ cudaError_t launch_chunk(const ChunkArgs &a, void *ws, cudaStream_t s) {
   const int64_t copies = a.k_new ? a.n_layers * ((a.T + kAppendTokens - 1) / kAppendTokens) : 0;
   k_chunk_append<<<static_cast<unsigned>(1 + copies), kAppendThreads, 0, s>>>(a, p, w.tpi, grid);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  return launch_after(k_chunk, dim3(grid), kThreads, kSmemBytes, s, a, p, qmap, kmap, vmap, qmap4, w.tpt, tpq, w.rows);
+  if ((e = launch_after(k_chunk, dim3(grid), kThreads, kSmemBytes, s, a, p, qmap, kmap, vmap, qmap4, w.tpt, tpq, w.rows)) != cudaSuccess)
+    return e;
+  return launch_after(k_chunk_join, dim3(kJoinShares * grid), 32 * kJoinWarps, 0, s, a, p, grid, w.rows);
 }
 
 }  // namespace dkv

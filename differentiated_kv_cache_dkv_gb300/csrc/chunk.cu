@@ -46,7 +46,7 @@
 //     full rate, 2048.  S = Q K^T reads both operands from shared memory, 128
 //     bytes a clock, which is all there is, beside TMA's writes.
 //   4 prompts of 2048 from their start (137 GFLOP): 167 us, 42%.  An item has
-//     8.5 key tiles there, and between items 7000 cycles pass in which outputs
+//     8.5 key tiles there, and between items 4700 cycles pass in which outputs
 //     leave and the next first softmax has no product beside it; append 14 us.
 //   16 requests, 0 to 333 tokens after 0 to 5001, 28 heads over 4 (98.7 GFLOP):
 //     122 us, 41%: the same; append 8 us.

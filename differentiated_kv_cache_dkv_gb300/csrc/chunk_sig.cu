@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (elect_one()) {
       constexpr uint32_t kStep = kTileBytes >> 4;
       const uint64_t dq = sw128_desc(saddr(sm.ring[0]), 16, 1024);
-      int32_t c = 0, gb = 0, nkr[2] = {0, 0};
+      int32_t c = 0, gb = 0;
       bool ok = true;
       for (int32_t s = 0; ok; ++s) {
         if (!(ok = wait(&sm.segfull, s & 1u))) break;
@@ -268,10 +268,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int32_t blocks = (sm.seg[s % kSegs].b1 - sm.seg[s % kSegs].b0) * (sm.seg[s % kSegs].tb1 - sm.seg[s % kSegs].tb0);
         mbar_arrive(&sm.segfree);
         if (nk == 0) break;
-        for (int32_t k = 0; k < nk && ok; ++k, ++c) {  // K is in tensor memory: its slot is free
-          if (!(ok = wait(&sm.kready[k], nkr[k] & 1u))) break;
-          ++nkr[k];
-          mbar_arrive(&sm.empty[c % kRing]);
+        for (int32_t k = 0; k < 2 && ok; ++k) {  // K is in tensor memory: its slot is free
+          if (!(ok = wait(&sm.kready[k], s & 1u))) break;
+          if (k < nk) mbar_arrive(&sm.empty[c++ % kRing]);
         }
         for (int32_t q = 0; q < blocks && ok; ++q, ++c) {
           const int32_t slot = c % kRing;
@@ -311,8 +310,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (g.nk == 0) break;
       const int32_t blocks = (g.b1 - g.b0) * (g.tb1 - g.tb0);
       const int32_t key = g.key0 + 128 * wg + row;
-      // the products of the segment before have read their K (a warpgroup without a tile waits too: it must not
-      // be more than one phase behind)
+      // the products of the segment before have read their K.  A warpgroup without a tile waits too, and says so in
+      // kready: were this segment's products complete before it has seen the last one's, it would take the phase of
+      // kdone for the one to come and wait on.
       if (s > 0 && !(ok = warp_wait(&sm.kdone, (s - 1) & 1u))) break;
       if (wg < g.nk) {
         // ---- K to tensor memory
@@ -330,9 +330,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tmem_wait_st();
         fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.kready[wg]);
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.kready[wg]);
       c += g.nk + blocks;
       float *dst = a.sig_sum + ((static_cast<int64_t>(a.layer0) + g.li) * a.R * a.cap + static_cast<int64_t>(g.r) * a.cap + key) * a.Hq + g.h * G;
       const bool there = key < g.ctx + g.n, held = key < g.ctx;

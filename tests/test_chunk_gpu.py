@@ -30,6 +30,11 @@ SHAPES = {
     "many of two row tiles": dict(Hq=16, Hkv=4, B=32, ctx=[0, 100, 2000], new=[700, 300, 500], fused=True),
     "one and two row tiles mixed": dict(Hq=16, Hkv=4, B=64, ctx=[211 * i % 1500 for i in range(40)],
                                         new=[(1, 33, 70, 5, 64)[i % 5] for i in range(40)]),
+    # significance: one key tile and two in turn, few blocks of rows in each, several a block of the launch
+    "short items of large groups": dict(Hq=64, Hkv=1, B=128, ctx=[0 if i % 3 == 0 else 83 * i % 300 for i in range(70)],
+                                        new=[1 + i % 2 for i in range(70)], L=3, n_layers=3),
+    "short items of the largest group": dict(Hq=128, Hkv=1, B=32, ctx=[0 if i % 5 == 0 else 131 * i % 301 for i in range(70)],
+                                             new=[i % 6 for i in range(70)]),
     "none new": dict(Hq=2, Hkv=1, B=16, ctx=[5, 300, 17], new=[0, 2, 0]),
 }
 

@@ -30,7 +30,7 @@
 // softmaxes over keys of their own, joined at the end (one warp alone would
 // take 3000 cycles a tile: 64 single tokens 314 us, then 273).
 //
-// The reference m of a row is the first tile's maximum, rounded up to a whole
+// The reference m of a row is the maximum of its first 32 columns, rounded up to a whole
 // number (log2 units), and moves only when the sum of a tile's weights (of 32
 // columns of it in the careful body) passes 2^13: weights and outputs in
 // progress have fp32's exponent, so nothing is lost by a reference that is not

@@ -24,7 +24,7 @@
 //
 // Measured (of 1951.6 TFLOP/s of bf16 products): 4 requests, 1024 tokens each
 // after 8192, 32 heads over 8 (0.292 TFLOP) 259 us, 58%; 16 requests of 0 to 333
-// tokens after 0 to 5001, 28 heads over 4 (49.3 GFLOP) 108 us, 23%; 16 tokens
+// tokens after 0 to 5001, 28 heads over 4 (49.3 GFLOP) 109 to 113 us, 23%; 16 tokens
 // after 512 18 us.  Bound by the sum warps: the exponentials' unit, the
 // products and the instructions' issue are each at 43 to 46% of their rates, and
 // the three buffers let a warpgroup run at most two blocks ahead.  Sixteen sum

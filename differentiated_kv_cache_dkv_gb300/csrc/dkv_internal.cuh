@@ -476,8 +476,9 @@ constexpr int32_t kEvictKeys = 40960;    // of them, those whose keys do too
 
 struct EvictWsHeader {
   uint64_t tail;   // the free list's tail before the call
-  int32_t err;     // first error of the plans, in no order; nothing is changed then
-  int32_t pad[13];
+  int64_t freed;   // pages that the call appends there
+  int32_t err;     // the lowest unit's error; nothing is changed then
+  int32_t pad[11];
 };
 
 // What the plan leaves of a unit (keep < 0: the unit stays as it is).

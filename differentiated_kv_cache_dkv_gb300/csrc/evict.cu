@@ -13,10 +13,11 @@
 //     Leaves the survivors' counts, the slots that stay and the evicted
 //     positions as bits.
 //   k_evict_scan   one block: freed pages of the units before each (prefix
-//     sum), the first error, the tail.  After an error nothing is changed.
-//   k_evict_apply  a block per unit: prefix counts over the slots that stay
-//     give every mover its hole; the moves, a group of lanes each; the cleared
-//     slots, the rows of the evicted, the tables and the ring.
+//     sum), the first error.  After an error nothing is changed.
+//   k_evict_apply  a block for 4096 positions of a unit: prefix counts over the
+//     slots that stay give every mover its hole; the moves, a group of lanes
+//     each; the cleared slots, the rows of the evicted, the tables, the ring
+//     and its tail.
 //
 // Floor: the significance (4 Hq bytes a position), slots and classes, and the
 // moved tokens' bytes.  What bounds it is latency: a unit's passes follow one
@@ -359,8 +360,8 @@ __global__ void __launch_bounds__(kScanThreads) k_evict_scan(const __grid_consta
       err = DKV_E_INTERNAL;
     a.ws->err = err;
     a.ws->tail = tail;
+    a.ws->freed = total;
     if (err) set_error(a.status, err);
-    else a.cursors[1] = tail + total;
   }
 }
 
@@ -440,6 +441,8 @@ __global__ void __launch_bounds__(kApplyThreads, 5) k_evict_apply(const __grid_c
   __shared__ int32_t wsum[kApplyThreads / 32];
   __shared__ int32_t last_s;
   if (a.ws->err) return;
+  // every block starts from the workspace's tail; the ring's own moves in the launch that fills it
+  if (blockIdx.x == 0 && threadIdx.x == 0) a.cursors[1] = a.ws->tail + static_cast<uint64_t>(a.ws->freed);
   const int32_t u = blockIdx.x / slices, slice = blockIdx.x - u * slices, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const EvictUnit un = a.unit[u];
   if (un.keep_hi < 0) return;
@@ -602,15 +605,21 @@ cudaError_t launch_after(void (*k)(P...), unsigned grid, int threads, size_t sme
 
 }  // namespace
 
+// Dynamic shared memory of the apply and of the plan kernel.
+static constexpr size_t apply_bytes(int32_t cap) { return 8 * static_cast<size_t>(cap / 32 + 2); }
+static constexpr size_t plan_bytes(int32_t cap) {
+  return apply_bytes(cap) + 4 * static_cast<size_t>(cap / 32 + 1) + (cap > kEvictKeys ? 0 : 4 * static_cast<size_t>(cap));
+}
+
 cudaError_t launch_evict(const EvictArgs &a, cudaStream_t s) {
-  const size_t maps = 8 * static_cast<size_t>(a.cap / 32 + 2);
-  const size_t plan = maps + 4 * static_cast<size_t>(a.cap / 32 + 1) + (a.cap > kEvictKeys ? 0 : 4 * static_cast<size_t>(a.cap));
+  const size_t maps = apply_bytes(a.cap), plan = plan_bytes(a.cap);
   // blocks a unit: one for 4096 positions
   const int32_t slices = static_cast<int32_t>(std::min<int64_t>((a.cap + 4095) / 4096, std::max<int64_t>(1, INT32_MAX / a.U)));
-  if (cudaError_t e = cudaFuncSetAttribute(k_evict_plan, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(plan)))
-    return e;
-  if (cudaError_t e = cudaFuncSetAttribute(k_evict_apply, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(maps)))
-    return e;
+  // the limits are the kernels', not the call's: always what any cap needs, as another thread's call may come between
+  constexpr int most_plan = static_cast<int>(std::max(plan_bytes(kEvictKeys), plan_bytes(kEvictCap)));
+  constexpr int most_apply = static_cast<int>(apply_bytes(kEvictCap));
+  if (cudaError_t e = cudaFuncSetAttribute(k_evict_plan, cudaFuncAttributeMaxDynamicSharedMemorySize, most_plan)) return e;
+  if (cudaError_t e = cudaFuncSetAttribute(k_evict_apply, cudaFuncAttributeMaxDynamicSharedMemorySize, most_apply)) return e;
   k_evict_plan<<<static_cast<unsigned>(a.U), kPlanThreads, plan, s>>>(a);
   if (cudaError_t e = cudaGetLastError()) return e;
   if (cudaError_t e = launch_after(k_evict_scan, 1, kScanThreads, 0, s, a)) return e;

@@ -317,6 +317,8 @@ constexpr int kAttendMaxG = 8;
 // registers a lane holds: one block per SM).
 __host__ __device__ constexpr int attend_warps(int G) { return G <= 4 ? 6 : 8; }
 __host__ __device__ constexpr int attend_blocks_per_sm(int G) { return G <= 4 ? 2 : 1; }
+// Most dynamic shared memory of an attention block: with the kernel's own (4.6 or 8.6 KB) it stays below 227 KB.
+__host__ __device__ constexpr int attend_bytes(int G) { return (G <= 4 ? 220 : 218) * 1024; }
 
 struct AttnArgs {
   int32_t L, R, Hq, Hkv, G, P, pmax, cap, layer0, n_layers;

@@ -324,7 +324,7 @@ bool valid_evict(const dkv_evict_batch *b, const dkv_pool *pool, const dkv_table
 int32_t apply_heads(int32_t Hkv, int32_t words, int32_t pmax) {
   int32_t hpc = Hkv < dkv::kMaxApplyWarps ? Hkv : dkv::kMaxApplyWarps;
   while (hpc > 1 && dkv::apply_smem(hpc, words, pmax) > 96 * 1024) hpc = (hpc + 1) / 2;
-  return dkv::apply_smem(hpc, words, pmax) <= 200 * 1024 ? hpc : 0;
+  return dkv::apply_smem(hpc, words, pmax) <= dkv::kApplyBytes ? hpc : 0;
 }
 
 }  // namespace

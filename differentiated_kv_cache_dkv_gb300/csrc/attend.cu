@@ -893,9 +893,10 @@ __global__ void __launch_bounds__(32 * attend_warps(4 * NT), attend_blocks_per_s
 
 template <int NT, int SC>
 cudaError_t launch_nt(const AttnArgs &a, int32_t S, size_t smem, cudaStream_t s) {
+  // the limit is the kernel's, not the call's: always the largest, as another thread's call may come between
   if (smem > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(k_attend<NT, SC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(smem));
+                                               attend_bytes(4 * NT));
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};

@@ -619,8 +619,9 @@ cudaError_t launch_classify(const CompactArgs &a, int grid, int sms, cudaStream_
   {
     const size_t smem = classify_smem(a.Hq, a.Hkv);
     const bool vec = (a.Hq % 4) == 0;
+    // the limit is the kernel's, not the call's: always the largest, as another thread's call may come between
     if (smem > 48 * 1024) {
-      const int limit = static_cast<int>(smem);
+      const int limit = static_cast<int>(classify_smem(kMaxHq, kMaxHq));
       cudaError_t e = vec ? cudaFuncSetAttribute(k_classify<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, limit)
                           : cudaFuncSetAttribute(k_classify<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, limit);
       if (e != cudaSuccess) return e;

@@ -1368,8 +1368,9 @@ cudaError_t launch_dscan(const DecodeArgs &a, int32_t npart, cudaStream_t s) {
 cudaError_t launch_apply(const DecodeArgs &a, int32_t hpc, int32_t words, cudaStream_t s) {
   const size_t smem = apply_smem(hpc, words, a.pmax);
   void (*kern)(DecodeArgs, int32_t, int32_t) = a.pg.vh == 2 ? k_apply<1> : (a.pg.kh == 4 ? k_apply<2> : k_apply<0>);
+  // the limit is the kernel's, not the call's: always the largest, as another thread's call may come between
   if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kApplyBytes);
     if (e != cudaSuccess) return e;
   }
   const dim3 grid((a.Hkv + hpc - 1) / hpc, a.R, a.L);

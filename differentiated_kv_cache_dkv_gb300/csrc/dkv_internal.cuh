@@ -212,6 +212,7 @@ inline int32_t reclass_chunk(int64_t lr, int32_t cap, int sms) {
   return c;
 }
 constexpr int kMaxApplyWarps = 8;     // units (KV heads) per apply block, one warp each
+constexpr int kApplyBytes = 200 * 1024;  // most dynamic shared memory of an apply block
 
 struct DecWsHeader {
   int32_t err;       // first device-side error of this call (0 = none)

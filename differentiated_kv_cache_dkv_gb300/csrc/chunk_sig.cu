@@ -314,6 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // kready: were this segment's products complete before it has seen the last one's, it would take the phase of
       // kdone for the one to come and wait on.
       if (s > 0 && !(ok = warp_wait(&sm.kdone, (s - 1) & 1u))) break;
+      fence_after();
       if (wg < g.nk) {
         // ---- K to tensor memory
         const int32_t kc = c + wg;

@@ -229,6 +229,12 @@ def _p(t) -> int | None:
     return None if t is None else t.data_ptr()
 
 
+def _holding(batch, *tensors):
+    """The batch with references to the tensors whose addresses it has: their memory is theirs as long as it lives."""
+    batch.tensors = tensors
+    return batch
+
+
 class DevicePool:
     """Pool state in device memory (torch tensors owned by this object)."""
 
@@ -288,9 +294,9 @@ class DeviceTables:
 
 
 def make_batch(inp: dict, classes: torch.Tensor, max_len: int, unit_base: int = 0) -> dkv_batch:
-    return dkv_batch(int(inp["L"]), int(inp["R"]), int(inp["Hq"]), int(inp["Hkv"]), 128, int(max_len),
-                     int(inp["T"]), int(unit_base), _p(inp["k"]), _p(inp["v"]), _p(inp["sig_sum"]),
-                     _p(inp["sig_cnt"]), _p(inp["lens"]), _p(classes))
+    at = (inp["k"], inp["v"], inp["sig_sum"], inp["sig_cnt"], inp["lens"], classes)
+    return _holding(dkv_batch(int(inp["L"]), int(inp["R"]), int(inp["Hq"]), int(inp["Hkv"]), 128, int(max_len),
+                              int(inp["T"]), int(unit_base), *map(_p, at)), *at)
 
 
 def dkv_workspace_size(batch: dkv_batch) -> int:
@@ -473,9 +479,10 @@ def make_extend_batch(L: int, Hkv: int, cap: int, q: torch.Tensor, new_lens: tor
     if ctx_lens.numel() != new_lens.numel():
         raise ValueError("new_lens and ctx_lens name the same requests")
     n_layers, T, Hq = int(q.shape[0]), int(q.shape[1]), int(q.shape[2])
-    return dkv_extend_batch(int(L), int(new_lens.numel()), Hq, int(Hkv), int(cap), int(layer0), n_layers,
-                            int(max_new), T, _p(q), _p(k_new), _p(v_new), _p(new_lens), _p(ctx_lens), float(scale),
-                            _p(out), _p(lse))
+    return _holding(dkv_extend_batch(int(L), int(new_lens.numel()), Hq, int(Hkv), int(cap), int(layer0), n_layers,
+                                     int(max_new), T, _p(q), _p(k_new), _p(v_new), _p(new_lens), _p(ctx_lens),
+                                     float(scale), _p(out), _p(lse)),
+                    q, k_new, v_new, new_lens, ctx_lens, out, lse)
 
 
 def dkv_extend_workspace_size(batch: dkv_extend_batch, pool: DevicePool, tables) -> int:
@@ -526,12 +533,13 @@ def make_fork_batch(L: int, R: int, Hq: int, Hkv: int, cap: int, src: torch.Tens
                     sig_cnt: torch.Tensor | None = None, unit_base: int = 0) -> dkv_fork_batch:
     if src.numel() != dst.numel():
         raise ValueError("src and dst name the same number of requests")
-    return dkv_fork_batch(int(L), int(R), int(Hq), int(Hkv), int(cap), int(src.numel()), int(unit_base), _p(src),
-                          _p(dst), _p(ctx_lens), _p(classes), _p(slot_of), _p(sig_sum), _p(sig_cnt))
+    at = (src, dst, ctx_lens, classes, slot_of, sig_sum, sig_cnt)
+    return _holding(dkv_fork_batch(int(L), int(R), int(Hq), int(Hkv), int(cap), int(src.numel()), int(unit_base),
+                                   *map(_p, at)), *at)
 
 
 def make_release_batch(L: int, R: int, Hkv: int, reqs: torch.Tensor, unit_base: int = 0) -> dkv_release_batch:
-    return dkv_release_batch(int(L), int(R), int(Hkv), int(reqs.numel()), int(unit_base), _p(reqs))
+    return _holding(dkv_release_batch(int(L), int(R), int(Hkv), int(reqs.numel()), int(unit_base), _p(reqs)), reqs)
 
 
 def dkv_fork(batch: dkv_fork_batch, pool: DevicePool, tables, workspace: torch.Tensor, stream=None) -> None:
@@ -631,9 +639,10 @@ def make_chunk_batch(Hkv: int, cap: int, q: torch.Tensor, new_lens: torch.Tensor
     kv_stride = 0 if k_new is None else _token_stride(k_new, "k_new")
     if v_new is not None and _token_stride(v_new, "v_new") != kv_stride:
         raise ValueError("k_new and v_new: tokens at the same distances are wanted")
-    return dkv_chunk_batch(int(L if L is not None else layer0 + n_layers), R, Hq, int(Hkv), int(cap), int(layer0),
-                           n_layers, int(max_new), T, _token_stride(q, "q"), kv_stride, _p(q), _p(k_new), _p(v_new),
-                           _p(new_lens), _p(ctx_lens), float(scale), _p(out), _p(lse))
+    return _holding(dkv_chunk_batch(int(L if L is not None else layer0 + n_layers), R, Hq, int(Hkv), int(cap),
+                                    int(layer0), n_layers, int(max_new), T, _token_stride(q, "q"), kv_stride, _p(q),
+                                    _p(k_new), _p(v_new), _p(new_lens), _p(ctx_lens), float(scale), _p(out), _p(lse)),
+                    q, k_new, v_new, new_lens, ctx_lens, out, lse)
 
 
 def _chunk_pages(batch: dkv_chunk_batch, pages: ChunkPages) -> dkv_chunk_pages:
@@ -686,8 +695,9 @@ def make_evict_batch(L: int, R: int, Hq: int, Hkv: int, cap: int, budgets: torch
     _want(sig_cnt, "sig_cnt", torch.int32, (int(R) * int(cap),), sig_sum)
     _want(classes, "classes", torch.uint8, (rows * int(Hkv),), sig_sum)
     _want(slot_of, "slot_of", torch.int32, (rows * int(Hkv),), sig_sum)
-    return dkv_evict_batch(int(L), int(R), int(Hq), int(Hkv), int(cap), int(sinks), int(window), 0, int(unit_base),
-                           _p(budgets), _p(ctx_lens), _p(sig_sum), _p(sig_cnt), _p(classes), _p(slot_of))
+    at = (budgets, ctx_lens, sig_sum, sig_cnt, classes, slot_of)
+    return _holding(dkv_evict_batch(int(L), int(R), int(Hq), int(Hkv), int(cap), int(sinks), int(window), 0,
+                                    int(unit_base), *map(_p, at)), *at)
 
 
 def dkv_evict_workspace_size(batch: dkv_evict_batch, pool: DevicePool, tables) -> int:
@@ -743,9 +753,9 @@ class Decoder:
 
     def batch(self, d: dict) -> dkv_decode_batch:
         g = d.get
-        return dkv_decode_batch(self.L, self.R, self.Hq, self.Hkv, 128, self.cap, 0, _p(g("k_new")), _p(g("v_new")),
-                                _p(g("sig_sum")), _p(g("sig_cnt")), _p(g("ctx_lens")), _p(g("new_lens")),
-                                _p(self.classes), _p(self.slot_of), self.window, self.mode)
+        at = (g("k_new"), g("v_new"), g("sig_sum"), g("sig_cnt"), g("ctx_lens"), g("new_lens"), self.classes, self.slot_of)
+        return _holding(dkv_decode_batch(self.L, self.R, self.Hq, self.Hkv, 128, self.cap, 0, *map(_p, at), self.window,
+                                         self.mode), *at)
 
     def prefill_layer(self, inp: dict, layer: int, max_len: int, alpha_h: float, alpha_l: float,
                       stream=None) -> None:

@@ -762,11 +762,11 @@ class Decoder:
         """dkv_compact of one layer's prefill inputs (L = 1) into this pool,
         units of layer `layer` (unit_base and table rows offset)."""
         T = int(inp["T"])
-        cls = torch.empty(max(T * self.Hkv, 1), dtype=torch.uint8, device=self.device)
+        cls = self._scratch(max(T * self.Hkv, 1), stream)
         b = make_batch(inp, cls, max_len, unit_base=layer * self.R * self.Hkv)
         need = dkv_workspace_size(b)
         if self._pre_ws is None or self._pre_ws.numel() < need:
-            self._pre_ws = torch.empty(need, dtype=torch.uint8, device=self.device)
+            self._pre_ws = self._scratch(need, stream)
         dkv_compact(b, alpha_h, alpha_l, self.pool, _TableView(self.tables, layer * self.R * self.Hkv),
                     self._pre_ws, stream=stream)
 

@@ -110,6 +110,12 @@ struct ChunkLayout {
   int32_t tpt, tpi, rows;  // tokens a row tile, an item; rows of a partial result
 };
 
+// Items a unit of all requests, at most.
+__host__ __device__ __forceinline__ int64_t items_most(const ChunkArgs &a, int32_t tpi) { return a.T / tpi + a.R + 1; }
+
+// (checked build) rows of the outputs
+__device__ __forceinline__ int64_t outs_of(const ChunkArgs &a) { return static_cast<int64_t>(a.n_layers) * a.T * a.Hq; }
+
 __host__ ChunkLayout chunk_layout(const ChunkArgs &a) {
   ChunkLayout w{};
   w.tpt = 128 / a.G;
@@ -117,7 +123,7 @@ __host__ ChunkLayout chunk_layout(const ChunkArgs &a) {
   w.rows = std::min(w.tpi, a.max_new) * a.G;
   size_t x = align256(sizeof(PlanHeader));
   w.req = x; x = align256(x + sizeof(ReqPlan) * static_cast<size_t>(a.R));
-  w.pre = x; x = align256(x + 4 * (static_cast<size_t>(a.T / w.tpi) + a.R + 1));
+  w.pre = x; x = align256(x + 4 * static_cast<size_t>(items_most(a, w.tpi)));
   w.cut = x; x = align256(x + 8 * (kBlocks + 1));
   w.item = x; x = align256(x + sizeof(CutItem) * kBlocks);
   w.ml = x;  x = align256(x + sizeof(float2) * 2 * kBlocks * static_cast<size_t>(w.rows));
@@ -229,7 +235,7 @@ __device__ void plan(const ChunkArgs &a, const PlanPtrs &p, int32_t tpi, int32_t
         const int32_t y = __shfl_up_sync(kFull, incl, o);
         if (lane >= o) incl += y;
       }
-      if (j < q.items) pre[q.rt0 + j] = sum + incl - t;
+      if (j < q.items && in_range(q.rt0 + j, items_most(a, tpi), a.status)) pre[q.rt0 + j] = sum + incl - t;
       sum += __shfl_sync(kFull, incl, 31);
     }
     if (lane == 0) req[r].tiles = sum;
@@ -247,7 +253,7 @@ __device__ void plan(const ChunkArgs &a, const PlanPtrs &p, int32_t tpi, int32_t
   __syncthreads();
   if (req == req_sm)
     for (int32_t r = tid; r < a.R; r += kAppendThreads) p.req[r] = req[r];
-  if (pre == pre_sm)
+  if (pre == pre_sm && in_range(rts, items_most(a, tpi) + 1, a.status))
     for (int32_t i = tid; i < static_cast<int32_t>(rts); i += kAppendThreads) p.pre[i] = pre[i];
   // waves of whole items, while no block gets more than the mean
   const int64_t items = rts * U1, target = (W + grid - 1) / grid;
@@ -329,10 +335,12 @@ __global__ void __launch_bounds__(kAppendThreads)
   bool bad = false;
   for (int32_t i = threadIdx.x; i < n * units; i += kAppendThreads) {
     const int32_t t = i / units, c = i - t * units, pos = pos_s[t];
+    if (!in_range(req_s[t], a.R, a.status) || !in_range(pos, a.cap, a.status) || !in_range(t0 + t, a.T, a.status)) continue;
     const int32_t id = chunk_page(a, req_s[t], pos / a.B);
     if (id < 0) continue;
     const int64_t from = (static_cast<int64_t>(li) * a.T + t0 + t) * a.kv_stride + c * 8;
     const int64_t to = (((static_cast<int64_t>(a.layer0) + li) * a.F + id) * a.B + pos % a.B) * (a.Hkv * int64_t{128}) + c * 8;
+    if (!in_range(to, static_cast<int64_t>(a.L) * a.F * a.B * a.Hkv * 128 - 7, a.status)) continue;
     uint4 x[2];
     x[0] = *reinterpret_cast<const uint4 *>(a.k_new + from);
     x[1] = *reinterpret_cast<const uint4 *>(a.v_new + from);
@@ -431,6 +439,9 @@ __device__ __forceinline__ Seg next_seg(const ChunkArgs &a, const PlanPtrs &p, i
   g.n = min(tpi, q.n - g.i0);
   g.tok = q.tok0 + g.i0;
   g.ctx = q.ctx;
+  if (!in_range(g.li, a.n_layers, a.status) || !in_range(g.tok, a.T + 1 - g.n, a.status) ||
+      !in_range(g.slot + 1, 2 * grid + 1, a.status) || !in_range(g.ctx, a.cap + 1 - g.i0 - g.n, a.status))
+    return Seg{};
   if (first && (threadIdx.x & 31) == 0) {
     cut.li = g.li;
     cut.h = g.h;
@@ -597,7 +608,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       auto copy_tile = [&](int32_t t, int32_t id) {
         const uint32_t boxes = __popc(__ballot_sync(kFull, id >= 0));
-        const int32_t at = static_cast<int32_t>((base + id) * a.B);
+        int32_t at = static_cast<int32_t>((base + id) * a.B);
+        if (id >= 0 && !in_range(at, static_cast<int64_t>(a.L) * a.F * a.B + 1 - a.B, a.status)) at = 0;
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
           const int32_t slot = c % kRing;
@@ -967,7 +979,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int e = 0; e < 8; ++e) x[e] += o[16 * e] * f;
           }
           const int64_t at = (static_cast<int64_t>(g.li) * a.T + g.tok + jr / G) * a.Hq + g.h * G + jr % G;
-          if (g.slot < 0) {
+          if (!in_range(at, outs_of(a), a.status) || !in_range(jr, rows, a.status)) {
+          } else if (g.slot < 0) {
             const float inv = 1.0f / l;
             *reinterpret_cast<uint4 *>(a.out + at * 128 + col) =
                 make_uint4(bf16x2_rn(x[0] * inv, x[1] * inv), bf16x2_rn(x[2] * inv, x[3] * inv),
@@ -1046,10 +1059,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     y[e] = make_uint4(bf16x2_rn(z[0], z[1]), bf16x2_rn(z[2], z[3]), bf16x2_rn(z[4], z[5]), bf16x2_rn(z[6], z[7]));
                   }
                   transpose2(y[0], y[1]);  // two lanes write 32 bytes of a row
-                  if (to0 >= 0) *reinterpret_cast<uint4 *>(dst0 + 32 * c + 16 * k) = y[0];
-                  if (to1 >= 0) *reinterpret_cast<uint4 *>(dst1 + 32 * c + 16 * k) = y[1];
+                  if (to0 >= 0 && in_range(to0, outs_of(a), a.status)) *reinterpret_cast<uint4 *>(dst0 + 32 * c + 16 * k) = y[0];
+                  if (to1 >= 0 && in_range(to1, outs_of(a), a.status)) *reinterpret_cast<uint4 *>(dst1 + 32 * c + 16 * k) = y[1];
                 }
-              } else if (live) {
+              } else if (live && in_range(prow, rows, a.status)) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                   p.o[(static_cast<int64_t>(g.slot) * 32 + 8 * c + e) * rows + prow] =
@@ -1058,8 +1071,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           if (join && wg == 1) sm.ml[row] = make_float2(m, l);
-          else if (live && g.slot >= 0) p.ml[static_cast<int64_t>(g.slot) * rows + prow] = make_float2(m, l);
-          else if (live && a.lse) a.lse[at] = (m + log2f(l)) * 0.693147180559945309f;
+          else if (live && g.slot >= 0 && in_range(prow, rows, a.status)) p.ml[static_cast<int64_t>(g.slot) * rows + prow] = make_float2(m, l);
+          else if (live && g.slot < 0 && a.lse && in_range(at, outs_of(a), a.status)) a.lse[at] = (m + log2f(l)) * 0.693147180559945309f;
         }
         fence_before();
         if (join) fence_async();  // the next Q is copied where these reads (and the other's writes) were
@@ -1107,7 +1120,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
       const int64_t x0 = b < grid ? p.cut[b] : g.end, x1 = b < grid ? p.cut[b + 1] : g.end;
       const bool has = x1 > x0 && x0 < g.end;
       const uint32_t m = __ballot_sync(kFull, has);
-      if (has) slots[parts + __popc(m & ((1u << lane) - 1u))] = 2 * b;
+      if (has && in_range(parts + __popc(m & ((1u << lane) - 1u)), kBlocks, a.status)) slots[parts + __popc(m & ((1u << lane) - 1u))] = 2 * b;
       parts += __popc(m);
       if (__any_sync(kFull, x0 >= g.end)) break;
     }
@@ -1142,6 +1155,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
           for (int k = 0; k < nk; ++k) {
             y[k][i].x = -INFINITY;
             if (!is || row_of(k) >= nr) continue;
+            if (!in_range(slot, 2 * grid, a.status) || !in_range(row_of(k), rows, a.status)) continue;
             y[k][i] = __ldcg(p.ml + slot * rows + row_of(k));
             u[k][i] = __ldcg(p.o + (slot * 32 + unit_of(k)) * rows + row_of(k));
             v[k][i] = __ldcg(p.o + (slot * 32 + unit_of(k) + 1) * rows + row_of(k));
@@ -1180,6 +1194,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
         if (jr >= nr) continue;
         const float inv = 1.0f / l[k];
         const int64_t at = (static_cast<int64_t>(g.li) * a.T + g.tok + jr / G) * a.Hq + g.h * G + jr % G;
+        if (!in_range(at, outs_of(a), a.status)) continue;
         *reinterpret_cast<uint4 *>(a.out + at * 128 + 4 * unit) =
             make_uint4(bf16x2_rn(x[k][0] * inv, x[k][1] * inv), bf16x2_rn(x[k][2] * inv, x[k][3] * inv),
                        bf16x2_rn(x[k][4] * inv, x[k][5] * inv), bf16x2_rn(x[k][6] * inv, x[k][7] * inv));

@@ -71,6 +71,9 @@ struct __align__(1024) Smem {
 constexpr size_t kSmemBytes = sizeof(Smem) + 1024;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 
+// (checked build) entries of sig_sum
+__device__ __forceinline__ int64_t sums_of(const ChunkArgs &a) { return static_cast<int64_t>(a.L) * a.R * a.cap * a.Hq; }
+
 // Requests by the length of their chunks, the longest first (ties: the first
 // one), when there are not more than the order has room for.
 __device__ __forceinline__ void sort_requests(const ChunkArgs &a, Smem &sm) {
@@ -218,9 +221,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint64_t *bar = &sm.full[c % kRing];
         if (lane == 0) mbar_expect_tx(bar, boxes * a.B * 128);
         __syncwarp();
+        int32_t at = static_cast<int32_t>((base + id) * a.B);
+        if (id >= 0 && !in_range(at, static_cast<int64_t>(a.L) * a.F * a.B + 1 - a.B, a.status)) at = 0;
         if (id >= 0)
-          copy_box(sm.ring[c % kRing] + (lane & 1) * kBox + (lane >> 1) * a.B * 128, &kmap, (lane & 1) * 64, g.h,
-                   static_cast<int32_t>((base + id) * a.B), bar);
+          copy_box(sm.ring[c % kRing] + (lane & 1) * kBox + (lane >> 1) * a.B * 128, &kmap, (lane & 1) * 64, g.h, at, bar);
         ++c;
       }
       for (int32_t b = g.b0; b < g.b1 && ok; ++b)
@@ -231,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 4; ++i) {
             const int32_t col = lane + 32 * i, hq = b * hb + col / nb, t = col % nb;
             e[i] = -INFINITY;
-            if (hq < G && tb * nb + t < g.n) e[i] = __ldg(a.lse + (static_cast<int64_t>(tok0) + t) * a.Hq + g.h * G + hq);
+            if (hq < G && tb * nb + t < g.n && in_range(static_cast<int64_t>(tok0) + t, a.n_layers * a.T, a.status)) e[i] = __ldg(a.lse + (static_cast<int64_t>(tok0) + t) * a.Hq + g.h * G + hq);
           }
           if (!slot_free()) break;
           if (lane == 0) {
@@ -372,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               return f2_add(t2[0], t2[1]);
             };
             auto flush = [&](int32_t hq) {  // a head's last columns are in
-              if (there && hq < G) {
+              if (there && hq < G && in_range(key, a.cap, a.status) && in_range(dst + hq - a.sig_sum, sums_of(a), a.status)) {
                 if (held) red_add(dst + hq, acc);
                 else dst[hq] = acc;
               }

@@ -91,6 +91,9 @@ __device__ __forceinline__ Place place_of(const EvictArgs &a, int32_t u) {
   return p;
 }
 
+// Positions of all layers and requests.
+__device__ __forceinline__ int64_t rows_of(const EvictArgs &a) { return static_cast<int64_t>(a.L) * a.R * a.cap; }
+
 // Words of the slot bitmaps: the high list's, then the low list's.
 __device__ __forceinline__ int32_t words_of(int32_t n) { return (n + 31) >> 5; }
 
@@ -110,6 +113,10 @@ __global__ void __launch_bounds__(kPlanThreads, 3) k_evict_plan(const __grid_con
   else if (n_hi < 0 || n_lo < 0 || static_cast<int64_t>(n_hi) + n_lo > ctx || hd.z != (n_hi + a.P - 1) / a.P ||
            hd.w != (n_lo + 2 * a.P - 1) / (2 * a.P) || hd.z + hd.w > a.pmax)
     err = DKV_E_INTERNAL;
+  if constexpr (kChecked) {  // words of the bitmaps, rows of the unit
+    if (!err && !(in_range(words_of(n_hi) + words_of(n_lo), a.cap / 32 + 3, a.status) && in_range(pl.row + ctx, rows_of(a) + 1, a.status)))
+      err = DKV_E_INTERNAL;
+  }
   if (err || budget < 0 || n_hi + n_lo <= budget) {
     if (tid == 0) a.unit[u] = EvictUnit{-1, -1, 0, err};
     return;
@@ -368,14 +375,19 @@ __global__ void __launch_bounds__(kScanThreads) k_evict_scan(const __grid_consta
 // One list of a unit, as a block sees it: its pages' ids, slots a page.
 struct List {
   const int32_t *ids;
-  int32_t per, ku, vu;  // slots a page; 16-byte units of K and of V a slot
+  int32_t pages, per, ku, vu;  // pages; slots a page; 16-byte units of K and of V a slot
   float inv;
 };
 // Where a slot lies: page id and slot of the page.
-__device__ __forceinline__ int2 slot_at(const List &l, int32_t s) {
+__device__ __forceinline__ int2 slot_at(const EvictArgs &a, const List &l, int32_t s) {
   // s below 2^18: the quotient is exact, the product's error is below half of 1 / per
   const int32_t j = static_cast<int32_t>((static_cast<float>(s) + 0.5f) * l.inv);
+  if (!in_range(j, l.pages, a.status)) return make_int2(-1, 0);
   return make_int2(l.ids[j], s - j * l.per);
+}
+// (checked build) a place that slot_at gave lies in the pool
+__device__ __forceinline__ bool in_pool(const EvictArgs &a, const List &l, int2 s) {
+  return in_range(s.x, a.F, a.status) && in_range(s.y, l.per, a.status);
 }
 
 // What lane j of a slot's lanes carries: a 16-byte unit of K or V, the
@@ -407,7 +419,9 @@ __device__ __forceinline__ void move_slots(const EvictArgs &a, const List &l, co
     uint4 x[kEach];
 #pragma unroll
     for (int e = 0; e < kEach; ++e) {
-      const uint8_t *f = at(src[min(m0 + e * kGroups, n - 1)]);
+      const int2 from = src[min(m0 + e * kGroups, n - 1)];
+      if (!in_pool(a, l, from)) continue;
+      const uint8_t *f = at(from);
       if (part.bytes == 16) x[e] = __ldcs(reinterpret_cast<const uint4 *>(f));
       else if (part.bytes == 8) *reinterpret_cast<uint2 *>(&x[e]) = *reinterpret_cast<const uint2 *>(f);
       else x[e].x = *reinterpret_cast<const uint32_t *>(f);
@@ -416,6 +430,7 @@ __device__ __forceinline__ void move_slots(const EvictArgs &a, const List &l, co
     for (int e = 0; e < kEach; ++e) {
       const int32_t m = m0 + e * kGroups;
       if (m >= n) break;
+      if (!in_pool(a, l, dst[m])) continue;
       uint8_t *t = at(dst[m]);
       if (part.bytes == 16) {
         *reinterpret_cast<uint4 *>(t) = x[e];
@@ -450,6 +465,7 @@ __global__ void __launch_bounds__(kApplyThreads, 5) k_evict_apply(const __grid_c
   const int32_t ctx = __ldg(a.ctx_lens + pl.r);
   const int4 hd = *reinterpret_cast<const int4 *>(a.unit_hdr + 4 * static_cast<int64_t>(u));
   const int32_t wh = words_of(hd.x), words = wh + words_of(hd.y);
+  if (!in_range(words, a.cap / 32 + 3, a.status)) return;
   uint32_t *stay = dyn, *rank = dyn + words;  // slots that stay, and how many of them before a word
   const uint32_t *stay_in = a.stay + static_cast<int64_t>(u) * (a.cap / 32 + 2);
   for (int32_t i = tid; i < words; i += kApplyThreads) stay[i] = __ldg(stay_in + i);
@@ -458,7 +474,7 @@ __global__ void __launch_bounds__(kApplyThreads, 5) k_evict_apply(const __grid_c
   int32_t *slots = a.slot_of + pl.row * a.Hkv + pl.h;
   const uint32_t *gone_pos = a.gone + static_cast<int64_t>(u) * ((a.cap + 31) / 32);
   for (int32_t p = slice * kApplyThreads + tid; p < ctx; p += slices * kApplyThreads)
-    if (__ldg(gone_pos + (p >> 5)) >> (p & 31) & 1u) {
+    if (__ldg(gone_pos + (p >> 5)) >> (p & 31) & 1u && in_range(pl.row + p, rows_of(a), a.status)) {
       cls[static_cast<int64_t>(p) * a.Hkv] = DKV_CLASS_PRUNE;
       slots[static_cast<int64_t>(p) * a.Hkv] = -1;
     }
@@ -486,7 +502,7 @@ __global__ void __launch_bounds__(kApplyThreads, 5) k_evict_apply(const __grid_c
   int32_t *row = a.fwd + static_cast<int64_t>(u) * a.pmax;
   auto list_of = [&](bool high) {
     const int32_t per = high ? a.P : 2 * a.P;
-    return List{row + (high ? 0 : hd.z), per, high ? a.pg.kh : a.pg.kh >> 1, high ? a.pg.vh : a.pg.vh >> 1,
+    return List{row + (high ? 0 : hd.z), high ? hd.z : hd.w, per, high ? a.pg.kh : a.pg.kh >> 1, high ? a.pg.vh : a.pg.vh >> 1,
                 1.0f / static_cast<float>(per)};
   };
   for (int i = 0; i < 2; ++i) {
@@ -517,12 +533,12 @@ __global__ void __launch_bounds__(kApplyThreads, 5) k_evict_apply(const __grid_c
           for (; hole; hole &= hole - 1u, ++m)
             if (m >= 0 && m < nm) {
               to_slot[m] = s0 + __ffs(hole) - 1;
-              dst[m] = slot_at(l, to_slot[m]);
+              dst[m] = slot_at(a, l, to_slot[m]);
             }
         m = before + __popc(st[w] & low) - b_keep - m0;
         if (m < nm && m + 32 > 0)
           for (; mover; mover &= mover - 1u, ++m)
-            if (m >= 0 && m < nm) src[m] = slot_at(l, s0 + __ffs(mover) - 1);
+            if (m >= 0 && m < nm) src[m] = slot_at(a, l, s0 + __ffs(mover) - 1);
       }
       __syncthreads();
       if (high) move_slots<16>(a, l, src, dst, to_slot, nm, slots, ctx);
@@ -548,7 +564,8 @@ __global__ void __launch_bounds__(kApplyThreads, 5) k_evict_apply(const __grid_c
     const int32_t end = min(n, (keep + l.per - 1) / l.per * l.per), lanes = high ? 16 : 8;
     for (int32_t k = tid; k < (end - keep) * lanes; k += kApplyThreads) {
       const LanePart part = lane_part(a, l, k % lanes);
-      const int2 at = slot_at(l, keep + k / lanes);
+      const int2 at = slot_at(a, l, keep + k / lanes);
+      if (!in_pool(a, l, at)) continue;
       uint8_t *t = a.pages + part.off + (at.x * a.pg.bytes + at.y * part.step);
       if (part.bytes == 16) *reinterpret_cast<uint4 *>(t) = make_uint4(0, 0, 0, 0);
       else if (part.bytes == 8) *reinterpret_cast<uint2 *>(t) = make_uint2(0, 0);
@@ -565,6 +582,7 @@ __global__ void __launch_bounds__(kApplyThreads, 5) k_evict_apply(const __grid_c
     const int32_t id = i < fh ? row[need_hi + i] : row[hd.z + need_lo + i - fh];
     uint64_t at = at0 + i;
     if (at >= F) at -= F;
+    if (!in_range(static_cast<int64_t>(at), a.F, a.status) || !in_range(id, a.F, a.status)) continue;
     a.free_list[at] = id;
     a.rev_unit[id] = -1;
     a.rev_idx[id] = -1;
@@ -576,14 +594,15 @@ __global__ void __launch_bounds__(kApplyThreads, 5) k_evict_apply(const __grid_c
     for (int32_t i0 = 0; i0 < need_lo; i0 += kApplyThreads) {
       const int32_t i = i0 + tid, id = i < need_lo ? row[hd.z + i] : 0;
       __syncthreads();
-      if (i < need_lo) {
+      if (i < need_lo && in_range(id, a.F, a.status) && in_range(need_hi + i, a.pmax, a.status)) {
         row[need_hi + i] = id;
         a.rev_idx[id] = need_hi + i;
       }
       __syncthreads();
     }
   }
-  for (int32_t i = need_hi + need_lo + tid; i < hd.z + hd.w; i += kApplyThreads) row[i] = -1;
+  for (int32_t i = need_hi + need_lo + tid; i < hd.z + hd.w; i += kApplyThreads)
+    if (in_range(i, a.pmax, a.status)) row[i] = -1;
   if (tid == 0)
     *reinterpret_cast<int4 *>(a.unit_hdr + 4 * static_cast<int64_t>(u)) = make_int4(un.keep_hi, un.keep_lo, need_hi, need_lo);
 }

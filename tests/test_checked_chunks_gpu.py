@@ -11,7 +11,8 @@ import pytest
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CSRC = os.path.join(ROOT, "differentiated_kv_cache_dkv_gb300", "csrc")
-TESTS = ["tests/test_chunk_gpu.py", "tests/test_chunk_segments_gpu.py", "tests/test_evict_gpu.py"]
+TESTS = ["tests/test_chunk_gpu.py", "tests/test_chunk_segments_gpu.py", "tests/test_evict_gpu.py",
+         "tests/test_evict_long_lists_gpu.py", "tests/test_chunk_weights_gpu.py"]
 
 
 @pytest.mark.parametrize("name", ["chunk.cu", "chunk_sig.cu", "evict.cu"])

@@ -75,11 +75,10 @@ constexpr int kSmemItems = 1024;
 
 // Costs are in key tiles; an item's are its key tiles' and kStart before them.
 struct PlanHeader {
-  int64_t tiles;   // cost of all items
   int64_t cut0;    // cost of the whole items that the waves take
   int32_t waves;
   int32_t ok;      // lengths valid
-  int32_t pad[10];
+  int32_t pad[12];
 };
 struct ReqPlan {
   int64_t tile0;       // cost of the requests before
@@ -169,10 +168,6 @@ __device__ __forceinline__ T block_scan(T x, T *sm, T &total) {
   return before + incl - x;
 }
 
-// An item by its number: request, unit of the request and item of that unit.
-struct ItemAt {
-  int32_t r, unit, j;
-};
 // The request of item i: the last whose first item (rt0 U1) is at most i, among those that have items.
 template <class F>
 __device__ __forceinline__ int32_t find_req(int32_t R, F first, int64_t i) {
@@ -286,7 +281,7 @@ __device__ void plan(const ChunkArgs &a, const PlanPtrs &p, int32_t tpi, int32_t
   if (tid < grid) p.cut[tid] = min(W, cut0 + b);
   if (tid == 0) {
     p.cut[grid] = W;
-    *p.hdr = PlanHeader{W, cut0, waves, 1, {}};
+    *p.hdr = PlanHeader{cut0, waves, 1, {}};
   }
 }
 

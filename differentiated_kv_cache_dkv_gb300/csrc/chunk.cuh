@@ -67,11 +67,6 @@ __device__ __forceinline__ void copy_box(void *dst, const CUtensorMap *map, int 
       : "memory");
 }
 
-// A later launch's blocks may start while the one before still runs and wait
-// here for its end.
-__device__ __forceinline__ void after_launch_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void let_next_launch_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
 // 3-D tensor map over bf16 channels of 128: extents n1 and n2 with strides s1
 // and s2 (elements), whose box is 64 channels by b1 by b2, written to shared
 // memory with the 128-byte swizzle (what lies past an extent reads as zeros).
@@ -93,22 +88,6 @@ inline cudaError_t chunk_map(CUtensorMap *map, const void *base, int64_t n1, int
                               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return res == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
-// A launch that may overlap the end of the one before it (after_launch_before).
-template <class... P, class... A>
-cudaError_t launch_after(void (*k)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, A... args) {
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t c{};
-  c.gridDim = grid;
-  c.blockDim = dim3(threads);
-  c.dynamicSmemBytes = smem;
-  c.stream = s;
-  c.attrs = &attr;
-  c.numAttrs = 1;
-  return cudaLaunchKernelEx(&c, k, static_cast<P>(args)...);
 }
 
 }  // namespace tc

@@ -20,6 +20,8 @@
 //   k_commit    forward / reverse tables, page classes, head cursor, status
 #pragma once
 
+#include <cuda_runtime.h>
+
 #include <algorithm>
 #include <cstdint>
 
@@ -529,6 +531,28 @@ struct EvictArgs {
   int64_t *off;
   uint32_t *gone, *stay, *keys;
 };
+
+// A later launch's blocks may start while the launch before still runs (all of
+// its blocks have begun then) and wait here for its end: launch latency is
+// hidden, the order kept.
+__device__ __forceinline__ void after_launch_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_launch_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// A launch that may overlap the end of the one before it (above).
+template <class... P, class... A>
+cudaError_t launch_after(void (*k)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, A... args) {
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c{};
+  c.gridDim = grid;
+  c.blockDim = dim3(threads);
+  c.dynamicSmemBytes = smem;
+  c.stream = s;
+  c.attrs = &attr;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, k, static_cast<P>(args)...);
+}
 
 }  // namespace dkv
 

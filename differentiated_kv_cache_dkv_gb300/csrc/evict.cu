@@ -46,11 +46,6 @@ constexpr int kPlanThreads = 512, kScanThreads = 1024, kApplyThreads = 256;
 constexpr int kMoves = 512;   // moves a block lists at a time
 constexpr int kIds = 1024;    // page ids of a list that a block keeps in shared memory
 
-// A later launch's blocks may start while the one before still runs and wait
-// here for its end.
-__device__ __forceinline__ void after_launch_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void let_next_launch_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
 // Order of the floats as unsigned numbers; 0 is left for "not held" and the
 // largest for the protected; a NaN is below every number.
 __device__ __forceinline__ uint32_t order_key(float x) {
@@ -605,21 +600,6 @@ __global__ void __launch_bounds__(kApplyThreads, 5) k_evict_apply(const __grid_c
     if (in_range(i, a.pmax, a.status)) row[i] = -1;
   if (tid == 0)
     *reinterpret_cast<int4 *>(a.unit_hdr + 4 * static_cast<int64_t>(u)) = make_int4(un.keep_hi, un.keep_lo, need_hi, need_lo);
-}
-
-template <class... P, class... A>
-cudaError_t launch_after(void (*k)(P...), unsigned grid, int threads, size_t smem, cudaStream_t s, A... args) {
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t c{};
-  c.gridDim = dim3(grid);
-  c.blockDim = dim3(threads);
-  c.dynamicSmemBytes = smem;
-  c.stream = s;
-  c.attrs = &attr;
-  c.numAttrs = 1;
-  return cudaLaunchKernelEx(&c, k, static_cast<P>(args)...);
 }
 
 }  // namespace

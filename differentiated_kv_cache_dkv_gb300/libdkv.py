@@ -289,6 +289,9 @@ class DeviceTables:
         self.pmax, self.fwd, self.unit_hdr = int(fwd.shape[1]), fwd, unit_hdr
         return self
 
+    def units(self) -> int:
+        return int(self.fwd.shape[0])
+
     def c(self) -> dkv_tables:
         return dkv_tables(_p(self.fwd), self.pmax, 0, _p(self.unit_hdr))
 
@@ -580,6 +583,14 @@ def _want(t: torch.Tensor | None, name: str, dtype: torch.dtype, shape: tuple, l
                          f"{like.device} is wanted")
 
 
+def _on_device_of(batch, *others) -> None:
+    """The batch's tensors (where it was made from tensors) are on the device of these."""
+    at = others[0].device
+    for t in (*getattr(batch, "tensors", ()), *others[1:]):
+        if t is not None and t.device != at:
+            raise ValueError(f"tensors of one device are wanted, not of {at} and {t.device}")
+
+
 def _token_stride(t: torch.Tensor, name: str) -> int:
     """Elements from one token's rows [H][128] to the next of a view [n_layers][T][H][128]."""
     n, T, H = int(t.shape[0]), int(t.shape[1]), int(t.shape[2])
@@ -652,6 +663,13 @@ def _chunk_pages(batch: dkv_chunk_batch, pages: ChunkPages) -> dkv_chunk_pages:
     return pages.c()
 
 
+def _evict_tables(batch: dkv_evict_batch, tables) -> dkv_tables:
+    units, there = batch.L * batch.R * batch.Hkv, tables.units()
+    if there < units:
+        raise ValueError(f"tables of {units} units are wanted, not of {there}")
+    return tables.c()
+
+
 def dkv_chunk_workspace_size(batch: dkv_chunk_batch, pages: ChunkPages) -> int:
     n = ctypes.c_size_t(0)
     pc = _chunk_pages(batch, pages)
@@ -664,6 +682,7 @@ def dkv_chunk_workspace_size(batch: dkv_chunk_batch, pages: ChunkPages) -> int:
 def dkv_chunk_attention(batch: dkv_chunk_batch, pages: ChunkPages, pool: DevicePool, workspace: torch.Tensor | None,
                         stream=None) -> None:
     """Append the chunk to its pages and attend; of the pool the status word is used."""
+    _on_device_of(batch, pages.k, pool.status, workspace)
     gc, pc = _chunk_pages(batch, pages), pool.c()
     rc = load().dkv_chunk_attention(ctypes.byref(batch), ctypes.byref(gc), ctypes.byref(pc), *_workspace(workspace),
                                     _stream(stream))
@@ -675,6 +694,7 @@ def dkv_chunk_significance(batch: dkv_chunk_batch, pages: ChunkPages, sig_sum: t
                            stream=None) -> None:
     """sig_sum fp32 [L][R * cap][Hq]."""
     _want(sig_sum, "sig_sum", torch.float32, (batch.L * batch.R * batch.cap * batch.Hq,), pages.k)
+    _on_device_of(batch, pages.k, pool.status)
     gc, pc = _chunk_pages(batch, pages), pool.c()
     rc = load().dkv_chunk_significance(ctypes.byref(batch), ctypes.byref(gc), _p(sig_sum), ctypes.byref(pc),
                                        _stream(stream))
@@ -702,7 +722,7 @@ def make_evict_batch(L: int, R: int, Hq: int, Hkv: int, cap: int, budgets: torch
 
 def dkv_evict_workspace_size(batch: dkv_evict_batch, pool: DevicePool, tables) -> int:
     n = ctypes.c_size_t(0)
-    pc, tc = pool.c(), tables.c()
+    pc, tc = pool.c(), _evict_tables(batch, tables)
     rc = load().dkv_evict_workspace_size(ctypes.byref(batch), ctypes.byref(pc), ctypes.byref(tc), ctypes.byref(n))
     if rc != DKV_OK:
         raise DkvError(rc, "dkv_evict_workspace_size")
@@ -710,7 +730,8 @@ def dkv_evict_workspace_size(batch: dkv_evict_batch, pool: DevicePool, tables) -
 
 
 def dkv_evict(batch: dkv_evict_batch, pool: DevicePool, tables, workspace: torch.Tensor, stream=None) -> None:
-    pc, tc = pool.c(), tables.c()
+    _on_device_of(batch, pool.status, workspace)
+    pc, tc = pool.c(), _evict_tables(batch, tables)
     rc = load().dkv_evict(ctypes.byref(batch), ctypes.byref(pc), ctypes.byref(tc), *_workspace(workspace),
                           _stream(stream))
     if rc != DKV_OK:
@@ -722,6 +743,9 @@ class _TableView:
 
     def __init__(self, t: DeviceTables, u0: int):
         self.t, self.u0 = t, int(u0)
+
+    def units(self) -> int:
+        return self.t.units() - self.u0
 
     def c(self) -> dkv_tables:
         return dkv_tables(_p(self.t.fwd) + 4 * self.u0 * self.t.pmax, self.t.pmax, 0,

@@ -584,9 +584,9 @@ def _want(t: torch.Tensor | None, name: str, dtype: torch.dtype, shape: tuple, l
 
 
 def _on_device_of(batch, *others) -> None:
-    """The batch's tensors (where it was made from tensors) are on the device of these."""
+    """The batch's tensors (where it was made from tensors, which lie on one device then) are on the device of these."""
     at = others[0].device
-    for t in (*getattr(batch, "tensors", ()), *others[1:]):
+    for t in (*getattr(batch, "tensors", ())[:1], *others[1:]):
         if t is not None and t.device != at:
             raise ValueError(f"tensors of one device are wanted, not of {at} and {t.device}")
 

@@ -38,6 +38,8 @@
 // add up to at most 2^15 a tile, 2^8 cap: that times the largest value has to
 // stay below 2^128.  P waits in registers until the test: the careful body then
 // starts again from S.  What a row does not see is taken out of S before.
+// With up to 16 rows every quarter's maximum is taken, and the reference moves
+// when it lies more than 8 above.
 //
 // Measured (a whole call, its append included; of 1951.6 TFLOP/s of bf16
 // products and 6773 GB/s of copies measured on the same kind of GPU):
@@ -54,6 +56,7 @@
 //     rate: five tiles of 32 KB a multiprocessor in flight, four of them 294 us,
 //     three 383; append 13 us.
 //   1 request, 16 tokens after 512: 32 us, three launches and a chain of waits.
+// k_chunk has 168 registers a thread and spills 52 bytes.
 #include <algorithm>
 #include <cmath>
 #include <cstddef>

@@ -21,15 +21,19 @@
 //
 // Floor: the significance (4 Hq bytes a position), slots and classes, and the
 // moved tokens' bytes.  What bounds it is latency: a unit's passes follow one
-// another (weights, counts, slots; then ranks, moves, tables), with 45% of the
-// warps' places taken.  Measured, with a copy that puts the state back: 8
-// layers of 16 requests of 2048 to 8192 positions, 8 KV heads, half evicted (0.5
-// GB) 281 us, 26% of 6773 GB/s; 28 layers of 7 requests, 4 KV heads, 85% kept (99
-// MB) 126 to 132 us, 12%; one layer of 4 requests of 512 50 us.  Four positions
-// in flight a thread in three blocks a multiprocessor: eight in two 294 us, four
-// in four 322 (spilled); 256 threads a block 305 to 342, 1024 327.  Five apply
-// blocks a multiprocessor: four 284, six 333 us; 256 or 1024 moves listed at a
-// time 291 to 293; a block for 2048 positions 302.
+// another (weights, counts, slots; then ranks, moves, tables), with 65% (plan)
+// and 53% (apply) of the warps' places taken.  Measured, with a copy that puts
+// the state back: 8 layers of 16 requests of 2048 to 8192 positions, 8 KV heads,
+// half evicted (0.5 GB) 281 us, 26% of 6773 GB/s; 28 layers of 7 requests, 4 KV
+// heads, 85% kept (99 MB) 123 to 136 us, 12%; one layer of 4 requests of 512 46
+// to 59 us.  Four positions in flight a thread in three blocks a multiprocessor
+// (40 registers, 20 bytes spilled): eight in two 294 us, four in four 322 (more
+// spilled); 256 threads a block 305 to 342, 1024 327.  Five apply blocks a
+// multiprocessor (48 registers, 16 bytes spilled): four 284, six 333 us; 256 or
+// 1024 moves listed at a time 291 to 293; a block for 2048 positions 302.
+//   Equal weights at the border are settled by one warp that walks the
+// positions: one unit of 8192 positions, halved, 67 us with distinct sums, 63
+// with equal ones, 97 with three values; of 262 000 positions 790, 1760, 2510.
 #include <cuda_runtime.h>
 
 #include <algorithm>

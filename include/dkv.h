@@ -507,9 +507,10 @@ int32_t dkv_extend_significance(const dkv_extend_batch *b, const int32_t *acc_le
  * outputs in progress are fp32; out is bf16.  A request's new tokens
  * are worked on 2 (128 / G) at a time; their weights enter the second product
  * rounded to bf16, and where only 128 / G or fewer are left (short chunks,
- * single tokens), as the sum of two bf16 values.  Range: queries and keys of any finite size; a query that is not
- * finite, or a logit that passes fp32's range, spoils its row; values up to
- * 2^100, or 2^120 / cap where that is less.  Slots of a page behind a request's
+ * single tokens), as the sum of two bf16 values.
+ * Range: queries and keys of any finite size; a query that is not finite, or a
+ * logit that passes fp32's range, spoils its row; values up to 2^100, or
+ * 2^120 / cap where that is less.  Slots of a page behind a request's
  * last token may hold anything; the tokens before it are finite (one that is
  * not may spoil the rows before it too).
  *
@@ -532,14 +533,15 @@ typedef struct dkv_chunk_pages {
 } dkv_chunk_pages;
 
 typedef struct dkv_chunk_batch {
-  int32_t L, R, Hq, Hkv;     /* the pages' layers, requests, heads; 1 <= Hq / Hkv <= 128 */
+  int32_t L, R, Hq, Hkv;     /* the pages' layers, requests, heads; L, R <= 65535, Hq <= 128.  L F B, R tmax,
+                                n_layers T and n_layers R Hkv stay below 2^31 */
   int32_t cap;               /* positions per request (sig_sum rows); ctx + new <= cap */
   int32_t layer0, n_layers;  /* attend layers [layer0, layer0 + n_layers) of the pages */
   int32_t max_new;           /* >= every new_lens[r]; exact is fastest.  A chunk's work, n G / 256 * (cap / 128 + 4)
                                 with n = min(max_new, T), has to stay below 2^31: split a larger one */
   int64_t T;                 /* sum of new_lens */
   int64_t q_stride, kv_stride; /* elements from one token's row of q (of k_new and v_new) to the next, a
-                                multiple of 8; 0: Hq * 128 (Hkv * 128).  Layers follow T rows later */
+                                multiple of 8, at most 2^32; 0: Hq * 128 (Hkv * 128).  Layers follow T rows later */
   const void *q;             /* bf16 [n_layers][T][Hq][128], 16-byte aligned */
   const void *k_new;         /* bf16 [n_layers][T][Hkv][128], 16-byte aligned, or NULL: the pages hold the new
                                 tokens already (not read by dkv_chunk_significance) */
@@ -573,8 +575,9 @@ int32_t dkv_chunk_attention(const dkv_chunk_batch *b, const dkv_chunk_pages *pag
 
 /* Significance of those rows (above), asynchronous; needs no workspace and
  * allocates nothing.  K is read from the pages, the new tokens' too.  sig_sum:
- * in/out fp32 [L][R * cap][Hq].  Errors as dkv_chunk_attention; a page id
- * outside [0, F) leaves the sums of that page's tokens without meaning. */
+ * in/out fp32 [L][R * cap][Hq], 16-byte aligned.  Errors as
+ * dkv_chunk_attention; a page id outside [0, F) leaves the sums of that page's
+ * tokens without meaning. */
 int32_t dkv_chunk_significance(const dkv_chunk_batch *b, const dkv_chunk_pages *pages, float *sig_sum,
                                const dkv_pool *pool, void *stream);
 
@@ -695,7 +698,9 @@ typedef struct dkv_evict_batch {
 int32_t dkv_evict_workspace_size(const dkv_evict_batch *b, const dkv_pool *pool, const dkv_tables *t, size_t *bytes);
 
 /* Evict (above), asynchronous; allocates nothing.  workspace: device, 256-byte
- * aligned, >= dkv_evict_workspace_size bytes, scratch.  Synchronous
+ * aligned, >= dkv_evict_workspace_size bytes, scratch: calls on different pools
+ * that may overlap on the GPU need one each (calls on one pool are ordered by
+ * the caller, as all that change it).  Synchronous
  * DKV_E_INVAL: a bad shape, pointer or workspace.  All-or-nothing: on a
  * device-side error (status word) nothing has changed: DKV_E_LENS (a
  * ctx_lens[r] outside [0, cap]), DKV_E_INTERNAL (headers, classes, slots, page

@@ -225,6 +225,13 @@ def _stream(stream=None) -> int:
     return stream.cuda_stream
 
 
+def _on_stream(stream, device):
+    """Within it torch allocates and works on the stream of the call (None: the current one)."""
+    if stream is not None and not isinstance(stream, torch.cuda.Stream):  # another library's
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device=device)
+    return torch.cuda.stream(stream)
+
+
 def _p(t) -> int | None:
     return None if t is None else t.data_ptr()
 
@@ -348,9 +355,10 @@ def dkv_get_status(pool: DevicePool, stream=None) -> int:
 def dkv_dequant_page(pool: DevicePool, page_id: int, stream=None):
     P = pool.P
     dev = pool.pages.device
-    k = torch.empty((2 * P, 128), dtype=torch.float32, device=dev)
-    v = torch.empty((2 * P, 128), dtype=torch.float32, device=dev)
-    pos = torch.empty(2 * P, dtype=torch.int32, device=dev)
+    with _on_stream(stream, dev):
+        k = torch.empty((2 * P, 128), dtype=torch.float32, device=dev)
+        v = torch.empty((2 * P, 128), dtype=torch.float32, device=dev)
+        pos = torch.empty(2 * P, dtype=torch.int32, device=dev)
     c = pool.c()
     rc = load().dkv_dequant_page(ctypes.byref(c), int(page_id), _p(k), _p(v), _p(pos), _stream(stream))
     if rc != DKV_OK:
@@ -362,10 +370,11 @@ def dkv_dequant_pages(pool: DevicePool, page_ids: torch.Tensor, stream=None):
     P = pool.P
     n = int(page_ids.numel())
     dev = pool.pages.device
-    ids = page_ids.to(device=dev, dtype=torch.int32).contiguous()
-    k = torch.empty((n, 2 * P, 128), dtype=torch.float32, device=dev)
-    v = torch.empty((n, 2 * P, 128), dtype=torch.float32, device=dev)
-    pos = torch.empty((n, 2 * P), dtype=torch.int32, device=dev)
+    with _on_stream(stream, dev):
+        ids = page_ids.to(device=dev, dtype=torch.int32).contiguous()
+        k = torch.empty((n, 2 * P, 128), dtype=torch.float32, device=dev)
+        v = torch.empty((n, 2 * P, 128), dtype=torch.float32, device=dev)
+        pos = torch.empty((n, 2 * P), dtype=torch.int32, device=dev)
     c = pool.c()
     rc = load().dkv_dequant_pages(ctypes.byref(c), _p(ids), n, _p(k), _p(v), _p(pos), _stream(stream))
     if rc != DKV_OK:
@@ -843,9 +852,7 @@ class Decoder:
     def _scratch(self, n: int, stream) -> torch.Tensor:
         # memory of the stream it is first used on: another stream's could still
         # be read or written by work that had it before
-        if stream is not None and not isinstance(stream, torch.cuda.Stream):  # another library's
-            stream = torch.cuda.ExternalStream(stream.cuda_stream, device=self.device)
-        with torch.cuda.stream(stream):
+        with _on_stream(stream, self.device):
             return torch.empty(n, dtype=torch.uint8, device=self.device)
 
     def _page_ops_ws(self, stream) -> torch.Tensor:
